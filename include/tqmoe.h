@@ -451,6 +451,130 @@ int tq_moe_forward_dequant(const uint16_t* x, const uint8_t* packed, const uint1
                            void* workspace, size_t workspace_bytes, uint16_t* y, tq_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Element types of the calls below that take more than one.
+ * ------------------------------------------------------------------------- */
+enum tq_type { TQ_FP32 = 0, TQ_BF16 = 1, TQ_FP16 = 2 };
+
+/* ---------------------------------------------------------------------------
+ * Scored router: scores of every expert, a bias that balances the choice,
+ * groups, top-k and weights.  Per token t, over its E logits x:
+ *   s_i = 1 / (1 + exp(-x_i))  (TQ_SCORE_SIGMOID)  or softmax(x)_i
+ *         (TQ_SCORE_SOFTMAX);  c_i = s_i + bias_i.
+ *   The experts are `groups` consecutive groups of E / groups; a group's value
+ *   is the sum of its two largest c (of its one); the `top_groups` groups of
+ *   largest value stay.  The chosen are the top_k largest c of the groups that
+ *   stay, in descending order; ties go to the lower index, of groups too.
+ *   Weights are the s of the chosen (without the bias), divided by their sum
+ *   with `renormalize`, times `scale`.
+ * A logit that is not finite is a masked expert: score 0, chosen only when the
+ * groups that stay hold fewer than top_k others.  Such a filler, and any other
+ * choice beyond the experts left, has weight 0, and so have all of a row's when
+ * their sum is 0 (a row with no finite logit).  A NaN in c or in a group's
+ * value counts as -infinity.
+ * The result of a row depends on that row alone: not on n, the launch or the
+ * device's load.  Scores, sums and weights are fp32 throughout.
+ *
+ * logits   (device) [n] rows of E logits_type values, logits_stride elements
+ *          apart (>= E; rows whose base and stride are multiples of 16 bytes
+ *          are read fastest, others are correct).
+ * bias     (device) fp32 [E], or NULL for none.
+ * topk_ids (device) int32 [n][top_k] out; topk_w (device) fp32 [n][top_k] out.
+ * Limits: E <= 1024, top_k <= 32, groups <= 32 dividing E, 1 <= top_groups <=
+ * groups, top_k <= top_groups * (E / groups).
+ *
+ * tq_router_scored_backward: the gradient of the logits from grad_w, the
+ * gradient of topk_w; topk_ids and topk_w are the forward's outputs for the
+ * same logits (the choice itself has no gradient, nor has the bias).  Every
+ * element of grad_logits, [n][E] dense in the logits' type, is written.  An id
+ * out of range is skipped and sets TQ_ERR_INVALID_ARG in the device error word.
+ * ------------------------------------------------------------------------- */
+enum tq_score { TQ_SCORE_SOFTMAX = 0, TQ_SCORE_SIGMOID = 1 };
+int tq_router_scored(const void* logits, int logits_type, int64_t logits_stride, const float* bias,
+                     int64_t n, int E, int top_k, int score, int groups, int top_groups,
+                     int renormalize, float scale, int32_t* topk_ids, float* topk_w, tq_stream_t stream);
+int tq_router_scored_backward(const void* logits, int logits_type, int64_t logits_stride,
+                              const int32_t* topk_ids, const float* topk_w, const float* grad_w,
+                              int64_t n, int E, int top_k, int score, int renormalize, float scale,
+                              void* grad_logits, tq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * 4-bit microscaled values.  A row of K values (K % 32 == 0) is kept as E2M1
+ * codes (0, .5, 1, 1.5, 2, 3, 4, 6 and a sign in bit 3), two to a byte, value
+ * 2i in the low half of byte i; blocks of consecutive values share a scale:
+ *   TQ_FP4_NV  blocks of 16, scale s = e4m3(max|x| / (6 g)), g the 32-bit
+ *              global scale (1 when NULL; positive and finite);
+ *              code = e2m1(x / (s g)), value = code * s * g.
+ *   TQ_FP4_MX  blocks of 32, scale s = 2^(floor(log2 max|x|) - 2) as E8M0
+ *              (2^-127 at least); code = e2m1(x / s); no global scale (the
+ *              pointer must be NULL).
+ * Arithmetic is fp32; both roundings are to nearest even and saturate.  NaN is
+ * kept as 0 and does not count for the maximum, an infinity counts as the
+ * largest finite number.  Values of a block whose scale rounds to 0 are 0.
+ * global_scale, x_scale, h_scale (device) fp32 [1] or NULL; w_scale, gu_scale,
+ * down_scale (device) fp32 [E] or NULL.
+ *
+ * tq_fp4_quantize: x (device) n rows of K x_type values, x_stride elements
+ *   apart, base and rows 16-byte aligned -> packed (device) uint8 [n][K/2],
+ *   8-byte aligned, and scales (device) uint8 [n][K / block].
+ * tq_fp4_dequantize: the values of packed and scales, (code * s) * g rounded
+ *   once to out_type; out (device) [n][K], 16-byte aligned.
+ * tq_fp4_tile_scales: the products below read block scales in tiles of 128
+ *   rows x 4 blocks (512 bytes; byte (row % 32) * 16 + (row % 128 / 32) * 4 +
+ *   block % 4), tiles of a group of 128 rows one after another along K, rows
+ *   padded to 128 and K to 256 values with zeros.  scales (device) uint8
+ *   [E][N][K / block] -> tiled (device), tq_fp4_tiled_scales_size() bytes (0
+ *   on invalid arguments), 16-byte aligned.  Done once, when weights load.
+ * ------------------------------------------------------------------------- */
+enum tq_fp4_format { TQ_FP4_NV = 0, TQ_FP4_MX = 1 };
+int tq_fp4_quantize(const void* x, int x_type, int64_t x_stride, int64_t n, int K, int fmt,
+                    const float* global_scale, uint8_t* packed, uint8_t* scales, tq_stream_t stream);
+int tq_fp4_dequantize(const uint8_t* packed, const uint8_t* scales, int64_t n, int K, int fmt,
+                      const float* global_scale, void* out, int out_type, tq_stream_t stream);
+size_t tq_fp4_tiled_scales_size(int E, int N, int K, int fmt);
+int tq_fp4_tile_scales(const uint8_t* scales, int E, int N, int K, int fmt, uint8_t* tiled,
+                       tq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Products of 4-bit microscaled weights.  The activations are quantised by the
+ * call (as by tq_fp4_quantize, x_scale their global scale), multiplied on the
+ * block-scaled tensor cores and summed in fp32; the result is rounded once to
+ * y_type.  Sums have a fixed order, so results repeat bit for bit.
+ *
+ * tq_fp4_linear:      y[t] = W x[t], W one matrix: packed [N][K/2].
+ * tq_fp4_moe_forward: y[t] = sum_j topk_w[t][j] W_{topk_ids[t][j]} x[t], packed
+ *   [E][N][K/2].  A pair whose id is out of range adds nothing and sets
+ *   TQ_ERR_INVALID_ARG in the device error word.
+ * tq_fp4_moe_mlp_forward: SwiGLU experts, packed_gu [E][2I][H/2] (rows 0..I-1
+ *   the gate, I..2I-1 the up projection), packed_down [E][H][I/2]:
+ *   h = silu(gate) * up per pair in fp32, quantised with global scale h_scale,
+ *   y[t] = sum_j topk_w[t][j] W_down h(t,j).
+ * x as in tq_fp4_quantize; packed and tiled_scales (tq_fp4_tile_scales) 16-byte
+ * aligned; y (device) dense [n][N] (or [n][H]).  N is any width; K, H and I are
+ * multiples of 32.  E <= 1024, top_k <= 32.  workspace (device) of at least
+ * the matching *_workspace_size() bytes (0 on invalid arguments), 256-byte
+ * aligned; its contents are undefined after the call.
+ * ------------------------------------------------------------------------- */
+size_t tq_fp4_linear_workspace_size(int64_t n, int K, int N, int fmt);
+int tq_fp4_linear(const void* x, int x_type, int64_t x_stride, const uint8_t* packed,
+                  const uint8_t* tiled_scales, int fmt, const float* w_scale, const float* x_scale,
+                  int64_t n, int K, int N, void* workspace, size_t workspace_bytes,
+                  void* y, int y_type, tq_stream_t stream);
+size_t tq_fp4_moe_workspace_size(int64_t n, int top_k, int E, int K, int N, int fmt);
+int tq_fp4_moe_forward(const void* x, int x_type, int64_t x_stride, const uint8_t* packed,
+                       const uint8_t* tiled_scales, int fmt, const float* w_scale, const float* x_scale,
+                       const int32_t* topk_ids, const float* topk_w,
+                       int64_t n, int top_k, int E, int K, int N, void* workspace, size_t workspace_bytes,
+                       void* y, int y_type, tq_stream_t stream);
+size_t tq_fp4_moe_mlp_workspace_size(int64_t n, int top_k, int E, int H, int I, int fmt);
+int tq_fp4_moe_mlp_forward(const void* x, int x_type, int64_t x_stride,
+                           const uint8_t* packed_gu, const uint8_t* tiled_gu, const float* gu_scale,
+                           const uint8_t* packed_down, const uint8_t* tiled_down, const float* down_scale,
+                           int fmt, const float* x_scale, const float* h_scale,
+                           const int32_t* topk_ids, const float* topk_w,
+                           int64_t n, int top_k, int E, int H, int I, void* workspace, size_t workspace_bytes,
+                           void* y, int y_type, tq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Diagnostics
  * ------------------------------------------------------------------------- */
 
@@ -488,6 +612,14 @@ int tq_probe_wait_timeout(int64_t timeout_ns, int* out, tq_stream_t stream);
  * arms), out[10] SwiGLU ([P3]: counters prove which arm ran). */
 #define TQ_NUM_LAUNCH_COUNTERS 11
 void tq_launch_counts(int64_t out[TQ_NUM_LAUNCH_COUNTERS]);
+
+/* The same and the counters that came later: out[11] scored router, out[12] its
+ * backward, out[13] 4-bit quantise, out[14] dequantise, out[15] scale tiling,
+ * out[16] activation staging, out[17] 4-bit GEMM, out[18] 4-bit combine,
+ * out[19] SwiGLU staging.  Writes the first `capacity` of them and returns how
+ * many there are. */
+#define TQ_NUM_ALL_LAUNCH_COUNTERS 20
+int tq_launch_counts_all(int64_t* out, int capacity);
 
 #ifdef __cplusplus
 }

@@ -24,16 +24,23 @@ __all__ = [
     "tq_moe_mlp_workspace_size", "tq_moe_mlp_forward", "tq_dequantize", "tq_grouped_gemm_dense",
     "tq_moe_dequant_workspace_size", "tq_moe_forward_dequant", "ARM_AUTO", "ARM_GEMV", "ARM_GROUPED", "ARM_MEASURED", "EXPORTED_SYMBOLS",
     "X_TOKENS", "X_PAIR_SORTED", "GATHER_MAX_TILE_M",
+    "tq_router_scored", "tq_router_scored_backward", "SCORE_SOFTMAX", "SCORE_SIGMOID",
+    "tq_fp4_quantize", "tq_fp4_dequantize", "tq_fp4_tiled_scales_size", "tq_fp4_tile_scales",
+    "tq_fp4_linear_workspace_size", "tq_fp4_linear", "tq_fp4_moe_workspace_size", "tq_fp4_moe_forward",
+    "tq_fp4_moe_mlp_workspace_size", "tq_fp4_moe_mlp_forward", "FP4_NV", "FP4_MX", "tq_launch_counts_all",
 ]
 
 ARM_AUTO, ARM_GEMV, ARM_GROUPED, ARM_MEASURED = 0, 1, 2, 3
 TILE_NATIVE = 0          # tile_m of the whole-product calls: the kernel's native m-tile
 X_TOKENS, X_PAIR_SORTED = 0, 1   # activation layouts of tq_grouped_gemm / tq_grouped_gemm_dense
 GATHER_MAX_TILE_M = 16   # the whole-product calls gather rows in the kernel up to this m-tile
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1   # scores of tq_router_scored
+FP4_NV, FP4_MX = 0, 1    # 4-bit formats: blocks of 16 with E4M3 scales, blocks of 32 with E8M0 scales
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libtqmoe.so")
 
 _c_i64, _c_int, _c_dbl, _c_p, _c_sz = ctypes.c_int64, ctypes.c_int, ctypes.c_double, ctypes.c_void_p, ctypes.c_size_t
+_c_flt = ctypes.c_float
 
 # name -> (restype, argtypes); the same set include/tqmoe.h declares
 _SIGS = {
@@ -81,6 +88,25 @@ _SIGS = {
                                         _c_int, _c_int, _c_p, _c_sz, _c_p, _c_p]),
     "tq_device_error": (_c_int, [ctypes.POINTER(_c_int), ctypes.POINTER(_c_int)]),
     "tq_launch_counts": (None, [ctypes.POINTER(_c_i64)]),
+    "tq_launch_counts_all": (_c_int, [ctypes.POINTER(_c_i64), _c_int]),
+    "tq_router_scored": (_c_int, [_c_p, _c_int, _c_i64, _c_p, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                  _c_flt, _c_p, _c_p, _c_p]),
+    "tq_router_scored_backward": (_c_int, [_c_p, _c_int, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_int, _c_int, _c_int,
+                                           _c_int, _c_flt, _c_p, _c_p]),
+    "tq_fp4_quantize": (_c_int, [_c_p, _c_int, _c_i64, _c_i64, _c_int, _c_int, _c_p, _c_p, _c_p, _c_p]),
+    "tq_fp4_dequantize": (_c_int, [_c_p, _c_p, _c_i64, _c_int, _c_int, _c_p, _c_p, _c_int, _c_p]),
+    "tq_fp4_tiled_scales_size": (_c_sz, [_c_int, _c_int, _c_int, _c_int]),
+    "tq_fp4_tile_scales": (_c_int, [_c_p, _c_int, _c_int, _c_int, _c_int, _c_p, _c_p]),
+    "tq_fp4_linear_workspace_size": (_c_sz, [_c_i64, _c_int, _c_int, _c_int]),
+    "tq_fp4_linear": (_c_int, [_c_p, _c_int, _c_i64, _c_p, _c_p, _c_int, _c_p, _c_p, _c_i64, _c_int, _c_int, _c_p,
+                               _c_sz, _c_p, _c_int, _c_p]),
+    "tq_fp4_moe_workspace_size": (_c_sz, [_c_i64, _c_int, _c_int, _c_int, _c_int, _c_int]),
+    "tq_fp4_moe_forward": (_c_int, [_c_p, _c_int, _c_i64, _c_p, _c_p, _c_int, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_int,
+                                    _c_int, _c_int, _c_int, _c_p, _c_sz, _c_p, _c_int, _c_p]),
+    "tq_fp4_moe_mlp_workspace_size": (_c_sz, [_c_i64, _c_int, _c_int, _c_int, _c_int, _c_int]),
+    "tq_fp4_moe_mlp_forward": (_c_int, [_c_p, _c_int, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_int, _c_p, _c_p,
+                                        _c_p, _c_p, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_p, _c_sz, _c_p, _c_int,
+                                        _c_p]),
 }
 EXPORTED_SYMBOLS = tuple(_SIGS)
 
@@ -586,3 +612,280 @@ def tq_launch_counts() -> dict:
     arr = (ctypes.c_int64 * len(LAUNCH_COUNTERS))()
     lib().tq_launch_counts(arr)
     return dict(zip(LAUNCH_COUNTERS, list(arr)))
+
+
+def tq_launch_counts_all() -> dict:
+    """tq_launch_counts and the counters of the scored router and the 4-bit operators."""
+    arr = (ctypes.c_int64 * len(ALL_LAUNCH_COUNTERS))()
+    lib().tq_launch_counts_all(arr, len(ALL_LAUNCH_COUNTERS))
+    return dict(zip(ALL_LAUNCH_COUNTERS, list(arr)))
+
+
+ALL_LAUNCH_COUNTERS = LAUNCH_COUNTERS + ("router_scored", "router_scored_backward", "fp4_quantize", "fp4_dequantize",
+                                         "fp4_tile_scales", "fp4_stage", "fp4_gemm", "fp4_combine", "fp4_swiglu")
+
+
+# ------------------------------------------------------------------ scored router, 4-bit operators
+
+_type_codes = None
+
+
+def _type_code(dtype, name):
+    """TQ_FP32, TQ_BF16 or TQ_FP16 of a torch dtype."""
+    global _type_codes
+    if _type_codes is None:
+        torch = _torch()
+        _type_codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    code = _type_codes.get(dtype)
+    if code is None:
+        raise TypeError(f"{name} has dtype {dtype}, expected one of {tuple(_type_codes)}")
+    return code
+
+
+def _rows(t, name):
+    """(address, type code, elements between rows) of a 2-D CUDA tensor with contiguous rows."""
+    try:
+        ok, code = t.is_cuda, _type_code(t.dtype, name)
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    if not ok:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, not {t.dim()}")
+    n, width = t.shape
+    step, inner = t.stride()
+    if inner != 1 and width > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), code, step if n > 1 else width
+
+
+def _out_ptr(t, shape, dtypes, name):
+    """Address of an output given by the caller: a contiguous CUDA tensor of that shape."""
+    ptr = _dev_ptr(t, dtypes, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return ptr
+
+
+def _scale_ptr(t, count, name):
+    """Address of `count` fp32 scales, or None."""
+    if t is None:
+        return None
+    ptr = _dev_ptr(t, (_torch().float32,), name)
+    if t.numel() != count:
+        raise ValueError(f"{name} has {t.numel()} values, expected {count}")
+    return ptr
+
+
+def tq_router_scored(logits, top_k: int, score: int = SCORE_SIGMOID, bias=None, groups: int = 1, top_groups: int = 1,
+                     renormalize: bool = True, scale: float = 1.0, topk_ids=None, topk_w=None, stream=None):
+    """Top-k experts by score + bias within the best groups -> (topk_ids int32 [n, top_k], topk_w fp32 [n, top_k]).
+
+    logits [n, E] fp32, bf16 or fp16 (rows may be strided); score SCORE_SIGMOID
+    or SCORE_SOFTMAX; bias fp32 [E] moves the choice, not the weights; of
+    `groups` equal groups the `top_groups` with the largest two best values
+    stay; the weights are the chosen scores, divided by their sum with
+    `renormalize`, times `scale`.  A non-finite logit masks its expert; a row
+    with none left has weights 0."""
+    torch = _torch()
+    ptr, code, step = _rows(logits, "logits")
+    n, E = logits.shape
+    dev = logits.device
+    if topk_ids is None:
+        topk_ids = torch.empty((n, top_k), dtype=torch.int32, device=dev)
+        ids_ptr = topk_ids.data_ptr()
+    else:
+        ids_ptr = _out_ptr(topk_ids, (n, top_k), (torch.int32,), "topk_ids")
+    if topk_w is None:
+        topk_w = torch.empty((n, top_k), dtype=torch.float32, device=dev)
+        w_ptr = topk_w.data_ptr()
+    else:
+        w_ptr = _out_ptr(topk_w, (n, top_k), (torch.float32,), "topk_w")
+    _check(lib().tq_router_scored(ptr, code, step, _scale_ptr(bias, E, "bias"), n, E, top_k, score, groups, top_groups,
+                                  1 if renormalize else 0, scale, ids_ptr, w_ptr, _stream(stream)),
+           "tq_router_scored")
+    return topk_ids, topk_w
+
+
+def tq_router_scored_backward(logits, topk_ids, topk_w, grad_w, score: int = SCORE_SIGMOID, renormalize: bool = True,
+                              scale: float = 1.0, grad_logits=None, stream=None):
+    """Gradient of the logits from the gradient of topk_w (fp32 [n, top_k]), in
+    the logits' dtype; topk_ids, topk_w and the options are those of the
+    forward call."""
+    torch = _torch()
+    ptr, code, step = _rows(logits, "logits")
+    n, E = logits.shape
+    shape = (n, topk_ids.shape[1])
+    if grad_logits is None:
+        grad_logits = torch.empty((n, E), dtype=logits.dtype, device=logits.device)
+    _check(lib().tq_router_scored_backward(
+        ptr, code, step, _out_ptr(topk_ids, shape, (torch.int32,), "topk_ids"),
+        _out_ptr(topk_w, shape, (torch.float32,), "topk_w"), _out_ptr(grad_w, shape, (torch.float32,), "grad_w"), n, E,
+        shape[1], score, 1 if renormalize else 0, scale,
+        _out_ptr(grad_logits, (n, E), (logits.dtype,), "grad_logits"), _stream(stream)), "tq_router_scored_backward")
+    return grad_logits
+
+
+def _fp4_block(fmt):
+    if fmt not in (FP4_NV, FP4_MX):
+        raise ValueError(f"fmt must be FP4_NV or FP4_MX, not {fmt}")
+    return 16 if fmt == FP4_NV else 32
+
+
+def tq_fp4_quantize(x, fmt: int = FP4_NV, global_scale=None, packed=None, scales=None, stream=None):
+    """4-bit microscaled copy of x [n, K] (fp32, bf16 or fp16; 16-byte aligned
+    rows; K % 32 == 0) -> (packed uint8 [n, K/2], scales uint8 [n, K/16] for
+    FP4_NV or [n, K/32] for FP4_MX).  global_scale: fp32 [1] on the device
+    (FP4_NV only)."""
+    torch = _torch()
+    ptr, code, step = _rows(x, "x")
+    n, K = x.shape
+    kb = K // _fp4_block(fmt)
+    packed = torch.empty((n, K // 2), dtype=torch.uint8, device=x.device) if packed is None else packed
+    scales = torch.empty((n, kb), dtype=torch.uint8, device=x.device) if scales is None else scales
+    _check(lib().tq_fp4_quantize(ptr, code, step, n, K, fmt, _scale_ptr(global_scale, 1, "global_scale"),
+                                 _out_ptr(packed, (n, K // 2), (torch.uint8,), "packed"),
+                                 _out_ptr(scales, (n, kb), (torch.uint8,), "scales"), _stream(stream)),
+           "tq_fp4_quantize")
+    return packed, scales
+
+
+def tq_fp4_dequantize(packed, scales, fmt: int = FP4_NV, global_scale=None, dtype=None, out=None, stream=None):
+    """The values of tq_fp4_quantize's output, [..., K] of `dtype` (fp32 when
+    neither it nor `out` is given)."""
+    torch = _torch()
+    K = 2 * packed.shape[-1]
+    n = packed.numel() // max(K // 2, 1)
+    if scales.numel() != n * (K // _fp4_block(fmt)):
+        raise ValueError("scales do not match packed")
+    shape = (*packed.shape[:-1], K)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32 if dtype is None else dtype, device=packed.device)
+    elif dtype is not None and out.dtype != dtype:
+        raise TypeError(f"out has dtype {out.dtype}, not {dtype}")
+    _check(lib().tq_fp4_dequantize(_dev_ptr(packed, (torch.uint8,), "packed"),
+                                   _dev_ptr(scales, (torch.uint8,), "scales"), n, K, fmt,
+                                   _scale_ptr(global_scale, 1, "global_scale"), _out_ptr(out, shape, (), "out"),
+                                   _type_code(out.dtype, "out"), _stream(stream)), "tq_fp4_dequantize")
+    return out
+
+
+def tq_fp4_tiled_scales_size(E: int, N: int, K: int, fmt: int = FP4_NV) -> int:
+    return int(lib().tq_fp4_tiled_scales_size(E, N, K, fmt))
+
+
+def tq_fp4_tile_scales(scales, fmt: int = FP4_NV, tiled=None, stream=None):
+    """Block scales [N, K/block] or [E, N, K/block] in the tiled layout the
+    products read (1-D uint8); done once, when weights load."""
+    torch = _torch()
+    E, N, kb = scales.shape if scales.dim() == 3 else (1, *scales.shape)
+    K = kb * _fp4_block(fmt)
+    size = tq_fp4_tiled_scales_size(E, N, K, fmt)
+    tiled = torch.empty(size, dtype=torch.uint8, device=scales.device) if tiled is None else tiled
+    if tiled.numel() != size:
+        raise ValueError(f"tiled has {tiled.numel()} bytes, expected {size}")
+    _check(lib().tq_fp4_tile_scales(_dev_ptr(scales, (torch.uint8,), "scales"), E, N, K, fmt,
+                                    _dev_ptr(tiled, (torch.uint8,), "tiled"), _stream(stream)), "tq_fp4_tile_scales")
+    return tiled
+
+
+def _fp4_matrix(packed, tiled_scales, E, N, K, fmt, name):
+    """Addresses of a 4-bit weight matrix (or E of them), sizes checked."""
+    torch = _torch()
+    if tuple(packed.shape[-2:]) != (N, K // 2) or packed.numel() != E * N * (K // 2):
+        raise ValueError(f"{name} has shape {tuple(packed.shape)}, expected {(E, N, K // 2)}")
+    B = _fp4_block(fmt)
+    if tiled_scales.numel() != E * (-(-N // 128) * 128) * (-(-K // 256) * 256 // B):
+        raise ValueError(f"the scales of {name} are not the tiled layout of {E} x {N} x {K}")
+    return _dev_ptr(packed, (torch.uint8,), name), _dev_ptr(tiled_scales, (torch.uint8,), f"scales of {name}")
+
+
+def _workspace(workspace, need, device):
+    torch = _torch()
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    return workspace, _dev_ptr(workspace, (torch.uint8,), "workspace")
+
+
+def tq_fp4_linear_workspace_size(n: int, K: int, N: int, fmt: int = FP4_NV) -> int:
+    return int(lib().tq_fp4_linear_workspace_size(n, K, N, fmt))
+
+
+def tq_fp4_linear(x, packed, tiled_scales, fmt: int = FP4_NV, w_scale=None, x_scale=None, workspace=None, y=None,
+                  stream=None):
+    """x [n, K], quantised by the call, times a 4-bit matrix packed [N, K/2]
+    with tiled_scales (tq_fp4_tile_scales) -> y [n, N] in x's dtype (or y's).
+    w_scale, x_scale: fp32 [1] global scales (FP4_NV)."""
+    torch = _torch()
+    ptr, code, step = _rows(x, "x")
+    n, K = x.shape
+    N = packed.shape[-2]
+    w_ptr, s_ptr = _fp4_matrix(packed, tiled_scales, 1, N, K, fmt, "packed")
+    workspace, ws_ptr = _workspace(workspace, tq_fp4_linear_workspace_size(n, K, N, fmt) if workspace is None else 0,
+                                   x.device)
+    y = torch.empty((n, N), dtype=x.dtype, device=x.device) if y is None else y
+    _check(lib().tq_fp4_linear(ptr, code, step, w_ptr, s_ptr, fmt, _scale_ptr(w_scale, 1, "w_scale"),
+                               _scale_ptr(x_scale, 1, "x_scale"), n, K, N, ws_ptr, workspace.numel(),
+                               _out_ptr(y, (n, N), (), "y"), _type_code(y.dtype, "y"), _stream(stream)),
+           "tq_fp4_linear")
+    return y
+
+
+def tq_fp4_moe_workspace_size(n: int, top_k: int, E: int, K: int, N: int, fmt: int = FP4_NV) -> int:
+    return int(lib().tq_fp4_moe_workspace_size(n, top_k, E, K, N, fmt))
+
+
+def tq_fp4_moe_forward(x, packed, tiled_scales, topk_ids, topk_w, fmt: int = FP4_NV, w_scale=None, x_scale=None,
+                       workspace=None, y=None, stream=None):
+    """Routed-expert product over 4-bit experts packed [E, N, K/2] with
+    tiled_scales (tq_fp4_tile_scales) -> y [n, N] in x's dtype (or y's):
+    y[t] = sum_j topk_w[t, j] * W_{topk_ids[t, j]} x[t].  w_scale fp32 [E],
+    x_scale fp32 [1]: global scales (FP4_NV)."""
+    torch = _torch()
+    ptr, code, step = _rows(x, "x")
+    n, K = x.shape
+    E, N, _ = packed.shape
+    top_k = topk_ids.shape[1]
+    w_ptr, s_ptr = _fp4_matrix(packed, tiled_scales, E, N, K, fmt, "packed")
+    workspace, ws_ptr = _workspace(workspace,
+                                   tq_fp4_moe_workspace_size(n, top_k, E, K, N, fmt) if workspace is None else 0,
+                                   x.device)
+    y = torch.empty((n, N), dtype=x.dtype, device=x.device) if y is None else y
+    _check(lib().tq_fp4_moe_forward(ptr, code, step, w_ptr, s_ptr, fmt, _scale_ptr(w_scale, E, "w_scale"),
+                                    _scale_ptr(x_scale, 1, "x_scale"),
+                                    _out_ptr(topk_ids, (n, top_k), (torch.int32,), "topk_ids"),
+                                    _out_ptr(topk_w, (n, top_k), (torch.float32,), "topk_w"), n, top_k, E, K, N,
+                                    ws_ptr, workspace.numel(), _out_ptr(y, (n, N), (), "y"), _type_code(y.dtype, "y"),
+                                    _stream(stream)), "tq_fp4_moe_forward")
+    return y
+
+
+def tq_fp4_moe_mlp_workspace_size(n: int, top_k: int, E: int, H: int, I: int, fmt: int = FP4_NV) -> int:
+    return int(lib().tq_fp4_moe_mlp_workspace_size(n, top_k, E, H, I, fmt))
+
+
+def tq_fp4_moe_mlp_forward(x, packed_gu, tiled_gu, packed_down, tiled_down, topk_ids, topk_w, fmt: int = FP4_NV,
+                           gu_scale=None, down_scale=None, x_scale=None, h_scale=None, workspace=None, y=None,
+                           stream=None):
+    """SwiGLU expert MLP over 4-bit experts: packed_gu [E, 2I, H/2] (gate rows,
+    then up rows), packed_down [E, H, I/2] -> y [n, H] in x's dtype (or y's).
+    gu_scale, down_scale fp32 [E]; x_scale, h_scale fp32 [1], the global scales
+    of x and of h = silu(gate) * up (FP4_NV)."""
+    torch = _torch()
+    ptr, code, step = _rows(x, "x")
+    n, H = x.shape
+    E, I = packed_gu.shape[0], packed_gu.shape[1] // 2
+    top_k = topk_ids.shape[1]
+    gu_ptr, gus_ptr = _fp4_matrix(packed_gu, tiled_gu, E, 2 * I, H, fmt, "packed_gu")
+    d_ptr, ds_ptr = _fp4_matrix(packed_down, tiled_down, E, H, I, fmt, "packed_down")
+    workspace, ws_ptr = _workspace(workspace,
+                                   tq_fp4_moe_mlp_workspace_size(n, top_k, E, H, I, fmt) if workspace is None else 0,
+                                   x.device)
+    y = torch.empty((n, H), dtype=x.dtype, device=x.device) if y is None else y
+    _check(lib().tq_fp4_moe_mlp_forward(
+        ptr, code, step, gu_ptr, gus_ptr, _scale_ptr(gu_scale, E, "gu_scale"), d_ptr, ds_ptr,
+        _scale_ptr(down_scale, E, "down_scale"), fmt, _scale_ptr(x_scale, 1, "x_scale"),
+        _scale_ptr(h_scale, 1, "h_scale"), _out_ptr(topk_ids, (n, top_k), (torch.int32,), "topk_ids"),
+        _out_ptr(topk_w, (n, top_k), (torch.float32,), "topk_w"), n, top_k, E, H, I, ws_ptr, workspace.numel(),
+        _out_ptr(y, (n, H), (), "y"), _type_code(y.dtype, "y"), _stream(stream)), "tq_fp4_moe_mlp_forward")
+    return y

@@ -13,7 +13,8 @@ namespace tq {
 enum ErrWhere : int {
   kWhereRoute = 1, kWhereTileMap = 2, kWhereGroupedProducer = 3, kWhereGroupedDecode = 4,
   kWhereGroupedMma = 5, kWhereGroupedEpilogue = 6, kWhereGroupedTeardown = 7, kWhereDequant = 8,
-  kWhereTableStage = 9, kWhereProbe = 10,
+  kWhereTableStage = 9, kWhereProbe = 10, kWhereRouter = 11, kWhereFp4Load = 12, kWhereFp4Mma = 13,
+  kWhereFp4Epilogue = 14, kWhereFp4Teardown = 15,
 };
 
 // A wait gives up after this long (ns of %globaltimer) and reports

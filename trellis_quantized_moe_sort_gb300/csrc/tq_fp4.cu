@@ -1,0 +1,314 @@
+// C entry points of the 4-bit operators: argument checks, workspace layout and
+// the launch chains of the products.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "tq_fp4.cuh"
+#include "tq_internal.h"
+
+namespace tq {
+namespace {
+
+size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool bad_format(int fmt) { return fmt != TQ_FP4_NV && fmt != TQ_FP4_MX; }
+constexpr int64_t kMaxIndex = static_cast<int64_t>(1) << 31;
+
+// Rows of fp4 values: K a multiple of 32, and small enough that a row's bytes
+// fit the 32-bit coordinates of the copies.
+bool bad_k(int K) { return K < 32 || K % 32 != 0; }
+
+// The smallest of 16, 32, 64, 128, 256 activation rows per m-tile that holds
+// the expected rows of a matrix, with room for the spread between experts.
+int tile_for(double rows) {
+  for (int t = 16; t < 256; t <<= 1) {
+    if (rows * 1.25 <= t) return t;
+  }
+  return 256;
+}
+int moe_tile(int64_t n, int top_k, int E) { return n > 0 ? tile_for(tq_pairs_per_woken_expert(n, top_k, E)) : 16; }
+int linear_tile(int64_t n) { return tile_for(static_cast<double>(n) / 1.25); }
+
+size_t staged_scale_bytes(int64_t tiles, int tile_m, int K, int fmt) {
+  return static_cast<size_t>(tiles) * ((tile_m + 127) / 128) * fp4_steps(K) * fp4_scale_step_bytes(fmt);
+}
+
+// Takes 256-byte aligned regions from a buffer, or only counts their bytes.
+struct Carver {
+  uint8_t* base;
+  size_t used = 0;
+  template <typename T>
+  T* take(size_t count) {
+    T* p = base ? reinterpret_cast<T*>(base + used) : nullptr;
+    used += align256(std::max<size_t>(count, 1) * sizeof(T));
+    return p;
+  }
+};
+
+struct Routed {
+  int32_t *counts, *offsets, *sorted_pairs, *slot_of, *tiles, *num_tiles;
+};
+Routed carve_routed(Carver& c, int64_t P, int E, int64_t cap) {
+  Routed r;
+  r.counts = c.take<int32_t>(E);
+  r.offsets = c.take<int32_t>(E + 1);
+  r.sorted_pairs = c.take<int32_t>(P);
+  r.slot_of = c.take<int32_t>(P);
+  r.tiles = c.take<int32_t>(3 * cap);
+  r.num_tiles = c.take<int32_t>(1);
+  return r;
+}
+
+struct Staged {
+  uint8_t *codes, *scales;
+};
+Staged carve_staged(Carver& c, int64_t P, int64_t tiles, int tile_m, int K, int fmt) {
+  Staged s;
+  s.codes = c.take<uint8_t>(static_cast<size_t>(P) * (K / 2));
+  s.scales = c.take<uint8_t>(staged_scale_bytes(tiles, tile_m, K, fmt));
+  return s;
+}
+
+bool bad_moe_shape(int64_t n, int top_k, int E) {
+  return E < 1 || E > 1024 || top_k < 1 || top_k > E || top_k > 32 || n < 0 || n * top_k >= kMaxIndex;
+}
+bool bad_matrix(int E, int K, int N) { return bad_k(K) || N < 1 || static_cast<int64_t>(E) * N >= kMaxIndex; }
+
+bool bad_rows(const void* x, int type, int64_t stride, int64_t n, int K) {
+  return bad_type(type) || stride < K || (stride * static_cast<int64_t>(type_size(type))) % 16 != 0 ||
+         (n > 0 && (!x || !aligned(x, 16)));
+}
+
+struct MoePlan {
+  int tile_m, splits;
+  int64_t cap, P;
+  Routed routed;
+  Staged staged;
+  float* part;
+  size_t bytes;
+};
+MoePlan plan_moe(void* base, int64_t n, int top_k, int E, int K, int N, int fmt) {
+  MoePlan m;
+  m.tile_m = moe_tile(n, top_k, E);
+  m.P = n * top_k;
+  m.cap = std::max<int64_t>(1, tq_tile_map_capacity(n, top_k, E, m.tile_m));
+  m.splits = fp4_splits(m.cap, K, N);
+  Carver c{static_cast<uint8_t*>(base)};
+  m.routed = carve_routed(c, m.P, E, m.cap);
+  m.staged = carve_staged(c, m.P, m.cap, m.tile_m, K, fmt);
+  m.part = c.take<float>(static_cast<size_t>(m.splits) * m.P * N);
+  m.bytes = c.used;
+  return m;
+}
+
+struct LinearPlan {
+  int tile_m, splits;
+  int64_t tiles;
+  Staged staged;
+  float* part;   // nullptr without splits
+  size_t bytes;
+};
+LinearPlan plan_linear(void* base, int64_t n, int K, int N, int fmt) {
+  LinearPlan l;
+  l.tile_m = linear_tile(n);
+  l.tiles = std::max<int64_t>(1, (n + l.tile_m - 1) / l.tile_m);
+  l.splits = fp4_splits(l.tiles, K, N);
+  Carver c{static_cast<uint8_t*>(base)};
+  l.staged = carve_staged(c, n, l.tiles, l.tile_m, K, fmt);
+  l.part = l.splits > 1 ? c.take<float>(static_cast<size_t>(l.splits) * n * N) : nullptr;
+  l.bytes = c.used;
+  return l;
+}
+
+struct MlpPlan {
+  int tile_m, splits_gu, splits_down;
+  int64_t cap, P;
+  Routed routed;
+  Staged x, h;
+  float *gate_up, *down;
+  size_t bytes;
+};
+MlpPlan plan_mlp(void* base, int64_t n, int top_k, int E, int H, int I, int fmt) {
+  MlpPlan m;
+  m.tile_m = moe_tile(n, top_k, E);
+  m.P = n * top_k;
+  m.cap = std::max<int64_t>(1, tq_tile_map_capacity(n, top_k, E, m.tile_m));
+  m.splits_gu = fp4_splits(m.cap, H, 2 * I);
+  m.splits_down = fp4_splits(m.cap, I, H);
+  Carver c{static_cast<uint8_t*>(base)};
+  m.routed = carve_routed(c, m.P, E, m.cap);
+  m.x = carve_staged(c, m.P, m.cap, m.tile_m, H, fmt);
+  m.h = carve_staged(c, m.P, m.cap, m.tile_m, I, fmt);
+  m.gate_up = c.take<float>(static_cast<size_t>(m.splits_gu) * m.P * 2 * I);
+  m.down = c.take<float>(static_cast<size_t>(m.splits_down) * m.P * H);
+  m.bytes = c.used;
+  return m;
+}
+
+bool bad_workspace(const void* p, size_t bytes, size_t need) { return !p || bytes < need || !aligned(p, 256); }
+
+int route_pairs(const Routed& r, const int32_t* ids, int64_t P, int E, int tile_m, int64_t cap, int* err,
+                cudaStream_t s) {
+  return launch_route_tile_map(ids, static_cast<int>(P), E, tile_m, r.counts, r.offsets, r.sorted_pairs, r.tiles,
+                               r.num_tiles, cap, err, s, nullptr, 0, r.slot_of);
+}
+
+}  // namespace
+}  // namespace tq
+
+using namespace tq;
+
+extern "C" {
+
+int tq_fp4_quantize(const void* x, int x_type, int64_t x_stride, int64_t n, int K, int fmt, const float* global_scale,
+                    uint8_t* packed, uint8_t* scales, tq_stream_t stream) {
+  if (n < 0 || bad_k(K) || bad_format(fmt) || (fmt == TQ_FP4_MX && global_scale)) return TQ_ERR_INVALID_ARG;
+  if (bad_rows(x, x_type, x_stride, n, K)) return TQ_ERR_INVALID_ARG;
+  if (n > 0 && (!packed || !scales || !aligned(packed, 8))) return TQ_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int rc = require_sm103(s);
+  if (rc != TQ_OK || n == 0) return rc;
+  return launch_fp4_quantize(x, x_type, x_stride, n, K, fmt, global_scale, packed, scales, s);
+}
+
+int tq_fp4_dequantize(const uint8_t* packed, const uint8_t* scales, int64_t n, int K, int fmt,
+                      const float* global_scale, void* out, int out_type, tq_stream_t stream) {
+  if (n < 0 || bad_k(K) || bad_format(fmt) || bad_type(out_type) || (fmt == TQ_FP4_MX && global_scale))
+    return TQ_ERR_INVALID_ARG;
+  if (n > 0 && (!packed || !scales || !out || !aligned(packed, 8) || !aligned(out, 16))) return TQ_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int rc = require_sm103(s);
+  if (rc != TQ_OK || n == 0) return rc;
+  return launch_fp4_dequantize(packed, scales, n, K, fmt, global_scale, out, out_type, s);
+}
+
+size_t tq_fp4_tiled_scales_size(int E, int N, int K, int fmt) {
+  if (E < 1 || N < 1 || bad_k(K) || bad_format(fmt)) return 0;
+  return static_cast<size_t>(E) * ((N + 127) / 128) * fp4_steps(K) * fp4_scale_step_bytes(fmt);
+}
+
+int tq_fp4_tile_scales(const uint8_t* scales, int E, int N, int K, int fmt, uint8_t* tiled, tq_stream_t stream) {
+  if (tq_fp4_tiled_scales_size(E, N, K, fmt) == 0 || !scales || !tiled || !aligned(tiled, 16))
+    return TQ_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int rc = require_sm103(s);
+  if (rc != TQ_OK) return rc;
+  return launch_fp4_tile_scales(scales, E, N, K, fmt, tiled, s);
+}
+
+size_t tq_fp4_linear_workspace_size(int64_t n, int K, int N, int fmt) {
+  if (n < 0 || n >= kMaxIndex || bad_matrix(1, K, N) || bad_format(fmt)) return 0;
+  return plan_linear(nullptr, n, K, N, fmt).bytes;
+}
+
+int tq_fp4_linear(const void* x, int x_type, int64_t x_stride, const uint8_t* packed, const uint8_t* tiled_scales,
+                  int fmt, const float* w_scale, const float* x_scale, int64_t n, int K, int N, void* workspace,
+                  size_t workspace_bytes, void* y, int y_type, tq_stream_t stream) {
+  if (n < 0 || n >= kMaxIndex || bad_matrix(1, K, N) || bad_format(fmt) || bad_type(y_type) ||
+      bad_rows(x, x_type, x_stride, n, K) || (fmt == TQ_FP4_MX && (w_scale || x_scale)))
+    return TQ_ERR_INVALID_ARG;
+  if (n > 0 && (!packed || !tiled_scales || !y || !aligned(packed, 16) || !aligned(tiled_scales, 16) ||
+                !aligned(y, type_size(y_type))))
+    return TQ_ERR_INVALID_ARG;
+  const LinearPlan l = plan_linear(workspace, n, K, N, fmt);
+  if (n > 0 && bad_workspace(workspace, workspace_bytes, l.bytes)) return TQ_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int rc = require_sm103(s);
+  if (rc != TQ_OK || n == 0) return rc;
+  int* err = error_word(&rc);
+  if (!err) return rc;
+  rc = launch_fp4_stage(x, x_type, x_stride, n, K, fmt, x_scale, 1, nullptr, nullptr, nullptr, l.tiles, l.tile_m,
+                        l.staged.codes, l.staged.scales, s);
+  if (rc != TQ_OK) return rc;
+  Fp4Gemm g{fmt, packed, tiled_scales, w_scale, l.staged.codes, l.staged.scales, x_scale, nullptr, nullptr, nullptr,
+            l.tiles, n, 1, K, N, l.tile_m, l.splits, l.part, l.splits > 1 ? nullptr : y, y_type, err};
+  rc = launch_fp4_gemm(g, s);
+  if (rc != TQ_OK || l.splits == 1) return rc;
+  return launch_fp4_combine(l.part, n * N, l.splits, nullptr, nullptr, x_scale, w_scale, n, 1, 1, N, y, y_type, s);
+}
+
+size_t tq_fp4_moe_workspace_size(int64_t n, int top_k, int E, int K, int N, int fmt) {
+  if (bad_moe_shape(n, top_k, E) || bad_matrix(E, K, N) || bad_format(fmt)) return 0;
+  return plan_moe(nullptr, n, top_k, E, K, N, fmt).bytes;
+}
+
+int tq_fp4_moe_forward(const void* x, int x_type, int64_t x_stride, const uint8_t* packed, const uint8_t* tiled_scales,
+                       int fmt, const float* w_scale, const float* x_scale, const int32_t* topk_ids,
+                       const float* topk_w, int64_t n, int top_k, int E, int K, int N, void* workspace,
+                       size_t workspace_bytes, void* y, int y_type, tq_stream_t stream) {
+  if (bad_moe_shape(n, top_k, E) || bad_matrix(E, K, N) || bad_format(fmt) || bad_type(y_type) ||
+      bad_rows(x, x_type, x_stride, n, K) || (fmt == TQ_FP4_MX && (w_scale || x_scale)))
+    return TQ_ERR_INVALID_ARG;
+  if (n > 0 && (!packed || !tiled_scales || !topk_ids || !topk_w || !y || !aligned(packed, 16) ||
+                !aligned(tiled_scales, 16) || !aligned(y, type_size(y_type))))
+    return TQ_ERR_INVALID_ARG;
+  const MoePlan m = plan_moe(workspace, n, top_k, E, K, N, fmt);
+  if (n > 0 && bad_workspace(workspace, workspace_bytes, m.bytes)) return TQ_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int rc = require_sm103(s);
+  if (rc != TQ_OK || n == 0) return rc;
+  int* err = error_word(&rc);
+  if (!err) return rc;
+  rc = route_pairs(m.routed, topk_ids, m.P, E, m.tile_m, m.cap, err, s);
+  if (rc == TQ_OK)
+    rc = launch_fp4_stage(x, x_type, x_stride, n, K, fmt, x_scale, top_k, m.routed.slot_of, m.routed.tiles,
+                          m.routed.num_tiles, m.cap, m.tile_m, m.staged.codes, m.staged.scales, s);
+  if (rc != TQ_OK) return rc;
+  Fp4Gemm g{fmt, packed, tiled_scales, w_scale, m.staged.codes, m.staged.scales, x_scale, m.routed.sorted_pairs,
+            m.routed.tiles, m.routed.num_tiles, m.cap, m.P, E, K, N, m.tile_m, m.splits, m.part, nullptr, y_type, err};
+  rc = launch_fp4_gemm(g, s);
+  if (rc != TQ_OK) return rc;
+  return launch_fp4_combine(m.part, m.P * N, m.splits, topk_ids, topk_w, x_scale, w_scale, n, top_k, E, N, y, y_type,
+                            s);
+}
+
+size_t tq_fp4_moe_mlp_workspace_size(int64_t n, int top_k, int E, int H, int I, int fmt) {
+  if (bad_moe_shape(n, top_k, E) || I < 1 || I > (1 << 29) || bad_matrix(E, H, 2 * I) || bad_matrix(E, I, H) ||
+      bad_format(fmt))
+    return 0;
+  return plan_mlp(nullptr, n, top_k, E, H, I, fmt).bytes;
+}
+
+int tq_fp4_moe_mlp_forward(const void* x, int x_type, int64_t x_stride, const uint8_t* packed_gu,
+                           const uint8_t* tiled_gu, const float* gu_scale, const uint8_t* packed_down,
+                           const uint8_t* tiled_down, const float* down_scale, int fmt, const float* x_scale,
+                           const float* h_scale, const int32_t* topk_ids, const float* topk_w, int64_t n, int top_k,
+                           int E, int H, int I, void* workspace, size_t workspace_bytes, void* y, int y_type,
+                           tq_stream_t stream) {
+  if (tq_fp4_moe_mlp_workspace_size(n, top_k, E, H, I, fmt) == 0 || bad_type(y_type) ||
+      bad_rows(x, x_type, x_stride, n, H) || (fmt == TQ_FP4_MX && (gu_scale || down_scale || x_scale || h_scale)))
+    return TQ_ERR_INVALID_ARG;
+  if (n > 0 && (!packed_gu || !tiled_gu || !packed_down || !tiled_down || !topk_ids || !topk_w || !y ||
+                !aligned(packed_gu, 16) || !aligned(tiled_gu, 16) || !aligned(packed_down, 16) ||
+                !aligned(tiled_down, 16) || !aligned(y, type_size(y_type))))
+    return TQ_ERR_INVALID_ARG;
+  const MlpPlan m = plan_mlp(workspace, n, top_k, E, H, I, fmt);
+  if (n > 0 && bad_workspace(workspace, workspace_bytes, m.bytes)) return TQ_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int rc = require_sm103(s);
+  if (rc != TQ_OK || n == 0) return rc;
+  int* err = error_word(&rc);
+  if (!err) return rc;
+  const Routed& r = m.routed;
+  rc = route_pairs(r, topk_ids, m.P, E, m.tile_m, m.cap, err, s);
+  if (rc == TQ_OK)
+    rc = launch_fp4_stage(x, x_type, x_stride, n, H, fmt, x_scale, top_k, r.slot_of, r.tiles, r.num_tiles, m.cap,
+                          m.tile_m, m.x.codes, m.x.scales, s);
+  if (rc != TQ_OK) return rc;
+  Fp4Gemm gu{fmt, packed_gu, tiled_gu, gu_scale, m.x.codes, m.x.scales, x_scale, r.sorted_pairs, r.tiles, r.num_tiles,
+             m.cap, m.P, E, H, 2 * I, m.tile_m, m.splits_gu, m.gate_up, nullptr, y_type, err};
+  rc = launch_fp4_gemm(gu, s);
+  if (rc == TQ_OK)
+    rc = launch_fp4_stage_swiglu(m.gate_up, m.P * 2 * I, m.splits_gu, topk_ids, x_scale, gu_scale, m.P, E, I, fmt,
+                                 h_scale, r.slot_of, r.tiles, r.num_tiles, m.cap, m.tile_m, m.h.codes, m.h.scales, s);
+  if (rc != TQ_OK) return rc;
+  Fp4Gemm down{fmt, packed_down, tiled_down, down_scale, m.h.codes, m.h.scales, h_scale, r.sorted_pairs, r.tiles,
+               r.num_tiles, m.cap, m.P, E, I, H, m.tile_m, m.splits_down, m.down, nullptr, y_type, err};
+  rc = launch_fp4_gemm(down, s);
+  if (rc != TQ_OK) return rc;
+  return launch_fp4_combine(m.down, m.P * H, m.splits_down, topk_ids, topk_w, h_scale, down_scale, n, top_k, E, H, y,
+                            y_type, s);
+}
+
+}  // extern "C"

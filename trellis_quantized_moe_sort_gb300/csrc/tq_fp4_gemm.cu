@@ -1,0 +1,486 @@
+// Product of 4-bit microscaled weights and activations on the block-scaled
+// tensor-core path of sm_103a: D = W X^T with W rows as the MMA's M and
+// activation rows as its N, for one matrix (linear) or for the experts of a
+// tile map.
+//
+// A unit is (m-tile of up to tile_m activation rows) x (128 weight rows), or a
+// split of its K range.  Persistent CTAs, one per SM, walk the units; per step
+// of 256 values the producer warp copies a 128 x 128-byte box of codes, the
+// tile's rows of codes (both 128-byte swizzled) and the two operands' block
+// scales (contiguous in the tiled layout); the MMA thread moves the scales to
+// tensor memory (32 x 128-bit copies, which tcgen05 orders before the MMAs
+// issued after them) and issues up to four MMAs of K = 64; four epilogue warps
+// drain the fp32 accumulator.  The accumulators alternate so that a unit's
+// drain overlaps the next unit's steps.
+//
+// Outputs: per pair in fp32, part[split][pair][N] (plain stores, one writer
+// each, summed in a fixed order by the combine: results do not depend on the
+// schedule), or, for a linear without splits, y itself.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "tq_fp4.cuh"
+#include "tq_internal.h"
+
+namespace tq {
+namespace {
+
+constexpr int kRows = 128;              // weight rows per unit (MMA M)
+constexpr int kRowBytes = kFp4Step / 2; // a step of one row: one 128-byte swizzle row
+constexpr int kWBytes = kRows * kRowBytes;
+constexpr int kMaxStages = 12;
+constexpr int kMaxAcc = 4;
+constexpr int kThreads = 192;
+constexpr int kWarpLoad = 0, kWarpMma = 1;   // warps 2-5: epilogue, one per lane quarter
+constexpr int kSmemLimit = 232448;
+constexpr int kNumBars = 2 * kMaxStages + 2 * kMaxAcc + 1;
+
+struct GemmParams {
+  const int32_t* sorted_pairs;   // nullptr: the pair of a slot is the slot
+  const int32_t* tiles;          // nullptr: tile i = rows [i * tile_m, ...) of expert 0
+  const int32_t* num_tiles;
+  const uint8_t* w_scales;       // tiled, [E][row groups][steps]
+  const uint8_t* x_scales;       // tiled, [tiles][tile row groups][steps]
+  const float* x_scale;
+  const float* w_scale;
+  float* part;
+  void* y;
+  int y_type;                    // of y; part is used when y is null
+  int* err;
+  long long cap, split_stride;
+  int P, E, K, N, tile_m;
+  int row_blocks, steps, splits;
+  int n_max;                     // tile_m rounded up to 16
+  int stages, accs, acc_cols;
+  int sf_col, tmem_cols;
+  int x_bytes, x_sf_bytes, stage_bytes;
+  uint32_t off_bar;
+};
+
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void advance(int n) {
+    if (++at == n) {
+      at = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+struct Unit {
+  int tile, e, slot0, rows, rb, k0, k1, split;
+  bool ok;
+};
+
+__device__ __forceinline__ Unit unit_at(const GemmParams& p, long long u, int num_tiles) {
+  Unit t;
+  t.rb = static_cast<int>(u % p.row_blocks);
+  u /= p.row_blocks;
+  t.tile = static_cast<int>(u % num_tiles);
+  t.split = static_cast<int>(u / num_tiles);
+  t.k0 = static_cast<int>(static_cast<long long>(p.steps) * t.split / p.splits);
+  t.k1 = static_cast<int>(static_cast<long long>(p.steps) * (t.split + 1) / p.splits);
+  if (p.tiles) {
+    const int32_t* const entry = p.tiles + 3ll * t.tile;
+    t.e = __ldg(entry);
+    t.slot0 = __ldg(entry + 1);
+    t.rows = __ldg(entry + 2);
+  } else {
+    t.e = 0;
+    t.slot0 = t.tile * p.tile_m;
+    t.rows = min(p.tile_m, p.P - t.slot0);
+  }
+  t.ok = t.e >= 0 && t.e < p.E && t.rows >= 1 && t.rows <= p.tile_m && t.slot0 >= 0 && t.slot0 <= p.P - t.rows;
+  return t;
+}
+
+// Instruction descriptor of the block-scaled kinds: E2M1 x E2M1, both K-major,
+// M x N, scales E4M3 (NV) or E8M0 (MX); the scales of the MMA start at byte
+// `sf` of their 32-bit columns.
+template <int kFmt>
+__device__ __forceinline__ uint32_t idesc_fp4(uint32_t n, uint32_t sf) {
+  return (sf << 4)                                        // B scale id
+         | (1u << 7)                                      // A: E2M1
+         | (1u << 10)                                     // B: E2M1
+         | ((n >> 3) << 17)                               // N / 8
+         | ((kFmt == TQ_FP4_MX ? 1u : 0u) << 23)          // scale type: E8M0 or E4M3
+         | ((kRows >> 4) << 24)                           // M / 16
+         | (sf << 29);                                    // A scale id
+}
+
+template <int kFmt>
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                        uint32_t accumulate) {
+  if constexpr (kFmt == TQ_FP4_NV) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  }
+}
+
+// One 512-byte scale tile (32 x 128 bits, 8-row groups of 128 bytes) to four
+// tensor-memory columns, replicated over the four lane quarters.
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t smem) {
+  const uint64_t desc = static_cast<uint64_t>((smem & 0x3FFFFu) >> 4) | static_cast<uint64_t>(16 >> 4) << 16 |
+                        static_cast<uint64_t>(128 >> 4) << 32 | static_cast<uint64_t>(1) << 46;
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ void store_y(const GemmParams& p, size_t at, float v) {
+  if (p.y_type == TQ_FP32)
+    static_cast<float*>(p.y)[at] = v;
+  else if (p.y_type == TQ_BF16)
+    static_cast<__nv_bfloat16*>(p.y)[at] = narrow<__nv_bfloat16>(v);
+  else
+    static_cast<__half*>(p.y)[at] = narrow<__half>(v);
+}
+
+template <int kFmt>
+__global__ void __launch_bounds__(kThreads, 1)
+fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                const GemmParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const gbase = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kSfStep = fp4_scale_step_bytes(kFmt);   // per 128 rows and step
+  constexpr int kSfTiles = kSfStep / 512;               // scale tiles per step (4 NV, 2 MX)
+
+  const uint32_t bar_full = base + p.off_bar;
+  const uint32_t bar_empty = bar_full + 8 * kMaxStages;
+  const uint32_t bar_accfull = bar_empty + 8 * kMaxStages;
+  const uint32_t bar_accempty = bar_accfull + 8 * kMaxAcc;
+  const uint32_t bar_drain = bar_accempty + 8 * kMaxAcc;
+  uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(gbase + p.off_bar + 8 * kNumBars);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, 1);
+    }
+    for (int a = 0; a < p.accs; ++a) {
+      mbar_init(bar_accfull + 8 * a, 1);
+      mbar_init(bar_accempty + 8 * a, 4);
+    }
+    mbar_init(bar_drain, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_x);
+  }
+  if (warp == kWarpLoad) tmem_alloc(smem_u32(tmem_holder), static_cast<uint32_t>(p.tmem_cols));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
+  pdl_wait();   // the tile map, the staged activations
+
+  const int num_tiles = p.tiles ? static_cast<int>(min(static_cast<long long>(*p.num_tiles), p.cap))
+                                : static_cast<int>(p.cap);
+  const long long units = static_cast<long long>(num_tiles) * p.row_blocks * p.splits;
+
+  if (warp == kWarpLoad) {
+    Ring ring;
+    long long issued = 0;
+    bool ok = true;
+    for (long long u = blockIdx.x; ok && u < units; u += gridDim.x) {
+      const Unit t = unit_at(p, u, num_tiles);
+      if (!t.ok) {
+        if (lane == 0) record_error(p.err, TQ_ERR_INVALID_ARG, kWhereFp4Load);
+        continue;
+      }
+      const int w_row = t.e * p.N + t.rb * kRows;
+      const uint8_t* const wsf = p.w_scales + (static_cast<size_t>(t.e) * p.row_blocks + t.rb) * p.steps * kSfStep;
+      const uint8_t* const xsf = p.x_scales + static_cast<size_t>(t.tile) * p.steps * p.x_sf_bytes;
+      for (int k = t.k0; k < t.k1; ++k) {
+        if (!mbar_wait(bar_empty + 8 * ring.at, ring.phase ^ 1u, abort_flag, p.err, kWhereFp4Load)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          const uint32_t full = bar_full + 8 * ring.at;
+          const uint32_t dst = base + static_cast<uint32_t>(ring.at * p.stage_bytes);
+          mbar_arrive_expect_tx(full, static_cast<uint32_t>(p.stage_bytes));
+          tma_load_2d(dst, &tm_w, k * kRowBytes, w_row, full);
+          tma_load_2d(dst + kWBytes, &tm_x, k * kRowBytes, t.slot0, full);
+          bulk_load(dst + kWBytes + p.x_bytes, wsf + static_cast<size_t>(k) * kSfStep, kSfStep, full);
+          // the tile's row groups are p.steps * kSfStep apart
+          for (int r = 0; r * kSfStep < p.x_sf_bytes; ++r)
+            bulk_load(dst + kWBytes + p.x_bytes + (1 + r) * kSfStep,
+                      xsf + (static_cast<size_t>(r) * p.steps + k) * kSfStep, kSfStep, full);
+        }
+        __syncwarp();
+        ++issued;
+        ring.advance(p.stages);
+      }
+    }
+    // every copy issued has landed before the CTA exits
+    const long long pending = min(issued, static_cast<long long>(p.stages));
+    for (long long i = 1; i <= pending; ++i) {
+      int st = ring.at - static_cast<int>(i);
+      uint32_t ph = ring.phase;
+      if (st < 0) {
+        st += p.stages;
+        ph ^= 1u;
+      }
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try_wait(bar_full + 8 * st, ph)) {
+        if (globaltimer() - t0 > kWaitTimeoutNs) {
+          record_error(p.err, TQ_ERR_DEVICE_TIMEOUT, kWhereFp4Teardown);
+          break;
+        }
+      }
+    }
+  } else if (warp == kWarpMma) {
+    Ring ring, acc;
+    bool ok = true;
+    for (long long u = blockIdx.x; ok && u < units; u += gridDim.x) {
+      const Unit t = unit_at(p, u, num_tiles);
+      if (!t.ok) continue;
+      const uint32_t n_mma = static_cast<uint32_t>((t.rows + 15) & ~15);
+      if (!mbar_wait(bar_accempty + 8 * acc.at, acc.phase ^ 1u, abort_flag, p.err, kWhereFp4Mma)) break;
+      tc_fence_after();
+      const uint32_t d = tmem + static_cast<uint32_t>(acc.at * p.acc_cols);
+      for (int k = t.k0; k < t.k1; ++k) {
+        if (!mbar_wait(bar_full + 8 * ring.at, ring.phase, abort_flag, p.err, kWhereFp4Mma)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t w = base + static_cast<uint32_t>(ring.at * p.stage_bytes);
+          const uint32_t x = w + kWBytes;
+          const uint32_t sf = x + static_cast<uint32_t>(p.x_bytes);
+          const uint32_t sfa = tmem + static_cast<uint32_t>(p.sf_col);
+          const uint32_t sfb = sfa + 4 * kSfTiles;
+          const int x_groups = (static_cast<int>(n_mma) + 127) / 128;
+#pragma unroll
+          for (int i = 0; i < kSfTiles; ++i) {
+            copy_scales(sfa + 4 * i, sf + 512 * i);
+            // row group r of the tile's scales: columns 4r .. 4r + 3 of its block group
+            for (int r = 0; r < x_groups; ++r)
+              copy_scales(sfb + 8 * i + 4 * r, sf + kSfStep * (1 + r) + 512 * i);
+          }
+          const int parts = min(4, (p.K - k * kFp4Step + 63) / 64);
+          for (int i = 0; i < parts; ++i) {
+            const int tile = kFmt == TQ_FP4_NV ? i : i / 2;
+            const uint32_t id = kFmt == TQ_FP4_NV ? 0u : 2u * (i & 1);
+            mma_fp4<kFmt>(d, smem_desc_sw128(w + 32 * i), smem_desc_sw128(x + 32 * i), idesc_fp4<kFmt>(n_mma, id),
+                          sfa + 4 * tile, sfb + 8 * tile, (k != t.k0 || i != 0) ? 1u : 0u);
+          }
+          mma_commit(bar_empty + 8 * ring.at);
+        }
+        __syncwarp();
+        ring.advance(p.stages);
+      }
+      if (!ok) break;
+      if (lane == 0) mma_commit(bar_accfull + 8 * acc.at);
+      __syncwarp();
+      acc.advance(p.accs);
+    }
+    if (lane == 0) {   // every MMA issued has completed before teardown
+      mma_commit(bar_drain);
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try_wait(bar_drain, 0)) {
+        if (globaltimer() - t0 > kWaitTimeoutNs) {
+          record_error(p.err, TQ_ERR_DEVICE_TIMEOUT, kWhereFp4Teardown);
+          break;
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3;
+    Ring acc;
+    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+      const Unit t = unit_at(p, u, num_tiles);
+      if (!t.ok) continue;
+      int pair[8];   // of columns lane + 32 i
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int col = lane + 32 * i;
+        pair[i] = -1;
+        if (col < t.rows) {
+          pair[i] = p.sorted_pairs ? __ldg(p.sorted_pairs + t.slot0 + col) : t.slot0 + col;
+          if (pair[i] < 0 || pair[i] >= p.P) {
+            record_error(p.err, TQ_ERR_INVALID_ARG, kWhereFp4Epilogue);
+            pair[i] = -1;
+          }
+        }
+      }
+      float alpha = 1.f;
+      if (p.y) alpha = (p.x_scale ? __ldg(p.x_scale) : 1.f) * (p.w_scale ? __ldg(p.w_scale + t.e) : 1.f);
+      if (!mbar_wait(bar_accfull + 8 * acc.at, acc.phase, abort_flag, p.err, kWhereFp4Epilogue)) break;
+      tc_fence_after();
+      const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(acc.at * p.acc_cols);
+      const int f = t.rb * kRows + 32 * q + lane;
+      float* const out = p.part + static_cast<size_t>(t.split) * p.split_stride + f;
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        if (32 * b >= t.rows) break;
+        uint32_t v[2][16];
+        tmem_ld16(src + 32 * b, v[0]);
+        if (32 * b + 16 < t.rows) tmem_ld16(src + 32 * b + 16, v[1]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          if (32 * b + j >= t.rows) break;
+          const int to = __shfl_sync(0xffffffffu, pair[b], j);
+          if (to >= 0 && f < p.N) {
+            const float r = __uint_as_float(v[j >> 4][j & 15]);
+            if (p.y)
+              store_y(p, static_cast<size_t>(to) * p.N + f, r * alpha);
+            else
+              out[static_cast<size_t>(to) * p.N] = r;
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_accempty + 8 * acc.at);
+      acc.advance(p.accs);
+    }
+  }
+
+  pdl_trigger();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpLoad) {
+    tc_fence_after();
+    tmem_dealloc(tmem, static_cast<uint32_t>(p.tmem_cols));
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// Codes as a 2-D tensor of bytes, boxes of one step x `rows`.
+bool encode_codes(CUtensorMap* m, const uint8_t* codes, int64_t rows, int K, int box_rows) {
+  auto encode = encoder();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K / 2), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 2)};
+  const cuuint32_t box[2] = {kRowBytes, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+// K splits of a product of at most `tiles` m-tiles: as many whole rounds of
+// the SMs as the units make, the count (up to 8, a step at least each) whose
+// last round wastes least; one when the units fill four rounds by themselves.
+int fp4_splits(int64_t tiles, int K, int N) {
+  const long long units = tiles * ((N + kRows - 1) / kRows);
+  const int sms = sm_count(), steps = fp4_steps(K);
+  if (units >= 4ll * sms) return 1;
+  int best = 1;
+  double best_cost = 1e30;
+  for (int s = 1; s <= std::min(8, steps); ++s) {
+    const long long rounds = (units * s + sms - 1) / sms;
+    const double cost = static_cast<double>(rounds) * ((steps + s - 1) / s + 1.0);   // a unit costs about a step more
+    if (cost < best_cost * 0.95) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
+int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s) {
+  GemmParams p{};
+  p.sorted_pairs = g.sorted_pairs;
+  p.tiles = g.tiles;
+  p.num_tiles = g.num_tiles;
+  p.w_scales = g.w_scales;
+  p.x_scales = g.x_scales;
+  p.x_scale = g.x_scale;
+  p.w_scale = g.w_scale;
+  p.part = g.part;
+  p.y = g.y;
+  p.y_type = g.y_type;
+  p.err = g.err;
+  p.cap = g.cap;
+  p.split_stride = static_cast<long long>(g.P) * g.N;
+  p.P = static_cast<int>(g.P);
+  p.E = g.E;
+  p.K = g.K;
+  p.N = g.N;
+  p.tile_m = g.tile_m;
+  p.row_blocks = (g.N + kRows - 1) / kRows;
+  p.steps = fp4_steps(g.K);
+  p.splits = g.splits;
+  p.n_max = (g.tile_m + 15) & ~15;
+
+  const int sf_step = fp4_scale_step_bytes(g.fmt);
+  const int x_groups = (p.n_max + 127) / 128;
+  p.x_bytes = p.n_max * kRowBytes;
+  p.x_sf_bytes = x_groups * sf_step;
+  p.stage_bytes = kWBytes + p.x_bytes + sf_step + p.x_sf_bytes;
+  const int bar_bytes = 8 * kNumBars + 16;
+  p.stages = std::min(kMaxStages, (kSmemLimit - 1024 - bar_bytes) / p.stage_bytes);
+  p.off_bar = static_cast<uint32_t>(p.stages * p.stage_bytes);
+  // one CTA (and one tensor-memory allocation) per SM
+  const int smem = std::max(1024 + p.stages * p.stage_bytes + bar_bytes, 120 * 1024);
+
+  // Tensor memory: accumulators, then the scales of one step (4 columns per
+  // scale tile of the weights, 8 of the activations).
+  const int sf_cols = (sf_step / 512) * 12;
+  p.acc_cols = p.n_max;
+  p.accs = std::min(kMaxAcc, (512 - sf_cols) / p.acc_cols);
+  p.sf_col = p.accs * p.acc_cols;
+  p.tmem_cols = 32;
+  while (p.tmem_cols < p.sf_col + sf_cols) p.tmem_cols <<= 1;
+
+  CUtensorMap tm_w, tm_x;
+  if (!encode_codes(&tm_w, g.w, static_cast<int64_t>(g.E) * g.N, g.K, kRows) ||
+      !encode_codes(&tm_x, g.x, g.P, g.K, p.n_max))
+    return TQ_ERR_INVALID_ARG;
+  auto kernel = g.fmt == TQ_FP4_NV ? fp4_gemm_kernel<TQ_FP4_NV> : fp4_gemm_kernel<TQ_FP4_MX>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess) {
+    cudaGetLastError();
+    return TQ_ERR_CUDA;
+  }
+  const long long units = g.cap * p.row_blocks * p.splits;
+  const int grid = static_cast<int>(std::max<long long>(1, std::min<long long>(units, sm_count())));
+  const int st = launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, s, tm_w, tm_x, p);
+  if (st == TQ_OK) count_launch(kCntFp4Gemm);
+  return st;
+}
+
+}  // namespace tq

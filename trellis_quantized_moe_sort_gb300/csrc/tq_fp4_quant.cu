@@ -1,0 +1,410 @@
+// 4-bit microscaled values: quantise, dequantise, the tiled scale layout, the
+// product's activation staging and the combine of its partial sums.
+//
+// All of these move bytes: a thread takes 16 consecutive values (two or four
+// 16-byte loads), so a warp reads 1 or 2 KiB of a row at once and writes 256
+// bytes of codes.  A block of 32 values is two neighbouring threads, which
+// share their maximum by one shuffle.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "tq_fp4.cuh"
+#include "tq_internal.h"
+
+namespace tq {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kQuantThreads = 256;
+
+// Quantises 16 values of a block (the whole of it, or one of its two halves in
+// neighbouring lanes; every lane of the warp takes part): codes and scale byte.
+template <int kFmt>
+__device__ __forceinline__ uint2 quantize16(float (&v)[16], float g, uint32_t* byte) {
+  float top = fp4_max16(v);
+  if (kFmt == TQ_FP4_MX) top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+  float d;
+  *byte = fp4_block_scale<kFmt>(top, g, &d);
+  return fp4_codes16(v, d);
+}
+
+template <typename T, int kFmt>
+__global__ void __launch_bounds__(kQuantThreads)
+fp4_quantize_kernel(const T* __restrict__ x, long long stride, long long n, int K, const float* __restrict__ scale,
+                    uint8_t* __restrict__ packed, uint8_t* __restrict__ scales) {
+  pdl_wait();
+  pdl_trigger();
+  const float g = scale ? *scale : 1.f;
+  const int lane = threadIdx.x & 31;
+  const int items = K / 16, chunks = (items + 31) / 32;
+  const long long total = n * chunks;
+  const long long warps = static_cast<long long>(gridDim.x) * (kQuantThreads / 32);
+  for (long long w = blockIdx.x * (kQuantThreads / 32ll) + (threadIdx.x >> 5); w < total; w += warps) {
+    const long long row = w / chunks;
+    const int item = static_cast<int>(w - row * chunks) * 32 + lane;
+    const bool in = item < items;
+    float v[16] = {};
+    if (in) load16(x + row * stride + 16 * item, v);
+    uint32_t byte;
+    const uint2 q = quantize16<kFmt>(v, g, &byte);
+    if (in) {
+      *reinterpret_cast<uint2*>(packed + row * (K / 2) + 8 * item) = q;
+      if (kFmt == TQ_FP4_NV)
+        scales[row * items + item] = static_cast<uint8_t>(byte);
+      else if ((lane & 1) == 0)
+        scales[row * (items / 2) + item / 2] = static_cast<uint8_t>(byte);
+    }
+  }
+}
+
+// Two E2M1 codes (low half first) as fp32.
+__device__ __forceinline__ float2 from_e2m1x2(uint32_t byte) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}"
+      : "=r"(h) : "r"(byte));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+template <typename T, int kFmt>
+__global__ void __launch_bounds__(kQuantThreads)
+fp4_dequantize_kernel(const uint8_t* __restrict__ packed, const uint8_t* __restrict__ scales, long long items,
+                      const float* __restrict__ scale, T* __restrict__ out) {
+  pdl_wait();
+  pdl_trigger();
+  const float g = scale ? *scale : 1.f;
+  const long long step = static_cast<long long>(gridDim.x) * kQuantThreads;
+  for (long long i = blockIdx.x * static_cast<long long>(kQuantThreads) + threadIdx.x; i < items; i += step) {
+    const uint2 q = __ldg(reinterpret_cast<const uint2*>(packed) + i);
+    const float s = fp4_scale_value<kFmt>(scales[kFmt == TQ_FP4_NV ? i : i / 2]);
+    T v[16];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 f = from_e2m1x2((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+      v[2 * j] = narrow<T>(__fmul_rn(__fmul_rn(f.x, s), g));
+      v[2 * j + 1] = narrow<T>(__fmul_rn(__fmul_rn(f.y, s), g));
+    }
+    uint4* const dst = reinterpret_cast<uint4*>(out + 16 * i);
+#pragma unroll
+    for (int j = 0; j < static_cast<int>(sizeof(T)); ++j) {
+      uint4 t;
+      memcpy(&t, reinterpret_cast<const char*>(v) + 16 * j, 16);
+      dst[j] = t;
+    }
+  }
+}
+
+// Row-major scales to the tiled layout: one thread per four blocks of a row,
+// padding rows and blocks zero.
+__global__ void __launch_bounds__(kQuantThreads)
+fp4_tile_scales_kernel(const uint8_t* __restrict__ scales, int E, int N, int kb, int kb4, uint32_t* __restrict__ tiled) {
+  pdl_wait();
+  pdl_trigger();
+  const int rows = (N + 127) / 128 * 128;
+  const long long total = static_cast<long long>(E) * rows * kb4;
+  const long long step = static_cast<long long>(gridDim.x) * kQuantThreads;
+  for (long long i = blockIdx.x * static_cast<long long>(kQuantThreads) + threadIdx.x; i < total; i += step) {
+    // i = ((e * row groups + group) * kb4 + b4) * 128 + (row % 32) * 4 + (row % 128) / 32
+    const int in = static_cast<int>(i & 127);
+    const long long tile = i >> 7;
+    const int b4 = static_cast<int>(tile % kb4);
+    const long long group = tile / kb4;
+    const long long e = group / (rows / 128);
+    const int r = static_cast<int>(group - e * (rows / 128)) * 128 + (in & 3) * 32 + (in >> 2);
+    uint32_t word = 0;
+    if (r < N) {
+      const uint8_t* const src = scales + (e * N + r) * kb + 4 * b4;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) word |= 4 * b4 + j < kb ? static_cast<uint32_t>(src[j]) << (8 * j) : 0u;
+    }
+    tiled[i] = word;
+  }
+}
+
+// Row `slot` of the staged activations: its m-tile and its row there.
+struct Place {
+  int slot, tile, row;
+};
+
+// The tile of a sorted slot: the last one that starts at or before it (the
+// map's first slots ascend and its tiles cover every slot).
+__device__ __forceinline__ Place place_of(int slot, const int32_t* __restrict__ tiles, int num_tiles) {
+  int lo = 0, hi = num_tiles;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(tiles + 3ll * mid + 1) <= slot) lo = mid; else hi = mid;
+  }
+  return {slot, lo, slot - __ldg(tiles + 3ll * lo + 1)};
+}
+
+// One block's share of a staged row: 16 values per thread from load(item, v),
+// their codes into the row's slots and their scales into the tiled layout of
+// each slot's m-tile (blocks past K zero, so that the MMA's last step
+// multiplies zeros by a finite scale).
+template <int kFmt, typename Load>
+__device__ __forceinline__ void stage_row(int K, float g, const Place* places, int count, int tile_m,
+                                          uint8_t* __restrict__ xq, uint8_t* __restrict__ xs, Load&& load) {
+  const int steps = fp4_steps(K);
+  const size_t tile_bytes = static_cast<size_t>((tile_m + 127) / 128) * steps * fp4_scale_step_bytes(kFmt);
+  const int items = K / 16, all = steps * (kFp4Step / 16);
+  const int lane = threadIdx.x & 31;
+  // whole warps stay in the loop together: all is a multiple of 16, a warp may end half empty
+  for (int item0 = threadIdx.x - lane; item0 < all; item0 += kQuantThreads) {
+    const int item = item0 + lane;
+    float v[16] = {};
+    if (item < items) load(item, v);
+    uint32_t byte;
+    const uint2 q = quantize16<kFmt>(v, g, &byte);
+    if (item >= items) byte = 0;
+    // four blocks' scales in one word
+    uint32_t word;
+    int word_lane;   // lane of the word's first block
+    if (kFmt == TQ_FP4_NV) {
+      word_lane = lane & ~3;
+      word = __shfl_sync(kAll, byte, word_lane) | __shfl_sync(kAll, byte, word_lane + 1) << 8 |
+             __shfl_sync(kAll, byte, word_lane + 2) << 16 | __shfl_sync(kAll, byte, word_lane + 3) << 24;
+    } else {
+      word_lane = lane & ~7;
+      word = __shfl_sync(kAll, byte, word_lane) | __shfl_sync(kAll, byte, word_lane + 2) << 8 |
+             __shfl_sync(kAll, byte, word_lane + 4) << 16 | __shfl_sync(kAll, byte, word_lane + 6) << 24;
+    }
+    const int block = kFmt == TQ_FP4_NV ? item : item / 2;
+    for (int j = 0; j < count; ++j) {
+      const Place p = places[j];
+      if (p.slot < 0) continue;
+      if (item < items) *reinterpret_cast<uint2*>(xq + static_cast<size_t>(p.slot) * (K / 2) + 8 * item) = q;
+      if (item < all && lane == word_lane)
+        *reinterpret_cast<uint32_t*>(xs + p.tile * tile_bytes + fp4_tiled_offset(kFmt, steps, p.row, block)) = word;
+    }
+  }
+}
+
+// The place of a pair from the sort's inverse; slot -1 (an expert out of
+// range) has none.
+__device__ __forceinline__ Place sorted_place(const int32_t* __restrict__ slot_of, long long pair,
+                                              const int32_t* __restrict__ tiles,
+                                              const int32_t* __restrict__ num_tiles, long long cap) {
+  const int slot = __ldg(slot_of + pair);
+  const int nt = static_cast<int>(min(static_cast<long long>(*num_tiles), cap));
+  return slot >= 0 && nt > 0 ? place_of(slot, tiles, nt) : Place{-1, 0, 0};
+}
+
+// Quantises each token's row once and writes it where the product reads it,
+// once per pair of the token.  Without slot_of a row's slot is its index and
+// its tile index / tile_m.  One block per row.
+template <typename T, int kFmt>
+__global__ void __launch_bounds__(kQuantThreads)
+fp4_stage_kernel(const T* __restrict__ x, long long stride, int K, const float* __restrict__ scale, int top_k,
+                 const int32_t* __restrict__ slot_of, const int32_t* __restrict__ tiles,
+                 const int32_t* __restrict__ num_tiles, long long cap, int tile_m, uint8_t* __restrict__ xq,
+                 uint8_t* __restrict__ xs) {
+  __shared__ Place places[32];
+  pdl_wait();
+  pdl_trigger();
+  const long long row = blockIdx.x;
+  const float g = scale ? *scale : 1.f;
+  if (static_cast<int>(threadIdx.x) < top_k) {
+    places[threadIdx.x] =
+        slot_of ? sorted_place(slot_of, row * top_k + threadIdx.x, tiles, num_tiles, cap)
+                : Place{static_cast<int>(row), static_cast<int>(row / tile_m), static_cast<int>(row % tile_m)};
+  }
+  __syncthreads();
+  stage_row<kFmt>(K, g, places, top_k, tile_m, xq, xs,
+                  [&](int item, float (&v)[16]) { load16(x + row * stride + 16 * item, v); });
+}
+
+// h = silu(gate) * up of one pair per block, quantised from fp32.  gate and up
+// are sums of the product's splits times x_scale * w_scale[expert].
+template <int kFmt>
+__global__ void __launch_bounds__(kQuantThreads)
+fp4_stage_swiglu_kernel(const float* __restrict__ part, long long split_stride, int splits,
+                        const int32_t* __restrict__ ids, const float* __restrict__ x_scale,
+                        const float* __restrict__ w_scale, int E, int I, const float* __restrict__ h_scale,
+                        const int32_t* __restrict__ slot_of, const int32_t* __restrict__ tiles,
+                        const int32_t* __restrict__ num_tiles, long long cap, int tile_m, uint8_t* __restrict__ hq,
+                        uint8_t* __restrict__ hs) {
+  __shared__ Place place;
+  pdl_wait();
+  pdl_trigger();
+  const long long pair = blockIdx.x;
+  if (threadIdx.x == 0) place = sorted_place(slot_of, pair, tiles, num_tiles, cap);
+  __syncthreads();
+  const int e = __ldg(ids + pair);
+  if (place.slot < 0 || e < 0 || e >= E) return;   // a pair without a slot has no gate and up either
+  const float alpha = (x_scale ? *x_scale : 1.f) * (w_scale ? __ldg(w_scale + e) : 1.f);
+  const float* const row = part + pair * 2 * I;
+  stage_row<kFmt>(I, h_scale ? *h_scale : 1.f, &place, 1, tile_m, hq, hs, [&](int item, float (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+      for (int s = 0; s < splits; ++s) {
+        const float* const src = row + s * split_stride + 16 * item + i;
+        const float4 c = __ldcs(reinterpret_cast<const float4*>(src));
+        const float4 d = __ldcs(reinterpret_cast<const float4*>(src + I));
+        a = make_float4(a.x + c.x, a.y + c.y, a.z + c.z, a.w + c.w);
+        b = make_float4(b.x + d.x, b.y + d.y, b.z + d.z, b.w + d.w);
+      }
+      const float gate[4] = {a.x * alpha, a.y * alpha, a.z * alpha, a.w * alpha};
+      const float up[4] = {b.x * alpha, b.y * alpha, b.z * alpha, b.w * alpha};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[i + j] = gate[j] / (1.f + expf(-gate[j])) * up[j];
+    }
+  });
+}
+
+// y[t][r] = sum_j c_tj sum_s part[s][t * top_k + j][r] in that order, in fp32,
+// rounded once; c_tj = topk_w[t][j] * x_scale * w_scale[expert].  A pair whose
+// expert is out of range adds nothing.  kVec columns per thread.
+template <typename T, int kVec>
+__global__ void __launch_bounds__(kQuantThreads)
+fp4_combine_kernel(const float* __restrict__ part, long long split_stride, int splits, const int32_t* __restrict__ ids,
+                   const float* __restrict__ topk_w, const float* __restrict__ x_scale,
+                   const float* __restrict__ w_scale, long long n, int top_k, int E, int N, T* __restrict__ y) {
+  pdl_wait();
+  pdl_trigger();
+  const int cols = N / kVec;
+  const int per_row = (cols + kQuantThreads - 1) / kQuantThreads;   // blocks per token
+  const long long t = blockIdx.x / per_row;
+  const int c = (blockIdx.x - static_cast<int>(t) * per_row) * kQuantThreads + threadIdx.x;
+  if (c >= cols) return;
+  const float xs = x_scale ? *x_scale : 1.f;
+  float sum[kVec] = {};
+  for (int j = 0; j < top_k; ++j) {
+    const long long pair = t * top_k + j;
+    const int e = ids ? __ldg(ids + pair) : 0;
+    if (e < 0 || e >= E) continue;
+    float v[kVec] = {};
+    const float* src = part + pair * N + static_cast<long long>(c) * kVec;
+    for (int s = 0; s < splits; ++s, src += split_stride) {
+      if constexpr (kVec == 4) {
+        const float4 f = __ldcs(reinterpret_cast<const float4*>(src));
+        v[0] += f.x;
+        v[1] += f.y;
+        v[2] += f.z;
+        v[3] += f.w;
+      } else {
+        v[0] += __ldcs(src);
+      }
+    }
+    const float w = (topk_w ? __ldg(topk_w + pair) : 1.f) * (xs * (w_scale ? __ldg(w_scale + e) : 1.f));
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) sum[i] += w * v[i];
+  }
+  T out[kVec];
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) out[i] = narrow<T>(sum[i]);
+  T* const dst = y + t * N + static_cast<long long>(c) * kVec;
+  if constexpr (kVec == 4 && sizeof(T) == 4) {
+    float4 o;
+    memcpy(&o, out, 16);
+    *reinterpret_cast<float4*>(dst) = o;
+  } else if constexpr (kVec == 4) {
+    uint2 o;
+    memcpy(&o, out, 8);
+    *reinterpret_cast<uint2*>(dst) = o;
+  } else {
+    dst[0] = out[0];
+  }
+}
+
+int quant_blocks(long long warps_of_work) {
+  const long long per = kQuantThreads / 32;
+  return static_cast<int>(std::max<long long>(1, std::min<long long>((warps_of_work + per - 1) / per,
+                                                                     static_cast<long long>(sm_count()) * 8)));
+}
+
+// f(T *, integral_constant fmt) for the element type and format.
+template <typename F>
+int by_type(int type, int fmt, F&& f) {
+  using NV = std::integral_constant<int, TQ_FP4_NV>;
+  using MX = std::integral_constant<int, TQ_FP4_MX>;
+  switch (type) {
+    case TQ_FP32: return fmt == TQ_FP4_NV ? f(static_cast<float*>(nullptr), NV()) : f(static_cast<float*>(nullptr), MX());
+    case TQ_BF16:
+      return fmt == TQ_FP4_NV ? f(static_cast<__nv_bfloat16*>(nullptr), NV())
+                              : f(static_cast<__nv_bfloat16*>(nullptr), MX());
+    default: return fmt == TQ_FP4_NV ? f(static_cast<__half*>(nullptr), NV()) : f(static_cast<__half*>(nullptr), MX());
+  }
+}
+
+}  // namespace
+
+int launch_fp4_quantize(const void* x, int type, int64_t stride, int64_t n, int K, int fmt, const float* scale,
+                        uint8_t* packed, uint8_t* scales, cudaStream_t s) {
+  const int chunks = (K / 16 + 31) / 32;
+  const int st = by_type(type, fmt, [&](auto* t, auto f) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    return launch_pdl(fp4_quantize_kernel<T, decltype(f)::value>, dim3(quant_blocks(n * chunks)), dim3(kQuantThreads),
+                      0, s, static_cast<const T*>(x), static_cast<long long>(stride), static_cast<long long>(n), K,
+                      scale, packed, scales);
+  });
+  if (st == TQ_OK) count_launch(kCntFp4Quantize);
+  return st;
+}
+
+int launch_fp4_dequantize(const uint8_t* packed, const uint8_t* scales, int64_t n, int K, int fmt, const float* scale,
+                          void* out, int type, cudaStream_t s) {
+  const long long items = n * (K / 16);
+  const int st = by_type(type, fmt, [&](auto* t, auto f) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    return launch_pdl(fp4_dequantize_kernel<T, decltype(f)::value>, dim3(quant_blocks((items + 31) / 32)),
+                      dim3(kQuantThreads), 0, s, packed, scales, items, scale, static_cast<T*>(out));
+  });
+  if (st == TQ_OK) count_launch(kCntFp4Dequantize);
+  return st;
+}
+
+int launch_fp4_tile_scales(const uint8_t* scales, int E, int N, int K, int fmt, uint8_t* tiled, cudaStream_t s) {
+  const int kb = K / fp4_block(fmt), kb4 = fp4_steps(K) * (kFp4Step / fp4_block(fmt)) / 4;
+  const long long words = static_cast<long long>(E) * ((N + 127) / 128 * 128) * kb4;
+  const int st = launch_pdl(fp4_tile_scales_kernel, dim3(quant_blocks((words + 31) / 32)), dim3(kQuantThreads), 0, s, scales,
+                    E, N, kb, kb4, reinterpret_cast<uint32_t*>(tiled));
+  if (st == TQ_OK) count_launch(kCntFp4TileScales);
+  return st;
+}
+
+int launch_fp4_stage(const void* x, int type, int64_t stride, int64_t n, int K, int fmt, const float* scale, int top_k,
+                     const int32_t* slot_of, const int32_t* tiles, const int32_t* num_tiles, int64_t cap, int tile_m,
+                     uint8_t* xq, uint8_t* xs, cudaStream_t s) {
+  const int st = by_type(type, fmt, [&](auto* t, auto f) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    return launch_pdl(fp4_stage_kernel<T, decltype(f)::value>, dim3(static_cast<unsigned>(n)), dim3(kQuantThreads), 0,
+                      s, static_cast<const T*>(x), static_cast<long long>(stride), K, scale, top_k, slot_of, tiles,
+                      num_tiles, static_cast<long long>(cap), tile_m, xq, xs);
+  });
+  if (st == TQ_OK) count_launch(kCntFp4Stage);
+  return st;
+}
+
+int launch_fp4_stage_swiglu(const float* part, int64_t split_stride, int splits, const int32_t* ids,
+                            const float* x_scale, const float* w_scale, int64_t P, int E, int I, int fmt,
+                            const float* h_scale, const int32_t* slot_of, const int32_t* tiles,
+                            const int32_t* num_tiles, int64_t cap, int tile_m, uint8_t* hq, uint8_t* hs,
+                            cudaStream_t s) {
+  auto kernel = fmt == TQ_FP4_NV ? fp4_stage_swiglu_kernel<TQ_FP4_NV> : fp4_stage_swiglu_kernel<TQ_FP4_MX>;
+  const int st = launch_pdl(kernel, dim3(static_cast<unsigned>(P)), dim3(kQuantThreads), 0, s, part,
+                            static_cast<long long>(split_stride), splits, ids, x_scale, w_scale, E, I, h_scale,
+                            slot_of, tiles, num_tiles, static_cast<long long>(cap), tile_m, hq, hs);
+  if (st == TQ_OK) count_launch(kCntFp4Swiglu);
+  return st;
+}
+
+int launch_fp4_combine(const float* part, int64_t split_stride, int splits, const int32_t* ids, const float* topk_w,
+                       const float* x_scale, const float* w_scale, int64_t n, int top_k, int E, int N, void* y,
+                       int type, cudaStream_t s) {
+  const bool vec = N % 4 == 0 && (reinterpret_cast<uintptr_t>(y) & 15u) == 0;
+  const int cols = vec ? N / 4 : N;
+  const long long blocks = n * ((cols + kQuantThreads - 1) / kQuantThreads);
+  if (blocks >= (1ll << 31)) return TQ_ERR_INVALID_ARG;
+  const int st = by_type(type, TQ_FP4_NV, [&](auto* t, auto) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    auto kernel = vec ? fp4_combine_kernel<T, 4> : fp4_combine_kernel<T, 1>;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kQuantThreads), 0, s, part,
+                      static_cast<long long>(split_stride), splits, ids, topk_w, x_scale, w_scale,
+                      static_cast<long long>(n), top_k, E, N, static_cast<T*>(y));
+  });
+  if (st == TQ_OK) count_launch(kCntFp4Combine);
+  return st;
+}
+
+}  // namespace tq

@@ -11,6 +11,7 @@
 // capture, only a successful answer cached).
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdio>
@@ -570,7 +571,12 @@ int tq_device_error(int* code, int* where) {
 
 void tq_launch_counts(int64_t out[TQ_NUM_LAUNCH_COUNTERS]) {
   if (!out) return;
-  for (int i = 0; i < kCntNum; ++i) out[i] = g_counts[i].load();
+  for (int i = 0; i < TQ_NUM_LAUNCH_COUNTERS; ++i) out[i] = g_counts[i].load();
+}
+
+int tq_launch_counts_all(int64_t* out, int capacity) {
+  for (int i = 0; out && i < std::min<int>(kCntNum, capacity); ++i) out[i] = g_counts[i].load();
+  return kCntNum;
 }
 
 }  // extern "C"

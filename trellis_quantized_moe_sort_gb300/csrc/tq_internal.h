@@ -20,9 +20,13 @@ int launch_status();
 
 enum Counter {
   kCntRoute = 0, kCntTileMap, kCntGrouped, kCntGemv, kCntCombine, kCntGather, kCntRouter, kCntDequant,
-  kCntRouteTileMap, kCntClear, kCntSwiglu, kCntNum
+  kCntRouteTileMap, kCntClear, kCntSwiglu,
+  // from here on only in tq_launch_counts_all
+  kCntRouterScored, kCntRouterScoredBackward, kCntFp4Quantize, kCntFp4Dequantize, kCntFp4TileScales, kCntFp4Stage,
+  kCntFp4Gemm, kCntFp4Combine, kCntFp4Swiglu, kCntNum
 };
-static_assert(kCntNum == TQ_NUM_LAUNCH_COUNTERS, "counter layout of tq_launch_counts");
+static_assert(kCntRouterScored == TQ_NUM_LAUNCH_COUNTERS, "counter layout of tq_launch_counts");
+static_assert(kCntNum == TQ_NUM_ALL_LAUNCH_COUNTERS, "counter layout of tq_launch_counts_all");
 void count_launch(Counter c);
 
 // Number of SMs of the current device (cached per device).
@@ -130,6 +134,58 @@ int launch_gemv(const uint16_t* x, const uint8_t* packed, const uint16_t* lut, i
                 const int32_t* topk_ids, const float* topk_w, int64_t n, int top_k, int E, int K,
                 int N, float* y32, int* err, cudaStream_t s, int pair_in = 0, int pair_out = 0,
                 bool early_prologue = false, uint16_t* y_tok = nullptr);
+// Arguments of the scored router, validated by the entry points.
+struct RouterArgs {
+  int64_t n, stride;   // stride: elements between rows of logits
+  const float* bias;
+  int E, top_k, score, groups, top_groups, renorm;
+  float scale;
+};
+
+// 4-bit operators (layouts: include/tqmoe.h, tq_fp4.cuh).
+int launch_fp4_quantize(const void* x, int type, int64_t stride, int64_t n, int K, int fmt, const float* scale,
+                        uint8_t* packed, uint8_t* scales, cudaStream_t s);
+int launch_fp4_dequantize(const uint8_t* packed, const uint8_t* scales, int64_t n, int K, int fmt, const float* scale,
+                          void* out, int type, cudaStream_t s);
+int launch_fp4_tile_scales(const uint8_t* scales, int E, int N, int K, int fmt, uint8_t* tiled, cudaStream_t s);
+// Activations quantised into the product's layout: codes xq [slots][K/2] and
+// tiled scales xs [tiles].  slot_of (pair -> slot) with its tile map, or
+// nullptr: row r is slot r of tile r / tile_m.
+int launch_fp4_stage(const void* x, int type, int64_t stride, int64_t n, int K, int fmt, const float* scale, int top_k,
+                     const int32_t* slot_of, const int32_t* tiles, const int32_t* num_tiles, int64_t cap, int tile_m,
+                     uint8_t* xq, uint8_t* xs, cudaStream_t s);
+// The same for h = silu(gate) * up of every pair, gate and up from the partial
+// sums part[split][pair][2I] times x_scale * w_scale[expert].
+int launch_fp4_stage_swiglu(const float* part, int64_t split_stride, int splits, const int32_t* ids,
+                            const float* x_scale, const float* w_scale, int64_t P, int E, int I, int fmt,
+                            const float* h_scale, const int32_t* slot_of, const int32_t* tiles,
+                            const int32_t* num_tiles, int64_t cap, int tile_m, uint8_t* hq, uint8_t* hs,
+                            cudaStream_t s);
+int launch_fp4_combine(const float* part, int64_t split_stride, int splits, const int32_t* ids, const float* topk_w,
+                       const float* x_scale, const float* w_scale, int64_t n, int top_k, int E, int N, void* y,
+                       int type, cudaStream_t s);
+struct Fp4Gemm {
+  int fmt;
+  const uint8_t* w;           // codes [E][N][K/2]
+  const uint8_t* w_scales;    // tiled
+  const float* w_scale;       // [E] or nullptr
+  const uint8_t* x;           // codes [P][K/2]
+  const uint8_t* x_scales;    // tiled per m-tile
+  const float* x_scale;       // [1] or nullptr
+  const int32_t* sorted_pairs;   // nullptr with tiles: one matrix, row = slot
+  const int32_t* tiles;
+  const int32_t* num_tiles;
+  int64_t cap;                // capacity of tiles, or the number of m-tiles
+  int64_t P;                  // activation rows
+  int E, K, N, tile_m, splits;
+  float* part;                // [splits][P][N] fp32, when y is nullptr
+  void* y;                    // [P][N] of y_type, scaled; splits == 1
+  int y_type;
+  int* err;
+};
+int fp4_splits(int64_t tiles, int K, int N);
+int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s);
+
 // TQ_FORCE_ARM (auto|gemv|grouped|measured) applied to an automatic pin.
 int env_pin(int pin);
 
