@@ -115,6 +115,31 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// The same wait for pipelines whose stages take well under a microsecond: the
+// first polls go by without reading %globaltimer, a read that by itself takes
+// about as long as such a stage; the limit counts from the 512th poll.
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err,
+                                                int where) {
+  for (int i = 0; i < 512; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+  }
+  return mbar_wait(bar, parity, abort_flag, err, where);
+}
+
+// True in one lane of a converged warp.  The tensor-core and bulk-copy
+// instructions take their operands from uniform registers: behind this
+// predicate the compiler knows that one thread issues them, behind lane == 0 it
+// loops over the lanes that might (about 100 cycles an instruction).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "elect.sync _|P, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, P;\n\t}"
+      : "=r"(is));
+  return is != 0;
+}
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");

@@ -133,11 +133,14 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint
   }
 }
 
-// One 512-byte scale tile (32 x 128 bits, 8-row groups of 128 bytes) to four
-// tensor-memory columns, replicated over the four lane quarters.
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t smem) {
-  const uint64_t desc = static_cast<uint64_t>((smem & 0x3FFFFu) >> 4) | static_cast<uint64_t>(16 >> 4) << 16 |
-                        static_cast<uint64_t>(128 >> 4) << 32 | static_cast<uint64_t>(1) << 46;
+// A 512-byte scale tile (32 x 128 bits, 8-row groups of 128 bytes) in shared
+// memory, and its copy to four tensor-memory columns, replicated over the four
+// lane quarters.  The address is kept in units of 16 bytes.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t smem) {
+  return static_cast<uint64_t>((smem & 0x3FFFFu) >> 4) | static_cast<uint64_t>(16 >> 4) << 16 |
+         static_cast<uint64_t>(128 >> 4) << 32 | static_cast<uint64_t>(1) << 46;
+}
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
 
@@ -164,7 +167,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const gbase = smem_raw + (base - raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   constexpr int kSfStep = fp4_scale_step_bytes(kFmt);   // per 128 rows and step
   constexpr int kSfTiles = kSfStep / 512;               // scale tiles per step (4 NV, 2 MX)
 
@@ -203,105 +206,109 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
   const long long units = static_cast<long long>(num_tiles) * p.row_blocks * p.splits;
 
   if (warp == kWarpLoad) {
-    Ring ring;
-    long long issued = 0;
-    bool ok = true;
-    for (long long u = blockIdx.x; ok && u < units; u += gridDim.x) {
-      const Unit t = unit_at(p, u, num_tiles);
-      if (!t.ok) {
-        if (lane == 0) record_error(p.err, TQ_ERR_INVALID_ARG, kWhereFp4Load);
-        continue;
-      }
-      const int w_row = t.e * p.N + t.rb * kRows;
-      const uint8_t* const wsf = p.w_scales + (static_cast<size_t>(t.e) * p.row_blocks + t.rb) * p.steps * kSfStep;
-      const uint8_t* const xsf = p.x_scales + static_cast<size_t>(t.tile) * p.steps * p.x_sf_bytes;
-      for (int k = t.k0; k < t.k1; ++k) {
-        if (!mbar_wait(bar_empty + 8 * ring.at, ring.phase ^ 1u, abort_flag, p.err, kWhereFp4Load)) {
-          ok = false;
-          break;
+    if (elect_one()) {
+      Ring ring;
+      long long issued = 0;
+      bool ok = true;
+      for (long long u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        const Unit t = unit_at(p, u, num_tiles);
+        if (!t.ok) {
+          record_error(p.err, TQ_ERR_INVALID_ARG, kWhereFp4Load);
+          continue;
         }
-        if (lane == 0) {
+        const int w_row = t.e * p.N + t.rb * kRows;
+        const uint8_t* wsf = p.w_scales +
+                             ((static_cast<size_t>(t.e) * p.row_blocks + t.rb) * p.steps + t.k0) * kSfStep;
+        // the tile's row groups are p.steps * kSfStep apart
+        const uint8_t* xsf = p.x_scales + static_cast<size_t>(t.tile) * p.steps * p.x_sf_bytes +
+                             static_cast<size_t>(t.k0) * kSfStep;
+        for (int k = t.k0; k < t.k1; ++k) {
+          if (!mbar_wait_short(bar_empty + 8 * ring.at, ring.phase ^ 1u, abort_flag, p.err, kWhereFp4Load)) {
+            ok = false;
+            break;
+          }
           const uint32_t full = bar_full + 8 * ring.at;
           const uint32_t dst = base + static_cast<uint32_t>(ring.at * p.stage_bytes);
           mbar_arrive_expect_tx(full, static_cast<uint32_t>(p.stage_bytes));
           tma_load_2d(dst, &tm_w, k * kRowBytes, w_row, full);
           tma_load_2d(dst + kWBytes, &tm_x, k * kRowBytes, t.slot0, full);
-          bulk_load(dst + kWBytes + p.x_bytes, wsf + static_cast<size_t>(k) * kSfStep, kSfStep, full);
-          // the tile's row groups are p.steps * kSfStep apart
-          for (int r = 0; r * kSfStep < p.x_sf_bytes; ++r)
-            bulk_load(dst + kWBytes + p.x_bytes + (1 + r) * kSfStep,
-                      xsf + (static_cast<size_t>(r) * p.steps + k) * kSfStep, kSfStep, full);
-        }
-        __syncwarp();
-        ++issued;
-        ring.advance(p.stages);
-      }
-    }
-    // every copy issued has landed before the CTA exits
-    const long long pending = min(issued, static_cast<long long>(p.stages));
-    for (long long i = 1; i <= pending; ++i) {
-      int st = ring.at - static_cast<int>(i);
-      uint32_t ph = ring.phase;
-      if (st < 0) {
-        st += p.stages;
-        ph ^= 1u;
-      }
-      const uint64_t t0 = globaltimer();
-      while (!mbar_try_wait(bar_full + 8 * st, ph)) {
-        if (globaltimer() - t0 > kWaitTimeoutNs) {
-          record_error(p.err, TQ_ERR_DEVICE_TIMEOUT, kWhereFp4Teardown);
-          break;
+          bulk_load(dst + kWBytes + p.x_bytes, wsf, kSfStep, full);
+          bulk_load(dst + kWBytes + p.x_bytes + kSfStep, xsf, kSfStep, full);
+          if (p.x_sf_bytes > kSfStep)
+            bulk_load(dst + kWBytes + p.x_bytes + 2 * kSfStep, xsf + static_cast<size_t>(p.steps) * kSfStep, kSfStep,
+                      full);
+          wsf += kSfStep;
+          xsf += kSfStep;
+          ++issued;
+          ring.advance(p.stages);
         }
       }
+      // every copy issued has landed before the CTA exits
+      const long long pending = min(issued, static_cast<long long>(p.stages));
+      for (long long i = 1; i <= pending; ++i) {
+        int st = ring.at - static_cast<int>(i);
+        uint32_t ph = ring.phase;
+        if (st < 0) {
+          st += p.stages;
+          ph ^= 1u;
+        }
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(bar_full + 8 * st, ph)) {
+          if (globaltimer() - t0 > kWaitTimeoutNs) {
+            record_error(p.err, TQ_ERR_DEVICE_TIMEOUT, kWhereFp4Teardown);
+            break;
+          }
+        }
+      }
     }
+    __syncwarp();
   } else if (warp == kWarpMma) {
+    // The whole warp walks the steps, so that stage addresses and descriptors
+    // stay in uniform registers; one elected thread issues.  A wait that gives
+    // up raises the abort flag, which ends the walk at the unit's end.
     Ring ring, acc;
-    bool ok = true;
-    for (long long u = blockIdx.x; ok && u < units; u += gridDim.x) {
+    const uint32_t sfa = tmem + static_cast<uint32_t>(p.sf_col);
+    const uint32_t sfb = sfa + 4 * kSfTiles;
+    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
       const Unit t = unit_at(p, u, num_tiles);
       if (!t.ok) continue;
       const uint32_t n_mma = static_cast<uint32_t>((t.rows + 15) & ~15);
-      if (!mbar_wait(bar_accempty + 8 * acc.at, acc.phase ^ 1u, abort_flag, p.err, kWhereFp4Mma)) break;
+      const bool wide = n_mma > 128;
+      const uint32_t idesc = idesc_fp4<kFmt>(n_mma, 0), idesc_odd = idesc_fp4<kFmt>(n_mma, 2);
+      mbar_wait_short(bar_accempty + 8 * acc.at, acc.phase ^ 1u, abort_flag, p.err, kWhereFp4Mma);
       tc_fence_after();
       const uint32_t d = tmem + static_cast<uint32_t>(acc.at * p.acc_cols);
       for (int k = t.k0; k < t.k1; ++k) {
-        if (!mbar_wait(bar_full + 8 * ring.at, ring.phase, abort_flag, p.err, kWhereFp4Mma)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t w = base + static_cast<uint32_t>(ring.at * p.stage_bytes);
-          const uint32_t x = w + kWBytes;
-          const uint32_t sf = x + static_cast<uint32_t>(p.x_bytes);
-          const uint32_t sfa = tmem + static_cast<uint32_t>(p.sf_col);
-          const uint32_t sfb = sfa + 4 * kSfTiles;
-          const int x_groups = (static_cast<int>(n_mma) + 127) / 128;
+        mbar_wait_short(bar_full + 8 * ring.at, ring.phase, abort_flag, p.err, kWhereFp4Mma);
+        const uint32_t w = base + static_cast<uint32_t>(ring.at * p.stage_bytes);
+        const uint64_t w_desc = smem_desc_sw128(w);
+        const uint64_t x_desc = smem_desc_sw128(w + kWBytes);
+        const uint64_t s_desc = scale_desc(w + kWBytes + static_cast<uint32_t>(p.x_bytes));
+        if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < kSfTiles; ++i) {
-            copy_scales(sfa + 4 * i, sf + 512 * i);
+            copy_scales(sfa + 4 * i, s_desc + 32 * i);
             // row group r of the tile's scales: columns 4r .. 4r + 3 of its block group
-            for (int r = 0; r < x_groups; ++r)
-              copy_scales(sfb + 8 * i + 4 * r, sf + kSfStep * (1 + r) + 512 * i);
+            copy_scales(sfb + 8 * i, s_desc + kSfStep / 16 + 32 * i);
+            if (wide) copy_scales(sfb + 8 * i + 4, s_desc + 2 * kSfStep / 16 + 32 * i);
           }
-          const int parts = min(4, (p.K - k * kFp4Step + 63) / 64);
-          for (int i = 0; i < parts; ++i) {
-            const int tile = kFmt == TQ_FP4_NV ? i : i / 2;
-            const uint32_t id = kFmt == TQ_FP4_NV ? 0u : 2u * (i & 1);
-            mma_fp4<kFmt>(d, smem_desc_sw128(w + 32 * i), smem_desc_sw128(x + 32 * i), idesc_fp4<kFmt>(n_mma, id),
-                          sfa + 4 * tile, sfb + 8 * tile, (k != t.k0 || i != 0) ? 1u : 0u);
+          // values past K are zeros with finite scales: always four MMAs
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            constexpr int kPer = 4 / kSfTiles;   // MMAs per scale tile
+            mma_fp4<kFmt>(d, w_desc + 2 * i, x_desc + 2 * i, (kPer == 2 && (i & 1)) ? idesc_odd : idesc,
+                          sfa + 4 * (i / kPer), sfb + 8 * (i / kPer), (k != t.k0 || i != 0) ? 1u : 0u);
           }
           mma_commit(bar_empty + 8 * ring.at);
+          if (k == t.k1 - 1) mma_commit(bar_accfull + 8 * acc.at);
         }
-        __syncwarp();
         ring.advance(p.stages);
       }
-      if (!ok) break;
-      if (lane == 0) mma_commit(bar_accfull + 8 * acc.at);
-      __syncwarp();
       acc.advance(p.accs);
+      if (*abort_flag) break;
     }
-    if (lane == 0) {   // every MMA issued has completed before teardown
+    __syncwarp();
+    if (elect_one()) {   // every MMA issued has completed before teardown
       mma_commit(bar_drain);
       const uint64_t t0 = globaltimer();
       while (!mbar_try_wait(bar_drain, 0)) {
@@ -333,7 +340,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
       }
       float alpha = 1.f;
       if (p.y) alpha = (p.x_scale ? __ldg(p.x_scale) : 1.f) * (p.w_scale ? __ldg(p.w_scale + t.e) : 1.f);
-      if (!mbar_wait(bar_accfull + 8 * acc.at, acc.phase, abort_flag, p.err, kWhereFp4Epilogue)) break;
+      if (!mbar_wait_short(bar_accfull + 8 * acc.at, acc.phase, abort_flag, p.err, kWhereFp4Epilogue)) break;
       tc_fence_after();
       const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(acc.at * p.acc_cols);
       const int f = t.rb * kRows + 32 * q + lane;
