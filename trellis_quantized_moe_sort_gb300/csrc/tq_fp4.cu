@@ -19,13 +19,15 @@ constexpr int64_t kMaxIndex = static_cast<int64_t>(1) << 31;
 // fit the 32-bit coordinates of the copies.
 bool bad_k(int K) { return K < 32 || K % 32 != 0; }
 
-// The smallest of 16, 32, 64, 128, 256 activation rows per m-tile that holds
+// The smallest of 16, 32, 64, 128, 224 activation rows per m-tile that holds
 // the expected rows of a matrix, with room for the spread between experts.
+// 224 is the most of which tensor memory holds two accumulators (448 columns)
+// beside a step's scales (48): a unit's drain overlaps the next unit's steps.
 int tile_for(double rows) {
-  for (int t = 16; t < 256; t <<= 1) {
+  for (int t = 16; t < 224; t <<= 1) {
     if (rows * 1.25 <= t) return t;
   }
-  return 256;
+  return 224;
 }
 int moe_tile(int64_t n, int top_k, int E) { return n > 0 ? tile_for(tq_pairs_per_woken_expert(n, top_k, E)) : 16; }
 int linear_tile(int64_t n) { return tile_for(static_cast<double>(n) / 1.25); }

@@ -50,6 +50,7 @@ struct GemmParams {
   float* part;
   void* y;
   int y_type;                    // of y; part is used when y is null
+  int y_pairs;                   // y's rows start on multiples of two values
   int* err;
   long long cap, split_stride;
   int P, E, K, N, tile_m;
@@ -58,7 +59,7 @@ struct GemmParams {
   int stages, accs, acc_cols;
   int sf_col, tmem_cols;
   int x_bytes, x_sf_bytes, stage_bytes;
-  uint32_t off_bar;
+  uint32_t off_bar, off_rows;
 };
 
 struct Ring {
@@ -150,13 +151,61 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
-__device__ __forceinline__ void store_y(const GemmParams& p, size_t at, float v) {
-  if (p.y_type == TQ_FP32)
-    static_cast<float*>(p.y)[at] = v;
-  else if (p.y_type == TQ_BF16)
-    static_cast<__nv_bfloat16*>(p.y)[at] = narrow<__nv_bfloat16>(v);
-  else
-    static_cast<__half*>(p.y)[at] = narrow<__half>(v);
+// take(values, output rows) for each 16 columns of this warp's accumulator
+// rows, the next 16 in flight meanwhile.
+template <typename Take>
+__device__ __forceinline__ void drain(uint32_t src, int rows, const int* rows_out, Take&& take) {
+  uint32_t v[2][16];
+  tmem_ld16(src, v[0]);
+#pragma unroll
+  for (int b = 0; b < 16; ++b) {
+    if (16 * b >= rows) break;
+    tmem_wait_ld();
+    if (16 * (b + 1) < rows) tmem_ld16(src + 16 * (b + 1), v[(b + 1) & 1]);
+    int row[16];
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+      const int4 r = *reinterpret_cast<const int4*>(rows_out + 16 * b + j);
+      row[j] = r.x;
+      row[j + 1] = r.y;
+      row[j + 2] = r.z;
+      row[j + 3] = r.w;
+    }
+    take(v[b & 1], row);
+  }
+}
+
+// y[row][f] = alpha * D, rounded once.  16-bit types with an even width:
+// neighbouring lanes exchange so that each stores two rows of one column.
+template <typename T>
+__device__ __forceinline__ void store_y(const GemmParams& p, uint32_t src, int rows, const int* rows_out, int f,
+                                        float alpha) {
+  T* const y = static_cast<T*>(p.y);
+  const int N = p.N;
+  if (sizeof(T) == 4 || !p.y_pairs) {
+    const bool in = f < N;
+    drain(src, rows, rows_out, [&](const uint32_t (&v)[16], const int (&row)[16]) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        if (row[j] >= 0 && in) y[static_cast<size_t>(row[j]) * N + f] = narrow<T>(__uint_as_float(v[j]) * alpha);
+      }
+    });
+  } else {
+    const bool odd = f & 1, in = (f & ~1) < N;
+    drain(src, rows, rows_out, [&](const uint32_t (&v)[16], const int (&row)[16]) {
+#pragma unroll
+      for (int j = 0; j < 16; j += 2) {
+        const uint32_t give = odd ? v[j] : v[j + 1], keep = odd ? v[j + 1] : v[j];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
+        T two[2] = {narrow<T>(__uint_as_float(odd ? got : keep) * alpha),
+                    narrow<T>(__uint_as_float(odd ? keep : got) * alpha)};
+        const int to = odd ? row[j + 1] : row[j];
+        uint32_t bits;
+        memcpy(&bits, two, 4);
+        if (to >= 0 && in) *reinterpret_cast<uint32_t*>(y + static_cast<size_t>(to) * N + (f & ~1)) = bits;
+      }
+    });
+  }
 }
 
 template <int kFmt>
@@ -204,6 +253,10 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
   const int num_tiles = p.tiles ? static_cast<int>(min(static_cast<long long>(*p.num_tiles), p.cap))
                                 : static_cast<int>(p.cap);
   const long long units = static_cast<long long>(num_tiles) * p.row_blocks * p.splits;
+  // in registers: read through the parameter they would be fetched again after
+  // every asm with a memory clobber
+  const int stages = p.stages, accs = p.accs, stage_bytes = p.stage_bytes, x_bytes = p.x_bytes;
+  int* const err = p.err;
 
   if (warp == kWarpLoad) {
     if (elect_one()) {
@@ -213,7 +266,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
       for (long long u = blockIdx.x; ok && u < units; u += gridDim.x) {
         const Unit t = unit_at(p, u, num_tiles);
         if (!t.ok) {
-          record_error(p.err, TQ_ERR_INVALID_ARG, kWhereFp4Load);
+          record_error(err, TQ_ERR_INVALID_ARG, kWhereFp4Load);
           continue;
         }
         const int w_row = t.e * p.N + t.rb * kRows;
@@ -223,39 +276,39 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
         const uint8_t* xsf = p.x_scales + static_cast<size_t>(t.tile) * p.steps * p.x_sf_bytes +
                              static_cast<size_t>(t.k0) * kSfStep;
         for (int k = t.k0; k < t.k1; ++k) {
-          if (!mbar_wait_short(bar_empty + 8 * ring.at, ring.phase ^ 1u, abort_flag, p.err, kWhereFp4Load)) {
+          if (!mbar_wait_short(bar_empty + 8 * ring.at, ring.phase ^ 1u, abort_flag, err, kWhereFp4Load)) {
             ok = false;
             break;
           }
           const uint32_t full = bar_full + 8 * ring.at;
-          const uint32_t dst = base + static_cast<uint32_t>(ring.at * p.stage_bytes);
-          mbar_arrive_expect_tx(full, static_cast<uint32_t>(p.stage_bytes));
+          const uint32_t dst = base + static_cast<uint32_t>(ring.at * stage_bytes);
+          mbar_arrive_expect_tx(full, static_cast<uint32_t>(stage_bytes));
           tma_load_2d(dst, &tm_w, k * kRowBytes, w_row, full);
           tma_load_2d(dst + kWBytes, &tm_x, k * kRowBytes, t.slot0, full);
-          bulk_load(dst + kWBytes + p.x_bytes, wsf, kSfStep, full);
-          bulk_load(dst + kWBytes + p.x_bytes + kSfStep, xsf, kSfStep, full);
+          bulk_load(dst + kWBytes + x_bytes, wsf, kSfStep, full);
+          bulk_load(dst + kWBytes + x_bytes + kSfStep, xsf, kSfStep, full);
           if (p.x_sf_bytes > kSfStep)
-            bulk_load(dst + kWBytes + p.x_bytes + 2 * kSfStep, xsf + static_cast<size_t>(p.steps) * kSfStep, kSfStep,
+            bulk_load(dst + kWBytes + x_bytes + 2 * kSfStep, xsf + static_cast<size_t>(p.steps) * kSfStep, kSfStep,
                       full);
           wsf += kSfStep;
           xsf += kSfStep;
           ++issued;
-          ring.advance(p.stages);
+          ring.advance(stages);
         }
       }
       // every copy issued has landed before the CTA exits
-      const long long pending = min(issued, static_cast<long long>(p.stages));
+      const long long pending = min(issued, static_cast<long long>(stages));
       for (long long i = 1; i <= pending; ++i) {
         int st = ring.at - static_cast<int>(i);
         uint32_t ph = ring.phase;
         if (st < 0) {
-          st += p.stages;
+          st += stages;
           ph ^= 1u;
         }
         const uint64_t t0 = globaltimer();
         while (!mbar_try_wait(bar_full + 8 * st, ph)) {
           if (globaltimer() - t0 > kWaitTimeoutNs) {
-            record_error(p.err, TQ_ERR_DEVICE_TIMEOUT, kWhereFp4Teardown);
+            record_error(err, TQ_ERR_DEVICE_TIMEOUT, kWhereFp4Teardown);
             break;
           }
         }
@@ -275,15 +328,15 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
       const uint32_t n_mma = static_cast<uint32_t>((t.rows + 15) & ~15);
       const bool wide = n_mma > 128;
       const uint32_t idesc = idesc_fp4<kFmt>(n_mma, 0), idesc_odd = idesc_fp4<kFmt>(n_mma, 2);
-      mbar_wait_short(bar_accempty + 8 * acc.at, acc.phase ^ 1u, abort_flag, p.err, kWhereFp4Mma);
+      mbar_wait_short(bar_accempty + 8 * acc.at, acc.phase ^ 1u, abort_flag, err, kWhereFp4Mma);
       tc_fence_after();
       const uint32_t d = tmem + static_cast<uint32_t>(acc.at * p.acc_cols);
       for (int k = t.k0; k < t.k1; ++k) {
-        mbar_wait_short(bar_full + 8 * ring.at, ring.phase, abort_flag, p.err, kWhereFp4Mma);
-        const uint32_t w = base + static_cast<uint32_t>(ring.at * p.stage_bytes);
+        mbar_wait_short(bar_full + 8 * ring.at, ring.phase, abort_flag, err, kWhereFp4Mma);
+        const uint32_t w = base + static_cast<uint32_t>(ring.at * stage_bytes);
         const uint64_t w_desc = smem_desc_sw128(w);
         const uint64_t x_desc = smem_desc_sw128(w + kWBytes);
-        const uint64_t s_desc = scale_desc(w + kWBytes + static_cast<uint32_t>(p.x_bytes));
+        const uint64_t s_desc = scale_desc(w + kWBytes + static_cast<uint32_t>(x_bytes));
         if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < kSfTiles; ++i) {
@@ -302,9 +355,9 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
           mma_commit(bar_empty + 8 * ring.at);
           if (k == t.k1 - 1) mma_commit(bar_accfull + 8 * acc.at);
         }
-        ring.advance(p.stages);
+        ring.advance(stages);
       }
-      acc.advance(p.accs);
+      acc.advance(accs);
       if (*abort_flag) break;
     }
     __syncwarp();
@@ -313,62 +366,63 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
       const uint64_t t0 = globaltimer();
       while (!mbar_try_wait(bar_drain, 0)) {
         if (globaltimer() - t0 > kWaitTimeoutNs) {
-          record_error(p.err, TQ_ERR_DEVICE_TIMEOUT, kWhereFp4Teardown);
+          record_error(err, TQ_ERR_DEVICE_TIMEOUT, kWhereFp4Teardown);
           break;
         }
       }
     }
     __syncwarp();
   } else {
+    // Lane l of quarter q holds weight row 32 q + l of every column.  The
+    // output row of each column is kept in shared memory (read back four at a
+    // time, the same for all lanes), -1 for none.
     const int q = warp & 3;
+    int* const rows_out = reinterpret_cast<int*>(gbase + p.off_rows) + 256 * q;
     Ring acc;
     for (long long u = blockIdx.x; u < units; u += gridDim.x) {
       const Unit t = unit_at(p, u, num_tiles);
       if (!t.ok) continue;
-      int pair[8];   // of columns lane + 32 i
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int col = lane + 32 * i;
-        pair[i] = -1;
+      __syncwarp();   // the last unit's rows have been read
+      for (int col = lane; col < ((t.rows + 15) & ~15); col += 32) {
+        int pair = -1;
         if (col < t.rows) {
-          pair[i] = p.sorted_pairs ? __ldg(p.sorted_pairs + t.slot0 + col) : t.slot0 + col;
-          if (pair[i] < 0 || pair[i] >= p.P) {
-            record_error(p.err, TQ_ERR_INVALID_ARG, kWhereFp4Epilogue);
-            pair[i] = -1;
+          pair = p.sorted_pairs ? __ldg(p.sorted_pairs + t.slot0 + col) : t.slot0 + col;
+          if (pair < 0 || pair >= p.P) {
+            record_error(err, TQ_ERR_INVALID_ARG, kWhereFp4Epilogue);
+            pair = -1;
           }
         }
+        rows_out[col] = pair;
       }
-      float alpha = 1.f;
-      if (p.y) alpha = (p.x_scale ? __ldg(p.x_scale) : 1.f) * (p.w_scale ? __ldg(p.w_scale + t.e) : 1.f);
-      if (!mbar_wait_short(bar_accfull + 8 * acc.at, acc.phase, abort_flag, p.err, kWhereFp4Epilogue)) break;
+      __syncwarp();
+      if (!mbar_wait_short(bar_accfull + 8 * acc.at, acc.phase, abort_flag, err, kWhereFp4Epilogue)) break;
       tc_fence_after();
       const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(acc.at * p.acc_cols);
       const int f = t.rb * kRows + 32 * q + lane;
-      float* const out = p.part + static_cast<size_t>(t.split) * p.split_stride + f;
+      if (!p.y) {
+        float* const out = p.part + static_cast<size_t>(t.split) * p.split_stride + f;
+        const int N = p.N;
+        const bool in = f < N;
+        drain(src, t.rows, rows_out, [&](const uint32_t (&v)[16], const int (&row)[16]) {
 #pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        if (32 * b >= t.rows) break;
-        uint32_t v[2][16];
-        tmem_ld16(src + 32 * b, v[0]);
-        if (32 * b + 16 < t.rows) tmem_ld16(src + 32 * b + 16, v[1]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          if (32 * b + j >= t.rows) break;
-          const int to = __shfl_sync(0xffffffffu, pair[b], j);
-          if (to >= 0 && f < p.N) {
-            const float r = __uint_as_float(v[j >> 4][j & 15]);
-            if (p.y)
-              store_y(p, static_cast<size_t>(to) * p.N + f, r * alpha);
-            else
-              out[static_cast<size_t>(to) * p.N] = r;
+          for (int j = 0; j < 16; ++j) {
+            if (row[j] >= 0 && in) out[static_cast<size_t>(row[j]) * N] = __uint_as_float(v[j]);
           }
+        });
+      } else {
+        const float alpha = (p.x_scale ? __ldg(p.x_scale) : 1.f) * (p.w_scale ? __ldg(p.w_scale + t.e) : 1.f);
+        if (p.y_type == TQ_FP32) {
+          store_y<float>(p, src, t.rows, rows_out, f, alpha);
+        } else if (p.y_type == TQ_BF16) {
+          store_y<__nv_bfloat16>(p, src, t.rows, rows_out, f, alpha);
+        } else {
+          store_y<__half>(p, src, t.rows, rows_out, f, alpha);
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_accempty + 8 * acc.at);
-      acc.advance(p.accs);
+      acc.advance(accs);
     }
   }
 
@@ -441,6 +495,7 @@ int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s) {
   p.part = g.part;
   p.y = g.y;
   p.y_type = g.y_type;
+  p.y_pairs = g.N % 2 == 0 && (reinterpret_cast<uintptr_t>(g.y) & 3u) == 0;
   p.err = g.err;
   p.cap = g.cap;
   p.split_stride = static_cast<long long>(g.P) * g.N;
@@ -459,11 +514,12 @@ int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s) {
   p.x_bytes = p.n_max * kRowBytes;
   p.x_sf_bytes = x_groups * sf_step;
   p.stage_bytes = kWBytes + p.x_bytes + sf_step + p.x_sf_bytes;
-  const int bar_bytes = 8 * kNumBars + 16;
-  p.stages = std::min(kMaxStages, (kSmemLimit - 1024 - bar_bytes) / p.stage_bytes);
+  const int bar_bytes = (8 * kNumBars + 16 + 15) / 16 * 16, rows_bytes = 4 * 256 * 4;
+  p.stages = std::min(kMaxStages, (kSmemLimit - 1024 - bar_bytes - rows_bytes) / p.stage_bytes);
   p.off_bar = static_cast<uint32_t>(p.stages * p.stage_bytes);
+  p.off_rows = p.off_bar + bar_bytes;
   // one CTA (and one tensor-memory allocation) per SM
-  const int smem = std::max(1024 + p.stages * p.stage_bytes + bar_bytes, 120 * 1024);
+  const int smem = std::max(1024 + p.stages * p.stage_bytes + bar_bytes + rows_bytes, 120 * 1024);
 
   // Tensor memory: accumulators, then the scales of one step (4 columns per
   // scale tile of the weights, 8 of the activations).
