@@ -550,9 +550,11 @@ int tq_fp4_tile_scales(const uint8_t* scales, int E, int N, int K, int fmt, uint
  *   y[t] = sum_j topk_w[t][j] W_down h(t,j).
  * x as in tq_fp4_quantize; packed and tiled_scales (tq_fp4_tile_scales) 16-byte
  * aligned; y (device) dense [n][N] (or [n][H]).  N is any width; K, H and I are
- * multiples of 32.  E <= 1024, top_k <= 32.  workspace (device) of at least
- * the matching *_workspace_size() bytes (0 on invalid arguments), 256-byte
- * aligned; its contents are undefined after the call.
+ * multiples of 32.  E <= 1024, top_k <= 32.  Few rows (by a rule on n, top_k,
+ * E, K and N) take one launch that needs no workspace.  workspace (device) of
+ * at least the matching *_workspace_size() bytes (0 on invalid arguments; 256,
+ * or a NULL workspace, where none is needed), 256-byte aligned; its contents
+ * are undefined after the call.
  * ------------------------------------------------------------------------- */
 size_t tq_fp4_linear_workspace_size(int64_t n, int K, int N, int fmt);
 int tq_fp4_linear(const void* x, int x_type, int64_t x_stride, const uint8_t* packed,
@@ -616,9 +618,9 @@ void tq_launch_counts(int64_t out[TQ_NUM_LAUNCH_COUNTERS]);
 /* The same and the counters that came later: out[11] scored router, out[12] its
  * backward, out[13] 4-bit quantise, out[14] dequantise, out[15] scale tiling,
  * out[16] activation staging, out[17] 4-bit GEMM, out[18] 4-bit combine,
- * out[19] SwiGLU staging.  Writes the first `capacity` of them and returns how
+ * out[19] SwiGLU staging, out[20] 4-bit GEMV.  Writes the first `capacity` of them and returns how
  * many there are. */
-#define TQ_NUM_ALL_LAUNCH_COUNTERS 20
+#define TQ_NUM_ALL_LAUNCH_COUNTERS 21
 int tq_launch_counts_all(int64_t* out, int capacity);
 
 #ifdef __cplusplus

@@ -622,7 +622,8 @@ def tq_launch_counts_all() -> dict:
 
 
 ALL_LAUNCH_COUNTERS = LAUNCH_COUNTERS + ("router_scored", "router_scored_backward", "fp4_quantize", "fp4_dequantize",
-                                         "fp4_tile_scales", "fp4_stage", "fp4_gemm", "fp4_combine", "fp4_swiglu")
+                                         "fp4_tile_scales", "fp4_stage", "fp4_gemm", "fp4_combine", "fp4_swiglu",
+                                         "fp4_gemv")
 
 
 # ------------------------------------------------------------------ scored router, 4-bit operators
@@ -801,10 +802,15 @@ def _fp4_matrix(packed, tiled_scales, E, N, K, fmt, name):
 
 
 def _workspace(workspace, need, device):
+    """(address, bytes) of the caller's workspace or of a new one (none where the call needs none)
+    and the tensor, to be kept until the call is enqueued."""
     torch = _torch()
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
-    return workspace, _dev_ptr(workspace, (torch.uint8,), "workspace")
+        if need <= 256:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        return workspace.data_ptr(), need, workspace
+    return _dev_ptr(workspace, (torch.uint8,), "workspace"), workspace.numel(), workspace
 
 
 def tq_fp4_linear_workspace_size(n: int, K: int, N: int, fmt: int = FP4_NV) -> int:
@@ -821,11 +827,11 @@ def tq_fp4_linear(x, packed, tiled_scales, fmt: int = FP4_NV, w_scale=None, x_sc
     n, K = x.shape
     N = packed.shape[-2]
     w_ptr, s_ptr = _fp4_matrix(packed, tiled_scales, 1, N, K, fmt, "packed")
-    workspace, ws_ptr = _workspace(workspace, tq_fp4_linear_workspace_size(n, K, N, fmt) if workspace is None else 0,
+    ws_ptr, ws_bytes, workspace = _workspace(workspace, tq_fp4_linear_workspace_size(n, K, N, fmt) if workspace is None else 0,
                                    x.device)
     y = torch.empty((n, N), dtype=x.dtype, device=x.device) if y is None else y
     _check(lib().tq_fp4_linear(ptr, code, step, w_ptr, s_ptr, fmt, _scale_ptr(w_scale, 1, "w_scale"),
-                               _scale_ptr(x_scale, 1, "x_scale"), n, K, N, ws_ptr, workspace.numel(),
+                               _scale_ptr(x_scale, 1, "x_scale"), n, K, N, ws_ptr, ws_bytes,
                                _out_ptr(y, (n, N), (), "y"), _type_code(y.dtype, "y"), _stream(stream)),
            "tq_fp4_linear")
     return y
@@ -847,7 +853,7 @@ def tq_fp4_moe_forward(x, packed, tiled_scales, topk_ids, topk_w, fmt: int = FP4
     E, N, _ = packed.shape
     top_k = topk_ids.shape[1]
     w_ptr, s_ptr = _fp4_matrix(packed, tiled_scales, E, N, K, fmt, "packed")
-    workspace, ws_ptr = _workspace(workspace,
+    ws_ptr, ws_bytes, workspace = _workspace(workspace,
                                    tq_fp4_moe_workspace_size(n, top_k, E, K, N, fmt) if workspace is None else 0,
                                    x.device)
     y = torch.empty((n, N), dtype=x.dtype, device=x.device) if y is None else y
@@ -855,7 +861,7 @@ def tq_fp4_moe_forward(x, packed, tiled_scales, topk_ids, topk_w, fmt: int = FP4
                                     _scale_ptr(x_scale, 1, "x_scale"),
                                     _out_ptr(topk_ids, (n, top_k), (torch.int32,), "topk_ids"),
                                     _out_ptr(topk_w, (n, top_k), (torch.float32,), "topk_w"), n, top_k, E, K, N,
-                                    ws_ptr, workspace.numel(), _out_ptr(y, (n, N), (), "y"), _type_code(y.dtype, "y"),
+                                    ws_ptr, ws_bytes, _out_ptr(y, (n, N), (), "y"), _type_code(y.dtype, "y"),
                                     _stream(stream)), "tq_fp4_moe_forward")
     return y
 
@@ -878,7 +884,7 @@ def tq_fp4_moe_mlp_forward(x, packed_gu, tiled_gu, packed_down, tiled_down, topk
     top_k = topk_ids.shape[1]
     gu_ptr, gus_ptr = _fp4_matrix(packed_gu, tiled_gu, E, 2 * I, H, fmt, "packed_gu")
     d_ptr, ds_ptr = _fp4_matrix(packed_down, tiled_down, E, H, I, fmt, "packed_down")
-    workspace, ws_ptr = _workspace(workspace,
+    ws_ptr, ws_bytes, workspace = _workspace(workspace,
                                    tq_fp4_moe_mlp_workspace_size(n, top_k, E, H, I, fmt) if workspace is None else 0,
                                    x.device)
     y = torch.empty((n, H), dtype=x.dtype, device=x.device) if y is None else y
@@ -886,6 +892,6 @@ def tq_fp4_moe_mlp_forward(x, packed_gu, tiled_gu, packed_down, tiled_down, topk
         ptr, code, step, gu_ptr, gus_ptr, _scale_ptr(gu_scale, E, "gu_scale"), d_ptr, ds_ptr,
         _scale_ptr(down_scale, E, "down_scale"), fmt, _scale_ptr(x_scale, 1, "x_scale"),
         _scale_ptr(h_scale, 1, "h_scale"), _out_ptr(topk_ids, (n, top_k), (torch.int32,), "topk_ids"),
-        _out_ptr(topk_w, (n, top_k), (torch.float32,), "topk_w"), n, top_k, E, H, I, ws_ptr, workspace.numel(),
+        _out_ptr(topk_w, (n, top_k), (torch.float32,), "topk_w"), n, top_k, E, H, I, ws_ptr, ws_bytes,
         _out_ptr(y, (n, H), (), "y"), _type_code(y.dtype, "y"), _stream(stream)), "tq_fp4_moe_mlp_forward")
     return y

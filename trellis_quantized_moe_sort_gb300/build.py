@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtqmoe.so")
 SOURCES = ["tq_host.cu", "tq_route.cu", "tq_grouped.cu", "tq_gemv.cu", "tq_noalloc.cu", "tq_probe.cu", "tq_mlp.cu", "tq_dequant.cu",
-           "tq_router.cu", "tq_fp4_quant.cu", "tq_fp4_gemm.cu", "tq_fp4.cu"]
+           "tq_router.cu", "tq_fp4_quant.cu", "tq_fp4_gemm.cu", "tq_fp4_gemv.cu", "tq_fp4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

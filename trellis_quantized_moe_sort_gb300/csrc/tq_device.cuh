@@ -14,7 +14,7 @@ enum ErrWhere : int {
   kWhereRoute = 1, kWhereTileMap = 2, kWhereGroupedProducer = 3, kWhereGroupedDecode = 4,
   kWhereGroupedMma = 5, kWhereGroupedEpilogue = 6, kWhereGroupedTeardown = 7, kWhereDequant = 8,
   kWhereTableStage = 9, kWhereProbe = 10, kWhereRouter = 11, kWhereFp4Load = 12, kWhereFp4Mma = 13,
-  kWhereFp4Epilogue = 14, kWhereFp4Teardown = 15,
+  kWhereFp4Epilogue = 14, kWhereFp4Teardown = 15, kWhereFp4Gemv = 16,
 };
 
 // A wait gives up after this long (ns of %globaltimer) and reports

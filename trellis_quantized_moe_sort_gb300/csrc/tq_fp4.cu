@@ -13,6 +13,7 @@ namespace {
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool bad_format(int fmt) { return fmt != TQ_FP4_NV && fmt != TQ_FP4_MX; }
+constexpr size_t kNoWorkspace = 256;   // reported where none is used; a null workspace will do
 constexpr int64_t kMaxIndex = static_cast<int64_t>(1) << 31;
 
 // Rows of fp4 values: K a multiple of 32, and small enough that a row's bytes
@@ -31,6 +32,22 @@ int tile_for(double rows) {
 }
 int moe_tile(int64_t n, int top_k, int E) { return n > 0 ? tile_for(tq_pairs_per_woken_expert(n, top_k, E)) : 16; }
 int linear_tile(int64_t n) { return tile_for(static_cast<double>(n) / 1.25); }
+
+// Whether a product takes the one-launch GEMV, which reads a matrix once per
+// activation row, or the tensor-core chain (three or four launches), which
+// reads it once per m-tile.  Times in us in a CUDA graph, u = N K / (2048 x
+// 4096), measured at u = 1, n rows: GEMV 3.8, 5.6, 8.7, 15.8 at 1, 2, 4, 8 rows
+// of a linear and 10.4, 17.6, 29.3, 55.0 at 1, 2, 4, 8 tokens of top-6 of 256;
+// the chain 7.9, 7.7, 7.8, 7.9 and 21.9, 26.1, 35.1, 53.1.
+bool takes_gemv(int64_t n, int top_k, double matrices, double chain_us, int K, int N) {
+  if (n > 64 || K > kFp4GemvMaxK) return false;
+  const double u = static_cast<double>(N) * K / (2048.0 * 4096.0);
+  return 2.0 + u * n * (0.65 + top_k) <= chain_us + 0.75 * u * matrices;
+}
+bool linear_gemv(int64_t n, int K, int N) { return takes_gemv(n, 1, 1.0, 7.0, K, N); }
+bool moe_gemv(int64_t n, int top_k, int E, int K, int N) {
+  return n > 0 && takes_gemv(n, top_k, n * top_k / tq_pairs_per_woken_expert(n, top_k, E), 15.0, K, N);
+}
 
 size_t staged_scale_bytes(int64_t tiles, int tile_m, int K, int fmt) {
   return static_cast<size_t>(tiles) * ((tile_m + 127) / 128) * fp4_steps(K) * fp4_scale_step_bytes(fmt);
@@ -201,7 +218,7 @@ int tq_fp4_tile_scales(const uint8_t* scales, int E, int N, int K, int fmt, uint
 
 size_t tq_fp4_linear_workspace_size(int64_t n, int K, int N, int fmt) {
   if (n < 0 || n >= kMaxIndex || bad_matrix(1, K, N) || bad_format(fmt)) return 0;
-  return plan_linear(nullptr, n, K, N, fmt).bytes;
+  return linear_gemv(n, K, N) ? kNoWorkspace : plan_linear(nullptr, n, K, N, fmt).bytes;
 }
 
 int tq_fp4_linear(const void* x, int x_type, int64_t x_stride, const uint8_t* packed, const uint8_t* tiled_scales,
@@ -213,13 +230,19 @@ int tq_fp4_linear(const void* x, int x_type, int64_t x_stride, const uint8_t* pa
   if (n > 0 && (!packed || !tiled_scales || !y || !aligned(packed, 16) || !aligned(tiled_scales, 16) ||
                 !aligned(y, type_size(y_type))))
     return TQ_ERR_INVALID_ARG;
+  const bool gemv = linear_gemv(n, K, N);
   const LinearPlan l = plan_linear(workspace, n, K, N, fmt);
-  if (n > 0 && bad_workspace(workspace, workspace_bytes, l.bytes)) return TQ_ERR_WORKSPACE;
+  if (n > 0 && !gemv && bad_workspace(workspace, workspace_bytes, l.bytes)) return TQ_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int rc = require_sm103(s);
   if (rc != TQ_OK || n == 0) return rc;
   int* err = error_word(&rc);
   if (!err) return rc;
+  if (gemv) {
+    const Fp4Gemv v{fmt, packed, tiled_scales, w_scale, x, x_type, x_stride, x_scale, nullptr, nullptr, n, 1, 1, K, N,
+                    y, y_type, err};
+    return launch_fp4_gemv(v, s);
+  }
   rc = launch_fp4_stage(x, x_type, x_stride, n, K, fmt, x_scale, 1, nullptr, nullptr, nullptr, l.tiles, l.tile_m,
                         l.staged.codes, l.staged.scales, s);
   if (rc != TQ_OK) return rc;
@@ -232,7 +255,7 @@ int tq_fp4_linear(const void* x, int x_type, int64_t x_stride, const uint8_t* pa
 
 size_t tq_fp4_moe_workspace_size(int64_t n, int top_k, int E, int K, int N, int fmt) {
   if (bad_moe_shape(n, top_k, E) || bad_matrix(E, K, N) || bad_format(fmt)) return 0;
-  return plan_moe(nullptr, n, top_k, E, K, N, fmt).bytes;
+  return moe_gemv(n, top_k, E, K, N) ? kNoWorkspace : plan_moe(nullptr, n, top_k, E, K, N, fmt).bytes;
 }
 
 int tq_fp4_moe_forward(const void* x, int x_type, int64_t x_stride, const uint8_t* packed, const uint8_t* tiled_scales,
@@ -245,13 +268,19 @@ int tq_fp4_moe_forward(const void* x, int x_type, int64_t x_stride, const uint8_
   if (n > 0 && (!packed || !tiled_scales || !topk_ids || !topk_w || !y || !aligned(packed, 16) ||
                 !aligned(tiled_scales, 16) || !aligned(y, type_size(y_type))))
     return TQ_ERR_INVALID_ARG;
+  const bool gemv = moe_gemv(n, top_k, E, K, N);
   const MoePlan m = plan_moe(workspace, n, top_k, E, K, N, fmt);
-  if (n > 0 && bad_workspace(workspace, workspace_bytes, m.bytes)) return TQ_ERR_WORKSPACE;
+  if (n > 0 && !gemv && bad_workspace(workspace, workspace_bytes, m.bytes)) return TQ_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int rc = require_sm103(s);
   if (rc != TQ_OK || n == 0) return rc;
   int* err = error_word(&rc);
   if (!err) return rc;
+  if (gemv) {
+    const Fp4Gemv v{fmt, packed, tiled_scales, w_scale, x, x_type, x_stride, x_scale, topk_ids, topk_w, n, top_k, E, K,
+                    N, y, y_type, err};
+    return launch_fp4_gemv(v, s);
+  }
   rc = route_pairs(m.routed, topk_ids, m.P, E, m.tile_m, m.cap, err, s);
   if (rc == TQ_OK)
     rc = launch_fp4_stage(x, x_type, x_stride, n, K, fmt, x_scale, top_k, m.routed.slot_of, m.routed.tiles,

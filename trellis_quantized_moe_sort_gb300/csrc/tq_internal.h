@@ -23,7 +23,7 @@ enum Counter {
   kCntRouteTileMap, kCntClear, kCntSwiglu,
   // from here on only in tq_launch_counts_all
   kCntRouterScored, kCntRouterScoredBackward, kCntFp4Quantize, kCntFp4Dequantize, kCntFp4TileScales, kCntFp4Stage,
-  kCntFp4Gemm, kCntFp4Combine, kCntFp4Swiglu, kCntNum
+  kCntFp4Gemm, kCntFp4Combine, kCntFp4Swiglu, kCntFp4Gemv, kCntNum
 };
 static_assert(kCntRouterScored == TQ_NUM_LAUNCH_COUNTERS, "counter layout of tq_launch_counts");
 static_assert(kCntNum == TQ_NUM_ALL_LAUNCH_COUNTERS, "counter layout of tq_launch_counts_all");
@@ -183,6 +183,27 @@ struct Fp4Gemm {
   int y_type;
   int* err;
 };
+// y[t] = sum_j topk_w[t][j] W_{ids[t][j]} x[t] (ids nullptr: one matrix) in
+// one launch, x quantised inside; n < 65536, K <= kFp4GemvMaxK.
+struct Fp4Gemv {
+  int fmt;
+  const uint8_t* w;
+  const uint8_t* w_scales;    // tiled
+  const float* w_scale;
+  const void* x;
+  int x_type;
+  int64_t stride;
+  const float* x_scale;
+  const int32_t* ids;
+  const float* topk_w;
+  int64_t n;
+  int top_k, E, K, N;
+  void* y;
+  int y_type;
+  int* err;
+};
+constexpr int kFp4GemvMaxK = 16384;   // x in shared memory, 2.25 bytes a value
+int launch_fp4_gemv(const Fp4Gemv& g, cudaStream_t s);
 int fp4_splits(int64_t tiles, int K, int N);
 int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s);
 
