@@ -655,7 +655,7 @@ def _rows(t, name):
         raise ValueError(f"{name} must have two dimensions, not {t.dim()}")
     n, width = t.shape
     step, inner = t.stride()
-    if inner != 1 and width > 1:
+    if inner != 1 and width > 1 and n > 0:
         raise ValueError(f"{name} must have contiguous rows")
     return t.data_ptr(), code, step if n > 1 else width
 
