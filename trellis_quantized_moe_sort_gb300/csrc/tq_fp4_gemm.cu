@@ -34,8 +34,8 @@ constexpr int kRowBytes = kFp4Step / 2; // a step of one row: one 128-byte swizz
 constexpr int kWBytes = kRows * kRowBytes;
 constexpr int kMaxStages = 12;
 constexpr int kMaxAcc = 4;
-constexpr int kThreads = 192;
-constexpr int kWarpLoad = 0, kWarpMma = 1;   // warps 2-5: epilogue, one per lane quarter
+constexpr int kThreads = 224;
+constexpr int kWarpLoadW = 0, kWarpMma = 1, kWarpLoadX = 6;   // warps 2-5: epilogue, one per lane quarter
 constexpr int kSmemLimit = 232448;
 constexpr int kNumBars = 2 * kMaxStages + 2 * kMaxAcc + 1;
 
@@ -134,13 +134,19 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint
   }
 }
 
-// A 512-byte scale tile (32 x 128 bits, 8-row groups of 128 bytes) in shared
-// memory, and its copy to four tensor-memory columns, replicated over the four
-// lane quarters.  The address is kept in units of 16 bytes.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t smem) {
-  return static_cast<uint64_t>((smem & 0x3FFFFu) >> 4) | static_cast<uint64_t>(16 >> 4) << 16 |
-         static_cast<uint64_t>(128 >> 4) << 32 | static_cast<uint64_t>(1) << 46;
+// Shared-memory descriptors from an address in units of 16 bytes: a K-major
+// operand in 128-byte swizzled rows (8-row groups 1024 bytes apart), and a
+// 512-byte scale tile (32 x 128 bits, 8-row groups of 128 bytes).
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t at) {
+  return static_cast<uint64_t>(at) | static_cast<uint64_t>(1) << 16 | static_cast<uint64_t>(1024 >> 4) << 32 |
+         static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
 }
+__device__ __forceinline__ uint64_t scale_desc(uint32_t at) {
+  return static_cast<uint64_t>(at) | static_cast<uint64_t>(1) << 16 | static_cast<uint64_t>(128 >> 4) << 32 |
+         static_cast<uint64_t>(1) << 46;
+}
+// Copies a scale tile to four tensor-memory columns, replicated over the four
+// lane quarters.
 __device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
@@ -230,7 +236,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
-      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_full + 8 * s, 2);
       mbar_init(bar_empty + 8 * s, 1);
     }
     for (int a = 0; a < p.accs; ++a) {
@@ -243,7 +249,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
     tma_prefetch_desc(&tm_w);
     tma_prefetch_desc(&tm_x);
   }
-  if (warp == kWarpLoad) tmem_alloc(smem_u32(tmem_holder), static_cast<uint32_t>(p.tmem_cols));
+  if (warp == kWarpLoadW) tmem_alloc(smem_u32(tmem_holder), static_cast<uint32_t>(p.tmem_cols));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -258,42 +264,49 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
   const int stages = p.stages, accs = p.accs, stage_bytes = p.stage_bytes, x_bytes = p.x_bytes;
   int* const err = p.err;
 
-  if (warp == kWarpLoad) {
+  if (warp == kWarpLoadW || warp == kWarpLoadX) {
+    // Two warps load, one thread each: the weights' codes and scales, and the
+    // activations'.  (One thread for both took about 500 cycles a step, as long
+    // as the step's MMAs.)
     if (elect_one()) {
+      const bool is_w = warp == kWarpLoadW;
+      const uint32_t bytes = static_cast<uint32_t>(is_w ? kWBytes + kSfStep : x_bytes + p.x_sf_bytes);
+      const uint32_t to_codes = is_w ? 0u : kWBytes;
+      const uint32_t to_scales = static_cast<uint32_t>(kWBytes + x_bytes + (is_w ? 0 : kSfStep));
+      const bool two_groups = !is_w && p.x_sf_bytes > kSfStep;
+      const CUtensorMap* const map = is_w ? &tm_w : &tm_x;
+      const size_t group = static_cast<size_t>(p.steps) * kSfStep;   // scales of one 128-row group
+      const uint8_t* const scales = is_w ? p.w_scales : p.x_scales;
+      const int x_groups = p.x_sf_bytes / kSfStep;
       Ring ring;
       long long issued = 0;
-      bool ok = true;
+      bool ok = true, ready = false;
       for (long long u = blockIdx.x; ok && u < units; u += gridDim.x) {
         const Unit t = unit_at(p, u, num_tiles);
         if (!t.ok) {
-          record_error(err, TQ_ERR_INVALID_ARG, kWhereFp4Load);
+          if (is_w) record_error(err, TQ_ERR_INVALID_ARG, kWhereFp4Load);
           continue;
         }
-        const int w_row = t.e * p.N + t.rb * kRows;
-        const uint8_t* wsf = p.w_scales +
-                             ((static_cast<size_t>(t.e) * p.row_blocks + t.rb) * p.steps + t.k0) * kSfStep;
-        // the tile's row groups are p.steps * kSfStep apart
-        const uint8_t* xsf = p.x_scales + static_cast<size_t>(t.tile) * p.steps * p.x_sf_bytes +
-                             static_cast<size_t>(t.k0) * kSfStep;
+        const int row = is_w ? t.e * p.N + t.rb * kRows : t.slot0;
+        const uint8_t* sf = scales + static_cast<size_t>(t.k0) * kSfStep +
+                            (is_w ? static_cast<size_t>(t.e) * p.row_blocks + t.rb
+                                  : static_cast<size_t>(t.tile) * x_groups) * group;
         for (int k = t.k0; k < t.k1; ++k) {
-          if (!mbar_wait_short(bar_empty + 8 * ring.at, ring.phase ^ 1u, abort_flag, err, kWhereFp4Load)) {
+          if (!ready &&
+              !mbar_wait_short(bar_empty + 8 * ring.at, ring.phase ^ 1u, abort_flag, err, kWhereFp4Load)) {
             ok = false;
             break;
           }
           const uint32_t full = bar_full + 8 * ring.at;
           const uint32_t dst = base + static_cast<uint32_t>(ring.at * stage_bytes);
-          mbar_arrive_expect_tx(full, static_cast<uint32_t>(stage_bytes));
-          tma_load_2d(dst, &tm_w, k * kRowBytes, w_row, full);
-          tma_load_2d(dst + kWBytes, &tm_x, k * kRowBytes, t.slot0, full);
-          bulk_load(dst + kWBytes + x_bytes, wsf, kSfStep, full);
-          bulk_load(dst + kWBytes + x_bytes + kSfStep, xsf, kSfStep, full);
-          if (p.x_sf_bytes > kSfStep)
-            bulk_load(dst + kWBytes + x_bytes + 2 * kSfStep, xsf + static_cast<size_t>(p.steps) * kSfStep, kSfStep,
-                      full);
-          wsf += kSfStep;
-          xsf += kSfStep;
+          mbar_arrive_expect_tx(full, bytes);
+          tma_load_2d(dst + to_codes, map, k * kRowBytes, row, full);
+          bulk_load(dst + to_scales, sf, kSfStep, full);
+          if (two_groups) bulk_load(dst + to_scales + kSfStep, sf + group, kSfStep, full);
+          sf += kSfStep;
           ++issued;
           ring.advance(stages);
+          ready = mbar_test(bar_empty + 8 * ring.at, ring.phase ^ 1u);
         }
       }
       // every copy issued has landed before the CTA exits
@@ -319,9 +332,18 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
     // The whole warp walks the steps, so that stage addresses and descriptors
     // stay in uniform registers; one elected thread issues.  A wait that gives
     // up raises the abort flag, which ends the walk at the unit's end.
-    Ring ring, acc;
     const uint32_t sfa = tmem + static_cast<uint32_t>(p.sf_col);
     const uint32_t sfb = sfa + 4 * kSfTiles;
+    // A stage's operands are at fixed distances from its start: one running
+    // 16-byte address serves the low words of the three descriptors, whose high
+    // words never change.
+    const uint32_t desc0 = (base & 0x3FFFFu) >> 4, desc_end = desc0 + static_cast<uint32_t>(stages * stage_bytes) / 16;
+    const uint32_t desc_stage = static_cast<uint32_t>(stage_bytes) / 16, desc_sf = static_cast<uint32_t>(kWBytes + x_bytes) / 16;
+    const uint32_t bar_end = bar_full + 8 * stages;
+    uint32_t desc = desc0, bar = bar_full, phase = 0;
+    bool ready = false;
+    const bool leader = elect_one();
+    Ring acc;
     for (long long u = blockIdx.x; u < units; u += gridDim.x) {
       const Unit t = unit_at(p, u, num_tiles);
       if (!t.ok) continue;
@@ -332,12 +354,20 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
       tc_fence_after();
       const uint32_t d = tmem + static_cast<uint32_t>(acc.at * p.acc_cols);
       for (int k = t.k0; k < t.k1; ++k) {
-        mbar_wait_short(bar_full + 8 * ring.at, ring.phase, abort_flag, err, kWhereFp4Mma);
-        const uint32_t w = base + static_cast<uint32_t>(ring.at * stage_bytes);
-        const uint64_t w_desc = smem_desc_sw128(w);
-        const uint64_t x_desc = smem_desc_sw128(w + kWBytes);
-        const uint64_t s_desc = scale_desc(w + kWBytes + static_cast<uint32_t>(x_bytes));
-        if (elect_one()) {
+        if (!ready) mbar_wait_short(bar, phase, abort_flag, err, kWhereFp4Mma);
+        const uint32_t this_bar = bar, this_desc = desc;
+        desc += desc_stage;
+        bar += 8;
+        if (bar == bar_end) {
+          desc = desc0;
+          bar = bar_full;
+          phase ^= 1u;
+        }
+        // the next stage's barrier is asked while this stage's work is issued
+        ready = mbar_test(bar, phase);
+        if (leader) {
+          const uint64_t w_desc = desc_sw128(this_desc), x_desc = desc_sw128(this_desc + kWBytes / 16);
+          const uint64_t s_desc = scale_desc(this_desc + desc_sf);
 #pragma unroll
           for (int i = 0; i < kSfTiles; ++i) {
             copy_scales(sfa + 4 * i, s_desc + 32 * i);
@@ -352,10 +382,9 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
             mma_fp4<kFmt>(d, w_desc + 2 * i, x_desc + 2 * i, (kPer == 2 && (i & 1)) ? idesc_odd : idesc,
                           sfa + 4 * (i / kPer), sfb + 8 * (i / kPer), (k != t.k0 || i != 0) ? 1u : 0u);
           }
-          mma_commit(bar_empty + 8 * ring.at);
+          mma_commit(this_bar + 8 * kMaxStages);   // the stage's empty barrier
           if (k == t.k1 - 1) mma_commit(bar_accfull + 8 * acc.at);
         }
-        ring.advance(stages);
       }
       acc.advance(accs);
       if (*abort_flag) break;
@@ -429,7 +458,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
   pdl_trigger();
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarpLoad) {
+  if (warp == kWarpLoadW) {
     tc_fence_after();
     tmem_dealloc(tmem, static_cast<uint32_t>(p.tmem_cols));
   }
