@@ -102,3 +102,36 @@ def test_binding_refuses_without_a_gpu(tq):
         tq.tq_router_scored(torch.zeros(4, 8), 2)
     with pytest.raises(RuntimeError, match="needs a CUDA device"):
         tq.tq_fp4_quantize(torch.zeros(4, 32))
+
+
+def test_short_calls_take_the_headers_arguments(tq):
+    """The C wrappers of the binding: each takes the arguments the header
+    declares, in kind and number (a float where it declares one, no text, no
+    integer past an int), and refuses others before the library is called."""
+    import os
+    import re
+    tq.lib()
+    header = open(os.path.join(os.path.dirname(tq.__file__), "..", "include", "tqmoe.h")).read()
+    header = re.sub(r"/\*.*?\*/", "", header, flags=re.S)
+    for name in tq._CALLS:
+        call = tq._call(name)
+        args = re.search(name + r"\s*\(([^;]*)\);", header, re.S).group(1).split(",")
+        # as many zeros as arguments: refused by the library, not by the wrapper
+        zeros = [None if "*" in a or "tq_stream_t" in a else 0.0 if "float" in a else 0 for a in args]
+        assert call(*zeros) == INVALID, name
+        if type(call).__name__ != "builtin_function_or_method":
+            continue
+        with pytest.raises(TypeError):
+            call(*zeros[:-1])
+        for k, a in enumerate(args):
+            wrong = list(zeros)
+            wrong[k] = "text"
+            with pytest.raises(TypeError):
+                call(*wrong)
+            if "*" not in a and "tq_stream_t" not in a and "float" not in a:
+                wrong[k] = 1 << 40
+                if "int64" in a or "size_t" in a:
+                    assert call(*wrong) == INVALID
+                else:
+                    with pytest.raises(OverflowError):
+                        call(*wrong)

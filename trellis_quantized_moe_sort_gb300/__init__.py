@@ -133,7 +133,34 @@ def lib() -> ctypes.CDLL:
             fn.restype = res
             fn.argtypes = args
         _lib = h
+        _bind_calls(h)
     return _lib
+
+
+# The scored router's and the 4-bit operators' calls, by name: the C wrappers of
+# csrc/tq_python.c, or ctypes' functions where those are not built.
+_CALLS = ("tq_router_scored", "tq_router_scored_backward", "tq_fp4_quantize", "tq_fp4_dequantize", "tq_fp4_linear",
+          "tq_fp4_moe_forward", "tq_fp4_moe_mlp_forward")
+_calls: dict = {}
+
+
+def _bind_calls(h: ctypes.CDLL) -> None:
+    try:
+        from . import _tqcall
+    except ImportError:
+        _tqcall = None
+    for name in _CALLS:
+        if _tqcall is None:
+            _calls[name] = getattr(h, name)
+        else:
+            _tqcall.bind(name, ctypes.cast(getattr(h, name), ctypes.c_void_p).value)
+            _calls[name] = getattr(_tqcall, name)
+
+
+def _call(name: str):
+    if not _calls:
+        lib()
+    return _calls[name]
 
 
 def tq_status_string(status: int) -> str:
@@ -644,35 +671,51 @@ def _type_code(dtype, name):
 
 
 def _rows(t, name):
-    """(address, type code, elements between rows) of a 2-D CUDA tensor with contiguous rows."""
+    """(address, type code, elements between rows, rows, elements) of a 2-D CUDA
+    tensor with contiguous rows."""
     try:
-        ok, code = t.is_cuda, _type_code(t.dtype, name)
+        code = _type_code(t.dtype, name)
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        shape = t.shape
+        if len(shape) != 2:
+            raise ValueError(f"{name} must have two dimensions, not {len(shape)}")
+        n, width = shape
+        if t.is_contiguous():
+            return t.data_ptr(), code, width, n, width
+        step, inner = t.stride()
     except AttributeError:
         raise TypeError(f"{name} must be a torch.Tensor") from None
-    if not ok:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, not {t.dim()}")
-    n, width = t.shape
-    step, inner = t.stride()
-    if inner != 1 and width > 1 and n > 0:
+    if inner != 1 and width > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), code, step if n > 1 else width
+    return t.data_ptr(), code, step if n > 1 else width, n, width
 
 
-def _out_ptr(t, shape, dtypes, name):
-    """Address of an output given by the caller: a contiguous CUDA tensor of that shape."""
+def _given(t, shape, dtypes, name):
+    """Address of an argument of a known shape: a contiguous CUDA tensor."""
     ptr = _dev_ptr(t, dtypes, name)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return ptr
+
+
+_common = None
+
+
+def _types():
+    """torch, its fp32, int32 and uint8 as tuples of one: what the calls below compare with."""
+    global _common
+    if _common is None:
+        torch = _torch()
+        _common = torch, (torch.float32,), (torch.int32,), (torch.uint8,)
+    return _common
 
 
 def _scale_ptr(t, count, name):
     """Address of `count` fp32 scales, or None."""
     if t is None:
         return None
-    ptr = _dev_ptr(t, (_torch().float32,), name)
+    ptr = _dev_ptr(t, _types()[1], name)
     if t.numel() != count:
         raise ValueError(f"{name} has {t.numel()} values, expected {count}")
     return ptr
@@ -688,23 +731,22 @@ def tq_router_scored(logits, top_k: int, score: int = SCORE_SIGMOID, bias=None, 
     stay; the weights are the chosen scores, divided by their sum with
     `renormalize`, times `scale`.  A non-finite logit masks its expert; a row
     with none left has weights 0."""
-    torch = _torch()
-    ptr, code, step = _rows(logits, "logits")
-    n, E = logits.shape
-    dev = logits.device
+    torch, fp32, int32, _ = _types()
+    ptr, code, step, n, E = _rows(logits, "logits")
     if topk_ids is None:
-        topk_ids = torch.empty((n, top_k), dtype=torch.int32, device=dev)
+        topk_ids = torch.empty((n, top_k), dtype=torch.int32, device=logits.device)
         ids_ptr = topk_ids.data_ptr()
     else:
-        ids_ptr = _out_ptr(topk_ids, (n, top_k), (torch.int32,), "topk_ids")
+        ids_ptr = _given(topk_ids, (n, top_k), int32, "topk_ids")
     if topk_w is None:
-        topk_w = torch.empty((n, top_k), dtype=torch.float32, device=dev)
+        topk_w = torch.empty((n, top_k), dtype=torch.float32, device=logits.device)
         w_ptr = topk_w.data_ptr()
     else:
-        w_ptr = _out_ptr(topk_w, (n, top_k), (torch.float32,), "topk_w")
-    _check(lib().tq_router_scored(ptr, code, step, _scale_ptr(bias, E, "bias"), n, E, top_k, score, groups, top_groups,
-                                  1 if renormalize else 0, scale, ids_ptr, w_ptr, _stream(stream)),
-           "tq_router_scored")
+        w_ptr = _given(topk_w, (n, top_k), fp32, "topk_w")
+    rc = _call("tq_router_scored")(ptr, code, step, _scale_ptr(bias, E, "bias"), n, E, top_k, score, groups, top_groups,
+                                   1 if renormalize else 0, scale, ids_ptr, w_ptr, _stream(stream))
+    if rc:
+        raise TQError(rc, "tq_router_scored")
     return topk_ids, topk_w
 
 
@@ -713,22 +755,25 @@ def tq_router_scored_backward(logits, topk_ids, topk_w, grad_w, score: int = SCO
     """Gradient of the logits from the gradient of topk_w (fp32 [n, top_k]), in
     the logits' dtype; topk_ids, topk_w and the options are those of the
     forward call."""
-    torch = _torch()
-    ptr, code, step = _rows(logits, "logits")
-    n, E = logits.shape
+    torch, fp32, int32, _ = _types()
+    ptr, code, step, n, E = _rows(logits, "logits")
     shape = (n, topk_ids.shape[1])
     if grad_logits is None:
         grad_logits = torch.empty((n, E), dtype=logits.dtype, device=logits.device)
-    _check(lib().tq_router_scored_backward(
-        ptr, code, step, _out_ptr(topk_ids, shape, (torch.int32,), "topk_ids"),
-        _out_ptr(topk_w, shape, (torch.float32,), "topk_w"), _out_ptr(grad_w, shape, (torch.float32,), "grad_w"), n, E,
-        shape[1], score, 1 if renormalize else 0, scale,
-        _out_ptr(grad_logits, (n, E), (logits.dtype,), "grad_logits"), _stream(stream)), "tq_router_scored_backward")
+        out = grad_logits.data_ptr()
+    else:
+        out = _given(grad_logits, (n, E), (logits.dtype,), "grad_logits")
+    rc = _call("tq_router_scored_backward")(
+        ptr, code, step, _given(topk_ids, shape, int32, "topk_ids"), _given(topk_w, shape, fp32, "topk_w"),
+        _given(grad_w, shape, fp32, "grad_w"), n, E, shape[1], score, 1 if renormalize else 0, scale, out,
+        _stream(stream))
+    if rc:
+        raise TQError(rc, "tq_router_scored_backward")
     return grad_logits
 
 
 def _fp4_block(fmt):
-    if fmt not in (FP4_NV, FP4_MX):
+    if fmt != FP4_NV and fmt != FP4_MX:
         raise ValueError(f"fmt must be FP4_NV or FP4_MX, not {fmt}")
     return 16 if fmt == FP4_NV else 32
 
@@ -738,23 +783,31 @@ def tq_fp4_quantize(x, fmt: int = FP4_NV, global_scale=None, packed=None, scales
     rows; K % 32 == 0) -> (packed uint8 [n, K/2], scales uint8 [n, K/16] for
     FP4_NV or [n, K/32] for FP4_MX).  global_scale: fp32 [1] on the device
     (FP4_NV only)."""
-    torch = _torch()
-    ptr, code, step = _rows(x, "x")
-    n, K = x.shape
+    torch, _, _, uint8 = _types()
+    ptr, code, step, n, K = _rows(x, "x")
     kb = K // _fp4_block(fmt)
-    packed = torch.empty((n, K // 2), dtype=torch.uint8, device=x.device) if packed is None else packed
-    scales = torch.empty((n, kb), dtype=torch.uint8, device=x.device) if scales is None else scales
-    _check(lib().tq_fp4_quantize(ptr, code, step, n, K, fmt, _scale_ptr(global_scale, 1, "global_scale"),
-                                 _out_ptr(packed, (n, K // 2), (torch.uint8,), "packed"),
-                                 _out_ptr(scales, (n, kb), (torch.uint8,), "scales"), _stream(stream)),
-           "tq_fp4_quantize")
+    if packed is None:
+        packed = torch.empty((n, K // 2), dtype=torch.uint8, device=x.device)
+        p_ptr = packed.data_ptr()
+    else:
+        p_ptr = _given(packed, (n, K // 2), uint8, "packed")
+    if scales is None:
+        scales = torch.empty((n, kb), dtype=torch.uint8, device=x.device)
+        s_ptr = scales.data_ptr()
+    else:
+        s_ptr = _given(scales, (n, kb), uint8, "scales")
+    rc = _call("tq_fp4_quantize")(ptr, code, step, n, K, fmt, _scale_ptr(global_scale, 1, "global_scale"), p_ptr, s_ptr,
+                                  _stream(stream))
+    if rc:
+        raise TQError(rc, "tq_fp4_quantize")
     return packed, scales
 
 
 def tq_fp4_dequantize(packed, scales, fmt: int = FP4_NV, global_scale=None, dtype=None, out=None, stream=None):
     """The values of tq_fp4_quantize's output, [..., K] of `dtype` (fp32 when
     neither it nor `out` is given)."""
-    torch = _torch()
+    torch, _, _, uint8 = _types()
+    p_ptr, s_ptr = _dev_ptr(packed, uint8, "packed"), _dev_ptr(scales, uint8, "scales")
     K = 2 * packed.shape[-1]
     n = packed.numel() // max(K // 2, 1)
     if scales.numel() != n * (K // _fp4_block(fmt)):
@@ -762,12 +815,15 @@ def tq_fp4_dequantize(packed, scales, fmt: int = FP4_NV, global_scale=None, dtyp
     shape = (*packed.shape[:-1], K)
     if out is None:
         out = torch.empty(shape, dtype=torch.float32 if dtype is None else dtype, device=packed.device)
-    elif dtype is not None and out.dtype != dtype:
-        raise TypeError(f"out has dtype {out.dtype}, not {dtype}")
-    _check(lib().tq_fp4_dequantize(_dev_ptr(packed, (torch.uint8,), "packed"),
-                                   _dev_ptr(scales, (torch.uint8,), "scales"), n, K, fmt,
-                                   _scale_ptr(global_scale, 1, "global_scale"), _out_ptr(out, shape, (), "out"),
-                                   _type_code(out.dtype, "out"), _stream(stream)), "tq_fp4_dequantize")
+        o_ptr = out.data_ptr()
+    else:
+        if dtype is not None and out.dtype != dtype:
+            raise TypeError(f"out has dtype {out.dtype}, not {dtype}")
+        o_ptr = _given(out, shape, (), "out")
+    rc = _call("tq_fp4_dequantize")(p_ptr, s_ptr, n, K, fmt, _scale_ptr(global_scale, 1, "global_scale"), o_ptr,
+                                    _type_code(out.dtype, "out"), _stream(stream))
+    if rc:
+        raise TQError(rc, "tq_fp4_dequantize")
     return out
 
 
@@ -792,29 +848,38 @@ def tq_fp4_tile_scales(scales, fmt: int = FP4_NV, tiled=None, stream=None):
 
 def _fp4_matrix(packed, tiled_scales, E, N, K, fmt, name):
     """Addresses of a 4-bit weight matrix (or E of them), sizes checked."""
-    torch = _torch()
-    if tuple(packed.shape[-2:]) != (N, K // 2) or packed.numel() != E * N * (K // 2):
+    uint8 = _types()[3]
+    if packed.shape[-1] != K // 2 or packed.shape[-2] != N or packed.numel() != E * N * (K // 2):
         raise ValueError(f"{name} has shape {tuple(packed.shape)}, expected {(E, N, K // 2)}")
-    B = _fp4_block(fmt)
-    if tiled_scales.numel() != E * (-(-N // 128) * 128) * (-(-K // 256) * 256 // B):
+    if tiled_scales.numel() != E * (-(-N // 128) * 128) * (-(-K // 256) * 256 // _fp4_block(fmt)):
         raise ValueError(f"the scales of {name} are not the tiled layout of {E} x {N} x {K}")
-    return _dev_ptr(packed, (torch.uint8,), name), _dev_ptr(tiled_scales, (torch.uint8,), f"scales of {name}")
+    return _dev_ptr(packed, uint8, name), _dev_ptr(tiled_scales, uint8, "tiled scales")
 
 
-def _workspace(workspace, need, device):
-    """(address, bytes) of the caller's workspace or of a new one (none where the call needs none)
-    and the tensor, to be kept until the call is enqueued."""
-    torch = _torch()
+def _workspace(workspace, size, device, *args):
+    """(address, bytes) of the caller's workspace, or of a new one of
+    size(*args) bytes (none where the call needs none), and the tensor, to be
+    kept until the call is enqueued."""
+    torch, _, _, uint8 = _types()
     if workspace is None:
+        need = size(*args)
         if need <= 256:
             return None, 0, None
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
         return workspace.data_ptr(), need, workspace
-    return _dev_ptr(workspace, (torch.uint8,), "workspace"), workspace.numel(), workspace
+    return _dev_ptr(workspace, uint8, "workspace"), workspace.numel(), workspace
+
+
+def _output(y, shape, x):
+    """(y, address, type code): the caller's, or a new one in x's dtype."""
+    if y is None:
+        y = _types()[0].empty(shape, dtype=x.dtype, device=x.device)
+        return y, y.data_ptr(), _type_code(y.dtype, "y")
+    return y, _given(y, shape, (), "y"), _type_code(y.dtype, "y")
 
 
 def tq_fp4_linear_workspace_size(n: int, K: int, N: int, fmt: int = FP4_NV) -> int:
-    return int(lib().tq_fp4_linear_workspace_size(n, K, N, fmt))
+    return lib().tq_fp4_linear_workspace_size(n, K, N, fmt)
 
 
 def tq_fp4_linear(x, packed, tiled_scales, fmt: int = FP4_NV, w_scale=None, x_scale=None, workspace=None, y=None,
@@ -822,23 +887,21 @@ def tq_fp4_linear(x, packed, tiled_scales, fmt: int = FP4_NV, w_scale=None, x_sc
     """x [n, K], quantised by the call, times a 4-bit matrix packed [N, K/2]
     with tiled_scales (tq_fp4_tile_scales) -> y [n, N] in x's dtype (or y's).
     w_scale, x_scale: fp32 [1] global scales (FP4_NV)."""
-    torch = _torch()
-    ptr, code, step = _rows(x, "x")
-    n, K = x.shape
+    ptr, code, step, n, K = _rows(x, "x")
     N = packed.shape[-2]
     w_ptr, s_ptr = _fp4_matrix(packed, tiled_scales, 1, N, K, fmt, "packed")
-    ws_ptr, ws_bytes, workspace = _workspace(workspace, tq_fp4_linear_workspace_size(n, K, N, fmt) if workspace is None else 0,
-                                   x.device)
-    y = torch.empty((n, N), dtype=x.dtype, device=x.device) if y is None else y
-    _check(lib().tq_fp4_linear(ptr, code, step, w_ptr, s_ptr, fmt, _scale_ptr(w_scale, 1, "w_scale"),
-                               _scale_ptr(x_scale, 1, "x_scale"), n, K, N, ws_ptr, ws_bytes,
-                               _out_ptr(y, (n, N), (), "y"), _type_code(y.dtype, "y"), _stream(stream)),
-           "tq_fp4_linear")
+    ws_ptr, ws_bytes, workspace = _workspace(workspace, tq_fp4_linear_workspace_size, x.device, n, K, N, fmt)
+    y, y_ptr, y_code = _output(y, (n, N), x)
+    rc = _call("tq_fp4_linear")(ptr, code, step, w_ptr, s_ptr, fmt, _scale_ptr(w_scale, 1, "w_scale"),
+                                _scale_ptr(x_scale, 1, "x_scale"), n, K, N, ws_ptr, ws_bytes, y_ptr, y_code,
+                                _stream(stream))
+    if rc:
+        raise TQError(rc, "tq_fp4_linear")
     return y
 
 
 def tq_fp4_moe_workspace_size(n: int, top_k: int, E: int, K: int, N: int, fmt: int = FP4_NV) -> int:
-    return int(lib().tq_fp4_moe_workspace_size(n, top_k, E, K, N, fmt))
+    return lib().tq_fp4_moe_workspace_size(n, top_k, E, K, N, fmt)
 
 
 def tq_fp4_moe_forward(x, packed, tiled_scales, topk_ids, topk_w, fmt: int = FP4_NV, w_scale=None, x_scale=None,
@@ -847,27 +910,24 @@ def tq_fp4_moe_forward(x, packed, tiled_scales, topk_ids, topk_w, fmt: int = FP4
     tiled_scales (tq_fp4_tile_scales) -> y [n, N] in x's dtype (or y's):
     y[t] = sum_j topk_w[t, j] * W_{topk_ids[t, j]} x[t].  w_scale fp32 [E],
     x_scale fp32 [1]: global scales (FP4_NV)."""
-    torch = _torch()
-    ptr, code, step = _rows(x, "x")
-    n, K = x.shape
+    _, fp32, int32, _ = _types()
+    ptr, code, step, n, K = _rows(x, "x")
     E, N, _ = packed.shape
     top_k = topk_ids.shape[1]
     w_ptr, s_ptr = _fp4_matrix(packed, tiled_scales, E, N, K, fmt, "packed")
-    ws_ptr, ws_bytes, workspace = _workspace(workspace,
-                                   tq_fp4_moe_workspace_size(n, top_k, E, K, N, fmt) if workspace is None else 0,
-                                   x.device)
-    y = torch.empty((n, N), dtype=x.dtype, device=x.device) if y is None else y
-    _check(lib().tq_fp4_moe_forward(ptr, code, step, w_ptr, s_ptr, fmt, _scale_ptr(w_scale, E, "w_scale"),
-                                    _scale_ptr(x_scale, 1, "x_scale"),
-                                    _out_ptr(topk_ids, (n, top_k), (torch.int32,), "topk_ids"),
-                                    _out_ptr(topk_w, (n, top_k), (torch.float32,), "topk_w"), n, top_k, E, K, N,
-                                    ws_ptr, ws_bytes, _out_ptr(y, (n, N), (), "y"), _type_code(y.dtype, "y"),
-                                    _stream(stream)), "tq_fp4_moe_forward")
+    ws_ptr, ws_bytes, workspace = _workspace(workspace, tq_fp4_moe_workspace_size, x.device, n, top_k, E, K, N, fmt)
+    y, y_ptr, y_code = _output(y, (n, N), x)
+    rc = _call("tq_fp4_moe_forward")(ptr, code, step, w_ptr, s_ptr, fmt, _scale_ptr(w_scale, E, "w_scale"),
+                                     _scale_ptr(x_scale, 1, "x_scale"), _given(topk_ids, (n, top_k), int32, "topk_ids"),
+                                     _given(topk_w, (n, top_k), fp32, "topk_w"), n, top_k, E, K, N, ws_ptr, ws_bytes,
+                                     y_ptr, y_code, _stream(stream))
+    if rc:
+        raise TQError(rc, "tq_fp4_moe_forward")
     return y
 
 
 def tq_fp4_moe_mlp_workspace_size(n: int, top_k: int, E: int, H: int, I: int, fmt: int = FP4_NV) -> int:
-    return int(lib().tq_fp4_moe_mlp_workspace_size(n, top_k, E, H, I, fmt))
+    return lib().tq_fp4_moe_mlp_workspace_size(n, top_k, E, H, I, fmt)
 
 
 def tq_fp4_moe_mlp_forward(x, packed_gu, tiled_gu, packed_down, tiled_down, topk_ids, topk_w, fmt: int = FP4_NV,
@@ -877,21 +937,20 @@ def tq_fp4_moe_mlp_forward(x, packed_gu, tiled_gu, packed_down, tiled_down, topk
     then up rows), packed_down [E, H, I/2] -> y [n, H] in x's dtype (or y's).
     gu_scale, down_scale fp32 [E]; x_scale, h_scale fp32 [1], the global scales
     of x and of h = silu(gate) * up (FP4_NV)."""
-    torch = _torch()
-    ptr, code, step = _rows(x, "x")
-    n, H = x.shape
+    _, fp32, int32, _ = _types()
+    ptr, code, step, n, H = _rows(x, "x")
     E, I = packed_gu.shape[0], packed_gu.shape[1] // 2
     top_k = topk_ids.shape[1]
     gu_ptr, gus_ptr = _fp4_matrix(packed_gu, tiled_gu, E, 2 * I, H, fmt, "packed_gu")
     d_ptr, ds_ptr = _fp4_matrix(packed_down, tiled_down, E, H, I, fmt, "packed_down")
-    ws_ptr, ws_bytes, workspace = _workspace(workspace,
-                                   tq_fp4_moe_mlp_workspace_size(n, top_k, E, H, I, fmt) if workspace is None else 0,
-                                   x.device)
-    y = torch.empty((n, H), dtype=x.dtype, device=x.device) if y is None else y
-    _check(lib().tq_fp4_moe_mlp_forward(
+    ws_ptr, ws_bytes, workspace = _workspace(workspace, tq_fp4_moe_mlp_workspace_size, x.device, n, top_k, E, H, I, fmt)
+    y, y_ptr, y_code = _output(y, (n, H), x)
+    rc = _call("tq_fp4_moe_mlp_forward")(
         ptr, code, step, gu_ptr, gus_ptr, _scale_ptr(gu_scale, E, "gu_scale"), d_ptr, ds_ptr,
         _scale_ptr(down_scale, E, "down_scale"), fmt, _scale_ptr(x_scale, 1, "x_scale"),
-        _scale_ptr(h_scale, 1, "h_scale"), _out_ptr(topk_ids, (n, top_k), (torch.int32,), "topk_ids"),
-        _out_ptr(topk_w, (n, top_k), (torch.float32,), "topk_w"), n, top_k, E, H, I, ws_ptr, ws_bytes,
-        _out_ptr(y, (n, H), (), "y"), _type_code(y.dtype, "y"), _stream(stream)), "tq_fp4_moe_mlp_forward")
+        _scale_ptr(h_scale, 1, "h_scale"), _given(topk_ids, (n, top_k), int32, "topk_ids"),
+        _given(topk_w, (n, top_k), fp32, "topk_w"), n, top_k, E, H, I, ws_ptr, ws_bytes, y_ptr, y_code,
+        _stream(stream))
+    if rc:
+        raise TQError(rc, "tq_fp4_moe_mlp_forward")
     return y

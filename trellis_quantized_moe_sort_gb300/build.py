@@ -12,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,6 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtqmoe.so")
+CALLS = os.path.join(HERE, "_tqcall.so")   # the binding's short calls (csrc/tq_python.c)
 SOURCES = ["tq_host.cu", "tq_route.cu", "tq_grouped.cu", "tq_gemv.cu", "tq_noalloc.cu", "tq_probe.cu", "tq_mlp.cu", "tq_dequant.cu",
            "tq_router.cu", "tq_fp4_quant.cu", "tq_fp4_gemm.cu", "tq_fp4_gemv.cu", "tq_fp4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -34,6 +36,22 @@ def cuda_home() -> str:
     raise RuntimeError("nvcc not found (set CUDA_HOME)")
 
 
+def python_include() -> str:
+    """Folder of Python.h, or an empty string: the binding then calls through ctypes."""
+    path = sysconfig.get_paths()["include"]
+    return path if os.path.exists(os.path.join(path, "Python.h")) and shutil.which("gcc") else ""
+
+
+def build_calls() -> None:
+    tmp = CALLS + ".tmp"
+    cmd = ["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", python_include(), "-I", INCLUDE,
+           os.path.join(CSRC, "tq_python.c"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def _deps() -> list[str]:
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     files.append(os.path.join(INCLUDE, "tqmoe.h"))
@@ -42,7 +60,7 @@ def _deps() -> list[str]:
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or (python_include() and not os.path.exists(CALLS)):
         return False
     t = os.path.getmtime(LIB)
     return all(os.path.getmtime(f) <= t for f in _deps())
@@ -69,6 +87,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
+    if python_include():
+        build_calls()
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
     tmp = LIB + ".tmp"

@@ -66,7 +66,7 @@ struct Carver {
 };
 
 struct Routed {
-  int32_t *counts, *offsets, *sorted_pairs, *slot_of, *tiles, *num_tiles;
+  int32_t *counts, *offsets, *sorted_pairs, *slot_of, *tiles, *num_tiles, *tile_first;
 };
 Routed carve_routed(Carver& c, int64_t P, int E, int64_t cap) {
   Routed r;
@@ -76,6 +76,7 @@ Routed carve_routed(Carver& c, int64_t P, int E, int64_t cap) {
   r.slot_of = c.take<int32_t>(P);
   r.tiles = c.take<int32_t>(3 * cap);
   r.num_tiles = c.take<int32_t>(1);
+  r.tile_first = c.take<int32_t>(E);
   return r;
 }
 
@@ -170,8 +171,10 @@ bool bad_workspace(const void* p, size_t bytes, size_t need) { return !p || byte
 int route_pairs(const Routed& r, const int32_t* ids, int64_t P, int E, int tile_m, int64_t cap, int* err,
                 cudaStream_t s) {
   return launch_route_tile_map(ids, static_cast<int>(P), E, tile_m, r.counts, r.offsets, r.sorted_pairs, r.tiles,
-                               r.num_tiles, cap, err, s, nullptr, 0, r.slot_of);
+                               r.num_tiles, cap, err, s, nullptr, 0, r.slot_of, r.tile_first);
 }
+
+Fp4Slots slots_of(const Routed& r, const int32_t* ids) { return {ids, r.slot_of, r.offsets, r.tile_first}; }
 
 }  // namespace
 }  // namespace tq
@@ -243,8 +246,7 @@ int tq_fp4_linear(const void* x, int x_type, int64_t x_stride, const uint8_t* pa
                     y, y_type, err};
     return launch_fp4_gemv(v, s);
   }
-  rc = launch_fp4_stage(x, x_type, x_stride, n, K, fmt, x_scale, 1, nullptr, nullptr, nullptr, l.tiles, l.tile_m,
-                        l.staged.codes, l.staged.scales, s);
+  rc = launch_fp4_stage(x, x_type, x_stride, n, K, fmt, x_scale, 1, Fp4Slots{}, l.tile_m, l.staged.codes, l.staged.scales, s);
   if (rc != TQ_OK) return rc;
   Fp4Gemm g{fmt, packed, tiled_scales, w_scale, l.staged.codes, l.staged.scales, x_scale, nullptr, nullptr, nullptr,
             l.tiles, n, 1, K, N, l.tile_m, l.splits, l.part, l.splits > 1 ? nullptr : y, y_type, err};
@@ -283,8 +285,8 @@ int tq_fp4_moe_forward(const void* x, int x_type, int64_t x_stride, const uint8_
   }
   rc = route_pairs(m.routed, topk_ids, m.P, E, m.tile_m, m.cap, err, s);
   if (rc == TQ_OK)
-    rc = launch_fp4_stage(x, x_type, x_stride, n, K, fmt, x_scale, top_k, m.routed.slot_of, m.routed.tiles,
-                          m.routed.num_tiles, m.cap, m.tile_m, m.staged.codes, m.staged.scales, s);
+    rc = launch_fp4_stage(x, x_type, x_stride, n, K, fmt, x_scale, top_k, slots_of(m.routed, topk_ids), m.tile_m,
+                          m.staged.codes, m.staged.scales, s);
   if (rc != TQ_OK) return rc;
   Fp4Gemm g{fmt, packed, tiled_scales, w_scale, m.staged.codes, m.staged.scales, x_scale, m.routed.sorted_pairs,
             m.routed.tiles, m.routed.num_tiles, m.cap, m.P, E, K, N, m.tile_m, m.splits, m.part, nullptr, y_type, err};
@@ -324,15 +326,14 @@ int tq_fp4_moe_mlp_forward(const void* x, int x_type, int64_t x_stride, const ui
   const Routed& r = m.routed;
   rc = route_pairs(r, topk_ids, m.P, E, m.tile_m, m.cap, err, s);
   if (rc == TQ_OK)
-    rc = launch_fp4_stage(x, x_type, x_stride, n, H, fmt, x_scale, top_k, r.slot_of, r.tiles, r.num_tiles, m.cap,
-                          m.tile_m, m.x.codes, m.x.scales, s);
+    rc = launch_fp4_stage(x, x_type, x_stride, n, H, fmt, x_scale, top_k, slots_of(r, topk_ids), m.tile_m, m.x.codes, m.x.scales, s);
   if (rc != TQ_OK) return rc;
   Fp4Gemm gu{fmt, packed_gu, tiled_gu, gu_scale, m.x.codes, m.x.scales, x_scale, r.sorted_pairs, r.tiles, r.num_tiles,
              m.cap, m.P, E, H, 2 * I, m.tile_m, m.splits_gu, m.gate_up, nullptr, y_type, err};
   rc = launch_fp4_gemm(gu, s);
   if (rc == TQ_OK)
-    rc = launch_fp4_stage_swiglu(m.gate_up, m.P * 2 * I, m.splits_gu, topk_ids, x_scale, gu_scale, m.P, E, I, fmt,
-                                 h_scale, r.slot_of, r.tiles, r.num_tiles, m.cap, m.tile_m, m.h.codes, m.h.scales, s);
+    rc = launch_fp4_stage_swiglu(m.gate_up, m.P * 2 * I, m.splits_gu, x_scale, gu_scale, m.P, E, I, fmt, h_scale,
+                                 slots_of(r, topk_ids), m.tile_m, m.h.codes, m.h.scales, s);
   if (rc != TQ_OK) return rc;
   Fp4Gemm down{fmt, packed_down, tiled_down, down_scale, m.h.codes, m.h.scales, h_scale, r.sorted_pairs, r.tiles,
                r.num_tiles, m.cap, m.P, E, I, H, m.tile_m, m.splits_down, m.down, nullptr, y_type, err};

@@ -104,12 +104,36 @@ __device__ __forceinline__ uint32_t fp4_block_scale(float top, float g, float* d
   return byte;
 }
 
-// 16 codes of v / d, d shared (0: all zeros).
-__device__ __forceinline__ uint2 fp4_codes16(const float (&v)[16], float d) {
+// 16 codes of v / d, d shared (0: all zeros), |v| <= top.
+//
+// MX: d is a power of two and v * (1 / d) exact (a product below the normal
+// range is far below the first midpoint).
+// NV: the quotient rounded as an IEEE division rounds it.  With r = 1 / d
+// rounded to nearest, q0 = v r is within an ulp of v / d; its remainder v - q0 d
+// is exact in an FMA, and q0 + r (v - q0 d) is the correctly rounded quotient
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990).  That wants no over- or underflow on the way: d well inside
+// the exponent range and quotients that are not huge; values so small that the
+// remainder underflows are again far below the first midpoint.  Anything else
+// divides.
+template <int kFmt>
+__device__ __forceinline__ uint2 fp4_codes16(const float (&v)[16], float d, float top) {
   if (!(d > 0.f)) return make_uint2(0u, 0u);
   float q[16];
+  const float r = __frcp_rn(d);
+  if (kFmt == TQ_FP4_MX) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) q[i] = __fdiv_rn(v[i], d);
+    for (int i = 0; i < 16; ++i) q[i] = v[i] * r;
+  } else if (d >= 0x1p-100f && d <= 0x1p100f && top <= 1024.f * d) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float q0 = __fmul_rn(v[i], r);
+      q[i] = __fmaf_rn(__fmaf_rn(-q0, d, v[i]), r, q0);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) q[i] = __fdiv_rn(v[i], d);
+  }
   return make_uint2(e2m1x8(q), e2m1x8(q + 8));
 }
 

@@ -190,7 +190,7 @@ fp4_gemv_kernel(const TX* __restrict__ x, const GemvParams p, TY* __restrict__ y
     if (kFmt == TQ_FP4_MX) top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
     float d;
     const uint32_t byte = fp4_block_scale<kFmt>(top, g, &d);
-    const uint2 q = fp4_codes16(v, d);
+    const uint2 q = fp4_codes16<kFmt>(v, d, top);
     if (item < items) {
       piece_x(q, &plane[(2 * (item & 1)) * chunks + item / 2], &plane[(2 * (item & 1) + 1) * chunks + item / 2]);
       xs[item] = fp4_scale_value<kFmt>(byte) * (1.f / kPieceScale);

@@ -26,13 +26,16 @@ __device__ __forceinline__ uint2 quantize16(float (&v)[16], float g, uint32_t* b
   if (kFmt == TQ_FP4_MX) top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
   float d;
   *byte = fp4_block_scale<kFmt>(top, g, &d);
-  return fp4_codes16(v, d);
+  return fp4_codes16<kFmt>(v, d, top);
 }
 
+// A warp takes kAhead chunks of 512 values at once, all of their loads in
+// flight before the first is used.
 template <typename T, int kFmt>
 __global__ void __launch_bounds__(kQuantThreads)
 fp4_quantize_kernel(const T* __restrict__ x, long long stride, long long n, int K, const float* __restrict__ scale,
                     uint8_t* __restrict__ packed, uint8_t* __restrict__ scales) {
+  constexpr int kAhead = 2;
   pdl_wait();
   pdl_trigger();
   const float g = scale ? *scale : 1.f;
@@ -40,20 +43,29 @@ fp4_quantize_kernel(const T* __restrict__ x, long long stride, long long n, int 
   const int items = K / 16, chunks = (items + 31) / 32;
   const long long total = n * chunks;
   const long long warps = static_cast<long long>(gridDim.x) * (kQuantThreads / 32);
-  for (long long w = blockIdx.x * (kQuantThreads / 32ll) + (threadIdx.x >> 5); w < total; w += warps) {
-    const long long row = w / chunks;
-    const int item = static_cast<int>(w - row * chunks) * 32 + lane;
-    const bool in = item < items;
-    float v[16] = {};
-    if (in) load16(x + row * stride + 16 * item, v);
-    uint32_t byte;
-    const uint2 q = quantize16<kFmt>(v, g, &byte);
-    if (in) {
-      *reinterpret_cast<uint2*>(packed + row * (K / 2) + 8 * item) = q;
-      if (kFmt == TQ_FP4_NV)
-        scales[row * items + item] = static_cast<uint8_t>(byte);
-      else if ((lane & 1) == 0)
-        scales[row * (items / 2) + item / 2] = static_cast<uint8_t>(byte);
+  for (long long w = blockIdx.x * (kQuantThreads / 32ll) + (threadIdx.x >> 5); w < total; w += kAhead * warps) {
+    float v[kAhead][16] = {};
+    long long row[kAhead];
+    int item[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const long long at = w + i * warps;
+      row[i] = at / chunks;
+      item[i] = static_cast<int>(at - row[i] * chunks) * 32 + lane;
+      if (at >= total) item[i] = items;
+      if (item[i] < items) load16(x + row[i] * stride + 16 * item[i], v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      uint32_t byte;
+      const uint2 q = quantize16<kFmt>(v[i], g, &byte);
+      if (item[i] < items) {
+        *reinterpret_cast<uint2*>(packed + row[i] * (K / 2) + 8 * item[i]) = q;
+        if (kFmt == TQ_FP4_NV)
+          scales[row[i] * items + item[i]] = static_cast<uint8_t>(byte);
+        else if ((lane & 1) == 0)
+          scales[row[i] * (items / 2) + item[i] / 2] = static_cast<uint8_t>(byte);
+      }
     }
   }
 }
@@ -66,30 +78,45 @@ __device__ __forceinline__ float2 from_e2m1x2(uint32_t byte) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// A thread writes 16 bytes of consecutive values (8 of 16 bits, 4 of 32), so
+// that a warp's stores are whole lines; kAhead of them at once.
 template <typename T, int kFmt>
 __global__ void __launch_bounds__(kQuantThreads)
 fp4_dequantize_kernel(const uint8_t* __restrict__ packed, const uint8_t* __restrict__ scales, long long items,
                       const float* __restrict__ scale, T* __restrict__ out) {
+  constexpr int kVals = 16 / static_cast<int>(sizeof(T)), kAhead = 4;
+  using Codes = std::conditional_t<kVals == 8, uint32_t, uint16_t>;
   pdl_wait();
   pdl_trigger();
   const float g = scale ? *scale : 1.f;
   const long long step = static_cast<long long>(gridDim.x) * kQuantThreads;
-  for (long long i = blockIdx.x * static_cast<long long>(kQuantThreads) + threadIdx.x; i < items; i += step) {
-    const uint2 q = __ldg(reinterpret_cast<const uint2*>(packed) + i);
-    const float s = fp4_scale_value<kFmt>(scales[kFmt == TQ_FP4_NV ? i : i / 2]);
-    T v[16];
+  for (long long i0 = blockIdx.x * static_cast<long long>(kQuantThreads) + threadIdx.x; i0 < items;
+       i0 += kAhead * step) {
+    Codes q[kAhead];
+    uint32_t b[kAhead];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 f = from_e2m1x2((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
-      v[2 * j] = narrow<T>(__fmul_rn(__fmul_rn(f.x, s), g));
-      v[2 * j + 1] = narrow<T>(__fmul_rn(__fmul_rn(f.y, s), g));
+    for (int a = 0; a < kAhead; ++a) {
+      const long long i = i0 + a * step;
+      if (i < items) {
+        q[a] = __ldg(reinterpret_cast<const Codes*>(packed) + i);
+        b[a] = __ldg(scales + i / (fp4_block(kFmt) / kVals));
+      }
     }
-    uint4* const dst = reinterpret_cast<uint4*>(out + 16 * i);
 #pragma unroll
-    for (int j = 0; j < static_cast<int>(sizeof(T)); ++j) {
-      uint4 t;
-      memcpy(&t, reinterpret_cast<const char*>(v) + 16 * j, 16);
-      dst[j] = t;
+    for (int a = 0; a < kAhead; ++a) {
+      const long long i = i0 + a * step;
+      if (i >= items) break;
+      const float s = fp4_scale_value<kFmt>(b[a]);
+      T v[kVals];
+#pragma unroll
+      for (int j = 0; j < kVals / 2; ++j) {
+        const float2 f = from_e2m1x2(static_cast<uint32_t>(q[a]) >> (8 * j));
+        v[2 * j] = narrow<T>(__fmul_rn(__fmul_rn(f.x, s), g));
+        v[2 * j + 1] = narrow<T>(__fmul_rn(__fmul_rn(f.y, s), g));
+      }
+      uint4 o;
+      memcpy(&o, v, 16);
+      reinterpret_cast<uint4*>(out)[i] = o;
     }
   }
 }
@@ -126,15 +153,13 @@ struct Place {
   int slot, tile, row;
 };
 
-// The tile of a sorted slot: the last one that starts at or before it (the
-// map's first slots ascend and its tiles cover every slot).
-__device__ __forceinline__ Place place_of(int slot, const int32_t* __restrict__ tiles, int num_tiles) {
-  int lo = 0, hi = num_tiles;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(tiles + 3ll * mid + 1) <= slot) lo = mid; else hi = mid;
-  }
-  return {slot, lo, slot - __ldg(tiles + 3ll * lo + 1)};
+// The place of a pair; slot -1 (an expert out of range) has none.
+__device__ __forceinline__ Place place_of(const Fp4Slots& s, long long pair, int tile_m) {
+  if (!s.slot_of) return {static_cast<int>(pair), static_cast<int>(pair / tile_m), static_cast<int>(pair % tile_m)};
+  const int slot = __ldg(s.slot_of + pair), e = __ldg(s.ids + pair);
+  if (slot < 0) return {-1, 0, 0};
+  const int rank = slot - __ldg(s.offsets + e);
+  return {slot, __ldg(s.tile_first + e) + rank / tile_m, rank % tile_m};
 }
 
 // One block's share of a staged row: 16 values per thread from load(item, v),
@@ -149,7 +174,7 @@ __device__ __forceinline__ void stage_row(int K, float g, const Place* places, i
   const int items = K / 16, all = steps * (kFp4Step / 16);
   const int lane = threadIdx.x & 31;
   // whole warps stay in the loop together: all is a multiple of 16, a warp may end half empty
-  for (int item0 = threadIdx.x - lane; item0 < all; item0 += kQuantThreads) {
+  for (int item0 = threadIdx.x - lane; item0 < all; item0 += blockDim.x) {
     const int item = item0 + lane;
     float v[16] = {};
     if (item < items) load(item, v);
@@ -179,38 +204,31 @@ __device__ __forceinline__ void stage_row(int K, float g, const Place* places, i
   }
 }
 
-// The place of a pair from the sort's inverse; slot -1 (an expert out of
-// range) has none.
-__device__ __forceinline__ Place sorted_place(const int32_t* __restrict__ slot_of, long long pair,
-                                              const int32_t* __restrict__ tiles,
-                                              const int32_t* __restrict__ num_tiles, long long cap) {
-  const int slot = __ldg(slot_of + pair);
-  const int nt = static_cast<int>(min(static_cast<long long>(*num_tiles), cap));
-  return slot >= 0 && nt > 0 ? place_of(slot, tiles, nt) : Place{-1, 0, 0};
-}
-
 // Quantises each token's row once and writes it where the product reads it,
 // once per pair of the token.  Without slot_of a row's slot is its index and
 // its tile index / tile_m.  One block per row.
 template <typename T, int kFmt>
 __global__ void __launch_bounds__(kQuantThreads)
 fp4_stage_kernel(const T* __restrict__ x, long long stride, int K, const float* __restrict__ scale, int top_k,
-                 const int32_t* __restrict__ slot_of, const int32_t* __restrict__ tiles,
-                 const int32_t* __restrict__ num_tiles, long long cap, int tile_m, uint8_t* __restrict__ xq,
-                 uint8_t* __restrict__ xs) {
+                 const Fp4Slots slots, int tile_m, uint8_t* __restrict__ xq, uint8_t* __restrict__ xs) {
   __shared__ Place places[32];
   pdl_wait();
   pdl_trigger();
   const long long row = blockIdx.x;
   const float g = scale ? *scale : 1.f;
-  if (static_cast<int>(threadIdx.x) < top_k) {
-    places[threadIdx.x] =
-        slot_of ? sorted_place(slot_of, row * top_k + threadIdx.x, tiles, num_tiles, cap)
-                : Place{static_cast<int>(row), static_cast<int>(row / tile_m), static_cast<int>(row % tile_m)};
-  }
+  // the row's first values are under way while its places are looked up
+  float first[16] = {};
+  if (static_cast<int>(threadIdx.x) < K / 16) load16(x + row * stride + 16 * threadIdx.x, first);
+  if (static_cast<int>(threadIdx.x) < top_k) places[threadIdx.x] = place_of(slots, row * top_k + threadIdx.x, tile_m);
   __syncthreads();
-  stage_row<kFmt>(K, g, places, top_k, tile_m, xq, xs,
-                  [&](int item, float (&v)[16]) { load16(x + row * stride + 16 * item, v); });
+  stage_row<kFmt>(K, g, places, top_k, tile_m, xq, xs, [&](int item, float (&v)[16]) {
+    if (item == static_cast<int>(threadIdx.x)) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = first[i];
+    } else {
+      load16(x + row * stride + 16 * item, v);
+    }
+  });
 }
 
 // h = silu(gate) * up of one pair per block, quantised from fp32.  gate and up
@@ -218,18 +236,16 @@ fp4_stage_kernel(const T* __restrict__ x, long long stride, int K, const float* 
 template <int kFmt>
 __global__ void __launch_bounds__(kQuantThreads)
 fp4_stage_swiglu_kernel(const float* __restrict__ part, long long split_stride, int splits,
-                        const int32_t* __restrict__ ids, const float* __restrict__ x_scale,
-                        const float* __restrict__ w_scale, int E, int I, const float* __restrict__ h_scale,
-                        const int32_t* __restrict__ slot_of, const int32_t* __restrict__ tiles,
-                        const int32_t* __restrict__ num_tiles, long long cap, int tile_m, uint8_t* __restrict__ hq,
-                        uint8_t* __restrict__ hs) {
+                        const float* __restrict__ x_scale, const float* __restrict__ w_scale, int E, int I,
+                        const float* __restrict__ h_scale, const Fp4Slots slots, int tile_m,
+                        uint8_t* __restrict__ hq, uint8_t* __restrict__ hs) {
   __shared__ Place place;
   pdl_wait();
   pdl_trigger();
   const long long pair = blockIdx.x;
-  if (threadIdx.x == 0) place = sorted_place(slot_of, pair, tiles, num_tiles, cap);
+  if (threadIdx.x == 0) place = place_of(slots, pair, tile_m);
   __syncthreads();
-  const int e = __ldg(ids + pair);
+  const int e = __ldg(slots.ids + pair);
   if (place.slot < 0 || e < 0 || e >= E) return;   // a pair without a slot has no gate and up either
   const float alpha = (x_scale ? *x_scale : 1.f) * (w_scale ? __ldg(w_scale + e) : 1.f);
   const float* const row = part + pair * 2 * I;
@@ -254,41 +270,66 @@ fp4_stage_swiglu_kernel(const float* __restrict__ part, long long split_stride, 
 
 // y[t][r] = sum_j c_tj sum_s part[s][t * top_k + j][r] in that order, in fp32,
 // rounded once; c_tj = topk_w[t][j] * x_scale * w_scale[expert].  A pair whose
-// expert is out of range adds nothing.  kVec columns per thread.
+// expert is out of range adds nothing (its partial sums were never written and
+// are not read).  kVec columns per thread; the loads of four pairs are in
+// flight at once.
 template <typename T, int kVec>
 __global__ void __launch_bounds__(kQuantThreads)
 fp4_combine_kernel(const float* __restrict__ part, long long split_stride, int splits, const int32_t* __restrict__ ids,
                    const float* __restrict__ topk_w, const float* __restrict__ x_scale,
-                   const float* __restrict__ w_scale, long long n, int top_k, int E, int N, T* __restrict__ y) {
+                   const float* __restrict__ w_scale, int top_k, int E, int N, int blocks_per_row, T* __restrict__ y) {
+  constexpr int kAhead = 4;
+  __shared__ float coef[32];   // 0 and skip[j] for a pair out of range
+  __shared__ bool skip[32];
   pdl_wait();
   pdl_trigger();
-  const int cols = N / kVec;
-  const int per_row = (cols + kQuantThreads - 1) / kQuantThreads;   // blocks per token
-  const long long t = blockIdx.x / per_row;
-  const int c = (blockIdx.x - static_cast<int>(t) * per_row) * kQuantThreads + threadIdx.x;
-  if (c >= cols) return;
-  const float xs = x_scale ? *x_scale : 1.f;
-  float sum[kVec] = {};
-  for (int j = 0; j < top_k; ++j) {
-    const long long pair = t * top_k + j;
+  const long long t = blockIdx.x / blocks_per_row;
+  const int c = (blockIdx.x - static_cast<int>(t * blocks_per_row)) * kQuantThreads + threadIdx.x;
+  if (static_cast<int>(threadIdx.x) < top_k) {
+    const long long pair = t * top_k + threadIdx.x;
     const int e = ids ? __ldg(ids + pair) : 0;
-    if (e < 0 || e >= E) continue;
-    float v[kVec] = {};
-    const float* src = part + pair * N + static_cast<long long>(c) * kVec;
-    for (int s = 0; s < splits; ++s, src += split_stride) {
-      if constexpr (kVec == 4) {
-        const float4 f = __ldcs(reinterpret_cast<const float4*>(src));
-        v[0] += f.x;
-        v[1] += f.y;
-        v[2] += f.z;
-        v[3] += f.w;
-      } else {
-        v[0] += __ldcs(src);
+    const bool in = e >= 0 && e < E;
+    skip[threadIdx.x] = !in;
+    coef[threadIdx.x] = in ? (topk_w ? __ldg(topk_w + pair) : 1.f) *
+                                 ((x_scale ? *x_scale : 1.f) * (w_scale ? __ldg(w_scale + e) : 1.f))
+                           : 0.f;
+  }
+  __syncthreads();
+  if (c * kVec >= N) return;
+  float sum[kVec] = {};
+  const float* const src = part + t * top_k * N + static_cast<long long>(c) * kVec;
+  for (int j0 = 0; j0 < top_k; j0 += kAhead) {
+    float v[kAhead][kVec] = {};
+    for (int s = 0; s < splits; ++s) {
+      float f[kAhead][kVec] = {};
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int j = j0 + i;
+        if (j >= top_k || skip[j]) continue;
+        const float* const p = src + s * split_stride + static_cast<long long>(j) * N;
+        if constexpr (kVec == 4) {
+          const float4 q = __ldcs(reinterpret_cast<const float4*>(p));
+          f[i][0] = q.x;
+          f[i][1] = q.y;
+          f[i][2] = q.z;
+          f[i][3] = q.w;
+        } else {
+          f[i][0] = __ldcs(p);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) v[i][k] += f[i][k];
       }
     }
-    const float w = (topk_w ? __ldg(topk_w + pair) : 1.f) * (xs * (w_scale ? __ldg(w_scale + e) : 1.f));
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) sum[i] += w * v[i];
+    for (int i = 0; i < kAhead; ++i) {
+      if (j0 + i >= top_k || skip[j0 + i]) continue;
+      const float w = coef[j0 + i];
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) sum[k] = fmaf(w, v[i][k], sum[k]);
+    }
   }
   T out[kVec];
 #pragma unroll
@@ -305,6 +346,11 @@ fp4_combine_kernel(const float* __restrict__ part, long long split_stride, int s
   } else {
     dst[0] = out[0];
   }
+}
+
+// Threads of a block that stages one row: one per 16 values, 32 to 256.
+int row_threads(int K) {
+  return std::min(kQuantThreads, (fp4_steps(K) * (kFp4Step / 16) + 31) / 32 * 32);
 }
 
 int quant_blocks(long long warps_of_work) {
@@ -344,7 +390,7 @@ int launch_fp4_quantize(const void* x, int type, int64_t stride, int64_t n, int 
 
 int launch_fp4_dequantize(const uint8_t* packed, const uint8_t* scales, int64_t n, int K, int fmt, const float* scale,
                           void* out, int type, cudaStream_t s) {
-  const long long items = n * (K / 16);
+  const long long items = n * K * static_cast<long long>(type_size(type)) / 16;
   const int st = by_type(type, fmt, [&](auto* t, auto f) {
     using T = std::remove_pointer_t<decltype(t)>;
     return launch_pdl(fp4_dequantize_kernel<T, decltype(f)::value>, dim3(quant_blocks((items + 31) / 32)),
@@ -364,27 +410,24 @@ int launch_fp4_tile_scales(const uint8_t* scales, int E, int N, int K, int fmt, 
 }
 
 int launch_fp4_stage(const void* x, int type, int64_t stride, int64_t n, int K, int fmt, const float* scale, int top_k,
-                     const int32_t* slot_of, const int32_t* tiles, const int32_t* num_tiles, int64_t cap, int tile_m,
-                     uint8_t* xq, uint8_t* xs, cudaStream_t s) {
+                     const Fp4Slots& slots, int tile_m, uint8_t* xq, uint8_t* xs, cudaStream_t s) {
   const int st = by_type(type, fmt, [&](auto* t, auto f) {
     using T = std::remove_pointer_t<decltype(t)>;
-    return launch_pdl(fp4_stage_kernel<T, decltype(f)::value>, dim3(static_cast<unsigned>(n)), dim3(kQuantThreads), 0,
-                      s, static_cast<const T*>(x), static_cast<long long>(stride), K, scale, top_k, slot_of, tiles,
-                      num_tiles, static_cast<long long>(cap), tile_m, xq, xs);
+    return launch_pdl(fp4_stage_kernel<T, decltype(f)::value>, dim3(static_cast<unsigned>(n)), dim3(row_threads(K)), 0,
+                      s, static_cast<const T*>(x), static_cast<long long>(stride), K, scale, top_k, slots, tile_m, xq,
+                      xs);
   });
   if (st == TQ_OK) count_launch(kCntFp4Stage);
   return st;
 }
 
-int launch_fp4_stage_swiglu(const float* part, int64_t split_stride, int splits, const int32_t* ids,
-                            const float* x_scale, const float* w_scale, int64_t P, int E, int I, int fmt,
-                            const float* h_scale, const int32_t* slot_of, const int32_t* tiles,
-                            const int32_t* num_tiles, int64_t cap, int tile_m, uint8_t* hq, uint8_t* hs,
-                            cudaStream_t s) {
+int launch_fp4_stage_swiglu(const float* part, int64_t split_stride, int splits, const float* x_scale,
+                            const float* w_scale, int64_t P, int E, int I, int fmt, const float* h_scale,
+                            const Fp4Slots& slots, int tile_m, uint8_t* hq, uint8_t* hs, cudaStream_t s) {
   auto kernel = fmt == TQ_FP4_NV ? fp4_stage_swiglu_kernel<TQ_FP4_NV> : fp4_stage_swiglu_kernel<TQ_FP4_MX>;
-  const int st = launch_pdl(kernel, dim3(static_cast<unsigned>(P)), dim3(kQuantThreads), 0, s, part,
-                            static_cast<long long>(split_stride), splits, ids, x_scale, w_scale, E, I, h_scale,
-                            slot_of, tiles, num_tiles, static_cast<long long>(cap), tile_m, hq, hs);
+  const int st = launch_pdl(kernel, dim3(static_cast<unsigned>(P)), dim3(row_threads(I)), 0, s, part,
+                            static_cast<long long>(split_stride), splits, x_scale, w_scale, E, I, h_scale, slots,
+                            tile_m, hq, hs);
   if (st == TQ_OK) count_launch(kCntFp4Swiglu);
   return st;
 }
@@ -394,14 +437,15 @@ int launch_fp4_combine(const float* part, int64_t split_stride, int splits, cons
                        int type, cudaStream_t s) {
   const bool vec = N % 4 == 0 && (reinterpret_cast<uintptr_t>(y) & 15u) == 0;
   const int cols = vec ? N / 4 : N;
-  const long long blocks = n * ((cols + kQuantThreads - 1) / kQuantThreads);
+  const int per_row = (cols + kQuantThreads - 1) / kQuantThreads;
+  const long long blocks = n * per_row;
   if (blocks >= (1ll << 31)) return TQ_ERR_INVALID_ARG;
   const int st = by_type(type, TQ_FP4_NV, [&](auto* t, auto) {
     using T = std::remove_pointer_t<decltype(t)>;
     auto kernel = vec ? fp4_combine_kernel<T, 4> : fp4_combine_kernel<T, 1>;
     return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kQuantThreads), 0, s, part,
-                      static_cast<long long>(split_stride), splits, ids, topk_w, x_scale, w_scale,
-                      static_cast<long long>(n), top_k, E, N, static_cast<T*>(y));
+                      static_cast<long long>(split_stride), splits, ids, topk_w, x_scale, w_scale, top_k, E, N, per_row,
+                      static_cast<T*>(y));
   });
   if (st == TQ_OK) count_launch(kCntFp4Combine);
   return st;

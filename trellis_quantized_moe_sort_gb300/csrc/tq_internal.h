@@ -70,11 +70,12 @@ int launch_gather(const uint16_t* x, const int32_t* sorted_pairs, int P, int top
 // extra blocks of the same launch, or by a separate memset when y32 is not
 // 16-byte aligned or y32_count % 4 != 0).
 // With slot_of (device, [P]) the sort also writes its inverse: slot_of[p] =
-// the sorted slot of pair p, -1 for a pair whose expert is out of range.
+// the sorted slot of pair p, -1 for a pair whose expert is out of range; with
+// tile_first ([E]) the first m-tile of every expert.
 int launch_route_tile_map(const int32_t* topk_ids, int P, int E, int tile_m, int32_t* counts, int32_t* offsets,
                           int32_t* sorted_pairs, int32_t* tiles, int32_t* num_tiles, int64_t cap, int* err,
                           cudaStream_t s, float* y32 = nullptr, int64_t y32_count = 0,
-                          int32_t* slot_of = nullptr);
+                          int32_t* slot_of = nullptr, int32_t* tile_first = nullptr);
 // x_sorted[slot_of[t * top_k + j]] = x[t]: the pair-sorted copy written in
 // token order (each row of x read once); slot -1 is skipped.
 int launch_gather_tokens(const uint16_t* x, const int32_t* slot_of, int64_t n, int top_k, int K, uint16_t* x_sorted,
@@ -148,19 +149,24 @@ int launch_fp4_quantize(const void* x, int type, int64_t stride, int64_t n, int 
 int launch_fp4_dequantize(const uint8_t* packed, const uint8_t* scales, int64_t n, int K, int fmt, const float* scale,
                           void* out, int type, cudaStream_t s);
 int launch_fp4_tile_scales(const uint8_t* scales, int E, int N, int K, int fmt, uint8_t* tiled, cudaStream_t s);
+// Where the staged row of a pair goes: the sort's inverse and, per expert, its
+// first slot and first m-tile.  All nullptr: row r is slot r of tile r / tile_m.
+struct Fp4Slots {
+  const int32_t* ids;
+  const int32_t* slot_of;
+  const int32_t* offsets;
+  const int32_t* tile_first;
+};
 // Activations quantised into the product's layout: codes xq [slots][K/2] and
-// tiled scales xs [tiles].  slot_of (pair -> slot) with its tile map, or
-// nullptr: row r is slot r of tile r / tile_m.
+// tiled scales xs [tiles].
 int launch_fp4_stage(const void* x, int type, int64_t stride, int64_t n, int K, int fmt, const float* scale, int top_k,
-                     const int32_t* slot_of, const int32_t* tiles, const int32_t* num_tiles, int64_t cap, int tile_m,
-                     uint8_t* xq, uint8_t* xs, cudaStream_t s);
+                     const Fp4Slots& slots, int tile_m, uint8_t* xq,
+                     uint8_t* xs, cudaStream_t s);
 // The same for h = silu(gate) * up of every pair, gate and up from the partial
 // sums part[split][pair][2I] times x_scale * w_scale[expert].
-int launch_fp4_stage_swiglu(const float* part, int64_t split_stride, int splits, const int32_t* ids,
-                            const float* x_scale, const float* w_scale, int64_t P, int E, int I, int fmt,
-                            const float* h_scale, const int32_t* slot_of, const int32_t* tiles,
-                            const int32_t* num_tiles, int64_t cap, int tile_m, uint8_t* hq, uint8_t* hs,
-                            cudaStream_t s);
+int launch_fp4_stage_swiglu(const float* part, int64_t split_stride, int splits, const float* x_scale,
+                            const float* w_scale, int64_t P, int E, int I, int fmt, const float* h_scale,
+                            const Fp4Slots& slots, int tile_m, uint8_t* hq, uint8_t* hs, cudaStream_t s);
 int launch_fp4_combine(const float* part, int64_t split_stride, int splits, const int32_t* ids, const float* topk_w,
                        const float* x_scale, const float* w_scale, int64_t n, int top_k, int E, int N, void* y,
                        int type, cudaStream_t s);

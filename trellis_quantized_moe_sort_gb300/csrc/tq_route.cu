@@ -196,12 +196,15 @@ route_kernel(const int32_t* __restrict__ ids, int P, int E, int sorters, int32_t
 }
 
 // The m-tile map of one block from expert e's (first slot, count) in thread e.
+// tile_first[e], when given, receives the expert's first tile.
 __device__ __forceinline__ void tile_map_block(int E, int off, int cnt, int tile_m, int32_t* __restrict__ tiles,
-                                               int32_t* __restrict__ num_tiles, long long cap, int* err) {
+                                               int32_t* __restrict__ num_tiles, long long cap, int* err,
+                                               int32_t* __restrict__ tile_first = nullptr) {
   const int e = threadIdx.x;
   const int nt = e < E ? (cnt + tile_m - 1) / tile_m : 0;
   int total = 0;
   const int start = block_exclusive_scan(nt, &total);
+  if (tile_first && e < E) tile_first[e] = start;
   for (int i = 0; i < nt; ++i) {
     const long long idx = static_cast<long long>(start) + i;
     if (idx >= cap) break;
@@ -243,7 +246,7 @@ route_tile_map_kernel(const int32_t* __restrict__ ids, int P, int E, int sorters
                       int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
                       int32_t* __restrict__ sorted_pairs, int32_t* __restrict__ tiles,
                       int32_t* __restrict__ num_tiles, long long cap, int* err, float4* __restrict__ zero4,
-                      long long zero_n4, int32_t* __restrict__ slot_of) {
+                      long long zero_n4, int32_t* __restrict__ slot_of, int32_t* __restrict__ tile_first) {
   pdl_wait();
   pdl_trigger();
   if (static_cast<int>(blockIdx.x) >= sorters) {
@@ -255,7 +258,7 @@ route_tile_map_kernel(const int32_t* __restrict__ ids, int P, int E, int sorters
   }
   int first, count;
   route_chunk(ids, P, E, sorters, counts, offsets, sorted_pairs, err, &first, &count, slot_of);
-  if (blockIdx.x == 0) tile_map_block(E, first, count, tile_m, tiles, num_tiles, cap, err);
+  if (blockIdx.x == 0) tile_map_block(E, first, count, tile_m, tiles, num_tiles, cap, err, tile_first);
 }
 
 // y[0 .. n) = 0: float4 stores over the 16-byte aligned middle, scalar
@@ -482,7 +485,7 @@ static size_t route_smem(int E) { return sizeof(int32_t) * (kWarps + 2) * static
 
 int launch_route_tile_map(const int32_t* topk_ids, int P, int E, int tile_m, int32_t* counts, int32_t* offsets,
                           int32_t* sorted_pairs, int32_t* tiles, int32_t* num_tiles, int64_t cap, int* err,
-                          cudaStream_t s, float* y32, int64_t y32_count, int32_t* slot_of) {
+                          cudaStream_t s, float* y32, int64_t y32_count, int32_t* slot_of, int32_t* tile_first) {
   const size_t smem = route_smem(E);
   if (cudaFuncSetAttribute(route_tile_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(route_smem(1024))) != cudaSuccess) {
@@ -507,7 +510,7 @@ int launch_route_tile_map(const int32_t* topk_ids, int P, int E, int tile_m, int
   const int sorters = route_sorters(P);
   int st = launch_pdl(route_tile_map_kernel, dim3(static_cast<unsigned>(sorters + clear_blocks)), dim3(kBlock), smem,
                       s, topk_ids, P, E, sorters, tile_m, counts, offsets, sorted_pairs, tiles, num_tiles,
-                      static_cast<long long>(cap), err, reinterpret_cast<float4*>(y32), z4, slot_of);
+                      static_cast<long long>(cap), err, reinterpret_cast<float4*>(y32), z4, slot_of, tile_first);
   if (st == TQ_OK) st = launch_status();
   if (st == TQ_OK) count_launch(kCntRouteTileMap);
   return st;
