@@ -87,13 +87,74 @@ __device__ __forceinline__ float fp4_max16(float (&v)[16]) {
   return __uint_as_float(m);
 }
 
+// 16 consecutive values of a row (16-byte aligned) as they are in memory, and their fp32 form with the largest
+// magnitude.  16-bit types find it two values at a time, as integers.
+template <typename T>
+struct Piece {
+  uint4 raw[sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ Piece<T> load_piece(const T* __restrict__ p) {
+  Piece<T> r;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) r.raw[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ float open_piece(const Piece<T>& r, float (&v)[16]) {
+  const T* const t = reinterpret_cast<const T*>(r.raw);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = widen(t[i]);
+  if constexpr (sizeof(T) == 2) {
+    constexpr uint32_t kInf = std::is_same_v<T, __half> ? 0x7c00u : 0x7f80u;
+    const uint32_t* const w = reinterpret_cast<const uint32_t*>(r.raw);
+    uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+    const uint32_t top = max(m & 0xffffu, m >> 16);
+    if (top >= kInf) return fp4_max16(v);
+    const uint16_t bits = static_cast<uint16_t>(top);
+    T value;
+    memcpy(&value, &bits, 2);
+    return widen(value);
+  } else {
+    return fp4_max16(v);
+  }
+}
+
+// a / b rounded to nearest, r = 1 / b rounded to nearest.  q0 = a r is within an
+// ulp of the quotient, its remainder a - q0 b exact in an FMA, and q0 + r (a - q0
+// b) the correctly rounded quotient (Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990).  That wants no over-
+// or underflow on the way: b well inside the exponent range and a quotient that
+// is not huge (`fits`).  A remainder that underflows belongs to a quotient far
+// below anything that the roundings after it can tell from 0.
+__device__ __forceinline__ bool divides_fast(float largest, float b) {
+  return b >= 0x1p-100f && b <= 0x1p100f && largest <= 0x1p20f * b;
+}
+__device__ __forceinline__ float divide_fast(float a, float b, float r) {
+  const float q0 = __fmul_rn(a, r);
+  return __fmaf_rn(__fmaf_rn(-q0, b, a), r, q0);
+}
+
+// The global scale as the quantisers use it: g, 6 g and 1 / (6 g).
+struct GlobalScale {
+  float g, six, r_six;
+  __device__ __forceinline__ explicit GlobalScale(const float* p) : g(p ? *p : 1.f) {
+    six = __fmul_rn(6.f, g);
+    r_six = __frcp_rn(six);
+  }
+};
+
 // Scale byte of a block whose largest magnitude is `top`; *d = the divisor of
-// its values.
+// its values, *r its reciprocal.
 template <int kFmt>
-__device__ __forceinline__ uint32_t fp4_block_scale(float top, float g, float* d) {
+__device__ __forceinline__ uint32_t fp4_block_scale(float top, const GlobalScale& g, float* d, float* r) {
   if (kFmt == TQ_FP4_NV) {
-    const uint32_t byte = to_e4m3(__fdiv_rn(top, __fmul_rn(6.f, g)));
-    *d = __fmul_rn(from_e4m3(byte), g);
+    const uint32_t byte =
+        to_e4m3(divides_fast(top, g.six) ? divide_fast(top, g.six, g.r_six) : __fdiv_rn(top, g.six));
+    *d = __fmul_rn(from_e4m3(byte), g.g);
+    *r = __frcp_rn(*d);
     return byte;
   }
   // floor(log2 top) from the exponent field; the smallest scale serves all
@@ -101,53 +162,28 @@ __device__ __forceinline__ uint32_t fp4_block_scale(float top, float g, float* d
   const int e = static_cast<int>(__float_as_uint(top) >> 23);
   const uint32_t byte = static_cast<uint32_t>(max(e - 2, 0));
   *d = from_e8m0(byte);
+  *r = __uint_as_float((254u - byte) << 23);   // byte <= 252
   return byte;
 }
 
-// 16 codes of v / d, d shared (0: all zeros), |v| <= top.
-//
-// MX: d is a power of two and v * (1 / d) exact (a product below the normal
-// range is far below the first midpoint).
-// NV: the quotient rounded as an IEEE division rounds it.  With r = 1 / d
-// rounded to nearest, q0 = v r is within an ulp of v / d; its remainder v - q0 d
-// is exact in an FMA, and q0 + r (v - q0 d) is the correctly rounded quotient
-// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990).  That wants no over- or underflow on the way: d well inside
-// the exponent range and quotients that are not huge; values so small that the
-// remainder underflows are again far below the first midpoint.  Anything else
-// divides.
+// 16 codes of v / d (d = 0: zeros), |v| <= top, r = 1 / d, each quotient rounded
+// as a division rounds it.  MX: d is a power of two and v r exact (a product
+// below the normal range is far below the first midpoint).
 template <int kFmt>
-__device__ __forceinline__ uint2 fp4_codes16(const float (&v)[16], float d, float top) {
+__device__ __forceinline__ uint2 fp4_codes16(const float (&v)[16], float d, float r, float top) {
   if (!(d > 0.f)) return make_uint2(0u, 0u);
   float q[16];
-  const float r = __frcp_rn(d);
   if (kFmt == TQ_FP4_MX) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) q[i] = v[i] * r;
-  } else if (d >= 0x1p-100f && d <= 0x1p100f && top <= 1024.f * d) {
+  } else if (divides_fast(top, d)) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float q0 = __fmul_rn(v[i], r);
-      q[i] = __fmaf_rn(__fmaf_rn(-q0, d, v[i]), r, q0);
-    }
+    for (int i = 0; i < 16; ++i) q[i] = divide_fast(v[i], d, r);
   } else {
 #pragma unroll
     for (int i = 0; i < 16; ++i) q[i] = __fdiv_rn(v[i], d);
   }
   return make_uint2(e2m1x8(q), e2m1x8(q + 8));
-}
-
-// 16 consecutive values of a row (16-byte aligned) in fp32.
-template <typename T>
-__device__ __forceinline__ void load16(const T* __restrict__ p, float (&v)[16]) {
-  constexpr int kPer = 16 / static_cast<int>(sizeof(T));
-#pragma unroll
-  for (int i = 0; i < 16; i += kPer) {
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p + i));
-    const T* const t = reinterpret_cast<const T*>(&q);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) v[i + j] = widen(t[j]);
-  }
 }
 
 }  // namespace tq

@@ -181,16 +181,15 @@ fp4_gemv_kernel(const TX* __restrict__ x, const GemvParams p, TY* __restrict__ y
   fetch(0);   // under way while x is quantised
 
   const TX* const row_x = x + t * p.stride;
-  const float g = p.x_scale ? *p.x_scale : 1.f;
+  const GlobalScale g(p.x_scale);
   for (int item0 = threadIdx.x - lane; item0 < items; item0 += kThreads) {
     const int item = item0 + lane;
-    float v[16] = {};
-    if (item < items) load16(row_x + 16 * item, v);
-    float top = fp4_max16(v);
+    float v[16] = {}, top = 0.f;
+    if (item < items) top = open_piece(load_piece(row_x + 16 * item), v);
     if (kFmt == TQ_FP4_MX) top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
-    float d;
-    const uint32_t byte = fp4_block_scale<kFmt>(top, g, &d);
-    const uint2 q = fp4_codes16<kFmt>(v, d, top);
+    float d, r;
+    const uint32_t byte = fp4_block_scale<kFmt>(top, g, &d, &r);
+    const uint2 q = fp4_codes16<kFmt>(v, d, r, top);
     if (item < items) {
       piece_x(q, &plane[(2 * (item & 1)) * chunks + item / 2], &plane[(2 * (item & 1) + 1) * chunks + item / 2]);
       xs[item] = fp4_scale_value<kFmt>(byte) * (1.f / kPieceScale);
@@ -240,7 +239,7 @@ fp4_gemv_kernel(const TX* __restrict__ x, const GemvParams p, TY* __restrict__ y
         if (threadIdx.x == 0) record_error(p.err, TQ_ERR_INVALID_ARG, kWhereFp4Gemv);
       } else {
         const float c =
-            (p.topk_w ? __ldg(p.topk_w + t * top_k + cj) : 1.f) * (g * (p.w_scale ? __ldg(p.w_scale + ce) : 1.f));
+            (p.topk_w ? __ldg(p.topk_w + t * top_k + cj) : 1.f) * (g.g * (p.w_scale ? __ldg(p.w_scale + ce) : 1.f));
         total[0] = fmaf(c, part[0], total[0]);
         total[1] = fmaf(c, part[1], total[1]);
       }

@@ -18,54 +18,55 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kQuantThreads = 256;
 
-// Quantises 16 values of a block (the whole of it, or one of its two halves in
-// neighbouring lanes; every lane of the warp takes part): codes and scale byte.
+// Quantises 16 values, the largest magnitude `top`, of a block (the whole of
+// it, or one of its two halves in neighbouring lanes; every lane of the warp
+// takes part): codes and scale byte.
 template <int kFmt>
-__device__ __forceinline__ uint2 quantize16(float (&v)[16], float g, uint32_t* byte) {
-  float top = fp4_max16(v);
+__device__ __forceinline__ uint2 quantize16(const float (&v)[16], float top, const GlobalScale& g, uint32_t* byte) {
   if (kFmt == TQ_FP4_MX) top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
-  float d;
-  *byte = fp4_block_scale<kFmt>(top, g, &d);
-  return fp4_codes16<kFmt>(v, d, top);
+  float d, r;
+  *byte = fp4_block_scale<kFmt>(top, g, &d, &r);
+  return fp4_codes16<kFmt>(v, d, r, top);
 }
 
-// A warp takes kAhead chunks of 512 values at once, all of their loads in
-// flight before the first is used.
+// A warp takes a chunk of 512 values at a time; the next chunk's loads are in
+// flight while the present one is quantised.  Row and chunk advance by the
+// launch's constant step (step_rows, step_chunks), without divisions.
 template <typename T, int kFmt>
 __global__ void __launch_bounds__(kQuantThreads)
 fp4_quantize_kernel(const T* __restrict__ x, long long stride, long long n, int K, const float* __restrict__ scale,
-                    uint8_t* __restrict__ packed, uint8_t* __restrict__ scales) {
-  constexpr int kAhead = 2;
+                    int step_rows, int step_chunks, uint8_t* __restrict__ packed, uint8_t* __restrict__ scales) {
   pdl_wait();
   pdl_trigger();
-  const float g = scale ? *scale : 1.f;
+  const GlobalScale g(scale);
   const int lane = threadIdx.x & 31;
   const int items = K / 16, chunks = (items + 31) / 32;
-  const long long total = n * chunks;
-  const long long warps = static_cast<long long>(gridDim.x) * (kQuantThreads / 32);
-  for (long long w = blockIdx.x * (kQuantThreads / 32ll) + (threadIdx.x >> 5); w < total; w += kAhead * warps) {
-    float v[kAhead][16] = {};
-    long long row[kAhead];
-    int item[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const long long at = w + i * warps;
-      row[i] = at / chunks;
-      item[i] = static_cast<int>(at - row[i] * chunks) * 32 + lane;
-      if (at >= total) item[i] = items;
-      if (item[i] < items) load16(x + row[i] * stride + 16 * item[i], v[i]);
+  const long long warp = blockIdx.x * (kQuantThreads / 32ll) + (threadIdx.x >> 5);
+  long long row = warp / chunks;
+  int chunk = static_cast<int>(warp - row * chunks);
+  Piece<T> next = {};
+  if (row < n && chunk * 32 + lane < items) next = load_piece(x + row * stride + 16 * (chunk * 32 + lane));
+  while (row < n) {
+    const Piece<T> piece = next;
+    const int item = chunk * 32 + lane;
+    const long long at = row;
+    row += step_rows;
+    chunk += step_chunks;
+    if (chunk >= chunks) {
+      chunk -= chunks;
+      ++row;
     }
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      uint32_t byte;
-      const uint2 q = quantize16<kFmt>(v[i], g, &byte);
-      if (item[i] < items) {
-        *reinterpret_cast<uint2*>(packed + row[i] * (K / 2) + 8 * item[i]) = q;
-        if (kFmt == TQ_FP4_NV)
-          scales[row[i] * items + item[i]] = static_cast<uint8_t>(byte);
-        else if ((lane & 1) == 0)
-          scales[row[i] * (items / 2) + item[i] / 2] = static_cast<uint8_t>(byte);
-      }
+    if (row < n && chunk * 32 + lane < items) next = load_piece(x + row * stride + 16 * (chunk * 32 + lane));
+    float v[16];
+    const float top = open_piece(piece, v);   // lanes past the row hold an old piece and write nothing
+    uint32_t byte;
+    const uint2 q = quantize16<kFmt>(v, top, g, &byte);
+    if (item < items) {
+      *reinterpret_cast<uint2*>(packed + at * (K / 2) + 8 * item) = q;
+      if (kFmt == TQ_FP4_NV)
+        scales[at * items + item] = static_cast<uint8_t>(byte);
+      else if ((lane & 1) == 0)
+        scales[at * (items / 2) + item / 2] = static_cast<uint8_t>(byte);
     }
   }
 }
@@ -162,12 +163,12 @@ __device__ __forceinline__ Place place_of(const Fp4Slots& s, long long pair, int
   return {slot, __ldg(s.tile_first + e) + rank / tile_m, rank % tile_m};
 }
 
-// One block's share of a staged row: 16 values per thread from load(item, v),
-// their codes into the row's slots and their scales into the tiled layout of
+// One block's share of a staged row: 16 values per thread and their largest
+// magnitude from load(item, v), their codes into the row's slots and their scales into the tiled layout of
 // each slot's m-tile (blocks past K zero, so that the MMA's last step
 // multiplies zeros by a finite scale).
 template <int kFmt, typename Load>
-__device__ __forceinline__ void stage_row(int K, float g, const Place* places, int count, int tile_m,
+__device__ __forceinline__ void stage_row(int K, const GlobalScale& g, const Place* places, int count, int tile_m,
                                           uint8_t* __restrict__ xq, uint8_t* __restrict__ xs, Load&& load) {
   const int steps = fp4_steps(K);
   const size_t tile_bytes = static_cast<size_t>((tile_m + 127) / 128) * steps * fp4_scale_step_bytes(kFmt);
@@ -176,10 +177,10 @@ __device__ __forceinline__ void stage_row(int K, float g, const Place* places, i
   // whole warps stay in the loop together: all is a multiple of 16, a warp may end half empty
   for (int item0 = threadIdx.x - lane; item0 < all; item0 += blockDim.x) {
     const int item = item0 + lane;
-    float v[16] = {};
-    if (item < items) load(item, v);
+    float v[16] = {}, top = 0.f;
+    if (item < items) top = load(item, v);
     uint32_t byte;
-    const uint2 q = quantize16<kFmt>(v, g, &byte);
+    const uint2 q = quantize16<kFmt>(v, top, g, &byte);
     if (item >= items) byte = 0;
     // four blocks' scales in one word
     uint32_t word;
@@ -215,19 +216,14 @@ fp4_stage_kernel(const T* __restrict__ x, long long stride, int K, const float* 
   pdl_wait();
   pdl_trigger();
   const long long row = blockIdx.x;
-  const float g = scale ? *scale : 1.f;
   // the row's first values are under way while its places are looked up
-  float first[16] = {};
-  if (static_cast<int>(threadIdx.x) < K / 16) load16(x + row * stride + 16 * threadIdx.x, first);
+  Piece<T> first = {};
+  if (static_cast<int>(threadIdx.x) < K / 16) first = load_piece(x + row * stride + 16 * threadIdx.x);
+  const GlobalScale g(scale);
   if (static_cast<int>(threadIdx.x) < top_k) places[threadIdx.x] = place_of(slots, row * top_k + threadIdx.x, tile_m);
   __syncthreads();
   stage_row<kFmt>(K, g, places, top_k, tile_m, xq, xs, [&](int item, float (&v)[16]) {
-    if (item == static_cast<int>(threadIdx.x)) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = first[i];
-    } else {
-      load16(x + row * stride + 16 * item, v);
-    }
+    return open_piece(item == static_cast<int>(threadIdx.x) ? first : load_piece(x + row * stride + 16 * item), v);
   });
 }
 
@@ -249,7 +245,7 @@ fp4_stage_swiglu_kernel(const float* __restrict__ part, long long split_stride, 
   if (place.slot < 0 || e < 0 || e >= E) return;   // a pair without a slot has no gate and up either
   const float alpha = (x_scale ? *x_scale : 1.f) * (w_scale ? __ldg(w_scale + e) : 1.f);
   const float* const row = part + pair * 2 * I;
-  stage_row<kFmt>(I, h_scale ? *h_scale : 1.f, &place, 1, tile_m, hq, hs, [&](int item, float (&v)[16]) {
+  stage_row<kFmt>(I, GlobalScale(h_scale), &place, 1, tile_m, hq, hs, [&](int item, float (&v)[16]) {
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
@@ -265,6 +261,7 @@ fp4_stage_swiglu_kernel(const float* __restrict__ part, long long split_stride, 
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[i + j] = gate[j] / (1.f + expf(-gate[j])) * up[j];
     }
+    return fp4_max16(v);
   });
 }
 
@@ -378,11 +375,12 @@ int by_type(int type, int fmt, F&& f) {
 int launch_fp4_quantize(const void* x, int type, int64_t stride, int64_t n, int K, int fmt, const float* scale,
                         uint8_t* packed, uint8_t* scales, cudaStream_t s) {
   const int chunks = (K / 16 + 31) / 32;
+  const int blocks = quant_blocks(n * chunks), warps = blocks * (kQuantThreads / 32);
   const int st = by_type(type, fmt, [&](auto* t, auto f) {
     using T = std::remove_pointer_t<decltype(t)>;
-    return launch_pdl(fp4_quantize_kernel<T, decltype(f)::value>, dim3(quant_blocks(n * chunks)), dim3(kQuantThreads),
-                      0, s, static_cast<const T*>(x), static_cast<long long>(stride), static_cast<long long>(n), K,
-                      scale, packed, scales);
+    return launch_pdl(fp4_quantize_kernel<T, decltype(f)::value>, dim3(blocks), dim3(kQuantThreads), 0, s,
+                      static_cast<const T*>(x), static_cast<long long>(stride), static_cast<long long>(n), K, scale,
+                      warps / chunks, warps % chunks, packed, scales);
   });
   if (st == TQ_OK) count_launch(kCntFp4Quantize);
   return st;

@@ -7,8 +7,8 @@
 //
 // The choice compares fp32 values, and a token whose candidates are an ulp
 // apart changes its experts with the order of a sum.  So every operation on
-// the way to the comparison has one order: the sigmoid is 1 / (1 + exp(-x))
-// with an IEEE division and no contraction; the softmax's denominator is a
+// the way to the comparison has one order: the sigmoid is 1 / (1 + exp(-x)),
+// the reciprocal rounded to nearest, no contraction; the softmax's denominator is a
 // balanced tree over neighbouring experts (a power of two of them, absent ones
 // zero), first in a lane's registers, then across lanes 1, 2, 4, 8 and 16
 // apart; a group's value is one addition.  The result depends on the token's
@@ -63,7 +63,7 @@ __device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int l
 
 // 1 / (1 + exp(-x)); 0 for a masked logit.
 __device__ __forceinline__ float sigmoid_score(float x) {
-  return x == -INFINITY ? 0.f : __fdiv_rn(1.f, __fadd_rn(1.f, expf(-x)));
+  return x == -INFINITY ? 0.f : __frcp_rn(__fadd_rn(1.f, expf(-x)));
 }
 
 // The softmax's numerator; 0 for a masked logit.
@@ -105,14 +105,19 @@ __device__ __forceinline__ void softmax_terms(float (&x)[PL], float* top, float*
   *total = s;
 }
 
-__device__ __forceinline__ float softmax_score(float term, float total) {
-  return term > 0.f ? __fdiv_rn(term, total) : 0.f;
+// term / total rounded to nearest, r = 1 / total rounded to nearest (total is 1
+// to 1024): by the residual of the product with r, which is exact in an FMA
+// (Markstein 1990), where nothing underflows.
+__device__ __forceinline__ float softmax_score(float term, float total, float r) {
+  if (term < 0x1p-100f) return term > 0.f ? __fdiv_rn(term, total) : 0.f;
+  const float q = __fmul_rn(term, r);
+  return __fmaf_rn(__fmaf_rn(-q, total, term), r, q);
 }
 
 // The score of one expert's logit, as the row's scores were computed.
 __device__ __forceinline__ float one_score(float x, int score, float top, float total) {
   if (!(fabsf(x) < INFINITY)) return 0.f;
-  return score == TQ_SCORE_SIGMOID ? sigmoid_score(x) : softmax_score(softmax_term(x, top), total);
+  return score == TQ_SCORE_SIGMOID ? sigmoid_score(x) : softmax_score(softmax_term(x, top), total, __frcp_rn(total));
 }
 
 // Two largest of the four values in (a1 >= a2) and (b1 >= b2).
@@ -151,15 +156,49 @@ __device__ __forceinline__ unsigned choose_groups(const float* c, int groups, in
   return __ballot_sync(kAll, g < groups && s == 0 && better < top_groups);
 }
 
+// The same for groups of whole lanes (PL divides their size and `lanes`, the
+// lanes of one, is a power of two), from the values in registers; true in every
+// lane of a group that stays.
+template <int PL>
+__device__ __forceinline__ bool choose_lane_groups(const float (&c)[PL], int groups, int top_groups, int lanes,
+                                                   int lane) {
+  float a1 = c[0], a2 = -INFINITY;
+#pragma unroll
+  for (int i = 1; i < PL; ++i) {
+    a2 = fmaxf(a2, fminf(a1, c[i]));
+    a1 = fmaxf(a1, c[i]);
+  }
+  for (int o = 1; o < lanes; o <<= 1)
+    merge_top2(a1, a2, __shfl_xor_sync(kAll, a1, o), __shfl_xor_sync(kAll, a2, o));
+  float value = PL * lanes > 1 ? __fadd_rn(a1, a2) : a1;
+  if (!(value == value)) value = -INFINITY;
+  // lanes past the last group have the lowest key
+  uint32_t key = lane < groups * lanes ? order_key(__fadd_rn(value, 0.f)) : 0u;
+  bool stays = false;
+  for (int i = 0; i < top_groups; ++i) {
+    const uint32_t best = __reduce_max_sync(kAll, key);
+    const int first = __ffs(__ballot_sync(kAll, key == best)) - 1;   // the lowest group that has it
+    if (lane / lanes == first / lanes) {
+      stays = true;
+      key = 0u;
+    }
+  }
+  return stays;
+}
+
 template <typename T, int PL>
 __global__ void __launch_bounds__(kRouterThreads)
 router_scored_kernel(const T* __restrict__ logits, long long stride, const float* __restrict__ bias, int n, int E,
-                     int top_k, int score, int groups, int top_groups, int group_lanes, int renorm, float scale,
-                     bool vec, int32_t* __restrict__ ids, float* __restrict__ w) {
+                     int top_k, int score, int groups, int top_groups, int lane_groups, int group_lanes, int renorm,
+                     float scale, bool vec, int32_t* __restrict__ ids, float* __restrict__ w) {
   extern __shared__ float rows[];   // [warps][E], with groups only
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int e0 = lane * PL;
+  float b[PL];
+#pragma unroll
+  for (int i = 0; i < PL; ++i) b[i] = bias && e0 + i < E ? __ldg(bias + e0 + i) : 0.f;
   for (long long t = blockIdx.x * kRouterWarps + warp; t < n; t += gridDim.x * kRouterWarps) {
     const T* const row = logits + t * stride;
     float x[PL];
@@ -170,19 +209,24 @@ router_scored_kernel(const T* __restrict__ logits, long long stride, const float
     float top = 0.f, total = 0.f;
     if (score == TQ_SCORE_SOFTMAX) {
       softmax_terms<PL>(x, &top, &total);
+      const float r = __frcp_rn(total);
 #pragma unroll
-      for (int i = 0; i < PL; ++i) x[i] = softmax_score(x[i], total);
+      for (int i = 0; i < PL; ++i) x[i] = softmax_score(x[i], total, r);
     } else {
 #pragma unroll
       for (int i = 0; i < PL; ++i) x[i] = sigmoid_score(x[i]);
     }
-    const int e0 = lane * PL;
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-      if (bias && e0 + i < E) x[i] = __fadd_rn(x[i], __ldg(bias + e0 + i));
+      if (bias) x[i] = __fadd_rn(x[i], b[i]);
       if (!((live >> i) & 1u) || !(x[i] == x[i])) x[i] = -INFINITY;
     }
-    if (groups > 1) {
+    if (lane_groups > 0) {
+      if (!choose_lane_groups<PL>(x, groups, top_groups, lane_groups, lane)) {
+#pragma unroll
+        for (int i = 0; i < PL; ++i) x[i] = -INFINITY;
+      }
+    } else if (groups > 1) {
       float* const c = rows + warp * E;
       const int size = E / groups;
 #pragma unroll
@@ -208,25 +252,30 @@ router_scored_kernel(const T* __restrict__ logits, long long stride, const float
     int mine_e = 0;
     uint32_t mine_key = 0;
     for (int j = 0; j < top_k; ++j) {
-      uint32_t best = key[0];
-      int at = 0;
+      // largest key of the lane, by a tree; then of the warp; the lowest lane
+      // that has it, and its lowest expert
+      uint32_t m[PL];
 #pragma unroll
-      for (int i = 1; i < PL; ++i) {
-        if (key[i] > best) {
-          best = key[i];
-          at = i;
-        }
+      for (int i = 0; i < PL; ++i) m[i] = key[i];
+#pragma unroll
+      for (int w = 1; w < PL; w <<= 1) {
+#pragma unroll
+        for (int i = 0; i < PL; i += 2 * w) m[i] = max(m[i], m[i + w]);
       }
-      const uint32_t m = __reduce_max_sync(kAll, best);
-      const int src = __ffs(__ballot_sync(kAll, best == m)) - 1;
-      const int e = __shfl_sync(kAll, e0 + at, src);
+      const uint32_t best = __reduce_max_sync(kAll, m[0]);
+      uint32_t has = 0;
+#pragma unroll
+      for (int i = 0; i < PL; ++i) has |= (key[i] == best ? 1u : 0u) << i;
+      const int src = __ffs(__ballot_sync(kAll, has != 0)) - 1;
+      has = lane == src ? has & (0u - has) : 0u;   // its lowest bit
 #pragma unroll
       for (int i = 0; i < PL; ++i) {
-        if (e0 + i == e) key[i] = 0u;
+        if ((has >> i) & 1u) key[i] = 0u;
       }
+      const int e = __shfl_sync(kAll, e0 + __ffs(has) - 1, src);
       if (lane == j) {
         mine_e = e;
-        mine_key = m;
+        mine_key = best;
       }
     }
     // lane j < top_k: the j-th chosen expert's weight
@@ -289,6 +338,7 @@ router_scored_backward_kernel(const T* __restrict__ logits, long long stride, co
     } else {
       own = g * p * (1.f - p);
     }
+    const float r = __frcp_rn(total);   // of a row without finite logits infinite, and its terms are 0
     T* const out = grad + static_cast<size_t>(t) * E;
     const int e0 = lane * PL;
     constexpr int kVec = PL * static_cast<int>(sizeof(T)) >= 16 ? 16 / static_cast<int>(sizeof(T)) : PL;
@@ -297,7 +347,7 @@ router_scored_backward_kernel(const T* __restrict__ logits, long long stride, co
       T v[kVec];
 #pragma unroll
       for (int j = 0; j < kVec; ++j)
-        v[j] = narrow<T>(score == TQ_SCORE_SOFTMAX ? -softmax_score(x[i + j], total) * dot : 0.f);
+        v[j] = narrow<T>(score == TQ_SCORE_SOFTMAX ? -softmax_score(x[i + j], total, r) * dot : 0.f);
       if (vec_out && kVec * sizeof(T) == 16 && e0 + i + kVec <= E) {
         uint4 q;
         memcpy(&q, v, 16);
@@ -335,10 +385,14 @@ template <typename T, int PL>
 int run_forward(const RouterArgs& a, const T* logits, int32_t* ids, float* w, cudaStream_t s) {
   int lanes = 32;
   while (lanes * a.groups > 32) lanes >>= 1;
-  const size_t smem = a.groups > 1 ? sizeof(float) * kRouterWarps * a.E : 0;
+  // groups of a power of two of whole lanes are chosen from registers (8192 x
+  // 256 in 8 groups: 15.0 -> 11.9 us), others through shared memory
+  const int size = a.E / a.groups, whole = size % PL == 0 ? size / PL : 0;
+  const int lane_groups = a.groups > 1 && whole > 0 && (whole & (whole - 1)) == 0 ? whole : 0;
+  const size_t smem = a.groups > 1 && !lane_groups ? sizeof(float) * kRouterWarps * a.E : 0;
   return launch_pdl(router_scored_kernel<T, PL>, dim3(router_blocks(a.n)), dim3(kRouterThreads), smem, s, logits,
-                    a.stride, a.bias, static_cast<int>(a.n), a.E, a.top_k, a.score, a.groups, a.top_groups, lanes,
-                    a.renorm, a.scale, rows_aligned(logits, a.stride, sizeof(T)), ids, w);
+                    a.stride, a.bias, static_cast<int>(a.n), a.E, a.top_k, a.score, a.groups, a.top_groups, lane_groups,
+                    lanes, a.renorm, a.scale, rows_aligned(logits, a.stride, sizeof(T)), ids, w);
 }
 
 template <typename T, int PL>
