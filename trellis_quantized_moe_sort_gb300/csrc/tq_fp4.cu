@@ -14,7 +14,8 @@ size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool bad_format(int fmt) { return fmt != TQ_FP4_NV && fmt != TQ_FP4_MX; }
 constexpr size_t kNoWorkspace = 256;   // reported where none is used; a null workspace will do
-constexpr int64_t kMaxIndex = static_cast<int64_t>(1) << 31;
+// Rows of pairs and of weights: 32-bit coordinates with room for a tile past the end.
+constexpr int64_t kMaxIndex = (static_cast<int64_t>(1) << 31) - 1024;
 
 // Rows of fp4 values: K a multiple of 32, and small enough that a row's bytes
 // fit the 32-bit coordinates of the copies.

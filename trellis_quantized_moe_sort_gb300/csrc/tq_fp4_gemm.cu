@@ -43,8 +43,6 @@ struct GemmParams {
   const int32_t* sorted_pairs;   // nullptr: the pair of a slot is the slot
   const int32_t* tiles;          // nullptr: tile i = rows [i * tile_m, ...) of expert 0
   const int32_t* num_tiles;
-  const uint8_t* w_scales;       // tiled, [E][row groups][steps]
-  const uint8_t* x_scales;       // tiled, [tiles][tile row groups][steps]
   const float* x_scale;
   const float* w_scale;
   float* part;
@@ -78,10 +76,16 @@ struct Unit {
   bool ok;
 };
 
-__device__ __forceinline__ Unit unit_at(const GemmParams& p, long long u, int num_tiles) {
+// Unit u of this CTA: a pair of CTAs takes neighbouring row blocks of the same
+// m-tile (the second of them past the matrix where their number is odd: its
+// loads read what follows and its output rows do not exist).
+template <bool kPair>
+__device__ __forceinline__ Unit unit_at(const GemmParams& p, long long u, int num_tiles, int rank) {
   Unit t;
-  t.rb = static_cast<int>(u % p.row_blocks);
-  u /= p.row_blocks;
+  const int groups = kPair ? (p.row_blocks + 1) / 2 : p.row_blocks;
+  t.rb = static_cast<int>(u % groups);
+  if (kPair) t.rb = 2 * t.rb + rank;
+  u /= groups;
   t.tile = static_cast<int>(u % num_tiles);
   t.split = static_cast<int>(u / num_tiles);
   t.k0 = static_cast<int>(static_cast<long long>(p.steps) * t.split / p.splits);
@@ -101,38 +105,40 @@ __device__ __forceinline__ Unit unit_at(const GemmParams& p, long long u, int nu
 }
 
 // Instruction descriptor of the block-scaled kinds: E2M1 x E2M1, both K-major,
-// M x N, scales E4M3 (NV) or E8M0 (MX); the scales of the MMA start at byte
-// `sf` of their 32-bit columns.
-template <int kFmt>
+// M x N (M = 256 over a pair), scales E4M3 (NV) or E8M0 (MX); the scales of the
+// MMA start at byte `sf` of their 32-bit columns.
+template <int kFmt, bool kPair>
 __device__ __forceinline__ uint32_t idesc_fp4(uint32_t n, uint32_t sf) {
   return (sf << 4)                                        // B scale id
          | (1u << 7)                                      // A: E2M1
          | (1u << 10)                                     // B: E2M1
          | ((n >> 3) << 17)                               // N / 8
          | ((kFmt == TQ_FP4_MX ? 1u : 0u) << 23)          // scale type: E8M0 or E4M3
-         | ((kRows >> 4) << 24)                           // M / 16
+         | (((kPair ? 2 * kRows : kRows) >> 4) << 24)     // M / 16
          | (sf << 29);                                    // A scale id
 }
 
-template <int kFmt>
+#define TQ_FP4_MMA(group, kind)                                                                              \
+  asm volatile(                                                                                             \
+      "{\n\t.reg .pred p;\n\t"                                                                             \
+      "setp.ne.b32 p, %6, 0;\n\t"                                                                           \
+      "tcgen05.mma.cta_group::" group ".kind::" kind " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),      \
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                                        \
+      : "memory")
+template <int kFmt, bool kPair>
 __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                         uint32_t accumulate) {
-  if constexpr (kFmt == TQ_FP4_NV) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
+  if constexpr (kFmt == TQ_FP4_NV && kPair) {
+    TQ_FP4_MMA("2", "mxf4nvf4.block_scale.scale_vec::4X");
+  } else if constexpr (kFmt == TQ_FP4_NV) {
+    TQ_FP4_MMA("1", "mxf4nvf4.block_scale.scale_vec::4X");
+  } else if constexpr (kPair) {
+    TQ_FP4_MMA("2", "mxf4.block_scale.scale_vec::2X");
   } else {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
+    TQ_FP4_MMA("1", "mxf4.block_scale.scale_vec::2X");
   }
 }
+#undef TQ_FP4_MMA
 
 // Shared-memory descriptors from an address in units of 16 bytes: a K-major
 // operand in 128-byte swizzled rows (8-row groups 1024 bytes apart), and a
@@ -146,15 +152,90 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t at) {
          static_cast<uint64_t>(1) << 46;
 }
 // Copies a scale tile to four tensor-memory columns, replicated over the four
-// lane quarters.
+// lane quarters; a pair's copy does so in both CTAs, each from its own shared
+// memory.
+template <bool kPair>
 __device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+  if constexpr (kPair)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
+// A 2-D box whose bytes count on the pair's first CTA's barrier (`bar`, an
+// address of the cluster's shared memory).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* m, int32_t x, int32_t y,
+                                                 uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+template <bool kPair>
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* m, int32_t x, int32_t y, uint32_t bar) {
+  if constexpr (kPair)
+    tma_load_2d_pair(dst, m, x, y, bar);
+  else
+    tma_load_2d(dst, m, x, y, bar);
+}
+
+// Arrives on the barrier (of both CTAs of a pair) once every MMA issued so far
+// has completed.
+template <bool kPair>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (kPair)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    mma_commit(bar);
+}
+
+// The same on a barrier of this CTA alone.
+template <bool kPair>
+__device__ __forceinline__ void commit_own(uint32_t bar) {
+  if constexpr (kPair)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  else
+    mma_commit(bar);
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The address in the cluster's shared memory of CTA `rank`'s `addr`.
+__device__ __forceinline__ uint32_t of_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <bool kPair>
+__device__ __forceinline__ void alloc_columns(uint32_t dst, uint32_t columns) {
+  if constexpr (kPair) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(dst, columns);
+  }
+}
+template <bool kPair>
+__device__ __forceinline__ void free_columns(uint32_t tmem, uint32_t columns) {
+  if constexpr (kPair)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns) : "memory");
+  else
+    tmem_dealloc(tmem, columns);
 }
 
 // take(values, output rows) for each 16 columns of this warp's accumulator
@@ -214,9 +295,10 @@ __device__ __forceinline__ void store_y(const GemmParams& p, uint32_t src, int r
   }
 }
 
-template <int kFmt>
+template <int kFmt, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
 fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                const __grid_constant__ CUtensorMap tm_ws, const __grid_constant__ CUtensorMap tm_xs,
                 const GemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -225,6 +307,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   constexpr int kSfStep = fp4_scale_step_bytes(kFmt);   // per 128 rows and step
   constexpr int kSfTiles = kSfStep / 512;               // scale tiles per step (4 NV, 2 MX)
+  const int rank = kPair ? static_cast<int>(cluster_rank()) : 0;
+  const bool first = rank == 0;   // of the pair: the barriers that the MMA waits for are its
 
   const uint32_t bar_full = base + p.off_bar;
   const uint32_t bar_empty = bar_full + 8 * kMaxStages;
@@ -241,24 +325,29 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
     }
     for (int a = 0; a < p.accs; ++a) {
       mbar_init(bar_accfull + 8 * a, 1);
-      mbar_init(bar_accempty + 8 * a, 4);
+      mbar_init(bar_accempty + 8 * a, kPair ? 8 : 4);
     }
     mbar_init(bar_drain, 1);
     *abort_flag = 0;
     mbar_fence_init();
     tma_prefetch_desc(&tm_w);
     tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_ws);
+    tma_prefetch_desc(&tm_xs);
   }
-  if (warp == kWarpLoadW) tmem_alloc(smem_u32(tmem_holder), static_cast<uint32_t>(p.tmem_cols));
+  if (warp == kWarpLoadW) alloc_columns<kPair>(smem_u32(tmem_holder), static_cast<uint32_t>(p.tmem_cols));
   tc_fence_before();
   __syncthreads();
+  if (kPair) cluster_sync();   // both CTAs' barriers are ready
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
   pdl_wait();   // the tile map, the staged activations
 
   const int num_tiles = p.tiles ? static_cast<int>(min(static_cast<long long>(*p.num_tiles), p.cap))
                                 : static_cast<int>(p.cap);
-  const long long units = static_cast<long long>(num_tiles) * p.row_blocks * p.splits;
+  const long long units =
+      static_cast<long long>(num_tiles) * (kPair ? (p.row_blocks + 1) / 2 : p.row_blocks) * p.splits;
+  const int unit0 = kPair ? blockIdx.x / 2 : blockIdx.x, unit_step = kPair ? gridDim.x / 2 : gridDim.x;
   // in registers: read through the parameter they would be fetched again after
   // every asm with a memory clobber
   const int stages = p.stages, accs = p.accs, stage_bytes = p.stage_bytes, x_bytes = p.x_bytes;
@@ -270,46 +359,51 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
     // as the step's MMAs.)
     if (elect_one()) {
       const bool is_w = warp == kWarpLoadW;
-      const uint32_t bytes = static_cast<uint32_t>(is_w ? kWBytes + kSfStep : x_bytes + p.x_sf_bytes);
+      // bytes of a step that count on the barrier: both CTAs' in a pair, which
+      // splits the tile's rows; each CTA holds all of their scales
+      const uint32_t bytes = static_cast<uint32_t>(is_w ? kWBytes + kSfStep : x_bytes + p.x_sf_bytes) * (kPair ? 2 : 1);
       const uint32_t to_codes = is_w ? 0u : kWBytes;
       const uint32_t to_scales = static_cast<uint32_t>(kWBytes + x_bytes + (is_w ? 0 : kSfStep));
       const bool two_groups = !is_w && p.x_sf_bytes > kSfStep;
       const CUtensorMap* const map = is_w ? &tm_w : &tm_x;
-      const size_t group = static_cast<size_t>(p.steps) * kSfStep;   // scales of one 128-row group
-      const uint8_t* const scales = is_w ? p.w_scales : p.x_scales;
-      const int x_groups = p.x_sf_bytes / kSfStep;
+      const CUtensorMap* const scale_map = is_w ? &tm_ws : &tm_xs;
+      constexpr int kSfRows = kSfStep / 128;   // 128-byte rows of the scale maps per step
+      const int x_groups = p.x_sf_bytes / kSfStep, group = p.steps * kSfRows;
+      const uint32_t full0 = kPair ? of_cta(bar_full, 0) : bar_full;
       Ring ring;
       long long issued = 0;
       bool ok = true, ready = false;
-      for (long long u = blockIdx.x; ok && u < units; u += gridDim.x) {
-        const Unit t = unit_at(p, u, num_tiles);
+      for (long long u = unit0; ok && u < units; u += unit_step) {
+        const Unit t = unit_at<kPair>(p, u, num_tiles, rank);
         if (!t.ok) {
-          if (is_w) record_error(err, TQ_ERR_INVALID_ARG, kWhereFp4Load);
+          if (is_w && first) record_error(err, TQ_ERR_INVALID_ARG, kWhereFp4Load);
           continue;
         }
-        const int row = is_w ? t.e * p.N + t.rb * kRows : t.slot0;
-        const uint8_t* sf = scales + static_cast<size_t>(t.k0) * kSfStep +
-                            (is_w ? static_cast<size_t>(t.e) * p.row_blocks + t.rb
-                                  : static_cast<size_t>(t.tile) * x_groups) * group;
+        const int half = kPair ? rank * (((t.rows + 15) & ~15) / 2) : 0;
+        const int row = is_w ? t.e * p.N + t.rb * kRows : t.slot0 + half;
+        int sf = t.k0 * kSfRows + (is_w ? t.e * p.row_blocks + t.rb : t.tile * x_groups) * group;
         for (int k = t.k0; k < t.k1; ++k) {
           if (!ready &&
               !mbar_wait_short(bar_empty + 8 * ring.at, ring.phase ^ 1u, abort_flag, err, kWhereFp4Load)) {
             ok = false;
             break;
           }
-          const uint32_t full = bar_full + 8 * ring.at;
+          const uint32_t full = full0 + 8 * ring.at;
           const uint32_t dst = base + static_cast<uint32_t>(ring.at * stage_bytes);
-          mbar_arrive_expect_tx(full, bytes);
-          tma_load_2d(dst + to_codes, map, k * kRowBytes, row, full);
-          bulk_load(dst + to_scales, sf, kSfStep, full);
-          if (two_groups) bulk_load(dst + to_scales + kSfStep, sf + group, kSfStep, full);
-          sf += kSfStep;
+          if (first) mbar_arrive_expect_tx(bar_full + 8 * ring.at, bytes);
+          load_box<kPair>(dst + to_codes, map, k * kRowBytes, row, full);
+          load_box<kPair>(dst + to_scales, scale_map, 0, sf, full);
+          if (two_groups) load_box<kPair>(dst + to_scales + kSfStep, scale_map, 0, sf + group, full);
+          sf += kSfRows;
           ++issued;
           ring.advance(stages);
           ready = mbar_test(bar_empty + 8 * ring.at, ring.phase ^ 1u);
         }
       }
-      // every copy issued has landed before the CTA exits
+      // Before the CTA exits, every copy issued has landed (of a pair: in both
+      // CTAs, counted on the first's barriers) and, in the second CTA, every
+      // arrival that the MMAs owe its barriers.
+      const uint32_t bars = first ? bar_full : bar_empty;
       const long long pending = min(issued, static_cast<long long>(stages));
       for (long long i = 1; i <= pending; ++i) {
         int st = ring.at - static_cast<int>(i);
@@ -319,7 +413,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
           ph ^= 1u;
         }
         const uint64_t t0 = globaltimer();
-        while (!mbar_try_wait(bar_full + 8 * st, ph)) {
+        while (!mbar_try_wait(bars + 8 * st, ph)) {
           if (globaltimer() - t0 > kWaitTimeoutNs) {
             record_error(err, TQ_ERR_DEVICE_TIMEOUT, kWhereFp4Teardown);
             break;
@@ -328,6 +422,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
       }
     }
     __syncwarp();
+  } else if (warp == kWarpMma && !first) {
+    // the first CTA of the pair issues for both
   } else if (warp == kWarpMma) {
     // The whole warp walks the steps, so that stage addresses and descriptors
     // stay in uniform registers; one elected thread issues.  A wait that gives
@@ -344,12 +440,12 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
     bool ready = false;
     const bool leader = elect_one();
     Ring acc;
-    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-      const Unit t = unit_at(p, u, num_tiles);
+    for (long long u = unit0; u < units; u += unit_step) {
+      const Unit t = unit_at<kPair>(p, u, num_tiles, rank);
       if (!t.ok) continue;
       const uint32_t n_mma = static_cast<uint32_t>((t.rows + 15) & ~15);
       const bool wide = n_mma > 128;
-      const uint32_t idesc = idesc_fp4<kFmt>(n_mma, 0), idesc_odd = idesc_fp4<kFmt>(n_mma, 2);
+      const uint32_t idesc = idesc_fp4<kFmt, kPair>(n_mma, 0), idesc_odd = idesc_fp4<kFmt, kPair>(n_mma, 2);
       mbar_wait_short(bar_accempty + 8 * acc.at, acc.phase ^ 1u, abort_flag, err, kWhereFp4Mma);
       tc_fence_after();
       const uint32_t d = tmem + static_cast<uint32_t>(acc.at * p.acc_cols);
@@ -370,20 +466,20 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
           const uint64_t s_desc = scale_desc(this_desc + desc_sf);
 #pragma unroll
           for (int i = 0; i < kSfTiles; ++i) {
-            copy_scales(sfa + 4 * i, s_desc + 32 * i);
+            copy_scales<kPair>(sfa + 4 * i, s_desc + 32 * i);
             // row group r of the tile's scales: columns 4r .. 4r + 3 of its block group
-            copy_scales(sfb + 8 * i, s_desc + kSfStep / 16 + 32 * i);
-            if (wide) copy_scales(sfb + 8 * i + 4, s_desc + 2 * kSfStep / 16 + 32 * i);
+            copy_scales<kPair>(sfb + 8 * i, s_desc + kSfStep / 16 + 32 * i);
+            if (wide) copy_scales<kPair>(sfb + 8 * i + 4, s_desc + 2 * kSfStep / 16 + 32 * i);
           }
           // values past K are zeros with finite scales: always four MMAs
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             constexpr int kPer = 4 / kSfTiles;   // MMAs per scale tile
-            mma_fp4<kFmt>(d, w_desc + 2 * i, x_desc + 2 * i, (kPer == 2 && (i & 1)) ? idesc_odd : idesc,
+            mma_fp4<kFmt, kPair>(d, w_desc + 2 * i, x_desc + 2 * i, (kPer == 2 && (i & 1)) ? idesc_odd : idesc,
                           sfa + 4 * (i / kPer), sfb + 8 * (i / kPer), (k != t.k0 || i != 0) ? 1u : 0u);
           }
-          mma_commit(this_bar + 8 * kMaxStages);   // the stage's empty barrier
-          if (k == t.k1 - 1) mma_commit(bar_accfull + 8 * acc.at);
+          commit<kPair>(this_bar + 8 * kMaxStages);   // the stage's empty barrier
+          if (k == t.k1 - 1) commit<kPair>(bar_accfull + 8 * acc.at);
         }
       }
       acc.advance(accs);
@@ -391,7 +487,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
     }
     __syncwarp();
     if (elect_one()) {   // every MMA issued has completed before teardown
-      mma_commit(bar_drain);
+      commit_own<kPair>(bar_drain);
       const uint64_t t0 = globaltimer();
       while (!mbar_try_wait(bar_drain, 0)) {
         if (globaltimer() - t0 > kWaitTimeoutNs) {
@@ -408,8 +504,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
     const int q = warp & 3;
     int* const rows_out = reinterpret_cast<int*>(gbase + p.off_rows) + 256 * q;
     Ring acc;
-    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-      const Unit t = unit_at(p, u, num_tiles);
+    for (long long u = unit0; u < units; u += unit_step) {
+      const Unit t = unit_at<kPair>(p, u, num_tiles, rank);
       if (!t.ok) continue;
       __syncwarp();   // the last unit's rows have been read
       for (int col = lane; col < ((t.rows + 15) & ~15); col += 32) {
@@ -450,7 +546,12 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_accempty + 8 * acc.at);
+      if (lane == 0) {
+        if (kPair && !first)
+          cluster_arrive(of_cta(bar_accempty + 8 * acc.at, 0));
+        else
+          mbar_arrive(bar_accempty + 8 * acc.at);
+      }
       acc.advance(accs);
     }
   }
@@ -458,9 +559,10 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
   pdl_trigger();
   tc_fence_before();
   __syncthreads();
+  if (kPair) cluster_sync();   // neither CTA's memory is needed by the other any more
   if (warp == kWarpLoadW) {
     tc_fence_after();
-    tmem_dealloc(tmem, static_cast<uint32_t>(p.tmem_cols));
+    free_columns<kPair>(tmem, static_cast<uint32_t>(p.tmem_cols));
   }
 }
 
@@ -477,16 +579,17 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-// Codes as a 2-D tensor of bytes, boxes of one step x `rows`.
-bool encode_codes(CUtensorMap* m, const uint8_t* codes, int64_t rows, int K, int box_rows) {
+// Codes as a 2-D tensor of bytes, boxes of one step x `box_rows`
+// (swizzled), or scales in the tiled layout as rows of 128 bytes.
+bool encode_bytes(CUtensorMap* m, const uint8_t* bytes, int64_t rows, int row_bytes, int box_rows, bool swizzle) {
   auto encode = encoder();
   if (!encode) return false;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K / 2), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 2)};
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
   const cuuint32_t box[2] = {kRowBytes, static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[2] = {1, 1};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, box, estr,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(bytes), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -517,8 +620,6 @@ int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s) {
   p.sorted_pairs = g.sorted_pairs;
   p.tiles = g.tiles;
   p.num_tiles = g.num_tiles;
-  p.w_scales = g.w_scales;
-  p.x_scales = g.x_scales;
   p.x_scale = g.x_scale;
   p.w_scale = g.w_scale;
   p.part = g.part;
@@ -540,7 +641,12 @@ int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s) {
 
   const int sf_step = fp4_scale_step_bytes(g.fmt);
   const int x_groups = (p.n_max + 127) / 128;
-  p.x_bytes = p.n_max * kRowBytes;
+  // Pairs of CTAs (two SMs sharing one MMA of 256 weight rows, each holding half
+  // of the activation rows) from 128 rows per m-tile on: a CTA then takes in 36
+  // KB a step for 128 x 224 results in place of 51, and that intake, about 50
+  // bytes a clock, is what bounds large products.
+  const bool pair = p.n_max >= 128;
+  p.x_bytes = (pair ? p.n_max / 2 : p.n_max) * kRowBytes;
   p.x_sf_bytes = x_groups * sf_step;
   p.stage_bytes = kWBytes + p.x_bytes + sf_step + p.x_sf_bytes;
   const int bar_bytes = (8 * kNumBars + 16 + 15) / 16 * 16, rows_bytes = 4 * 256 * 4;
@@ -559,20 +665,42 @@ int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s) {
   p.tmem_cols = 32;
   while (p.tmem_cols < p.sf_col + sf_cols) p.tmem_cols <<= 1;
 
-  CUtensorMap tm_w, tm_x;
-  if (!encode_codes(&tm_w, g.w, static_cast<int64_t>(g.E) * g.N, g.K, kRows) ||
-      !encode_codes(&tm_x, g.x, g.P, g.K, p.n_max))
+  CUtensorMap tm_w, tm_x, tm_ws, tm_xs;
+  const int64_t w_groups = static_cast<int64_t>(g.E) * p.row_blocks, x_tiles = g.cap * x_groups;
+  const int sf_rows = sf_step / 128;
+  if (!encode_bytes(&tm_w, g.w, static_cast<int64_t>(g.E) * g.N, g.K / 2, kRows, true) ||
+      !encode_bytes(&tm_x, g.x, g.P, g.K / 2, pair ? p.n_max / 2 : p.n_max, true) ||
+      !encode_bytes(&tm_ws, g.w_scales, w_groups * p.steps * sf_rows, 128, sf_rows, false) ||
+      !encode_bytes(&tm_xs, g.x_scales, x_tiles * p.steps * sf_rows, 128, sf_rows, false))
     return TQ_ERR_INVALID_ARG;
-  auto kernel = g.fmt == TQ_FP4_NV ? fp4_gemm_kernel<TQ_FP4_NV> : fp4_gemm_kernel<TQ_FP4_MX>;
+  auto kernel = g.fmt == TQ_FP4_NV ? (pair ? fp4_gemm_kernel<TQ_FP4_NV, true> : fp4_gemm_kernel<TQ_FP4_NV, false>)
+                                   : (pair ? fp4_gemm_kernel<TQ_FP4_MX, true> : fp4_gemm_kernel<TQ_FP4_MX, false>);
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess) {
     cudaGetLastError();
     return TQ_ERR_CUDA;
   }
-  const long long units = g.cap * p.row_blocks * p.splits;
-  const int grid = static_cast<int>(std::max<long long>(1, std::min<long long>(units, sm_count())));
-  const int st = launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, s, tm_w, tm_x, p);
-  if (st == TQ_OK) count_launch(kCntFp4Gemm);
-  return st;
+  const long long units = g.cap * (pair ? (p.row_blocks + 1) / 2 : p.row_blocks) * p.splits;
+  const int width = pair ? 2 : 1;
+  const int grid = width * static_cast<int>(std::max<long long>(1, std::min<long long>(units, sm_count() / width)));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = width;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pair ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_x, tm_ws, tm_xs, p) != cudaSuccess) {
+    cudaGetLastError();
+    return TQ_ERR_LAUNCH;
+  }
+  count_launch(kCntFp4Gemm);
+  return TQ_OK;
 }
 
 }  // namespace tq
