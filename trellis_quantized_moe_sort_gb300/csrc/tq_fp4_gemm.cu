@@ -34,8 +34,9 @@ constexpr int kRowBytes = kFp4Step / 2; // a step of one row: one 128-byte swizz
 constexpr int kWBytes = kRows * kRowBytes;
 constexpr int kMaxStages = 12;
 constexpr int kMaxAcc = 4;
-constexpr int kThreads = 224;
-constexpr int kWarpLoadW = 0, kWarpMma = 1, kWarpLoadX = 6;   // warps 2-5: epilogue, one per lane quarter
+constexpr int kWarpLoadW = 0, kWarpMma = 1, kWarpEpi0 = 2, kEpiWarps = 8;   // epilogue: two warps per lane quarter
+constexpr int kWarpLoadX = kWarpEpi0 + kEpiWarps;
+constexpr int kThreads = 32 * (kWarpLoadX + 1);
 constexpr int kSmemLimit = 232448;
 constexpr int kNumBars = 2 * kMaxStages + 2 * kMaxAcc + 1;
 
@@ -45,9 +46,8 @@ struct GemmParams {
   const int32_t* num_tiles;
   const float* x_scale;
   const float* w_scale;
-  float* part;
-  void* y;
-  int y_type;                    // of y; part is used when y is null
+  void* y;                       // [P][N], or fp32 [splits][P][N]
+  int scaled;                    // by x_scale and w_scale: y is the result, not partial sums
   int y_pairs;                   // y's rows start on multiples of two values
   int* err;
   long long cap, split_stride;
@@ -238,48 +238,60 @@ __device__ __forceinline__ void free_columns(uint32_t tmem, uint32_t columns) {
     tmem_dealloc(tmem, columns);
 }
 
-// take(values, output rows) for each 16 columns of this warp's accumulator
-// rows, the next 16 in flight meanwhile.
-template <typename Take>
-__device__ __forceinline__ void drain(uint32_t src, int rows, const int* rows_out, Take&& take) {
-  uint32_t v[2][16];
-  tmem_ld16(src, v[0]);
+// The output rows of 16 columns.
+__device__ __forceinline__ void read_rows(const int* p, int (&row)[16]) {
 #pragma unroll
-  for (int b = 0; b < 16; ++b) {
-    if (16 * b >= rows) break;
-    tmem_wait_ld();
-    if (16 * (b + 1) < rows) tmem_ld16(src + 16 * (b + 1), v[(b + 1) & 1]);
-    int row[16];
-#pragma unroll
-    for (int j = 0; j < 16; j += 4) {
-      const int4 r = *reinterpret_cast<const int4*>(rows_out + 16 * b + j);
-      row[j] = r.x;
-      row[j + 1] = r.y;
-      row[j + 2] = r.z;
-      row[j + 3] = r.w;
-    }
-    take(v[b & 1], row);
+  for (int j = 0; j < 16; j += 4) {
+    const int4 r = *reinterpret_cast<const int4*>(p + j);
+    row[j] = r.x;
+    row[j + 1] = r.y;
+    row[j + 2] = r.z;
+    row[j + 3] = r.w;
   }
 }
 
-// y[row][f] = alpha * D, rounded once.  16-bit types with an even width:
+// take(values, output rows) for every second 16 columns of this warp's
+// accumulator rows, from the `half`-th on, the next ones in flight meanwhile.
+// (Two blocks a turn and no more: unrolled over the whole tile the addresses
+// spill.)
+template <typename Take>
+__device__ __forceinline__ void drain(uint32_t src, int rows, int half, const int* rows_out, Take&& take) {
+  uint32_t v[2][16];
+  int row[16];
+  src += 16 * half;
+  rows -= 16 * half;
+  rows_out += 16 * half;
+  if (rows > 0) tmem_ld16(src, v[0]);
+#pragma unroll 1
+  for (int c = 0; c < rows; c += 64) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = c + 32 * i;
+      if (at >= rows) break;
+      tmem_wait_ld();
+      if (at + 32 < rows) tmem_ld16(src + at + 32, v[(i + 1) & 1]);
+      read_rows(rows_out + at, row);
+      take(v[i], row);
+    }
+  }
+}
+
+// out[row][f] = alpha * D, rounded once.  16-bit types with an even width:
 // neighbouring lanes exchange so that each stores two rows of one column.
 template <typename T>
-__device__ __forceinline__ void store_y(const GemmParams& p, uint32_t src, int rows, const int* rows_out, int f,
-                                        float alpha) {
-  T* const y = static_cast<T*>(p.y);
-  const int N = p.N;
-  if (sizeof(T) == 4 || !p.y_pairs) {
+__device__ __forceinline__ void store_columns(T* out, bool by_two, int N, uint32_t src, int rows, int half,
+                                              const int* rows_out, int f, float alpha) {
+  if (sizeof(T) == 4 || !by_two) {
     const bool in = f < N;
-    drain(src, rows, rows_out, [&](const uint32_t (&v)[16], const int (&row)[16]) {
+    drain(src, rows, half, rows_out, [&](const uint32_t (&v)[16], const int (&row)[16]) {
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        if (row[j] >= 0 && in) y[static_cast<size_t>(row[j]) * N + f] = narrow<T>(__uint_as_float(v[j]) * alpha);
+        if (row[j] >= 0 && in) out[static_cast<size_t>(row[j]) * N + f] = narrow<T>(__uint_as_float(v[j]) * alpha);
       }
     });
   } else {
     const bool odd = f & 1, in = (f & ~1) < N;
-    drain(src, rows, rows_out, [&](const uint32_t (&v)[16], const int (&row)[16]) {
+    drain(src, rows, half, rows_out, [&](const uint32_t (&v)[16], const int (&row)[16]) {
 #pragma unroll
       for (int j = 0; j < 16; j += 2) {
         const uint32_t give = odd ? v[j] : v[j + 1], keep = odd ? v[j + 1] : v[j];
@@ -289,13 +301,13 @@ __device__ __forceinline__ void store_y(const GemmParams& p, uint32_t src, int r
         const int to = odd ? row[j + 1] : row[j];
         uint32_t bits;
         memcpy(&bits, two, 4);
-        if (to >= 0 && in) *reinterpret_cast<uint32_t*>(y + static_cast<size_t>(to) * N + (f & ~1)) = bits;
+        if (to >= 0 && in) *reinterpret_cast<uint32_t*>(out + static_cast<size_t>(to) * N + (f & ~1)) = bits;
       }
     });
   }
 }
 
-template <int kFmt, bool kPair>
+template <int kFmt, bool kPair, typename TOut>
 __global__ void __launch_bounds__(kThreads, 1)
 fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                 const __grid_constant__ CUtensorMap tm_ws, const __grid_constant__ CUtensorMap tm_xs,
@@ -325,7 +337,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
     }
     for (int a = 0; a < p.accs; ++a) {
       mbar_init(bar_accfull + 8 * a, 1);
-      mbar_init(bar_accempty + 8 * a, kPair ? 8 : 4);
+      mbar_init(bar_accempty + 8 * a, (kPair ? 2 : 1) * kEpiWarps);
     }
     mbar_init(bar_drain, 1);
     *abort_flag = 0;
@@ -501,8 +513,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
     // Lane l of quarter q holds weight row 32 q + l of every column.  The
     // output row of each column is kept in shared memory (read back four at a
     // time, the same for all lanes), -1 for none.
-    const int q = warp & 3;
-    int* const rows_out = reinterpret_cast<int*>(gbase + p.off_rows) + 256 * q;
+    const int q = warp & 3, half = (warp - kWarpEpi0) >> 2;
+    int* const rows_out = reinterpret_cast<int*>(gbase + p.off_rows) + 256 * (warp - kWarpEpi0);
     Ring acc;
     for (long long u = unit0; u < units; u += unit_step) {
       const Unit t = unit_at<kPair>(p, u, num_tiles, rank);
@@ -524,26 +536,13 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
       tc_fence_after();
       const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(acc.at * p.acc_cols);
       const int f = t.rb * kRows + 32 * q + lane;
-      if (!p.y) {
-        float* const out = p.part + static_cast<size_t>(t.split) * p.split_stride + f;
-        const int N = p.N;
-        const bool in = f < N;
-        drain(src, t.rows, rows_out, [&](const uint32_t (&v)[16], const int (&row)[16]) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            if (row[j] >= 0 && in) out[static_cast<size_t>(row[j]) * N] = __uint_as_float(v[j]);
-          }
-        });
-      } else {
-        const float alpha = (p.x_scale ? __ldg(p.x_scale) : 1.f) * (p.w_scale ? __ldg(p.w_scale + t.e) : 1.f);
-        if (p.y_type == TQ_FP32) {
-          store_y<float>(p, src, t.rows, rows_out, f, alpha);
-        } else if (p.y_type == TQ_BF16) {
-          store_y<__nv_bfloat16>(p, src, t.rows, rows_out, f, alpha);
-        } else {
-          store_y<__half>(p, src, t.rows, rows_out, f, alpha);
-        }
-      }
+      TOut* out = static_cast<TOut*>(p.y);
+      float alpha = 1.f;
+      if (p.scaled)
+        alpha = (p.x_scale ? __ldg(p.x_scale) : 1.f) * (p.w_scale ? __ldg(p.w_scale + t.e) : 1.f);
+      else
+        out += static_cast<size_t>(t.split) * p.split_stride;
+      store_columns<TOut>(out, p.y_pairs, p.N, src, t.rows, half, rows_out, f, alpha);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -595,6 +594,12 @@ bool encode_bytes(CUtensorMap* m, const uint8_t* bytes, int64_t rows, int row_by
 
 }  // namespace
 
+template <typename TOut>
+static auto kernel_for(int fmt, bool pair) {
+  return fmt == TQ_FP4_NV ? (pair ? fp4_gemm_kernel<TQ_FP4_NV, true, TOut> : fp4_gemm_kernel<TQ_FP4_NV, false, TOut>)
+                          : (pair ? fp4_gemm_kernel<TQ_FP4_MX, true, TOut> : fp4_gemm_kernel<TQ_FP4_MX, false, TOut>);
+}
+
 // K splits of a product of at most `tiles` m-tiles: as many whole rounds of
 // the SMs as the units make, the count (up to 8, a step at least each) whose
 // last round wastes least; one when the units fill four rounds by themselves.
@@ -622,9 +627,8 @@ int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s) {
   p.num_tiles = g.num_tiles;
   p.x_scale = g.x_scale;
   p.w_scale = g.w_scale;
-  p.part = g.part;
-  p.y = g.y;
-  p.y_type = g.y_type;
+  p.y = g.y ? g.y : g.part;
+  p.scaled = g.y != nullptr;
   p.y_pairs = g.N % 2 == 0 && (reinterpret_cast<uintptr_t>(g.y) & 3u) == 0;
   p.err = g.err;
   p.cap = g.cap;
@@ -649,7 +653,7 @@ int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s) {
   p.x_bytes = (pair ? p.n_max / 2 : p.n_max) * kRowBytes;
   p.x_sf_bytes = x_groups * sf_step;
   p.stage_bytes = kWBytes + p.x_bytes + sf_step + p.x_sf_bytes;
-  const int bar_bytes = (8 * kNumBars + 16 + 15) / 16 * 16, rows_bytes = 4 * 256 * 4;
+  const int bar_bytes = (8 * kNumBars + 16 + 15) / 16 * 16, rows_bytes = kEpiWarps * 256 * 4;
   p.stages = std::min(kMaxStages, (kSmemLimit - 1024 - bar_bytes - rows_bytes) / p.stage_bytes);
   p.off_bar = static_cast<uint32_t>(p.stages * p.stage_bytes);
   p.off_rows = p.off_bar + bar_bytes;
@@ -673,8 +677,10 @@ int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s) {
       !encode_bytes(&tm_ws, g.w_scales, w_groups * p.steps * sf_rows, 128, sf_rows, false) ||
       !encode_bytes(&tm_xs, g.x_scales, x_tiles * p.steps * sf_rows, 128, sf_rows, false))
     return TQ_ERR_INVALID_ARG;
-  auto kernel = g.fmt == TQ_FP4_NV ? (pair ? fp4_gemm_kernel<TQ_FP4_NV, true> : fp4_gemm_kernel<TQ_FP4_NV, false>)
-                                   : (pair ? fp4_gemm_kernel<TQ_FP4_MX, true> : fp4_gemm_kernel<TQ_FP4_MX, false>);
+  const int type = g.y ? g.y_type : TQ_FP32;
+  auto kernel = type == TQ_FP32   ? kernel_for<float>(g.fmt, pair)
+                : type == TQ_BF16 ? kernel_for<__nv_bfloat16>(g.fmt, pair)
+                                  : kernel_for<__half>(g.fmt, pair);
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess) {
     cudaGetLastError();
     return TQ_ERR_CUDA;
