@@ -360,3 +360,57 @@ def test_argument_errors():
             tq.tq_fp4_moe_forward(x, a["packed"], w.tiled, a["ids"], a["tw"], y=a["y"])
     with pytest.raises(tq.TQError):                                  # MX has no global scales
         tq.tq_fp4_linear(x, w.packed[0], w.tiled[: w.tiled.numel() // 8], fmt=tq.FP4_MX, w_scale=torch.ones(1, device="cuda"))
+
+
+# Many pairs to an expert, rows of very different sizes, an id out of range.
+@pytest.mark.parametrize("N", [1024, 1027, 1006])
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+def test_experts_many_pairs(fmt, N):
+    rng = np.random.default_rng(N)
+    n, E, k, K = 1500, 8, 3, 96
+    w = Weights(rng, E, N, K, fmt)
+    x = _x(rng, n, K, "bf16", spread=1.0)
+    x[3] = 0
+    x[4] *= 2.0 ** 60
+    x[5] *= 2.0 ** -60
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(n)]).astype(np.int32)
+    ids[7, 1] = 99
+    weights = rng.standard_normal((n, k)).astype(np.float32)
+    args = (x.cuda(), w.packed, w.tiled, torch.from_numpy(ids).cuda(), torch.from_numpy(weights).cuda())
+    y = tq.tq_fp4_moe_forward(*args, fmt=w.fmt, w_scale=w.scale)
+    torch.cuda.synchronize()
+    assert tq.tq_device_error()[0] == -1                      # of the one id
+    xq = M.quantize(_f64(x), fmt)[2]
+    want, size = np.zeros((n, N)), np.zeros((n, N))
+    for e in range(E):
+        t, j = np.nonzero(ids == e)
+        p = xq[t] @ w.values[e].T
+        c = weights[t, j, None].astype(np.float64)
+        np.add.at(want, t, c * p)
+        np.add.at(size, t, np.abs(c) * (np.abs(xq[t]) @ np.abs(w.values[e]).T))
+    got = _f64(y)
+    limit = 2.0 ** -16 * size + 2.0 ** -8 * np.abs(want) + 1e-37
+    assert (np.abs(got - want) <= limit).all()
+    # values themselves, not only the largest: the 2-norm is that of bf16 rounding
+    rows = np.setdiff1d(np.arange(n), [4])
+    assert np.linalg.norm(got[rows] - want[rows]) <= 2.0 ** -9 * np.linalg.norm(want[rows])
+    y32 = tq.tq_fp4_moe_forward(*args, fmt=w.fmt, w_scale=w.scale, y=torch.empty(n, N, device="cuda"))
+    tq.tq_device_error()
+    assert (np.abs(_f64(y32) - want) <= 2.0 ** -16 * size + 2.0 ** -22 * np.abs(want) + 1e-37).all()
+
+
+def test_not_finite_weights_stay_in_their_outputs():
+    """A NaN scale in one weight row: that output is NaN for the tokens of its expert, its neighbours are not."""
+    rng = np.random.default_rng(6)
+    n, E, k, K, N = 1500, 8, 3, 64, 1024
+    w = Weights(rng, E, N, K, "nv")
+    byte = np.zeros((E, N, K // 16), np.uint8) + 0x38
+    byte[2, 100, 1] = 0x7f
+    tiled = tq.tq_fp4_tile_scales(torch.from_numpy(byte).cuda(), tq.FP4_NV)
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(n)]).astype(np.int32)
+    y = tq.tq_fp4_moe_forward(_x(rng, n, K, "bf16").cuda(), w.packed, tiled, torch.from_numpy(ids).cuda(),
+                              torch.ones(n, k, device="cuda"))
+    bad = torch.isnan(y).cpu().numpy()
+    want = np.zeros((n, N), bool)
+    want[(ids == 2).any(1), 100] = True
+    assert np.array_equal(bad, want) and torch.isfinite(y[~torch.isnan(y)]).all()

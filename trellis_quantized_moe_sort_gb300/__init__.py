@@ -13,6 +13,7 @@ torch.float32 [n, top_k].
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 __all__ = [
@@ -878,6 +879,7 @@ def _output(y, shape, x):
     return y, _given(y, shape, (), "y"), _type_code(y.dtype, "y")
 
 
+@functools.lru_cache(maxsize=4096)
 def tq_fp4_linear_workspace_size(n: int, K: int, N: int, fmt: int = FP4_NV) -> int:
     return lib().tq_fp4_linear_workspace_size(n, K, N, fmt)
 
@@ -900,6 +902,7 @@ def tq_fp4_linear(x, packed, tiled_scales, fmt: int = FP4_NV, w_scale=None, x_sc
     return y
 
 
+@functools.lru_cache(maxsize=4096)
 def tq_fp4_moe_workspace_size(n: int, top_k: int, E: int, K: int, N: int, fmt: int = FP4_NV) -> int:
     return lib().tq_fp4_moe_workspace_size(n, top_k, E, K, N, fmt)
 
@@ -926,6 +929,7 @@ def tq_fp4_moe_forward(x, packed, tiled_scales, topk_ids, topk_w, fmt: int = FP4
     return y
 
 
+@functools.lru_cache(maxsize=4096)
 def tq_fp4_moe_mlp_workspace_size(n: int, top_k: int, E: int, H: int, I: int, fmt: int = FP4_NV) -> int:
     return lib().tq_fp4_moe_mlp_workspace_size(n, top_k, E, H, I, fmt)
 

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "tq_fp4.cuh"
 #include "tq_internal.h"
@@ -21,29 +22,74 @@ constexpr int64_t kMaxIndex = (static_cast<int64_t>(1) << 31) - 1024;
 // fit the 32-bit coordinates of the copies.
 bool bad_k(int K) { return K < 32 || K % 32 != 0; }
 
-// The smallest of 16, 32, 64, 128, 224 activation rows per m-tile that holds
-// the expected rows of a matrix, with room for the spread between experts.
-// 224 is the most of which tensor memory holds two accumulators (448 columns)
-// beside a step's scales (48): a unit's drain overlaps the next unit's steps.
-int tile_for(double rows) {
-  for (int t = 16; t < 224; t <<= 1) {
-    if (rows * 1.25 <= t) return t;
+// Rows per m-tile and K splits of a tensor-core product, by the time that the
+// kernel's parts take (cycles of an SM; the pair kernel's for two of them):
+//   a step of 256 values   the MMAs, 4 x T / 2 and a seventh more, the issue of
+//                          one step (360), or the step's bytes at 72 a clock
+//   a unit                 2500 beside its steps; its drain of 22 a column runs
+//                          beside the next unit's
+//   the launch             about 4000 until the first MMA
+//   weights                from memory at 3400 bytes a clock over the chip
+//   splits                 their partial sums written and read again at 3000
+//                          bytes a clock, and the combine's launch (5000),
+//                          which the experts' product has in any case
+// `rows` a matrix, `matrices` of them.  T is a multiple of 16 up to 224, the
+// most of which tensor memory holds two accumulators (448 columns) beside a
+// step's scales (48).  Experts take as few m-tiles as hold their rows: another
+// reads the matrix again.
+// Measured against m-tiles of a power of two or 224 and splits by the units
+// alone (us): linear 4096 -> 4096, 500 rows 22.3 -> 12.2; 4096 -> 2048, 1500 rows
+// 32.7 -> 15.6; 512 -> 256, 4000 rows 17.6 -> 10.3.
+struct Tiling {
+  int tile_m, splits;
+};
+Tiling choose_tiling(double rows, double matrices, int K, int N, int fmt, bool experts) {
+  const int steps = fp4_steps(K), blocks = (N + 127) / 128, sms = sm_count();
+  const double sf = fp4_scale_step_bytes(fmt);
+  const double weights = matrices * N * (K / 2.0 + K / fp4_block(fmt)) / 3400.0;
+  Tiling best{16, 1};
+  double best_cost = 1e300;
+  const int fewest = experts ? static_cast<int>(std::ceil(rows / 224.0)) : 0;   // m-tiles of a matrix
+  for (int T = 16; T <= 224; T += 16) {
+    if (experts && std::ceil(rows / T) > fewest) continue;
+    const bool pair = fp4_takes_pairs(T);
+    const double tiles = matrices * std::ceil(rows / T);
+    const double units = tiles * (pair ? (blocks + 1) / 2 : blocks);
+    const int slots = pair ? sms / 2 : sms;
+    const double bytes = 128.0 * 128 + sf + 128.0 * (pair ? T / 2 : T) + sf * ((T + 127) / 128);
+    const double step = std::max({360.0, 2.3 * T, bytes / 72.0});
+    for (int s = 1; s <= std::min(8, steps); ++s) {
+      const double unit = std::max(((steps + s - 1) / s) * step + 2500.0, 22.0 * T);
+      double cost = 4000.0 + std::max(std::ceil(units * s / slots) * unit, weights) + 22.0 * T;
+      if (s > 1 || experts) cost += 5000.0 + 8.0 * s * rows * matrices * N / 3000.0;
+      if (cost < best_cost * 0.99) {
+        best = {T, s};
+        best_cost = cost;
+      }
+    }
   }
-  return 224;
+  return best;
 }
-int moe_tile(int64_t n, int top_k, int E) { return n > 0 ? tile_for(tq_pairs_per_woken_expert(n, top_k, E)) : 16; }
-int linear_tile(int64_t n) { return tile_for(static_cast<double>(n) / 1.25); }
+// The rows that most experts stay below: their expectation and two standard
+// deviations of an even routing.
+Tiling moe_tiling(int64_t n, int top_k, int E, int K, int N, int fmt) {
+  if (n == 0) return {16, 1};
+  const double mean = tq_pairs_per_woken_expert(n, top_k, E);
+  return choose_tiling(mean + 2.0 * std::sqrt(mean), n * top_k / mean, K, N, fmt, true);
+}
 
 // Whether a product takes the one-launch GEMV, which reads a matrix once per
 // activation row, or the tensor-core chain (three or four launches), which
-// reads it once per m-tile.  Times in us in a CUDA graph, u = N K / (2048 x
-// 4096), measured at u = 1, n rows: GEMV 3.8, 5.6, 8.7, 15.8 at 1, 2, 4, 8 rows
-// of a linear and 10.4, 17.6, 29.3, 55.0 at 1, 2, 4, 8 tokens of top-6 of 256;
-// the chain 7.9, 7.7, 7.8, 7.9 and 21.9, 26.1, 35.1, 53.1.
+// reads it once per m-tile.  In us, fitted in CUDA graphs: the GEMV 2 and, per
+// row and 2048 weight rows, 0.85 (its blocks, each quantising the row) and 0.93
+// per 4096 values of each of top_k matrices; the chain 7 (linear) or 15 (experts)
+// and 0.75 per 2048 x 4096 matrix.  At 2048 x 4096 the GEMV took 3.8, 5.6, 8.7,
+// 15.8 for 1, 2, 4, 8 rows of a linear and 10.4, 17.6, 29.3, 55.0 for 1, 2, 4, 8
+// tokens of top-6 of 256, the chain 7.9, 7.7, 7.8, 7.9 and 21.9, 26.1, 35.1, 53.1.
 bool takes_gemv(int64_t n, int top_k, double matrices, double chain_us, int K, int N) {
   if (n > 64 || K > kFp4GemvMaxK) return false;
-  const double u = static_cast<double>(N) * K / (2048.0 * 4096.0);
-  return 2.0 + u * n * (0.65 + top_k) <= chain_us + 0.75 * u * matrices;
+  const double rows = N / 2048.0, values = K / 4096.0;
+  return 2.0 + n * rows * (0.85 + 0.93 * top_k * values) <= chain_us + 0.75 * rows * values * matrices;
 }
 bool linear_gemv(int64_t n, int K, int N) { return takes_gemv(n, 1, 1.0, 7.0, K, N); }
 bool moe_gemv(int64_t n, int top_k, int E, int K, int N) {
@@ -111,10 +157,11 @@ struct MoePlan {
 };
 MoePlan plan_moe(void* base, int64_t n, int top_k, int E, int K, int N, int fmt) {
   MoePlan m;
-  m.tile_m = moe_tile(n, top_k, E);
+  const Tiling tiling = moe_tiling(n, top_k, E, K, N, fmt);
+  m.tile_m = tiling.tile_m;
+  m.splits = tiling.splits;
   m.P = n * top_k;
   m.cap = std::max<int64_t>(1, tq_tile_map_capacity(n, top_k, E, m.tile_m));
-  m.splits = fp4_splits(m.cap, K, N);
   Carver c{static_cast<uint8_t*>(base)};
   m.routed = carve_routed(c, m.P, E, m.cap);
   m.staged = carve_staged(c, m.P, m.cap, m.tile_m, K, fmt);
@@ -132,9 +179,10 @@ struct LinearPlan {
 };
 LinearPlan plan_linear(void* base, int64_t n, int K, int N, int fmt) {
   LinearPlan l;
-  l.tile_m = linear_tile(n);
+  const Tiling tiling = choose_tiling(static_cast<double>(n), 1.0, K, N, fmt, false);
+  l.tile_m = tiling.tile_m;
+  l.splits = tiling.splits;
   l.tiles = std::max<int64_t>(1, (n + l.tile_m - 1) / l.tile_m);
-  l.splits = fp4_splits(l.tiles, K, N);
   Carver c{static_cast<uint8_t*>(base)};
   l.staged = carve_staged(c, n, l.tiles, l.tile_m, K, fmt);
   l.part = l.splits > 1 ? c.take<float>(static_cast<size_t>(l.splits) * n * N) : nullptr;
@@ -152,11 +200,13 @@ struct MlpPlan {
 };
 MlpPlan plan_mlp(void* base, int64_t n, int top_k, int E, int H, int I, int fmt) {
   MlpPlan m;
-  m.tile_m = moe_tile(n, top_k, E);
+  // one tile map for both products: the larger's rows, each its own splits
+  const Tiling gu = moe_tiling(n, top_k, E, H, 2 * I, fmt), down = moe_tiling(n, top_k, E, I, H, fmt);
+  m.tile_m = gu.tile_m;
+  m.splits_gu = gu.splits;
+  m.splits_down = down.splits;
   m.P = n * top_k;
   m.cap = std::max<int64_t>(1, tq_tile_map_capacity(n, top_k, E, m.tile_m));
-  m.splits_gu = fp4_splits(m.cap, H, 2 * I);
-  m.splits_down = fp4_splits(m.cap, I, H);
   Carver c{static_cast<uint8_t*>(base)};
   m.routed = carve_routed(c, m.P, E, m.cap);
   m.x = carve_staged(c, m.P, m.cap, m.tile_m, H, fmt);

@@ -600,26 +600,6 @@ static auto kernel_for(int fmt, bool pair) {
                           : (pair ? fp4_gemm_kernel<TQ_FP4_MX, true, TOut> : fp4_gemm_kernel<TQ_FP4_MX, false, TOut>);
 }
 
-// K splits of a product of at most `tiles` m-tiles: as many whole rounds of
-// the SMs as the units make, the count (up to 8, a step at least each) whose
-// last round wastes least; one when the units fill four rounds by themselves.
-int fp4_splits(int64_t tiles, int K, int N) {
-  const long long units = tiles * ((N + kRows - 1) / kRows);
-  const int sms = sm_count(), steps = fp4_steps(K);
-  if (units >= 4ll * sms) return 1;
-  int best = 1;
-  double best_cost = 1e30;
-  for (int s = 1; s <= std::min(8, steps); ++s) {
-    const long long rounds = (units * s + sms - 1) / sms;
-    const double cost = static_cast<double>(rounds) * ((steps + s - 1) / s + 1.0);   // a unit costs about a step more
-    if (cost < best_cost * 0.95) {
-      best = s;
-      best_cost = cost;
-    }
-  }
-  return best;
-}
-
 int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s) {
   GemmParams p{};
   p.sorted_pairs = g.sorted_pairs;
@@ -645,11 +625,7 @@ int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s) {
 
   const int sf_step = fp4_scale_step_bytes(g.fmt);
   const int x_groups = (p.n_max + 127) / 128;
-  // Pairs of CTAs (two SMs sharing one MMA of 256 weight rows, each holding half
-  // of the activation rows) from 128 rows per m-tile on: a CTA then takes in 36
-  // KB a step for 128 x 224 results in place of 51, and that intake, about 50
-  // bytes a clock, is what bounds large products.
-  const bool pair = p.n_max >= 128;
+  const bool pair = fp4_takes_pairs(g.tile_m);
   p.x_bytes = (pair ? p.n_max / 2 : p.n_max) * kRowBytes;
   p.x_sf_bytes = x_groups * sf_step;
   p.stage_bytes = kWBytes + p.x_bytes + sf_step + p.x_sf_bytes;

@@ -210,7 +210,12 @@ struct Fp4Gemv {
 };
 constexpr int kFp4GemvMaxK = 16384;   // x in shared memory, 2.25 bytes a value
 int launch_fp4_gemv(const Fp4Gemv& g, cudaStream_t s);
-int fp4_splits(int64_t tiles, int K, int N);
+// Pairs of CTAs (two SMs sharing one MMA of 256 weight rows, each holding half
+// of the activation rows) from 128 rows per m-tile on: a CTA then takes in 36 KB
+// a step for 128 x 224 results in place of 51 (experts, 8192 tokens: 460 -> 424
+// us).  At 64 rows the pairs are no faster, and their second CTA idles where
+// there are few weight rows.
+inline bool fp4_takes_pairs(int tile_m) { return tile_m >= 128; }
 int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s);
 
 // TQ_FORCE_ARM (auto|gemv|grouped|measured) applied to an automatic pin.
