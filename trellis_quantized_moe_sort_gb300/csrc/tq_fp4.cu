@@ -33,9 +33,9 @@ bool bad_k(int K) { return K < 32 || K % 32 != 0; }
 //   splits                 their partial sums written and read again at 3000
 //                          bytes a clock, and the combine's launch (5000),
 //                          which the experts' product has in any case
-// `rows` a matrix, `matrices` of them.  T is a multiple of 16 up to 224, the
-// most of which tensor memory holds two accumulators (448 columns) beside a
-// step's scales (48).  Experts take as few m-tiles as hold their rows: another
+// `rows` a matrix, `matrices` of them.  T is a multiple of 16 up to the most of
+// which tensor memory holds two accumulators beside a step's scales: 224 (NV, 48
+// columns of scales) or 240 (MX, 24).  Experts take as few m-tiles as hold their rows: another
 // reads the matrix again.
 // Measured against m-tiles of a power of two or 224 and splits by the units
 // alone (us): linear 4096 -> 4096, 500 rows 22.3 -> 12.2; 4096 -> 2048, 1500 rows
@@ -43,14 +43,15 @@ bool bad_k(int K) { return K < 32 || K % 32 != 0; }
 struct Tiling {
   int tile_m, splits;
 };
-Tiling choose_tiling(double rows, double matrices, int K, int N, int fmt, bool experts) {
+Tiling search_tiling(double rows, double matrices, int K, int N, int fmt, bool experts) {
   const int steps = fp4_steps(K), blocks = (N + 127) / 128, sms = sm_count();
   const double sf = fp4_scale_step_bytes(fmt);
   const double weights = matrices * N * (K / 2.0 + K / fp4_block(fmt)) / 3400.0;
   Tiling best{16, 1};
   double best_cost = 1e300;
-  const int fewest = experts ? static_cast<int>(std::ceil(rows / 224.0)) : 0;   // m-tiles of a matrix
-  for (int T = 16; T <= 224; T += 16) {
+  const int most = (512 - fp4_scale_columns(fmt)) / 2 / 16 * 16;
+  const int fewest = experts ? static_cast<int>(std::ceil(rows / most)) : 0;   // m-tiles of a matrix
+  for (int T = 16; T <= most; T += 16) {
     if (experts && std::ceil(rows / T) > fewest) continue;
     const bool pair = fp4_takes_pairs(T);
     const double tiles = matrices * std::ceil(rows / T);
@@ -69,6 +70,25 @@ Tiling choose_tiling(double rows, double matrices, int K, int N, int fmt, bool e
     }
   }
   return best;
+}
+// The search takes about 2 us, so a thread keeps the answers of the sizes it has
+// met last (a pure function of them and of the device's SM count).
+Tiling choose_tiling(double rows, double matrices, int K, int N, int fmt, bool experts) {
+  struct Entry {
+    double rows, matrices;
+    int K, N, fmt, experts, sms;
+    Tiling tiling;
+  };
+  constexpr int kEntries = 64;
+  static thread_local Entry kept[kEntries];
+  const int sms = sm_count();
+  const uint64_t mix = (static_cast<uint64_t>(rows * 16.0) * 0x9E3779B97F4A7C15ull) ^
+                       (static_cast<uint64_t>(K) * 0xC2B2AE3D27D4EB4Full) ^ (static_cast<uint64_t>(N) * 0x165667B19E3779F9ull);
+  Entry& e = kept[(mix >> 40) % kEntries];
+  if (!(e.sms == sms && e.rows == rows && e.matrices == matrices && e.K == K && e.N == N && e.fmt == fmt &&
+        e.experts == experts))
+    e = {rows, matrices, K, N, fmt, experts, sms, search_tiling(rows, matrices, K, N, fmt, experts)};
+  return e.tiling;
 }
 // The rows that most experts stay below: their expectation and two standard
 // deviations of an even routing.

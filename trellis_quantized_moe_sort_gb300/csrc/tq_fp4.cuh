@@ -23,6 +23,9 @@ __host__ __device__ constexpr int fp4_block(int fmt) { return fmt == TQ_FP4_NV ?
 // (row / 32) * 4 + block % 4 -- what one 32 x 128-bit copy into tensor memory
 // takes and the block-scaled MMA reads.
 __host__ __device__ constexpr int fp4_scale_step_bytes(int fmt) { return 128 * (kFp4Step / fp4_block(fmt)); }
+// Tensor-memory columns of a step's scales: 4 a tile for the weights, 8 for up
+// to 256 activation rows.
+__host__ __device__ constexpr int fp4_scale_columns(int fmt) { return fp4_scale_step_bytes(fmt) / 512 * 12; }
 __host__ __device__ constexpr int fp4_steps(int K) { return (K + kFp4Step - 1) / kFp4Step; }
 
 // Offset of block `b`'s scale of row `r` inside a tiled scale matrix of

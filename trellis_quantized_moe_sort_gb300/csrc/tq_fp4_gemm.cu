@@ -21,6 +21,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include "tq_fp4.cuh"
@@ -594,10 +595,31 @@ bool encode_bytes(CUtensorMap* m, const uint8_t* bytes, int64_t rows, int row_by
 
 }  // namespace
 
+using GemmKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, GemmParams);
+
+// The kernel of an output type, allowed its shared memory on the current device
+// (once for each; nullptr where that fails).
 template <typename TOut>
-static auto kernel_for(int fmt, bool pair) {
-  return fmt == TQ_FP4_NV ? (pair ? fp4_gemm_kernel<TQ_FP4_NV, true, TOut> : fp4_gemm_kernel<TQ_FP4_NV, false, TOut>)
-                          : (pair ? fp4_gemm_kernel<TQ_FP4_MX, true, TOut> : fp4_gemm_kernel<TQ_FP4_MX, false, TOut>);
+static GemmKernel kernel_for(int fmt, bool pair) {
+  static std::atomic<uint64_t> allowed[4];   // bit d: device d
+  GemmKernel const kernel =
+      fmt == TQ_FP4_NV ? (pair ? fp4_gemm_kernel<TQ_FP4_NV, true, TOut> : fp4_gemm_kernel<TQ_FP4_NV, false, TOut>)
+                       : (pair ? fp4_gemm_kernel<TQ_FP4_MX, true, TOut> : fp4_gemm_kernel<TQ_FP4_MX, false, TOut>);
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  std::atomic<uint64_t>& done = allowed[2 * (fmt == TQ_FP4_NV) + pair];
+  const uint64_t bit = 1ull << (device & 63);
+  if (!(done.load() & bit)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    done.fetch_or(bit);
+  }
+  return kernel;
 }
 
 int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s) {
@@ -638,7 +660,7 @@ int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s) {
 
   // Tensor memory: accumulators, then the scales of one step (4 columns per
   // scale tile of the weights, 8 of the activations).
-  const int sf_cols = (sf_step / 512) * 12;
+  const int sf_cols = fp4_scale_columns(g.fmt);
   p.acc_cols = p.n_max;
   p.accs = std::min(kMaxAcc, (512 - sf_cols) / p.acc_cols);
   p.sf_col = p.accs * p.acc_cols;
@@ -654,13 +676,10 @@ int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s) {
       !encode_bytes(&tm_xs, g.x_scales, x_tiles * p.steps * sf_rows, 128, sf_rows, false))
     return TQ_ERR_INVALID_ARG;
   const int type = g.y ? g.y_type : TQ_FP32;
-  auto kernel = type == TQ_FP32   ? kernel_for<float>(g.fmt, pair)
-                : type == TQ_BF16 ? kernel_for<__nv_bfloat16>(g.fmt, pair)
-                                  : kernel_for<__half>(g.fmt, pair);
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess) {
-    cudaGetLastError();
-    return TQ_ERR_CUDA;
-  }
+  const GemmKernel kernel = type == TQ_FP32   ? kernel_for<float>(g.fmt, pair)
+                            : type == TQ_BF16 ? kernel_for<__nv_bfloat16>(g.fmt, pair)
+                                              : kernel_for<__half>(g.fmt, pair);
+  if (!kernel) return TQ_ERR_CUDA;
   const long long units = g.cap * (pair ? (p.row_blocks + 1) / 2 : p.row_blocks) * p.splits;
   const int width = pair ? 2 : 1;
   const int grid = width * static_cast<int>(std::max<long long>(1, std::min<long long>(units, sm_count() / width)));
