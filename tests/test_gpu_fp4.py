@@ -414,3 +414,54 @@ def test_not_finite_weights_stay_in_their_outputs():
     want = np.zeros((n, N), bool)
     want[(ids == 2).any(1), 100] = True
     assert np.array_equal(bad, want) and torch.isfinite(y[~torch.isnan(y)]).all()
+
+
+def test_weights_past_four_gigabytes():
+    """Experts whose codes start past 2^32 bytes, on both arms."""
+    E, N, K = 600, 4096, 4096
+    g = torch.Generator(device="cuda").manual_seed(3)
+    packed = torch.randint(0, 256, (E, N, K // 2), dtype=torch.uint8, device="cuda", generator=g)
+    scales = torch.randint(0x28, 0x40, (E, N, K // 16), dtype=torch.uint8, device="cuda", generator=g)
+    tiled = tq.tq_fp4_tile_scales(scales)
+    x = torch.randn(70, K, device="cuda", generator=g).bfloat16()
+    xq = tq.tq_fp4_dequantize(*tq.tq_fp4_quantize(x)).double()
+    used = [0, 300, 599]
+    values = {e: tq.tq_fp4_dequantize(packed[e], scales[e]).double() for e in used}
+    before = tq.tq_launch_counts_all()
+    for n in (2, 70):
+        ids = torch.tensor(used, dtype=torch.int32, device="cuda").repeat(n, 1)
+        w = torch.rand(n, 3, device="cuda", generator=g)
+        y = tq.tq_fp4_moe_forward(x[:n], packed, tiled, ids, w, y=torch.empty(n, N, device="cuda"))
+        check_no_device_error()
+        want = sum(w[:, j, None].double() * (xq[:n] @ values[e].t()) for j, e in enumerate(used))
+        size = sum(w[:, j, None].double() * (xq[:n].abs() @ values[e].abs().t()) for j, e in enumerate(used))
+        assert bool(((y.double() - want).abs() <= 2.0 ** -16 * size).all())
+    after = tq.tq_launch_counts_all()
+    assert after["fp4_gemv"] == before["fp4_gemv"] + 1 and after["fp4_gemm"] == before["fp4_gemm"] + 1
+
+
+def test_outputs_past_two_to_the_32():
+    """More than 2^32 results, and more than 2^32 partial sums of pairs."""
+    K, N = 32, 8192
+    rng = np.random.default_rng(1)
+    w = Weights(rng, 4, N, K, "mx")
+    values = torch.from_numpy(w.values).cuda()
+    n = 530_000
+    x = torch.randn(n, K, device="cuda").bfloat16()
+    xq = tq.tq_fp4_dequantize(*tq.tq_fp4_quantize(x, tq.FP4_MX), tq.FP4_MX).double()
+    rows = torch.tensor([0, 1, 262_143, 262_144, 400_001, n - 1], device="cuda")
+    y = tq.tq_fp4_linear(x, w.packed[1], w.tiled[w.tiled.numel() // 4: w.tiled.numel() // 2], fmt=tq.FP4_MX)
+    check_no_device_error()
+    want, size = xq[rows] @ values[1].t(), xq[rows].abs() @ values[1].abs().t()
+    assert bool(((y[rows].double() - want).abs() <= 2.0 ** -16 * size + 2.0 ** -8 * want.abs()).all())
+    del y
+    n, k = 180_000, 3
+    ids = torch.stack([torch.randperm(4, device="cuda")[:k] for _ in range(64)]).int().repeat(n // 64 + 1, 1)[:n].contiguous()
+    tw = torch.rand(n, k, device="cuda")
+    y = tq.tq_fp4_moe_forward(x[:n], w.packed, w.tiled, ids, tw, fmt=tq.FP4_MX)
+    check_no_device_error()
+    for t in (0, 100_003, 174_762, 174_763, n - 1):
+        e = ids[t].long()
+        want = (tw[t, :, None].double() * (values[e] @ xq[t])).sum(0)
+        size = (tw[t, :, None].double() * (values[e].abs() @ xq[t].abs())).sum(0)
+        assert bool(((y[t].double() - want).abs() <= 2.0 ** -16 * size + 2.0 ** -8 * want.abs()).all())
