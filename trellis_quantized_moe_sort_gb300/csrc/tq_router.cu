@@ -14,8 +14,12 @@
 // apart; a group's value is one addition.  The result depends on the token's
 // row alone, not on the batch or the launch.
 //
-// Bound: 8192 x 256 fp32 logits are 8.4 MB, 1.3 us of HBM time, so the forward
-// is bound by the top_k dependent rounds of the arg-max and by the launch.
+// Bound: 8192 x 256 fp32 logits are 8.4 MB, 1.3 us of HBM time, so both
+// directions are bound by the issue of a row's instructions (eight exponentials
+// and reciprocals a lane, then the rounds of the choice) and by the launch:
+// 10.6 us forward (top-6 of 256 in 8 groups, biased sigmoid), 6.9 us backward
+// (softmax).  One row per warp, no more registers than let 36 warps live on an
+// SM; 40 or 48 warps (fewer registers) took 0.2 and 0.5 us more.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -178,12 +182,58 @@ __device__ __forceinline__ bool choose_lane_groups(const float (&c)[PL], int gro
   for (int i = 0; i < top_groups; ++i) {
     const uint32_t best = __reduce_max_sync(kAll, key);
     const int first = __ffs(__ballot_sync(kAll, key == best)) - 1;   // the lowest group that has it
-    if (lane / lanes == first / lanes) {
+    if ((lane ^ first) < lanes) {   // of the same group
       stays = true;
       key = 0u;
     }
   }
   return stays;
+}
+
+// The top_k largest keys, by rounds over at most 32 of them, one per lane: those
+// that are no smaller than the top_k-th largest of the lanes' maxima, which at
+// least top_k keys are.  Lane j gets the j-th of the order (the lower expert
+// first where keys tie).  False, with nothing chosen, where more keys are left
+// (ties, or a choice confined to a few lanes by its groups).  At 8192 rows of 256
+// a round over the lanes' whole pieces costs 0.65 us, one of these 0.18 and their
+// gathering 0.6: 10.9 -> 9.4 us for top-6, 14.9 -> 10.3 for top-12, 7.7 -> 8.5 for
+// top-1, so one or two experts are taken from the whole pieces.
+template <int PL>
+__device__ __forceinline__ bool choose_from_few(const uint32_t (&key)[PL], int top_k, int lane, uint2* few, int* e,
+                                                uint32_t* k) {
+  uint32_t head = key[0];
+#pragma unroll
+  for (int i = 1; i < PL; ++i) head = max(head, key[i]);
+  uint32_t least = 0;
+  for (int j = 0; j < top_k; ++j) {
+    least = __reduce_max_sync(kAll, head);
+    if (head == least) head = 0u;
+  }
+  if (least <= kKeyMasked) return false;
+  const unsigned below = (1u << lane) - 1u;
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < PL; ++i) {
+    const bool in = key[i] >= least;
+    const unsigned all = __ballot_sync(kAll, in);
+    const int at = count + __popc(all & below);
+    if (in && at < 32) few[at] = make_uint2(key[i], lane * PL + i);
+    count += __popc(all);
+  }
+  __syncwarp();
+  if (count > 32) return false;
+  uint2 mine = lane < count ? few[lane] : make_uint2(0u, 0u);
+  __syncwarp();   // read before the next row's are written
+  for (int j = 0; j < top_k; ++j) {
+    const uint32_t best = __reduce_max_sync(kAll, mine.x);
+    const uint32_t which = __reduce_min_sync(kAll, mine.x == best ? mine.y : 0xffffffffu);
+    if (mine.x == best && mine.y == which) mine.x = 0u;
+    if (lane == j) {
+      *e = static_cast<int>(which);
+      *k = best;
+    }
+  }
+  return true;
 }
 
 template <typename T, int PL>
@@ -192,6 +242,7 @@ router_scored_kernel(const T* __restrict__ logits, long long stride, const float
                      int top_k, int score, int groups, int top_groups, int lane_groups, int group_lanes, int renorm,
                      float scale, bool vec, int32_t* __restrict__ ids, float* __restrict__ w) {
   extern __shared__ float rows[];   // [warps][E], with groups only
+  __shared__ uint2 few[kRouterWarps][32];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -251,7 +302,9 @@ router_scored_kernel(const T* __restrict__ logits, long long stride, const float
     for (int i = 0; i < PL; ++i) key[i] = e0 + i < E ? order_key(x[i]) : 0u;
     int mine_e = 0;
     uint32_t mine_key = 0;
-    for (int j = 0; j < top_k; ++j) {
+    bool chosen = false;
+    if constexpr (PL >= 4) chosen = top_k > 2 && choose_from_few<PL>(key, top_k, lane, few[warp], &mine_e, &mine_key);
+    for (int j = 0; j < top_k && !chosen; ++j) {
       // largest key of the lane, by a tree; then of the warp; the lowest lane
       // that has it, and its lowest expert
       uint32_t m[PL];
@@ -386,7 +439,7 @@ int run_forward(const RouterArgs& a, const T* logits, int32_t* ids, float* w, cu
   int lanes = 32;
   while (lanes * a.groups > 32) lanes >>= 1;
   // groups of a power of two of whole lanes are chosen from registers (8192 x
-  // 256 in 8 groups: 15.0 -> 11.9 us), others through shared memory
+  // 256 in 8 groups: 15.0 -> 11.9 us when it came in), others through shared memory
   const int size = a.E / a.groups, whole = size % PL == 0 ? size / PL : 0;
   const int lane_groups = a.groups > 1 && whole > 0 && (whole & (whole - 1)) == 0 ? whole : 0;
   const size_t smem = a.groups > 1 && !lane_groups ? sizeof(float) * kRouterWarps * a.E : 0;
