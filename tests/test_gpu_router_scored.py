@@ -71,6 +71,18 @@ def test_ties_go_to_the_lower_index(score, groups, top_groups):
     _check_forward(logits, 6, score, np.full(64, -1.0, np.float32), groups, top_groups)
 
 
+@pytest.mark.parametrize("E,k,groups,top_groups", [
+    (65, 3, 1, 1), (128, 32, 1, 1), (256, 8, 1, 1), (256, 12, 8, 1), (256, 3, 8, 1), (480, 7, 6, 2), (1024, 32, 1, 1)])
+@pytest.mark.parametrize("values", [1, 2, 12, 400])
+def test_many_equal_candidates(E, k, groups, top_groups, values):
+    """From every expert equal (more candidates than a warp has lanes) to a few ties; some rows mostly masked."""
+    rng = np.random.default_rng([E, k, values])
+    x = rng.integers(0, values, (70, E)).astype(np.float32) / 64
+    x[60:][rng.random((10, E)) < 0.97] = -np.inf
+    _check_forward(torch.from_numpy(x), k, "sigmoid", None, groups, top_groups, most_unclear=0.05)
+    _check_forward(torch.from_numpy(x), k, "softmax", None, groups, top_groups, most_unclear=0.05)
+
+
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("groups,top_groups", [(1, 1), (4, 2)])
 def test_masked_and_empty_rows(score, groups, top_groups):
