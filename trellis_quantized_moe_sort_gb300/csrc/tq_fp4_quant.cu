@@ -149,29 +149,40 @@ fp4_tile_scales_kernel(const uint8_t* __restrict__ scales, int E, int N, int kb,
   }
 }
 
-// Row `slot` of the staged activations: its m-tile and its row there.
+// Where a pair's staged row goes: byte offsets of its codes and of its first
+// scale in the tiled layout of its m-tile; codes -1 for a pair without a place
+// (an expert out of range).
 struct Place {
-  int slot, tile, row;
+  long long codes, scales;
 };
 
-// The place of a pair; slot -1 (an expert out of range) has none.
-__device__ __forceinline__ Place place_of(const Fp4Slots& s, long long pair, int tile_m) {
-  if (!s.slot_of) return {static_cast<int>(pair), static_cast<int>(pair / tile_m), static_cast<int>(pair % tile_m)};
-  const int slot = __ldg(s.slot_of + pair), e = __ldg(s.ids + pair);
-  if (slot < 0) return {-1, 0, 0};
-  const int rank = slot - __ldg(s.offsets + e);
-  return {slot, __ldg(s.tile_first + e) + rank / tile_m, rank % tile_m};
+template <int kFmt>
+__device__ __forceinline__ Place place_of(const Fp4Slots& s, long long pair, int tile_m, int K) {
+  long long slot = pair, tile, row;
+  if (s.slot_of) {
+    const int e = __ldg(s.ids + pair);
+    slot = __ldg(s.slot_of + pair);
+    if (slot < 0) return {-1, 0};
+    const int rank = static_cast<int>(slot) - __ldg(s.offsets + e);
+    tile = __ldg(s.tile_first + e) + rank / tile_m;
+    row = rank % tile_m;
+  } else {
+    tile = pair / tile_m;
+    row = pair % tile_m;
+  }
+  const int steps = fp4_steps(K);
+  const long long tile_bytes = static_cast<long long>((tile_m + 127) / 128) * steps * fp4_scale_step_bytes(kFmt);
+  return {slot * (K / 2), tile * tile_bytes + static_cast<long long>(fp4_tiled_offset(kFmt, steps, row, 0))};
 }
 
 // One block's share of a staged row: 16 values per thread and their largest
-// magnitude from load(item, v), their codes into the row's slots and their scales into the tiled layout of
-// each slot's m-tile (blocks past K zero, so that the MMA's last step
-// multiplies zeros by a finite scale).
+// magnitude from load(item, v), their codes and scales to each of the row's places
+// (blocks past K zero, so that the MMA's last step multiplies zeros by a finite
+// scale).
 template <int kFmt, typename Load>
-__device__ __forceinline__ void stage_row(int K, const GlobalScale& g, const Place* places, int count, int tile_m,
+__device__ __forceinline__ void stage_row(int K, const GlobalScale& g, const Place* places, int count,
                                           uint8_t* __restrict__ xq, uint8_t* __restrict__ xs, Load&& load) {
   const int steps = fp4_steps(K);
-  const size_t tile_bytes = static_cast<size_t>((tile_m + 127) / 128) * steps * fp4_scale_step_bytes(kFmt);
   const int items = K / 16, all = steps * (kFp4Step / 16);
   const int lane = threadIdx.x & 31;
   // whole warps stay in the loop together: all is a multiple of 16, a warp may end half empty
@@ -195,12 +206,14 @@ __device__ __forceinline__ void stage_row(int K, const GlobalScale& g, const Pla
              __shfl_sync(kAll, byte, word_lane + 4) << 16 | __shfl_sync(kAll, byte, word_lane + 6) << 24;
     }
     const int block = kFmt == TQ_FP4_NV ? item : item / 2;
+    uint8_t* const codes = xq + 8 * item;
+    uint8_t* const scales = xs + fp4_tiled_offset(kFmt, steps, 0, block);
+    const bool writes_scales = item < all && lane == word_lane;
     for (int j = 0; j < count; ++j) {
       const Place p = places[j];
-      if (p.slot < 0) continue;
-      if (item < items) *reinterpret_cast<uint2*>(xq + static_cast<size_t>(p.slot) * (K / 2) + 8 * item) = q;
-      if (item < all && lane == word_lane)
-        *reinterpret_cast<uint32_t*>(xs + p.tile * tile_bytes + fp4_tiled_offset(kFmt, steps, p.row, block)) = word;
+      if (p.codes < 0) continue;
+      if (item < items) *reinterpret_cast<uint2*>(codes + p.codes) = q;
+      if (writes_scales) *reinterpret_cast<uint32_t*>(scales + p.scales) = word;
     }
   }
 }
@@ -220,9 +233,10 @@ fp4_stage_kernel(const T* __restrict__ x, long long stride, int K, const float* 
   Piece<T> first = {};
   if (static_cast<int>(threadIdx.x) < K / 16) first = load_piece(x + row * stride + 16 * threadIdx.x);
   const GlobalScale g(scale);
-  if (static_cast<int>(threadIdx.x) < top_k) places[threadIdx.x] = place_of(slots, row * top_k + threadIdx.x, tile_m);
+  if (static_cast<int>(threadIdx.x) < top_k)
+    places[threadIdx.x] = place_of<kFmt>(slots, row * top_k + threadIdx.x, tile_m, K);
   __syncthreads();
-  stage_row<kFmt>(K, g, places, top_k, tile_m, xq, xs, [&](int item, float (&v)[16]) {
+  stage_row<kFmt>(K, g, places, top_k, xq, xs, [&](int item, float (&v)[16]) {
     return open_piece(item == static_cast<int>(threadIdx.x) ? first : load_piece(x + row * stride + 16 * item), v);
   });
 }
@@ -239,13 +253,13 @@ fp4_stage_swiglu_kernel(const float* __restrict__ part, long long split_stride, 
   pdl_wait();
   pdl_trigger();
   const long long pair = blockIdx.x;
-  if (threadIdx.x == 0) place = place_of(slots, pair, tile_m);
+  if (threadIdx.x == 0) place = place_of<kFmt>(slots, pair, tile_m, I);
   __syncthreads();
   const int e = __ldg(slots.ids + pair);
-  if (place.slot < 0 || e < 0 || e >= E) return;   // a pair without a slot has no gate and up either
+  if (place.codes < 0 || e < 0 || e >= E) return;   // a pair without a slot has no gate and up either
   const float alpha = (x_scale ? *x_scale : 1.f) * (w_scale ? __ldg(w_scale + e) : 1.f);
   const float* const row = part + pair * 2 * I;
-  stage_row<kFmt>(I, GlobalScale(h_scale), &place, 1, tile_m, hq, hs, [&](int item, float (&v)[16]) {
+  stage_row<kFmt>(I, GlobalScale(h_scale), &place, 1, hq, hs, [&](int item, float (&v)[16]) {
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
