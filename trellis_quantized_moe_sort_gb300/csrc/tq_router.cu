@@ -18,8 +18,8 @@
 // directions are bound by the issue of a row's instructions (eight exponentials
 // and reciprocals a lane, then the rounds of the choice) and by the launch:
 // 10.6 us forward (top-6 of 256 in 8 groups, biased sigmoid), 6.9 us backward
-// (softmax).  One row per warp, no more registers than let 36 warps live on an
-// SM; 40 or 48 warps (fewer registers) took 0.2 and 0.5 us more.
+// (softmax).  One row per warp, 64 registers, so 32 warps live on an SM; held to
+// 48 or 40 registers it took 0.2 and 0.6 us more.
 #include <cuda_runtime.h>
 
 #include <algorithm>
