@@ -284,6 +284,44 @@ def test_results_repeat_on_streams_and_in_graphs(n):
         assert all(torch.equal(p, q) for p, q in zip(got, want))
 
 
+def test_a_given_stream_owns_the_memory(monkeypatch):
+    """Everything that a call allocates comes from the stream that it runs on, so
+    that no other stream's work can be given it before the call has run."""
+    rng = np.random.default_rng(4)
+    w = Weights(rng, 4, 128, 256, "nv")
+    x = _x(rng, 40, 256, "bf16").cuda()
+    ids = torch.from_numpy(rng.integers(0, 4, (40, 2)).astype(np.int32)).cuda()
+    weights = torch.rand(40, 2, device="cuda")
+    logits = torch.randn(40, 64, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    seen, empty = [], torch.empty
+
+    def record(*args, **kwargs):
+        seen.append(torch.cuda.current_stream())
+        return empty(*args, **kwargs)
+
+    def all_calls(stream):
+        moe = tq.tq_fp4_moe_forward(x, w.packed, w.tiled, ids, weights, w_scale=w.scale, stream=stream)
+        picks = tq.tq_router_scored(logits, 2, stream=stream)
+        grad = tq.tq_router_scored_backward(logits, *picks, weights, stream=stream)
+        packed, scales = tq.tq_fp4_quantize(x, stream=stream)
+        tiled = tq.tq_fp4_tile_scales(scales, stream=stream)
+        linear = tq.tq_fp4_linear(x, packed, tiled, stream=stream)
+        return moe, *picks, grad, packed, scales, tiled, linear, tq.tq_fp4_dequantize(packed, scales, stream=stream)
+
+    want = all_calls(None)
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch, "empty", record)
+    got = all_calls(side)
+    monkeypatch.undo()
+    side.synchronize()
+    check_no_device_error()
+    assert len(seen) >= len(got) and all(s == side for s in seen)
+    assert torch.cuda.current_stream() != side
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_both_arms_of_a_linear_agree():
     """A row alone (one launch) and among others (tensor cores): the same values to fp32 rounding."""
     rng = np.random.default_rng(77)

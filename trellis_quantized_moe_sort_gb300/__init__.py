@@ -722,6 +722,17 @@ def _scale_ptr(t, count, name):
     return ptr
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor in the memory of the stream that the call runs on: memory of
+    another stream's may still be in use there, or be given away there before
+    the call has run."""
+    torch = _types()[0]
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def tq_router_scored(logits, top_k: int, score: int = SCORE_SIGMOID, bias=None, groups: int = 1, top_groups: int = 1,
                      renormalize: bool = True, scale: float = 1.0, topk_ids=None, topk_w=None, stream=None):
     """Top-k experts by score + bias within the best groups -> (topk_ids int32 [n, top_k], topk_w fp32 [n, top_k]).
@@ -735,12 +746,12 @@ def tq_router_scored(logits, top_k: int, score: int = SCORE_SIGMOID, bias=None, 
     torch, fp32, int32, _ = _types()
     ptr, code, step, n, E = _rows(logits, "logits")
     if topk_ids is None:
-        topk_ids = torch.empty((n, top_k), dtype=torch.int32, device=logits.device)
+        topk_ids = _empty((n, top_k), torch.int32, logits.device, stream)
         ids_ptr = topk_ids.data_ptr()
     else:
         ids_ptr = _given(topk_ids, (n, top_k), int32, "topk_ids")
     if topk_w is None:
-        topk_w = torch.empty((n, top_k), dtype=torch.float32, device=logits.device)
+        topk_w = _empty((n, top_k), torch.float32, logits.device, stream)
         w_ptr = topk_w.data_ptr()
     else:
         w_ptr = _given(topk_w, (n, top_k), fp32, "topk_w")
@@ -760,7 +771,7 @@ def tq_router_scored_backward(logits, topk_ids, topk_w, grad_w, score: int = SCO
     ptr, code, step, n, E = _rows(logits, "logits")
     shape = (n, topk_ids.shape[1])
     if grad_logits is None:
-        grad_logits = torch.empty((n, E), dtype=logits.dtype, device=logits.device)
+        grad_logits = _empty((n, E), logits.dtype, logits.device, stream)
         out = grad_logits.data_ptr()
     else:
         out = _given(grad_logits, (n, E), (logits.dtype,), "grad_logits")
@@ -788,12 +799,12 @@ def tq_fp4_quantize(x, fmt: int = FP4_NV, global_scale=None, packed=None, scales
     ptr, code, step, n, K = _rows(x, "x")
     kb = K // _fp4_block(fmt)
     if packed is None:
-        packed = torch.empty((n, K // 2), dtype=torch.uint8, device=x.device)
+        packed = _empty((n, K // 2), torch.uint8, x.device, stream)
         p_ptr = packed.data_ptr()
     else:
         p_ptr = _given(packed, (n, K // 2), uint8, "packed")
     if scales is None:
-        scales = torch.empty((n, kb), dtype=torch.uint8, device=x.device)
+        scales = _empty((n, kb), torch.uint8, x.device, stream)
         s_ptr = scales.data_ptr()
     else:
         s_ptr = _given(scales, (n, kb), uint8, "scales")
@@ -815,7 +826,7 @@ def tq_fp4_dequantize(packed, scales, fmt: int = FP4_NV, global_scale=None, dtyp
         raise ValueError("scales do not match packed")
     shape = (*packed.shape[:-1], K)
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32 if dtype is None else dtype, device=packed.device)
+        out = _empty(shape, torch.float32 if dtype is None else dtype, packed.device, stream)
         o_ptr = out.data_ptr()
     else:
         if dtype is not None and out.dtype != dtype:
@@ -839,7 +850,7 @@ def tq_fp4_tile_scales(scales, fmt: int = FP4_NV, tiled=None, stream=None):
     E, N, kb = scales.shape if scales.dim() == 3 else (1, *scales.shape)
     K = kb * _fp4_block(fmt)
     size = tq_fp4_tiled_scales_size(E, N, K, fmt)
-    tiled = torch.empty(size, dtype=torch.uint8, device=scales.device) if tiled is None else tiled
+    tiled = _empty(size, torch.uint8, scales.device, stream) if tiled is None else tiled
     if tiled.numel() != size:
         raise ValueError(f"tiled has {tiled.numel()} bytes, expected {size}")
     _check(lib().tq_fp4_tile_scales(_dev_ptr(scales, (torch.uint8,), "scales"), E, N, K, fmt,
@@ -857,7 +868,7 @@ def _fp4_matrix(packed, tiled_scales, E, N, K, fmt, name):
     return _dev_ptr(packed, uint8, name), _dev_ptr(tiled_scales, uint8, "tiled scales")
 
 
-def _workspace(workspace, size, device, *args):
+def _workspace(workspace, size, device, stream, *args):
     """(address, bytes) of the caller's workspace, or of a new one of
     size(*args) bytes (none where the call needs none), and the tensor, to be
     kept until the call is enqueued."""
@@ -866,15 +877,15 @@ def _workspace(workspace, size, device, *args):
         need = size(*args)
         if need <= 256:
             return None, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = _empty(need, torch.uint8, device, stream)
         return workspace.data_ptr(), need, workspace
     return _dev_ptr(workspace, uint8, "workspace"), workspace.numel(), workspace
 
 
-def _output(y, shape, x):
+def _output(y, shape, x, stream):
     """(y, address, type code): the caller's, or a new one in x's dtype."""
     if y is None:
-        y = _types()[0].empty(shape, dtype=x.dtype, device=x.device)
+        y = _empty(shape, x.dtype, x.device, stream)
         return y, y.data_ptr(), _type_code(y.dtype, "y")
     return y, _given(y, shape, (), "y"), _type_code(y.dtype, "y")
 
@@ -892,8 +903,8 @@ def tq_fp4_linear(x, packed, tiled_scales, fmt: int = FP4_NV, w_scale=None, x_sc
     ptr, code, step, n, K = _rows(x, "x")
     N = packed.shape[-2]
     w_ptr, s_ptr = _fp4_matrix(packed, tiled_scales, 1, N, K, fmt, "packed")
-    ws_ptr, ws_bytes, workspace = _workspace(workspace, tq_fp4_linear_workspace_size, x.device, n, K, N, fmt)
-    y, y_ptr, y_code = _output(y, (n, N), x)
+    ws_ptr, ws_bytes, workspace = _workspace(workspace, tq_fp4_linear_workspace_size, x.device, stream, n, K, N, fmt)
+    y, y_ptr, y_code = _output(y, (n, N), x, stream)
     rc = _call("tq_fp4_linear")(ptr, code, step, w_ptr, s_ptr, fmt, _scale_ptr(w_scale, 1, "w_scale"),
                                 _scale_ptr(x_scale, 1, "x_scale"), n, K, N, ws_ptr, ws_bytes, y_ptr, y_code,
                                 _stream(stream))
@@ -918,8 +929,9 @@ def tq_fp4_moe_forward(x, packed, tiled_scales, topk_ids, topk_w, fmt: int = FP4
     E, N, _ = packed.shape
     top_k = topk_ids.shape[1]
     w_ptr, s_ptr = _fp4_matrix(packed, tiled_scales, E, N, K, fmt, "packed")
-    ws_ptr, ws_bytes, workspace = _workspace(workspace, tq_fp4_moe_workspace_size, x.device, n, top_k, E, K, N, fmt)
-    y, y_ptr, y_code = _output(y, (n, N), x)
+    ws_ptr, ws_bytes, workspace = _workspace(workspace, tq_fp4_moe_workspace_size, x.device, stream, n, top_k, E, K, N,
+                                               fmt)
+    y, y_ptr, y_code = _output(y, (n, N), x, stream)
     rc = _call("tq_fp4_moe_forward")(ptr, code, step, w_ptr, s_ptr, fmt, _scale_ptr(w_scale, E, "w_scale"),
                                      _scale_ptr(x_scale, 1, "x_scale"), _given(topk_ids, (n, top_k), int32, "topk_ids"),
                                      _given(topk_w, (n, top_k), fp32, "topk_w"), n, top_k, E, K, N, ws_ptr, ws_bytes,
@@ -947,8 +959,9 @@ def tq_fp4_moe_mlp_forward(x, packed_gu, tiled_gu, packed_down, tiled_down, topk
     top_k = topk_ids.shape[1]
     gu_ptr, gus_ptr = _fp4_matrix(packed_gu, tiled_gu, E, 2 * I, H, fmt, "packed_gu")
     d_ptr, ds_ptr = _fp4_matrix(packed_down, tiled_down, E, H, I, fmt, "packed_down")
-    ws_ptr, ws_bytes, workspace = _workspace(workspace, tq_fp4_moe_mlp_workspace_size, x.device, n, top_k, E, H, I, fmt)
-    y, y_ptr, y_code = _output(y, (n, H), x)
+    ws_ptr, ws_bytes, workspace = _workspace(workspace, tq_fp4_moe_mlp_workspace_size, x.device, stream, n, top_k, E, H, I,
+                                               fmt)
+    y, y_ptr, y_code = _output(y, (n, H), x, stream)
     rc = _call("tq_fp4_moe_mlp_forward")(
         ptr, code, step, gu_ptr, gus_ptr, _scale_ptr(gu_scale, E, "gu_scale"), d_ptr, ds_ptr,
         _scale_ptr(down_scale, E, "down_scale"), fmt, _scale_ptr(x_scale, 1, "x_scale"),
