@@ -550,7 +550,8 @@ int tq_fp4_tile_scales(const uint8_t* scales, int E, int N, int K, int fmt, uint
  *   y[t] = sum_j topk_w[t][j] W_down h(t,j).
  * x as in tq_fp4_quantize; packed and tiled_scales (tq_fp4_tile_scales) 16-byte
  * aligned; y (device) dense [n][N] (or [n][H]).  N is any width; K, H and I are
- * multiples of 32.  E <= 1024, top_k <= 32.  Few rows (by a rule on n, top_k,
+ * multiples of 32.  E <= 1024, top_k <= 32; n * top_k and E * N below
+ * 2^31 - 1024, n * top_k * N below 2^58.  Few rows (by a rule on n, top_k,
  * E, K and N) take one launch that needs no workspace.  workspace (device) of
  * at least the matching *_workspace_size() bytes (0 on invalid arguments; 256,
  * or a NULL workspace, where none is needed), 256-byte aligned; its contents

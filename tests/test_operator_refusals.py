@@ -135,3 +135,15 @@ def test_short_calls_take_the_headers_arguments(tq):
                 else:
                     with pytest.raises(OverflowError):
                         call(*wrong)
+
+
+def test_sizes_past_a_size_t_are_refused(tq):
+    """Rows x N values whose fp32 partial sums need 2^63 bytes or more."""
+    big = 1 << 30
+    assert tq.lib().tq_fp4_linear_workspace_size(big, 32, big, 0) == 0
+    assert tq.lib().tq_fp4_linear(A, 1, 32, A, A, 0, None, None, big, 32, big, A, 1 << 20, A, 1, None) == INVALID
+    assert tq.lib().tq_fp4_moe_workspace_size(big, 1, 1, 32, big, 0) == 0
+    assert tq.lib().tq_fp4_moe_forward(A, 1, 32, A, A, 0, None, None, A, A, big, 1, 1, 32, big, A, 1 << 20, A, 1,
+                                       None) == INVALID
+    assert tq.lib().tq_fp4_moe_mlp_workspace_size(big, 1, 1, 32, 1 << 28, 0) == 0
+    assert tq.lib().tq_fp4_linear_workspace_size(big, 32, 1 << 20, 0) > 1 << 35   # within it

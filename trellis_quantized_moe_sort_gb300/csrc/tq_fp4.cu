@@ -162,6 +162,9 @@ bool bad_moe_shape(int64_t n, int top_k, int E) {
 }
 bool bad_matrix(int E, int K, int N) { return bad_k(K) || N < 1 || static_cast<int64_t>(E) * N >= kMaxIndex; }
 
+// Partial sums whose bytes, up to 8 splits of them, would not fit a size_t.
+bool bad_output(int64_t rows, int64_t N) { return static_cast<double>(rows) * static_cast<double>(N) >= 0x1p58; }
+
 bool bad_rows(const void* x, int type, int64_t stride, int64_t n, int K) {
   return bad_type(type) || stride < K || (stride * static_cast<int64_t>(type_size(type))) % 16 != 0 ||
          (n > 0 && (!x || !aligned(x, 16)));
@@ -291,14 +294,14 @@ int tq_fp4_tile_scales(const uint8_t* scales, int E, int N, int K, int fmt, uint
 }
 
 size_t tq_fp4_linear_workspace_size(int64_t n, int K, int N, int fmt) {
-  if (n < 0 || n >= kMaxIndex || bad_matrix(1, K, N) || bad_format(fmt)) return 0;
+  if (n < 0 || n >= kMaxIndex || bad_matrix(1, K, N) || bad_output(n, N) || bad_format(fmt)) return 0;
   return linear_gemv(n, K, N) ? kNoWorkspace : plan_linear(nullptr, n, K, N, fmt).bytes;
 }
 
 int tq_fp4_linear(const void* x, int x_type, int64_t x_stride, const uint8_t* packed, const uint8_t* tiled_scales,
                   int fmt, const float* w_scale, const float* x_scale, int64_t n, int K, int N, void* workspace,
                   size_t workspace_bytes, void* y, int y_type, tq_stream_t stream) {
-  if (n < 0 || n >= kMaxIndex || bad_matrix(1, K, N) || bad_format(fmt) || bad_type(y_type) ||
+  if (n < 0 || n >= kMaxIndex || bad_matrix(1, K, N) || bad_output(n, N) || bad_format(fmt) || bad_type(y_type) ||
       bad_rows(x, x_type, x_stride, n, K) || (fmt == TQ_FP4_MX && (w_scale || x_scale)))
     return TQ_ERR_INVALID_ARG;
   if (n > 0 && (!packed || !tiled_scales || !y || !aligned(packed, 16) || !aligned(tiled_scales, 16) ||
@@ -327,7 +330,7 @@ int tq_fp4_linear(const void* x, int x_type, int64_t x_stride, const uint8_t* pa
 }
 
 size_t tq_fp4_moe_workspace_size(int64_t n, int top_k, int E, int K, int N, int fmt) {
-  if (bad_moe_shape(n, top_k, E) || bad_matrix(E, K, N) || bad_format(fmt)) return 0;
+  if (bad_moe_shape(n, top_k, E) || bad_matrix(E, K, N) || bad_output(n * top_k, N) || bad_format(fmt)) return 0;
   return moe_gemv(n, top_k, E, K, N) ? kNoWorkspace : plan_moe(nullptr, n, top_k, E, K, N, fmt).bytes;
 }
 
@@ -335,8 +338,8 @@ int tq_fp4_moe_forward(const void* x, int x_type, int64_t x_stride, const uint8_
                        int fmt, const float* w_scale, const float* x_scale, const int32_t* topk_ids,
                        const float* topk_w, int64_t n, int top_k, int E, int K, int N, void* workspace,
                        size_t workspace_bytes, void* y, int y_type, tq_stream_t stream) {
-  if (bad_moe_shape(n, top_k, E) || bad_matrix(E, K, N) || bad_format(fmt) || bad_type(y_type) ||
-      bad_rows(x, x_type, x_stride, n, K) || (fmt == TQ_FP4_MX && (w_scale || x_scale)))
+  if (bad_moe_shape(n, top_k, E) || bad_matrix(E, K, N) || bad_output(n * top_k, N) || bad_format(fmt) ||
+      bad_type(y_type) || bad_rows(x, x_type, x_stride, n, K) || (fmt == TQ_FP4_MX && (w_scale || x_scale)))
     return TQ_ERR_INVALID_ARG;
   if (n > 0 && (!packed || !tiled_scales || !topk_ids || !topk_w || !y || !aligned(packed, 16) ||
                 !aligned(tiled_scales, 16) || !aligned(y, type_size(y_type))))
@@ -369,7 +372,7 @@ int tq_fp4_moe_forward(const void* x, int x_type, int64_t x_stride, const uint8_
 
 size_t tq_fp4_moe_mlp_workspace_size(int64_t n, int top_k, int E, int H, int I, int fmt) {
   if (bad_moe_shape(n, top_k, E) || I < 1 || I > (1 << 29) || bad_matrix(E, H, 2 * I) || bad_matrix(E, I, H) ||
-      bad_format(fmt))
+      bad_output(n * top_k, 2ll * I) || bad_output(n * top_k, H) || bad_format(fmt))
     return 0;
   return plan_mlp(nullptr, n, top_k, E, H, I, fmt).bytes;
 }
