@@ -200,6 +200,26 @@ def test_linear_into_a_given_buffer(n, N, offset):
         assert (buffer[:offset] == 7).all() and (buffer[offset + n * N:] == 7).all()
 
 
+@pytest.mark.parametrize("fmt,dtype", [("nv", "bf16"), ("mx", "fp16")])
+@pytest.mark.parametrize("n,N", [(70, 1), (70, 7), (71, 9), (77, 24), (130, 127), (250, 128), (259, 131), (300, 264),
+                                 (500, 385), (1000, 520)])
+def test_linear_rows_at_every_alignment(n, N, fmt, dtype):
+    """One step of K, so no splits: 16-bit rows that start anywhere in their 16 bytes."""
+    rng = np.random.default_rng([n, N])
+    w = Weights(rng, 1, N, 64, fmt)
+    x = _x(rng, n, 64, dtype, spread=1.0)
+    xq = M.quantize(_f64(x), fmt)[2]
+    want, size = xq @ w.values[0].T, np.abs(xq) @ np.abs(w.values[0]).T
+    x = x.cuda()
+    for offset in range(8):
+        buffer = torch.full((n * N + 64,), 7.0, dtype=DTYPES[dtype], device="cuda")
+        y = buffer[offset:offset + n * N].view(n, N)
+        tq.tq_fp4_linear(x, w.packed[0], w.tiled, fmt=w.fmt, w_scale=w.scale, y=y)
+        check_no_device_error()
+        _close(y, want, size, dtype)
+        assert (buffer[:offset] == 7).all() and (buffer[offset + n * N:] == 7).all()
+
+
 # tokens, experts, top_k, K, N: few tokens (one launch), every m-tile size, experts
 # without tokens, one with all of them
 EXPERTS = [(1, 8, 2, 512, 256), (1, 256, 6, 256, 64), (2, 4, 4, 96, 5), (5, 1, 1, 288, 129), (40, 8, 2, 512, 257),

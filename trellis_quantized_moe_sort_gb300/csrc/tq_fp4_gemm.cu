@@ -62,7 +62,7 @@ struct GemmParams {
   const float* w_scale;
   void* y;                       // [P][N], or fp32 [splits][P][N]
   int scaled;                    // by x_scale and w_scale: y is the result, not partial sums
-  int y_pairs;                   // y's rows start on multiples of two values
+  int y_words;                   // each row of y starts on a multiple of four bytes
   int* err;
   long long cap, split_stride;
   int P, E, K, N, tile_m;
@@ -264,61 +264,81 @@ __device__ __forceinline__ void read_rows(const int* p, int (&row)[16]) {
   }
 }
 
-// take(values, output rows) for every second 16 columns of this warp's
+// take(values, column) for every second 16 columns of this warp's
 // accumulator rows, from the `half`-th on, the next ones in flight meanwhile.
 // (Two blocks a turn and no more: unrolled over the whole tile the addresses
 // spill.)
 template <typename Take>
-__device__ __forceinline__ void drain(uint32_t src, int rows, int half, const int* rows_out, Take&& take) {
+__device__ __forceinline__ void drain(uint32_t src, int rows, int half, Take&& take) {
   uint32_t v[2][16];
-  int row[16];
-  src += 16 * half;
-  rows -= 16 * half;
-  rows_out += 16 * half;
-  if (rows > 0) tmem_ld16(src, v[0]);
+  const int first = 16 * half;
+  if (first < rows) tmem_ld16(src + first, v[0]);
 #pragma unroll 1
-  for (int c = 0; c < rows; c += 64) {
+  for (int c = first; c < rows; c += 64) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int at = c + 32 * i;
       if (at >= rows) break;
       tmem_wait_ld();
       if (at + 32 < rows) tmem_ld16(src + at + 32, v[(i + 1) & 1]);
-      read_rows(rows_out + at, row);
-      take(v[i], row);
+      take(v[i], at);
     }
   }
 }
 
-// out[row][f] = alpha * D, rounded once.  16-bit types with an even width:
-// neighbouring lanes exchange so that each stores two rows of one column.
-template <typename T>
-__device__ __forceinline__ void store_columns(T* out, bool by_two, int N, uint32_t src, int rows, int half,
-                                              const int* rows_out, int f, float alpha) {
-  if (sizeof(T) == 4 || !by_two) {
-    const bool in = f < N;
-    drain(src, rows, half, rows_out, [&](const uint32_t (&v)[16], const int (&row)[16]) {
+// out[row][f] = alpha * D, to the rows of a list.
+__device__ __forceinline__ void store_scattered(float* out, int N, uint32_t src, int rows, int half, const int* rows_out,
+                                                int f, float alpha) {
+  const bool in = f < N;
+  drain(src, rows, half, [&](const uint32_t (&v)[16], int at) {
+    int row[16];
+    read_rows(rows_out + at, row);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        if (row[j] >= 0 && in) out[static_cast<size_t>(row[j]) * N + f] = narrow<T>(__uint_as_float(v[j]) * alpha);
-      }
-    });
-  } else {
-    const bool odd = f & 1, in = (f & ~1) < N;
-    drain(src, rows, half, rows_out, [&](const uint32_t (&v)[16], const int (&row)[16]) {
+    for (int j = 0; j < 16; ++j) {
+      if (row[j] >= 0 && in) out[static_cast<size_t>(row[j]) * N + f] = __uint_as_float(v[j]) * alpha;
+    }
+  });
+}
+
+// Neighbouring lanes exchange their values of two rows: the even one returns its
+// column and the next of the first row, the odd one those of the second.
+template <typename T>
+__device__ __forceinline__ uint32_t two_of_a_row(uint32_t first, uint32_t second, bool odd, float alpha) {
+  const uint32_t give = odd ? first : second, keep = odd ? second : first;
+  const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
+  const T two[2] = {narrow<T>(__uint_as_float(odd ? got : keep) * alpha),
+                    narrow<T>(__uint_as_float(odd ? keep : got) * alpha)};
+  uint32_t bits;
+  memcpy(&bits, two, 4);
+  return bits;
+}
+
+// y[row0 + c][f] = alpha * D[c], rounded once: consecutive rows.  16-bit types
+// with words on word boundaries: neighbouring lanes exchange so that each stores
+// two rows of one column.  (Row addresses by one addition each: from a list in
+// shared memory, as the scattered rows' are, 3001 rows 2048 -> 4099 took 27.6 us
+// and not 22.1.  Turning blocks in shared memory for stores of 256 bytes a row
+// gained nothing: the tensor path and the copies need its rate.)
+template <typename T>
+__device__ __forceinline__ void store_rows(T* y, bool by_two, int N, long long row0, uint32_t src, int rows, int half,
+                                           int f, float alpha) {
+  const bool odd = f & 1, in = by_two ? (f & ~1) < N : f < N;
+  drain(src, rows, half, [&](const uint32_t (&v)[16], int at) {
+    T* const out = y + (row0 + at) * N + f;
+    if (sizeof(T) == 2 && by_two) {
 #pragma unroll
       for (int j = 0; j < 16; j += 2) {
-        const uint32_t give = odd ? v[j] : v[j + 1], keep = odd ? v[j + 1] : v[j];
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
-        T two[2] = {narrow<T>(__uint_as_float(odd ? got : keep) * alpha),
-                    narrow<T>(__uint_as_float(odd ? keep : got) * alpha)};
-        const int to = odd ? row[j + 1] : row[j];
-        uint32_t bits;
-        memcpy(&bits, two, 4);
-        if (to >= 0 && in) *reinterpret_cast<uint32_t*>(out + static_cast<size_t>(to) * N + (f & ~1)) = bits;
+        const uint32_t bits = two_of_a_row<T>(v[j], v[j + 1], odd, alpha);
+        const int c = odd ? j + 1 : j;
+        if (in && at + c < rows) *reinterpret_cast<uint32_t*>(out + static_cast<long long>(c) * N - odd) = bits;
       }
-    });
-  }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        if (in && at + j < rows) out[static_cast<long long>(j) * N] = narrow<T>(__uint_as_float(v[j]) * alpha);
+      }
+    }
+  });
 }
 
 template <int kFmt, bool kPair, typename TOut>
@@ -459,7 +479,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
     // A stage's operands are at fixed distances from its start: one running
     // 16-byte address serves the low words of the three descriptors, whose high
     // words never change.
-    const uint32_t desc0 = (base & 0x3FFFFu) >> 4, desc_end = desc0 + static_cast<uint32_t>(stages * stage_bytes) / 16;
+    const uint32_t desc0 = (base & 0x3FFFFu) >> 4;
     const uint32_t desc_stage = static_cast<uint32_t>(stage_bytes) / 16, desc_sf = static_cast<uint32_t>(kWBytes + x_bytes) / 16;
     const uint32_t bar_end = bar_full + 8 * stages;
     uint32_t desc = desc0, bar = bar_full, phase = 0;
@@ -524,28 +544,30 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
     }
     __syncwarp();
   } else {
-    // Lane l of quarter q holds weight row 32 q + l of every column.  The
-    // output row of each column is kept in shared memory (read back four at a
-    // time, the same for all lanes), -1 for none.
+    // Lane l of quarter q holds weight row 32 q + l of every column.
     const int q = warp & 3, half = (warp - kWarpEpi0) >> 2;
+    // The output row of each column of an experts' tile is kept in shared memory
+    // (read back four at a time, the same for all lanes), -1 for none.
     int* const rows_out = reinterpret_cast<int*>(gbase + p.off_rows) + 256 * (warp - kWarpEpi0);
     Ring acc;
     for (long long u = unit0; u < units; u += unit_step) {
       const Unit t = unit_at<kPair>(p, u, num_tiles, rank);
       if (!t.ok) continue;
-      __syncwarp();   // the last unit's rows have been read
-      for (int col = lane; col < ((t.rows + 15) & ~15); col += 32) {
-        int pair = -1;
-        if (col < t.rows) {
-          pair = p.sorted_pairs ? __ldg(p.sorted_pairs + t.slot0 + col) : t.slot0 + col;
-          if (pair < 0 || pair >= p.P) {
-            record_error(err, TQ_ERR_INVALID_ARG, kWhereFp4Epilogue);
-            pair = -1;
+      if (p.sorted_pairs) {
+        __syncwarp();   // the last unit's rows have been read
+        for (int col = lane; col < ((t.rows + 15) & ~15); col += 32) {
+          int pair = -1;
+          if (col < t.rows) {
+            pair = __ldg(p.sorted_pairs + t.slot0 + col);
+            if (pair < 0 || pair >= p.P) {
+              record_error(err, TQ_ERR_INVALID_ARG, kWhereFp4Epilogue);
+              pair = -1;
+            }
           }
+          rows_out[col] = pair;
         }
-        rows_out[col] = pair;
+        __syncwarp();
       }
-      __syncwarp();
       if (!mbar_wait_short(bar_accfull + 8 * acc.at, acc.phase, abort_flag, err, kWhereFp4Epilogue)) break;
       tc_fence_after();
       const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(acc.at * p.acc_cols);
@@ -556,7 +578,10 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
         alpha = (p.x_scale ? __ldg(p.x_scale) : 1.f) * (p.w_scale ? __ldg(p.w_scale + t.e) : 1.f);
       else
         out += static_cast<size_t>(t.split) * p.split_stride;
-      store_columns<TOut>(out, p.y_pairs, p.N, src, t.rows, half, rows_out, f, alpha);
+      if (sizeof(TOut) == 4 && p.sorted_pairs)   // experts' partial sums
+        store_scattered(reinterpret_cast<float*>(out), p.N, src, t.rows, half, rows_out, f, alpha);
+      else
+        store_rows(out, p.y_words, p.N, t.slot0, src, t.rows, half, f, alpha);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -644,7 +669,7 @@ int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s) {
   p.w_scale = g.w_scale;
   p.y = g.y ? g.y : g.part;
   p.scaled = g.y != nullptr;
-  p.y_pairs = g.N % 2 == 0 && (reinterpret_cast<uintptr_t>(g.y) & 3u) == 0;
+  p.y_words = g.N % 2 == 0 && (reinterpret_cast<uintptr_t>(g.y) & 3u) == 0;
   p.err = g.err;
   p.cap = g.cap;
   p.split_stride = static_cast<long long>(g.P) * g.N;
@@ -664,7 +689,9 @@ int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s) {
   p.x_bytes = (pair ? p.n_max / 2 : p.n_max) * kRowBytes;
   p.x_sf_bytes = x_groups * sf_step;
   p.stage_bytes = kWBytes + p.x_bytes + sf_step + p.x_sf_bytes;
-  const int bar_bytes = (8 * kNumBars + 16 + 15) / 16 * 16, rows_bytes = kEpiWarps * 256 * 4;
+  const int type = g.y ? g.y_type : TQ_FP32;
+  const int bar_bytes = (8 * kNumBars + 16 + 15) / 16 * 16;
+  const int rows_bytes = g.sorted_pairs ? kEpiWarps * 256 * 4 : 0;
   p.stages = std::min(kMaxStages, (kSmemLimit - 1024 - bar_bytes - rows_bytes) / p.stage_bytes);
   p.off_bar = static_cast<uint32_t>(p.stages * p.stage_bytes);
   p.off_rows = p.off_bar + bar_bytes;
@@ -688,7 +715,6 @@ int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s) {
       !encode_bytes(&tm_ws, g.w_scales, w_groups * p.steps * sf_rows, 128, sf_rows, false) ||
       !encode_bytes(&tm_xs, g.x_scales, x_tiles * p.steps * sf_rows, 128, sf_rows, false))
     return TQ_ERR_INVALID_ARG;
-  const int type = g.y ? g.y_type : TQ_FP32;
   const GemmKernel kernel = type == TQ_FP32   ? kernel_for<float>(g.fmt, pair)
                             : type == TQ_BF16 ? kernel_for<__nv_bfloat16>(g.fmt, pair)
                                               : kernel_for<__half>(g.fmt, pair);
