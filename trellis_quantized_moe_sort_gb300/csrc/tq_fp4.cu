@@ -26,7 +26,7 @@ bool bad_k(int K) { return K < 32 || K % 32 != 0; }
 // kernel's parts take (cycles of an SM; the pair kernel's for two of them):
 //   a step of 256 values   the MMAs, 4 x T / 2 and a seventh more, the issue of
 //                          one step (360), or the step's bytes at 72 a clock
-//   a unit                 2500 beside its steps; its drain of 22 a column runs
+//   a unit                 2500 beside its steps; its drain of 14 a column runs
 //                          beside the next unit's
 //   the launch             about 4000 until the first MMA
 //   weights                from memory at 3400 bytes a clock over the chip
@@ -39,7 +39,8 @@ bool bad_k(int K) { return K < 32 || K % 32 != 0; }
 // reads the matrix again.
 // Measured against m-tiles of a power of two or 224 and splits by the units
 // alone (us): linear 4096 -> 4096, 500 rows 22.3 -> 12.2; 4096 -> 2048, 1500 rows
-// 32.7 -> 15.6; 512 -> 256, 4000 rows 17.6 -> 10.3.
+// 32.7 -> 15.6; 512 -> 256, 4000 rows 17.6 -> 10.3 when it came in (now 11.7,
+// 15.0 and 9.1).
 struct Tiling {
   int tile_m, splits;
 };
@@ -60,8 +61,8 @@ Tiling search_tiling(double rows, double matrices, int K, int N, int fmt, bool e
     const double bytes = 128.0 * 128 + sf + 128.0 * (pair ? T / 2 : T) + sf * ((T + 127) / 128);
     const double step = std::max({360.0, 2.3 * T, bytes / 72.0});
     for (int s = 1; s <= std::min(8, steps); ++s) {
-      const double unit = std::max(((steps + s - 1) / s) * step + 2500.0, 22.0 * T);
-      double cost = 4000.0 + std::max(std::ceil(units * s / slots) * unit, weights) + 22.0 * T;
+      const double unit = std::max(((steps + s - 1) / s) * step + 2500.0, 14.0 * T);
+      double cost = 4000.0 + std::max(std::ceil(units * s / slots) * unit, weights) + 14.0 * T;
       if (s > 1 || experts) cost += 5000.0 + 8.0 * s * rows * matrices * N / 3000.0;
       if (cost < best_cost * 0.99) {
         best = {T, s};
