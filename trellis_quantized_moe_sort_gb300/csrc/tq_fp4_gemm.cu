@@ -27,7 +27,7 @@
 // 75 us for 333 MB read and 75 MB written (2048 tokens on 64 NV experts; the
 // tensor pipe is busy 30% of it), 271 us for 1.2 GB read and 0.4 GB written
 // (8192 tokens on 256).  A linear of many rows is bound by the units' fixed parts
-// (first copies, last drain) beside MMAs of 4 x T / 2 cycles a step: 27.4 us for
+// (first copies, last drain) beside MMAs of 4 x T / 2 cycles a step: 21.9 us for
 // 3001 rows 2048 -> 4099, staging included.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -317,7 +317,7 @@ __device__ __forceinline__ uint32_t two_of_a_row(uint32_t first, uint32_t second
 // with words on word boundaries: neighbouring lanes exchange so that each stores
 // two rows of one column.  (Row addresses by one addition each: from a list in
 // shared memory, as the scattered rows' are, 3001 rows 2048 -> 4099 took 27.6 us
-// and not 22.1.  Turning blocks in shared memory for stores of 256 bytes a row
+// and not 21.9.  Turning blocks in shared memory for stores of 256 bytes a row
 // gained nothing: the tensor path and the copies need its rate.)
 template <typename T>
 __device__ __forceinline__ void store_rows(T* y, bool by_two, int N, long long row0, uint32_t src, int rows, int half,
