@@ -22,8 +22,8 @@
 // each, summed in a fixed order by the combine: results do not depend on the
 // schedule), or, for a linear without splits, y itself.
 //
-// Bound: memory, where the experts' weights are read for few rows each: 92 us
-// for the 587 MB of 136 MX experts 4096 -> 2048 (32 tokens of top-6, 6.4 TB/s),
+// Bound: memory, where the experts' weights are read for few rows each: 92-96 us
+// for the 587 MB of 136 MX experts 4096 -> 2048 (32 tokens of top-6, 6.1-6.4 TB/s),
 // 75 us for 333 MB read and 75 MB written (2048 tokens on 64 NV experts; the
 // tensor pipe is busy 30% of it), 271 us for 1.2 GB read and 0.4 GB written
 // (8192 tokens on 256).  A linear of many rows is bound by the units' fixed parts

@@ -8,7 +8,7 @@
 //
 // Measured for 8192 x 4096 bf16 values, NV: quantise 17.9 us for 86 MB (the
 // issue of its instructions is 71% busy), dequantise 13.8 us for 86 MB (6.2
-// TB/s); the two in turn 31.2 us.  Staging 2048 tokens for top-6 products: 16.8 us
+// TB/s); the two in turn 31.2 us.  Staging 2048 tokens for top-6 products: 15.5 us
 // for 17 MB read and 28 MB written: a pair's scales are single words 16 bytes
 // apart in the tiled layout, a 32-byte sector of L2 each, so that the scales
 // take twice the sectors of the codes.  The combine of those 12288 x 2048
