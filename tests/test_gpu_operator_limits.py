@@ -1,0 +1,103 @@
+"""The scored router's gradient and the 4-bit operators at the ends of the fp32
+range, and with scales that are zero or no number."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.moe_operators as M
+import trellis_quantized_moe_sort_gb300 as tq
+from gpu_util import check_no_device_error
+
+pytestmark = pytest.mark.gpu
+FMT = {"nv": tq.FP4_NV, "mx": tq.FP4_MX}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from trellis_quantized_moe_sort_gb300 import build
+    build.build()
+    tq.tq_init(0)
+
+
+def _f64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def _scale(*g):
+    return torch.tensor(g, dtype=torch.float32, device="cuda")
+
+
+class Matrices:
+    """E seeded matrices N(0, factor^2 / K), quantised by the definition."""
+
+    def __init__(self, rng, E, N, K, fmt, factor=1.0):
+        self.g = 2.0 ** -9 if fmt == "nv" else 1.0
+        code, byte, values = M.quantize(factor * rng.standard_normal((E * N, K)) / np.sqrt(K), fmt, self.g)
+        self.packed = torch.from_numpy(M.pack(code).reshape(E, N, K // 2)).cuda()
+        self.byte = byte.reshape(E, N, -1)
+        self.tiled = tq.tq_fp4_tile_scales(torch.from_numpy(self.byte).cuda(), FMT[fmt])
+        self.scale = torch.full((E,), self.g, device="cuda") if fmt == "nv" else None
+        self.values = values.reshape(E, N, K)
+
+
+def _arms(call):
+    """call()'s result and whether it took the one launch for few rows."""
+    before = tq.tq_launch_counts_all()
+    y = call()
+    after = tq.tq_launch_counts_all()
+    few, many = (after[c] - before[c] for c in ("fp4_gemv", "fp4_gemm"))
+    assert few + many == 1
+    return y, few == 1
+
+
+# Both sides' values are those of the definition, so what differs is the fp32
+# sum: at most K / 64 + 64 roundings of partial sums no larger than sum |w| |x|.
+@pytest.mark.parametrize("n", [1, 300])
+@pytest.mark.parametrize("dtype,special,factor", [
+    (torch.bfloat16, float("inf"), 1.0), (torch.float16, float("-inf"), 1.0), (torch.float32, float("inf"), 1.0),
+    (torch.float32, 2.0 ** 124, 1.0), (torch.bfloat16, -2.0 ** 126, 2.0 ** -100), (torch.float32, 2.0 ** 123, 2.0 ** -20),
+    (torch.float32, 3e38, 1.0)])
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+def test_largest_activations(fmt, dtype, special, factor, n):
+    """An infinity counts as the largest finite number, in every product; a block of such values
+    against weights that cancel it out is 0."""
+    rng = np.random.default_rng([n, 5])
+    E, N, K = 3, 129, 512
+    w = Matrices(rng, E, N, K, fmt, factor if fmt == "mx" else 1.0)
+    x = torch.from_numpy(rng.standard_normal((n, K)).astype(np.float32)).to(dtype)
+    x[:, 7] = special
+    x[n // 2, 40] = -special
+    g = 2.0 ** 110 if fmt == "nv" and dtype != torch.float16 else None
+    xs = None if g is None else _scale(g)
+    xq = M.quantize(_f64(x), fmt, 1.0 if g is None else g)[2]
+    x = x.cuda()
+    y, few = _arms(lambda: tq.tq_fp4_linear(x, w.packed[0], w.tiled[: w.tiled.numel() // E], fmt=FMT[fmt],
+                                            w_scale=None if w.scale is None else w.scale[:1], x_scale=xs,
+                                            y=torch.empty(n, N, device="cuda")))
+    assert few == (n == 1)
+    want, size = xq @ w.values[0].T, np.abs(xq) @ np.abs(w.values[0]).T
+    assert (np.abs(_f64(y) - want) <= 2.0 ** -16 * size + 2.0 ** -23 * np.abs(want)).all()
+    ids = np.stack([rng.permutation(E)[:2] for _ in range(n)]).astype(np.int32)
+    tw = (0.5 * rng.random((n, 2))).astype(np.float32)
+    y, few = _arms(lambda: tq.tq_fp4_moe_forward(x, w.packed, w.tiled, torch.from_numpy(ids).cuda(),
+                                                 torch.from_numpy(tw).cuda(), fmt=FMT[fmt], w_scale=w.scale, x_scale=xs,
+                                                 y=torch.empty(n, N, device="cuda")))
+    assert few == (n == 1)
+    check_no_device_error()
+    want, size = M.moe(xq, ids, tw, w.values)
+    assert (np.abs(_f64(y) - want) <= 2.0 ** -16 * size + 2.0 ** -23 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("n", [1, 300])
+@pytest.mark.parametrize("x_factor,w_factor", [(2.0 ** -110, 2.0 ** 115), (2.0 ** 122, 2.0 ** -120), (2.0 ** -60, 2.0 ** -40)])
+def test_scales_far_apart(x_factor, w_factor, n):
+    """Power-of-two scales whose product is an ordinary number, or near fp32's smallest ones."""
+    rng = np.random.default_rng([n, 6])
+    N, K = 130, 512
+    w = Matrices(rng, 1, N, K, "mx", w_factor)
+    x = torch.from_numpy((x_factor * rng.standard_normal((n, K))).astype(np.float32))
+    xq = M.quantize(_f64(x), "mx")[2]
+    y, few = _arms(lambda: tq.tq_fp4_linear(x.cuda(), w.packed[0], w.tiled, fmt=tq.FP4_MX))
+    assert few == (n == 1)
+    want, size = xq @ w.values[0].T, np.abs(xq) @ np.abs(w.values[0]).T
+    assert (np.abs(_f64(y) - want) <= 2.0 ** -16 * size + 2.0 ** -23 * np.abs(want)).all()

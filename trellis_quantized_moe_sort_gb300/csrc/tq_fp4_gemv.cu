@@ -121,6 +121,19 @@ __device__ __forceinline__ void piece_x(uint2 q, uint4* a, uint4* b) {
   memcpy(b, &p1, 16);
 }
 
+// The E8M0 scale 2^e of a block of x as two factors: a block's dot product takes
+// the first (`second` 0; 2^7 above its part, for kPieceScale), the weights' scale
+// and then the other.  One scale can be 2^125 where the other is small: their
+// product, or that of one of them and kPieceScale's inverse, would be infinite,
+// and NaN beside a sum of 0.  With 2^e in halves for e > 0 no step is infinite
+// unless the result is; for e <= 0 the whole of it comes first and is exact (a
+// sum is a multiple of 1/4).
+static_assert(kPieceScale == 0x1p-7f, "mx_factor");
+__device__ __forceinline__ float mx_factor(uint32_t byte, int second) {
+  const int late = max(static_cast<int>(byte) - 127, 0) >> 1;
+  return __uint_as_float(static_cast<uint32_t>(second ? late + 127 : static_cast<int>(byte) - late + 7) << 23);
+}
+
 template <typename TX, typename TY, int kFmt>
 __global__ void __launch_bounds__(kThreads, 4)
 fp4_gemv_kernel(const TX* __restrict__ x, const GemvParams p, TY* __restrict__ y) {
@@ -134,6 +147,7 @@ fp4_gemv_kernel(const TX* __restrict__ x, const GemvParams p, TY* __restrict__ y
   const int K = p.K, N = p.N, top_k = p.top_k, E = p.E, chunks = K / kChunk, items = K / 16;
   // x in four planes of 8 values: chunk c's values 8 i .. 8 i + 7 at plane[i * chunks + c],
   // so that neighbouring lanes read neighbouring 16 bytes; then the scales of its 16-value pieces
+  // (MX: the two factors of its blocks')
   uint4* const plane = smem;
   float* const xs = reinterpret_cast<float*>(smem + 4 * chunks);
   const long long t = blockIdx.y;
@@ -195,7 +209,7 @@ fp4_gemv_kernel(const TX* __restrict__ x, const GemvParams p, TY* __restrict__ y
     const uint2 q = fp4_codes16<kFmt>(v, d, r, top);
     if (item < items) {
       piece_x(q, &plane[(2 * (item & 1)) * chunks + item / 2], &plane[(2 * (item & 1) + 1) * chunks + item / 2]);
-      xs[item] = fp4_scale_value<kFmt>(byte) * (1.f / kPieceScale);
+      xs[item] = kFmt == TQ_FP4_NV ? from_e4m3(byte) * (1.f / kPieceScale) : mx_factor(byte, item & 1);
     }
   }
 
@@ -233,7 +247,7 @@ fp4_gemv_kernel(const TX* __restrict__ x, const GemvParams p, TY* __restrict__ y
           part[r] = fmaf(d0, s.x * f.x, part[r]);
           part[r] = fmaf(d1, s.y * f.y, part[r]);
         } else {
-          part[r] = fmaf(d0 + d1, s.x * from_e8m0(sw[(in / 4) * 32 + r * 16 + (in & 3)]), part[r]);
+          part[r] = fmaf((d0 + d1) * s.x * from_e8m0(sw[(in / 4) * 32 + r * 16 + (in & 3)]), s.y, part[r]);
         }
       }
     }
