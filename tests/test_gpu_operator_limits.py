@@ -101,3 +101,25 @@ def test_scales_far_apart(x_factor, w_factor, n):
     assert few == (n == 1)
     want, size = xq @ w.values[0].T, np.abs(xq) @ np.abs(w.values[0]).T
     assert (np.abs(_f64(y) - want) <= 2.0 ** -16 * size + 2.0 ** -23 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("n", [1, 300])
+def test_zeros_with_a_global_scale_of_zero(n):
+    """amax / (6 * 448) of an all-zero tensor is 0: its values are 0, and so are its products."""
+    N, K = 129, 512
+    zero = _scale(0.0)
+    packed, scales = tq.tq_fp4_quantize(torch.zeros(N, K, device="cuda"), tq.FP4_NV, zero)
+    assert not packed.any() and not scales.any()
+    assert not tq.tq_fp4_dequantize(packed, scales, tq.FP4_NV, zero).any()
+    w = Matrices(np.random.default_rng(n), 1, N, K, "nv")
+    for x, x_scale, codes, byte, w_scale in (
+            (torch.randn(n, K, device="cuda"), _scale(2.0 ** -9), packed, scales, zero),
+            (torch.zeros(n, K, device="cuda"), zero, w.packed[0], torch.from_numpy(w.byte[0]).cuda(), w.scale),
+            (torch.randn(n, K, device="cuda"), zero, w.packed[0], torch.from_numpy(w.byte[0]).cuda(), w.scale)):
+        tiled = tq.tq_fp4_tile_scales(byte)
+        y, few = _arms(lambda: tq.tq_fp4_linear(x, codes, tiled, w_scale=w_scale, x_scale=x_scale))
+        assert few == (n == 1) and bool((y == 0).all())
+        ids, tw = torch.zeros(n, 1, dtype=torch.int32, device="cuda"), torch.ones(n, 1, device="cuda")
+        y = tq.tq_fp4_moe_forward(x, codes[None], tiled, ids, tw, w_scale=w_scale, x_scale=x_scale)
+        assert bool((y == 0).all())
+    check_no_device_error()

@@ -8,7 +8,8 @@
 //   MX: scale s = 2^(floor(log2 max|x|) - 2) as E8M0; value = e2m1(x / s).
 // Roundings are to nearest even and saturate.  NaN is kept as 0 and does not
 // count for the maximum; an infinity counts as the largest finite number.  A
-// block whose scale is 0 (all zeros, or below E4M3's range) is kept as zeros.
+// block whose scale is 0 (all zeros, below E4M3's range, or g not positive) is
+// kept as zeros.
 #pragma once
 #include "tq_device.cuh"
 #include "tq_types.cuh"
@@ -140,11 +141,13 @@ __device__ __forceinline__ float divide_fast(float a, float b, float r) {
   return __fmaf_rn(__fmaf_rn(-q0, b, a), r, q0);
 }
 
-// The global scale as the quantisers use it: g, 6 g and 1 / (6 g).
+// The global scale as the quantisers use it: g, 6 g and 1 / (6 g).  Where g is
+// not positive (of an all-zero tensor it is often 0, and 0 / 0 would be NaN) an
+// infinite divisor makes every block scale 0.
 struct GlobalScale {
   float g, six, r_six;
   __device__ __forceinline__ explicit GlobalScale(const float* p) : g(p ? *p : 1.f) {
-    six = __fmul_rn(6.f, g);
+    six = g > 0.f ? __fmul_rn(6.f, g) : INFINITY;
     r_six = __frcp_rn(six);
   }
 };
