@@ -123,3 +123,34 @@ def test_zeros_with_a_global_scale_of_zero(n):
         y = tq.tq_fp4_moe_forward(x, codes[None], tiled, ids, tw, w_scale=w_scale, x_scale=x_scale)
         assert bool((y == 0).all())
     check_no_device_error()
+
+
+# Scores of the chosen near fp32's smallest normal number (1.2e-38): their
+# relative error is at most expf's 2 ulp, an addition's and a reciprocal's
+# rounding, and half of a subnormal's last place (2^-22 of 2.9e-39 or more), below 2^-20;
+# a quotient of two of them 2^-19, the row's dot product and the rest a few 2^-24
+# more: within 2^-18 of the sum of the gradients' magnitudes.
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,k", [(8, 2), (64, 6), (200, 9)])
+def test_gradient_of_tiny_scores(score, E, k):
+    rng = np.random.default_rng([E, k])
+    n = 40
+    if score == "sigmoid":
+        x, bias = -88.5 + 0.7 * rng.random((n, E)), None
+    else:                                    # the bias picks experts far below the row's largest
+        x, bias = -87.0 + 0.5 * rng.random((n, E)), np.zeros(E, np.float32)
+        x[:, 0], bias[1:] = 0.0, 2.0
+    x = x.astype(np.float32)
+    g = (1000.0 * rng.standard_normal((n, k))).astype(np.float32)
+    code = tq.SCORE_SIGMOID if score == "sigmoid" else tq.SCORE_SOFTMAX
+    logits = torch.from_numpy(x).cuda()
+    ids, w = tq.tq_router_scored(logits, k, score=code, bias=None if bias is None else torch.from_numpy(bias).cuda(),
+                                 renormalize=True, scale=2.5)
+    assert torch.allclose(w.sum(1), torch.full((n,), 2.5, device="cuda"), rtol=1e-5)
+    got = _f64(tq.tq_router_scored_backward(logits, ids, w, torch.from_numpy(g).cuda(), score=code, renormalize=True,
+                                            scale=2.5))
+    check_no_device_error()
+    ids = ids.cpu().numpy()
+    want = M.router_backward(x, ids, np.ones((n, k)), g, score, True, 2.5)
+    size = 2.5 * np.abs(g).astype(np.float64).sum(1, keepdims=True)
+    assert (np.abs(got - want) <= 2.0 ** -18 * size).all()

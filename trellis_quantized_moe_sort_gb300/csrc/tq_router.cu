@@ -347,8 +347,9 @@ router_scored_kernel(const T* __restrict__ logits, long long stride, const float
 
 // The gradient of the logits.  Chosen experts with a weight of zero (masked
 // fillers) take and give none.  A row is first written as every expert's own
-// part (0 for sigmoid scores, -p_i sum_j dp_j p_j for softmax), then the
-// chosen experts' values go over it.
+// part (-p_i sum_j dp_j p_j for softmax scores, 0 for sigmoid ones and with
+// renormalised weights, which depend on the chosen alone), then the chosen
+// experts' values go over it.
 template <typename T, int PL>
 __global__ void __launch_bounds__(kRouterThreads)
 router_scored_backward_kernel(const T* __restrict__ logits, long long stride, const int32_t* __restrict__ ids,
@@ -379,18 +380,20 @@ router_scored_backward_kernel(const T* __restrict__ logits, long long stride, co
       softmax_terms<PL>(x, &top, &total);
     }
     const float p = live ? one_score(widen(row[e]), score, top, total) : 0.f;
-    if (renorm) {
-      const float sum = warp_sum(p);
-      const float dot = warp_sum(g * p);
-      g = live && sum > 0.f ? (g - dot / sum) / sum : 0.f;
-    }
     float own, dot = 0.f;
-    if (score == TQ_SCORE_SOFTMAX) {
+    if (renorm) {
+      // q (g - sum_j g_j q_j) with q = p / sum: no step exceeds g, where g / sum
+      // may overflow for scores near fp32's smallest.  Its sum over the chosen is 0.
+      const float sum = warp_sum(p);
+      const float q = sum > 0.f ? (live ? p : sum) / sum : 0.f;   // g is 0 in the other lanes; 0 / sum divides slowly
+      own = q * (g - warp_sum(g * q));
+    } else if (score == TQ_SCORE_SOFTMAX) {
       dot = warp_sum(g * p);
       own = p * (g - dot);
     } else {
-      own = g * p * (1.f - p);
+      own = g * p;
     }
+    if (score == TQ_SCORE_SIGMOID) own *= 1.f - p;
     const float r = __frcp_rn(total);   // of a row without finite logits infinite, and its terms are 0
     T* const out = grad + static_cast<size_t>(t) * E;
     const int e0 = lane * PL;
