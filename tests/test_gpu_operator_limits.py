@@ -154,3 +154,34 @@ def test_gradient_of_tiny_scores(score, E, k):
     want = M.router_backward(x, ids, np.ones((n, k)), g, score, True, 2.5)
     size = 2.5 * np.abs(g).astype(np.float64).sum(1, keepdims=True)
     assert (np.abs(got - want) <= 2.0 ** -18 * size).all()
+
+
+# p (1 - p) of a score near 1: each factor has expf's 2 ulp, an addition's and a
+# reciprocal's rounding (2^-21 together), the products three more.
+@pytest.mark.parametrize("dtype,rounding", [(torch.float32, 0.0), (torch.bfloat16, 2.0 ** -8)])
+def test_gradient_of_saturated_sigmoid_scores(dtype, rounding):
+    rng = np.random.default_rng(1)
+    n, E, k = 60, 32, 4
+    logits = torch.from_numpy((3.0 + 77.0 * rng.random((n, E))).astype(np.float32)).to(dtype)
+    x = _f64(logits)
+    ids = torch.stack([torch.randperm(E)[:k] for _ in range(n)]).int()
+    g = rng.standard_normal((n, k)).astype(np.float32)
+    got = _f64(tq.tq_router_scored_backward(logits.cuda(), ids.cuda(), torch.ones(n, k, device="cuda"),
+                                            torch.from_numpy(g).cuda(), score=tq.SCORE_SIGMOID, renormalize=False))
+    check_no_device_error()
+    i = ids.numpy().astype(np.int64)
+    slope = np.exp(-x) / (1.0 + np.exp(-x)) ** 2
+    want = np.zeros((n, E))
+    np.put_along_axis(want, i, g * np.take_along_axis(slope, i, 1), 1)
+    assert (np.abs(got - want) <= (2.0 ** -19 + rounding) * np.abs(want)).all()
+    assert (got[want != 0] != 0).all()
+    p = np.take_along_axis(1.0 / (1.0 + np.exp(-x)), i, 1)
+    got = _f64(tq.tq_router_scored_backward(logits.cuda(), ids.cuda(), torch.ones(n, k, device="cuda"),
+                                            torch.from_numpy(g).cuda(), score=tq.SCORE_SIGMOID, renormalize=True))
+    q = p / p.sum(1, keepdims=True)
+    per = q * (1.0 / (1.0 + np.exp(np.take_along_axis(x, i, 1))))
+    want = np.zeros((n, E))
+    np.put_along_axis(want, i, per * (g - (g * q).sum(1, keepdims=True)), 1)
+    size = np.zeros((n, E))
+    np.put_along_axis(size, i, per * (np.abs(g) + np.abs(g * q).sum(1, keepdims=True)), 1)
+    assert (np.abs(got - want) <= 2.0 ** -19 * size + rounding * np.abs(want)).all()

@@ -379,7 +379,8 @@ router_scored_backward_kernel(const T* __restrict__ logits, long long stride, co
       load_row<T, PL>(row, E, lane, vec, x);
       softmax_terms<PL>(x, &top, &total);
     }
-    const float p = live ? one_score(widen(row[e]), score, top, total) : 0.f;
+    const float logit = live ? widen(row[e]) : -INFINITY;
+    const float p = one_score(logit, score, top, total);
     float own, dot = 0.f;
     if (renorm) {
       // q (g - sum_j g_j q_j) with q = p / sum: no step exceeds g, where g / sum
@@ -393,7 +394,8 @@ router_scored_backward_kernel(const T* __restrict__ logits, long long stride, co
     } else {
       own = g * p;
     }
-    if (score == TQ_SCORE_SIGMOID) own *= 1.f - p;
+    // 1 - p as p exp(-x): the difference loses its bits as p nears 1
+    if (score == TQ_SCORE_SIGMOID && p > 0.f) own *= p * expf(-logit);
     const float r = __frcp_rn(total);   // of a row without finite logits infinite, and its terms are 0
     T* const out = grad + static_cast<size_t>(t) * E;
     const int e0 = lane * PL;
