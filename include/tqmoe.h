@@ -510,7 +510,9 @@ int tq_router_scored_backward(const void* logits, int logits_type, int64_t logit
  *              pointer must be NULL).
  * Arithmetic is fp32; both roundings are to nearest even and saturate.  NaN is
  * kept as 0 and does not count for the maximum, an infinity counts as the
- * largest finite number.  Values of a block whose scale rounds to 0 are 0.
+ * largest finite number.  Values of a block whose scale rounds to 0 are 0.  A
+ * scale byte that is NaN (0x7f as E4M3, 0xff as E8M0; the quantiser writes none)
+ * makes the values of its block NaN.
  * global_scale, x_scale, h_scale (device) fp32 [1] or NULL; w_scale, gu_scale,
  * down_scale (device) fp32 [E] or NULL.
  *

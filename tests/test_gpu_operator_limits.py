@@ -104,6 +104,26 @@ def test_scales_far_apart(x_factor, w_factor, n):
 
 
 @pytest.mark.parametrize("n", [1, 300])
+def test_mx_scale_that_is_no_number(n):
+    """E8M0's byte 255 is NaN: all values of its block, and the outputs of its weight row alone."""
+    rng = np.random.default_rng(n)
+    N, K = 130, 512
+    w = Matrices(rng, 1, N, K, "mx")
+    byte = w.byte.copy()
+    byte[0, 77, 3] = 255
+    scales = torch.from_numpy(byte).cuda()
+    want = torch.zeros(N, K, dtype=torch.bool)
+    want[77, 96:128] = True
+    for dtype in (torch.float32, torch.bfloat16, torch.float16):
+        got = tq.tq_fp4_dequantize(w.packed[0], scales[0], tq.FP4_MX, dtype=dtype)
+        assert torch.equal(torch.isnan(got).cpu(), want) and torch.isfinite(got[~want.cuda()]).all()
+    y, few = _arms(lambda: tq.tq_fp4_linear(torch.randn(n, K, device="cuda"), w.packed[0],
+                                            tq.tq_fp4_tile_scales(scales, tq.FP4_MX), fmt=tq.FP4_MX))
+    assert few == (n == 1)
+    assert torch.isnan(y[:, 77]).all() and torch.isfinite(y[:, :77]).all() and torch.isfinite(y[:, 78:]).all()
+
+
+@pytest.mark.parametrize("n", [1, 300])
 def test_zeros_with_a_global_scale_of_zero(n):
     """amax / (6 * 448) of an all-zero tensor is 0: its values are 0, and so are its products."""
     N, K = 129, 512

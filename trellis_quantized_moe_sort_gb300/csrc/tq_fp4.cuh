@@ -60,9 +60,12 @@ __device__ __forceinline__ float from_e4m3(uint32_t byte) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(byte)));
   return __half2float(__ushort_as_half(static_cast<uint16_t>(h & 0xffffu)));
 }
-// 2^(byte - 127); byte 0 is the subnormal 2^-127.
+// 2^(byte - 127), byte 0 the subnormal 2^-127, byte 255 NaN; through bf16, which
+// has fp32's exponents.
 __device__ __forceinline__ float from_e8m0(uint32_t byte) {
-  return __uint_as_float(byte ? byte << 23 : 1u << 22);
+  uint32_t two;
+  asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(two) : "h"(static_cast<uint16_t>(byte)));
+  return __uint_as_float(two << 16);
 }
 template <int kFmt>
 __device__ __forceinline__ float fp4_scale_value(uint32_t byte) {
