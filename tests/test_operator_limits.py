@@ -1,0 +1,28 @@
+"""What the scored router and the 4-bit operators do at the ends of their
+arguments' ranges, and their binding apart from any device: no GPU is needed."""
+import pytest
+
+INVALID = -1
+A = 0x10000            # 256-byte aligned stand-in address, never dereferenced
+
+
+@pytest.fixture(scope="module")
+def tq():
+    from trellis_quantized_moe_sort_gb300 import build
+    build.build()
+    import trellis_quantized_moe_sort_gb300 as tq
+    return tq
+
+
+# n * top_k is 2^64 or a multiple of it for each of these, 0 in 64 bits
+@pytest.mark.parametrize("n,k", [(1 << 62, 4), (1 << 60, 16), (1 << 59, 32), (3 << 61, 8)])
+def test_pairs_that_wrap_are_refused(tq, n, k):
+    lib = tq.lib()
+    assert n * k % (1 << 64) == 0 and n < 1 << 63
+    assert lib.tq_router_scored(A, 0, 64, None, n, 64, k, 1, 1, 1, 1, 1.0, A, A, None) == INVALID
+    assert lib.tq_router_scored_backward(A, 0, 64, A, A, A, n, 64, k, 1, 1, 1.0, A, None) == INVALID
+    assert lib.tq_fp4_moe_workspace_size(n, k, 64, 64, 64, 0) == 0
+    assert lib.tq_fp4_moe_mlp_workspace_size(n, k, 64, 64, 64, 0) == 0
+    assert lib.tq_fp4_moe_forward(A, 1, 64, A, A, 0, None, None, A, A, n, k, 64, 64, 64, A, 1 << 30, A, 1, None) == INVALID
+    assert lib.tq_fp4_moe_mlp_forward(A, 1, 64, A, A, None, A, A, None, 0, None, None, A, A, n, k, 64, 64, 64, A, 1 << 30,
+                                      A, 1, None) == INVALID

@@ -161,7 +161,8 @@ Staged carve_staged(Carver& c, int64_t P, int64_t tiles, int tile_m, int K, int 
 }
 
 bool bad_moe_shape(int64_t n, int top_k, int E) {
-  return E < 1 || E > 1024 || top_k < 1 || top_k > E || top_k > 32 || n < 0 || n * top_k >= kMaxIndex;
+  return E < 1 || E > 1024 || top_k < 1 || top_k > E || top_k > 32 || n < 0 || n >= kMaxIndex ||
+         n * top_k >= kMaxIndex;
 }
 bool bad_matrix(int E, int K, int N) { return bad_k(K) || N < 1 || static_cast<int64_t>(E) * N >= kMaxIndex; }
 

@@ -491,8 +491,9 @@ int backward_typed(const RouterArgs& a, const void* logits, const int32_t* ids, 
 }
 
 bool bad_router_args(const RouterArgs& a, int type) {
-  return a.E < 1 || a.E > 1024 || a.top_k < 1 || a.top_k > 32 || a.top_k > a.E || a.n < 0 ||
-         a.n * a.top_k >= (static_cast<int64_t>(1) << 31) || a.stride < a.E || bad_type(type) ||
+  constexpr int64_t kMost = static_cast<int64_t>(1) << 31;
+  return a.E < 1 || a.E > 1024 || a.top_k < 1 || a.top_k > 32 || a.top_k > a.E || a.n < 0 || a.n >= kMost ||
+         a.n * a.top_k >= kMost || a.stride < a.E || bad_type(type) ||
          (a.score != TQ_SCORE_SOFTMAX && a.score != TQ_SCORE_SIGMOID);
 }
 
