@@ -26,3 +26,13 @@ def test_pairs_that_wrap_are_refused(tq, n, k):
     assert lib.tq_fp4_moe_forward(A, 1, 64, A, A, 0, None, None, A, A, n, k, 64, 64, 64, A, 1 << 30, A, 1, None) == INVALID
     assert lib.tq_fp4_moe_mlp_forward(A, 1, 64, A, A, None, A, A, None, 0, None, None, A, A, n, k, 64, 64, 64, A, 1 << 30,
                                       A, 1, None) == INVALID
+
+
+def test_values_that_wrap_are_refused(tq):
+    lib = tq.lib()
+    n = 1 << 59                # times 32 values of 4 bytes, 0 in 64 bits
+    assert lib.tq_fp4_quantize(A, 0, 32, n, 32, 0, None, A, A, None) == INVALID
+    assert lib.tq_fp4_dequantize(A, A, n, 32, 0, None, A, 0, None) == INVALID
+    # rows 2^62 elements apart: the second one's address wraps
+    assert lib.tq_fp4_quantize(A, 0, 1 << 62, 2, 32, 0, None, A, A, None) == INVALID
+    assert lib.tq_fp4_linear(A, 0, 1 << 62, A, A, 0, None, None, 2, 32, 32, None, 0, A, 0, None) == INVALID

@@ -166,12 +166,12 @@ bool bad_moe_shape(int64_t n, int top_k, int E) {
 }
 bool bad_matrix(int E, int K, int N) { return bad_k(K) || N < 1 || static_cast<int64_t>(E) * N >= kMaxIndex; }
 
-// Partial sums whose bytes, up to 8 splits of them, would not fit a size_t.
+// Values whose bytes, up to 8 splits of fp32 partial sums, would not fit a size_t.
 bool bad_output(int64_t rows, int64_t N) { return static_cast<double>(rows) * static_cast<double>(N) >= 0x1p58; }
 
 bool bad_rows(const void* x, int type, int64_t stride, int64_t n, int K) {
-  return bad_type(type) || stride < K || (stride * static_cast<int64_t>(type_size(type))) % 16 != 0 ||
-         (n > 0 && (!x || !aligned(x, 16)));
+  return bad_type(type) || stride < K || (stride % 16 * static_cast<int64_t>(type_size(type))) % 16 != 0 ||
+         (n > 1 && bad_output(n, stride)) || (n > 0 && (!x || !aligned(x, 16)));
 }
 
 struct MoePlan {
@@ -263,7 +263,8 @@ extern "C" {
 
 int tq_fp4_quantize(const void* x, int x_type, int64_t x_stride, int64_t n, int K, int fmt, const float* global_scale,
                     uint8_t* packed, uint8_t* scales, tq_stream_t stream) {
-  if (n < 0 || bad_k(K) || bad_format(fmt) || (fmt == TQ_FP4_MX && global_scale)) return TQ_ERR_INVALID_ARG;
+  if (n < 0 || bad_k(K) || bad_output(n, K) || bad_format(fmt) || (fmt == TQ_FP4_MX && global_scale))
+    return TQ_ERR_INVALID_ARG;
   if (bad_rows(x, x_type, x_stride, n, K)) return TQ_ERR_INVALID_ARG;
   if (n > 0 && (!packed || !scales || !aligned(packed, 8))) return TQ_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -274,7 +275,8 @@ int tq_fp4_quantize(const void* x, int x_type, int64_t x_stride, int64_t n, int 
 
 int tq_fp4_dequantize(const uint8_t* packed, const uint8_t* scales, int64_t n, int K, int fmt,
                       const float* global_scale, void* out, int out_type, tq_stream_t stream) {
-  if (n < 0 || bad_k(K) || bad_format(fmt) || bad_type(out_type) || (fmt == TQ_FP4_MX && global_scale))
+  if (n < 0 || bad_k(K) || bad_output(n, K) || bad_format(fmt) || bad_type(out_type) ||
+      (fmt == TQ_FP4_MX && global_scale))
     return TQ_ERR_INVALID_ARG;
   if (n > 0 && (!packed || !scales || !out || !aligned(packed, 8) || !aligned(out, 16))) return TQ_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

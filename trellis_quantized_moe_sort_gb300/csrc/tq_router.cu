@@ -431,7 +431,7 @@ int pieces(int E) {   // experts per lane
 
 // The stride and base keep every lane's 16-byte piece aligned.
 bool rows_aligned(const void* p, long long stride, size_t size) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (stride * static_cast<long long>(size)) % 16 == 0;
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (stride % 16 * static_cast<long long>(size)) % 16 == 0;
 }
 
 int router_blocks(int64_t n) {
