@@ -36,3 +36,16 @@ def test_values_that_wrap_are_refused(tq):
     # rows 2^62 elements apart: the second one's address wraps
     assert lib.tq_fp4_quantize(A, 0, 1 << 62, 2, 32, 0, None, A, A, None) == INVALID
     assert lib.tq_fp4_linear(A, 0, 1 << 62, A, A, 0, None, None, 2, 32, 32, None, 0, A, 0, None) == INVALID
+
+
+def test_longest_rows(tq):
+    """K up to the largest multiple of 32 that an int holds: sizes grow with it and do not wrap."""
+    longest = (1 << 31) - 32
+    for fmt, per in ((tq.FP4_NV, 2048), (tq.FP4_MX, 1024)):
+        assert tq.tq_fp4_tiled_scales_size(1, 1, longest, fmt) == (1 << 23) * per
+        assert tq.tq_fp4_tiled_scales_size(2, 129, longest, fmt) == 4 * (1 << 23) * per
+        for K in ((1 << 31) - 256, longest):
+            size = tq.lib().tq_fp4_linear_workspace_size(100, K, 1, fmt)
+            assert 100 * (K // 2) + -(-K // 256) * per <= size < 1 << 42
+            size = tq.lib().tq_fp4_moe_workspace_size(100, 1, 1, K, 1, fmt)
+            assert 100 * (K // 2) + -(-K // 256) * per <= size < 1 << 42

@@ -18,8 +18,8 @@ constexpr size_t kNoWorkspace = 256;   // reported where none is used; a null wo
 // Rows of pairs and of weights: 32-bit coordinates with room for a tile past the end.
 constexpr int64_t kMaxIndex = (static_cast<int64_t>(1) << 31) - 1024;
 
-// Rows of fp4 values: K a multiple of 32, and small enough that a row's bytes
-// fit the 32-bit coordinates of the copies.
+// Rows of fp4 values: K a multiple of 32.  (A row's K / 2 bytes of codes fit the
+// 32-bit coordinates of the copies.)
 bool bad_k(int K) { return K < 32 || K % 32 != 0; }
 
 // Rows per m-tile and K splits of a tensor-core product, by the time that the

@@ -27,7 +27,7 @@ __host__ __device__ constexpr int fp4_scale_step_bytes(int fmt) { return 128 * (
 // Tensor-memory columns of a step's scales: 4 a tile for the weights, 8 for up
 // to 256 activation rows.
 __host__ __device__ constexpr int fp4_scale_columns(int fmt) { return fp4_scale_step_bytes(fmt) / 512 * 12; }
-__host__ __device__ constexpr int fp4_steps(int K) { return (K + kFp4Step - 1) / kFp4Step; }
+__host__ __device__ constexpr int fp4_steps(int K) { return (K - 1) / kFp4Step + 1; }   // K >= 1, up to 2^31 - 1
 
 // Offset of block `b`'s scale of row `r` inside a tiled scale matrix of
 // 128-row groups with `steps` steps each.
