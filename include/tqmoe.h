@@ -526,7 +526,8 @@ int tq_router_scored_backward(const void* logits, int logits_type, int64_t logit
  *   block % 4), tiles of a group of 128 rows one after another along K, rows
  *   padded to 128 and K to 256 values with zeros.  scales (device) uint8
  *   [E][N][K / block] -> tiled (device), tq_fp4_tiled_scales_size() bytes (0
- *   on invalid arguments), 16-byte aligned.  Done once, when weights load.
+ *   on invalid arguments; E * N below 2^31 - 1024, as the products take),
+ *   16-byte aligned.  Done once, when weights load.
  * ------------------------------------------------------------------------- */
 enum tq_fp4_format { TQ_FP4_NV = 0, TQ_FP4_MX = 1 };
 int tq_fp4_quantize(const void* x, int x_type, int64_t x_stride, int64_t n, int K, int fmt,

@@ -49,3 +49,12 @@ def test_longest_rows(tq):
             assert 100 * (K // 2) + -(-K // 256) * per <= size < 1 << 42
             size = tq.lib().tq_fp4_moe_workspace_size(100, 1, 1, K, 1, fmt)
             assert 100 * (K // 2) + -(-K // 256) * per <= size < 1 << 42
+
+
+def test_scale_tiling_keeps_to_the_products_sizes(tq):
+    most = (1 << 31) - 1024
+    assert tq.tq_fp4_tiled_scales_size(1, most - 1, 32) == (1 << 24) * 2048 - 8 * 2048
+    for E, N in ((1, most), (1, (1 << 31) - 1), (1024, most // 1024 + 1), ((1 << 31) - 1, (1 << 31) - 1)):
+        assert tq.tq_fp4_tiled_scales_size(E, N, 32) == 0
+        assert tq.lib().tq_fp4_tile_scales(A, E, N, 32, 0, A, None) == INVALID
+    assert tq.tq_fp4_tiled_scales_size((1 << 31) - 1025, 1, (1 << 31) - 32) == 0     # bytes past a size_t

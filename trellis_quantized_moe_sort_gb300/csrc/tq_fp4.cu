@@ -286,7 +286,7 @@ int tq_fp4_dequantize(const uint8_t* packed, const uint8_t* scales, int64_t n, i
 }
 
 size_t tq_fp4_tiled_scales_size(int E, int N, int K, int fmt) {
-  if (E < 1 || N < 1 || bad_k(K) || bad_format(fmt)) return 0;
+  if (E < 1 || bad_matrix(E, K, N) || bad_output(static_cast<int64_t>(E) * (N + 127ll), K) || bad_format(fmt)) return 0;
   return static_cast<size_t>(E) * ((N + 127) / 128) * fp4_steps(K) * fp4_scale_step_bytes(fmt);
 }
 
