@@ -1,5 +1,9 @@
 """What the scored router and the 4-bit operators do at the ends of their
 arguments' ranges, and their binding apart from any device: no GPU is needed."""
+import os
+import subprocess
+import sys
+
 import pytest
 
 INVALID = -1
@@ -58,3 +62,36 @@ def test_scale_tiling_keeps_to_the_products_sizes(tq):
         assert tq.tq_fp4_tiled_scales_size(E, N, 32) == 0
         assert tq.lib().tq_fp4_tile_scales(A, E, N, 32, 0, A, None) == INVALID
     assert tq.tq_fp4_tiled_scales_size((1 << 31) - 1025, 1, (1 << 31) - 32) == 0     # bytes past a size_t
+
+
+def test_other_threads_run_during_a_short_call(tq):
+    """A wrapper of the binding bound to a function that sleeps for as many microseconds as its first argument says:
+    another thread gets on meanwhile."""
+    tq.lib()
+    if type(tq._call("tq_fp4_dequantize")).__name__ != "builtin_function_or_method":
+        pytest.skip("the calls go through ctypes")
+    program = """
+import ctypes, threading, time
+from trellis_quantized_moe_sort_gb300 import _tqcall
+usleep = ctypes.CDLL(None).usleep
+_tqcall.bind("tq_fp4_dequantize", ctypes.cast(usleep, ctypes.c_void_p).value)
+seen, stop = [], threading.Event()
+def tick():
+    while not stop.is_set():
+        seen.append(time.monotonic())
+        time.sleep(0.005)
+t = threading.Thread(target=tick)
+t.start()
+time.sleep(0.05)
+start = time.monotonic()
+_tqcall.tq_fp4_dequantize(500000, None, 0, 0, 0, None, None, 0, None)
+end = time.monotonic()
+stop.set()
+t.join()
+assert end - start >= 0.4, end - start
+print(sum(start + 0.1 < s < end - 0.1 for s in seen))
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(tq.__file__)))
+    r = subprocess.run([sys.executable, "-c", program], capture_output=True, text=True, cwd=root, timeout=120)
+    assert r.returncode == 0, r.stderr
+    assert int(r.stdout) > 0

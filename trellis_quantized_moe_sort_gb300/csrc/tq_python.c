@@ -3,6 +3,10 @@
  * null pointer).  Marshalling fifteen arguments through ctypes takes about
  * 1.5 us, nearly as long as the launch itself.
  *
+ * As ctypes does, a wrapper lets other Python threads run during the call: a
+ * launch can wait for room in the device's queue, or for a host callback that
+ * needs the interpreter.
+ *
  * bind(name, address) gives a function its address in the loaded libtqmoe.so;
  * the module links to nothing but Python. */
 #define PY_SSIZE_T_CLEAN
@@ -50,10 +54,14 @@ static int take(const char* sig, const void* fn, PyObject* const* a, Py_ssize_t 
   static PyObject* call_##name(PyObject* self, PyObject* const* a, Py_ssize_t n) {     \
     long long v[MAX_ARGS];                                                             \
     float f = 0.f;                                                                     \
+    int rc;                                                                            \
     (void)self;                                                                        \
     (void)f;                                                                           \
     if (!take(sig, (const void*)fn_##name, a, n, v, &f)) return NULL;                  \
-    return PyLong_FromLong(fn_##name(__VA_ARGS__));                                    \
+    Py_BEGIN_ALLOW_THREADS                                                             \
+    rc = fn_##name(__VA_ARGS__);                                                       \
+    Py_END_ALLOW_THREADS                                                               \
+    return PyLong_FromLong(rc);                                                        \
   }
 
 WRAPPER(tq_router_scored, "pilpliiiiiifppp", PTR(0), INT(1), v[2], PTR(3), v[4], INT(5), INT(6), INT(7), INT(8), INT(9),
