@@ -95,3 +95,30 @@ print(sum(start + 0.1 < s < end - 0.1 for s in seen))
     r = subprocess.run([sys.executable, "-c", program], capture_output=True, text=True, cwd=root, timeout=120)
     assert r.returncode == 0, r.stderr
     assert int(r.stdout) > 0
+
+
+def test_a_failing_compiler_leaves_the_calls_to_ctypes(tq, monkeypatch, tmp_path, capsys):
+    """The short calls are an extra: where gcc cannot build them the rest is built all the same, and no
+    earlier one stays in their place."""
+    import importlib.machinery
+    import types
+    from trellis_quantized_moe_sort_gb300 import build
+    if not build.python_include():
+        pytest.skip("no Python.h or no gcc")
+    assert os.path.basename(build.CALLS) == "_tqcall" + importlib.machinery.EXTENSION_SUFFIXES[0]
+    calls = tmp_path / os.path.basename(build.CALLS)
+    monkeypatch.setattr(build, "CALLS", str(calls))
+    assert build.build_calls(True) and calls.exists()
+    stamp = calls.stat().st_mtime_ns
+    assert build.build_calls() and calls.stat().st_mtime_ns == stamp      # nothing to do
+    ran = []
+
+    def run(cmd, **kwargs):
+        ran.append(cmd[0])
+        return types.SimpleNamespace(returncode=1, stdout="", stderr="no such file")
+
+    monkeypatch.setattr(build.subprocess, "run", run)
+    assert not build.build_calls(True) and not calls.exists() and ran == ["gcc"]
+    assert "ctypes" in capsys.readouterr().err
+    assert build.build() == build.LIB                                     # the library is up to date without them
+    assert "nvcc" not in " ".join(ran)

@@ -20,7 +20,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtqmoe.so")
-CALLS = os.path.join(HERE, "_tqcall.so")   # the binding's short calls (csrc/tq_python.c)
+# the binding's short calls (csrc/tq_python.c), by the interpreter that they are built for
+CALLS = os.path.join(HERE, "_tqcall" + sysconfig.get_config_var("EXT_SUFFIX"))
+CALLS_SOURCES = [os.path.join(CSRC, "tq_python.c"), os.path.join(INCLUDE, "tqmoe.h")]
 SOURCES = ["tq_host.cu", "tq_route.cu", "tq_grouped.cu", "tq_gemv.cu", "tq_noalloc.cu", "tq_probe.cu", "tq_mlp.cu", "tq_dequant.cu",
            "tq_router.cu", "tq_fp4_quant.cu", "tq_fp4_gemm.cu", "tq_fp4_gemv.cu", "tq_fp4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -42,14 +44,28 @@ def python_include() -> str:
     return path if os.path.exists(os.path.join(path, "Python.h")) and shutil.which("gcc") else ""
 
 
-def build_calls() -> None:
+def build_calls(force: bool = False) -> bool:
+    """Builds the binding's short calls; False, with none left in place, where that
+    cannot be done: the binding then calls through ctypes."""
+    include = python_include()
+    if include and not force and os.path.exists(CALLS):
+        t = os.path.getmtime(CALLS)
+        if all(os.path.getmtime(f) <= t for f in CALLS_SOURCES):
+            return True
+    # one of an earlier source, or without an interpreter's name, must not be imported in its place
+    for old in (CALLS, os.path.join(HERE, "_tqcall.so")):
+        if os.path.exists(old):
+            os.remove(old)
+    if not include:
+        return False
     tmp = CALLS + ".tmp"
-    cmd = ["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", python_include(), "-I", INCLUDE,
-           os.path.join(CSRC, "tq_python.c"), "-o", tmp]
+    cmd = ["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", include, "-I", INCLUDE, CALLS_SOURCES[0], "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"gcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+        sys.stderr.write(f"calls go through ctypes: gcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}\n")
+        return False
     os.replace(tmp, CALLS)
+    return True
 
 
 def _deps() -> list[str]:
@@ -60,13 +76,14 @@ def _deps() -> list[str]:
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or (python_include() and not os.path.exists(CALLS)):
+    if not os.path.exists(LIB):
         return False
     t = os.path.getmtime(LIB)
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_calls(force)
     if not force and up_to_date():
         return LIB
     home = cuda_home()
@@ -87,8 +104,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    if python_include():
-        build_calls()
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
     tmp = LIB + ".tmp"
