@@ -122,3 +122,78 @@ def test_a_failing_compiler_leaves_the_calls_to_ctypes(tq, monkeypatch, tmp_path
     assert "ctypes" in capsys.readouterr().err
     assert build.build() == build.LIB                                     # the library is up to date without them
     assert "nvcc" not in " ".join(ran)
+
+
+class _OnDevice:
+    """What the binding asks of a tensor on CUDA device `device`."""
+    is_cuda = True
+
+    def __init__(self, dtype, *shape, device=0):
+        import torch
+        self.dtype, self.shape, self._device = dtype, torch.Size(shape), device
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return A
+
+    def get_device(self):
+        return self._device
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+
+def test_tensors_of_another_device_are_refused(tq, monkeypatch):
+    """Device 0 is current: a call with any one of its tensors on device 1 is refused before the library is called."""
+    import torch
+    f32, i32, u8 = torch.float32, torch.int32, torch.uint8
+    for name, value in (("_torch_mod", torch), ("_common", None), ("_type_codes", None), ("_raw_stream_fn", lambda: 0)):
+        monkeypatch.setattr(tq, name, value)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    called = []
+    monkeypatch.setattr(tq, "_calls", {name: (lambda *a, name=name: called.append(name) or 0) for name in tq._CALLS})
+    monkeypatch.setattr(tq.lib(), "tq_fp4_tile_scales", lambda *a: called.append("tq_fp4_tile_scales") or 0)
+    n, E, k, K, N = 4, 8, 2, 64, 96
+
+    def rows(v):
+        return -(-v // 128) * 128
+
+    weights = lambda e, r, c: dict(packed=(u8, e, r, c // 2), tiled=(u8, e * rows(r) * (-(-c // 256) * 256 // 16)))
+    t = lambda dtype, *shape: (dtype, *shape)
+    calls = {
+        "router": (lambda a: tq.tq_router_scored(a["x"], k, bias=a["bias"], topk_ids=a["ids"], topk_w=a["w"]),
+                   dict(x=t(f32, n, E), bias=t(f32, E), ids=t(i32, n, k), w=t(f32, n, k))),
+        "router backward": (lambda a: tq.tq_router_scored_backward(a["x"], a["ids"], a["w"], a["g"], grad_logits=a["out"]),
+                            dict(x=t(f32, n, E), ids=t(i32, n, k), w=t(f32, n, k), g=t(f32, n, k), out=t(f32, n, E))),
+        "quantize": (lambda a: tq.tq_fp4_quantize(a["x"], tq.FP4_NV, a["g"], a["packed"], a["scales"]),
+                     dict(x=t(f32, n, K), g=t(f32, 1), packed=t(u8, n, K // 2), scales=t(u8, n, K // 16))),
+        "dequantize": (lambda a: tq.tq_fp4_dequantize(a["packed"], a["scales"], tq.FP4_NV, a["g"], out=a["out"]),
+                       dict(packed=t(u8, n, K // 2), scales=t(u8, n, K // 16), g=t(f32, 1), out=t(f32, n, K))),
+        "tile scales": (lambda a: tq.tq_fp4_tile_scales(a["scales"], tq.FP4_NV, a["tiled"]),
+                        dict(scales=t(u8, N, K // 16), tiled=t(u8, 128 * 16))),
+        "linear": (lambda a: tq.tq_fp4_linear(a["x"], a["packed"], a["tiled"], tq.FP4_NV, a["ws"], a["xs"], a["work"], a["y"]),
+                   dict(x=t(f32, n, K), **weights(1, N, K), ws=t(f32, 1), xs=t(f32, 1), work=t(u8, 1 << 20), y=t(f32, n, N))),
+        "experts": (lambda a: tq.tq_fp4_moe_forward(a["x"], a["packed"], a["tiled"], a["ids"], a["w"], tq.FP4_NV, a["ws"],
+                                                    a["xs"], a["work"], a["y"]),
+                    dict(x=t(f32, n, K), **weights(E, N, K), ids=t(i32, n, k), w=t(f32, n, k), ws=t(f32, E), xs=t(f32, 1),
+                         work=t(u8, 1 << 20), y=t(f32, n, N))),
+        "mlp": (lambda a: tq.tq_fp4_moe_mlp_forward(a["x"], a["gu"], a["gut"], a["packed"], a["tiled"], a["ids"], a["w"],
+                                                    tq.FP4_NV, a["gs"], a["ds"], a["xs"], a["hs"], a["work"], a["y"]),
+                dict(x=t(f32, n, K), gu=t(u8, E, 2 * N, K // 2), gut=t(u8, E * rows(2 * N) * 16), **weights(E, K, N),
+                     ids=t(i32, n, k), w=t(f32, n, k), gs=t(f32, E), ds=t(f32, E), xs=t(f32, 1), hs=t(f32, 1),
+                     work=t(u8, 1 << 20), y=t(f32, n, K))),
+    }
+    for what, (call, args) in calls.items():
+        make = lambda other: {name: _OnDevice(*spec, device=int(name == other)) for name, spec in args.items()}
+        call(make(None))
+        assert len(called) == 1, what
+        called.clear()
+        for name in args:
+            with pytest.raises(ValueError, match="cuda:1"):
+                call(make(name))
+            assert not called, (what, name)

@@ -671,30 +671,45 @@ def _type_code(dtype, name):
     return code
 
 
+def _check_device(t, device, name):
+    """The kernels run on one device: every tensor of a call has to be there."""
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the call runs on cuda:{device}")
+
+
 def _rows(t, name):
-    """(address, type code, elements between rows, rows, elements) of a 2-D CUDA
-    tensor with contiguous rows."""
+    """(address, type code, elements between rows, rows, elements, device) of a 2-D
+    tensor with contiguous rows on the current CUDA device."""
     try:
         code = _type_code(t.dtype, name)
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
+        device = _torch().cuda.current_device()
+        _check_device(t, device, name)
         shape = t.shape
         if len(shape) != 2:
             raise ValueError(f"{name} must have two dimensions, not {len(shape)}")
         n, width = shape
         if t.is_contiguous():
-            return t.data_ptr(), code, width, n, width
+            return t.data_ptr(), code, width, n, width, device
         step, inner = t.stride()
     except AttributeError:
         raise TypeError(f"{name} must be a torch.Tensor") from None
     if inner != 1 and width > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), code, step if n > 1 else width, n, width
+    return t.data_ptr(), code, step if n > 1 else width, n, width, device
 
 
-def _given(t, shape, dtypes, name):
-    """Address of an argument of a known shape: a contiguous CUDA tensor."""
+def _there(t, dtypes, name, device):
+    """Address of a contiguous tensor of one of `dtypes` on the device."""
     ptr = _dev_ptr(t, dtypes, name)
+    _check_device(t, device, name)
+    return ptr
+
+
+def _given(t, shape, dtypes, name, device):
+    """Address of an argument of a known shape: a contiguous tensor on the device."""
+    ptr = _there(t, dtypes, name, device)
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return ptr
@@ -712,11 +727,11 @@ def _types():
     return _common
 
 
-def _scale_ptr(t, count, name):
+def _scale_ptr(t, count, name, device):
     """Address of `count` fp32 scales, or None."""
     if t is None:
         return None
-    ptr = _dev_ptr(t, _types()[1], name)
+    ptr = _there(t, _types()[1], name, device)
     if t.numel() != count:
         raise ValueError(f"{name} has {t.numel()} values, expected {count}")
     return ptr
@@ -744,19 +759,19 @@ def tq_router_scored(logits, top_k: int, score: int = SCORE_SIGMOID, bias=None, 
     `renormalize`, times `scale`.  A non-finite logit masks its expert; a row
     with none left has weights 0."""
     torch, fp32, int32, _ = _types()
-    ptr, code, step, n, E = _rows(logits, "logits")
+    ptr, code, step, n, E, device = _rows(logits, "logits")
     if topk_ids is None:
         topk_ids = _empty((n, top_k), torch.int32, logits.device, stream)
         ids_ptr = topk_ids.data_ptr()
     else:
-        ids_ptr = _given(topk_ids, (n, top_k), int32, "topk_ids")
+        ids_ptr = _given(topk_ids, (n, top_k), int32, "topk_ids", device)
     if topk_w is None:
         topk_w = _empty((n, top_k), torch.float32, logits.device, stream)
         w_ptr = topk_w.data_ptr()
     else:
-        w_ptr = _given(topk_w, (n, top_k), fp32, "topk_w")
-    rc = _call("tq_router_scored")(ptr, code, step, _scale_ptr(bias, E, "bias"), n, E, top_k, score, groups, top_groups,
-                                   1 if renormalize else 0, scale, ids_ptr, w_ptr, _stream(stream))
+        w_ptr = _given(topk_w, (n, top_k), fp32, "topk_w", device)
+    rc = _call("tq_router_scored")(ptr, code, step, _scale_ptr(bias, E, "bias", device), n, E, top_k, score, groups,
+                                   top_groups, 1 if renormalize else 0, scale, ids_ptr, w_ptr, _stream(stream))
     if rc:
         raise TQError(rc, "tq_router_scored")
     return topk_ids, topk_w
@@ -768,17 +783,17 @@ def tq_router_scored_backward(logits, topk_ids, topk_w, grad_w, score: int = SCO
     the logits' dtype; topk_ids, topk_w and the options are those of the
     forward call."""
     torch, fp32, int32, _ = _types()
-    ptr, code, step, n, E = _rows(logits, "logits")
+    ptr, code, step, n, E, device = _rows(logits, "logits")
     shape = (n, topk_ids.shape[1])
     if grad_logits is None:
         grad_logits = _empty((n, E), logits.dtype, logits.device, stream)
         out = grad_logits.data_ptr()
     else:
-        out = _given(grad_logits, (n, E), (logits.dtype,), "grad_logits")
+        out = _given(grad_logits, (n, E), (logits.dtype,), "grad_logits", device)
     rc = _call("tq_router_scored_backward")(
-        ptr, code, step, _given(topk_ids, shape, int32, "topk_ids"), _given(topk_w, shape, fp32, "topk_w"),
-        _given(grad_w, shape, fp32, "grad_w"), n, E, shape[1], score, 1 if renormalize else 0, scale, out,
-        _stream(stream))
+        ptr, code, step, _given(topk_ids, shape, int32, "topk_ids", device),
+        _given(topk_w, shape, fp32, "topk_w", device), _given(grad_w, shape, fp32, "grad_w", device), n, E, shape[1],
+        score, 1 if renormalize else 0, scale, out, _stream(stream))
     if rc:
         raise TQError(rc, "tq_router_scored_backward")
     return grad_logits
@@ -796,20 +811,20 @@ def tq_fp4_quantize(x, fmt: int = FP4_NV, global_scale=None, packed=None, scales
     FP4_NV or [n, K/32] for FP4_MX).  global_scale: fp32 [1] on the device
     (FP4_NV only)."""
     torch, _, _, uint8 = _types()
-    ptr, code, step, n, K = _rows(x, "x")
+    ptr, code, step, n, K, device = _rows(x, "x")
     kb = K // _fp4_block(fmt)
     if packed is None:
         packed = _empty((n, K // 2), torch.uint8, x.device, stream)
         p_ptr = packed.data_ptr()
     else:
-        p_ptr = _given(packed, (n, K // 2), uint8, "packed")
+        p_ptr = _given(packed, (n, K // 2), uint8, "packed", device)
     if scales is None:
         scales = _empty((n, kb), torch.uint8, x.device, stream)
         s_ptr = scales.data_ptr()
     else:
-        s_ptr = _given(scales, (n, kb), uint8, "scales")
-    rc = _call("tq_fp4_quantize")(ptr, code, step, n, K, fmt, _scale_ptr(global_scale, 1, "global_scale"), p_ptr, s_ptr,
-                                  _stream(stream))
+        s_ptr = _given(scales, (n, kb), uint8, "scales", device)
+    rc = _call("tq_fp4_quantize")(ptr, code, step, n, K, fmt, _scale_ptr(global_scale, 1, "global_scale", device),
+                                  p_ptr, s_ptr, _stream(stream))
     if rc:
         raise TQError(rc, "tq_fp4_quantize")
     return packed, scales
@@ -819,7 +834,8 @@ def tq_fp4_dequantize(packed, scales, fmt: int = FP4_NV, global_scale=None, dtyp
     """The values of tq_fp4_quantize's output, [..., K] of `dtype` (fp32 when
     neither it nor `out` is given)."""
     torch, _, _, uint8 = _types()
-    p_ptr, s_ptr = _dev_ptr(packed, uint8, "packed"), _dev_ptr(scales, uint8, "scales")
+    device = torch.cuda.current_device()
+    p_ptr, s_ptr = _there(packed, uint8, "packed", device), _there(scales, uint8, "scales", device)
     K = 2 * packed.shape[-1]
     n = packed.numel() // max(K // 2, 1)
     if scales.numel() != n * (K // _fp4_block(fmt)):
@@ -831,8 +847,8 @@ def tq_fp4_dequantize(packed, scales, fmt: int = FP4_NV, global_scale=None, dtyp
     else:
         if dtype is not None and out.dtype != dtype:
             raise TypeError(f"out has dtype {out.dtype}, not {dtype}")
-        o_ptr = _given(out, shape, (), "out")
-    rc = _call("tq_fp4_dequantize")(p_ptr, s_ptr, n, K, fmt, _scale_ptr(global_scale, 1, "global_scale"), o_ptr,
+        o_ptr = _given(out, shape, (), "out", device)
+    rc = _call("tq_fp4_dequantize")(p_ptr, s_ptr, n, K, fmt, _scale_ptr(global_scale, 1, "global_scale", device), o_ptr,
                                     _type_code(out.dtype, "out"), _stream(stream))
     if rc:
         raise TQError(rc, "tq_fp4_dequantize")
@@ -853,19 +869,21 @@ def tq_fp4_tile_scales(scales, fmt: int = FP4_NV, tiled=None, stream=None):
     tiled = _empty(size, torch.uint8, scales.device, stream) if tiled is None else tiled
     if tiled.numel() != size:
         raise ValueError(f"tiled has {tiled.numel()} bytes, expected {size}")
-    _check(lib().tq_fp4_tile_scales(_dev_ptr(scales, (torch.uint8,), "scales"), E, N, K, fmt,
-                                    _dev_ptr(tiled, (torch.uint8,), "tiled"), _stream(stream)), "tq_fp4_tile_scales")
+    device = torch.cuda.current_device()
+    _check(lib().tq_fp4_tile_scales(_there(scales, (torch.uint8,), "scales", device), E, N, K, fmt,
+                                    _there(tiled, (torch.uint8,), "tiled", device), _stream(stream)),
+           "tq_fp4_tile_scales")
     return tiled
 
 
-def _fp4_matrix(packed, tiled_scales, E, N, K, fmt, name):
+def _fp4_matrix(packed, tiled_scales, E, N, K, fmt, name, device):
     """Addresses of a 4-bit weight matrix (or E of them), sizes checked."""
     uint8 = _types()[3]
     if packed.shape[-1] != K // 2 or packed.shape[-2] != N or packed.numel() != E * N * (K // 2):
         raise ValueError(f"{name} has shape {tuple(packed.shape)}, expected {(E, N, K // 2)}")
     if tiled_scales.numel() != E * (-(-N // 128) * 128) * (-(-K // 256) * 256 // _fp4_block(fmt)):
         raise ValueError(f"the scales of {name} are not the tiled layout of {E} x {N} x {K}")
-    return _dev_ptr(packed, uint8, name), _dev_ptr(tiled_scales, uint8, "tiled scales")
+    return _there(packed, uint8, name, device), _there(tiled_scales, uint8, "tiled scales", device)
 
 
 def _workspace(workspace, size, device, stream, *args):
@@ -879,15 +897,15 @@ def _workspace(workspace, size, device, stream, *args):
             return None, 0, None
         workspace = _empty(need, torch.uint8, device, stream)
         return workspace.data_ptr(), need, workspace
-    return _dev_ptr(workspace, uint8, "workspace"), workspace.numel(), workspace
+    return _there(workspace, uint8, "workspace", device), workspace.numel(), workspace
 
 
-def _output(y, shape, x, stream):
+def _output(y, shape, x, stream, device):
     """(y, address, type code): the caller's, or a new one in x's dtype."""
     if y is None:
         y = _empty(shape, x.dtype, x.device, stream)
         return y, y.data_ptr(), _type_code(y.dtype, "y")
-    return y, _given(y, shape, (), "y"), _type_code(y.dtype, "y")
+    return y, _given(y, shape, (), "y", device), _type_code(y.dtype, "y")
 
 
 @functools.lru_cache(maxsize=4096)
@@ -900,13 +918,13 @@ def tq_fp4_linear(x, packed, tiled_scales, fmt: int = FP4_NV, w_scale=None, x_sc
     """x [n, K], quantised by the call, times a 4-bit matrix packed [N, K/2]
     with tiled_scales (tq_fp4_tile_scales) -> y [n, N] in x's dtype (or y's).
     w_scale, x_scale: fp32 [1] global scales (FP4_NV)."""
-    ptr, code, step, n, K = _rows(x, "x")
+    ptr, code, step, n, K, device = _rows(x, "x")
     N = packed.shape[-2]
-    w_ptr, s_ptr = _fp4_matrix(packed, tiled_scales, 1, N, K, fmt, "packed")
-    ws_ptr, ws_bytes, workspace = _workspace(workspace, tq_fp4_linear_workspace_size, x.device, stream, n, K, N, fmt)
-    y, y_ptr, y_code = _output(y, (n, N), x, stream)
-    rc = _call("tq_fp4_linear")(ptr, code, step, w_ptr, s_ptr, fmt, _scale_ptr(w_scale, 1, "w_scale"),
-                                _scale_ptr(x_scale, 1, "x_scale"), n, K, N, ws_ptr, ws_bytes, y_ptr, y_code,
+    w_ptr, s_ptr = _fp4_matrix(packed, tiled_scales, 1, N, K, fmt, "packed", device)
+    ws_ptr, ws_bytes, workspace = _workspace(workspace, tq_fp4_linear_workspace_size, device, stream, n, K, N, fmt)
+    y, y_ptr, y_code = _output(y, (n, N), x, stream, device)
+    rc = _call("tq_fp4_linear")(ptr, code, step, w_ptr, s_ptr, fmt, _scale_ptr(w_scale, 1, "w_scale", device),
+                                _scale_ptr(x_scale, 1, "x_scale", device), n, K, N, ws_ptr, ws_bytes, y_ptr, y_code,
                                 _stream(stream))
     if rc:
         raise TQError(rc, "tq_fp4_linear")
@@ -925,17 +943,18 @@ def tq_fp4_moe_forward(x, packed, tiled_scales, topk_ids, topk_w, fmt: int = FP4
     y[t] = sum_j topk_w[t, j] * W_{topk_ids[t, j]} x[t].  w_scale fp32 [E],
     x_scale fp32 [1]: global scales (FP4_NV)."""
     _, fp32, int32, _ = _types()
-    ptr, code, step, n, K = _rows(x, "x")
+    ptr, code, step, n, K, device = _rows(x, "x")
     E, N, _ = packed.shape
     top_k = topk_ids.shape[1]
-    w_ptr, s_ptr = _fp4_matrix(packed, tiled_scales, E, N, K, fmt, "packed")
-    ws_ptr, ws_bytes, workspace = _workspace(workspace, tq_fp4_moe_workspace_size, x.device, stream, n, top_k, E, K, N,
-                                               fmt)
-    y, y_ptr, y_code = _output(y, (n, N), x, stream)
-    rc = _call("tq_fp4_moe_forward")(ptr, code, step, w_ptr, s_ptr, fmt, _scale_ptr(w_scale, E, "w_scale"),
-                                     _scale_ptr(x_scale, 1, "x_scale"), _given(topk_ids, (n, top_k), int32, "topk_ids"),
-                                     _given(topk_w, (n, top_k), fp32, "topk_w"), n, top_k, E, K, N, ws_ptr, ws_bytes,
-                                     y_ptr, y_code, _stream(stream))
+    w_ptr, s_ptr = _fp4_matrix(packed, tiled_scales, E, N, K, fmt, "packed", device)
+    ws_ptr, ws_bytes, workspace = _workspace(workspace, tq_fp4_moe_workspace_size, device, stream, n, top_k, E, K, N,
+                                             fmt)
+    y, y_ptr, y_code = _output(y, (n, N), x, stream, device)
+    rc = _call("tq_fp4_moe_forward")(ptr, code, step, w_ptr, s_ptr, fmt, _scale_ptr(w_scale, E, "w_scale", device),
+                                     _scale_ptr(x_scale, 1, "x_scale", device),
+                                     _given(topk_ids, (n, top_k), int32, "topk_ids", device),
+                                     _given(topk_w, (n, top_k), fp32, "topk_w", device), n, top_k, E, K, N, ws_ptr,
+                                     ws_bytes, y_ptr, y_code, _stream(stream))
     if rc:
         raise TQError(rc, "tq_fp4_moe_forward")
     return y
@@ -954,19 +973,19 @@ def tq_fp4_moe_mlp_forward(x, packed_gu, tiled_gu, packed_down, tiled_down, topk
     gu_scale, down_scale fp32 [E]; x_scale, h_scale fp32 [1], the global scales
     of x and of h = silu(gate) * up (FP4_NV)."""
     _, fp32, int32, _ = _types()
-    ptr, code, step, n, H = _rows(x, "x")
+    ptr, code, step, n, H, device = _rows(x, "x")
     E, I = packed_gu.shape[0], packed_gu.shape[1] // 2
     top_k = topk_ids.shape[1]
-    gu_ptr, gus_ptr = _fp4_matrix(packed_gu, tiled_gu, E, 2 * I, H, fmt, "packed_gu")
-    d_ptr, ds_ptr = _fp4_matrix(packed_down, tiled_down, E, H, I, fmt, "packed_down")
-    ws_ptr, ws_bytes, workspace = _workspace(workspace, tq_fp4_moe_mlp_workspace_size, x.device, stream, n, top_k, E, H, I,
-                                               fmt)
-    y, y_ptr, y_code = _output(y, (n, H), x, stream)
+    gu_ptr, gus_ptr = _fp4_matrix(packed_gu, tiled_gu, E, 2 * I, H, fmt, "packed_gu", device)
+    d_ptr, ds_ptr = _fp4_matrix(packed_down, tiled_down, E, H, I, fmt, "packed_down", device)
+    ws_ptr, ws_bytes, workspace = _workspace(workspace, tq_fp4_moe_mlp_workspace_size, device, stream, n, top_k, E, H,
+                                             I, fmt)
+    y, y_ptr, y_code = _output(y, (n, H), x, stream, device)
     rc = _call("tq_fp4_moe_mlp_forward")(
-        ptr, code, step, gu_ptr, gus_ptr, _scale_ptr(gu_scale, E, "gu_scale"), d_ptr, ds_ptr,
-        _scale_ptr(down_scale, E, "down_scale"), fmt, _scale_ptr(x_scale, 1, "x_scale"),
-        _scale_ptr(h_scale, 1, "h_scale"), _given(topk_ids, (n, top_k), int32, "topk_ids"),
-        _given(topk_w, (n, top_k), fp32, "topk_w"), n, top_k, E, H, I, ws_ptr, ws_bytes, y_ptr, y_code,
+        ptr, code, step, gu_ptr, gus_ptr, _scale_ptr(gu_scale, E, "gu_scale", device), d_ptr, ds_ptr,
+        _scale_ptr(down_scale, E, "down_scale", device), fmt, _scale_ptr(x_scale, 1, "x_scale", device),
+        _scale_ptr(h_scale, 1, "h_scale", device), _given(topk_ids, (n, top_k), int32, "topk_ids", device),
+        _given(topk_w, (n, top_k), fp32, "topk_w", device), n, top_k, E, H, I, ws_ptr, ws_bytes, y_ptr, y_code,
         _stream(stream))
     if rc:
         raise TQError(rc, "tq_fp4_moe_mlp_forward")
