@@ -197,3 +197,24 @@ def test_tensors_of_another_device_are_refused(tq, monkeypatch):
             with pytest.raises(ValueError, match="cuda:1"):
                 call(make(name))
             assert not called, (what, name)
+
+
+def test_workspace_sizes_follow_the_device(tq, monkeypatch, request):
+    """The library's answer depends on the current device: the sizes are asked anew, and a call keeps them by device."""
+    import torch
+    request.addfinalizer(tq._workspace_bytes.cache_clear)     # of the sizes made up here
+    current = [0]
+    sizes = {0: 4096, 1: 8192}
+    monkeypatch.setattr(tq, "_torch_mod", torch)
+    monkeypatch.setattr(tq, "_common", None)
+    for name, args in (("tq_fp4_linear_workspace_size", (300, 96, 33)), ("tq_fp4_moe_workspace_size", (300, 2, 8, 96, 33)),
+                       ("tq_fp4_moe_mlp_workspace_size", (300, 2, 8, 96, 32))):
+        monkeypatch.setattr(tq.lib(), name, lambda *a: sizes[current[0]])
+        made = []
+        monkeypatch.setattr(tq, "_empty", lambda n, dtype, device, stream: made.append((n, device)) or torch.empty(n, dtype=dtype))
+        size = getattr(tq, name)
+        for device in (0, 1, 0):
+            current[0] = device
+            assert size(*args) == sizes[device], name
+            assert tq._workspace(None, size, device, None, *args, tq.FP4_NV)[1] == sizes[device], name
+        assert made == [(4096, 0), (8192, 1), (4096, 0)]

@@ -886,13 +886,19 @@ def _fp4_matrix(packed, tiled_scales, E, N, K, fmt, name, device):
     return _there(packed, uint8, name, device), _there(tiled_scales, uint8, "tiled scales", device)
 
 
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(size, device, *args):
+    """size(*args), which depends on the device's SM count too; `device` is the current one."""
+    return size(*args)
+
+
 def _workspace(workspace, size, device, stream, *args):
     """(address, bytes) of the caller's workspace, or of a new one of
     size(*args) bytes (none where the call needs none), and the tensor, to be
     kept until the call is enqueued."""
     torch, _, _, uint8 = _types()
     if workspace is None:
-        need = size(*args)
+        need = _workspace_bytes(size, device, *args)
         if need <= 256:
             return None, 0, None
         workspace = _empty(need, torch.uint8, device, stream)
@@ -908,7 +914,6 @@ def _output(y, shape, x, stream, device):
     return y, _given(y, shape, (), "y", device), _type_code(y.dtype, "y")
 
 
-@functools.lru_cache(maxsize=4096)
 def tq_fp4_linear_workspace_size(n: int, K: int, N: int, fmt: int = FP4_NV) -> int:
     return lib().tq_fp4_linear_workspace_size(n, K, N, fmt)
 
@@ -931,7 +936,6 @@ def tq_fp4_linear(x, packed, tiled_scales, fmt: int = FP4_NV, w_scale=None, x_sc
     return y
 
 
-@functools.lru_cache(maxsize=4096)
 def tq_fp4_moe_workspace_size(n: int, top_k: int, E: int, K: int, N: int, fmt: int = FP4_NV) -> int:
     return lib().tq_fp4_moe_workspace_size(n, top_k, E, K, N, fmt)
 
@@ -960,7 +964,6 @@ def tq_fp4_moe_forward(x, packed, tiled_scales, topk_ids, topk_w, fmt: int = FP4
     return y
 
 
-@functools.lru_cache(maxsize=4096)
 def tq_fp4_moe_mlp_workspace_size(n: int, top_k: int, E: int, H: int, I: int, fmt: int = FP4_NV) -> int:
     return lib().tq_fp4_moe_mlp_workspace_size(n, top_k, E, H, I, fmt)
 
