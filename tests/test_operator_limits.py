@@ -152,7 +152,7 @@ def test_tensors_of_another_device_are_refused(tq, monkeypatch):
     """Device 0 is current: a call with any one of its tensors on device 1 is refused before the library is called."""
     import torch
     f32, i32, u8 = torch.float32, torch.int32, torch.uint8
-    for name, value in (("_torch_mod", torch), ("_common", None), ("_type_codes", None), ("_raw_stream_fn", lambda: 0)):
+    for name, value in (("_torch_mod", torch), ("_common", None), ("_type_codes", None), ("_raw_stream_fn", lambda device: 0)):
         monkeypatch.setattr(tq, name, value)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     called = []

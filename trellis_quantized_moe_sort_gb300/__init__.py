@@ -204,16 +204,12 @@ def _dev_ptr(t, dtypes, name):
     return t.data_ptr()
 
 
-def _current_stream_fast():
-    """Raw handle of torch's current stream on the current device."""
-    torch = _torch()
-    return torch.cuda.current_stream().cuda_stream
-
-
 _raw_stream_fn = None
 
 
-def _stream(stream):
+def _stream(stream, device=None):
+    """Raw handle of the given stream, or of torch's current one on the device
+    (by default the current one)."""
     global _raw_stream_fn
     if stream is not None:
         return stream.cuda_stream
@@ -221,10 +217,9 @@ def _stream(stream):
     if _raw_stream_fn is None:
         # the C-level getter of torch's current stream (a plain integer), when
         # this torch build has it; else the public (slower) route
-        getter = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        _raw_stream_fn = ((lambda: getter(torch.cuda.current_device())) if getter is not None
-                          else _current_stream_fast)
-    return _raw_stream_fn()
+        _raw_stream_fn = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _raw_stream_fn(torch.cuda.current_device() if device is None else device)
 
 
 _bits16_types = None
@@ -671,10 +666,10 @@ def _type_code(dtype, name):
     return code
 
 
-def _check_device(t, device, name):
-    """The kernels run on one device: every tensor of a call has to be there."""
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the call runs on cuda:{device}")
+def _elsewhere(t, device, name):
+    """The kernels run on the current device: every tensor of a call has to be there."""
+    return ValueError(f"{name} is on cuda:{t.get_device()}, the call runs on cuda:{device}" if t.is_cuda
+                      else f"{name} must be a CUDA tensor")
 
 
 def _rows(t, name):
@@ -682,10 +677,9 @@ def _rows(t, name):
     tensor with contiguous rows on the current CUDA device."""
     try:
         code = _type_code(t.dtype, name)
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
         device = _torch().cuda.current_device()
-        _check_device(t, device, name)
+        if t.get_device() != device:
+            raise _elsewhere(t, device, name)
         shape = t.shape
         if len(shape) != 2:
             raise ValueError(f"{name} must have two dimensions, not {len(shape)}")
@@ -702,9 +696,13 @@ def _rows(t, name):
 
 def _there(t, dtypes, name, device):
     """Address of a contiguous tensor of one of `dtypes` on the device."""
-    ptr = _dev_ptr(t, dtypes, name)
-    _check_device(t, device, name)
-    return ptr
+    try:
+        if t.get_device() == device and (not dtypes or t.dtype in dtypes) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev_ptr(t, dtypes, name)     # raises, unless the device is all that is wrong
+    raise _elsewhere(t, device, name)
 
 
 def _given(t, shape, dtypes, name, device):
@@ -771,7 +769,7 @@ def tq_router_scored(logits, top_k: int, score: int = SCORE_SIGMOID, bias=None, 
     else:
         w_ptr = _given(topk_w, (n, top_k), fp32, "topk_w", device)
     rc = _call("tq_router_scored")(ptr, code, step, _scale_ptr(bias, E, "bias", device), n, E, top_k, score, groups,
-                                   top_groups, 1 if renormalize else 0, scale, ids_ptr, w_ptr, _stream(stream))
+                                   top_groups, 1 if renormalize else 0, scale, ids_ptr, w_ptr, _stream(stream, device))
     if rc:
         raise TQError(rc, "tq_router_scored")
     return topk_ids, topk_w
@@ -793,7 +791,7 @@ def tq_router_scored_backward(logits, topk_ids, topk_w, grad_w, score: int = SCO
     rc = _call("tq_router_scored_backward")(
         ptr, code, step, _given(topk_ids, shape, int32, "topk_ids", device),
         _given(topk_w, shape, fp32, "topk_w", device), _given(grad_w, shape, fp32, "grad_w", device), n, E, shape[1],
-        score, 1 if renormalize else 0, scale, out, _stream(stream))
+        score, 1 if renormalize else 0, scale, out, _stream(stream, device))
     if rc:
         raise TQError(rc, "tq_router_scored_backward")
     return grad_logits
@@ -824,7 +822,7 @@ def tq_fp4_quantize(x, fmt: int = FP4_NV, global_scale=None, packed=None, scales
     else:
         s_ptr = _given(scales, (n, kb), uint8, "scales", device)
     rc = _call("tq_fp4_quantize")(ptr, code, step, n, K, fmt, _scale_ptr(global_scale, 1, "global_scale", device),
-                                  p_ptr, s_ptr, _stream(stream))
+                                  p_ptr, s_ptr, _stream(stream, device))
     if rc:
         raise TQError(rc, "tq_fp4_quantize")
     return packed, scales
@@ -849,7 +847,7 @@ def tq_fp4_dequantize(packed, scales, fmt: int = FP4_NV, global_scale=None, dtyp
             raise TypeError(f"out has dtype {out.dtype}, not {dtype}")
         o_ptr = _given(out, shape, (), "out", device)
     rc = _call("tq_fp4_dequantize")(p_ptr, s_ptr, n, K, fmt, _scale_ptr(global_scale, 1, "global_scale", device), o_ptr,
-                                    _type_code(out.dtype, "out"), _stream(stream))
+                                    _type_code(out.dtype, "out"), _stream(stream, device))
     if rc:
         raise TQError(rc, "tq_fp4_dequantize")
     return out
@@ -871,7 +869,7 @@ def tq_fp4_tile_scales(scales, fmt: int = FP4_NV, tiled=None, stream=None):
         raise ValueError(f"tiled has {tiled.numel()} bytes, expected {size}")
     device = torch.cuda.current_device()
     _check(lib().tq_fp4_tile_scales(_there(scales, (torch.uint8,), "scales", device), E, N, K, fmt,
-                                    _there(tiled, (torch.uint8,), "tiled", device), _stream(stream)),
+                                    _there(tiled, (torch.uint8,), "tiled", device), _stream(stream, device)),
            "tq_fp4_tile_scales")
     return tiled
 
@@ -930,7 +928,7 @@ def tq_fp4_linear(x, packed, tiled_scales, fmt: int = FP4_NV, w_scale=None, x_sc
     y, y_ptr, y_code = _output(y, (n, N), x, stream, device)
     rc = _call("tq_fp4_linear")(ptr, code, step, w_ptr, s_ptr, fmt, _scale_ptr(w_scale, 1, "w_scale", device),
                                 _scale_ptr(x_scale, 1, "x_scale", device), n, K, N, ws_ptr, ws_bytes, y_ptr, y_code,
-                                _stream(stream))
+                                _stream(stream, device))
     if rc:
         raise TQError(rc, "tq_fp4_linear")
     return y
@@ -958,7 +956,7 @@ def tq_fp4_moe_forward(x, packed, tiled_scales, topk_ids, topk_w, fmt: int = FP4
                                      _scale_ptr(x_scale, 1, "x_scale", device),
                                      _given(topk_ids, (n, top_k), int32, "topk_ids", device),
                                      _given(topk_w, (n, top_k), fp32, "topk_w", device), n, top_k, E, K, N, ws_ptr,
-                                     ws_bytes, y_ptr, y_code, _stream(stream))
+                                     ws_bytes, y_ptr, y_code, _stream(stream, device))
     if rc:
         raise TQError(rc, "tq_fp4_moe_forward")
     return y
@@ -989,7 +987,7 @@ def tq_fp4_moe_mlp_forward(x, packed_gu, tiled_gu, packed_down, tiled_down, topk
         _scale_ptr(down_scale, E, "down_scale", device), fmt, _scale_ptr(x_scale, 1, "x_scale", device),
         _scale_ptr(h_scale, 1, "h_scale", device), _given(topk_ids, (n, top_k), int32, "topk_ids", device),
         _given(topk_w, (n, top_k), fp32, "topk_w", device), n, top_k, E, H, I, ws_ptr, ws_bytes, y_ptr, y_code,
-        _stream(stream))
+        _stream(stream, device))
     if rc:
         raise TQError(rc, "tq_fp4_moe_mlp_forward")
     return y
