@@ -109,6 +109,11 @@ Tiling moe_tiling(int64_t n, int top_k, int E, int K, int N, int fmt) {
 // and 0.75 per 2048 x 4096 matrix.  At 2048 x 4096 the GEMV took 3.8, 5.6, 8.7,
 // 15.8 for 1, 2, 4, 8 rows of a linear and 10.4, 17.6, 29.3, 55.0 for 1, 2, 4, 8
 // tokens of top-6 of 256, the chain 7.9, 7.7, 7.8, 7.9 and 21.9, 26.1, 35.1, 53.1.
+// Held against both arms at 14 other sizes (linears 256 -> 256 to 8192 -> 8192,
+// experts 256 -> 256 to 4096 -> 4096 of 8 to 256, 1 to 32 rows each): the arm that
+// it takes is the slower one in 5 of 84 cases, by 8% at most (256 -> 256, 32 tokens
+// of top-6 of 64: 15.6 for the chain's 14.4; linear 4096 -> 4096, 2 rows: 8.2 for
+// the GEMV's 7.8).
 bool takes_gemv(int64_t n, int top_k, double matrices, double chain_us, int K, int N) {
   if (n > 64 || K > kFp4GemvMaxK) return false;
   const double rows = N / 2048.0, values = K / 4096.0;

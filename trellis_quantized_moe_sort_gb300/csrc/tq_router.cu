@@ -17,8 +17,8 @@
 // Bound: 8192 x 256 fp32 logits are 8.4 MB, 1.3 us of HBM time, so both
 // directions are bound by the issue of a row's instructions (eight exponentials
 // and reciprocals a lane, then the rounds of the choice) and by the launch:
-// 10.6 us forward (top-6 of 256 in 8 groups, biased sigmoid), 6.9 us backward
-// (softmax).  One row per warp, 64 registers, so 32 warps live on an SM; held to
+// 10.6 us forward (top-6 of 256 in 8 groups, biased sigmoid), 6.7 us backward
+// (softmax; sigmoid 5.7).  One row per warp, 64 registers, so 32 warps live on an SM; held to
 // 48 or 40 registers it took 0.2 and 0.6 us more.
 #include <cuda_runtime.h>
 
