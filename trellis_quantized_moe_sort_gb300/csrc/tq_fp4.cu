@@ -232,7 +232,8 @@ struct MlpPlan {
 };
 MlpPlan plan_mlp(void* base, int64_t n, int top_k, int E, int H, int I, int fmt) {
   MlpPlan m;
-  // one tile map for both products: the larger's rows, each its own splits
+  // one tile map for both products, by the gate and up product; the down product's
+  // splits are those of a search over m-tiles of its own (any number gives the sum)
   const Tiling gu = moe_tiling(n, top_k, E, H, 2 * I, fmt), down = moe_tiling(n, top_k, E, I, H, fmt);
   m.tile_m = gu.tile_m;
   m.splits_gu = gu.splits;
