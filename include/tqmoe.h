@@ -502,7 +502,7 @@ int tq_router_scored_backward(const void* logits, int logits_type, int64_t logit
  * codes (0, .5, 1, 1.5, 2, 3, 4, 6 and a sign in bit 3), two to a byte, value
  * 2i in the low half of byte i; blocks of consecutive values share a scale:
  *   TQ_FP4_NV  blocks of 16, scale s = e4m3(max|x| / (6 g)), g the 32-bit
- *              global scale (1 when NULL; positive and finite, or 0, with
+ *              global scale (1 when NULL; positive with 6 g finite, or 0, with
  *              which every s is 0, as the g of an all-zero tensor may be);
  *              code = e2m1(x / (s g)), value = code * s * g.
  *   TQ_FP4_MX  blocks of 32, scale s = 2^(floor(log2 max|x|) - 2) as E8M0

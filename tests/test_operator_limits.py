@@ -211,7 +211,8 @@ def test_workspace_sizes_follow_the_device(tq, monkeypatch, request):
                        ("tq_fp4_moe_mlp_workspace_size", (300, 2, 8, 96, 32))):
         monkeypatch.setattr(tq.lib(), name, lambda *a: sizes[current[0]])
         made = []
-        monkeypatch.setattr(tq, "_empty", lambda n, dtype, device, stream: made.append((n, device)) or torch.empty(n, dtype=dtype))
+        monkeypatch.setattr(tq, "_empty", lambda n, dtype, device, stream:
+                            made.append((n, device)) or torch.empty(n, dtype=dtype))
         size = getattr(tq, name)
         for device in (0, 1, 0):
             current[0] = device
