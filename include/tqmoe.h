@@ -582,6 +582,132 @@ int tq_fp4_moe_mlp_forward(const void* x, int x_type, int64_t x_stride,
                            void* y, int y_type, tq_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Root-mean-square norm with the residual's addition.  Per row, over its K values:
+ *   r = x + residual, rounded to x_type and kept in residual_out (residual NULL:
+ *   r = x);  rstd = 1 / sqrt(mean(r^2) + eps);  y = (r * rstd) * weight.
+ * The output is y in x's type, or in 8 bits with block scales (codes, scales as
+ * tq_fp8_quantize writes them for y before its rounding), or both.  Arithmetic is
+ * fp32; the sum of squares carries its rounding errors along, so that rstd is
+ * rounded once and results do not depend on the order of a sum.
+ * x, residual (device) n rows of K x_type values, *_stride elements apart (>= K);
+ *   rows on 16-byte boundaries with K a multiple of 16 are read fastest and are
+ *   required for codes.
+ * weight       (device) w_type [K], or NULL for ones.
+ * residual_out (device) [n][K] of x_type, dense, with a residual; it may be the
+ *   residual or x itself where that is dense (in place).
+ * y (device) [n][K] of x_type, dense, or NULL; it may be x where that is dense.
+ * rstd (device) fp32 [n] or NULL: what the gradient takes.
+ * codes (device) uint8 [n][K], 16-byte aligned, and scales (device) fp32
+ *   [n][ceil(K / 128)], or both NULL.
+ * Limits: 1 <= K <= TQ_NORM_MAX_WIDTH, eps >= 0 and finite.
+ *
+ * tq_rms_norm_backward: with x the normed rows (residual_out of the forward call,
+ *   or its x), rstd of that call and a = grad_y * weight:
+ *   grad_x = rstd * (a - x * rstd^2 * mean(a * x)) + grad_residual, in x_type,
+ *   dense [n][K]: the gradient of x and of the residual alike;
+ *   grad_weight[k] = sum over rows of grad_y * x * rstd, in w_type, or NULL.
+ *   grad_residual (what arrives through residual_out) may be NULL.  Sums are fp32
+ *   in a fixed order.  grad_x may be grad_y or grad_residual where that is dense.
+ *   workspace (device, 256-byte aligned) of tq_rms_norm_backward_workspace_size()
+ *   bytes (0 on invalid arguments); not used without grad_weight.
+ * ------------------------------------------------------------------------- */
+#define TQ_NORM_MAX_WIDTH 16384
+int tq_rms_norm(const void* x, int x_type, int64_t x_stride, const void* residual, int64_t residual_stride,
+                const void* weight, int w_type, float eps, int64_t n, int K, void* residual_out, void* y,
+                float* rstd, uint8_t* codes, float* scales, tq_stream_t stream);
+size_t tq_rms_norm_backward_workspace_size(int64_t n, int K);
+int tq_rms_norm_backward(const void* grad_y, int64_t grad_y_stride, const void* x, int x_type, int64_t x_stride,
+                         const void* weight, int w_type, const float* rstd, const void* grad_residual,
+                         int64_t grad_residual_stride, int64_t n, int K, void* workspace, size_t workspace_bytes,
+                         void* grad_x, void* grad_weight, tq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * 8-bit block-scaled values.  Blocks of rows_per_block x 128 values of a matrix of
+ * rows of K (K % 16 == 0; the last block may be short) share an fp32 scale
+ * s = max|x| / 448; a value is kept as the E4M3 code of x / s, value = code * s.
+ * rows_per_block is 1 (activations) or 128 (weights).  Both quotients are rounded
+ * to fp32 and the conversion to nearest even, saturating.  NaN is kept as NaN and
+ * does not count for the maximum, an infinity counts as the largest finite number
+ * and is kept as 448 (so code * s is that number).  In a block with s = 0 all but
+ * NaN is kept as 0.
+ *
+ * tq_fp8_quantize: x (device) E matrices of n rows of K x_type values, x_stride
+ *   elements apart (matrix e starts at row e * n), base and rows 16-byte aligned ->
+ *   codes (device) uint8 [E][n][K], 16-byte aligned, and scales (device) fp32
+ *   [E][ceil(n / rows_per_block)][ceil(K / 128)].
+ * tq_fp8_dequantize: code * s rounded once to out_type; out (device) [E][n][K],
+ *   16-byte aligned.
+ * Limits: E * n below 2^31 - 1024; with rows_per_block 128 also E <= 65535.
+ * ------------------------------------------------------------------------- */
+int tq_fp8_quantize(const void* x, int x_type, int64_t x_stride, int E, int64_t n, int K, int rows_per_block,
+                    uint8_t* codes, float* scales, tq_stream_t stream);
+int tq_fp8_dequantize(const uint8_t* codes, const float* scales, int E, int64_t n, int K, int rows_per_block,
+                      void* out, int out_type, tq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Products of 8-bit block-scaled rows x (rows_per_block 1) with 8-bit matrices
+ * (rows_per_block 128).  The partial sums of each block of 128 are accumulated in
+ * fp32, multiplied by both scales and added up in fp32; the result is rounded once
+ * to y_type.  Sums have a fixed order, so results repeat bit for bit.
+ *
+ * tq_fp8_linear:      y[t] = W x[t], w [N][K], w_scales [ceil(N/128)][ceil(K/128)].
+ * tq_fp8_moe_forward: y[t] = sum_j topk_w[t][j] W_{topk_ids[t][j]} x[t], w [E][N][K]
+ *   and w_scales [E][..].  A pair whose id is out of range adds nothing and sets
+ *   TQ_ERR_INVALID_ARG in the device error word.
+ * tq_fp8_moe_mlp_forward: SwiGLU experts, w_gu [E][2I][H] (rows 0..I-1 the gate,
+ *   I..2I-1 the up projection), w_down [E][H][I], I a multiple of 128:
+ *   h = silu(gate) * up per pair in fp32, kept in 8 bits (blocks of 128 of a row),
+ *   y[t] = sum_j topk_w[t][j] W_down h(t,j).  E = 1, top_k = 1: a dense MLP.
+ * x, w (device) codes, 16-byte aligned; x_scales (device) fp32 [n][ceil(K/128)];
+ * y (device) dense.  K and H are multiples of 16, N is any width.  E <= 1024,
+ * top_k <= 32; n * top_k and E * N (E * 2I, E * H) below 2^31 - 1024, n * top_k * N
+ * below 2^58.  workspace (device) of at least the matching *_workspace_size() bytes
+ * (0 on invalid arguments; 256, or a NULL workspace, where none is needed),
+ * 256-byte aligned; its contents are undefined after the call.
+ * ------------------------------------------------------------------------- */
+size_t tq_fp8_linear_workspace_size(int64_t n, int K, int N);
+int tq_fp8_linear(const uint8_t* x, const float* x_scales, const uint8_t* w, const float* w_scales, int64_t n, int K,
+                  int N, void* workspace, size_t workspace_bytes, void* y, int y_type, tq_stream_t stream);
+size_t tq_fp8_moe_workspace_size(int64_t n, int top_k, int E, int K, int N);
+int tq_fp8_moe_forward(const uint8_t* x, const float* x_scales, const uint8_t* w, const float* w_scales,
+                       const int32_t* topk_ids, const float* topk_w, int64_t n, int top_k, int E, int K, int N,
+                       void* workspace, size_t workspace_bytes, void* y, int y_type, tq_stream_t stream);
+size_t tq_fp8_moe_mlp_workspace_size(int64_t n, int top_k, int E, int H, int I);
+int tq_fp8_moe_mlp_forward(const uint8_t* x, const float* x_scales, const uint8_t* w_gu, const float* gu_scales,
+                           const uint8_t* w_down, const float* down_scales, const int32_t* topk_ids,
+                           const float* topk_w, int64_t n, int top_k, int E, int H, int I, void* workspace,
+                           size_t workspace_bytes, void* y, int y_type, tq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Gated projection in 16 bits (type TQ_BF16 or TQ_FP16), with its gradient:
+ *   gate|up = x W_gu^T, h = silu(gate) * up, sums in fp32, h rounded once.
+ * x    (device) n rows of H values, x_stride elements apart (a multiple of 8, base
+ *   16-byte aligned).
+ * w_gu (device) [2I][H], rows 0..I-1 the gate, I..2I-1 the up projection, 16-byte
+ *   aligned.  H and I are multiples of 8.
+ * h (device) [n][I], 16-byte aligned, or NULL when only gate_up is wanted.
+ * gate_up (device) fp32 [n][2I], 16-byte aligned, or NULL: gate and up as the
+ *   gradient takes them (fp32: their roundings to 16 bits would be as large as the
+ *   one of d below).
+ *
+ * tq_swiglu_linear_backward: from grad_h (device, [n][I] dense, 16-byte aligned)
+ *   dgate = grad_h * up * s * (1 + gate * (1 - s)), dup = grad_h * gate * s,
+ *   s = 1 / (1 + exp(-gate)), as rows d = [dgate dup] rounded to the type (the
+ *   products' operands have 16 bits), then grad_x = d W_gu (dense [n][H]) and
+ *   grad_w_gu = d^T x ([2I][H]), either may be NULL, 16-byte aligned.  gate_up is
+ *   the forward call's, or NULL: computed again from x and w_gu.  Sums have a fixed
+ *   order.  workspace (device, 256-byte aligned) of
+ *   tq_swiglu_linear_backward_workspace_size() bytes (0 on invalid arguments).
+ * Limits: n, 2I and H below 2^31 - 1024, products of two of them below 2^57.
+ * ------------------------------------------------------------------------- */
+int tq_swiglu_linear(const void* x, int type, int64_t x_stride, const void* w_gu, int64_t n, int H, int I, void* h,
+                     float* gate_up, tq_stream_t stream);
+size_t tq_swiglu_linear_backward_workspace_size(int64_t n, int H, int I, int has_gate_up);
+int tq_swiglu_linear_backward(const void* x, int type, int64_t x_stride, const void* w_gu, const float* gate_up,
+                              const void* grad_h, int64_t n, int H, int I, void* workspace, size_t workspace_bytes,
+                              void* grad_x, void* grad_w_gu, tq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Diagnostics
  * ------------------------------------------------------------------------- */
 
@@ -622,10 +748,15 @@ void tq_launch_counts(int64_t out[TQ_NUM_LAUNCH_COUNTERS]);
 
 /* The same and the counters that came later: out[11] scored router, out[12] its
  * backward, out[13] 4-bit quantise, out[14] dequantise, out[15] scale tiling,
- * out[16] activation staging, out[17] 4-bit GEMM, out[18] 4-bit combine,
- * out[19] SwiGLU staging, out[20] 4-bit GEMV.  Writes the first `capacity` of them and returns how
+ * out[16] activation staging, out[17] 4-bit GEMM, out[18] combine (of
+ * 4- and 8-bit products, and of K splits),
+ * out[19] SwiGLU staging, out[20] 4-bit GEMV, out[21] RMS norm, out[22] its
+ * gradient, out[23] the sum of its weight's gradient, out[24] 8-bit quantise,
+ * out[25] dequantise, out[26] SwiGLU to 8 bits, out[27] 8-bit product, out[28]
+ * product with few rows (8 or 16 bits), out[29] 16-bit product, out[30] gradient
+ * of the gated activation.  Writes the first `capacity` of them and returns how
  * many there are. */
-#define TQ_NUM_ALL_LAUNCH_COUNTERS 21
+#define TQ_NUM_ALL_LAUNCH_COUNTERS 31
 int tq_launch_counts_all(int64_t* out, int capacity);
 
 #ifdef __cplusplus

@@ -29,6 +29,10 @@ __all__ = [
     "tq_fp4_quantize", "tq_fp4_dequantize", "tq_fp4_tiled_scales_size", "tq_fp4_tile_scales",
     "tq_fp4_linear_workspace_size", "tq_fp4_linear", "tq_fp4_moe_workspace_size", "tq_fp4_moe_forward",
     "tq_fp4_moe_mlp_workspace_size", "tq_fp4_moe_mlp_forward", "FP4_NV", "FP4_MX", "tq_launch_counts_all",
+    "tq_rms_norm", "tq_rms_norm_fp8", "tq_rms_norm_backward_workspace_size", "tq_rms_norm_backward",
+    "tq_fp8_quantize", "tq_fp8_dequantize", "tq_fp8_linear_workspace_size", "tq_fp8_linear", "tq_fp8_moe_workspace_size",
+    "tq_fp8_moe_forward", "tq_fp8_moe_mlp_workspace_size", "tq_fp8_moe_mlp_forward", "FP8_BLOCK",
+    "tq_swiglu_linear", "tq_swiglu_linear_backward_workspace_size", "tq_swiglu_linear_backward",
 ]
 
 ARM_AUTO, ARM_GEMV, ARM_GROUPED, ARM_MEASURED = 0, 1, 2, 3
@@ -37,6 +41,7 @@ X_TOKENS, X_PAIR_SORTED = 0, 1   # activation layouts of tq_grouped_gemm / tq_gr
 GATHER_MAX_TILE_M = 16   # the whole-product calls gather rows in the kernel up to this m-tile
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1   # scores of tq_router_scored
 FP4_NV, FP4_MX = 0, 1    # 4-bit formats: blocks of 16 with E4M3 scales, blocks of 32 with E8M0 scales
+FP8_BLOCK = 128          # values of a row, or rows and columns of a matrix, that share an 8-bit scale
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libtqmoe.so")
 
@@ -108,6 +113,25 @@ _SIGS = {
     "tq_fp4_moe_mlp_forward": (_c_int, [_c_p, _c_int, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_int, _c_p, _c_p,
                                         _c_p, _c_p, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_p, _c_sz, _c_p, _c_int,
                                         _c_p]),
+    "tq_rms_norm": (_c_int, [_c_p, _c_int, _c_i64, _c_p, _c_i64, _c_p, _c_int, _c_flt, _c_i64, _c_int, _c_p, _c_p, _c_p,
+                             _c_p, _c_p, _c_p]),
+    "tq_rms_norm_backward_workspace_size": (_c_sz, [_c_i64, _c_int]),
+    "tq_rms_norm_backward": (_c_int, [_c_p, _c_i64, _c_p, _c_int, _c_i64, _c_p, _c_int, _c_p, _c_p, _c_i64, _c_i64, _c_int,
+                                      _c_p, _c_sz, _c_p, _c_p, _c_p]),
+    "tq_fp8_quantize": (_c_int, [_c_p, _c_int, _c_i64, _c_int, _c_i64, _c_int, _c_int, _c_p, _c_p, _c_p]),
+    "tq_fp8_dequantize": (_c_int, [_c_p, _c_p, _c_int, _c_i64, _c_int, _c_int, _c_p, _c_int, _c_p]),
+    "tq_fp8_linear_workspace_size": (_c_sz, [_c_i64, _c_int, _c_int]),
+    "tq_fp8_linear": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_i64, _c_int, _c_int, _c_p, _c_sz, _c_p, _c_int, _c_p]),
+    "tq_fp8_moe_workspace_size": (_c_sz, [_c_i64, _c_int, _c_int, _c_int, _c_int]),
+    "tq_fp8_moe_forward": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_p,
+                                    _c_sz, _c_p, _c_int, _c_p]),
+    "tq_fp8_moe_mlp_workspace_size": (_c_sz, [_c_i64, _c_int, _c_int, _c_int, _c_int]),
+    "tq_fp8_moe_mlp_forward": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_int, _c_int, _c_int,
+                                        _c_int, _c_p, _c_sz, _c_p, _c_int, _c_p]),
+    "tq_swiglu_linear": (_c_int, [_c_p, _c_int, _c_i64, _c_p, _c_i64, _c_int, _c_int, _c_p, _c_p, _c_p]),
+    "tq_swiglu_linear_backward_workspace_size": (_c_sz, [_c_i64, _c_int, _c_int, _c_int]),
+    "tq_swiglu_linear_backward": (_c_int, [_c_p, _c_int, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_int, _c_int, _c_p, _c_sz,
+                                           _c_p, _c_p, _c_p]),
 }
 EXPORTED_SYMBOLS = tuple(_SIGS)
 
@@ -138,10 +162,12 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
-# The scored router's and the 4-bit operators' calls, by name: the C wrappers of
+# The calls of the scored router, the norm and the 4-, 8- and 16-bit operators, by name: the C wrappers of
 # csrc/tq_python.c, or ctypes' functions where those are not built.
 _CALLS = ("tq_router_scored", "tq_router_scored_backward", "tq_fp4_quantize", "tq_fp4_dequantize", "tq_fp4_linear",
-          "tq_fp4_moe_forward", "tq_fp4_moe_mlp_forward")
+          "tq_fp4_moe_forward", "tq_fp4_moe_mlp_forward", "tq_rms_norm", "tq_rms_norm_backward", "tq_fp8_quantize",
+          "tq_fp8_dequantize", "tq_fp8_linear", "tq_fp8_moe_forward", "tq_fp8_moe_mlp_forward", "tq_swiglu_linear",
+          "tq_swiglu_linear_backward")
 _calls: dict = {}
 
 
@@ -646,7 +672,9 @@ def tq_launch_counts_all() -> dict:
 
 ALL_LAUNCH_COUNTERS = LAUNCH_COUNTERS + ("router_scored", "router_scored_backward", "fp4_quantize", "fp4_dequantize",
                                          "fp4_tile_scales", "fp4_stage", "fp4_gemm", "fp4_combine", "fp4_swiglu",
-                                         "fp4_gemv")
+                                         "fp4_gemv", "rms_norm", "rms_norm_backward", "rms_norm_weight", "fp8_quantize",
+                                         "fp8_dequantize", "fp8_swiglu", "fp8_gemm", "few_rows", "gemm_f16",
+                                         "swiglu_grad")
 
 
 # ------------------------------------------------------------------ scored router, 4-bit operators
@@ -890,14 +918,14 @@ def _workspace_bytes(size, device, *args):
     return size(*args)
 
 
-def _workspace(workspace, size, device, stream, *args):
+def _workspace(workspace, size, device, stream, *args, keep_small=False):
     """(address, bytes) of the caller's workspace, or of a new one of
-    size(*args) bytes (none where the call needs none), and the tensor, to be
-    kept until the call is enqueued."""
+    size(*args) bytes (none where the call needs none: 256 reported, unless
+    keep_small), and the tensor, to be kept until the call is enqueued."""
     torch, _, _, uint8 = _types()
     if workspace is None:
         need = _workspace_bytes(size, device, *args)
-        if need <= 256:
+        if need <= (0 if keep_small else 256):
             return None, 0, None
         workspace = _empty(need, torch.uint8, device, stream)
         return workspace.data_ptr(), need, workspace
@@ -991,3 +1019,347 @@ def tq_fp4_moe_mlp_forward(x, packed_gu, tiled_gu, packed_down, tiled_down, topk
     if rc:
         raise TQError(rc, "tq_fp4_moe_mlp_forward")
     return y
+
+
+# ------------------------------------------------------------------ norm
+
+def _dense(t, rows, width, dtype, name, device, x, stream):
+    """(tensor, address) of a dense output [rows, width]: the caller's, or a new one."""
+    if t is None:
+        t = _empty((rows, width), dtype, x.device, stream)
+        return t, t.data_ptr()
+    return t, _given(t, (rows, width), (dtype,), name, device)
+
+
+def _same_rows(t, n, K, dtype, name):
+    """(address, elements between rows) of rows that go with x [n, K]."""
+    ptr, _, step, rows, width, _ = _rows(t, name)
+    if (rows, width) != (n, K):
+        raise ValueError(f"{name} has shape {(rows, width)}, expected {(n, K)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    return ptr, step
+
+
+def _norm_weight(weight, K, device):
+    """(address, type code) of the weights, or of none."""
+    if weight is None:
+        return None, 0
+    return _given(weight, (K,), (), "weight", device), _type_code(weight.dtype, "weight")
+
+
+def _norm(what, x, weight, eps, residual, residual_out, y, rstd, codes, scales, stream, has_y, has_codes):
+    torch, fp32, _, _ = _types()
+    ptr, code, step, n, K, device = _rows(x, "x")
+    w_ptr, w_code = _norm_weight(weight, K, device)
+    r_ptr, r_step, o_ptr = None, 0, None
+    if residual is not None:
+        r_ptr, r_step = _same_rows(residual, n, K, x.dtype, "residual")
+        residual_out, o_ptr = _dense(residual_out, n, K, x.dtype, "residual_out", device, x, stream)
+    elif residual_out is not None:
+        raise ValueError("residual_out is an output of the addition of a residual")
+    y_ptr = rstd_ptr = c_ptr = s_ptr = None
+    if has_y:
+        y, y_ptr = _dense(y, n, K, x.dtype, "y", device, x, stream)
+        if rstd is None:
+            rstd = _empty((n,), torch.float32, x.device, stream)
+            rstd_ptr = rstd.data_ptr()
+        else:
+            rstd_ptr = _given(rstd, (n,), fp32, "rstd", device)
+    if has_codes:
+        if y is not None:
+            y_ptr = _given(y, (n, K), (x.dtype,), "y", device)
+        codes, c_ptr = _dense(codes, n, K, torch.float8_e4m3fn, "codes", device, x, stream)
+        scales, s_ptr = _dense(scales, n, -(-K // FP8_BLOCK), torch.float32, "scales", device, x, stream)
+    rc = _call("tq_rms_norm")(ptr, code, step, r_ptr, r_step, w_ptr, w_code, eps, n, K, o_ptr, y_ptr, rstd_ptr, c_ptr,
+                              s_ptr, _stream(stream, device))
+    if rc:
+        raise TQError(rc, what)
+    return y, residual_out if residual is not None else x, rstd, codes, scales
+
+
+def tq_rms_norm(x, weight=None, eps: float = 1e-6, residual=None, y=None, residual_out=None, rstd=None, stream=None):
+    """RMS norm of r = x + residual over rows x [n, K] (fp32, bf16 or fp16; rows may
+    be strided) -> (y, r, rstd): y = r * rstd * weight in x's dtype; r as the next
+    block's residual and the gradient take it (x itself without a residual; in place
+    with residual_out=residual); rstd fp32 [n] = 1 / sqrt(mean(r^2) + eps).  weight:
+    [K] of any of the three types, or None for ones."""
+    y, r, rstd, _, _ = _norm("tq_rms_norm", x, weight, eps, residual, residual_out, y, rstd, None, None, stream, True,
+                             False)
+    return y, r, rstd
+
+
+def tq_rms_norm_fp8(x, weight=None, eps: float = 1e-6, residual=None, codes=None, scales=None, y=None,
+                    residual_out=None, stream=None):
+    """tq_rms_norm with its output in 8 bits, as tq_fp8_linear and the experts read
+    it -> (codes float8_e4m3fn [n, K], scales fp32 [n, ceil(K / 128)], r).  K a
+    multiple of 16, rows 16-byte aligned.  With y (a tensor [n, K] in x's dtype) the
+    unquantised output is written too."""
+    _, r, _, codes, scales = _norm("tq_rms_norm_fp8", x, weight, eps, residual, residual_out, y, None, codes, scales,
+                                   stream, False, True)
+    return codes, scales, r
+
+
+def tq_rms_norm_backward_workspace_size(n: int, K: int) -> int:
+    return lib().tq_rms_norm_backward_workspace_size(n, K)
+
+
+def tq_rms_norm_backward(grad_y, x, weight, rstd, grad_residual=None, grad_x=None, grad_weight=None, workspace=None,
+                         stream=None):
+    """Gradients of tq_rms_norm -> (grad_x, grad_weight): x is the normed r and rstd
+    what that call returned, grad_residual the gradient that arrives through r.
+    grad_x, in x's dtype, is the gradient of the call's x and residual alike;
+    grad_weight has the weight's dtype (None without a weight)."""
+    torch, fp32, _, _ = _types()
+    ptr, code, step, n, K, device = _rows(x, "x")
+    dy_ptr, dy_step = _same_rows(grad_y, n, K, x.dtype, "grad_y")
+    w_ptr, w_code = _norm_weight(weight, K, device)
+    g_ptr, g_step = (None, 0) if grad_residual is None else _same_rows(grad_residual, n, K, x.dtype, "grad_residual")
+    grad_x, gx_ptr = _dense(grad_x, n, K, x.dtype, "grad_x", device, x, stream)
+    gw_ptr = ws_ptr = None
+    ws_bytes = 0
+    if weight is not None:
+        if grad_weight is None:
+            grad_weight = _empty((K,), weight.dtype, x.device, stream)
+            gw_ptr = grad_weight.data_ptr()
+        else:
+            gw_ptr = _given(grad_weight, (K,), (weight.dtype,), "grad_weight", device)
+        ws_ptr, ws_bytes, workspace = _workspace(workspace, tq_rms_norm_backward_workspace_size, device, stream, n, K,
+                                                 keep_small=True)
+    elif grad_weight is not None:
+        raise ValueError("grad_weight needs a weight")
+    rc = _call("tq_rms_norm_backward")(dy_ptr, dy_step, ptr, code, step, w_ptr, w_code,
+                                       _given(rstd, (n,), fp32, "rstd", device), g_ptr, g_step, n, K, ws_ptr, ws_bytes,
+                                       gx_ptr, gw_ptr, _stream(stream, device))
+    if rc:
+        raise TQError(rc, "tq_rms_norm_backward")
+    return grad_x, grad_weight
+
+
+# ------------------------------------------------------------------ 8-bit operators
+
+_code_types = None
+
+
+def _fp8():
+    """The dtypes that 8-bit codes may have."""
+    global _code_types
+    if _code_types is None:
+        torch = _torch()
+        _code_types = (torch.float8_e4m3fn, torch.uint8)
+    return _code_types
+
+
+def _scale_shape(shape, rows_per_block):
+    return (*shape[:-2], -(-shape[-2] // rows_per_block), -(-shape[-1] // FP8_BLOCK))
+
+
+def _fp8_rows(x, x_scales):
+    """(address, scales' address, rows, K, device) of 8-bit activations [n, K]."""
+    device = _torch().cuda.current_device()
+    ptr = _there(x, _fp8(), "x", device)
+    if len(x.shape) != 2:
+        raise ValueError(f"x must have two dimensions, not {len(x.shape)}")
+    n, K = x.shape
+    return ptr, _given(x_scales, _scale_shape((n, K), 1), _types()[1], "x_scales", device), n, K, device
+
+
+def _fp8_matrix(w, scales, shape, name, device):
+    """Addresses of 8-bit weights of a known shape and of their scales."""
+    return (_given(w, shape, _fp8(), name, device),
+            _given(scales, _scale_shape(shape, FP8_BLOCK), _types()[1], f"the scales of {name}", device))
+
+
+def tq_fp8_quantize(x, rows_per_block: int = 1, codes=None, scales=None, stream=None):
+    """8-bit block-scaled copy of x [n, K] or [E, n, K] (fp32, bf16 or fp16; 16-byte
+    aligned rows; K % 16 == 0) -> (codes float8_e4m3fn of x's shape, scales fp32
+    [.., ceil(n / rows_per_block), ceil(K / 128)]).  rows_per_block: 1 for
+    activations (rows may be strided), 128 for weights."""
+    torch, fp32, _, _ = _types()
+    shape = x.shape
+    if len(shape) == 3:
+        E, n, K = shape
+        x = x.reshape(E * n, K) if x.is_contiguous() else x
+        if len(x.shape) != 2:
+            raise ValueError("x [E, n, K] must be contiguous")
+    elif len(shape) == 2:
+        E, (n, K) = 1, shape
+    else:
+        raise ValueError(f"x must have two or three dimensions, not {len(shape)}")
+    if rows_per_block != 1 and rows_per_block != FP8_BLOCK:
+        raise ValueError(f"rows_per_block must be 1 or {FP8_BLOCK}, not {rows_per_block}")
+    ptr, code, step, _, _, device = _rows(x, "x")
+    if codes is None:
+        codes = _empty(shape, torch.float8_e4m3fn, x.device, stream)
+        c_ptr = codes.data_ptr()
+    else:
+        c_ptr = _given(codes, shape, _fp8(), "codes", device)
+    want = _scale_shape(shape, rows_per_block)
+    if scales is None:
+        scales = _empty(want, torch.float32, x.device, stream)
+        s_ptr = scales.data_ptr()
+    else:
+        s_ptr = _given(scales, want, fp32, "scales", device)
+    rc = _call("tq_fp8_quantize")(ptr, code, step, E, n, K, rows_per_block, c_ptr, s_ptr, _stream(stream, device))
+    if rc:
+        raise TQError(rc, "tq_fp8_quantize")
+    return codes, scales
+
+
+def tq_fp8_dequantize(codes, scales, rows_per_block: int = 1, dtype=None, out=None, stream=None):
+    """The values of tq_fp8_quantize's output, in `dtype` (fp32 when neither it nor
+    `out` is given)."""
+    torch, fp32, _, _ = _types()
+    device = torch.cuda.current_device()
+    c_ptr = _there(codes, _fp8(), "codes", device)
+    shape = codes.shape
+    if len(shape) not in (2, 3):
+        raise ValueError(f"codes must have two or three dimensions, not {len(shape)}")
+    if rows_per_block != 1 and rows_per_block != FP8_BLOCK:
+        raise ValueError(f"rows_per_block must be 1 or {FP8_BLOCK}, not {rows_per_block}")
+    s_ptr = _given(scales, _scale_shape(shape, rows_per_block), fp32, "scales", device)
+    if out is None:
+        out = _empty(shape, torch.float32 if dtype is None else dtype, codes.device, stream)
+        o_ptr = out.data_ptr()
+    else:
+        if dtype is not None and out.dtype != dtype:
+            raise TypeError(f"out has dtype {out.dtype}, not {dtype}")
+        o_ptr = _given(out, shape, (), "out", device)
+    E = shape[0] if len(shape) == 3 else 1
+    rc = _call("tq_fp8_dequantize")(c_ptr, s_ptr, E, shape[-2], shape[-1], rows_per_block, o_ptr,
+                                    _type_code(out.dtype, "out"), _stream(stream, device))
+    if rc:
+        raise TQError(rc, "tq_fp8_dequantize")
+    return out
+
+
+def _result(y, shape, dtype, x, stream, device):
+    """(y, address, type code) of a product: the caller's, or a new one of `dtype` (bf16 by default)."""
+    if y is None:
+        y = _empty(shape, _types()[0].bfloat16 if dtype is None else dtype, x.device, stream)
+        return y, y.data_ptr(), _type_code(y.dtype, "y")
+    if dtype is not None and y.dtype != dtype:
+        raise TypeError(f"y has dtype {y.dtype}, not {dtype}")
+    return y, _given(y, shape, (), "y", device), _type_code(y.dtype, "y")
+
+
+def tq_fp8_linear_workspace_size(n: int, K: int, N: int) -> int:
+    return lib().tq_fp8_linear_workspace_size(n, K, N)
+
+
+def tq_fp8_linear(x, x_scales, w, w_scales, dtype=None, workspace=None, y=None, stream=None):
+    """8-bit rows x [n, K] (tq_fp8_quantize or tq_rms_norm_fp8) times an 8-bit matrix
+    w [N, K] with scales [ceil(N / 128), ceil(K / 128)] -> y [n, N] in `dtype`
+    (bf16 by default)."""
+    ptr, xs_ptr, n, K, device = _fp8_rows(x, x_scales)
+    N = w.shape[0]
+    w_ptr, ws_ptr = _fp8_matrix(w, w_scales, (N, K), "w", device)
+    work_ptr, work_bytes, workspace = _workspace(workspace, tq_fp8_linear_workspace_size, device, stream, n, K, N)
+    y, y_ptr, y_code = _result(y, (n, N), dtype, x, stream, device)
+    rc = _call("tq_fp8_linear")(ptr, xs_ptr, w_ptr, ws_ptr, n, K, N, work_ptr, work_bytes, y_ptr, y_code,
+                                _stream(stream, device))
+    if rc:
+        raise TQError(rc, "tq_fp8_linear")
+    return y
+
+
+def tq_fp8_moe_workspace_size(n: int, top_k: int, E: int, K: int, N: int) -> int:
+    return lib().tq_fp8_moe_workspace_size(n, top_k, E, K, N)
+
+
+def tq_fp8_moe_forward(x, x_scales, w, w_scales, topk_ids, topk_w, dtype=None, workspace=None, y=None, stream=None):
+    """Routed-expert product over 8-bit experts w [E, N, K] with scales [E,
+    ceil(N / 128), ceil(K / 128)] -> y [n, N] in `dtype` (bf16 by default):
+    y[t] = sum_j topk_w[t, j] * W_{topk_ids[t, j]} x[t]."""
+    _, fp32, int32, _ = _types()
+    ptr, xs_ptr, n, K, device = _fp8_rows(x, x_scales)
+    E, N = w.shape[0], w.shape[1]
+    top_k = topk_ids.shape[1]
+    w_ptr, ws_ptr = _fp8_matrix(w, w_scales, (E, N, K), "w", device)
+    work_ptr, work_bytes, workspace = _workspace(workspace, tq_fp8_moe_workspace_size, device, stream, n, top_k, E, K, N,
+                                                 keep_small=True)
+    y, y_ptr, y_code = _result(y, (n, N), dtype, x, stream, device)
+    rc = _call("tq_fp8_moe_forward")(ptr, xs_ptr, w_ptr, ws_ptr, _given(topk_ids, (n, top_k), int32, "topk_ids", device),
+                                     _given(topk_w, (n, top_k), fp32, "topk_w", device), n, top_k, E, K, N, work_ptr,
+                                     work_bytes, y_ptr, y_code, _stream(stream, device))
+    if rc:
+        raise TQError(rc, "tq_fp8_moe_forward")
+    return y
+
+
+def tq_fp8_moe_mlp_workspace_size(n: int, top_k: int, E: int, H: int, I: int) -> int:
+    return lib().tq_fp8_moe_mlp_workspace_size(n, top_k, E, H, I)
+
+
+def tq_fp8_moe_mlp_forward(x, x_scales, w_gu, gu_scales, w_down, down_scales, topk_ids, topk_w, dtype=None,
+                           workspace=None, y=None, stream=None):
+    """SwiGLU expert MLP over 8-bit experts: w_gu [E, 2I, H] (gate rows, then up
+    rows), w_down [E, H, I], I a multiple of 128 -> y [n, H] in `dtype` (bf16 by
+    default).  h = silu(gate) * up is kept in 8 bits between the products."""
+    _, fp32, int32, _ = _types()
+    ptr, xs_ptr, n, H, device = _fp8_rows(x, x_scales)
+    E, I = w_gu.shape[0], w_gu.shape[1] // 2
+    top_k = topk_ids.shape[1]
+    gu_ptr, gus_ptr = _fp8_matrix(w_gu, gu_scales, (E, 2 * I, H), "w_gu", device)
+    d_ptr, ds_ptr = _fp8_matrix(w_down, down_scales, (E, H, I), "w_down", device)
+    work_ptr, work_bytes, workspace = _workspace(workspace, tq_fp8_moe_mlp_workspace_size, device, stream, n, top_k, E, H,
+                                                 I, keep_small=True)
+    y, y_ptr, y_code = _result(y, (n, H), dtype, x, stream, device)
+    rc = _call("tq_fp8_moe_mlp_forward")(
+        ptr, xs_ptr, gu_ptr, gus_ptr, d_ptr, ds_ptr, _given(topk_ids, (n, top_k), int32, "topk_ids", device),
+        _given(topk_w, (n, top_k), fp32, "topk_w", device), n, top_k, E, H, I, work_ptr, work_bytes, y_ptr, y_code,
+        _stream(stream, device))
+    if rc:
+        raise TQError(rc, "tq_fp8_moe_mlp_forward")
+    return y
+
+
+# ------------------------------------------------------------------ gated projection
+
+def _rows16(x):
+    """_rows of a 16-bit tensor."""
+    rows = _rows(x, "x")
+    if rows[1] == 0:
+        raise TypeError(f"x has dtype {x.dtype}, expected bf16 or fp16")
+    return rows
+
+
+def tq_swiglu_linear(x, w_gu, h=None, gate_up=None, stream=None):
+    """h [n, I] = silu(x Wg^T) * (x Wu^T) for x [n, H] in bf16 or fp16 (rows may be
+    strided) and w_gu [2I, H] of the same dtype, gate rows first; H and I multiples
+    of 8.  With gate_up (fp32 [n, 2I]) gate and up are kept there for the gradient."""
+    _, fp32, _, _ = _types()
+    ptr, code, step, n, H, device = _rows16(x)
+    I = w_gu.shape[0] // 2
+    w_ptr = _given(w_gu, (2 * I, H), (x.dtype,), "w_gu", device)
+    h, h_ptr = _dense(h, n, I, x.dtype, "h", device, x, stream)
+    gu_ptr = None if gate_up is None else _given(gate_up, (n, 2 * I), fp32, "gate_up", device)
+    rc = _call("tq_swiglu_linear")(ptr, code, step, w_ptr, n, H, I, h_ptr, gu_ptr, _stream(stream, device))
+    if rc:
+        raise TQError(rc, "tq_swiglu_linear")
+    return h
+
+
+def tq_swiglu_linear_backward_workspace_size(n: int, H: int, I: int, has_gate_up: bool = True) -> int:
+    return lib().tq_swiglu_linear_backward_workspace_size(n, H, I, 1 if has_gate_up else 0)
+
+
+def tq_swiglu_linear_backward(x, w_gu, grad_h, gate_up=None, grad_x=None, grad_w_gu=None, workspace=None, stream=None):
+    """Gradients of tq_swiglu_linear from that of h -> (grad_x [n, H], grad_w_gu
+    [2I, H]) in x's dtype.  gate_up: what the forward call kept, or None to compute
+    it again."""
+    _, fp32, _, _ = _types()
+    ptr, code, step, n, H, device = _rows16(x)
+    I = w_gu.shape[0] // 2
+    w_ptr = _given(w_gu, (2 * I, H), (x.dtype,), "w_gu", device)
+    gh_ptr = _given(grad_h, (n, I), (x.dtype,), "grad_h", device)
+    gu_ptr = None if gate_up is None else _given(gate_up, (n, 2 * I), fp32, "gate_up", device)
+    grad_x, gx_ptr = _dense(grad_x, n, H, x.dtype, "grad_x", device, x, stream)
+    grad_w_gu, gw_ptr = _dense(grad_w_gu, 2 * I, H, x.dtype, "grad_w_gu", device, x, stream)
+    work_ptr, work_bytes, workspace = _workspace(workspace, tq_swiglu_linear_backward_workspace_size, device, stream, n,
+                                                 H, I, gate_up is not None, keep_small=True)
+    rc = _call("tq_swiglu_linear_backward")(ptr, code, step, w_ptr, gu_ptr, gh_ptr, n, H, I, work_ptr, work_bytes, gx_ptr,
+                                            gw_ptr, _stream(stream, device))
+    if rc:
+        raise TQError(rc, "tq_swiglu_linear_backward")
+    return grad_x, grad_w_gu

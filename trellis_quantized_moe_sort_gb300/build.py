@@ -24,7 +24,8 @@ LIB = os.path.join(HERE, "libtqmoe.so")
 CALLS = os.path.join(HERE, "_tqcall" + sysconfig.get_config_var("EXT_SUFFIX"))
 CALLS_SOURCES = [os.path.join(CSRC, "tq_python.c"), os.path.join(INCLUDE, "tqmoe.h")]
 SOURCES = ["tq_host.cu", "tq_route.cu", "tq_grouped.cu", "tq_gemv.cu", "tq_noalloc.cu", "tq_probe.cu", "tq_mlp.cu", "tq_dequant.cu",
-           "tq_router.cu", "tq_fp4_quant.cu", "tq_fp4_gemm.cu", "tq_fp4_gemv.cu", "tq_fp4.cu"]
+           "tq_router.cu", "tq_fp4_quant.cu", "tq_fp4_gemm.cu", "tq_fp4_gemv.cu", "tq_fp4.cu", "tq_norm.cu", "tq_fp8_quant.cu",
+           "tq_fp8_gemm.cu", "tq_few_rows.cu", "tq_fp8.cu", "tq_gemm_f16.cu", "tq_swiglu_linear.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

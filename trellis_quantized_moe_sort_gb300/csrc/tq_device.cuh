@@ -15,6 +15,7 @@ enum ErrWhere : int {
   kWhereGroupedMma = 5, kWhereGroupedEpilogue = 6, kWhereGroupedTeardown = 7, kWhereDequant = 8,
   kWhereTableStage = 9, kWhereProbe = 10, kWhereRouter = 11, kWhereFp4Load = 12, kWhereFp4Mma = 13,
   kWhereFp4Epilogue = 14, kWhereFp4Teardown = 15, kWhereFp4Gemv = 16,
+  kWhereTileLoad = 17, kWhereTileMma = 18, kWhereTileEpilogue = 19, kWhereTileTeardown = 20, kWhereFewRows = 21,
 };
 
 // A wait gives up after this long (ns of %globaltimer) and reports

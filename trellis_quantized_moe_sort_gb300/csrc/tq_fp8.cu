@@ -1,0 +1,360 @@
+// C entry points of the 8-bit operators: argument checks, workspace layout and the
+// launch chains of the products.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "tq_fp8.cuh"
+#include "tq_internal.h"
+#include "tq_tiling.h"
+
+namespace tq {
+namespace {
+
+size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+constexpr size_t kNoWorkspace = 256;   // reported where none is used; a null workspace will do
+// Rows of pairs and of weights: 32-bit coordinates with room for a tile past the end.
+constexpr int64_t kMaxIndex = (static_cast<int64_t>(1) << 31) - 1024;
+
+bool bad_k(int K) { return K < 16 || K % 16 != 0 || K >= kMaxIndex; }
+int blocks_of(int K) { return (K - 1) / kFp8Block + 1; }
+// Values whose bytes, up to 16 splits of fp32 partial sums, would not fit a size_t.
+bool bad_output(int64_t rows, int64_t N) { return static_cast<double>(rows) * static_cast<double>(N) >= 0x1p57; }
+bool bad_matrix(int64_t E, int K, int64_t N) { return bad_k(K) || N < 1 || E * N >= kMaxIndex; }
+bool bad_moe_shape(int64_t n, int top_k, int E) {
+  return E < 1 || E > 1024 || top_k < 1 || top_k > E || top_k > 32 || n < 0 || n >= kMaxIndex ||
+         n * top_k >= kMaxIndex;
+}
+bool bad_blocking(int rows_per_block) { return rows_per_block != 1 && rows_per_block != kFp8Block; }
+bool bad_workspace(const void* p, size_t bytes, size_t need) { return !p || bytes < need || !aligned(p, 256); }
+
+// Takes 256-byte aligned regions from a buffer, or only counts their bytes.
+struct Carver {
+  uint8_t* base;
+  size_t used = 0;
+  template <typename T>
+  T* take(size_t count) {
+    T* p = base ? reinterpret_cast<T*>(base + used) : nullptr;
+    used += align256(std::max<size_t>(count, 1) * sizeof(T));
+    return p;
+  }
+};
+
+constexpr int kFewRowsMost = 16;   // rows of an MMA pair of the few-rows kernel
+
+struct LinearPlan {
+  bool few;
+  TileChoice tile;
+  float* part;   // nullptr without splits
+  size_t bytes;
+};
+LinearPlan plan_linear(void* base, int64_t n, int K, int N) {
+  LinearPlan l{};
+  l.few = n <= kFewRowsMost;
+  l.bytes = kNoWorkspace;
+  if (l.few) return l;
+  l.tile = choose_tile(static_cast<double>(n), 1.0, blocks_of(K), N, false, false, false, true);
+  if (l.tile.splits > 1) {
+    Carver c{static_cast<uint8_t*>(base)};
+    l.part = c.take<float>(static_cast<size_t>(l.tile.splits) * n * N);
+    l.bytes = c.used;
+  }
+  return l;
+}
+
+// How the experts' products go: every pair by itself, without a sort; m-tiles of up
+// to 16 rows by the few-rows kernel; or the tensor-core tiles.
+enum Arm { kPairs, kFew, kTiles };
+struct MoePlan {
+  Arm arm;
+  int tile_m;
+  int64_t cap, P;
+};
+MoePlan plan_arm(int64_t n, int top_k, int E, TileChoice tile) {
+  MoePlan m;
+  m.P = n * top_k;
+  const double mean = n ? tq_pairs_per_woken_expert(n, top_k, E) : 0.0;
+  if (m.P <= 2 * top_k || mean < 1.1) {
+    // (almost) no expert has two pairs: sorting them would save nothing
+    m.arm = m.P <= 4096 ? kPairs : kFew;
+  } else {
+    m.arm = mean <= 10.0 ? kFew : kTiles;
+  }
+  m.tile_m = m.arm == kTiles ? tile.tile_m : mean <= 4.0 ? 8 : 16;
+  m.cap = std::max<int64_t>(1, tq_tile_map_capacity(n, top_k, E, m.tile_m));
+  return m;
+}
+double typical_rows(int64_t n, int top_k, int E) {
+  const double mean = n ? tq_pairs_per_woken_expert(n, top_k, E) : 1.0;
+  return mean + 2.0 * std::sqrt(mean);
+}
+TileChoice moe_tile(int64_t n, int top_k, int E, int steps, int N, bool gated) {
+  if (n == 0) return {128, 128, 1};
+  const double mean = tq_pairs_per_woken_expert(n, top_k, E);
+  return choose_tile(typical_rows(n, top_k, E), n * top_k / mean, steps, N, gated, !gated, gated, !gated);
+}
+
+struct Routed {
+  int32_t *counts, *offsets, *sorted_pairs, *tiles, *num_tiles;
+};
+Routed carve_routed(Carver& c, const MoePlan& m, int E) {
+  Routed r{};
+  if (m.arm == kPairs) return r;
+  r.counts = c.take<int32_t>(E);
+  r.offsets = c.take<int32_t>(E + 1);
+  r.sorted_pairs = c.take<int32_t>(m.P);
+  r.tiles = c.take<int32_t>(3 * m.cap);
+  r.num_tiles = c.take<int32_t>(1);
+  return r;
+}
+int route_pairs(const MoePlan& m, const Routed& r, const int32_t* ids, int E, int* err, cudaStream_t s) {
+  if (m.arm == kPairs) return TQ_OK;
+  return launch_route_tile_map(ids, static_cast<int>(m.P), E, m.tile_m, r.counts, r.offsets, r.sorted_pairs, r.tiles,
+                               r.num_tiles, m.cap, err, s);
+}
+
+struct ProductPlan {
+  MoePlan m;
+  TileChoice tile;
+  Routed routed;
+  float* part;
+  size_t bytes;
+};
+ProductPlan plan_moe(void* base, int64_t n, int top_k, int E, int K, int N) {
+  ProductPlan p;
+  p.tile = moe_tile(n, top_k, E, blocks_of(K), N, false);
+  p.m = plan_arm(n, top_k, E, p.tile);
+  if (p.m.arm != kTiles) p.tile.splits = 1;
+  Carver c{static_cast<uint8_t*>(base)};
+  p.routed = carve_routed(c, p.m, E);
+  p.part = c.take<float>(static_cast<size_t>(p.tile.splits) * p.m.P * N);
+  p.bytes = c.used;
+  return p;
+}
+
+struct MlpPlan {
+  MoePlan m;
+  TileChoice down;
+  Routed routed;
+  float *gate_up, *part;   // gate_up: the few-rows kernel's sums
+  uint8_t* h;
+  float* h_scales;
+  size_t bytes;
+};
+MlpPlan plan_mlp(void* base, int64_t n, int top_k, int E, int H, int I) {
+  MlpPlan p;
+  // one tile map for both products, by the gate and up projections'
+  const TileChoice gu = moe_tile(n, top_k, E, blocks_of(H), I, true);
+  p.m = plan_arm(n, top_k, E, gu);
+  p.down = moe_tile(n, top_k, E, blocks_of(I), H, false);
+  if (p.m.arm != kTiles) p.down.splits = 1;
+  p.down.tile_m = p.m.tile_m;
+  if (p.down.tile_m > 128) p.down.cols = 128;
+  Carver c{static_cast<uint8_t*>(base)};
+  p.routed = carve_routed(c, p.m, E);
+  p.gate_up = p.m.arm == kTiles ? nullptr : c.take<float>(static_cast<size_t>(p.m.P) * 2 * I);
+  p.h = c.take<uint8_t>(static_cast<size_t>(p.m.P) * I);
+  p.h_scales = c.take<float>(static_cast<size_t>(p.m.P) * (I / kFp8Block));
+  p.part = c.take<float>(static_cast<size_t>(p.down.splits) * p.m.P * H);
+  p.bytes = c.used;
+  return p;
+}
+
+// One product of a routed chain, its rows gathered from the tokens or in slot order,
+// its output by pair or by slot.
+struct Operand {
+  const uint8_t* codes;
+  const float* scales;
+};
+int routed_product(const MoePlan& m, const Routed& r, const int32_t* ids, Operand x, int64_t x_rows, bool gather,
+                   Operand w, int top_k, int E, int K, int N, TileChoice tile, bool scatter, float* out, int* err,
+                   cudaStream_t s) {
+  const int steps = blocks_of(K);
+  if (m.arm == kTiles) {
+    Fp8Gemm g{x.codes, x.scales, x_rows, w.codes, w.scales, r.sorted_pairs, r.tiles, r.num_tiles, m.cap, m.P, top_k, E,
+              K, N, gather, scatter, false, m.tile_m, tile.cols, tile.splits, out, TQ_FP32, nullptr, nullptr, err};
+    return launch_fp8_gemm(g, s);
+  }
+  FewRows f{};
+  f.w = w.codes;
+  f.x = x.codes;
+  f.w_scales = w.scales;
+  f.x_scales = x.scales;
+  f.tiles = r.tiles;
+  f.num_tiles = r.num_tiles;
+  f.sorted_pairs = r.sorted_pairs;
+  f.ids = m.arm == kPairs ? ids : nullptr;
+  f.row_bytes = f.x_stride = K;
+  f.M = static_cast<int>(m.P);
+  f.E = E;
+  f.N = N;
+  f.top_k = top_k;
+  f.steps = steps;
+  f.w_blocks = (N + kFp8Block - 1) / kFp8Block;
+  f.gather = gather;
+  f.scatter = scatter;
+  f.y = out;
+  f.y_type = TQ_FP32;
+  f.err = err;
+  return launch_few_rows(f, kFewRowsFp8, false, m.arm == kPairs ? 8 : m.tile_m, m.arm == kPairs ? m.P : m.cap, s);
+}
+
+}  // namespace
+}  // namespace tq
+
+using namespace tq;
+
+extern "C" {
+
+int tq_fp8_quantize(const void* x, int x_type, int64_t x_stride, int E, int64_t n, int K, int rows_per_block,
+                    uint8_t* codes, float* scales, tq_stream_t stream) {
+  if (E < 0 || n < 0 || n >= kMaxIndex || E * n >= kMaxIndex || bad_k(K) || bad_type(x_type) ||
+      bad_blocking(rows_per_block) || x_stride < K || (rows_per_block != 1 && E > 65535))
+    return TQ_ERR_INVALID_ARG;
+  const int64_t rows = E * n;
+  if (bad_output(rows, x_stride) || (x_stride % 16 * static_cast<int64_t>(type_size(x_type))) % 16 != 0)
+    return TQ_ERR_INVALID_ARG;
+  if (rows > 0 && (!x || !codes || !scales || !aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4)))
+    return TQ_ERR_INVALID_ARG;
+  if (rows_per_block != 1 && (n + kFp8Block - 1) / kFp8Block > 65535) return TQ_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int rc = require_sm103(s);
+  if (rc != TQ_OK || rows == 0) return rc;
+  return rows_per_block == 1
+             ? launch_fp8_quantize_rows(x, x_type, x_stride, rows, K, codes, scales, s)
+             : launch_fp8_quantize_blocks(x, x_type, x_stride, E, static_cast<int>(n), K, codes, scales, s);
+}
+
+int tq_fp8_dequantize(const uint8_t* codes, const float* scales, int E, int64_t n, int K, int rows_per_block, void* out,
+                      int out_type, tq_stream_t stream) {
+  if (E < 0 || n < 0 || n >= kMaxIndex || E * n >= kMaxIndex || bad_k(K) || bad_type(out_type) ||
+      bad_blocking(rows_per_block) || bad_output(E * n, K))
+    return TQ_ERR_INVALID_ARG;
+  if (E * n > 0 && (!codes || !scales || !out || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(out, 16)))
+    return TQ_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int rc = require_sm103(s);
+  if (rc != TQ_OK || E * n == 0) return rc;
+  return launch_fp8_dequantize(codes, scales, E, n, K, rows_per_block, out, out_type, s);
+}
+
+size_t tq_fp8_linear_workspace_size(int64_t n, int K, int N) {
+  if (n < 0 || n >= kMaxIndex || bad_matrix(1, K, N) || bad_output(n, N)) return 0;
+  return plan_linear(nullptr, n, K, N).bytes;
+}
+
+int tq_fp8_linear(const uint8_t* x, const float* x_scales, const uint8_t* w, const float* w_scales, int64_t n, int K,
+                  int N, void* workspace, size_t workspace_bytes, void* y, int y_type, tq_stream_t stream) {
+  if (n < 0 || n >= kMaxIndex || bad_matrix(1, K, N) || bad_output(n, N) || bad_type(y_type)) return TQ_ERR_INVALID_ARG;
+  if (n > 0 && (!x || !x_scales || !w || !w_scales || !y || !aligned(x, 16) || !aligned(w, 16) || !aligned(x_scales, 4) ||
+                !aligned(w_scales, 4) || !aligned(y, type_size(y_type))))
+    return TQ_ERR_INVALID_ARG;
+  const LinearPlan l = plan_linear(workspace, n, K, N);
+  const bool splits = !l.few && l.tile.splits > 1;
+  if (n > 0 && splits && bad_workspace(workspace, workspace_bytes, l.bytes)) return TQ_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int rc = require_sm103(s);
+  if (rc != TQ_OK || n == 0) return rc;
+  int* err = error_word(&rc);
+  if (!err) return rc;
+  if (l.few) {
+    FewRows f{};
+    f.w = w;
+    f.x = x;
+    f.w_scales = w_scales;
+    f.x_scales = x_scales;
+    f.row_bytes = f.x_stride = K;
+    f.M = static_cast<int>(n);
+    f.E = f.top_k = 1;
+    f.N = N;
+    f.steps = blocks_of(K);
+    f.w_blocks = (N + kFp8Block - 1) / kFp8Block;
+    f.y = y;
+    f.y_type = y_type;
+    f.err = err;
+    return launch_few_rows(f, kFewRowsFp8, false, n <= 8 ? 8 : 16, 1, s);
+  }
+  Fp8Gemm g{x, x_scales, n, w, w_scales, nullptr, nullptr, nullptr, (n + l.tile.tile_m - 1) / l.tile.tile_m, n, 1, 1, K, N,
+            false, false, false, l.tile.tile_m, l.tile.cols, l.tile.splits, splits ? l.part : y,
+            splits ? TQ_FP32 : y_type, nullptr, nullptr, err};
+  rc = launch_fp8_gemm(g, s);
+  if (rc != TQ_OK || !splits) return rc;
+  return launch_fp4_combine(l.part, n * N, l.tile.splits, nullptr, nullptr, nullptr, nullptr, n, 1, 1, N, y, y_type, s);
+}
+
+size_t tq_fp8_moe_workspace_size(int64_t n, int top_k, int E, int K, int N) {
+  if (bad_moe_shape(n, top_k, E) || bad_matrix(E, K, N) || bad_output(n * top_k, N)) return 0;
+  return plan_moe(nullptr, n, top_k, E, K, N).bytes;
+}
+
+int tq_fp8_moe_forward(const uint8_t* x, const float* x_scales, const uint8_t* w, const float* w_scales,
+                       const int32_t* topk_ids, const float* topk_w, int64_t n, int top_k, int E, int K, int N,
+                       void* workspace, size_t workspace_bytes, void* y, int y_type, tq_stream_t stream) {
+  if (bad_moe_shape(n, top_k, E) || bad_matrix(E, K, N) || bad_output(n * top_k, N) || bad_type(y_type))
+    return TQ_ERR_INVALID_ARG;
+  if (n > 0 && (!x || !x_scales || !w || !w_scales || !topk_ids || !topk_w || !y || !aligned(x, 16) || !aligned(w, 16) ||
+                !aligned(x_scales, 4) || !aligned(w_scales, 4) || !aligned(y, type_size(y_type))))
+    return TQ_ERR_INVALID_ARG;
+  const ProductPlan p = plan_moe(workspace, n, top_k, E, K, N);
+  if (n > 0 && bad_workspace(workspace, workspace_bytes, p.bytes)) return TQ_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int rc = require_sm103(s);
+  if (rc != TQ_OK || n == 0) return rc;
+  int* err = error_word(&rc);
+  if (!err) return rc;
+  rc = route_pairs(p.m, p.routed, topk_ids, E, err, s);
+  if (rc != TQ_OK) return rc;
+  rc = routed_product(p.m, p.routed, topk_ids, {x, x_scales}, n, true, {w, w_scales}, top_k, E, K, N, p.tile, true, p.part,
+                      err, s);
+  if (rc != TQ_OK) return rc;
+  return launch_fp4_combine(p.part, p.m.P * N, p.tile.splits, topk_ids, topk_w, nullptr, nullptr, n, top_k, E, N, y,
+                            y_type, s);
+}
+
+size_t tq_fp8_moe_mlp_workspace_size(int64_t n, int top_k, int E, int H, int I) {
+  if (bad_moe_shape(n, top_k, E) || I < 1 || I > (1 << 29) || I % kFp8Block != 0 || bad_matrix(E, H, 2ll * I) ||
+      bad_matrix(E, I, H) || bad_output(n * top_k, 2ll * I) || bad_output(n * top_k, H))
+    return 0;
+  return plan_mlp(nullptr, n, top_k, E, H, I).bytes;
+}
+
+int tq_fp8_moe_mlp_forward(const uint8_t* x, const float* x_scales, const uint8_t* w_gu, const float* gu_scales,
+                           const uint8_t* w_down, const float* down_scales, const int32_t* topk_ids,
+                           const float* topk_w, int64_t n, int top_k, int E, int H, int I, void* workspace,
+                           size_t workspace_bytes, void* y, int y_type, tq_stream_t stream) {
+  if (tq_fp8_moe_mlp_workspace_size(n, top_k, E, H, I) == 0 || bad_type(y_type)) return TQ_ERR_INVALID_ARG;
+  if (n > 0 && (!x || !x_scales || !w_gu || !gu_scales || !w_down || !down_scales || !topk_ids || !topk_w || !y ||
+                !aligned(x, 16) || !aligned(w_gu, 16) || !aligned(w_down, 16) || !aligned(x_scales, 4) ||
+                !aligned(gu_scales, 4) || !aligned(down_scales, 4) || !aligned(y, type_size(y_type))))
+    return TQ_ERR_INVALID_ARG;
+  const MlpPlan p = plan_mlp(workspace, n, top_k, E, H, I);
+  if (n > 0 && bad_workspace(workspace, workspace_bytes, p.bytes)) return TQ_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int rc = require_sm103(s);
+  if (rc != TQ_OK || n == 0) return rc;
+  int* err = error_word(&rc);
+  if (!err) return rc;
+  const MoePlan& m = p.m;
+  const Routed& r = p.routed;
+  rc = route_pairs(m, r, topk_ids, E, err, s);
+  if (rc != TQ_OK) return rc;
+  if (m.arm == kTiles) {
+    Fp8Gemm g{x, x_scales, n, w_gu, gu_scales, r.sorted_pairs, r.tiles, r.num_tiles, m.cap, m.P, top_k, E, H, I, true,
+              false, true, m.tile_m, 128, 1, nullptr, TQ_FP32, p.h, p.h_scales, err};
+    rc = launch_fp8_gemm(g, s);
+  } else {
+    rc = routed_product(m, r, topk_ids, {x, x_scales}, n, true, {w_gu, gu_scales}, top_k, E, H, 2 * I, {}, false,
+                        p.gate_up, err, s);
+    if (rc == TQ_OK) rc = launch_fp8_swiglu(p.gate_up, m.P, I, p.h, p.h_scales, s);
+  }
+  if (rc != TQ_OK) return rc;
+  rc = routed_product(m, r, topk_ids, {p.h, p.h_scales}, m.P, false, {w_down, down_scales}, top_k, E, I, H, p.down, true,
+                      p.part, err, s);
+  if (rc != TQ_OK) return rc;
+  return launch_fp4_combine(p.part, m.P * H, p.down.splits, topk_ids, topk_w, nullptr, nullptr, n, top_k, E, H, y, y_type,
+                            s);
+}
+
+}  // extern "C"

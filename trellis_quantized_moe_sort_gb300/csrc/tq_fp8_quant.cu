@@ -1,0 +1,244 @@
+// 8-bit block-scaled values: quantise (rows, and matrices in blocks of 128 x 128),
+// dequantise, and the SwiGLU experts' h from the gate and up sums of few rows.
+//
+// All of these move bytes: a thread takes 16 consecutive values, a block of 128 of a
+// row is eight neighbouring lanes, which share their maximum by three shuffles.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "tq_fp8.cuh"
+#include "tq_internal.h"
+
+namespace tq {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kThreads = 256;
+
+template <typename T>
+struct Piece {
+  uint4 raw[sizeof(T)];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) raw[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void open(float (&v)[16]) const {
+    const T* const t = reinterpret_cast<const T*>(raw);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = widen(t[i]);
+  }
+};
+
+__device__ __forceinline__ float top_of_eight(float top) {
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+  return top;
+}
+
+// A warp takes 512 values of a row at a time, the next ones' loads in flight.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+fp8_quantize_rows_kernel(const T* __restrict__ x, long long stride, long long n, int K, int step_rows, int step_chunks,
+                         uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int items = K / 16, chunks = (items + 31) / 32, blocks = (K + kFp8Block - 1) / kFp8Block;
+  const long long warp = blockIdx.x * (kThreads / 32ll) + (threadIdx.x >> 5);
+  long long row = warp / chunks;
+  int chunk = static_cast<int>(warp - row * chunks);
+  Piece<T> next = {};
+  if (row < n && chunk * 32 + lane < items) next.load(x + row * stride + 16 * (chunk * 32 + lane));
+  while (row < n) {
+    const Piece<T> piece = next;
+    const int item = chunk * 32 + lane;
+    const long long at = row;
+    row += step_rows;
+    chunk += step_chunks;
+    if (chunk >= chunks) {
+      chunk -= chunks;
+      ++row;
+    }
+    if (row < n && chunk * 32 + lane < items) next.load(x + row * stride + 16 * (chunk * 32 + lane));
+    float v[16];
+    piece.open(v);
+    const float top = top_of_eight(item < items ? fp8_top<16>(v) : 0.f);   // lanes past the row hold an old piece
+    if (item < items) {
+      const Fp8Scale s(top);
+      *reinterpret_cast<uint4*>(codes + at * K + 16ll * item) = fp8_codes16(v, s);
+      if ((lane & 7) == 0) scales[at * blocks + item / 8] = s.s;
+    }
+  }
+}
+
+// A block of threads takes 128 x 128 values, four pieces a thread held between the
+// maximum and the codes.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+fp8_quantize_blocks_kernel(const T* __restrict__ x, long long stride, int N, int K, uint8_t* __restrict__ codes,
+                           float* __restrict__ scales) {
+  __shared__ float tops[kThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int cb = blockIdx.x, rb = blockIdx.y;
+  const long long e = blockIdx.z;
+  const int col = cb * kFp8Block + 16 * (threadIdx.x % 8), row0 = rb * kFp8Block + threadIdx.x / 8;
+  Piece<T> piece[4] = {};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = row0 + 32 * i;
+    if (r < N && col < K) piece[i].load(x + (e * N + r) * stride + col);
+  }
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float v[16];
+    piece[i].open(v);
+    top = fmaxf(top, fp8_top<16>(v));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+  if (lane == 0) tops[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) top = fmaxf(top, tops[i]);
+  const Fp8Scale s(top);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = row0 + 32 * i;
+    if (r >= N || col >= K) continue;
+    float v[16];
+    piece[i].open(v);
+    *reinterpret_cast<uint4*>(codes + (e * N + r) * K + col) = fp8_codes16(v, s);
+  }
+  if (threadIdx.x == 0) scales[(e * gridDim.y + rb) * gridDim.x + cb] = s.s;
+}
+
+// A thread reads 16 codes and writes their values, one warp 512 of a row.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+fp8_dequantize_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scales, long long rows, int N, int K,
+                      int rows_per_block, T* __restrict__ out) {
+  pdl_wait();
+  pdl_trigger();
+  const int items = K / 16, blocks = (K + kFp8Block - 1) / kFp8Block;
+  const int row_blocks = (N + rows_per_block - 1) / rows_per_block;
+  const long long total = rows * items, step = static_cast<long long>(gridDim.x) * kThreads;
+  for (long long i = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x; i < total; i += step) {
+    const long long row = i / items, e = row / N;
+    const int item = static_cast<int>(i - row * items);
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(codes) + i);
+    const float s = __ldg(scales + (e * row_blocks + (row - e * N) / rows_per_block) * blocks + item / 8);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    T v[16];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 f = from_e4m3x2((w[j / 2] >> (16 * (j & 1))) & 0xffffu);
+      v[2 * j] = narrow<T>(__fmul_rn(f.x, s));
+      v[2 * j + 1] = narrow<T>(__fmul_rn(f.y, s));
+    }
+#pragma unroll
+    for (int j = 0; j < static_cast<int>(sizeof(T)); ++j)
+      reinterpret_cast<uint4*>(out)[i * sizeof(T) + j] = reinterpret_cast<const uint4*>(v)[j];
+  }
+}
+
+// h = silu(gate) * up of rows [rows][2 I], I a multiple of 128, in 8 bits.
+__global__ void __launch_bounds__(kThreads)
+fp8_swiglu_kernel(const float* __restrict__ gate_up, long long rows, int I, uint8_t* __restrict__ codes,
+                  float* __restrict__ scales) {
+  pdl_wait();
+  pdl_trigger();
+  const int items = I / 16;   // a multiple of 8: whole blocks of lanes
+  const long long total = rows * items, step = static_cast<long long>(gridDim.x) * kThreads;
+  const int lane = threadIdx.x & 31;
+  for (long long i0 = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x - lane; i0 < total; i0 += step) {
+    const long long i = i0 + lane;
+    float v[16] = {};
+    if (i < total) {
+      const long long row = i / items;
+      const float4* const g = reinterpret_cast<const float4*>(gate_up + row * 2 * I + 16 * (i - row * items));
+      const float4* const u = g + I / 4;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 a = __ldcs(g + j), b = __ldcs(u + j);
+        v[4 * j] = a.x / (1.f + expf(-a.x)) * b.x;
+        v[4 * j + 1] = a.y / (1.f + expf(-a.y)) * b.y;
+        v[4 * j + 2] = a.z / (1.f + expf(-a.z)) * b.z;
+        v[4 * j + 3] = a.w / (1.f + expf(-a.w)) * b.w;
+      }
+    }
+    const float top = top_of_eight(fp8_top<16>(v));
+    if (i < total) {
+      const Fp8Scale s(top);
+      reinterpret_cast<uint4*>(codes)[i] = fp8_codes16(v, s);
+      if ((lane & 7) == 0) scales[i / 8] = s.s;
+    }
+  }
+}
+
+int blocks_for(long long warps_of_work) {
+  const long long per = kThreads / 32;
+  return static_cast<int>(std::max<long long>(
+      1, std::min<long long>((warps_of_work + per - 1) / per, static_cast<long long>(sm_count()) * 8)));
+}
+
+template <typename F>
+int by_type(int type, F&& f) {
+  switch (type) {
+    case TQ_FP32: return f(static_cast<float*>(nullptr));
+    case TQ_BF16: return f(static_cast<__nv_bfloat16*>(nullptr));
+    default: return f(static_cast<__half*>(nullptr));
+  }
+}
+
+}  // namespace
+
+int launch_fp8_quantize_rows(const void* x, int type, int64_t stride, int64_t n, int K, uint8_t* codes, float* scales,
+                             cudaStream_t s) {
+  const int chunks = (K / 16 + 31) / 32;
+  const int blocks = blocks_for(n * chunks), warps = blocks * (kThreads / 32);
+  const int st = by_type(type, [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    return launch_pdl(fp8_quantize_rows_kernel<T>, dim3(blocks), dim3(kThreads), 0, s, static_cast<const T*>(x),
+                      static_cast<long long>(stride), static_cast<long long>(n), K, warps / chunks, warps % chunks,
+                      codes, scales);
+  });
+  if (st == TQ_OK) count_launch(kCntFp8Quantize);
+  return st;
+}
+
+int launch_fp8_quantize_blocks(const void* x, int type, int64_t stride, int E, int N, int K, uint8_t* codes,
+                               float* scales, cudaStream_t s) {
+  const dim3 grid((K + kFp8Block - 1) / kFp8Block, (N + kFp8Block - 1) / kFp8Block, E);
+  const int st = by_type(type, [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    return launch_pdl(fp8_quantize_blocks_kernel<T>, grid, dim3(kThreads), 0, s, static_cast<const T*>(x),
+                      static_cast<long long>(stride), N, K, codes, scales);
+  });
+  if (st == TQ_OK) count_launch(kCntFp8Quantize);
+  return st;
+}
+
+int launch_fp8_dequantize(const uint8_t* codes, const float* scales, int E, int64_t N, int K, int rows_per_block,
+                          void* out, int type, cudaStream_t s) {
+  const int st = by_type(type, [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    return launch_pdl(fp8_dequantize_kernel<T>, dim3(blocks_for(E * N * (K / 16) / 32 + 1)), dim3(kThreads), 0, s, codes,
+                      scales, static_cast<long long>(E) * N, static_cast<int>(N), K, rows_per_block,
+                      static_cast<T*>(out));
+  });
+  if (st == TQ_OK) count_launch(kCntFp8Dequantize);
+  return st;
+}
+
+int launch_fp8_swiglu(const float* gate_up, int64_t rows, int I, uint8_t* codes, float* scales, cudaStream_t s) {
+  const int st = launch_pdl(fp8_swiglu_kernel, dim3(blocks_for((rows * (I / 16) + 31) / 32)), dim3(kThreads), 0, s,
+                            gate_up, static_cast<long long>(rows), I, codes, scales);
+  if (st == TQ_OK) count_launch(kCntFp8Swiglu);
+  return st;
+}
+
+}  // namespace tq

@@ -23,7 +23,8 @@ enum Counter {
   kCntRouteTileMap, kCntClear, kCntSwiglu,
   // from here on only in tq_launch_counts_all
   kCntRouterScored, kCntRouterScoredBackward, kCntFp4Quantize, kCntFp4Dequantize, kCntFp4TileScales, kCntFp4Stage,
-  kCntFp4Gemm, kCntFp4Combine, kCntFp4Swiglu, kCntFp4Gemv, kCntNum
+  kCntFp4Gemm, kCntFp4Combine, kCntFp4Swiglu, kCntFp4Gemv, kCntNorm, kCntNormBackward, kCntNormWeight, kCntFp8Quantize,
+  kCntFp8Dequantize, kCntFp8Swiglu, kCntFp8Gemm, kCntFewRows, kCntGatedGemm, kCntSwigluGrad, kCntNum
 };
 static_assert(kCntRouterScored == TQ_NUM_LAUNCH_COUNTERS, "counter layout of tq_launch_counts");
 static_assert(kCntNum == TQ_NUM_ALL_LAUNCH_COUNTERS, "counter layout of tq_launch_counts_all");
@@ -217,6 +218,96 @@ int launch_fp4_gemv(const Fp4Gemv& g, cudaStream_t s);
 // there are few weight rows.
 inline bool fp4_takes_pairs(int tile_m) { return tile_m >= 128; }
 int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s);
+
+// The norm and its gradient (tq_norm.cu).  Rows of the outputs are dense.
+struct NormArgs {
+  const void *x, *residual, *weight;
+  void *residual_out, *y;
+  float* rstd;
+  uint8_t* codes;
+  float* scales;
+  long long x_stride, residual_stride, n;
+  int K, w_type;
+  float eps;
+};
+struct NormGradArgs {
+  const void *grad_y, *x, *weight, *grad_residual;
+  const float* rstd;
+  void* grad_x;
+  float* part;   // [blocks][K] shares of grad_weight, or nullptr
+  long long grad_y_stride, x_stride, grad_residual_stride, n;
+  int K, w_type;
+};
+
+// 8-bit block-scaled values (tq_fp8.cuh).
+int launch_fp8_quantize_rows(const void* x, int type, int64_t stride, int64_t n, int K, uint8_t* codes, float* scales,
+                             cudaStream_t s);
+int launch_fp8_quantize_blocks(const void* x, int type, int64_t stride, int E, int N, int K, uint8_t* codes,
+                               float* scales, cudaStream_t s);
+int launch_fp8_dequantize(const uint8_t* codes, const float* scales, int E, int64_t N, int K, int rows_per_block,
+                          void* out, int type, cudaStream_t s);
+// h = silu(gate) * up of rows [rows][2 I] in fp32, kept in 8 bits.
+int launch_fp8_swiglu(const float* gate_up, int64_t rows, int I, uint8_t* codes, float* scales, cudaStream_t s);
+
+// Product of 8-bit rows with 8-bit matrices on the tensor cores (tq_tile_gemm.cuh).
+struct Fp8Gemm {
+  const uint8_t* x;             // codes [x_rows][K]
+  const float* x_scales;        // [x_rows][K / 128]
+  int64_t x_rows;
+  const uint8_t* w;             // codes [E][N][K], gated [E][2 N][K]
+  const float* w_scales;        // [E][N / 128][K / 128]
+  const int32_t *sorted_pairs, *tiles, *num_tiles;   // nullptr: one matrix, row = slot
+  int64_t cap;                  // capacity of tiles, or the number of m-tiles
+  int64_t M;                    // slots
+  int top_k, E, K, N;
+  bool gather;                  // x holds token rows
+  bool scatter;                 // output rows are pairs, else slots
+  bool gated;                   // h in codes and scales, else y
+  int tile_m;                   // 128, or 256: pairs of CTAs
+  int cols;                     // half the columns of a unit: 128, 64 or 32 (128 in pairs and gated)
+  int splits;                   // y is fp32 [splits][M][N]
+  void* y;
+  int y_type;
+  uint8_t* codes;
+  float* scales;
+  int* err;
+};
+int launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s);
+
+// Product of 16-bit matrices, D[M][N] = A B^T over K (tq_tile_gemm.cuh).
+struct GemmF16 {
+  int type;
+  const void* a;                // [M][K], or [K][M] with a_mn
+  int64_t a_stride;
+  const void* b;                // [N][K] (gated: [2 N][K]), or [K][N] with b_mn
+  int64_t b_stride;
+  int64_t M, N, K;
+  bool a_mn, b_mn, gated;       // a_mn only with b_mn, gated with neither
+  int tile_m, cols, splits;
+  void* y;                      // [M][N] of y_type, or fp32 [splits][M][N]
+  int y_type;
+  float* gate_up;               // gated: fp32 [M][2 N], or nullptr
+  int* err;
+};
+int launch_gemm_f16(const GemmF16& g, cudaStream_t s);
+
+// Products with few activation rows a matrix (tq_few_rows.cu).
+struct FewRows {
+  const uint8_t* w;             // [E][N] rows, gated [2 N]
+  const uint8_t* x;
+  const float *w_scales, *x_scales;   // 8 bits
+  const int32_t *tiles, *num_tiles, *sorted_pairs;   // a unit = an m-tile
+  const int32_t* ids;           // without tiles: a unit = a pair
+  long long row_bytes, x_stride;   // bytes: of a row's values; between rows of x
+  int M, E, N, top_k, steps, w_blocks;
+  int gather, scatter;
+  void* y;
+  int y_type;
+  float* gate_up;
+  int* err;
+};
+constexpr int kFewRowsFp8 = -1;   // `type` of the 8-bit product
+int launch_few_rows(const FewRows& p, int type, bool gated, int cols, int64_t units, cudaStream_t s);
 
 // TQ_FORCE_ARM (auto|gemv|grouped|measured) applied to an automatic pin.
 int env_pin(int pin);

@@ -78,6 +78,22 @@ WRAPPER(tq_fp4_moe_mlp_forward, "pilppppppippppliiiiplpip", PTR(0), INT(1), v[2]
         PTR(7), PTR(8), INT(9), PTR(10), PTR(11), PTR(12), PTR(13), v[14], INT(15), INT(16), INT(17), INT(18), PTR(19),
         (size_t)v[20], PTR(21), INT(22), STREAM(23))
 
+WRAPPER(tq_rms_norm, "pilplpiflipppppp", PTR(0), INT(1), v[2], PTR(3), v[4], PTR(5), INT(6), f, v[8], INT(9), PTR(10),
+        PTR(11), PTR(12), PTR(13), PTR(14), STREAM(15))
+WRAPPER(tq_rms_norm_backward, "plpilpipplliplppp", PTR(0), v[1], PTR(2), INT(3), v[4], PTR(5), INT(6), PTR(7), PTR(8),
+        v[9], v[10], INT(11), PTR(12), (size_t)v[13], PTR(14), PTR(15), STREAM(16))
+WRAPPER(tq_fp8_quantize, "pililiippp", PTR(0), INT(1), v[2], INT(3), v[4], INT(5), INT(6), PTR(7), PTR(8), STREAM(9))
+WRAPPER(tq_fp8_dequantize, "ppiliipip", PTR(0), PTR(1), INT(2), v[3], INT(4), INT(5), PTR(6), INT(7), STREAM(8))
+WRAPPER(tq_fp8_linear, "ppppliiplpip", PTR(0), PTR(1), PTR(2), PTR(3), v[4], INT(5), INT(6), PTR(7), (size_t)v[8],
+        PTR(9), INT(10), STREAM(11))
+WRAPPER(tq_fp8_moe_forward, "ppppppliiiiplpip", PTR(0), PTR(1), PTR(2), PTR(3), PTR(4), PTR(5), v[6], INT(7),
+        INT(8), INT(9), INT(10), PTR(11), (size_t)v[12], PTR(13), INT(14), STREAM(15))
+WRAPPER(tq_fp8_moe_mlp_forward, "ppppppppliiiiplpip", PTR(0), PTR(1), PTR(2), PTR(3), PTR(4), PTR(5), PTR(6),
+        PTR(7), v[8], INT(9), INT(10), INT(11), INT(12), PTR(13), (size_t)v[14], PTR(15), INT(16), STREAM(17))
+WRAPPER(tq_swiglu_linear, "pilpliippp", PTR(0), INT(1), v[2], PTR(3), v[4], INT(5), INT(6), PTR(7), PTR(8), STREAM(9))
+WRAPPER(tq_swiglu_linear_backward, "pilpppliiplppp", PTR(0), INT(1), v[2], PTR(3), PTR(4), PTR(5), v[6], INT(7),
+        INT(8), PTR(9), (size_t)v[10], PTR(11), PTR(12), STREAM(13))
+
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))call_##name, METH_FASTCALL, NULL}
 #define BIND(name)                                         \
   if (!strcmp(which, #name)) {                             \
@@ -97,6 +113,15 @@ static PyObject* bind(PyObject* self, PyObject* args) {
   BIND(tq_fp4_linear)
   BIND(tq_fp4_moe_forward)
   BIND(tq_fp4_moe_mlp_forward)
+  BIND(tq_rms_norm)
+  BIND(tq_rms_norm_backward)
+  BIND(tq_fp8_quantize)
+  BIND(tq_fp8_dequantize)
+  BIND(tq_fp8_linear)
+  BIND(tq_fp8_moe_forward)
+  BIND(tq_fp8_moe_mlp_forward)
+  BIND(tq_swiglu_linear)
+  BIND(tq_swiglu_linear_backward)
   PyErr_Format(PyExc_KeyError, "no wrapper of %s", which);
   return NULL;
 }
@@ -109,6 +134,15 @@ static PyMethodDef methods[] = {{"bind", bind, METH_VARARGS, NULL},
                                 METHOD(tq_fp4_linear),
                                 METHOD(tq_fp4_moe_forward),
                                 METHOD(tq_fp4_moe_mlp_forward),
+                                METHOD(tq_rms_norm),
+                                METHOD(tq_rms_norm_backward),
+                                METHOD(tq_fp8_quantize),
+                                METHOD(tq_fp8_dequantize),
+                                METHOD(tq_fp8_linear),
+                                METHOD(tq_fp8_moe_forward),
+                                METHOD(tq_fp8_moe_mlp_forward),
+                                METHOD(tq_swiglu_linear),
+                                METHOD(tq_swiglu_linear_backward),
                                 {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tqcall", NULL, -1, methods, NULL, NULL, NULL, NULL};
