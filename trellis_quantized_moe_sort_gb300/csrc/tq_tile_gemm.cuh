@@ -42,11 +42,11 @@ constexpr int kRows = 128;                    // rows of A per CTA
 constexpr int kStepBytes = 128;               // of a row and step: one swizzle row
 constexpr int kABytes = kRows * kStepBytes;
 constexpr int kMaxStages = 12, kMaxAcc = 8;
-constexpr int kThreads = 384;                 // warps 0-3: load A, load B, MMA, none; 4-11: epilogue
-constexpr int kWarpA = 0, kWarpB = 1, kWarpMma = 2, kWarpEpi0 = 4, kEpiWarps = 8;
+constexpr int kThreads = 384;                 // warps 0-3: load A, load B, MMA, load A's gathered rows; 4-11: epilogue
+constexpr int kWarpA = 0, kWarpB = 1, kWarpMma = 2, kWarpA2 = 3, kWarpEpi0 = 4, kEpiWarps = 8;
 constexpr int kSmemLimit = 232448;
 constexpr int kNumBars = 2 * kMaxStages + 2 * kMaxAcc + 1;
-constexpr int kPitch = 33;                    // floats per row of an epilogue warp's 32 x 32 turning block
+constexpr int kPitch = 33;                    // floats per row of an epilogue warp's 32 x 32 turning block (or 32 x 128 bytes)
 constexpr int kTurnBytes = kEpiWarps * 32 * kPitch * 4;
 constexpr int kListBytes = kRows * 4;         // rows of A that a CTA gathers
 constexpr int kTopBytes = 2 * 2 * kRows * 4;  // two buffers of both column halves' largest magnitudes
@@ -212,7 +212,10 @@ __device__ __forceinline__ uint32_t of_cta(uint32_t addr, uint32_t rank) {
   return r;
 }
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  // No memory of this thread is handed over, only tensor memory that it has read: the
+  // cluster-wide release, which waits for the thread's outstanding accesses, would cost
+  // more than a step (8192 rows 4096 -> 4096: 237 us, and 129 without it).
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -301,51 +304,78 @@ __device__ __forceinline__ int pair_of(const Params& p, int slot, int where) {
   return -1;
 }
 
+// Copies of four rows that CTA `rank` gathers of a tile's rows, and how many of `n`
+// copies a warp takes: `share` from the lead-th of every eight.
+__device__ __forceinline__ int gathered(int rows, int rank) {
+  return (max(0, min(kRows, rows - rank * kRows)) + 3) / 4;
+}
+__device__ __forceinline__ int shared_copies(int n, int lead, int share) {
+  return n / 8 * share + max(0, min(share, n % 8 - lead));
+}
+
 __device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
 
-// 32 values of this lane's row to columns [col, col + 32) of y, those below N.
-// `row` < 0: none.  Rows that start on 16-byte boundaries take them as vectors, one
-// row a lane; others go through the warp's turning block, so that a store writes 32
-// neighbours of one row (one element a lane and row, 12.3M results of 3001 x 4099
-// would be as many 32-byte sectors).
-template <typename T>
-__device__ __forceinline__ void store32(T* y, const float (&v)[32], long long row, int col, int N, bool aligned,
-                                        float* turn, int lane) {
-  constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+// kCount values of this lane's row to columns [col, col + kCount) of y, those below N;
+// `row` < 0: none.  A lane's own stores would be 32 rows' sectors an instruction (128 x
+// 256 results a CTA: 4000 cycles), so the warp turns blocks of 32 rows x 128 bytes in
+// shared memory and stores whole lines of them, 16 bytes a lane.  Rows that do not
+// start on 16-byte boundaries are turned by single values, 32 columns at a time.
+template <typename T, int kCount>
+__device__ __forceinline__ void store_columns(T* y, const float (&v)[kCount], long long row, int col, int N, bool aligned,
+                                              uint8_t* turn, int lane) {
+  constexpr int kVec = 16 / static_cast<int>(sizeof(T)), kLine = 8 * kVec;   // values of 16 and of 128 bytes
+  constexpr int kBlock = kLine < kCount ? kLine : kCount, kParts = kBlock / kVec;
   if (aligned) {
-    if (row < 0) return;
-    T* const out = y + row * N + col;
+    constexpr int kRowsOnce = 32 / kParts;
 #pragma unroll
-    for (int i = 0; i < 32; i += kVec) {
-      if (col + i >= N) break;   // N is a multiple of kVec
-      T t[kVec];
+    for (int b = 0; b < kCount; b += kBlock) {
+      __syncwarp();
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) t[j] = narrow<T>(v[i + j]);
-      uint4 o;
-      memcpy(&o, t, 16);
-      *reinterpret_cast<uint4*>(out + i) = o;
+      for (int i = 0; i < kParts; ++i) {
+        T t[kVec];
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) t[j] = narrow<T>(v[b + i * kVec + j]);
+        uint4 o;
+        memcpy(&o, t, 16);
+        // neighbouring rows start in different banks
+        *reinterpret_cast<uint4*>(turn + 128 * lane + 16 * (i ^ (lane & 7))) = o;
+      }
+      __syncwarp();
+      const int part = lane % kParts, at = col + b + part * kVec;
+#pragma unroll
+      for (int r0 = 0; r0 < 32; r0 += kRowsOnce) {
+        const int r = r0 + lane / kParts;
+        const long long to = __shfl_sync(0xffffffffu, row, r);
+        const uint4 o = *reinterpret_cast<const uint4*>(turn + 128 * r + 16 * (part ^ (r & 7)));
+        if (to >= 0 && at < N) *reinterpret_cast<uint4*>(y + to * N + at) = o;   // N is a multiple of kVec
+      }
     }
     return;
   }
-  __syncwarp();
+  float* const floats = reinterpret_cast<float*>(turn);
 #pragma unroll
-  for (int i = 0; i < 32; ++i) turn[lane * kPitch + i] = v[i];
-  __syncwarp();
-  const bool in = col + lane < N;
+  for (int b = 0; b < kCount; b += 32) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) floats[lane * kPitch + i] = v[b + i];
+    __syncwarp();
+    const bool in = col + b + lane < N;
 #pragma unroll 4
-  for (int r = 0; r < 32; ++r) {
-    const long long to = __shfl_sync(0xffffffffu, row, r);
-    if (to >= 0 && in) y[to * N + col + lane] = narrow<T>(turn[r * kPitch + lane]);
+    for (int r = 0; r < 32; ++r) {
+      const long long to = __shfl_sync(0xffffffffu, row, r);
+      if (to >= 0 && in) y[to * N + col + b + lane] = narrow<T>(floats[r * kPitch + lane]);
+    }
   }
 }
-__device__ __forceinline__ void store32_typed(void* y, int type, const float (&v)[32], long long row, int col, int N,
-                                              bool aligned, float* turn, int lane) {
+template <int kCount>
+__device__ __forceinline__ void store_typed(void* y, int type, const float (&v)[kCount], long long row, int col, int N,
+                                            bool aligned, uint8_t* turn, int lane) {
   if (type == TQ_FP32)
-    store32(static_cast<float*>(y), v, row, col, N, aligned, turn, lane);
+    store_columns(static_cast<float*>(y), v, row, col, N, aligned, turn, lane);
   else if (type == TQ_BF16)
-    store32(static_cast<__nv_bfloat16*>(y), v, row, col, N, aligned, turn, lane);
+    store_columns(static_cast<__nv_bfloat16*>(y), v, row, col, N, aligned, turn, lane);
   else
-    store32(static_cast<__half*>(y), v, row, col, N, aligned, turn, lane);
+    store_columns(static_cast<__half*>(y), v, row, col, N, aligned, turn, lane);
 }
 
 template <bool k8, bool kPair, int kCols, bool kAMn, bool kBMn, int kEpi>
@@ -355,6 +385,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
   static_assert(!k8 || (!kAMn && !kBMn), "8-bit operands keep K along their rows");
   static_assert(kEpi != kGated8 || (k8 && kCols == 128), "a block of h is one unit's columns");
   static_assert(kEpi == kStore || kCols >= 64, "");
+  static_assert(k8 || kCols >= 64, "16-bit sums are read 64 columns at a time");
   static_assert(!kBMn || kCols >= 64, "");
   constexpr bool kGated = kEpi != kStore, kSplitRegisters = splits_registers(k8, kCols);
   constexpr int kN = 2 * kCols;                                   // the MMA's N
@@ -382,7 +413,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
-      mbar_init(bar_full + 8 * s, 2);
+      mbar_init(bar_full + 8 * s, p.gather ? 3 : 2);
       mbar_init(bar_empty + 8 * s, 1);
     }
     for (int a = 0; a < p.accs; ++a) {
@@ -412,8 +443,15 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
 
   if (warp < kWarpEpi0) {
   if constexpr (kSplitRegisters) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-  if (warp == kWarpA || warp == kWarpB) {
-    const bool is_a = warp == kWarpA;
+  if (warp != kWarpMma && (warp != kWarpA2 || p.gather)) {
+    // The whole warp walks the steps, so that addresses stay in uniform registers;
+    // one elected thread issues (a loop that only it walks takes about 100 cycles a
+    // copy).  Gathered rows come four to a copy, and a copy takes about 80 cycles of a
+    // warp: three warps share them, in every eight copies three, two (beside B's box)
+    // and three, none for the rows past the tile, whose results are not stored (8192
+    // tokens of top-6 of 256, 4096 -> 2048: 1113 us by one warp, 744 by two).
+    const bool is_b = warp == kWarpB;
+    const int lead = is_b ? 3 : warp == kWarpA ? 0 : 5, share = is_b ? 2 : 3;
     int* const list = reinterpret_cast<int*>(gbase + p.off_list);
     const uint32_t full0 = kPair ? of_cta(bar_full, 0) : bar_full;
     const bool leader = elect_one();
@@ -423,46 +461,41 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     for (long long u = unit0; ok && u < units; u += unit_step) {
       const Unit t = unit_at(p, u, num_tiles);
       if (!t.ok) {
-        if (is_a && first && leader) record_error(err, TQ_ERR_INVALID_ARG, kWhereTileLoad);
+        if (is_b && first && leader) record_error(err, TQ_ERR_INVALID_ARG, kWhereTileLoad);
         continue;
       }
       const int row0 = t.slot0 + rank * kRows;
-      if (is_a && p.gather) {
-        // this CTA's rows; those past the tile repeat its last one
+      // this CTA's copies of four rows, and the bytes of this warp's copies (of a pair: in both CTAs)
+      const int copies = gathered(t.rows, rank);
+      uint32_t bytes = static_cast<uint32_t>(is_b ? kBBytes : 0) * (kPair ? 2 : 1);
+      if (p.gather) {
+        bytes += 4 * kStepBytes * (shared_copies(gathered(t.rows, 0), lead, share) +
+                                   (kPair ? shared_copies(gathered(t.rows, 1), lead, share) : 0));
         __syncwarp();
-        for (int i = lane; i < kRows; i += 32) {
-          const int pair = __ldg(p.sorted_pairs + t.slot0 + min(rank * kRows + i, t.rows - 1));
-          list[i] = pair >= 0 && pair < p.M ? pair / p.top_k : 0;   // the epilogue reports and skips a bad pair
+        for (int i = lane; i < 16 * share; i += 32) {
+          const int in = 32 * (i / (4 * share)) + 4 * lead + i % (4 * share);   // row of this CTA
+          const int pair = __ldg(p.sorted_pairs + t.slot0 + min(rank * kRows + in, t.rows - 1));
+          list[in] = pair >= 0 && pair < p.M ? pair / p.top_k : 0;   // the epilogue reports and skips a bad pair
         }
         __syncwarp();
+      } else if (!is_b) {
+        bytes = kABytes * (kPair ? 2 : 1);
       }
-      if (leader) {
-        // column of D of this CTA's first box, and the second's distance from it
-        const int col = t.cb * (kGated ? kCols : kN);
-        const int second = kGated ? p.N : kCols;
-        const int b_row = (kBMn ? 0 : t.e * (kGated ? 2 * p.N : p.N)) + col;
-        for (int k = t.k0; k < t.k1; ++k) {
-          if (!ready && !mbar_wait_short(bar_empty + 8 * ring.at, ring.phase ^ 1u, abort_flag, err, kWhereTileLoad)) {
-            ok = false;
-            break;
-          }
-          const uint32_t full = full0 + 8 * ring.at;
-          const uint32_t dst = base + static_cast<uint32_t>(ring.at * kStageBytes);
-          if (first)
-            mbar_arrive_expect_tx(bar_full + 8 * ring.at,
-                                  static_cast<uint32_t>(is_a ? kABytes : kBBytes) * (kPair ? 2 : 1));
-          const int at = k * kStepValues;
-          if (is_a) {
-            if (p.gather) {
-#pragma unroll 4
-              for (int i = 0; i < kRows; i += 4)
-                load_rows<kPair>(dst + i * kStepBytes, &tm_a, at, *reinterpret_cast<const int4*>(list + i), full);
-            } else {
-#pragma unroll
-              for (int i = 0; i < kABoxes; ++i)
-                load_box<kPair>(dst + i * 8192, &tm_a, kAMn ? row0 + 64 * i : at, kAMn ? at : row0, full);
-            }
-          } else {
+      // column of D of this CTA's first box, and the second's distance from it
+      const int col = t.cb * (kGated ? kCols : kN);
+      const int second = kGated ? p.N : kCols;
+      const int b_row = (kBMn ? 0 : t.e * (kGated ? 2 * p.N : p.N)) + col;
+      for (int k = t.k0; k < t.k1; ++k) {
+        if (!ready && !mbar_wait_short(bar_empty + 8 * ring.at, ring.phase ^ 1u, abort_flag, err, kWhereTileLoad)) {
+          ok = false;
+          break;
+        }
+        const uint32_t full = full0 + 8 * ring.at;
+        const uint32_t dst = base + static_cast<uint32_t>(ring.at * kStageBytes);
+        const int at = k * kStepValues;
+        if (leader) {
+          if (first) mbar_arrive_expect_tx(bar_full + 8 * ring.at, bytes);
+          if (is_b) {
 #pragma unroll
             for (int i = 0; i < kBBoxes; ++i) {
               const int c = (kPair ? rank * kCols : 0) + i * kBoxRows;   // column of the MMA's N
@@ -470,12 +503,27 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
               load_box<kPair>(dst + kABytes + i * kBoxRows * kStepBytes, &tm_b, kBMn ? row : at, kBMn ? at : row, full);
             }
           }
-          ++issued;
-          ring.advance(stages);
-          ready = mbar_test(bar_empty + 8 * ring.at, ring.phase ^ 1u);
+          if (p.gather) {
+#pragma unroll
+            for (int j = 0; j < kRows / 4; j += 8) {
+#pragma unroll
+              for (int i = 0; i < 3; ++i) {
+                const int c = j + lead + i;
+                if (i < share && c < copies)
+                  load_rows<kPair>(dst + 4 * c * kStepBytes, &tm_a, at, *reinterpret_cast<const int4*>(list + 4 * c), full);
+              }
+            }
+          } else if (!is_b) {
+#pragma unroll
+            for (int i = 0; i < kABoxes; ++i)
+              load_box<kPair>(dst + i * 8192, &tm_a, kAMn ? row0 + 64 * i : at, kAMn ? at : row0, full);
+          }
         }
+        ++issued;
+        ring.advance(stages);
+        ready = mbar_test(bar_empty + 8 * ring.at, ring.phase ^ 1u);
       }
-      ok = __all_sync(0xffffffffu, ok);   // the leader's
+      ok = __all_sync(0xffffffffu, ok);
     }
     if (leader) {
       // Before the CTA exits, every copy issued has landed (of a pair: in both
@@ -560,7 +608,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
   } else {
     if constexpr (kSplitRegisters) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int q = warp & 3, half = (warp - kWarpEpi0) >> 2;
-    float* const turn = reinterpret_cast<float*>(gbase + p.off_turn) + (warp - kWarpEpi0) * 32 * kPitch;
+    uint8_t* const turn = gbase + p.off_turn + (warp - kWarpEpi0) * (32 * kPitch * 4);
     float* const tops = reinterpret_cast<float*>(gbase + p.off_top);
     // Column of D's tile of this thread's 32-column chunk c: its half of the columns,
     // or its half of the gate's and then of the up projection's.
@@ -603,27 +651,30 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
           if (!ok) break;
           tc_fence_after();
           const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(acc.at * kN);
-          uint32_t v[2][16];
-          tmem_ld16(src + chunk_at(0), v[0]);
+          uint32_t v[2][32];
+          constexpr int kChunks = kCols / 32;
+          tmem_ld32(src + chunk_at(0), v[0]);
+          if (kChunks > 1) tmem_ld32(src + chunk_at(1), v[1]);
 #pragma unroll
-          for (int c = 0; c < kCols / 16; ++c) {
-            tmem_wait_ld();
-            if (c + 1 < kCols / 16) {
-              tmem_ld16(src + chunk_at((c + 1) / 2) + 16 * ((c + 1) & 1), v[(c + 1) & 1]);
-            } else {
-              // read: the accumulator may be written again
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) {
-                if (kPair && !first)
-                  cluster_arrive(of_cta(bar_accempty + 8 * acc.at, 0));
-                else
-                  mbar_arrive(bar_accempty + 8 * acc.at);
+          for (int c = 0; c < kChunks; ++c) {
+            if (c % 2 == 0) {
+              tmem_wait_ld();
+              if (c + 2 >= kChunks) {
+                // read: the accumulator may be written again
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                  if (kPair && !first)
+                    cluster_arrive(of_cta(bar_accempty + 8 * acc.at, 0));
+                  else
+                    mbar_arrive(bar_accempty + 8 * acc.at);
+                }
               }
             }
-            const float f = kGated && c >= kCols / 32 ? f1 : f0;
+            const float f = kGated && c >= kCols / 64 ? f1 : f0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) fma2(sum[8 * c + i], v[c & 1][2 * i], v[c & 1][2 * i + 1], f);
+            for (int i = 0; i < 16; ++i) fma2(sum[16 * c + i], v[c & 1][2 * i], v[c & 1][2 * i + 1], f);
+            if (c + 2 < kChunks) tmem_ld32(src + chunk_at(c + 2), v[c & 1]);
           }
           acc.advance(accs);
         }
@@ -654,15 +705,16 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
           if (!ok) break;
           const size_t width = p.y_type == TQ_FP32 ? 4 : 2;
           uint8_t* const y = static_cast<uint8_t*>(p.y) + static_cast<size_t>(t.split) * p.split_stride * width;
+          constexpr int kCount = kCols < 64 ? kCols : 64;
 #pragma unroll
-          for (int c = 0; c < kCols / 32; ++c) {
-            float v[32];
+          for (int c = 0; c < kCols; c += kCount) {
+            float v[kCount];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              v[2 * i] = sum[16 * c + i].x;
-              v[2 * i + 1] = sum[16 * c + i].y;
+            for (int i = 0; i < kCount / 2; ++i) {
+              v[2 * i] = sum[c / 2 + i].x;
+              v[2 * i + 1] = sum[c / 2 + i].y;
             }
-            store32_typed(y, p.y_type, v, out_row, col + half * kCols + 32 * c, p.N, p.aligned, turn, lane);
+            store_typed(y, p.y_type, v, out_row, col + half * kCols + c, p.N, p.aligned, turn, lane);
           }
         }
       } else {
@@ -685,30 +737,30 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
               float* const gu = p.gate_up;
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(g[i]);
-              store32(gu, v, out_row < 0 ? -1 : 2 * out_row, at, p.N, p.N % 4 == 0, turn, lane);
+              store_columns(gu, v, out_row < 0 ? -1 : 2 * out_row, at, p.N, p.N % 4 == 0, turn, lane);
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(up[i]);
-              store32(gu, v, out_row < 0 ? -1 : 2 * out_row + 1, at, p.N, p.N % 4 == 0, turn, lane);
+              store_columns(gu, v, out_row < 0 ? -1 : 2 * out_row + 1, at, p.N, p.N % 4 == 0, turn, lane);
             }
             if (p.y) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = silu(__uint_as_float(g[i])) * __uint_as_float(up[i]);
-              store32_typed(p.y, p.y_type, v, out_row, at, p.N, p.aligned, turn, lane);
+              store_typed(p.y, p.y_type, v, out_row, at, p.N, p.aligned, turn, lane);
             }
           }
         } else {
           const size_t width = p.y_type == TQ_FP32 ? 4 : 2;
           uint8_t* const y = static_cast<uint8_t*>(p.y) + static_cast<size_t>(t.split) * p.split_stride * width;
-          uint32_t v[2][32];
-          tmem_ld32(src + chunk_at(0), v[0]);
 #pragma unroll
-          for (int c = 0; c < kCols / 32; ++c) {
+          for (int c = 0; c < kCols / 64; ++c) {
+            uint32_t v[2][32];
+            tmem_ld32(src + half * kCols + 64 * c, v[0]);
+            tmem_ld32(src + half * kCols + 64 * c + 32, v[1]);
             tmem_wait_ld();
-            if (c + 1 < kCols / 32) tmem_ld32(src + chunk_at(c + 1), v[(c + 1) & 1]);
-            float f[32];
+            float f[64];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[c & 1][i]);
-            store32_typed(y, p.y_type, f, out_row, col + half * kCols + 32 * c, p.N, p.aligned, turn, lane);
+            for (int i = 0; i < 64; ++i) f[i] = __uint_as_float(v[i / 32][i % 32]);
+            store_typed(y, p.y_type, f, out_row, col + half * kCols + 64 * c, p.N, p.aligned, turn, lane);
           }
         }
         tc_fence_before();
