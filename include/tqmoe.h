@@ -752,11 +752,10 @@ void tq_launch_counts(int64_t out[TQ_NUM_LAUNCH_COUNTERS]);
  * 4- and 8-bit products, and of K splits),
  * out[19] SwiGLU staging, out[20] 4-bit GEMV, out[21] RMS norm, out[22] its
  * gradient, out[23] the sum of its weight's gradient, out[24] 8-bit quantise,
- * out[25] dequantise, out[26] SwiGLU to 8 bits, out[27] 8-bit product, out[28]
- * product with few rows (8 or 16 bits), out[29] 16-bit product, out[30] gradient
- * of the gated activation.  Writes the first `capacity` of them and returns how
+ * out[25] dequantise, out[26] 8-bit product, out[27] product with few rows (8 or 16
+ * bits), out[28] 16-bit product, out[29] gradient of the gated activation.  Writes the first `capacity` of them and returns how
  * many there are. */
-#define TQ_NUM_ALL_LAUNCH_COUNTERS 31
+#define TQ_NUM_ALL_LAUNCH_COUNTERS 30
 int tq_launch_counts_all(int64_t* out, int capacity);
 
 #ifdef __cplusplus

@@ -167,6 +167,10 @@ def test_rows_out_of_the_ordinary():
         assert np.all(_f64(codes)[0] == 0) and np.all(_f64(scales)[0] == 0)
         assert np.isnan(_f64(codes)[3]).all()
         assert _f64(codes)[6, 7] == -448.0
+        # without eps tiny rows count, down to those whose squares are no fp32 numbers
+        tiny = torch.full((1, K), 3e-33, dtype=DTYPES[dtype], device="cuda")
+        y1, _, _ = tq.tq_rms_norm(tiny, None, eps=0.0)
+        assert torch.allclose(y1.float(), torch.ones(1, device="cuda"), rtol=4 * U, atol=0.0)
         # eps 0 and a row of zeros: 0 times infinity
         y0, _, rstd0 = tq.tq_rms_norm(x[:1], None, eps=0.0)
         assert torch.isinf(rstd0).all() and torch.isnan(y0).all()

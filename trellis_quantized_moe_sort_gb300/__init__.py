@@ -673,7 +673,7 @@ def tq_launch_counts_all() -> dict:
 ALL_LAUNCH_COUNTERS = LAUNCH_COUNTERS + ("router_scored", "router_scored_backward", "fp4_quantize", "fp4_dequantize",
                                          "fp4_tile_scales", "fp4_stage", "fp4_gemm", "fp4_combine", "fp4_swiglu",
                                          "fp4_gemv", "rms_norm", "rms_norm_backward", "rms_norm_weight", "fp8_quantize",
-                                         "fp8_dequantize", "fp8_swiglu", "fp8_gemm", "few_rows", "gemm_f16",
+                                         "fp8_dequantize", "fp8_gemm", "few_rows", "gemm_f16",
                                          "swiglu_grad")
 
 

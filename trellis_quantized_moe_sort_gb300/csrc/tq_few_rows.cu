@@ -1,24 +1,31 @@
 // Matrix products with few activation rows: y[t] = W x[t] for up to 8 or 16 rows of x
 // that share a matrix, bound by the reading of W.
 //
-// A warp multiplies 16 weight rows (gated: 16 of the gate and 16 of the up
-// projection) with all the activation rows, K 128 bytes at a time, by m16n8
-// MMAs whose operands come straight from global memory: the order of K inside a sum
-// is free, so a lane takes 16 consecutive bytes of a weight row and of an activation
-// row and gives them to the MMAs four bytes at a time, both in the same order.  No
-// shared memory and no conversion on the way; tensor memory and its 128-row tiles
-// would mean a pipeline set up for 16 KB of weights.  The MMA is not the bound: 8
-// rows a pass are far below its rate at the memory's.
+// A warp multiplies 16 weight rows (gated: 8 of the gate and 8 of the up projection)
+// with all the activation rows, K 128 bytes at a time, by m16n8 MMAs whose operands
+// come as they are in memory: the order of K inside a sum is free, so a lane takes
+// 16 consecutive bytes of a weight row and of an activation row and gives them to the
+// MMAs four bytes at a time, both in the same order.  A lane's weights wait for it in
+// shared memory (asynchronous copies that it alone reads back: six steps ahead and no
+// barrier; in registers four were the most).  Tensor memory and its 128-row tiles would
+// mean a pipeline set up for 16 KB of weights.  The MMA is not the bound: 8 rows a pass
+// are far below its rate at the memory's.
 //
 // The eight warps of a block split K by blocks of 128 bytes and add up through
-// shared memory in a fixed order; a block's warps have up to four such blocks each
-// in flight.
+// shared memory in a fixed order.  Blocks walk their share of the units (an m-tile x 16
+// weight rows), each warp with its next blocks of weights under way, across units
+// too: a block of threads for each unit left the memory idle between their starts and
+// ends (32 tokens of top-6 of 256, 4096 -> 2048: 247 us for 1.14 GB, walking 197).
+//
+// A single token's experts are the segments of one unit, whose sums, weighted, add up
+// in the same registers: its product is this one launch.
 //
 // 8-bit products: 128 bytes are a scale block, whose partial sums are scaled into
 // fp32 registers.
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "tq_device.cuh"
 #include "tq_internal.h"
@@ -28,18 +35,26 @@ namespace tq {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kRows = 16;          // weight rows per block
+constexpr int kRows = 16;          // weight rows per unit
 constexpr int kStepBytes = 128;    // of a row per step
-// Steps in flight per warp: 64 registers of weights.
-template <int kParts>
-constexpr int kAheadOf = 4 / kParts;
+
+constexpr int kAhead = 6;          // steps of weights in flight per warp
+constexpr int kLaneBytes = 64;     // of a step: 16 rows x 128 bytes over a warp
+constexpr int kRingBytes = kAhead * kThreads * kLaneBytes;
 
 enum Kind { kFp8 = 0, kBf16 = 1, kFp16 = 2 };
 
-__device__ __forceinline__ uint4 load_stream(const uint8_t* p) {
+// Copies 16 bytes (or, with `bytes` 0, zeros), 4 bytes, to shared memory in this
+// thread's current group of copies.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 read16(uint32_t src) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
   return v;
 }
 
@@ -69,208 +84,344 @@ __device__ __forceinline__ T& either(T& a, T& b) {
     return b;
 }
 
-// kParts: matrices of 16 rows per warp (2 gated); kTiles: groups of 8 activation rows.
-template <int kKind, int kParts, int kTiles>
-__global__ void __launch_bounds__(kThreads, 2) few_rows_kernel(const FewRows p) {
-  constexpr int kCols = 8 * kTiles, kAhead = kAheadOf<kParts>;
-  __shared__ float sums[kWarps][kParts][kRows][kCols];
-  __shared__ int x_row[kCols], y_row[kCols];
-  __shared__ int expert;
+// A unit's activation rows: of a tile map's tile, of one pair or token, or consecutive.
+struct Tile {
+  int slot0, rows;
+};
+__device__ __forceinline__ Tile tile_at(const FewRows& p, int tile, int cols) {
+  if (p.tiles) return {__ldg(p.tiles + 3ll * tile + 1), __ldg(p.tiles + 3ll * tile + 2)};
+  if (p.ids) return {tile, 1};
+  return {tile * cols, min(cols, p.M - tile * cols)};
+}
+// The matrix of a unit's segment; -1 when out of range.
+__device__ __forceinline__ int matrix_at(const FewRows& p, int tile, int segment) {
+  const int e = p.tiles ? __ldg(p.tiles + 3ll * tile) : p.ids ? __ldg(p.ids + static_cast<long long>(tile) * p.segments + segment) : 0;
+  return e >= 0 && e < p.E ? e : -1;
+}
+
+// A place in the walk over units, their segments and this warp's steps: k = warp, warp +
+// 8, ... of a unit's segments laid end to end.
+template <bool kSegments>
+struct Place {
+  unsigned unit;
+  int tile, block, segment, k;
+  __device__ __forceinline__ void start(const FewRows& p, int warp) {
+    segment = 0;
+    k = warp;
+    settle(p);
+  }
+  __device__ __forceinline__ bool settle(const FewRows& p) {
+    bool moved = false;
+    if constexpr (kSegments) {
+      while (k >= p.steps && segment < p.segments) {
+        k -= p.steps;
+        ++segment;
+        moved = true;
+      }
+    }
+    return moved;
+  }
+  __device__ __forceinline__ void next_unit(const FewRows& p, int row_blocks, int warp) {
+    ++unit;
+    if (++block == row_blocks) {
+      block = 0;
+      ++tile;
+    }
+    start(p, warp);
+  }
+  __device__ __forceinline__ bool past_unit(const FewRows& p) const { return kSegments ? segment >= p.segments : k >= p.steps; }
+};
+
+// kTiles: groups of 8 activation rows; kSegments: a token's experts one after another.
+template <int kKind, bool kGated, int kTiles, bool kSegments>
+__global__ void __launch_bounds__(kThreads, 2) few_rows_kernel(const FewRows p, const int row_blocks, const int max_tiles) {
+  constexpr int kCols = 8 * kTiles, kFeatures = kGated ? kRows / 2 : kRows;
+  extern __shared__ uint4 ring[];   // [kAhead][warps][4][lanes]: a lane's own bytes, read back by it alone
+  __shared__ float scale_ring[kAhead][kWarps][2];
+  __shared__ float sums[2][kWarps][kRows][kCols];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, q = lane & 3;
-  const int tile = blockIdx.y;
-  if (p.num_tiles && tile >= *p.num_tiles) return;
-  // the unit's activation rows: of a tile map's tile, of one pair, or consecutive
-  if (threadIdx.x < kCols) {
-    const int c = threadIdx.x;
-    int e = 0, slot0 = tile * kCols, rows = p.M - slot0, xr = -1, yr = -1;
-    if (p.tiles) {
-      e = __ldg(p.tiles + 3 * tile);
-      slot0 = __ldg(p.tiles + 3 * tile + 1);
-      rows = __ldg(p.tiles + 3 * tile + 2);
-    } else if (p.ids) {
-      slot0 = tile;
-      rows = 1;
-      e = __ldg(p.ids + tile);
-    }
-    if (e < 0 || e >= p.E || slot0 < 0 || rows > p.M - slot0) {
-      if (c == 0) record_error(p.err, TQ_ERR_INVALID_ARG, kWhereFewRows);
-      e = -1;
-    } else if (c < rows) {
-      const int slot = slot0 + c;
-      const int pair = p.sorted_pairs ? __ldg(p.sorted_pairs + slot) : slot;
-      if (pair >= 0 && pair < p.M) {
-        xr = p.gather ? pair / p.top_k : slot;
-        yr = p.scatter ? pair : slot;
-      } else {
-        record_error(p.err, TQ_ERR_INVALID_ARG, kWhereFewRows);
-      }
-    }
-    x_row[c] = xr;
-    y_row[c] = yr;
-    if (c == 0) expert = e;
-  }
-  __syncthreads();
-  const int e = expert;
-  if (e < 0) return;
-
-  const int row0 = blockIdx.x * kRows;
   const long long row_bytes = p.row_bytes;
-  const uint8_t* w[kParts][2];   // this lane's two rows of each part
-  bool in[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = row0 + g + 8 * h;
-    in[h] = r < p.N;
-#pragma unroll
-    for (int a = 0; a < kParts; ++a)
-      w[a][h] = p.w + (static_cast<long long>(e) * kParts * p.N + a * p.N + min(r, p.N - 1)) * row_bytes + 16 * q;
-  }
-  const uint8_t* x[kTiles];
-  bool has[kTiles];
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t) {
-    const int xr = x_row[8 * t + g];
-    has[t] = xr >= 0;
-    x[t] = p.x + max(xr, 0) * p.x_stride + 16 * q;
-  }
-  // the scales of a lane's two columns of sums, and of the weights' rows
-  const float* sx[kTiles][2];
-  const float* sw[kParts];
-  if constexpr (kKind == kFp8) {
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) sx[t][i] = p.x_scales + static_cast<long long>(max(x_row[8 * t + 2 * q + i], 0)) * p.steps;
-    }
-#pragma unroll
-    for (int a = 0; a < kParts; ++a)
-      sw[a] = p.w_scales + (static_cast<long long>(e) * p.w_blocks + (a * p.N + row0) / 128) * p.steps;
-  }
+  const int tiles = p.num_tiles ? min(*p.num_tiles, max_tiles) : max_tiles;
+  // this block's units, neighbours
+  const unsigned units = static_cast<unsigned>(tiles) * row_blocks, each = units / gridDim.x, more = units % gridDim.x;
+  const unsigned u0 = each * blockIdx.x + min(blockIdx.x, more), u1 = u0 + each + (blockIdx.x < more ? 1u : 0u);
+  if (u0 == u1) return;
 
-  float sum[kParts][kTiles][4] = {};
-  for (int k0 = warp; k0 < p.steps; k0 += kWarps * kAhead) {
-    uint4 wv[kAhead][kParts][2][2];
+  // Weights: the place that is loaded next, kAhead steps before its use.
+  Place<kSegments> here;
+  here.unit = u0;
+  here.tile = static_cast<int>(u0 / row_blocks);
+  here.block = static_cast<int>(u0 - static_cast<unsigned>(here.tile) * row_blocks);
+  here.start(p, warp);
+  const bool idle = here.past_unit(p);   // a warp without a step in a unit only joins its sums
+  Place<kSegments> ahead = here;
+  const uint8_t* w[2];    // this lane's two rows
+  const float* sw[2];     // and their scales
+  bool in[2];
+  auto aim = [&] {
+    const int e = matrix_at(p, ahead.tile, ahead.segment);
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int k = k0 + i * kWarps;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int at = k * kStepBytes + 64 * j;
-        const bool there = k < p.steps && at + 16 * q < row_bytes;
-#pragma unroll
-        for (int a = 0; a < kParts; ++a) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            wv[i][a][h][j] = make_uint4(0u, 0u, 0u, 0u);
-            if (there && in[h]) wv[i][a][h][j] = load_stream(w[a][h] + at);
-          }
-        }
-      }
+    for (int h = 0; h < 2; ++h) {
+      const int first = ahead.block * kFeatures, f = first + g + (kGated ? 0 : 8 * h);
+      in[h] = e >= 0 && f < p.N;
+      w[h] = p.w + (in[h] ? (kGated ? (2ll * e + h) * p.N : static_cast<long long>(e) * p.N) + f : 0) * row_bytes + 16 * q;
+      if (kKind == kFp8)
+        sw[h] = p.w_scales +
+                (static_cast<long long>(max(e, 0)) * p.w_blocks + (first + (kGated ? h * p.N : 0)) / 128) * p.steps;
     }
+  };
+  const uint32_t mine = smem_u32(ring) + static_cast<uint32_t>(warp * 32 * kLaneBytes + lane * 16);
+  auto load = [&](int slot) {
+    if (!idle && ahead.unit < u1) {
+      const long long at = static_cast<long long>(ahead.k) * kStepBytes;
+      const uint32_t dst = mine + static_cast<uint32_t>(slot * kThreads * kLaneBytes);
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int k = k0 + i * kWarps;
-      if (k >= p.steps) break;
-      float part[kParts][kTiles][4];
-      if constexpr (kKind == kFp8) {
-#pragma unroll
-        for (int a = 0; a < kParts; ++a)
-#pragma unroll
-          for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) part[a][t][c] = 0.f;
-      }
-      auto& to = either<kKind == kFp8>(part, sum);
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
+      for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int at = k * kStepBytes + 64 * j;
-          uint4 xv = make_uint4(0u, 0u, 0u, 0u);
-          if (has[t] && at + 16 * q < row_bytes) xv = __ldg(reinterpret_cast<const uint4*>(x[t] + at));
-#pragma unroll
-          for (int a = 0; a < kParts; ++a) {
-            const uint4 lo = wv[i][a][0][j], hi = wv[i][a][1][j];
-            mma16x8<kKind>(to[a][t], lo.x, hi.x, lo.y, hi.y, xv.x, xv.y);
-            mma16x8<kKind>(to[a][t], lo.z, hi.z, lo.w, hi.w, xv.z, xv.w);
-          }
+          const bool inside = in[h] && at + 64 * j + 16 * q < row_bytes;
+          copy16(dst + (2 * h + j) * 512, inside ? w[h] + at + 64 * j : p.w, inside ? 16 : 0);
         }
       }
+      if (kKind == kFp8 && lane <= (kGated ? 1 : 0))
+        copy4(smem_u32(&scale_ring[slot][warp][lane]), (kGated && lane ? sw[1] : sw[0]) + ahead.k);
+      ahead.k += kWarps;
+      bool moved = ahead.settle(p);
+      if (ahead.past_unit(p)) {
+        ahead.next_unit(p, row_blocks, warp);
+        moved = ahead.unit < u1;
+      }
+      if (moved) aim();
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (!idle) aim();
+#pragma unroll 1
+  for (int i = 0; i < kAhead; ++i) load(i);
+
+  // The unit that is multiplied.  Column g (+ 8 c) is this lane's: its rows of x and of
+  // the output, -1 for none.
+  int x_row[kTiles], y_row[kTiles];
+  const uint8_t* x[kTiles];
+  const float* sx[kTiles][2];   // the scales of this lane's two columns of sums
+  float weight = 1.f;           // of the segment
+  auto enter_tile = [&] {
+    const Tile t = tile_at(p, here.tile, kCols);
+    const bool ok = t.slot0 >= 0 && t.rows >= 1 && t.rows <= p.M - t.slot0;
+    if (!ok && here.block == 0 && threadIdx.x == 0) record_error(p.err, TQ_ERR_INVALID_ARG, kWhereFewRows);
+#pragma unroll
+    for (int c = 0; c < kTiles; ++c) {
+      x_row[c] = y_row[c] = -1;
+      if (ok && 8 * c + g < t.rows) {
+        const int slot = t.slot0 + 8 * c + g;
+        const int pair = p.sorted_pairs ? __ldg(p.sorted_pairs + slot) : slot;
+        if (pair >= 0 && pair < p.M) {
+          x_row[c] = p.gather ? pair / p.top_k : slot;
+          y_row[c] = p.scatter ? pair : slot;
+        } else if (here.block == 0 && warp == 0 && q == 0) {
+          record_error(p.err, TQ_ERR_INVALID_ARG, kWhereFewRows);
+        }
+      }
+    }
+  };
+  auto enter_segment = [&] {
+    const int e = matrix_at(p, here.tile, here.segment);
+    if (e < 0 && here.block == 0 && lane == 0) record_error(p.err, TQ_ERR_INVALID_ARG, kWhereFewRows);
+    if (kSegments) weight = __ldg(p.topk_w + static_cast<long long>(here.tile) * p.segments + here.segment);
+#pragma unroll
+    for (int c = 0; c < kTiles; ++c) {
+      // a unit of segments has one row of x for all, or one for each
+      const int row = kSegments && !p.gather && x_row[c] >= 0 ? x_row[c] * p.segments + here.segment : x_row[c];
+      x[c] = p.x + max(row, 0) * p.x_stride + 16 * q;
       if constexpr (kKind == kFp8) {
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-          const float s0 = __ldg(sx[t][0] + k), s1 = __ldg(sx[t][1] + k);
+        for (int i = 0; i < 2; ++i)
+          sx[c][i] = p.x_scales + static_cast<long long>(max(__shfl_sync(0xffffffffu, row, 4 * (2 * q + i)), 0)) * p.steps;
+      }
+    }
+    return e >= 0;
+  };
+  // x of a step, loaded a step ahead inside a segment
+  struct Step {
+    uint4 v[kTiles][2];
+    float s0[kTiles], s1[kTiles];
+  };
+  Step next;
+  auto load_x = [&](int k) {
 #pragma unroll
-          for (int a = 0; a < kParts; ++a) {
-            const float f = __ldg(sw[a] + k);
-            sum[a][t][0] = fmaf(part[a][t][0], s0 * f, sum[a][t][0]);
-            sum[a][t][1] = fmaf(part[a][t][1], s1 * f, sum[a][t][1]);
-            sum[a][t][2] = fmaf(part[a][t][2], s0 * f, sum[a][t][2]);
-            sum[a][t][3] = fmaf(part[a][t][3], s1 * f, sum[a][t][3]);
+    for (int c = 0; c < kTiles; ++c) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const long long at = static_cast<long long>(k) * kStepBytes + 64 * j;
+        next.v[c][j] = make_uint4(0u, 0u, 0u, 0u);
+        if (x_row[c] >= 0 && at + 16 * q < row_bytes) next.v[c][j] = __ldg(reinterpret_cast<const uint4*>(x[c] + at));
+      }
+      if constexpr (kKind == kFp8) {
+        next.s0[c] = __ldg(sx[c][0] + k);
+        next.s1[c] = __ldg(sx[c][1] + k);
+      }
+    }
+  };
+  enter_tile();
+  bool live = false;
+  if (!idle) {
+    live = enter_segment();
+    load_x(here.k);
+  }
+
+  float sum[kTiles][4] = {};
+  int buffer = 0, slot = 0;
+  while (true) {
+      if (!idle) {
+        const Step xs = next;
+        if (here.k + kWarps < p.steps) load_x(here.k + kWarps);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        __syncwarp();
+        const uint32_t src = mine + static_cast<uint32_t>(slot * kThreads * kLaneBytes);
+        const float w0 = kKind == kFp8 ? scale_ring[slot][warp][0] : 0.f;
+        const float w1 = kKind == kFp8 && kGated ? scale_ring[slot][warp][1] : w0;
+      if (live) {
+        float part[kTiles][4];
+        if constexpr (kKind == kFp8) {
+#pragma unroll
+          for (int c = 0; c < kTiles; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) part[c][j] = 0.f;
+        }
+        auto& to = either<kKind == kFp8>(part, sum);
+        const float f0 = w0 * weight, f1 = w1 * weight;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint4 lo = read16(src + 512 * j), hi = read16(src + 512 * (2 + j));
+#pragma unroll
+          for (int c = 0; c < kTiles; ++c) {
+            const uint4 v = xs.v[c][j];
+            mma16x8<kKind>(to[c], lo.x, hi.x, lo.y, hi.y, v.x, v.y);
+            mma16x8<kKind>(to[c], lo.z, hi.z, lo.w, hi.w, v.z, v.w);
+          }
+        }
+        if constexpr (kKind == kFp8) {
+#pragma unroll
+          for (int c = 0; c < kTiles; ++c) {
+            sum[c][0] = fmaf(part[c][0], xs.s0[c] * f0, sum[c][0]);
+            sum[c][1] = fmaf(part[c][1], xs.s1[c] * f0, sum[c][1]);
+            sum[c][2] = fmaf(part[c][2], xs.s0[c] * f1, sum[c][2]);
+            sum[c][3] = fmaf(part[c][3], xs.s1[c] * f1, sum[c][3]);
           }
         }
       }
-    }
-  }
-#pragma unroll
-  for (int a = 0; a < kParts; ++a) {
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<float2*>(&sums[warp][a][g + 8 * h][8 * t + 2 * q]) =
-            make_float2(sum[a][t][2 * h], sum[a][t][2 * h + 1]);
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < kRows * kCols; i += kThreads) {
-    const int r = i % kRows, c = i / kRows;
-    const long long to = y_row[c];
-    if (to < 0 || row0 + r >= p.N) continue;
-    float v[kParts];
-#pragma unroll
-    for (int a = 0; a < kParts; ++a) {
-      v[a] = 0.f;
-#pragma unroll
-      for (int s = 0; s < kWarps; ++s) v[a] += sums[s][a][r][c];
-    }
-    float out = v[0];
-    if constexpr (kParts == 2) {
-      if (p.gate_up) {
-        p.gate_up[to * 2 * p.N + row0 + r] = v[0];
-        p.gate_up[(to * 2 + 1) * p.N + row0 + r] = v[1];
+        __syncwarp();   // every lane has its scales
+        load(slot);
+        if (++slot == kAhead) slot = 0;
+        here.k += kWarps;
+        const bool moved = here.settle(p);
+        if (!here.past_unit(p)) {
+          if (moved) {
+            live = enter_segment();
+            load_x(here.k);
+          }
+          continue;
+        }
       }
-      out = v[0] / (1.f + expf(-v[0])) * v[1];
-    }
-    const long long at = to * p.N + row0 + r;
-    if (!p.y) continue;
-    if (p.y_type == TQ_FP32)
-      static_cast<float*>(p.y)[at] = out;
-    else if (p.y_type == TQ_BF16)
-      static_cast<__nv_bfloat16*>(p.y)[at] = narrow<__nv_bfloat16>(out);
-    else
-      static_cast<__half*>(p.y)[at] = narrow<__half>(out);
+      // the unit's end: its sums, and the next one
+#pragma unroll
+      for (int c = 0; c < kTiles; ++c) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          *reinterpret_cast<float2*>(&sums[buffer][warp][g + 8 * h][8 * c + 2 * q]) =
+              make_float2(sum[c][2 * h], sum[c][2 * h + 1]);
+          sum[c][2 * h] = sum[c][2 * h + 1] = 0.f;
+        }
+      }
+      __syncthreads();   // (a buffer is written again after the next unit's barrier)
+      if (threadIdx.x < kFeatures * kCols) {
+        static_assert(kFeatures * kCols <= kThreads && kFeatures * kCols % 32 == 0, "one result a thread, whole warps");
+        const int r = threadIdx.x % kFeatures, c = threadIdx.x / kFeatures;   // a warp's columns are of the same eight
+        int row = y_row[0];
+        if (kTiles > 1 && c >= 8) row = y_row[kTiles - 1];
+        const long long to = __shfl_sync(0xffffffffu, row, 4 * (c % 8));
+        const int f = here.block * kFeatures + r;
+        if (to >= 0 && f < p.N) {
+          float v[2] = {0.f, 0.f};
+#pragma unroll
+          for (int s = 0; s < kWarps; ++s) {
+            v[0] += sums[buffer][s][r][c];
+            if (kGated) v[1] += sums[buffer][s][r + (kGated ? 8 : 0)][c];
+          }
+          float out = v[0];
+          if constexpr (kGated) {
+            if (p.gate_up) {
+              p.gate_up[to * 2 * p.N + f] = v[0];
+              p.gate_up[(to * 2 + 1) * p.N + f] = v[1];
+            }
+            out = v[0] / (1.f + expf(-v[0])) * v[1];
+          }
+          const long long at = to * p.N + f;
+          if (!p.y) {
+          } else if (p.y_type == TQ_FP32) {
+            static_cast<float*>(p.y)[at] = out;
+          } else if (p.y_type == TQ_BF16) {
+            static_cast<__nv_bfloat16*>(p.y)[at] = narrow<__nv_bfloat16>(out);
+          } else {
+            static_cast<__half*>(p.y)[at] = narrow<__half>(out);
+          }
+        }
+      }
+      buffer ^= 1;
+      const int tile = here.tile;
+      here.next_unit(p, row_blocks, warp);
+      if (here.unit >= u1) return;
+      if (here.tile != tile) enter_tile();
+      if (!idle) {
+        if (kSegments || here.tile != tile) live = enter_segment();
+        load_x(here.k);
+      }
   }
 }
 
-template <int kKind, int kParts>
-int run(const FewRows& p, int cols, unsigned units, cudaStream_t s) {
-  const dim3 grid((p.N + kRows - 1) / kRows, units);
-  return cols == 8 ? launch_pdl(few_rows_kernel<kKind, kParts, 1>, grid, dim3(kThreads), 0, s, p)
-                   : launch_pdl(few_rows_kernel<kKind, kParts, 2>, grid, dim3(kThreads), 0, s, p);
+template <int kKind, bool kGated, int kTiles, bool kSegments>
+int run(const FewRows& p, int tiles, cudaStream_t s) {
+  const int features = kGated ? kRows / 2 : kRows, row_blocks = (p.N + features - 1) / features;
+  const long long units = static_cast<long long>(tiles) * row_blocks;
+  if (units >= (1ll << 31)) return TQ_ERR_INVALID_ARG;
+  const dim3 grid(static_cast<unsigned>(std::min<long long>(units, 2ll * sm_count())));
+  auto kernel = few_rows_kernel<kKind, kGated, kTiles, kSegments>;
+  static std::atomic<uint64_t> allowed{0};   // bit d: device d
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) {
+    cudaGetLastError();
+    return TQ_ERR_CUDA;
+  }
+  const uint64_t bit = 1ull << (device & 63);
+  if (!(allowed.load() & bit)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess) {
+      cudaGetLastError();
+      return TQ_ERR_CUDA;
+    }
+    allowed.fetch_or(bit);
+  }
+  return launch_pdl(kernel, grid, dim3(kThreads), kRingBytes, s, p, row_blocks, tiles);
+}
+template <int kKind, bool kGated>
+int run(const FewRows& p, int cols, int tiles, cudaStream_t s) {
+  return cols == 8 ? run<kKind, kGated, 1, false>(p, tiles, s) : run<kKind, kGated, 2, false>(p, tiles, s);
 }
 
 }  // namespace
 
 int launch_few_rows(const FewRows& p, int type, bool gated, int cols, int64_t units, cudaStream_t s) {
-  if (units < 1 || units > 65535 || (cols != 8 && cols != 16)) return TQ_ERR_INVALID_ARG;
-  const unsigned u = static_cast<unsigned>(units);
-  const int st = type == kFewRowsFp8 ? run<kFp8, 1>(p, cols, u, s)
-                 : type == TQ_BF16   ? (gated ? run<kBf16, 2>(p, cols, u, s) : run<kBf16, 1>(p, cols, u, s))
-                                     : (gated ? run<kFp16, 2>(p, cols, u, s) : run<kFp16, 1>(p, cols, u, s));
+  if (units < 1 || units > 0x7fffffff || (cols != 8 && cols != 16)) return TQ_ERR_INVALID_ARG;
+  const int u = static_cast<int>(units);
+  int st;
+  if (type == kFewRowsFp8)
+    st = p.topk_w ? run<kFp8, false, 1, true>(p, u, s)
+         : gated  ? run<kFp8, true>(p, cols, u, s)
+                  : run<kFp8, false>(p, cols, u, s);
+  else
+    st = type == TQ_BF16 ? run<kBf16, true>(p, cols, u, s) : run<kFp16, true>(p, cols, u, s);
   if (st == TQ_OK) count_launch(kCntFewRows);
   return st;
 }

@@ -64,9 +64,9 @@ LinearPlan plan_linear(void* base, int64_t n, int K, int N) {
   return l;
 }
 
-// How the experts' products go: every pair by itself, without a sort; m-tiles of up
-// to 16 rows by the few-rows kernel; or the tensor-core tiles.
-enum Arm { kPairs, kFew, kTiles };
+// How the experts' products go: a token's pairs one after another, without a sort;
+// m-tiles of up to 16 rows by the few-rows kernel; or the tensor-core tiles.
+enum Arm { kTokens, kFew, kTiles };
 struct MoePlan {
   Arm arm;
   int tile_m;
@@ -78,7 +78,7 @@ MoePlan plan_arm(int64_t n, int top_k, int E, TileChoice tile) {
   const double mean = n ? tq_pairs_per_woken_expert(n, top_k, E) : 0.0;
   if (m.P <= 2 * top_k || mean < 1.1) {
     // (almost) no expert has two pairs: sorting them would save nothing
-    m.arm = m.P <= 4096 ? kPairs : kFew;
+    m.arm = kTokens;
   } else {
     m.arm = mean <= 10.0 ? kFew : kTiles;
   }
@@ -101,7 +101,7 @@ struct Routed {
 };
 Routed carve_routed(Carver& c, const MoePlan& m, int E) {
   Routed r{};
-  if (m.arm == kPairs) return r;
+  if (m.arm == kTokens) return r;
   r.counts = c.take<int32_t>(E);
   r.offsets = c.take<int32_t>(E + 1);
   r.sorted_pairs = c.take<int32_t>(m.P);
@@ -110,7 +110,7 @@ Routed carve_routed(Carver& c, const MoePlan& m, int E) {
   return r;
 }
 int route_pairs(const MoePlan& m, const Routed& r, const int32_t* ids, int E, int* err, cudaStream_t s) {
-  if (m.arm == kPairs) return TQ_OK;
+  if (m.arm == kTokens) return TQ_OK;
   return launch_route_tile_map(ids, static_cast<int>(m.P), E, m.tile_m, r.counts, r.offsets, r.sorted_pairs, r.tiles,
                                r.num_tiles, m.cap, err, s);
 }
@@ -129,8 +129,8 @@ ProductPlan plan_moe(void* base, int64_t n, int top_k, int E, int K, int N) {
   if (p.m.arm != kTiles) p.tile.splits = 1;
   Carver c{static_cast<uint8_t*>(base)};
   p.routed = carve_routed(c, p.m, E);
-  p.part = c.take<float>(static_cast<size_t>(p.tile.splits) * p.m.P * N);
-  p.bytes = c.used;
+  p.part = p.m.arm == kTokens ? nullptr : c.take<float>(static_cast<size_t>(p.tile.splits) * p.m.P * N);
+  p.bytes = std::max(c.used, kNoWorkspace);
   return p;
 }
 
@@ -138,13 +138,13 @@ struct MlpPlan {
   MoePlan m;
   TileChoice down;
   Routed routed;
-  float *gate_up, *part;   // gate_up: the few-rows kernel's sums
+  float *h32, *part;   // h32: the few-rows kernel's h
   uint8_t* h;
   float* h_scales;
   size_t bytes;
 };
 MlpPlan plan_mlp(void* base, int64_t n, int top_k, int E, int H, int I) {
-  MlpPlan p;
+  MlpPlan p{};
   // one tile map for both products, by the gate and up projections'
   const TileChoice gu = moe_tile(n, top_k, E, blocks_of(H), I, true);
   p.m = plan_arm(n, top_k, E, gu);
@@ -154,51 +154,69 @@ MlpPlan plan_mlp(void* base, int64_t n, int top_k, int E, int H, int I) {
   if (p.down.tile_m > 128) p.down.cols = 128;
   Carver c{static_cast<uint8_t*>(base)};
   p.routed = carve_routed(c, p.m, E);
-  p.gate_up = p.m.arm == kTiles ? nullptr : c.take<float>(static_cast<size_t>(p.m.P) * 2 * I);
+  p.h32 = p.m.arm == kTiles ? nullptr : c.take<float>(static_cast<size_t>(p.m.P) * I);
   p.h = c.take<uint8_t>(static_cast<size_t>(p.m.P) * I);
   p.h_scales = c.take<float>(static_cast<size_t>(p.m.P) * (I / kFp8Block));
-  p.part = c.take<float>(static_cast<size_t>(p.down.splits) * p.m.P * H);
+  if (p.m.arm != kTokens) p.part = c.take<float>(static_cast<size_t>(p.down.splits) * p.m.P * H);
   p.bytes = c.used;
   return p;
 }
 
-// One product of a routed chain, its rows gathered from the tokens or in slot order,
-// its output by pair or by slot.
 struct Operand {
   const uint8_t* codes;
   const float* scales;
 };
-int routed_product(const MoePlan& m, const Routed& r, const int32_t* ids, Operand x, int64_t x_rows, bool gather,
-                   Operand w, int top_k, int E, int K, int N, TileChoice tile, bool scatter, float* out, int* err,
-                   cudaStream_t s) {
-  const int steps = blocks_of(K);
-  if (m.arm == kTiles) {
-    Fp8Gemm g{x.codes, x.scales, x_rows, w.codes, w.scales, r.sorted_pairs, r.tiles, r.num_tiles, m.cap, m.P, top_k, E,
-              K, N, gather, scatter, false, m.tile_m, tile.cols, tile.splits, out, TQ_FP32, nullptr, nullptr, err};
-    return launch_fp8_gemm(g, s);
-  }
+
+// What the few-rows products of a chain have in common: w [E][N (gated 2 N)][K].
+FewRows few_rows(Operand x, Operand w, int64_t M, int top_k, int E, int K, int N, bool gated, void* y, int y_type, int* err) {
   FewRows f{};
   f.w = w.codes;
   f.x = x.codes;
   f.w_scales = w.scales;
   f.x_scales = x.scales;
-  f.tiles = r.tiles;
-  f.num_tiles = r.num_tiles;
-  f.sorted_pairs = r.sorted_pairs;
-  f.ids = m.arm == kPairs ? ids : nullptr;
   f.row_bytes = f.x_stride = K;
-  f.M = static_cast<int>(m.P);
+  f.M = static_cast<int>(M);
   f.E = E;
   f.N = N;
   f.top_k = top_k;
-  f.steps = steps;
-  f.w_blocks = (N + kFp8Block - 1) / kFp8Block;
-  f.gather = gather;
-  f.scatter = scatter;
-  f.y = out;
-  f.y_type = TQ_FP32;
+  f.steps = blocks_of(K);
+  f.w_blocks = ((gated ? 2 * N : N) + kFp8Block - 1) / kFp8Block;
+  f.segments = 1;
+  f.y = y;
+  f.y_type = y_type;
   f.err = err;
-  return launch_few_rows(f, kFewRowsFp8, false, m.arm == kPairs ? 8 : m.tile_m, m.arm == kPairs ? m.P : m.cap, s);
+  return f;
+}
+void set_tiles(FewRows& f, const Routed& r) {
+  f.tiles = r.tiles;
+  f.num_tiles = r.num_tiles;
+  f.sorted_pairs = r.sorted_pairs;
+}
+
+// The product of sorted pairs to partial sums by pair, its rows gathered from the
+// tokens or in slot order.
+int sorted_product(const MoePlan& m, const Routed& r, Operand x, int64_t x_rows, bool gather, Operand w, int top_k, int E,
+                   int K, int N, TileChoice tile, float* part, int* err, cudaStream_t s) {
+  if (m.arm == kTiles) {
+    Fp8Gemm g{x.codes, x.scales, x_rows, w.codes, w.scales, r.sorted_pairs, r.tiles, r.num_tiles, m.cap, m.P, top_k, E,
+              K, N, gather, true, false, m.tile_m, tile.cols, tile.splits, part, TQ_FP32, nullptr, nullptr, err};
+    return launch_fp8_gemm(g, s);
+  }
+  FewRows f = few_rows(x, w, m.P, top_k, E, K, N, false, part, TQ_FP32, err);
+  set_tiles(f, r);
+  f.gather = gather;
+  f.scatter = 1;
+  return launch_few_rows(f, kFewRowsFp8, false, m.tile_m, m.cap, s);
+}
+
+// y[t] = sum_j topk_w[t][j] W x, in one launch: x the token's row, or its pairs' rows.
+int token_product(FewRows f, const int32_t* ids, const float* topk_w, bool gather, int64_t n, cudaStream_t s) {
+  f.ids = ids;
+  f.topk_w = topk_w;
+  f.segments = f.top_k;
+  f.top_k = 1;
+  f.gather = gather;
+  return launch_few_rows(f, kFewRowsFp8, false, 8, n, s);
 }
 
 }  // namespace
@@ -259,23 +277,9 @@ int tq_fp8_linear(const uint8_t* x, const float* x_scales, const uint8_t* w, con
   if (rc != TQ_OK || n == 0) return rc;
   int* err = error_word(&rc);
   if (!err) return rc;
-  if (l.few) {
-    FewRows f{};
-    f.w = w;
-    f.x = x;
-    f.w_scales = w_scales;
-    f.x_scales = x_scales;
-    f.row_bytes = f.x_stride = K;
-    f.M = static_cast<int>(n);
-    f.E = f.top_k = 1;
-    f.N = N;
-    f.steps = blocks_of(K);
-    f.w_blocks = (N + kFp8Block - 1) / kFp8Block;
-    f.y = y;
-    f.y_type = y_type;
-    f.err = err;
-    return launch_few_rows(f, kFewRowsFp8, false, n <= 8 ? 8 : 16, 1, s);
-  }
+  if (l.few)
+    return launch_few_rows(few_rows({x, x_scales}, {w, w_scales}, n, 1, 1, K, N, false, y, y_type, err), kFewRowsFp8, false,
+                           n <= 8 ? 8 : 16, 1, s);
   Fp8Gemm g{x, x_scales, n, w, w_scales, nullptr, nullptr, nullptr, (n + l.tile.tile_m - 1) / l.tile.tile_m, n, 1, 1, K, N,
             false, false, false, l.tile.tile_m, l.tile.cols, l.tile.splits, splits ? l.part : y,
             splits ? TQ_FP32 : y_type, nullptr, nullptr, err};
@@ -298,16 +302,18 @@ int tq_fp8_moe_forward(const uint8_t* x, const float* x_scales, const uint8_t* w
                 !aligned(x_scales, 4) || !aligned(w_scales, 4) || !aligned(y, type_size(y_type))))
     return TQ_ERR_INVALID_ARG;
   const ProductPlan p = plan_moe(workspace, n, top_k, E, K, N);
-  if (n > 0 && bad_workspace(workspace, workspace_bytes, p.bytes)) return TQ_ERR_WORKSPACE;
+  if (n > 0 && p.m.arm != kTokens && bad_workspace(workspace, workspace_bytes, p.bytes)) return TQ_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int rc = require_sm103(s);
   if (rc != TQ_OK || n == 0) return rc;
   int* err = error_word(&rc);
   if (!err) return rc;
+  if (p.m.arm == kTokens)
+    return token_product(few_rows({x, x_scales}, {w, w_scales}, n, top_k, E, K, N, false, y, y_type, err), topk_ids, topk_w,
+                         true, n, s);
   rc = route_pairs(p.m, p.routed, topk_ids, E, err, s);
   if (rc != TQ_OK) return rc;
-  rc = routed_product(p.m, p.routed, topk_ids, {x, x_scales}, n, true, {w, w_scales}, top_k, E, K, N, p.tile, true, p.part,
-                      err, s);
+  rc = sorted_product(p.m, p.routed, {x, x_scales}, n, true, {w, w_scales}, top_k, E, K, N, p.tile, p.part, err, s);
   if (rc != TQ_OK) return rc;
   return launch_fp4_combine(p.part, p.m.P * N, p.tile.splits, topk_ids, topk_w, nullptr, nullptr, n, top_k, E, N, y,
                             y_type, s);
@@ -345,13 +351,20 @@ int tq_fp8_moe_mlp_forward(const uint8_t* x, const float* x_scales, const uint8_
               false, true, m.tile_m, 128, 1, nullptr, TQ_FP32, p.h, p.h_scales, err};
     rc = launch_fp8_gemm(g, s);
   } else {
-    rc = routed_product(m, r, topk_ids, {x, x_scales}, n, true, {w_gu, gu_scales}, top_k, E, H, 2 * I, {}, false,
-                        p.gate_up, err, s);
-    if (rc == TQ_OK) rc = launch_fp8_swiglu(p.gate_up, m.P, I, p.h, p.h_scales, s);
+    FewRows f = few_rows({x, x_scales}, {w_gu, gu_scales}, m.P, top_k, E, H, I, true, p.h32, TQ_FP32, err);
+    f.gather = 1;
+    if (m.arm == kTokens)
+      f.ids = topk_ids;
+    else
+      set_tiles(f, r);
+    rc = launch_few_rows(f, kFewRowsFp8, true, m.arm == kTokens ? 8 : m.tile_m, m.arm == kTokens ? m.P : m.cap, s);
+    if (rc == TQ_OK) rc = launch_fp8_quantize_rows(p.h32, TQ_FP32, I, m.P, I, p.h, p.h_scales, s);
+    if (rc == TQ_OK && m.arm == kTokens)
+      return token_product(few_rows({p.h, p.h_scales}, {w_down, down_scales}, n, top_k, E, I, H, false, y, y_type, err),
+                           topk_ids, topk_w, false, n, s);
   }
   if (rc != TQ_OK) return rc;
-  rc = routed_product(m, r, topk_ids, {p.h, p.h_scales}, m.P, false, {w_down, down_scales}, top_k, E, I, H, p.down, true,
-                      p.part, err, s);
+  rc = sorted_product(m, r, {p.h, p.h_scales}, m.P, false, {w_down, down_scales}, top_k, E, I, H, p.down, p.part, err, s);
   if (rc != TQ_OK) return rc;
   return launch_fp4_combine(p.part, m.P * H, p.down.splits, topk_ids, topk_w, nullptr, nullptr, n, top_k, E, H, y, y_type,
                             s);

@@ -1,5 +1,5 @@
-// 8-bit block-scaled values: quantise (rows, and matrices in blocks of 128 x 128),
-// dequantise, and the SwiGLU experts' h from the gate and up sums of few rows.
+// 8-bit block-scaled values: quantise (rows, and matrices in blocks of 128 x 128) and
+// dequantise.
 //
 // All of these move bytes: a thread takes 16 consecutive values, a block of 128 of a
 // row is eight neighbouring lanes, which share their maximum by three shuffles.
@@ -145,40 +145,6 @@ fp8_dequantize_kernel(const uint8_t* __restrict__ codes, const float* __restrict
   }
 }
 
-// h = silu(gate) * up of rows [rows][2 I], I a multiple of 128, in 8 bits.
-__global__ void __launch_bounds__(kThreads)
-fp8_swiglu_kernel(const float* __restrict__ gate_up, long long rows, int I, uint8_t* __restrict__ codes,
-                  float* __restrict__ scales) {
-  pdl_wait();
-  pdl_trigger();
-  const int items = I / 16;   // a multiple of 8: whole blocks of lanes
-  const long long total = rows * items, step = static_cast<long long>(gridDim.x) * kThreads;
-  const int lane = threadIdx.x & 31;
-  for (long long i0 = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x - lane; i0 < total; i0 += step) {
-    const long long i = i0 + lane;
-    float v[16] = {};
-    if (i < total) {
-      const long long row = i / items;
-      const float4* const g = reinterpret_cast<const float4*>(gate_up + row * 2 * I + 16 * (i - row * items));
-      const float4* const u = g + I / 4;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 a = __ldcs(g + j), b = __ldcs(u + j);
-        v[4 * j] = a.x / (1.f + expf(-a.x)) * b.x;
-        v[4 * j + 1] = a.y / (1.f + expf(-a.y)) * b.y;
-        v[4 * j + 2] = a.z / (1.f + expf(-a.z)) * b.z;
-        v[4 * j + 3] = a.w / (1.f + expf(-a.w)) * b.w;
-      }
-    }
-    const float top = top_of_eight(fp8_top<16>(v));
-    if (i < total) {
-      const Fp8Scale s(top);
-      reinterpret_cast<uint4*>(codes)[i] = fp8_codes16(v, s);
-      if ((lane & 7) == 0) scales[i / 8] = s.s;
-    }
-  }
-}
-
 int blocks_for(long long warps_of_work) {
   const long long per = kThreads / 32;
   return static_cast<int>(std::max<long long>(
@@ -231,13 +197,6 @@ int launch_fp8_dequantize(const uint8_t* codes, const float* scales, int E, int6
                       static_cast<T*>(out));
   });
   if (st == TQ_OK) count_launch(kCntFp8Dequantize);
-  return st;
-}
-
-int launch_fp8_swiglu(const float* gate_up, int64_t rows, int I, uint8_t* codes, float* scales, cudaStream_t s) {
-  const int st = launch_pdl(fp8_swiglu_kernel, dim3(blocks_for((rows * (I / 16) + 31) / 32)), dim3(kThreads), 0, s,
-                            gate_up, static_cast<long long>(rows), I, codes, scales);
-  if (st == TQ_OK) count_launch(kCntFp8Swiglu);
   return st;
 }
 

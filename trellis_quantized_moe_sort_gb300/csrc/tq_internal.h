@@ -24,7 +24,7 @@ enum Counter {
   // from here on only in tq_launch_counts_all
   kCntRouterScored, kCntRouterScoredBackward, kCntFp4Quantize, kCntFp4Dequantize, kCntFp4TileScales, kCntFp4Stage,
   kCntFp4Gemm, kCntFp4Combine, kCntFp4Swiglu, kCntFp4Gemv, kCntNorm, kCntNormBackward, kCntNormWeight, kCntFp8Quantize,
-  kCntFp8Dequantize, kCntFp8Swiglu, kCntFp8Gemm, kCntFewRows, kCntGatedGemm, kCntSwigluGrad, kCntNum
+  kCntFp8Dequantize, kCntFp8Gemm, kCntFewRows, kCntGatedGemm, kCntSwigluGrad, kCntNum
 };
 static_assert(kCntRouterScored == TQ_NUM_LAUNCH_COUNTERS, "counter layout of tq_launch_counts");
 static_assert(kCntNum == TQ_NUM_ALL_LAUNCH_COUNTERS, "counter layout of tq_launch_counts_all");
@@ -246,8 +246,6 @@ int launch_fp8_quantize_blocks(const void* x, int type, int64_t stride, int E, i
                                float* scales, cudaStream_t s);
 int launch_fp8_dequantize(const uint8_t* codes, const float* scales, int E, int64_t N, int K, int rows_per_block,
                           void* out, int type, cudaStream_t s);
-// h = silu(gate) * up of rows [rows][2 I] in fp32, kept in 8 bits.
-int launch_fp8_swiglu(const float* gate_up, int64_t rows, int I, uint8_t* codes, float* scales, cudaStream_t s);
 
 // Product of 8-bit rows with 8-bit matrices on the tensor cores (tq_tile_gemm.cuh).
 struct Fp8Gemm {
@@ -291,16 +289,18 @@ struct GemmF16 {
 };
 int launch_gemm_f16(const GemmF16& g, cudaStream_t s);
 
-// Products with few activation rows a matrix (tq_few_rows.cu).
+// Products with few activation rows a matrix (tq_few_rows.cu); in 16 bits the gated one alone.
 struct FewRows {
   const uint8_t* w;             // [E][N] rows, gated [2 N]
   const uint8_t* x;
   const float *w_scales, *x_scales;   // 8 bits
   const int32_t *tiles, *num_tiles, *sorted_pairs;   // a unit = an m-tile
-  const int32_t* ids;           // without tiles: a unit = a pair
-  long long row_bytes, x_stride;   // bytes: of a row's values; between rows of x
-  int M, E, N, top_k, steps, w_blocks;
-  int gather, scatter;
+  const int32_t* ids;           // without tiles: a unit = `segments` pairs of one row of the output
+  const float* topk_w;          // with segments: their weights
+  long long row_bytes, x_stride;   // bytes: of a row of w; between rows of x
+  int M, E, N, top_k, steps, w_blocks;   // M: slots, pairs, or (segments > 1) tokens
+  int segments;
+  int gather, scatter;          // as in Fp8Gemm; gather with segments: x holds token rows
   void* y;
   int y_type;
   float* gate_up;

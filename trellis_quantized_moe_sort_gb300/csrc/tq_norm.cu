@@ -36,40 +36,70 @@ struct Sum2 {
     lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(v, b)));
     hi = s;
   }
-  __device__ __forceinline__ void add_square(float v) {
-    const float p = __fmul_rn(v, v);
-    add(p);
-    lo = __fadd_rn(lo, __fmaf_rn(v, v, -p));   // 0 for 16-bit values
-  }
 };
-__device__ __forceinline__ Sum2 warp_sum(Sum2 s) {
+// The sum of a thread's squares: two sums side by side, two operations an instruction.
+// kExact: a square has no rounding error (values of 16 bits).
+template <bool kExact>
+__device__ __forceinline__ Sum2 sum_of_squares(const float (&v)[kPer], float scale) {
+  float2 hi = make_float2(0.f, 0.f), lo = hi;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int i = 0; i < kPer; i += 2) {
+    float2 a = make_float2(v[i], v[i + 1]);
+    if (!kExact) a = mul2(a, make_float2(scale, scale));
+    const float2 p = mul2(a, a), s = add2(hi, p), b = sub2(s, hi);
+    lo = add2(lo, add2(sub2(hi, sub2(s, b)), sub2(p, b)));
+    if (!kExact) lo = add2(lo, fma2(a, a, make_float2(-p.x, -p.y)));
+    hi = s;
+  }
+  Sum2 s;
+  s.hi = hi.x;
+  s.lo = lo.x;
+  s.add(hi.y);
+  s.lo = __fadd_rn(s.lo, lo.y);
+  return s;
+}
+// Over the lanes, or the first `lanes` of them (a power of two).
+__device__ __forceinline__ Sum2 warp_sum(Sum2 s, int lanes = 32) {
+  for (int o = lanes / 2; o > 0; o >>= 1) {
     const float hi = __shfl_xor_sync(kAll, s.hi, o), lo = __shfl_xor_sync(kAll, s.lo, o);
     s.add(hi);
     s.lo = __fadd_rn(s.lo, lo);
   }
   return s;
 }
-__device__ __forceinline__ float warp_sum(float s) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+__device__ __forceinline__ float warp_sum(float s, int lanes = 32) {
+  for (int o = lanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
   return s;
 }
 
-// 1 / sqrt(m) rounded to fp32: one Newton step in 64 bits from the approximation.
-__device__ __forceinline__ float rsqrt_rounded(double m) {
-  double back = 1.0;
-  if (m > 0x1p100) {
-    m *= 0x1p-200;   // up to 2^256
-    back = 0x1p-100;
-  } else if (m < 0x1p-100) {
-    m *= 0x1p200;
-    back = 0x1p100;
+// 1 / sqrt(hi + lo), rounded to fp32: a Newton step from the approximation r, its
+// residual 1 - m r^2 by exact products.  (In 64 bits the step would take longer than
+// the row: an SM does two such operations a clock.)
+__device__ __forceinline__ float rsqrt_rounded(float hi, float lo) {
+  float back = 1.f;
+  if (hi > 0x1p100f) {
+    hi *= 0x1p-100f;
+    lo *= 0x1p-100f;
+    back = 0x1p-50f;
+  } else if (hi < 0x1p-80f) {
+    hi *= 0x1p60f;
+    lo *= 0x1p60f;
+    back = 0x1p30f;
   }
-  const double r = rsqrtf(static_cast<float>(m));
-  if (!(r < 3e38) || r == 0.0) return static_cast<float>(r);   // of 0, infinity or NaN
-  return static_cast<float>(back * (r + 0.5 * r * (1.0 - m * r * r)));
+  const float r = rsqrtf(hi);
+  if (!(r < 3e38f) || r == 0.f) return r;   // of 0, infinity or NaN
+  const float t = __fmul_rn(r, r), t_lo = __fmaf_rn(r, r, -t);
+  const float e = __fmaf_rn(-hi, t, 1.f) - hi * t_lo - lo * t;
+  return __fmul_rn(__fmaf_rn(0.5f * r, e, r), back);
+}
+// 1 / sqrt(s / K + eps).
+__device__ __forceinline__ float rstd_of(const Sum2& s, float K, float eps) {
+  if (!(s.hi <= FLT_MAX)) return rsqrtf(s.hi);
+  const float q = __fdiv_rn(s.hi, K), q_lo = __fdiv_rn(__fmaf_rn(-q, K, s.hi) + s.lo, K);
+  Sum2 m;
+  m.hi = q;
+  m.add(eps);
+  return rsqrt_rounded(m.hi, m.lo + q_lo);
 }
 
 // A thread's columns: 16 consecutive ones, or every blockDim.x-th.
@@ -78,27 +108,31 @@ __device__ __forceinline__ int column(int i) {
   return kVec ? kPer * static_cast<int>(threadIdx.x) + i : static_cast<int>(threadIdx.x) + i * static_cast<int>(blockDim.x);
 }
 
+// A thread's values of a row as they are in memory; zeros past its end.
 template <bool kVec, typename T>
-__device__ __forceinline__ void load16(const T* __restrict__ p, int K, float (&v)[kPer]) {
-  if constexpr (kVec) {
-    T t[kPer];
-    if (column<true>(0) < K) {
+struct Raw {
+  alignas(16) T t[kPer];
+  __device__ __forceinline__ void load(const T* p, int K) {
+    if constexpr (kVec) {
 #pragma unroll
       for (int i = 0; i < static_cast<int>(sizeof(T)); ++i)
-        reinterpret_cast<uint4*>(t)[i] = reinterpret_cast<const uint4*>(p + column<true>(0))[i];
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) v[i] = widen(t[i]);
+        reinterpret_cast<uint4*>(t)[i] = column<true>(0) < K ? reinterpret_cast<const uint4*>(p + column<true>(0))[i]
+                                                             : make_uint4(0u, 0u, 0u, 0u);
     } else {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) v[i] = 0.f;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int c = column<false>(i);
-      v[i] = c < K ? widen(p[c]) : 0.f;
+      for (int i = 0; i < kPer; ++i) t[i] = column<false>(i) < K ? p[column<false>(i)] : narrow<T>(0.f);
     }
   }
+  __device__ __forceinline__ void open(float (&v)[kPer]) const {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = widen(t[i]);
+  }
+};
+template <bool kVec, typename T>
+__device__ __forceinline__ void load16(const T* p, int K, float (&v)[kPer]) {
+  Raw<kVec, T> raw;
+  raw.load(p, K);
+  raw.open(v);
 }
 template <bool kVec, typename T>
 __device__ __forceinline__ void store16(T* __restrict__ p, int K, const float (&v)[kPer]) {
@@ -128,68 +162,96 @@ __device__ __forceinline__ void load_weight(const void* w, int type, int K, floa
     load16<kVec>(static_cast<const __half*>(w), K, v);
 }
 
+// Lanes that a sum over the block's warps takes.
+__device__ __forceinline__ int power_above(int warps) { return warps > 1 ? 1 << (32 - __clz(warps - 1)) : 1; }
+
+// rstd of a row from its threads' sums of squares times scale^2, or, for a first sum
+// (scale 1) that did not keep its range, kTooLarge or kTooSmall.  One warp adds up and
+// takes the root: with every warp doing so a block's eight of them spent a third of
+// their instructions on it.
+constexpr float kTooLarge = -1.f, kTooSmall = -2.f;
+__device__ __forceinline__ float block_rstd(Sum2 s, float scale, const NormArgs& a, int lane, int warp, int warps,
+                                            int lanes, int& buffer, Sum2 (&parts)[2][32], float (&result)[2]) {
+  s = warp_sum(s);
+  if (warps > 1) {
+    if (lane == 0) parts[buffer][warp] = s;
+    __syncthreads();
+    if (warp == 0) {
+      s = lane < warps ? parts[buffer][lane] : Sum2();
+      s = warp_sum(s, lanes);
+    }
+  }
+  if (warp == 0 && lane == 0) {
+    float r = rstd_of(s, static_cast<float>(a.K), a.eps * scale * scale) * scale;
+    if (scale == 1.f && s.hi > FLT_MAX) r = kTooLarge;
+    if (scale == 1.f && s.hi < 0x1p-100f && a.eps < 0x1p-100f) r = kTooSmall;
+    result[buffer] = r;
+  }
+  __syncthreads();
+  // (written again after the next sum's first barrier; of one warp, after its second)
+  const float r = result[buffer];
+  buffer ^= 1;
+  return r;
+}
+
+// Blocks walk the rows, the next row's loads under way while the present one is summed
+// and written.
 template <typename T, bool kVec, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads) rms_norm_kernel(const NormArgs a) {
-  __shared__ Sum2 parts[32];
-  __shared__ float shared_rstd;
+__global__ void __launch_bounds__(kMaxThreads, kMaxThreads == 256 ? 4 : 1) rms_norm_kernel(const NormArgs a) {
+  __shared__ Sum2 parts[2][32];
+  __shared__ float result[2];
   pdl_wait();
   pdl_trigger();
   const int K = a.K, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32;
-  const long long row = blockIdx.x;
-  float v[kPer];
-  load16<kVec>(static_cast<const T*>(a.x) + row * a.x_stride, K, v);
-  if (a.residual) {
-    float r[kPer];
-    load16<kVec>(static_cast<const T*>(a.residual) + row * a.residual_stride, K, r);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] = widen(narrow<T>(v[i] + r[i]));
-    store16<kVec>(static_cast<T*>(a.residual_out) + row * K, K, v);
-  }
+  const int lanes = power_above(warps);
+  const T* const x = static_cast<const T*>(a.x);
+  const T* const residual = static_cast<const T*>(a.residual);
+  Raw<kVec, T> next_x, next_r = {};
+  next_x.load(x + blockIdx.x * a.x_stride, K);
+  if (residual) next_r.load(residual + blockIdx.x * a.residual_stride, K);
   float w[kPer];
-  if (a.weight) load_weight<kVec>(a.weight, a.w_type, K, w);   // under way while the row is summed
-
-  // Squares of values beyond 2^63 overflow: such a row is summed again, 2^-96 of it.
-  for (float scale = 1.f;; scale = 0x1p-96f) {
-    Sum2 s;
+  if (a.weight) load_weight<kVec>(a.weight, a.w_type, K, w);
+  int buffer = 0;
+  for (long long row = blockIdx.x; row < a.n; row += gridDim.x) {
+    Raw<kVec, T> r = next_x;
+    float v[kPer];
+    if (residual) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) s.add_square(v[i] * scale);
-    s = warp_sum(s);
-    if (lane == 0) parts[warp] = s;
-    __syncthreads();
-    if (warp == 0) {
-      s = lane < warps ? parts[lane] : Sum2();
-      s = warp_sum(s);
-      if (lane == 0) {
-        if (scale == 1.f && s.hi > FLT_MAX) {
-          shared_rstd = -1.f;
-        } else {
-          // (a sum that overflowed makes its error term NaN)
-          double m = static_cast<double>(s.hi) + (s.hi <= FLT_MAX ? static_cast<double>(s.lo) : 0.0);
-          if (scale != 1.f) m *= 0x1p192;
-          shared_rstd = rsqrt_rounded(m / K + static_cast<double>(a.eps));
-        }
-      }
+      for (int i = 0; i < kPer; ++i) r.t[i] = narrow<T>(widen(r.t[i]) + widen(next_r.t[i]));
     }
-    __syncthreads();
-    if (shared_rstd >= 0.f || scale != 1.f || shared_rstd != shared_rstd) break;
-  }
-  const float rstd = shared_rstd;
-  if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+    if (row + gridDim.x < a.n) {
+      next_x.load(x + (row + gridDim.x) * a.x_stride, K);
+      if (residual) next_r.load(residual + (row + gridDim.x) * a.residual_stride, K);
+    }
+    r.open(v);
+    if (residual) store16<kVec>(static_cast<T*>(a.residual_out) + row * K, K, v);
+
+    // Squares of values beyond 2^63 overflow, and where eps does not count those of tiny
+    // values underflow: such a row is summed again, 2^-96 or 2^90 of it.
+    float rstd = block_rstd(sum_of_squares<sizeof(T) == 2>(v, 1.f), 1.f, a, lane, warp, warps, lanes, buffer, parts, result);
+    if (rstd < 0.f) {
+      const float scale = rstd == kTooLarge ? 0x1p-96f : 0x1p90f;
+      rstd = block_rstd(sum_of_squares<false>(v, scale), scale, a, lane, warp, warps, lanes, buffer, parts, result);
+    }
+    if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    v[i] = __fmul_rn(v[i], rstd);
-    if (a.weight) v[i] = __fmul_rn(v[i], w[i]);
-  }
-  if (a.y) store16<kVec>(static_cast<T*>(a.y) + row * K, K, v);
-  if constexpr (kVec) {
-    if (a.codes) {   // a block of 128 is eight neighbouring threads
-      float top = fp8_top<kPer>(v);
+    for (int i = 0; i < kPer; i += 2) {
+      float2 t = mul2(make_float2(v[i], v[i + 1]), make_float2(rstd, rstd));
+      if (a.weight) t = mul2(t, make_float2(w[i], w[i + 1]));
+      v[i] = t.x;
+      v[i + 1] = t.y;
+    }
+    if (a.y) store16<kVec>(static_cast<T*>(a.y) + row * K, K, v);
+    if constexpr (kVec) {
+      if (a.codes) {   // a block of 128 is eight neighbouring threads
+        float top = fp8_top<kPer>(v);
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-      if (column<true>(0) < K) {
-        const Fp8Scale s(top);
-        *reinterpret_cast<uint4*>(a.codes + row * K + column<true>(0)) = fp8_codes16(v, s);
-        if ((lane & 7) == 0) a.scales[row * ((K + kFp8Block - 1) / kFp8Block) + threadIdx.x / 8] = s.s;
+        for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+        if (column<true>(0) < K) {
+          const Fp8Scale s(top);
+          *reinterpret_cast<uint4*>(a.codes + row * K + column<true>(0)) = fp8_codes16(v, s);
+          if ((lane & 7) == 0) a.scales[row * ((K + kFp8Block - 1) / kFp8Block) + threadIdx.x / 8] = s.s;
+        }
       }
     }
   }
@@ -200,6 +262,19 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_kernel(const No
   __shared__ float parts[2][32];
   pdl_wait();
   const int K = a.K, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32;
+  const int lanes = power_above(warps);
+  const T* const x = static_cast<const T*>(a.x);
+  const T* const grad_y = static_cast<const T*>(a.grad_y);
+  const T* const grad_r = static_cast<const T*>(a.grad_residual);
+  Raw<kVec, T> next_x, next_y, next_r = {};
+  float next_rstd = 0.f;
+  auto fetch = [&](long long row) {
+    next_x.load(x + row * a.x_stride, K);
+    next_y.load(grad_y + row * a.grad_y_stride, K);
+    if (grad_r) next_r.load(grad_r + row * a.grad_residual_stride, K);
+    next_rstd = a.rstd[row];
+  };
+  fetch(blockIdx.x);
   float w[kPer], gw[kPer] = {};
   if (a.weight) {
     load_weight<kVec>(a.weight, a.w_type, K, w);
@@ -209,29 +284,28 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_kernel(const No
   }
   int buffer = 0;
   for (long long row = blockIdx.x; row < a.n; row += gridDim.x, buffer ^= 1) {
+    const Raw<kVec, T> g = next_r;
+    const float rstd = next_rstd;
     float v[kPer], d[kPer], dot = 0.f;
-    load16<kVec>(static_cast<const T*>(a.x) + row * a.x_stride, K, v);
-    load16<kVec>(static_cast<const T*>(a.grad_y) + row * a.grad_y_stride, K, d);
-    const float rstd = __ldg(a.rstd + row);
+    next_x.open(v);
+    next_y.open(d);
+    if (row + gridDim.x < a.n) fetch(row + gridDim.x);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      gw[i] = fmaf(d[i], v[i] * rstd, gw[i]);
-      d[i] *= w[i];
       v[i] *= rstd;
+      gw[i] = fmaf(d[i], v[i], gw[i]);
+      d[i] *= w[i];
       dot = fmaf(d[i], v[i], dot);
     }
     dot = warp_sum(dot);
     if (lane == 0) parts[buffer][warp] = dot;   // read until the next row's barrier at the latest
     __syncthreads();
     dot = lane < warps ? parts[buffer][lane] : 0.f;
-    dot = warp_sum(dot) / static_cast<float>(K);
+    dot = __shfl_sync(kAll, warp_sum(dot, lanes), 0) / static_cast<float>(K);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) d[i] = rstd * (d[i] - v[i] * dot);
-    if (a.grad_residual) {
-      float g[kPer];
-      load16<kVec>(static_cast<const T*>(a.grad_residual) + row * a.grad_residual_stride, K, g);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) d[i] += g[i];
+    for (int i = 0; i < kPer; ++i) {
+      d[i] = rstd * (d[i] - v[i] * dot);
+      if (grad_r) d[i] += widen(g.t[i]);
     }
     store16<kVec>(static_cast<T*>(a.grad_x) + row * K, K, d);
   }
@@ -278,12 +352,34 @@ bool bad_rows(const void* p, int64_t stride, int64_t n, int K) {
 }
 bool bad_width(int K) { return K < 1 || K > TQ_NORM_MAX_WIDTH; }
 
+// Blocks of a kernel that the device holds at once (asked once per kernel, block and device).
+template <typename Kernel>
+long long resident(Kernel kernel, int threads) {
+  struct Entry {
+    const void* kernel;
+    int threads, sms, blocks;
+  };
+  static thread_local Entry kept[64];
+  const int sms = sm_count();
+  const void* const id = reinterpret_cast<const void*>(kernel);
+  Entry& e = kept[(reinterpret_cast<uintptr_t>(id) / 16 + threads / 32) % 64];
+  if (e.kernel != id || e.threads != threads || e.sms != sms) {
+    int per_sm = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0) != cudaSuccess) cudaGetLastError();
+    e = {id, threads, sms, sms * std::max(1, per_sm)};
+  }
+  return e.blocks;
+}
+
 template <typename T>
 int run_norm(const NormArgs& a, bool vec, cudaStream_t s) {
   const int threads = block_threads(a.K);
-  auto kernel = vec ? (threads <= 512 ? rms_norm_kernel<T, true, 512> : rms_norm_kernel<T, true, 1024>)
+  auto kernel = vec ? (threads <= 256   ? rms_norm_kernel<T, true, 256>
+                       : threads <= 512 ? rms_norm_kernel<T, true, 512>
+                                        : rms_norm_kernel<T, true, 1024>)
                     : (threads <= 512 ? rms_norm_kernel<T, false, 512> : rms_norm_kernel<T, false, 1024>);
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(a.n)), dim3(threads), 0, s, a);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(std::min<long long>(a.n, resident(kernel, threads)))), dim3(threads),
+                    0, s, a);
 }
 
 template <typename T>
@@ -295,9 +391,9 @@ int run_backward(const NormGradArgs& a, bool vec, int blocks, cudaStream_t s) {
   return launch_pdl(kernel, dim3(blocks), dim3(threads), 0, s, a);
 }
 
-// Blocks of the gradient: what the SMs hold at once at 64 registers a thread.
+// Blocks of the gradient: what the SMs hold at once at 128 registers a thread.
 int backward_blocks(int64_t n, int K) {
-  const int per_sm = std::max(1, std::min(16, 1024 / block_threads(K)));
+  const int per_sm = std::max(1, std::min(16, 512 / block_threads(K)));
   return static_cast<int>(std::min<int64_t>(n, static_cast<int64_t>(sm_count()) * per_sm));
 }
 

@@ -70,7 +70,7 @@ int forward(const void* x, int type, int64_t x_stride, const void* w, int64_t n,
     f.row_bytes = 2ll * H;
     f.x_stride = 2 * x_stride;
     f.M = static_cast<int>(n);
-    f.E = f.top_k = 1;
+    f.E = f.top_k = f.segments = 1;
     f.N = I;
     f.steps = (H + 63) / 64;
     f.y = h;

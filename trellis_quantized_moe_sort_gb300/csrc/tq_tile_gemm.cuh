@@ -249,7 +249,7 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "memory");
 }
 // (a.x, a.y) + (p.x, p.y) * f, each rounded once, in one instruction.
-__device__ __forceinline__ void fma2(float2& a, uint32_t p0, uint32_t p1, float f) {
+__device__ __forceinline__ void add_scaled(float2& a, uint32_t p0, uint32_t p1, float f) {
   asm("{\n\t.reg .b64 a, p, f;\n\t"
       "mov.b64 a, {%0, %1};\n\tmov.b64 p, {%2, %3};\n\tmov.b64 f, {%4, %4};\n\t"
       "fma.rn.f32x2 a, p, f, a;\n\t"
@@ -673,7 +673,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
             }
             const float f = kGated && c >= kCols / 64 ? f1 : f0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) fma2(sum[16 * c + i], v[c & 1][2 * i], v[c & 1][2 * i + 1], f);
+            for (int i = 0; i < 16; ++i) add_scaled(sum[16 * c + i], v[c & 1][2 * i], v[c & 1][2 * i + 1], f);
             if (c + 2 < kChunks) tmem_ld32(src + chunk_at(c + 2), v[c & 1]);
           }
           acc.advance(accs);
