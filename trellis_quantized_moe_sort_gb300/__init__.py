@@ -694,6 +694,20 @@ def _type_code(dtype, name):
     return code
 
 
+_device_fn = None
+
+
+def _current_device():
+    """The current device, by the C-level getter where this torch build has it (half
+    the public one's time, once that has set CUDA up)."""
+    global _device_fn
+    if _device_fn is None:
+        torch = _torch()
+        torch.cuda.current_device()
+        _device_fn = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _device_fn()
+
+
 def _elsewhere(t, device, name):
     """The kernels run on the current device: every tensor of a call has to be there."""
     return ValueError(f"{name} is on cuda:{t.get_device()}, the call runs on cuda:{device}" if t.is_cuda
@@ -704,8 +718,10 @@ def _rows(t, name):
     """(address, type code, elements between rows, rows, elements, device) of a 2-D
     tensor with contiguous rows on the current CUDA device."""
     try:
-        code = _type_code(t.dtype, name)
-        device = _torch().cuda.current_device()
+        code = _type_codes.get(t.dtype) if _type_codes is not None else None
+        if code is None:
+            code = _type_code(t.dtype, name)
+        device = _current_device()
         if t.get_device() != device:
             raise _elsewhere(t, device, name)
         shape = t.shape
@@ -1023,18 +1039,10 @@ def tq_fp4_moe_mlp_forward(x, packed_gu, tiled_gu, packed_down, tiled_down, topk
 
 # ------------------------------------------------------------------ norm
 
-def _dense(t, rows, width, dtype, name, device, x, stream):
-    """(tensor, address) of a dense output [rows, width]: the caller's, or a new one."""
-    if t is None:
-        t = _empty((rows, width), dtype, x.device, stream)
-        return t, t.data_ptr()
-    return t, _given(t, (rows, width), (dtype,), name, device)
-
-
 def _same_rows(t, n, K, dtype, name):
     """(address, elements between rows) of rows that go with x [n, K]."""
     ptr, _, step, rows, width, _ = _rows(t, name)
-    if (rows, width) != (n, K):
+    if rows != n or width != K:
         raise ValueError(f"{name} has shape {(rows, width)}, expected {(n, K)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
@@ -1048,34 +1056,23 @@ def _norm_weight(weight, K, device):
     return _given(weight, (K,), (), "weight", device), _type_code(weight.dtype, "weight")
 
 
-def _norm(what, x, weight, eps, residual, residual_out, y, rstd, codes, scales, stream, has_y, has_codes):
-    torch, fp32, _, _ = _types()
+def _norm_rows(x, weight, residual, residual_out, stream):
+    """What both forms of the norm take: x's, the residual's and the weight's addresses
+    and strides, and residual_out."""
     ptr, code, step, n, K, device = _rows(x, "x")
     w_ptr, w_code = _norm_weight(weight, K, device)
-    r_ptr, r_step, o_ptr = None, 0, None
-    if residual is not None:
-        r_ptr, r_step = _same_rows(residual, n, K, x.dtype, "residual")
-        residual_out, o_ptr = _dense(residual_out, n, K, x.dtype, "residual_out", device, x, stream)
-    elif residual_out is not None:
-        raise ValueError("residual_out is an output of the addition of a residual")
-    y_ptr = rstd_ptr = c_ptr = s_ptr = None
-    if has_y:
-        y, y_ptr = _dense(y, n, K, x.dtype, "y", device, x, stream)
-        if rstd is None:
-            rstd = _empty((n,), torch.float32, x.device, stream)
-            rstd_ptr = rstd.data_ptr()
-        else:
-            rstd_ptr = _given(rstd, (n,), fp32, "rstd", device)
-    if has_codes:
-        if y is not None:
-            y_ptr = _given(y, (n, K), (x.dtype,), "y", device)
-        codes, c_ptr = _dense(codes, n, K, torch.float8_e4m3fn, "codes", device, x, stream)
-        scales, s_ptr = _dense(scales, n, -(-K // FP8_BLOCK), torch.float32, "scales", device, x, stream)
-    rc = _call("tq_rms_norm")(ptr, code, step, r_ptr, r_step, w_ptr, w_code, eps, n, K, o_ptr, y_ptr, rstd_ptr, c_ptr,
-                              s_ptr, _stream(stream, device))
-    if rc:
-        raise TQError(rc, what)
-    return y, residual_out if residual is not None else x, rstd, codes, scales
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out is an output of the addition of a residual")
+        return n, K, device, (ptr, code, step, None, 0, w_ptr, w_code), x, None
+    dtype = x.dtype
+    r_ptr, r_step = _same_rows(residual, n, K, dtype, "residual")
+    if residual_out is None:
+        residual_out = _empty((n, K), dtype, x.device, stream)
+        o_ptr = residual_out.data_ptr()
+    else:
+        o_ptr = _given(residual_out, (n, K), (dtype,), "residual_out", device)
+    return n, K, device, (ptr, code, step, r_ptr, r_step, w_ptr, w_code), residual_out, o_ptr
 
 
 def tq_rms_norm(x, weight=None, eps: float = 1e-6, residual=None, y=None, residual_out=None, rstd=None, stream=None):
@@ -1084,8 +1081,21 @@ def tq_rms_norm(x, weight=None, eps: float = 1e-6, residual=None, y=None, residu
     block's residual and the gradient take it (x itself without a residual; in place
     with residual_out=residual); rstd fp32 [n] = 1 / sqrt(mean(r^2) + eps).  weight:
     [K] of any of the three types, or None for ones."""
-    y, r, rstd, _, _ = _norm("tq_rms_norm", x, weight, eps, residual, residual_out, y, rstd, None, None, stream, True,
-                             False)
+    torch, fp32, _, _ = _types()
+    n, K, device, rows, r, o_ptr = _norm_rows(x, weight, residual, residual_out, stream)
+    if y is None:
+        y = _empty((n, K), x.dtype, x.device, stream)
+        y_ptr = y.data_ptr()
+    else:
+        y_ptr = _given(y, (n, K), (x.dtype,), "y", device)
+    if rstd is None:
+        rstd = _empty((n,), torch.float32, x.device, stream)
+        rstd_ptr = rstd.data_ptr()
+    else:
+        rstd_ptr = _given(rstd, (n,), fp32, "rstd", device)
+    rc = _call("tq_rms_norm")(*rows, eps, n, K, o_ptr, y_ptr, rstd_ptr, None, None, _stream(stream, device))
+    if rc:
+        raise TQError(rc, "tq_rms_norm")
     return y, r, rstd
 
 
@@ -1095,8 +1105,23 @@ def tq_rms_norm_fp8(x, weight=None, eps: float = 1e-6, residual=None, codes=None
     it -> (codes float8_e4m3fn [n, K], scales fp32 [n, ceil(K / 128)], r).  K a
     multiple of 16, rows 16-byte aligned.  With y (a tensor [n, K] in x's dtype) the
     unquantised output is written too."""
-    _, r, _, codes, scales = _norm("tq_rms_norm_fp8", x, weight, eps, residual, residual_out, y, None, codes, scales,
-                                   stream, False, True)
+    torch, fp32, _, _ = _types()
+    n, K, device, rows, r, o_ptr = _norm_rows(x, weight, residual, residual_out, stream)
+    y_ptr = None if y is None else _given(y, (n, K), (x.dtype,), "y", device)
+    blocks = (K + 127) // 128
+    if codes is None:
+        codes = _empty((n, K), torch.float8_e4m3fn, x.device, stream)
+        c_ptr = codes.data_ptr()
+    else:
+        c_ptr = _given(codes, (n, K), _fp8(), "codes", device)
+    if scales is None:
+        scales = _empty((n, blocks), torch.float32, x.device, stream)
+        s_ptr = scales.data_ptr()
+    else:
+        s_ptr = _given(scales, (n, blocks), fp32, "scales", device)
+    rc = _call("tq_rms_norm")(*rows, eps, n, K, o_ptr, y_ptr, None, c_ptr, s_ptr, _stream(stream, device))
+    if rc:
+        raise TQError(rc, "tq_rms_norm_fp8")
     return codes, scales, r
 
 
@@ -1115,7 +1140,7 @@ def tq_rms_norm_backward(grad_y, x, weight, rstd, grad_residual=None, grad_x=Non
     dy_ptr, dy_step = _same_rows(grad_y, n, K, x.dtype, "grad_y")
     w_ptr, w_code = _norm_weight(weight, K, device)
     g_ptr, g_step = (None, 0) if grad_residual is None else _same_rows(grad_residual, n, K, x.dtype, "grad_residual")
-    grad_x, gx_ptr = _dense(grad_x, n, K, x.dtype, "grad_x", device, x, stream)
+    grad_x, gx_ptr = _dense(grad_x, n, K, x, "grad_x", device, stream)
     gw_ptr = ws_ptr = None
     ws_bytes = 0
     if weight is not None:
@@ -1136,6 +1161,14 @@ def tq_rms_norm_backward(grad_y, x, weight, rstd, grad_residual=None, grad_x=Non
     return grad_x, grad_weight
 
 
+def _dense(t, rows, width, x, name, device, stream):
+    """(tensor, address) of a dense output [rows, width] in x's dtype: the caller's, or a new one."""
+    if t is None:
+        t = _empty((rows, width), x.dtype, x.device, stream)
+        return t, t.data_ptr()
+    return t, _given(t, (rows, width), (x.dtype,), name, device)
+
+
 # ------------------------------------------------------------------ 8-bit operators
 
 _code_types = None
@@ -1150,24 +1183,35 @@ def _fp8():
     return _code_types
 
 
-def _scale_shape(shape, rows_per_block):
-    return (*shape[:-2], -(-shape[-2] // rows_per_block), -(-shape[-1] // FP8_BLOCK))
-
-
 def _fp8_rows(x, x_scales):
     """(address, scales' address, rows, K, device) of 8-bit activations [n, K]."""
-    device = _torch().cuda.current_device()
+    device = _current_device()
     ptr = _there(x, _fp8(), "x", device)
-    if len(x.shape) != 2:
-        raise ValueError(f"x must have two dimensions, not {len(x.shape)}")
-    n, K = x.shape
-    return ptr, _given(x_scales, _scale_shape((n, K), 1), _types()[1], "x_scales", device), n, K, device
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x must have two dimensions, not {len(shape)}")
+    n, K = shape
+    return ptr, _given(x_scales, (n, (K + 127) // 128), _types()[1], "x_scales", device), n, K, device
 
 
-def _fp8_matrix(w, scales, shape, name, device):
-    """Addresses of 8-bit weights of a known shape and of their scales."""
-    return (_given(w, shape, _fp8(), name, device),
-            _given(scales, _scale_shape(shape, FP8_BLOCK), _types()[1], f"the scales of {name}", device))
+def _fp8_matrix(w, scales, E, N, K, name, device):
+    """Addresses of 8-bit weights [N, K] (E None) or [E, N, K] and of their scales."""
+    blocks = ((N + 127) // 128, (K + 127) // 128)
+    return (_given(w, (N, K) if E is None else (E, N, K), _fp8(), name, device),
+            _given(scales, blocks if E is None else (E, *blocks), _types()[1], f"the scales of {name}", device))
+
+
+def _fp8_blocking(shape, rows_per_block, name):
+    """(matrices, rows of each, K, shape of the scales) of values [n, K] or [E, n, K]."""
+    if rows_per_block != 1 and rows_per_block != FP8_BLOCK:
+        raise ValueError(f"rows_per_block must be 1 or {FP8_BLOCK}, not {rows_per_block}")
+    if len(shape) == 2:
+        n, K = shape
+        return 1, n, K, (-(-n // rows_per_block), (K + 127) // 128)
+    if len(shape) != 3:
+        raise ValueError(f"{name} must have two or three dimensions, not {len(shape)}")
+    E, n, K = shape
+    return E, n, K, (E, -(-n // rows_per_block), (K + 127) // 128)
 
 
 def tq_fp8_quantize(x, rows_per_block: int = 1, codes=None, scales=None, stream=None):
@@ -1177,29 +1221,22 @@ def tq_fp8_quantize(x, rows_per_block: int = 1, codes=None, scales=None, stream=
     activations (rows may be strided), 128 for weights."""
     torch, fp32, _, _ = _types()
     shape = x.shape
+    E, n, K, blocks = _fp8_blocking(shape, rows_per_block, "x")
     if len(shape) == 3:
-        E, n, K = shape
-        x = x.reshape(E * n, K) if x.is_contiguous() else x
-        if len(x.shape) != 2:
+        if not x.is_contiguous():
             raise ValueError("x [E, n, K] must be contiguous")
-    elif len(shape) == 2:
-        E, (n, K) = 1, shape
-    else:
-        raise ValueError(f"x must have two or three dimensions, not {len(shape)}")
-    if rows_per_block != 1 and rows_per_block != FP8_BLOCK:
-        raise ValueError(f"rows_per_block must be 1 or {FP8_BLOCK}, not {rows_per_block}")
+        x = x.view(E * n, K)
     ptr, code, step, _, _, device = _rows(x, "x")
     if codes is None:
         codes = _empty(shape, torch.float8_e4m3fn, x.device, stream)
         c_ptr = codes.data_ptr()
     else:
         c_ptr = _given(codes, shape, _fp8(), "codes", device)
-    want = _scale_shape(shape, rows_per_block)
     if scales is None:
-        scales = _empty(want, torch.float32, x.device, stream)
+        scales = _empty(blocks, torch.float32, x.device, stream)
         s_ptr = scales.data_ptr()
     else:
-        s_ptr = _given(scales, want, fp32, "scales", device)
+        s_ptr = _given(scales, blocks, fp32, "scales", device)
     rc = _call("tq_fp8_quantize")(ptr, code, step, E, n, K, rows_per_block, c_ptr, s_ptr, _stream(stream, device))
     if rc:
         raise TQError(rc, "tq_fp8_quantize")
@@ -1210,14 +1247,11 @@ def tq_fp8_dequantize(codes, scales, rows_per_block: int = 1, dtype=None, out=No
     """The values of tq_fp8_quantize's output, in `dtype` (fp32 when neither it nor
     `out` is given)."""
     torch, fp32, _, _ = _types()
-    device = torch.cuda.current_device()
+    device = _current_device()
     c_ptr = _there(codes, _fp8(), "codes", device)
     shape = codes.shape
-    if len(shape) not in (2, 3):
-        raise ValueError(f"codes must have two or three dimensions, not {len(shape)}")
-    if rows_per_block != 1 and rows_per_block != FP8_BLOCK:
-        raise ValueError(f"rows_per_block must be 1 or {FP8_BLOCK}, not {rows_per_block}")
-    s_ptr = _given(scales, _scale_shape(shape, rows_per_block), fp32, "scales", device)
+    E, n, K, blocks = _fp8_blocking(shape, rows_per_block, "codes")
+    s_ptr = _given(scales, blocks, fp32, "scales", device)
     if out is None:
         out = _empty(shape, torch.float32 if dtype is None else dtype, codes.device, stream)
         o_ptr = out.data_ptr()
@@ -1225,9 +1259,8 @@ def tq_fp8_dequantize(codes, scales, rows_per_block: int = 1, dtype=None, out=No
         if dtype is not None and out.dtype != dtype:
             raise TypeError(f"out has dtype {out.dtype}, not {dtype}")
         o_ptr = _given(out, shape, (), "out", device)
-    E = shape[0] if len(shape) == 3 else 1
-    rc = _call("tq_fp8_dequantize")(c_ptr, s_ptr, E, shape[-2], shape[-1], rows_per_block, o_ptr,
-                                    _type_code(out.dtype, "out"), _stream(stream, device))
+    rc = _call("tq_fp8_dequantize")(c_ptr, s_ptr, E, n, K, rows_per_block, o_ptr, _type_code(out.dtype, "out"),
+                                    _stream(stream, device))
     if rc:
         raise TQError(rc, "tq_fp8_dequantize")
     return out
@@ -1253,7 +1286,7 @@ def tq_fp8_linear(x, x_scales, w, w_scales, dtype=None, workspace=None, y=None, 
     (bf16 by default)."""
     ptr, xs_ptr, n, K, device = _fp8_rows(x, x_scales)
     N = w.shape[0]
-    w_ptr, ws_ptr = _fp8_matrix(w, w_scales, (N, K), "w", device)
+    w_ptr, ws_ptr = _fp8_matrix(w, w_scales, None, N, K, "w", device)
     work_ptr, work_bytes, workspace = _workspace(workspace, tq_fp8_linear_workspace_size, device, stream, n, K, N)
     y, y_ptr, y_code = _result(y, (n, N), dtype, x, stream, device)
     rc = _call("tq_fp8_linear")(ptr, xs_ptr, w_ptr, ws_ptr, n, K, N, work_ptr, work_bytes, y_ptr, y_code,
@@ -1275,7 +1308,7 @@ def tq_fp8_moe_forward(x, x_scales, w, w_scales, topk_ids, topk_w, dtype=None, w
     ptr, xs_ptr, n, K, device = _fp8_rows(x, x_scales)
     E, N = w.shape[0], w.shape[1]
     top_k = topk_ids.shape[1]
-    w_ptr, ws_ptr = _fp8_matrix(w, w_scales, (E, N, K), "w", device)
+    w_ptr, ws_ptr = _fp8_matrix(w, w_scales, E, N, K, "w", device)
     work_ptr, work_bytes, workspace = _workspace(workspace, tq_fp8_moe_workspace_size, device, stream, n, top_k, E, K, N,
                                                  keep_small=True)
     y, y_ptr, y_code = _result(y, (n, N), dtype, x, stream, device)
@@ -1300,8 +1333,8 @@ def tq_fp8_moe_mlp_forward(x, x_scales, w_gu, gu_scales, w_down, down_scales, to
     ptr, xs_ptr, n, H, device = _fp8_rows(x, x_scales)
     E, I = w_gu.shape[0], w_gu.shape[1] // 2
     top_k = topk_ids.shape[1]
-    gu_ptr, gus_ptr = _fp8_matrix(w_gu, gu_scales, (E, 2 * I, H), "w_gu", device)
-    d_ptr, ds_ptr = _fp8_matrix(w_down, down_scales, (E, H, I), "w_down", device)
+    gu_ptr, gus_ptr = _fp8_matrix(w_gu, gu_scales, E, 2 * I, H, "w_gu", device)
+    d_ptr, ds_ptr = _fp8_matrix(w_down, down_scales, E, H, I, "w_down", device)
     work_ptr, work_bytes, workspace = _workspace(workspace, tq_fp8_moe_mlp_workspace_size, device, stream, n, top_k, E, H,
                                                  I, keep_small=True)
     y, y_ptr, y_code = _result(y, (n, H), dtype, x, stream, device)
@@ -1332,7 +1365,7 @@ def tq_swiglu_linear(x, w_gu, h=None, gate_up=None, stream=None):
     ptr, code, step, n, H, device = _rows16(x)
     I = w_gu.shape[0] // 2
     w_ptr = _given(w_gu, (2 * I, H), (x.dtype,), "w_gu", device)
-    h, h_ptr = _dense(h, n, I, x.dtype, "h", device, x, stream)
+    h, h_ptr = _dense(h, n, I, x, "h", device, stream)
     gu_ptr = None if gate_up is None else _given(gate_up, (n, 2 * I), fp32, "gate_up", device)
     rc = _call("tq_swiglu_linear")(ptr, code, step, w_ptr, n, H, I, h_ptr, gu_ptr, _stream(stream, device))
     if rc:
@@ -1354,8 +1387,8 @@ def tq_swiglu_linear_backward(x, w_gu, grad_h, gate_up=None, grad_x=None, grad_w
     w_ptr = _given(w_gu, (2 * I, H), (x.dtype,), "w_gu", device)
     gh_ptr = _given(grad_h, (n, I), (x.dtype,), "grad_h", device)
     gu_ptr = None if gate_up is None else _given(gate_up, (n, 2 * I), fp32, "gate_up", device)
-    grad_x, gx_ptr = _dense(grad_x, n, H, x.dtype, "grad_x", device, x, stream)
-    grad_w_gu, gw_ptr = _dense(grad_w_gu, 2 * I, H, x.dtype, "grad_w_gu", device, x, stream)
+    grad_x, gx_ptr = _dense(grad_x, n, H, x, "grad_x", device, stream)
+    grad_w_gu, gw_ptr = _dense(grad_w_gu, 2 * I, H, x, "grad_w_gu", device, stream)
     work_ptr, work_bytes, workspace = _workspace(workspace, tq_swiglu_linear_backward_workspace_size, device, stream, n,
                                                  H, I, gate_up is not None, keep_small=True)
     rc = _call("tq_swiglu_linear_backward")(ptr, code, step, w_ptr, gu_ptr, gh_ptr, n, H, I, work_ptr, work_bytes, gx_ptr,
