@@ -184,12 +184,33 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* m, in
     tma_gather4_2d(dst, m, x, r.x, r.y, r.z, r.w, bar);
 }
 
+// The same to the CTAs of a mask, at the same place in each; the bytes count on the
+// barriers of the first CTAs of their pairs.
+__device__ __forceinline__ void load_box_to(uint32_t dst, const CUtensorMap* m, int32_t x, int32_t y, uint32_t bar,
+                                            uint16_t mask) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
+      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar), "h"(mask)
+      : "memory");
+}
+__device__ __forceinline__ void load_rows_to(uint32_t dst, const CUtensorMap* m, int32_t x, int4 r, uint32_t bar,
+                                             uint16_t mask) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      ".multicast::cluster [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar), "h"(mask)
+      : "memory");
+}
+
+// Arrives on the barrier (of each CTA of the mask) once every MMA issued so far has
+// completed.
 template <bool kPair>
-__device__ __forceinline__ void commit(uint32_t bar) {
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t mask) {
   if constexpr (kPair)
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(static_cast<uint16_t>(3))
+        "h"(static_cast<uint16_t>(mask))
         : "memory");
   else
     mma_commit(bar);
@@ -274,10 +295,15 @@ struct Unit {
   bool ok;
 };
 
-__device__ __forceinline__ Unit unit_at(const Params& p, long long u, int num_tiles) {
+// Unit u of a cluster; two pairs of CTAs take neighbouring column blocks of it (the
+// second of them past the matrix where their number is odd: its loads read what follows
+// and its results do not exist).
+template <bool kQuad>
+__device__ __forceinline__ Unit unit_at(const Params& p, long long u, int num_tiles, int col_units, int pair) {
   Unit t;
-  t.cb = static_cast<int>(u % p.col_blocks);
-  u /= p.col_blocks;
+  t.cb = static_cast<int>(u % col_units);
+  u /= col_units;
+  if (kQuad) t.cb = 2 * t.cb + pair;
   const int tile = static_cast<int>(u % num_tiles);
   t.split = static_cast<int>(u / num_tiles);
   t.k0 = static_cast<int>(static_cast<long long>(p.steps) * t.split / p.splits);
@@ -309,20 +335,32 @@ __device__ __forceinline__ int pair_of(const Params& p, int slot, int where) {
 __device__ __forceinline__ int gathered(int rows, int rank) {
   return (max(0, min(kRows, rows - rank * kRows)) + 3) / 4;
 }
+// Of those, the part that one of two pairs of CTAs gathers for both.
+__device__ __forceinline__ int part_of(int copies, int pair) { return max(0, min(kRows / 8, copies - pair * (kRows / 8))); }
 __device__ __forceinline__ int shared_copies(int n, int lead, int share) {
   return n / 8 * share + max(0, min(share, n % 8 - lead));
 }
 
 __device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
+// The same to about |g| 2^-23 of it, for a product that is kept in 8 bits: 64 of them a
+// thread and unit took 11000 cycles with expf and a division, while the MMAs waited.
+__device__ __forceinline__ float silu_fast(float g) { return __fdividef(g, 1.f + __expf(-g)); }
 
 // kCount values of this lane's row to columns [col, col + kCount) of y, those below N;
 // `row` < 0: none.  A lane's own stores would be 32 rows' sectors an instruction (128 x
 // 256 results a CTA: 4000 cycles), so the warp turns blocks of 32 rows x 128 bytes in
 // shared memory and stores whole lines of them, 16 bytes a lane.  Rows that do not
 // start on 16-byte boundaries are turned by single values, 32 columns at a time.
+// Output rows of a warp's 32: of lane l, `row`; where they are first + l * step for l <
+// live, step is not 0.
+struct Rows {
+  long long row, first;
+  int step, live;
+};
 template <typename T, int kCount>
-__device__ __forceinline__ void store_columns(T* y, const float (&v)[kCount], long long row, int col, int N, bool aligned,
+__device__ __forceinline__ void store_columns(T* y, const float (&v)[kCount], const Rows& rows, int col, int N, bool aligned,
                                               uint8_t* turn, int lane) {
+  const long long row = rows.row;
   constexpr int kVec = 16 / static_cast<int>(sizeof(T)), kLine = 8 * kVec;   // values of 16 and of 128 bytes
   constexpr int kBlock = kLine < kCount ? kLine : kCount, kParts = kBlock / kVec;
   if (aligned) {
@@ -353,13 +391,25 @@ __device__ __forceinline__ void store_columns(T* y, const float (&v)[kCount], lo
     return;
   }
   float* const floats = reinterpret_cast<float*>(turn);
+  constexpr int kWide = kCount < 32 ? kCount : 32;
 #pragma unroll
-  for (int b = 0; b < kCount; b += 32) {
+  for (int b = 0; b < kCount; b += kWide) {
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 32; ++i) floats[lane * kPitch + i] = v[b + i];
+    for (int i = 0; i < kWide; ++i) floats[lane * kPitch + i] = v[b + i];
     __syncwarp();
-    const bool in = col + b + lane < N;
+    const bool in = col + b + lane < N && lane < kWide;
+    if (rows.step) {
+      // an addition a row, where the lookup of each took 12 instructions (3001 rows 2048 ->
+      // 4099: 59 us with it)
+      T* to = y + rows.first * N + col + b + lane;
+      const long long next = static_cast<long long>(rows.step) * N;
+#pragma unroll 8
+      for (int r = 0; r < rows.live; ++r, to += next) {
+        if (in) *to = narrow<T>(floats[r * kPitch + lane]);
+      }
+      continue;
+    }
 #pragma unroll 4
     for (int r = 0; r < 32; ++r) {
       const long long to = __shfl_sync(0xffffffffu, row, r);
@@ -368,7 +418,7 @@ __device__ __forceinline__ void store_columns(T* y, const float (&v)[kCount], lo
   }
 }
 template <int kCount>
-__device__ __forceinline__ void store_typed(void* y, int type, const float (&v)[kCount], long long row, int col, int N,
+__device__ __forceinline__ void store_typed(void* y, int type, const float (&v)[kCount], const Rows& row, int col, int N,
                                             bool aligned, uint8_t* turn, int lane) {
   if (type == TQ_FP32)
     store_columns(static_cast<float*>(y), v, row, col, N, aligned, turn, lane);
@@ -378,7 +428,7 @@ __device__ __forceinline__ void store_typed(void* y, int type, const float (&v)[
     store_columns(static_cast<__half*>(y), v, row, col, N, aligned, turn, lane);
 }
 
-template <bool k8, bool kPair, int kCols, bool kAMn, bool kBMn, int kEpi>
+template <bool k8, int kCtas, int kCols, bool kAMn, bool kBMn, int kEpi>
 __global__ void __launch_bounds__(kThreads, 1)
 tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Params p) {
   static_assert(kCols == 128 || kCols == 64 || kCols == 32, "");
@@ -387,6 +437,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
   static_assert(kEpi == kStore || kCols >= 64, "");
   static_assert(k8 || kCols >= 64, "16-bit sums are read 64 columns at a time");
   static_assert(!kBMn || kCols >= 64, "");
+  constexpr bool kPair = kCtas > 1, kQuad = kCtas == 4;
   constexpr bool kGated = kEpi != kStore, kSplitRegisters = splits_registers(k8, kCols);
   constexpr int kN = 2 * kCols;                                   // the MMA's N
   constexpr int kBBytes = (kPair ? kCols : kN) * kStepBytes;      // of B per CTA and step
@@ -400,8 +451,10 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const gbase = smem_raw + (base - raw);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  const int rank = kPair ? static_cast<int>(cluster_rank()) : 0;
+  const int cta = kPair ? static_cast<int>(cluster_rank()) : 0;
+  const int rank = cta & 1, pair_of_ctas = cta >> 1;   // rank in its pair
   const bool first = rank == 0;   // of the pair: the barriers that the MMA waits for are its
+  const uint32_t own_pair = 3u << (2 * pair_of_ctas);
 
   const uint32_t bar_full = base + p.off_bar;
   const uint32_t bar_empty = bar_full + 8 * kMaxStages;
@@ -414,7 +467,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(bar_full + 8 * s, p.gather ? 3 : 2);
-      mbar_init(bar_empty + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, kQuad ? 2 : 1);   // the MMAs of every pair that a copy may write to
     }
     for (int a = 0; a < p.accs; ++a) {
       mbar_init(bar_accfull + 8 * a, 1);
@@ -429,15 +482,16 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
   if (warp == kWarpA) alloc_columns<kPair>(smem_u32(tmem_holder), static_cast<uint32_t>(p.tmem_cols));
   tc_fence_before();
   __syncthreads();
-  if (kPair) cluster_sync();   // both CTAs' barriers are ready
+  if (kPair) cluster_sync();   // every CTA's barriers are ready
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
   pdl_wait();
 
   const int num_tiles = p.tiles ? static_cast<int>(min(static_cast<long long>(*p.num_tiles), p.cap))
                                 : static_cast<int>(p.cap);
-  const long long units = static_cast<long long>(num_tiles) * p.col_blocks * p.splits;
-  const int unit0 = kPair ? blockIdx.x / 2 : blockIdx.x, unit_step = kPair ? gridDim.x / 2 : gridDim.x;
+  const int col_units = kQuad ? (p.col_blocks + 1) / 2 : p.col_blocks;
+  const long long units = static_cast<long long>(num_tiles) * col_units * p.splits;
+  const int unit0 = blockIdx.x / kCtas, unit_step = gridDim.x / kCtas;
   const int stages = p.stages, accs = p.accs;
   int* const err = p.err;
 
@@ -453,13 +507,14 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     const bool is_b = warp == kWarpB;
     const int lead = is_b ? 3 : warp == kWarpA ? 0 : 5, share = is_b ? 2 : 3;
     int* const list = reinterpret_cast<int*>(gbase + p.off_list);
-    const uint32_t full0 = kPair ? of_cta(bar_full, 0) : bar_full;
+    const uint32_t full0 = kPair ? of_cta(bar_full, cta & ~1) : bar_full;
+    const uint16_t both_pairs = static_cast<uint16_t>(5u << rank);   // the CTAs that hold the same rows of A
     const bool leader = elect_one();
     Ring ring;
     long long issued = 0;
     bool ok = true, ready = false;
     for (long long u = unit0; ok && u < units; u += unit_step) {
-      const Unit t = unit_at(p, u, num_tiles);
+      const Unit t = unit_at<kQuad>(p, u, num_tiles, col_units, pair_of_ctas);
       if (!t.ok) {
         if (is_b && first && leader) record_error(err, TQ_ERR_INVALID_ARG, kWhereTileLoad);
         continue;
@@ -469,8 +524,14 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
       const int copies = gathered(t.rows, rank);
       uint32_t bytes = static_cast<uint32_t>(is_b ? kBBytes : 0) * (kPair ? 2 : 1);
       if (p.gather) {
-        bytes += 4 * kStepBytes * (shared_copies(gathered(t.rows, 0), lead, share) +
-                                   (kPair ? shared_copies(gathered(t.rows, 1), lead, share) : 0));
+#pragma unroll
+        for (int r = 0; r < (kPair ? 2 : 1); ++r) {
+          if (kQuad)
+            bytes += 4 * kStepBytes * (shared_copies(part_of(gathered(t.rows, r), 0), lead, share) +
+                                       shared_copies(part_of(gathered(t.rows, r), 1), lead, share));
+          else
+            bytes += 4 * kStepBytes * shared_copies(gathered(t.rows, r), lead, share);
+        }
         __syncwarp();
         for (int i = lane; i < 16 * share; i += 32) {
           const int in = 32 * (i / (4 * share)) + 4 * lead + i % (4 * share);   // row of this CTA
@@ -505,14 +566,22 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
           }
           if (p.gather) {
 #pragma unroll
-            for (int j = 0; j < kRows / 4; j += 8) {
+            for (int j = 0; j < kRows / (kQuad ? 8 : 4); j += 8) {
 #pragma unroll
               for (int i = 0; i < 3; ++i) {
-                const int c = j + lead + i;
-                if (i < share && c < copies)
-                  load_rows<kPair>(dst + 4 * c * kStepBytes, &tm_a, at, *reinterpret_cast<const int4*>(list + 4 * c), full);
+                const int c = (kQuad ? pair_of_ctas * (kRows / 8) : 0) + j + lead + i;
+                if (i < share && c < copies) {
+                  const int4 rows = *reinterpret_cast<const int4*>(list + 4 * c);
+                  if constexpr (kQuad)
+                    load_rows_to(dst + 4 * c * kStepBytes, &tm_a, at, rows, full, both_pairs);
+                  else
+                    load_rows<kPair>(dst + 4 * c * kStepBytes, &tm_a, at, rows, full);
+                }
               }
             }
+          } else if (kQuad && !is_b) {
+            const int half = row0 + 64 * pair_of_ctas;
+            load_box_to(dst + 8192 * pair_of_ctas, &tm_a, kAMn ? half : at, kAMn ? at : half, full, both_pairs);
           } else if (!is_b) {
 #pragma unroll
             for (int i = 0; i < kABoxes; ++i)
@@ -527,9 +596,8 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     }
     if (leader) {
       // Before the CTA exits, every copy issued has landed (of a pair: in both
-      // CTAs, counted on the first's barriers) and, in the second CTA, every
-      // arrival that the MMAs owe its barriers.
-      const uint32_t bars = first ? bar_full : bar_empty;
+      // CTAs, counted on the first's barriers) and every arrival that the MMAs owe its
+      // barriers; the empty ones, whose MMAs waited for the copies, tell both.
       const long long pending = min(issued, static_cast<long long>(stages));
       for (long long i = 1; i <= pending; ++i) {
         int st = ring.at - static_cast<int>(i);
@@ -539,7 +607,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
           ph ^= 1u;
         }
         const uint64_t t0 = globaltimer();
-        while (!mbar_try_wait(bars + 8 * st, ph)) {
+        while (!mbar_try_wait(bar_empty + 8 * st, ph)) {
           if (globaltimer() - t0 > kWaitTimeoutNs) {
             record_error(err, TQ_ERR_DEVICE_TIMEOUT, kWhereTileTeardown);
             break;
@@ -558,7 +626,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     const bool leader = elect_one();
     Ring acc;
     for (long long u = unit0; u < units; u += unit_step) {
-      const Unit t = unit_at(p, u, num_tiles);
+      const Unit t = unit_at<kQuad>(p, u, num_tiles, col_units, pair_of_ctas);
       if (!t.ok) continue;
       for (int k = t.k0; k < t.k1; ++k) {
         if (k8 || k == t.k0) {
@@ -584,8 +652,8 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
           for (int i = 0; i < 4; ++i)
             mma<k8, kPair>(d, a + i * (kAMn ? 128 : 2), b + i * (kBMn ? 128 : 2), idesc,
                            (i != 0 || (!k8 && k != t.k0)) ? 1u : 0u);
-          commit<kPair>(this_bar + 8 * kMaxStages);   // the stage's empty barrier
-          if (last) commit<kPair>(bar_accfull + 8 * acc.at);
+          commit<kPair>(this_bar + 8 * kMaxStages, kQuad ? 15u : 3u);   // the stage's empty barrier
+          if (last) commit<kPair>(bar_accfull + 8 * acc.at, own_pair);
         }
         if (last) acc.advance(accs);
         if (*abort_flag) break;
@@ -619,33 +687,44 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     int parity = 0;
     Ring acc;
     for (long long u = unit0; u < units; u += unit_step) {
-      const Unit t = unit_at(p, u, num_tiles);
+      const Unit t = unit_at<kQuad>(p, u, num_tiles, col_units, pair_of_ctas);
       if (!t.ok) continue;
       const int in_tile = rank * kRows + 32 * q + lane;
       const int slot = t.slot0 + min(in_tile, t.rows - 1);
       int pair = slot;
       if (p.gather || p.scatter) pair = pair_of(p, slot, kWhereTileEpilogue);
       const bool live = in_tile < t.rows && pair >= 0;
-      const long long out_row = !live ? -1 : p.scatter ? pair : slot;
+      const int first_row = t.slot0 + rank * kRows + 32 * q;
+      const Rows out_row{!live ? -1 : p.scatter ? pair : slot, first_row, p.scatter ? 0 : 1,
+                         max(0, min(32, t.slot0 + t.rows - first_row))};
       bool ok = true;
       if constexpr (k8) {
         const int a_row = p.gather ? max(pair, 0) / p.top_k : slot;
         const float* sa = p.a_scales + static_cast<long long>(a_row) * p.steps + t.k0;
         // the blocks of this thread's columns; past the matrix the last one (nothing of it is stored)
         const int col = t.cb * (kGated ? kCols : kN);
-        const int b0 = min((kGated ? col : col + half * kCols) / 128, p.b_blocks - 1);
+        const int last_block = (kGated ? p.N / 128 : p.b_blocks) - 1;
+        const int b0 = min((kGated ? col : col + half * kCols) / 128, last_block);
         const float* sb = p.b_scales + (static_cast<long long>(t.e) * p.b_blocks + b0) * p.steps + t.k0;
         const float* sc = kGated ? sb + static_cast<long long>(p.N / 128) * p.steps : sb;
         float2 sum[kCols / 2];
 #pragma unroll
         for (int i = 0; i < kCols / 2; ++i) sum[i] = make_float2(0.f, 0.f);
+        // The scales are read two steps ahead: a read that misses L1, which has little room
+        // beside the stages, takes longer than a step.
         float na = __ldg(sa), nb = __ldg(sb), nc = kGated ? __ldg(sc) : 0.f;
+        int ahead = t.k1 - t.k0 > 1 ? 1 : 0;
+        float ma = __ldg(sa + ahead), mb = __ldg(sb + ahead), mc = kGated ? __ldg(sc + ahead) : 0.f;
         for (int k = t.k0; k < t.k1; ++k) {
           const float f0 = na * nb, f1 = kGated ? na * nc : f0;
-          if (k + 1 < t.k1) {
-            na = __ldg(++sa);
-            nb = __ldg(++sb);
-            if (kGated) nc = __ldg(++sc);
+          na = ma;
+          nb = mb;
+          nc = mc;
+          if (k + 2 < t.k1) {
+            ++ahead;
+            ma = __ldg(sa + ahead);
+            mb = __ldg(sb + ahead);
+            if (kGated) mc = __ldg(sc + ahead);
           }
           ok = mbar_wait_short(bar_accfull + 8 * acc.at, acc.phase, abort_flag, err, kWhereTileEpilogue);
           if (!ok) break;
@@ -665,7 +744,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                 __syncwarp();
                 if (lane == 0) {
                   if (kPair && !first)
-                    cluster_arrive(of_cta(bar_accempty + 8 * acc.at, 0));
+                    cluster_arrive(of_cta(bar_accempty + 8 * acc.at, cta & ~1));
                   else
                     mbar_arrive(bar_accempty + 8 * acc.at);
                 }
@@ -685,8 +764,8 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
           float h[64], top = 0.f;
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            h[2 * i] = silu(sum[i].x) * sum[32 + i].x;
-            h[2 * i + 1] = silu(sum[i].y) * sum[32 + i].y;
+            h[2 * i] = silu_fast(sum[i].x) * sum[32 + i].x;
+            h[2 * i + 1] = silu_fast(sum[i].y) * sum[32 + i].y;
           }
           top = fp8_top<64>(h);
           float* const mine = tops + (2 * parity + half) * kRows + 32 * q + lane;
@@ -694,7 +773,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
           asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
           top = fmaxf(top, tops[(2 * parity + (half ^ 1)) * kRows + 32 * q + lane]);
           parity ^= 1;
-          if (live && ok) {
+          if (live && ok && col < p.N) {
             const Fp8Scale s(top);
             uint8_t* const out = p.codes + static_cast<long long>(slot) * p.N + col + 64 * half;
 #pragma unroll
@@ -735,12 +814,14 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
             if (p.gate_up) {
               // rows of 2 N values: the gate's below N, then the up projection's
               float* const gu = p.gate_up;
+              const Rows gate_row{out_row.row < 0 ? -1 : 2 * out_row.row, 2 * out_row.first, 2, out_row.live};
+              const Rows up_row{out_row.row < 0 ? -1 : 2 * out_row.row + 1, 2 * out_row.first + 1, 2, out_row.live};
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(g[i]);
-              store_columns(gu, v, out_row < 0 ? -1 : 2 * out_row, at, p.N, p.N % 4 == 0, turn, lane);
+              store_columns(gu, v, gate_row, at, p.N, p.N % 4 == 0, turn, lane);
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(up[i]);
-              store_columns(gu, v, out_row < 0 ? -1 : 2 * out_row + 1, at, p.N, p.N % 4 == 0, turn, lane);
+              store_columns(gu, v, up_row, at, p.N, p.N % 4 == 0, turn, lane);
             }
             if (p.y) {
 #pragma unroll
@@ -767,7 +848,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
         __syncwarp();
         if (lane == 0) {
           if (kPair && !first)
-            cluster_arrive(of_cta(bar_accempty + 8 * acc.at, 0));
+            cluster_arrive(of_cta(bar_accempty + 8 * acc.at, cta & ~1));
           else
             mbar_arrive(bar_accempty + 8 * acc.at);
         }
@@ -779,18 +860,23 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
   pdl_trigger();
   tc_fence_before();
   __syncthreads();
-  if (kPair) cluster_sync();   // neither CTA's memory is needed by the other any more
+  if (kPair) cluster_sync();   // no CTA's memory is needed by another any more
   if (warp == kWarpA) {
     tc_fence_after();
     free_columns<kPair>(tmem, static_cast<uint32_t>(p.tmem_cols));
   }
 }
 
+// Clusters of four CTAs that the device holds at once: fewer than a quarter of its SMs,
+// as they do not cross its partitions (36 of GB300's 152 / 4 = 38).
+int quads();
+
 // Launches one variant; `units` bounds the units of a launch whose tile map is on the
 // device.  Stages, accumulators and shared memory are filled in here.
-template <bool k8, bool kPair, int kCols, bool kAMn, bool kBMn, int kEpi>
+template <bool k8, int kCtas, int kCols, bool kAMn, bool kBMn, int kEpi>
 int launch(Params p, const CUtensorMap& a, const CUtensorMap& b, long long units, cudaStream_t s) {
-  auto kernel = tile_gemm_kernel<k8, kPair, kCols, kAMn, kBMn, kEpi>;
+  constexpr bool kPair = kCtas > 1;
+  auto kernel = tile_gemm_kernel<k8, kCtas, kCols, kAMn, kBMn, kEpi>;
   static std::atomic<uint64_t> allowed{0};   // bit d: device d
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) {
@@ -818,21 +904,21 @@ int launch(Params p, const CUtensorMap& a, const CUtensorMap& b, long long units
   p.off_bar = static_cast<uint32_t>(p.stages * kStageBytes);
   p.off_list = p.off_bar + kBarBytes;
   p.off_top = p.off_turn = p.off_list + kListBytes;
-  const int width = kPair ? 2 : 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(width * static_cast<int>(std::max<long long>(1, std::min<long long>(units, sm_count() / width))));
   cfg.blockDim = dim3(kThreads);
   // one CTA (and one tensor-memory allocation) per SM
   cfg.dynamicSmemBytes = std::max(1024 + p.stages * kStageBytes + kFixed, 120 * 1024);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = width;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCtas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = kPair ? 2 : 1;
+  cfg.numAttrs = 2;
+  const long long clusters = kCtas == 4 ? quads() : sm_count() / kCtas;
+  cfg.gridDim = dim3(kCtas * static_cast<int>(std::max<long long>(1, std::min<long long>(units, clusters))));
   if (cudaLaunchKernelEx(&cfg, kernel, a, b, p) != cudaSuccess) {
     cudaGetLastError();
     return TQ_ERR_LAUNCH;
