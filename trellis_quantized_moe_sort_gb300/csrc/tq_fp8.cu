@@ -55,7 +55,7 @@ LinearPlan plan_linear(void* base, int64_t n, int K, int N) {
   l.few = n <= kFewRowsMost;
   l.bytes = kNoWorkspace;
   if (l.few) return l;
-  l.tile = choose_tile(static_cast<double>(n), 1.0, blocks_of(K), N, false, false, false, true);
+  l.tile = choose_tile(static_cast<double>(n), 1.0, blocks_of(K), N, false, TileRows::kOne, false, true);
   if (l.tile.splits > 1) {
     Carver c{static_cast<uint8_t*>(base)};
     l.part = c.take<float>(static_cast<size_t>(l.tile.splits) * n * N);
@@ -90,10 +90,10 @@ double typical_rows(int64_t n, int top_k, int E) {
   const double mean = n ? tq_pairs_per_woken_expert(n, top_k, E) : 1.0;
   return mean + 2.0 * std::sqrt(mean);
 }
-TileChoice moe_tile(int64_t n, int top_k, int E, int steps, int N, bool gated, bool gather) {
+TileChoice moe_tile(int64_t n, int top_k, int E, int steps, int N, bool gated, TileRows kind) {
   if (n == 0) return {128, false, 128, 1};
   const double mean = tq_pairs_per_woken_expert(n, top_k, E);
-  return choose_tile(typical_rows(n, top_k, E), n * top_k / mean, steps, N, gated, gather, !gated, !gated);
+  return choose_tile(typical_rows(n, top_k, E), n * top_k / mean, steps, N, gated, kind, !gated, !gated);
 }
 
 struct Routed {
@@ -124,7 +124,7 @@ struct ProductPlan {
 };
 ProductPlan plan_moe(void* base, int64_t n, int top_k, int E, int K, int N) {
   ProductPlan p;
-  p.tile = moe_tile(n, top_k, E, blocks_of(K), N, false, true);
+  p.tile = moe_tile(n, top_k, E, blocks_of(K), N, false, TileRows::kGathered);
   p.m = plan_arm(n, top_k, E, p.tile);
   if (p.m.arm != kTiles) p.tile.splits = 1;
   Carver c{static_cast<uint8_t*>(base)};
@@ -146,14 +146,10 @@ struct MlpPlan {
 MlpPlan plan_mlp(void* base, int64_t n, int top_k, int E, int H, int I) {
   MlpPlan p{};
   // one tile map for both products, by the gate and up projections'
-  p.gu = moe_tile(n, top_k, E, blocks_of(H), I, true, true);
+  p.gu = moe_tile(n, top_k, E, blocks_of(H), I, true, TileRows::kGathered);
   p.m = plan_arm(n, top_k, E, p.gu);
-  p.down = moe_tile(n, top_k, E, blocks_of(I), H, false, false);
+  p.down = moe_tile(n, top_k, E, blocks_of(I), H, false, TileRows::kSlots);
   if (p.m.arm != kTiles) p.down.splits = 1;
-  if (p.down.tile_m != p.m.tile_m) {
-    p.down.tile_m = p.m.tile_m;
-    p.down.cols = 128;
-  }
   Carver c{static_cast<uint8_t*>(base)};
   p.routed = carve_routed(c, p.m, E);
   p.h32 = p.m.arm == kTiles ? nullptr : c.take<float>(static_cast<size_t>(p.m.P) * I);
@@ -201,7 +197,7 @@ int sorted_product(const MoePlan& m, const Routed& r, Operand x, int64_t x_rows,
                    int K, int N, TileChoice tile, float* part, int* err, cudaStream_t s) {
   if (m.arm == kTiles) {
     Fp8Gemm g{x.codes, x.scales, x_rows, w.codes, w.scales, r.sorted_pairs, r.tiles, r.num_tiles, m.cap, m.P, top_k, E,
-              K, N, gather, true, false, m.tile_m, tile.quad, tile.cols, tile.splits, part, TQ_FP32, nullptr, nullptr, err};
+              K, N, gather, true, false, m.tile_m, tile.shared, tile.cols, tile.splits, part, TQ_FP32, nullptr, nullptr, err};
     return launch_fp8_gemm(g, s);
   }
   FewRows f = few_rows(x, w, m.P, top_k, E, K, N, false, part, TQ_FP32, err);
@@ -283,7 +279,7 @@ int tq_fp8_linear(const uint8_t* x, const float* x_scales, const uint8_t* w, con
     return launch_few_rows(few_rows({x, x_scales}, {w, w_scales}, n, 1, 1, K, N, false, y, y_type, err), kFewRowsFp8, false,
                            n <= 8 ? 8 : 16, 1, s);
   Fp8Gemm g{x, x_scales, n, w, w_scales, nullptr, nullptr, nullptr, (n + l.tile.tile_m - 1) / l.tile.tile_m, n, 1, 1, K, N,
-            false, false, false, l.tile.tile_m, l.tile.quad, l.tile.cols, l.tile.splits, splits ? l.part : y,
+            false, false, false, l.tile.tile_m, l.tile.shared, l.tile.cols, l.tile.splits, splits ? l.part : y,
             splits ? TQ_FP32 : y_type, nullptr, nullptr, err};
   rc = launch_fp8_gemm(g, s);
   if (rc != TQ_OK || !splits) return rc;
@@ -350,7 +346,7 @@ int tq_fp8_moe_mlp_forward(const uint8_t* x, const float* x_scales, const uint8_
   if (rc != TQ_OK) return rc;
   if (m.arm == kTiles) {
     Fp8Gemm g{x, x_scales, n, w_gu, gu_scales, r.sorted_pairs, r.tiles, r.num_tiles, m.cap, m.P, top_k, E, H, I, true,
-              false, true, m.tile_m, p.gu.quad, 128, 1, nullptr, TQ_FP32, p.h, p.h_scales, err};
+              false, true, m.tile_m, p.gu.shared, 128, 1, nullptr, TQ_FP32, p.h, p.h_scales, err};
     rc = launch_fp8_gemm(g, s);
   } else {
     FewRows f = few_rows({x, x_scales}, {w_gu, gu_scales}, m.P, top_k, E, H, I, true, p.h32, TQ_FP32, err);

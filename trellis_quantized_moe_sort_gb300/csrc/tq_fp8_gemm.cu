@@ -4,45 +4,10 @@
 #include "tq_tile_gemm.cuh"
 
 namespace tq {
-namespace {
-
-__global__ void __launch_bounds__(tile::kThreads, 1) quad_probe_kernel() {}
-
-}  // namespace
-
-int tile::quads() {
-  static std::atomic<int> kept[64];
-  int device = 0;
-  if (cudaGetDevice(&device) != cudaSuccess) {
-    cudaGetLastError();
-    return 1;
-  }
-  std::atomic<int>& known = kept[device & 63];
-  int n = known.load();
-  if (n > 0) return n;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(4);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemLimit;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 4;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaFuncSetAttribute(quad_probe_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, quad_probe_kernel, &cfg) != cudaSuccess || n < 1) {
-    cudaGetLastError();
-    n = 1;
-  }
-  known.store(n);
-  return n;
-}
-
 int launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
   using namespace tile;
   Params p{};
-  const bool pair = g.tile_m > kRows, quad = pair && g.quad;
+  const bool pair = g.tile_m > kRows, shared = !pair && g.shared;
   p.tiles = g.tiles;
   p.num_tiles = g.num_tiles;
   p.sorted_pairs = g.sorted_pairs;
@@ -71,21 +36,20 @@ int launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
   p.err = g.err;
   CUtensorMap a, b;
   const int64_t w_rows = static_cast<int64_t>(g.E) * (g.gated ? 2 : 1) * g.N;
-  if (!encode(&a, g.x, 1, g.K, g.x_rows, g.K, g.gather ? 1 : quad ? kRows / 2 : kRows) ||
+  if (!encode(&a, g.x, 1, g.K, g.x_rows, g.K, g.gather ? 1 : shared ? kRows / 2 : kRows) ||
       !encode(&b, g.w, 1, g.K, w_rows, g.K, g.cols))
     return TQ_ERR_INVALID_ARG;
-  const long long units = g.cap * (quad ? (p.col_blocks + 1) / 2 : p.col_blocks) * g.splits;
+  const long long units = g.cap * (shared ? (p.col_blocks + 1) / 2 : p.col_blocks) * g.splits;
   int st;
   if (g.gated)
-    st = quad   ? launch<true, 4, 128, false, false, kGated8>(p, a, b, units, s)
-         : pair ? launch<true, 2, 128, false, false, kGated8>(p, a, b, units, s)
-                : launch<true, 1, 128, false, false, kGated8>(p, a, b, units, s);
+    st = shared ? launch<true, kSharing, 128, false, false, kGated8>(p, a, b, units, s)
+                : launch<true, kAlone, 128, false, false, kGated8>(p, a, b, units, s);
   else
-    st = quad              ? launch<true, 4, 128, false, false, kStore>(p, a, b, units, s)
-         : pair            ? launch<true, 2, 128, false, false, kStore>(p, a, b, units, s)
-         : g.cols == 128   ? launch<true, 1, 128, false, false, kStore>(p, a, b, units, s)
-         : g.cols == 64    ? launch<true, 1, 64, false, false, kStore>(p, a, b, units, s)
-                           : launch<true, 1, 32, false, false, kStore>(p, a, b, units, s);
+    st = pair            ? launch<true, kPaired, 128, false, false, kStore>(p, a, b, units, s)
+         : shared        ? launch<true, kSharing, 128, false, false, kStore>(p, a, b, units, s)
+         : g.cols == 128 ? launch<true, kAlone, 128, false, false, kStore>(p, a, b, units, s)
+         : g.cols == 64  ? launch<true, kAlone, 64, false, false, kStore>(p, a, b, units, s)
+                         : launch<true, kAlone, 32, false, false, kStore>(p, a, b, units, s);
   if (st == TQ_OK) count_launch(kCntFp8Gemm);
   return st;
 }

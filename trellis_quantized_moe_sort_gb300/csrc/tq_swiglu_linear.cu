@@ -79,17 +79,17 @@ int forward(const void* x, int type, int64_t x_stride, const void* w, int64_t n,
     f.err = err;
     return launch_few_rows(f, type, true, n <= 8 ? 8 : 16, 1, s);
   }
-  const TileChoice t = choose_tile(static_cast<double>(n), 1.0, (H + 63) / 64, I, true, false, false, false);
+  const TileChoice t = choose_tile(static_cast<double>(n), 1.0, (H + 63) / 64, I, true, TileRows::kOne, false, false);
   GemmF16 g{type, x, x_stride, w, H, n, I, H, false, false, true, t.tile_m, t.cols, 1, h, type, gate_up, err};
   return launch_gemm_f16(g, s);
 }
 
 // The two products of the gradient.
 TileChoice tile_x(int64_t n, int H, int I) {
-  return choose_tile(static_cast<double>(n), 1.0, static_cast<int>((2ll * I + 63) / 64), H, false, false, false, true);
+  return choose_tile(static_cast<double>(n), 1.0, static_cast<int>((2ll * I + 63) / 64), H, false, TileRows::kOne, false, true);
 }
 TileChoice tile_w(int64_t n, int H, int I) {
-  return choose_tile(2.0 * I, 1.0, static_cast<int>((n + 63) / 64), H, false, false, false, true);
+  return choose_tile(2.0 * I, 1.0, static_cast<int>((n + 63) / 64), H, false, TileRows::kOne, false, true);
 }
 TileChoice at_least_64(TileChoice t) {   // operands across K come in boxes of 64 columns
   t.cols = std::max(t.cols, 64);

@@ -21,7 +21,9 @@
 // reads), as boxes of 64 columns x 64 rows of K.
 //
 // A pair shares one MMA of 256 rows and halves B: 32 KB a CTA and step for 128 x 256
-// results, in place of 48.
+// results, in place of 48.  Experts' rows fill tiles of 128 better than of 256, and the
+// copies of their gathered rows, four at a time, cost 50 cycles each: there two CTAs
+// take neighbouring columns of 128 rows and copy half of them each, to both.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -55,6 +57,11 @@ constexpr int kTopBytes = 2 * 2 * kRows * 4;  // two buffers of both column halv
 // up registers to 256, 128 x 40 + 256 x 232 = 384 x 168, which the launch has to have.
 constexpr bool splits_registers(bool k8, int cols) { return k8 && cols == 128; }
 constexpr int kLaunchRegisters = 168;
+
+// How CTAs work together: each by itself; as a pair on one MMA of 256 rows; or two by
+// two on neighbouring column blocks of the same 128 rows, of which each copies half to
+// both.
+enum Group { kAlone = 0, kPaired = 1, kSharing = 2 };
 
 enum Epilogue {
   kStore = 0,     // y[row][column], or partial sums, one fp32 matrix per split
@@ -184,33 +191,37 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* m, in
     tma_gather4_2d(dst, m, x, r.x, r.y, r.z, r.w, bar);
 }
 
-// The same to the CTAs of a mask, at the same place in each; the bytes count on the
-// barriers of the first CTAs of their pairs.
-__device__ __forceinline__ void load_box_to(uint32_t dst, const CUtensorMap* m, int32_t x, int32_t y, uint32_t bar,
-                                            uint16_t mask) {
+// The same to both CTAs of a cluster, at the same place in each; the bytes count on the
+// barrier at the same place in each.
+__device__ __forceinline__ void load_box_to_both(uint32_t dst, const CUtensorMap* m, int32_t x, int32_t y, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
       " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar), "h"(mask)
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar), "h"(static_cast<uint16_t>(3))
       : "memory");
 }
-__device__ __forceinline__ void load_rows_to(uint32_t dst, const CUtensorMap* m, int32_t x, int4 r, uint32_t bar,
-                                             uint16_t mask) {
+__device__ __forceinline__ void load_rows_to_both(uint32_t dst, const CUtensorMap* m, int32_t x, int4 r, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      ".multicast::cluster [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar), "h"(mask)
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.multicast::cluster"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar),
+      "h"(static_cast<uint16_t>(3))
       : "memory");
 }
 
-// Arrives on the barrier (of each CTA of the mask) once every MMA issued so far has
-// completed.
-template <bool kPair>
-__device__ __forceinline__ void commit(uint32_t bar, uint32_t mask) {
+// Arrives on the barrier (of both CTAs of a pair, or of two that share their rows of A)
+// once every MMA issued so far has completed.
+template <bool kPair, bool kShared>
+__device__ __forceinline__ void commit(uint32_t bar) {
   if constexpr (kPair)
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(static_cast<uint16_t>(mask))
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else if constexpr (kShared)
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
         : "memory");
   else
     mma_commit(bar);
@@ -295,15 +306,15 @@ struct Unit {
   bool ok;
 };
 
-// Unit u of a cluster; two pairs of CTAs take neighbouring column blocks of it (the
-// second of them past the matrix where their number is odd: its loads read what follows
-// and its results do not exist).
-template <bool kQuad>
-__device__ __forceinline__ Unit unit_at(const Params& p, long long u, int num_tiles, int col_units, int pair) {
+// Unit u of a cluster; two CTAs that share the rows of A take neighbouring column blocks
+// of it (the second of them past the matrix where their number is odd: its loads read
+// what follows and its results do not exist).
+template <int kShare>
+__device__ __forceinline__ Unit unit_at(const Params& p, long long u, int num_tiles, int col_units, int sharer) {
   Unit t;
   t.cb = static_cast<int>(u % col_units);
   u /= col_units;
-  if (kQuad) t.cb = 2 * t.cb + pair;
+  if (kShare == 2) t.cb = 2 * t.cb + sharer;
   const int tile = static_cast<int>(u % num_tiles);
   t.split = static_cast<int>(u / num_tiles);
   t.k0 = static_cast<int>(static_cast<long long>(p.steps) * t.split / p.splits);
@@ -335,8 +346,10 @@ __device__ __forceinline__ int pair_of(const Params& p, int slot, int where) {
 __device__ __forceinline__ int gathered(int rows, int rank) {
   return (max(0, min(kRows, rows - rank * kRows)) + 3) / 4;
 }
-// Of those, the part that one of two pairs of CTAs gathers for both.
-__device__ __forceinline__ int part_of(int copies, int pair) { return max(0, min(kRows / 8, copies - pair * (kRows / 8))); }
+// Of those, the part that one of two CTAs gathers for both.
+__device__ __forceinline__ int part_of(int copies, int sharer) {
+  return max(0, min(kRows / 8, copies - sharer * (kRows / 8)));
+}
 __device__ __forceinline__ int shared_copies(int n, int lead, int share) {
   return n / 8 * share + max(0, min(share, n % 8 - lead));
 }
@@ -428,7 +441,7 @@ __device__ __forceinline__ void store_typed(void* y, int type, const float (&v)[
     store_columns(static_cast<__half*>(y), v, row, col, N, aligned, turn, lane);
 }
 
-template <bool k8, int kCtas, int kCols, bool kAMn, bool kBMn, int kEpi>
+template <bool k8, Group kGroup, int kCols, bool kAMn, bool kBMn, int kEpi>
 __global__ void __launch_bounds__(kThreads, 1)
 tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Params p) {
   static_assert(kCols == 128 || kCols == 64 || kCols == 32, "");
@@ -437,7 +450,9 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
   static_assert(kEpi == kStore || kCols >= 64, "");
   static_assert(k8 || kCols >= 64, "16-bit sums are read 64 columns at a time");
   static_assert(!kBMn || kCols >= 64, "");
-  constexpr bool kPair = kCtas > 1, kQuad = kCtas == 4;
+  static_assert(kGroup != kSharing || k8, "");
+  constexpr bool kPair = kGroup == kPaired, kShared = kGroup == kSharing;
+  constexpr int kShare = kShared ? 2 : 1;
   constexpr bool kGated = kEpi != kStore, kSplitRegisters = splits_registers(k8, kCols);
   constexpr int kN = 2 * kCols;                                   // the MMA's N
   constexpr int kBBytes = (kPair ? kCols : kN) * kStepBytes;      // of B per CTA and step
@@ -451,10 +466,9 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const gbase = smem_raw + (base - raw);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  const int cta = kPair ? static_cast<int>(cluster_rank()) : 0;
-  const int rank = cta & 1, pair_of_ctas = cta >> 1;   // rank in its pair
-  const bool first = rank == 0;   // of the pair: the barriers that the MMA waits for are its
-  const uint32_t own_pair = 3u << (2 * pair_of_ctas);
+  const int cta = kGroup != kAlone ? static_cast<int>(cluster_rank()) : 0;
+  const int rank = kPair ? cta : 0, sharer = kShared ? cta : 0;
+  const bool first = rank == 0;   // of a pair: the barriers that the MMA waits for are its
 
   const uint32_t bar_full = base + p.off_bar;
   const uint32_t bar_empty = bar_full + 8 * kMaxStages;
@@ -467,7 +481,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(bar_full + 8 * s, p.gather ? 3 : 2);
-      mbar_init(bar_empty + 8 * s, kQuad ? 2 : 1);   // the MMAs of every pair that a copy may write to
+      mbar_init(bar_empty + 8 * s, kShare);   // the MMAs of every CTA that a copy writes to
     }
     for (int a = 0; a < p.accs; ++a) {
       mbar_init(bar_accfull + 8 * a, 1);
@@ -482,15 +496,16 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
   if (warp == kWarpA) alloc_columns<kPair>(smem_u32(tmem_holder), static_cast<uint32_t>(p.tmem_cols));
   tc_fence_before();
   __syncthreads();
-  if (kPair) cluster_sync();   // every CTA's barriers are ready
+  if (kGroup != kAlone) cluster_sync();   // every CTA's barriers are ready
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
   pdl_wait();
 
   const int num_tiles = p.tiles ? static_cast<int>(min(static_cast<long long>(*p.num_tiles), p.cap))
                                 : static_cast<int>(p.cap);
-  const int col_units = kQuad ? (p.col_blocks + 1) / 2 : p.col_blocks;
+  const int col_units = (p.col_blocks + kShare - 1) / kShare;
   const long long units = static_cast<long long>(num_tiles) * col_units * p.splits;
+  constexpr int kCtas = kGroup != kAlone ? 2 : 1;
   const int unit0 = blockIdx.x / kCtas, unit_step = gridDim.x / kCtas;
   const int stages = p.stages, accs = p.accs;
   int* const err = p.err;
@@ -503,18 +518,18 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     // copy).  Gathered rows come four to a copy, and a copy takes about 80 cycles of a
     // warp: three warps share them, in every eight copies three, two (beside B's box)
     // and three, none for the rows past the tile, whose results are not stored (8192
-    // tokens of top-6 of 256, 4096 -> 2048: 1113 us by one warp, 744 by two).
+    // tokens of top-6 of 256, 4096 -> 2048, in pairs of CTAs: 1113 us by one warp, 744 by
+    // two, 716 so).
     const bool is_b = warp == kWarpB;
     const int lead = is_b ? 3 : warp == kWarpA ? 0 : 5, share = is_b ? 2 : 3;
     int* const list = reinterpret_cast<int*>(gbase + p.off_list);
-    const uint32_t full0 = kPair ? of_cta(bar_full, cta & ~1) : bar_full;
-    const uint16_t both_pairs = static_cast<uint16_t>(5u << rank);   // the CTAs that hold the same rows of A
+    const uint32_t full0 = kPair ? of_cta(bar_full, 0) : bar_full;
     const bool leader = elect_one();
     Ring ring;
     long long issued = 0;
     bool ok = true, ready = false;
     for (long long u = unit0; ok && u < units; u += unit_step) {
-      const Unit t = unit_at<kQuad>(p, u, num_tiles, col_units, pair_of_ctas);
+      const Unit t = unit_at<kShare>(p, u, num_tiles, col_units, sharer);
       if (!t.ok) {
         if (is_b && first && leader) record_error(err, TQ_ERR_INVALID_ARG, kWhereTileLoad);
         continue;
@@ -526,7 +541,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
       if (p.gather) {
 #pragma unroll
         for (int r = 0; r < (kPair ? 2 : 1); ++r) {
-          if (kQuad)
+          if (kShared)
             bytes += 4 * kStepBytes * (shared_copies(part_of(gathered(t.rows, r), 0), lead, share) +
                                        shared_copies(part_of(gathered(t.rows, r), 1), lead, share));
           else
@@ -566,22 +581,21 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
           }
           if (p.gather) {
 #pragma unroll
-            for (int j = 0; j < kRows / (kQuad ? 8 : 4); j += 8) {
+            for (int j = 0; j < kRows / (4 * kShare); j += 8) {
 #pragma unroll
               for (int i = 0; i < 3; ++i) {
-                const int c = (kQuad ? pair_of_ctas * (kRows / 8) : 0) + j + lead + i;
+                const int c = sharer * (kRows / 8) + j + lead + i;
                 if (i < share && c < copies) {
                   const int4 rows = *reinterpret_cast<const int4*>(list + 4 * c);
-                  if constexpr (kQuad)
-                    load_rows_to(dst + 4 * c * kStepBytes, &tm_a, at, rows, full, both_pairs);
+                  if constexpr (kShared)
+                    load_rows_to_both(dst + 4 * c * kStepBytes, &tm_a, at, rows, full);
                   else
                     load_rows<kPair>(dst + 4 * c * kStepBytes, &tm_a, at, rows, full);
                 }
               }
             }
-          } else if (kQuad && !is_b) {
-            const int half = row0 + 64 * pair_of_ctas;
-            load_box_to(dst + 8192 * pair_of_ctas, &tm_a, kAMn ? half : at, kAMn ? at : half, full, both_pairs);
+          } else if (kShared && !is_b) {
+            load_box_to_both(dst + 8192 * sharer, &tm_a, at, row0 + 64 * sharer, full);
           } else if (!is_b) {
 #pragma unroll
             for (int i = 0; i < kABoxes; ++i)
@@ -626,7 +640,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     const bool leader = elect_one();
     Ring acc;
     for (long long u = unit0; u < units; u += unit_step) {
-      const Unit t = unit_at<kQuad>(p, u, num_tiles, col_units, pair_of_ctas);
+      const Unit t = unit_at<kShare>(p, u, num_tiles, col_units, sharer);
       if (!t.ok) continue;
       for (int k = t.k0; k < t.k1; ++k) {
         if (k8 || k == t.k0) {
@@ -652,8 +666,8 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
           for (int i = 0; i < 4; ++i)
             mma<k8, kPair>(d, a + i * (kAMn ? 128 : 2), b + i * (kBMn ? 128 : 2), idesc,
                            (i != 0 || (!k8 && k != t.k0)) ? 1u : 0u);
-          commit<kPair>(this_bar + 8 * kMaxStages, kQuad ? 15u : 3u);   // the stage's empty barrier
-          if (last) commit<kPair>(bar_accfull + 8 * acc.at, own_pair);
+          commit<kPair, kShared>(this_bar + 8 * kMaxStages);   // the stage's empty barrier
+          if (last) commit<kPair, false>(bar_accfull + 8 * acc.at);
         }
         if (last) acc.advance(accs);
         if (*abort_flag) break;
@@ -687,7 +701,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     int parity = 0;
     Ring acc;
     for (long long u = unit0; u < units; u += unit_step) {
-      const Unit t = unit_at<kQuad>(p, u, num_tiles, col_units, pair_of_ctas);
+      const Unit t = unit_at<kShare>(p, u, num_tiles, col_units, sharer);
       if (!t.ok) continue;
       const int in_tile = rank * kRows + 32 * q + lane;
       const int slot = t.slot0 + min(in_tile, t.rows - 1);
@@ -744,7 +758,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                 __syncwarp();
                 if (lane == 0) {
                   if (kPair && !first)
-                    cluster_arrive(of_cta(bar_accempty + 8 * acc.at, cta & ~1));
+                    cluster_arrive(of_cta(bar_accempty + 8 * acc.at, 0));
                   else
                     mbar_arrive(bar_accempty + 8 * acc.at);
                 }
@@ -848,7 +862,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
         __syncwarp();
         if (lane == 0) {
           if (kPair && !first)
-            cluster_arrive(of_cta(bar_accempty + 8 * acc.at, cta & ~1));
+            cluster_arrive(of_cta(bar_accempty + 8 * acc.at, 0));
           else
             mbar_arrive(bar_accempty + 8 * acc.at);
         }
@@ -860,23 +874,20 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
   pdl_trigger();
   tc_fence_before();
   __syncthreads();
-  if (kPair) cluster_sync();   // no CTA's memory is needed by another any more
+  if (kGroup != kAlone) cluster_sync();   // no CTA's memory is needed by another any more
   if (warp == kWarpA) {
     tc_fence_after();
     free_columns<kPair>(tmem, static_cast<uint32_t>(p.tmem_cols));
   }
 }
 
-// Clusters of four CTAs that the device holds at once: fewer than a quarter of its SMs,
-// as they do not cross its partitions (36 of GB300's 152 / 4 = 38).
-int quads();
-
 // Launches one variant; `units` bounds the units of a launch whose tile map is on the
 // device.  Stages, accumulators and shared memory are filled in here.
-template <bool k8, int kCtas, int kCols, bool kAMn, bool kBMn, int kEpi>
+template <bool k8, Group kGroup, int kCols, bool kAMn, bool kBMn, int kEpi>
 int launch(Params p, const CUtensorMap& a, const CUtensorMap& b, long long units, cudaStream_t s) {
-  constexpr bool kPair = kCtas > 1;
-  auto kernel = tile_gemm_kernel<k8, kCtas, kCols, kAMn, kBMn, kEpi>;
+  constexpr bool kPair = kGroup == kPaired;
+  constexpr int kCtas = kGroup != kAlone ? 2 : 1;
+  auto kernel = tile_gemm_kernel<k8, kGroup, kCols, kAMn, kBMn, kEpi>;
   static std::atomic<uint64_t> allowed{0};   // bit d: device d
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) {
@@ -917,8 +928,7 @@ int launch(Params p, const CUtensorMap& a, const CUtensorMap& b, long long units
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const long long clusters = kCtas == 4 ? quads() : sm_count() / kCtas;
-  cfg.gridDim = dim3(kCtas * static_cast<int>(std::max<long long>(1, std::min<long long>(units, clusters))));
+  cfg.gridDim = dim3(kCtas * static_cast<int>(std::max<long long>(1, std::min<long long>(units, sm_count() / kCtas))));
   if (cudaLaunchKernelEx(&cfg, kernel, a, b, p) != cudaSuccess) {
     cudaGetLastError();
     return TQ_ERR_LAUNCH;
