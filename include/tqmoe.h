@@ -689,6 +689,8 @@ int tq_fp8_moe_mlp_forward(const uint8_t* x, const float* x_scales, const uint8_
  * gate_up (device) fp32 [n][2I], 16-byte aligned, or NULL: gate and up as the
  *   gradient takes them (fp32: their roundings to 16 bits would be as large as the
  *   one of d below).
+ * workspace (device, 256-byte aligned) of tq_swiglu_linear_workspace_size() bytes (0
+ *   on invalid arguments; 256, or a NULL workspace, where none is needed).
  *
  * tq_swiglu_linear_backward: from grad_h (device, [n][I] dense, 16-byte aligned)
  *   dgate = grad_h * up * s * (1 + gate * (1 - s)), dup = grad_h * gate * s,
@@ -700,8 +702,9 @@ int tq_fp8_moe_mlp_forward(const uint8_t* x, const float* x_scales, const uint8_
  *   tq_swiglu_linear_backward_workspace_size() bytes (0 on invalid arguments).
  * Limits: n, 2I and H below 2^31 - 1024, products of two of them below 2^57.
  * ------------------------------------------------------------------------- */
-int tq_swiglu_linear(const void* x, int type, int64_t x_stride, const void* w_gu, int64_t n, int H, int I, void* h,
-                     float* gate_up, tq_stream_t stream);
+size_t tq_swiglu_linear_workspace_size(int64_t n, int H, int I);
+int tq_swiglu_linear(const void* x, int type, int64_t x_stride, const void* w_gu, int64_t n, int H, int I,
+                     void* workspace, size_t workspace_bytes, void* h, float* gate_up, tq_stream_t stream);
 size_t tq_swiglu_linear_backward_workspace_size(int64_t n, int H, int I, int has_gate_up);
 int tq_swiglu_linear_backward(const void* x, int type, int64_t x_stride, const void* w_gu, const float* gate_up,
                               const void* grad_h, int64_t n, int H, int I, void* workspace, size_t workspace_bytes,
@@ -753,9 +756,10 @@ void tq_launch_counts(int64_t out[TQ_NUM_LAUNCH_COUNTERS]);
  * out[19] SwiGLU staging, out[20] 4-bit GEMV, out[21] RMS norm, out[22] its
  * gradient, out[23] the sum of its weight's gradient, out[24] 8-bit quantise,
  * out[25] dequantise, out[26] 8-bit product, out[27] product with few rows (8 or 16
- * bits), out[28] 16-bit product, out[29] gradient of the gated activation.  Writes the first `capacity` of them and returns how
+ * bits), out[28] 16-bit product, out[29] sum of a gated projection's K splits, out[30]
+ * gradient of the gated activation.  Writes the first `capacity` of them and returns how
  * many there are. */
-#define TQ_NUM_ALL_LAUNCH_COUNTERS 30
+#define TQ_NUM_ALL_LAUNCH_COUNTERS 31
 int tq_launch_counts_all(int64_t* out, int capacity);
 
 #ifdef __cplusplus

@@ -32,7 +32,7 @@ __all__ = [
     "tq_rms_norm", "tq_rms_norm_fp8", "tq_rms_norm_backward_workspace_size", "tq_rms_norm_backward",
     "tq_fp8_quantize", "tq_fp8_dequantize", "tq_fp8_linear_workspace_size", "tq_fp8_linear", "tq_fp8_moe_workspace_size",
     "tq_fp8_moe_forward", "tq_fp8_moe_mlp_workspace_size", "tq_fp8_moe_mlp_forward", "FP8_BLOCK",
-    "tq_swiglu_linear", "tq_swiglu_linear_backward_workspace_size", "tq_swiglu_linear_backward",
+    "tq_swiglu_linear_workspace_size", "tq_swiglu_linear", "tq_swiglu_linear_backward_workspace_size", "tq_swiglu_linear_backward",
 ]
 
 ARM_AUTO, ARM_GEMV, ARM_GROUPED, ARM_MEASURED = 0, 1, 2, 3
@@ -128,7 +128,8 @@ _SIGS = {
     "tq_fp8_moe_mlp_workspace_size": (_c_sz, [_c_i64, _c_int, _c_int, _c_int, _c_int]),
     "tq_fp8_moe_mlp_forward": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_int, _c_int, _c_int,
                                         _c_int, _c_p, _c_sz, _c_p, _c_int, _c_p]),
-    "tq_swiglu_linear": (_c_int, [_c_p, _c_int, _c_i64, _c_p, _c_i64, _c_int, _c_int, _c_p, _c_p, _c_p]),
+    "tq_swiglu_linear_workspace_size": (_c_sz, [_c_i64, _c_int, _c_int]),
+    "tq_swiglu_linear": (_c_int, [_c_p, _c_int, _c_i64, _c_p, _c_i64, _c_int, _c_int, _c_p, _c_sz, _c_p, _c_p, _c_p]),
     "tq_swiglu_linear_backward_workspace_size": (_c_sz, [_c_i64, _c_int, _c_int, _c_int]),
     "tq_swiglu_linear_backward": (_c_int, [_c_p, _c_int, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_int, _c_int, _c_p, _c_sz,
                                            _c_p, _c_p, _c_p]),
@@ -674,7 +675,7 @@ ALL_LAUNCH_COUNTERS = LAUNCH_COUNTERS + ("router_scored", "router_scored_backwar
                                          "fp4_tile_scales", "fp4_stage", "fp4_gemm", "fp4_combine", "fp4_swiglu",
                                          "fp4_gemv", "rms_norm", "rms_norm_backward", "rms_norm_weight", "fp8_quantize",
                                          "fp8_dequantize", "fp8_gemm", "few_rows", "gemm_f16",
-                                         "swiglu_grad")
+                                         "swiglu_sum", "swiglu_grad")
 
 
 # ------------------------------------------------------------------ scored router, 4-bit operators
@@ -1357,7 +1358,11 @@ def _rows16(x):
     return rows
 
 
-def tq_swiglu_linear(x, w_gu, h=None, gate_up=None, stream=None):
+def tq_swiglu_linear_workspace_size(n: int, H: int, I: int) -> int:
+    return lib().tq_swiglu_linear_workspace_size(n, H, I)
+
+
+def tq_swiglu_linear(x, w_gu, h=None, gate_up=None, workspace=None, stream=None):
     """h [n, I] = silu(x Wg^T) * (x Wu^T) for x [n, H] in bf16 or fp16 (rows may be
     strided) and w_gu [2I, H] of the same dtype, gate rows first; H and I multiples
     of 8.  With gate_up (fp32 [n, 2I]) gate and up are kept there for the gradient."""
@@ -1367,7 +1372,9 @@ def tq_swiglu_linear(x, w_gu, h=None, gate_up=None, stream=None):
     w_ptr = _given(w_gu, (2 * I, H), (x.dtype,), "w_gu", device)
     h, h_ptr = _dense(h, n, I, x, "h", device, stream)
     gu_ptr = None if gate_up is None else _given(gate_up, (n, 2 * I), fp32, "gate_up", device)
-    rc = _call("tq_swiglu_linear")(ptr, code, step, w_ptr, n, H, I, h_ptr, gu_ptr, _stream(stream, device))
+    work_ptr, work_bytes, workspace = _workspace(workspace, tq_swiglu_linear_workspace_size, device, stream, n, H, I)
+    rc = _call("tq_swiglu_linear")(ptr, code, step, w_ptr, n, H, I, work_ptr, work_bytes, h_ptr, gu_ptr,
+                                   _stream(stream, device))
     if rc:
         raise TQError(rc, "tq_swiglu_linear")
     return h

@@ -1,5 +1,5 @@
 // Matrix products with few activation rows: y[t] = W x[t] for up to 8 or 16 rows of x
-// that share a matrix, bound by the reading of W.
+// at a time, of one matrix or of the experts of a few tokens, bound by the reading of W.
 //
 // A warp multiplies 16 weight rows (gated: 8 of the gate and 8 of the up projection)
 // with all the activation rows, K 128 bytes at a time, by m16n8 MMAs whose operands
@@ -12,10 +12,12 @@
 // are far below its rate at the memory's.
 //
 // The eight warps of a block split K by blocks of 128 bytes and add up through
-// shared memory in a fixed order.  Blocks walk their share of the units (an m-tile x 16
-// weight rows), each warp with its next blocks of weights under way, across units
-// too: a block of threads for each unit left the memory idle between their starts and
-// ends (32 tokens of top-6 of 256, 4096 -> 2048: 247 us for 1.14 GB, walking 197).
+// shared memory in a fixed order.  Blocks walk their share of the units (a group of
+// rows x 16 weight rows), each warp with its next blocks of weights under way, across
+// units too.  A step costs about 200 instructions of a warp (the 8-bit MMAs are
+// expanded into conversions and 16-bit ones): 55 to 75% of the memory's rate; from
+// where experts share tokens on the tensor-memory tiles are faster (16 tokens of top-6 of
+// 256, 4096 -> 2048: 156 us here, 138 there).
 //
 // A single token's experts are the segments of one unit, whose sums, weighted, add up
 // in the same registers: its product is this one launch.
@@ -46,6 +48,9 @@ enum Kind { kFp8 = 0, kBf16 = 1, kFp16 = 2 };
 
 // Copies 16 bytes (or, with `bytes` 0, zeros), 4 bytes, to shared memory in this
 // thread's current group of copies.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -84,18 +89,9 @@ __device__ __forceinline__ T& either(T& a, T& b) {
     return b;
 }
 
-// A unit's activation rows: of a tile map's tile, of one pair or token, or consecutive.
-struct Tile {
-  int slot0, rows;
-};
-__device__ __forceinline__ Tile tile_at(const FewRows& p, int tile, int cols) {
-  if (p.tiles) return {__ldg(p.tiles + 3ll * tile + 1), __ldg(p.tiles + 3ll * tile + 2)};
-  if (p.ids) return {tile, 1};
-  return {tile * cols, min(cols, p.M - tile * cols)};
-}
 // The matrix of a unit's segment; -1 when out of range.
 __device__ __forceinline__ int matrix_at(const FewRows& p, int tile, int segment) {
-  const int e = p.tiles ? __ldg(p.tiles + 3ll * tile) : p.ids ? __ldg(p.ids + static_cast<long long>(tile) * p.segments + segment) : 0;
+  const int e = p.ids ? __ldg(p.ids + static_cast<long long>(tile) * p.segments + segment) : 0;
   return e >= 0 && e < p.E ? e : -1;
 }
 
@@ -134,7 +130,7 @@ struct Place {
 
 // kTiles: groups of 8 activation rows; kSegments: a token's experts one after another.
 template <int kKind, bool kGated, int kTiles, bool kSegments>
-__global__ void __launch_bounds__(kThreads, 2) few_rows_kernel(const FewRows p, const int row_blocks, const int max_tiles) {
+__global__ void __launch_bounds__(kThreads, 2) few_rows_kernel(const FewRows p, const int row_blocks, const unsigned units) {
   constexpr int kCols = 8 * kTiles, kFeatures = kGated ? kRows / 2 : kRows;
   extern __shared__ uint4 ring[];   // [kAhead][warps][4][lanes]: a lane's own bytes, read back by it alone
   __shared__ float scale_ring[kAhead][kWarps][2];
@@ -144,11 +140,9 @@ __global__ void __launch_bounds__(kThreads, 2) few_rows_kernel(const FewRows p, 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, q = lane & 3;
   const long long row_bytes = p.row_bytes;
-  const int tiles = p.num_tiles ? min(*p.num_tiles, max_tiles) : max_tiles;
   // this block's units, neighbours
-  const unsigned units = static_cast<unsigned>(tiles) * row_blocks, each = units / gridDim.x, more = units % gridDim.x;
+  const unsigned each = units / gridDim.x, more = units % gridDim.x;
   const unsigned u0 = each * blockIdx.x + min(blockIdx.x, more), u1 = u0 + each + (blockIdx.x < more ? 1u : 0u);
-  if (u0 == u1) return;
 
   // Weights: the place that is loaded next, kAhead steps before its use.
   Place<kSegments> here;
@@ -158,37 +152,46 @@ __global__ void __launch_bounds__(kThreads, 2) few_rows_kernel(const FewRows p, 
   here.start(p, warp);
   const bool idle = here.past_unit(p);   // a warp without a step in a unit only joins its sums
   Place<kSegments> ahead = here;
-  const uint8_t* w[2];    // this lane's two rows
-  const float* sw[2];     // and their scales
-  bool in[2];
+  // This lane's two rows of the step that is loaded next, and the scales of one (gated:
+  // of the first lane the gate's, of the others the up projection's).  Rows past the
+  // matrix repeat its last: nothing of theirs is stored.
+  const uint8_t* w[2];
+  const float* sw = nullptr;
   auto aim = [&] {
-    const int e = matrix_at(p, ahead.tile, ahead.segment);
+    const int e = max(matrix_at(p, ahead.tile, ahead.segment), 0), first = ahead.block * kFeatures;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int first = ahead.block * kFeatures, f = first + g + (kGated ? 0 : 8 * h);
-      in[h] = e >= 0 && f < p.N;
-      w[h] = p.w + (in[h] ? (kGated ? (2ll * e + h) * p.N : static_cast<long long>(e) * p.N) + f : 0) * row_bytes + 16 * q;
-      if (kKind == kFp8)
-        sw[h] = p.w_scales +
-                (static_cast<long long>(max(e, 0)) * p.w_blocks + (first + (kGated ? h * p.N : 0)) / 128) * p.steps;
+      const int f = min(first + g + (kGated ? 0 : 8 * h), p.N - 1);
+      w[h] = p.w + ((kGated ? (2ll * e + h) * p.N : static_cast<long long>(e) * p.N) + f) * row_bytes +
+             static_cast<long long>(ahead.k) * kStepBytes + 16 * q;
     }
+    if (kKind == kFp8)
+      sw = p.w_scales + (static_cast<long long>(e) * p.w_blocks + (first + (kGated && lane ? p.N : 0)) / 128) * p.steps +
+           ahead.k;
   };
+  const int full_steps = static_cast<int>(row_bytes / kStepBytes), tail = static_cast<int>(row_bytes % kStepBytes);
   const uint32_t mine = smem_u32(ring) + static_cast<uint32_t>(warp * 32 * kLaneBytes + lane * 16);
   auto load = [&](int slot) {
     if (!idle && ahead.unit < u1) {
-      const long long at = static_cast<long long>(ahead.k) * kStepBytes;
       const uint32_t dst = mine + static_cast<uint32_t>(slot * kThreads * kLaneBytes);
+      if (ahead.k < full_steps) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h) {
+          copy16(dst + 1024 * h, w[h]);
+          copy16(dst + 1024 * h + 512, w[h] + 64);
+        }
+      } else {   // the last bytes of the rows, zeros behind them
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const bool inside = in[h] && at + 64 * j + 16 * q < row_bytes;
-          copy16(dst + (2 * h + j) * 512, inside ? w[h] + at + 64 * j : p.w, inside ? 16 : 0);
+        for (int h = 0; h < 2; ++h) {
+          copy16(dst + 1024 * h, w[h], 16 * q < tail ? 16 : 0);
+          copy16(dst + 1024 * h + 512, 64 + 16 * q < tail ? w[h] + 64 : w[h], 64 + 16 * q < tail ? 16 : 0);
         }
       }
-      if (kKind == kFp8 && lane <= (kGated ? 1 : 0))
-        copy4(smem_u32(&scale_ring[slot][warp][lane]), (kGated && lane ? sw[1] : sw[0]) + ahead.k);
+      if (kKind == kFp8 && lane <= (kGated ? 1 : 0)) copy4(smem_u32(&scale_ring[slot][warp][lane]), sw);
       ahead.k += kWarps;
+      w[0] += kWarps * kStepBytes;
+      w[1] += kWarps * kStepBytes;
+      sw += kWarps;
       bool moved = ahead.settle(p);
       if (ahead.past_unit(p)) {
         ahead.next_unit(p, row_blocks, warp);
@@ -205,26 +208,16 @@ __global__ void __launch_bounds__(kThreads, 2) few_rows_kernel(const FewRows p, 
   // The unit that is multiplied.  Column g (+ 8 c) is this lane's: its rows of x and of
   // the output, -1 for none.
   int x_row[kTiles], y_row[kTiles];
-  const uint8_t* x[kTiles];
-  const float* sx[kTiles][2];   // the scales of this lane's two columns of sums
+  const uint8_t* x[kTiles];     // of the step that is loaded next
+  const float* sx[kTiles][2];   // and the scales of this lane's two columns of sums
   float weight = 1.f;           // of the segment
   auto enter_tile = [&] {
-    const Tile t = tile_at(p, here.tile, kCols);
-    const bool ok = t.slot0 >= 0 && t.rows >= 1 && t.rows <= p.M - t.slot0;
-    if (!ok && here.block == 0 && threadIdx.x == 0) record_error(p.err, TQ_ERR_INVALID_ARG, kWhereFewRows);
 #pragma unroll
     for (int c = 0; c < kTiles; ++c) {
-      x_row[c] = y_row[c] = -1;
-      if (ok && 8 * c + g < t.rows) {
-        const int slot = t.slot0 + 8 * c + g;
-        const int pair = p.sorted_pairs ? __ldg(p.sorted_pairs + slot) : slot;
-        if (pair >= 0 && pair < p.M) {
-          x_row[c] = p.gather ? pair / p.top_k : slot;
-          y_row[c] = p.scatter ? pair : slot;
-        } else if (here.block == 0 && warp == 0 && q == 0) {
-          record_error(p.err, TQ_ERR_INVALID_ARG, kWhereFewRows);
-        }
-      }
+      // the rows of one matrix lie together; a pair's, or a token's, is alone
+      const int row = p.ids ? (8 * c + g == 0 ? here.tile : p.M) : here.tile * kCols + 8 * c + g;
+      y_row[c] = row < p.M ? row : -1;
+      x_row[c] = y_row[c] >= 0 && p.gather ? row / p.top_k : y_row[c];
     }
   };
   auto enter_segment = [&] {
@@ -235,11 +228,11 @@ __global__ void __launch_bounds__(kThreads, 2) few_rows_kernel(const FewRows p, 
     for (int c = 0; c < kTiles; ++c) {
       // a unit of segments has one row of x for all, or one for each
       const int row = kSegments && !p.gather && x_row[c] >= 0 ? x_row[c] * p.segments + here.segment : x_row[c];
-      x[c] = p.x + max(row, 0) * p.x_stride + 16 * q;
+      x[c] = p.x + max(row, 0) * p.x_stride + static_cast<long long>(here.k) * kStepBytes + 16 * q;
       if constexpr (kKind == kFp8) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          sx[c][i] = p.x_scales + static_cast<long long>(max(__shfl_sync(0xffffffffu, row, 4 * (2 * q + i)), 0)) * p.steps;
+          sx[c][i] = p.x_scales + static_cast<long long>(max(__shfl_sync(0xffffffffu, row, 4 * (2 * q + i)), 0)) * p.steps + here.k;
       }
     }
     return e >= 0;
@@ -249,40 +242,49 @@ __global__ void __launch_bounds__(kThreads, 2) few_rows_kernel(const FewRows p, 
     uint4 v[kTiles][2];
     float s0[kTiles], s1[kTiles];
   };
-  Step next;
-  auto load_x = [&](int k) {
+  auto load_x = [&](Step& to, int k) {
 #pragma unroll
     for (int c = 0; c < kTiles; ++c) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const long long at = static_cast<long long>(k) * kStepBytes + 64 * j;
-        next.v[c][j] = make_uint4(0u, 0u, 0u, 0u);
-        if (x_row[c] >= 0 && at + 16 * q < row_bytes) next.v[c][j] = __ldg(reinterpret_cast<const uint4*>(x[c] + at));
+      const uint4* const src = reinterpret_cast<const uint4*>(x[c]);
+      if (x_row[c] < 0) {
+        // nothing of the column is stored
+      } else if (k < full_steps) {
+        to.v[c][0] = __ldg(src);
+        to.v[c][1] = __ldg(src + 4);
+      } else {
+        to.v[c][0] = to.v[c][1] = make_uint4(0u, 0u, 0u, 0u);
+        if (16 * q < tail) to.v[c][0] = __ldg(src);
+        if (64 + 16 * q < tail) to.v[c][1] = __ldg(src + 4);
       }
+      x[c] += kWarps * kStepBytes;
       if constexpr (kKind == kFp8) {
-        next.s0[c] = __ldg(sx[c][0] + k);
-        next.s1[c] = __ldg(sx[c][1] + k);
+        to.s0[c] = __ldg(sx[c][0]);
+        to.s1[c] = __ldg(sx[c][1]);
+        sx[c][0] += kWarps;
+        sx[c][1] += kWarps;
       }
     }
   };
   enter_tile();
   bool live = false;
+  Step steps[2] = {};
   if (!idle) {
     live = enter_segment();
-    load_x(here.k);
+    load_x(steps[0], here.k);
   }
 
   float sum[kTiles][4] = {};
   int buffer = 0, slot = 0;
-  while (true) {
-      if (!idle) {
-        const Step xs = next;
-        if (here.k + kWarps < p.steps) load_x(here.k + kWarps);
-        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
-        __syncwarp();
-        const uint32_t src = mine + static_cast<uint32_t>(slot * kThreads * kLaneBytes);
-        const float w0 = kKind == kFp8 ? scale_ring[slot][warp][0] : 0.f;
-        const float w1 = kKind == kFp8 && kGated ? scale_ring[slot][warp][1] : w0;
+  const int per_unit = (p.steps - warp + kWarps - 1) / kWarps;   // steps of this warp, without segments
+  // One step, its x in `now`; false after the last.
+  auto turn = [&](const Step& now, Step& next) {
+    if (!idle) {
+      if (here.k + kWarps < p.steps) load_x(next, here.k + kWarps);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+      __syncwarp();
+      const uint32_t src = mine + static_cast<uint32_t>(slot * kThreads * kLaneBytes);
+      const float w0 = kKind == kFp8 ? scale_ring[slot][warp][0] : 0.f;
+      const float w1 = kKind == kFp8 && kGated ? scale_ring[slot][warp][1] : w0;
       if (live) {
         float part[kTiles][4];
         if constexpr (kKind == kFp8) {
@@ -298,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_rows_kernel(const FewRows p, 
           const uint4 lo = read16(src + 512 * j), hi = read16(src + 512 * (2 + j));
 #pragma unroll
           for (int c = 0; c < kTiles; ++c) {
-            const uint4 v = xs.v[c][j];
+            const uint4 v = now.v[c][j];
             mma16x8<kKind>(to[c], lo.x, hi.x, lo.y, hi.y, v.x, v.y);
             mma16x8<kKind>(to[c], lo.z, hi.z, lo.w, hi.w, v.z, v.w);
           }
@@ -306,79 +308,93 @@ __global__ void __launch_bounds__(kThreads, 2) few_rows_kernel(const FewRows p, 
         if constexpr (kKind == kFp8) {
 #pragma unroll
           for (int c = 0; c < kTiles; ++c) {
-            sum[c][0] = fmaf(part[c][0], xs.s0[c] * f0, sum[c][0]);
-            sum[c][1] = fmaf(part[c][1], xs.s1[c] * f0, sum[c][1]);
-            sum[c][2] = fmaf(part[c][2], xs.s0[c] * f1, sum[c][2]);
-            sum[c][3] = fmaf(part[c][3], xs.s1[c] * f1, sum[c][3]);
+            sum[c][0] = fmaf(part[c][0], now.s0[c] * f0, sum[c][0]);
+            sum[c][1] = fmaf(part[c][1], now.s1[c] * f0, sum[c][1]);
+            sum[c][2] = fmaf(part[c][2], now.s0[c] * f1, sum[c][2]);
+            sum[c][3] = fmaf(part[c][3], now.s1[c] * f1, sum[c][3]);
           }
         }
       }
-        __syncwarp();   // every lane has its scales
-        load(slot);
-        if (++slot == kAhead) slot = 0;
-        here.k += kWarps;
-        const bool moved = here.settle(p);
-        if (!here.past_unit(p)) {
-          if (moved) {
-            live = enter_segment();
-            load_x(here.k);
-          }
-          continue;
+      __syncwarp();   // every lane has its scales
+      load(slot);
+      if (++slot == kAhead) slot = 0;
+      here.k += kWarps;
+      const bool moved = here.settle(p);
+      if (!here.past_unit(p)) {
+        if (moved) {
+          live = enter_segment();
+          load_x(next, here.k);
         }
+        return true;
       }
-      // the unit's end: its sums, and the next one
+    }
+    // the unit's end: its sums, and the next one
 #pragma unroll
-      for (int c = 0; c < kTiles; ++c) {
+    for (int c = 0; c < kTiles; ++c) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          *reinterpret_cast<float2*>(&sums[buffer][warp][g + 8 * h][8 * c + 2 * q]) =
-              make_float2(sum[c][2 * h], sum[c][2 * h + 1]);
-          sum[c][2 * h] = sum[c][2 * h + 1] = 0.f;
+      for (int h = 0; h < 2; ++h) {
+        *reinterpret_cast<float2*>(&sums[buffer][warp][g + 8 * h][8 * c + 2 * q]) =
+            make_float2(sum[c][2 * h], sum[c][2 * h + 1]);
+        sum[c][2 * h] = sum[c][2 * h + 1] = 0.f;
+      }
+    }
+    __syncthreads();   // (a buffer is written again after the next unit's barrier)
+    if (threadIdx.x < kFeatures * kCols) {
+      static_assert(kFeatures * kCols <= kThreads && kFeatures * kCols % 32 == 0, "one result a thread, whole warps");
+      const int r = threadIdx.x % kFeatures, c = threadIdx.x / kFeatures;   // a warp's columns are of the same eight
+      int row = y_row[0];
+      if (kTiles > 1 && c >= 8) row = y_row[kTiles - 1];
+      const long long to = __shfl_sync(0xffffffffu, row, 4 * (c % 8));
+      const int f = here.block * kFeatures + r;
+      if (to >= 0 && f < p.N) {
+        float v[2] = {0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < kWarps; ++s) {
+          v[0] += sums[buffer][s][r][c];
+          if (kGated) v[1] += sums[buffer][s][r + (kGated ? 8 : 0)][c];
+        }
+        float out = v[0];
+        if constexpr (kGated) {
+          if (p.gate_up) {
+            p.gate_up[to * 2 * p.N + f] = v[0];
+            p.gate_up[(to * 2 + 1) * p.N + f] = v[1];
+          }
+          out = v[0] / (1.f + expf(-v[0])) * v[1];
+        }
+        const long long at = to * p.N + f;
+        if (!p.y) {
+        } else if (p.y_type == TQ_FP32) {
+          static_cast<float*>(p.y)[at] = out;
+        } else if (p.y_type == TQ_BF16) {
+          static_cast<__nv_bfloat16*>(p.y)[at] = narrow<__nv_bfloat16>(out);
+        } else {
+          static_cast<__half*>(p.y)[at] = narrow<__half>(out);
         }
       }
-      __syncthreads();   // (a buffer is written again after the next unit's barrier)
-      if (threadIdx.x < kFeatures * kCols) {
-        static_assert(kFeatures * kCols <= kThreads && kFeatures * kCols % 32 == 0, "one result a thread, whole warps");
-        const int r = threadIdx.x % kFeatures, c = threadIdx.x / kFeatures;   // a warp's columns are of the same eight
-        int row = y_row[0];
-        if (kTiles > 1 && c >= 8) row = y_row[kTiles - 1];
-        const long long to = __shfl_sync(0xffffffffu, row, 4 * (c % 8));
-        const int f = here.block * kFeatures + r;
-        if (to >= 0 && f < p.N) {
-          float v[2] = {0.f, 0.f};
+    }
+    buffer ^= 1;
+    const int tile = here.tile;
+    here.next_unit(p, row_blocks, warp);
+    if (here.unit >= u1) return false;
+    if (here.tile != tile) enter_tile();
+    if (!idle) {
+      if (kSegments || here.tile != tile) {
+        live = enter_segment();
+      } else {   // the same rows from their start
 #pragma unroll
-          for (int s = 0; s < kWarps; ++s) {
-            v[0] += sums[buffer][s][r][c];
-            if (kGated) v[1] += sums[buffer][s][r + (kGated ? 8 : 0)][c];
-          }
-          float out = v[0];
-          if constexpr (kGated) {
-            if (p.gate_up) {
-              p.gate_up[to * 2 * p.N + f] = v[0];
-              p.gate_up[(to * 2 + 1) * p.N + f] = v[1];
-            }
-            out = v[0] / (1.f + expf(-v[0])) * v[1];
-          }
-          const long long at = to * p.N + f;
-          if (!p.y) {
-          } else if (p.y_type == TQ_FP32) {
-            static_cast<float*>(p.y)[at] = out;
-          } else if (p.y_type == TQ_BF16) {
-            static_cast<__nv_bfloat16*>(p.y)[at] = narrow<__nv_bfloat16>(out);
-          } else {
-            static_cast<__half*>(p.y)[at] = narrow<__half>(out);
+        for (int c = 0; c < kTiles; ++c) {
+          x[c] -= static_cast<long long>(per_unit) * (kWarps * kStepBytes);
+          if constexpr (kKind == kFp8) {
+            sx[c][0] -= per_unit * kWarps;
+            sx[c][1] -= per_unit * kWarps;
           }
         }
       }
-      buffer ^= 1;
-      const int tile = here.tile;
-      here.next_unit(p, row_blocks, warp);
-      if (here.unit >= u1) return;
-      if (here.tile != tile) enter_tile();
-      if (!idle) {
-        if (kSegments || here.tile != tile) live = enter_segment();
-        load_x(here.k);
-      }
+      load_x(next, here.k);
+    }
+    return true;
+  };
+  while (turn(steps[0], steps[1]) && turn(steps[1], steps[0])) {
   }
 }
 
@@ -403,25 +419,23 @@ int run(const FewRows& p, int tiles, cudaStream_t s) {
     }
     allowed.fetch_or(bit);
   }
-  return launch_pdl(kernel, grid, dim3(kThreads), kRingBytes, s, p, row_blocks, tiles);
+  return launch_pdl(kernel, grid, dim3(kThreads), kRingBytes, s, p, row_blocks, static_cast<unsigned>(units));
 }
 template <int kKind, bool kGated>
-int run(const FewRows& p, int cols, int tiles, cudaStream_t s) {
-  return cols == 8 ? run<kKind, kGated, 1, false>(p, tiles, s) : run<kKind, kGated, 2, false>(p, tiles, s);
+int run_rows(const FewRows& p, cudaStream_t s) {
+  return p.M <= 8 ? run<kKind, kGated, 1, false>(p, 1, s) : run<kKind, kGated, 2, false>(p, (p.M + 15) / 16, s);
 }
 
 }  // namespace
 
-int launch_few_rows(const FewRows& p, int type, bool gated, int cols, int64_t units, cudaStream_t s) {
-  if (units < 1 || units > 0x7fffffff || (cols != 8 && cols != 16)) return TQ_ERR_INVALID_ARG;
-  const int u = static_cast<int>(units);
+int launch_few_rows(const FewRows& p, int type, cudaStream_t s) {
   int st;
   if (type == kFewRowsFp8)
-    st = p.topk_w ? run<kFp8, false, 1, true>(p, u, s)
-         : gated  ? run<kFp8, true>(p, cols, u, s)
-                  : run<kFp8, false>(p, cols, u, s);
+    st = p.topk_w ? run<kFp8, false, 1, true>(p, p.M, s)
+         : p.ids  ? run<kFp8, true, 1, false>(p, p.M, s)
+                  : run_rows<kFp8, false>(p, s);
   else
-    st = type == TQ_BF16 ? run<kBf16, true>(p, cols, u, s) : run<kFp16, true>(p, cols, u, s);
+    st = type == TQ_BF16 ? run_rows<kBf16, true>(p, s) : run_rows<kFp16, true>(p, s);
   if (st == TQ_OK) count_launch(kCntFewRows);
   return st;
 }

@@ -42,7 +42,9 @@ struct Carver {
   }
 };
 
-constexpr int kFewRowsMost = 16;   // rows of an MMA pair of the few-rows kernel
+// Rows that the few-rows kernel takes of one matrix: two passes over it (4096 -> 2048: 16
+// rows 6.0 us there and 9.7 in tiles; 17 and 32 FEW32).
+constexpr int kFewRowsMost = 32;
 
 struct LinearPlan {
   bool few;
@@ -64,25 +66,22 @@ LinearPlan plan_linear(void* base, int64_t n, int K, int N) {
   return l;
 }
 
-// How the experts' products go: a token's pairs one after another, without a sort;
-// m-tiles of up to 16 rows by the few-rows kernel; or the tensor-core tiles.
-enum Arm { kTokens, kFew, kTiles };
+// How the experts' products go: a token's pairs one after another, without a sort, or in
+// the tensor-core tiles of sorted pairs.
+enum Arm { kTokens, kTiles };
 struct MoePlan {
   Arm arm;
   int tile_m;
   int64_t cap, P;
 };
-MoePlan plan_arm(int64_t n, int top_k, int E, TileChoice tile) {
+// Tokens by themselves where (almost) no expert has two pairs: of top-6 of 256, 4096 ->
+// 2048, 4 and 8 tokens took 57 and 83 us so and 65 and 90 in tiles, 16 156 and 138.
+MoePlan plan_arm(int64_t n, int top_k, int E) {
   MoePlan m;
   m.P = n * top_k;
   const double mean = n ? tq_pairs_per_woken_expert(n, top_k, E) : 0.0;
-  if (m.P <= 2 * top_k || mean < 1.1) {
-    // (almost) no expert has two pairs: sorting them would save nothing
-    m.arm = kTokens;
-  } else {
-    m.arm = mean <= 10.0 ? kFew : kTiles;
-  }
-  m.tile_m = m.arm == kTiles ? tile.tile_m : mean <= 4.0 ? 8 : 16;
+  m.arm = n <= 2 || (mean < 1.1 && n <= 1024) ? kTokens : kTiles;
+  m.tile_m = 128;
   m.cap = std::max<int64_t>(1, tq_tile_map_capacity(n, top_k, E, m.tile_m));
   return m;
 }
@@ -91,7 +90,7 @@ double typical_rows(int64_t n, int top_k, int E) {
   return mean + 2.0 * std::sqrt(mean);
 }
 TileChoice moe_tile(int64_t n, int top_k, int E, int steps, int N, bool gated, TileRows kind) {
-  if (n == 0) return {128, false, 128, 1};
+  if (n == 0) return {128, false, 128, 1, 0.0};
   const double mean = tq_pairs_per_woken_expert(n, top_k, E);
   return choose_tile(typical_rows(n, top_k, E), n * top_k / mean, steps, N, gated, kind, !gated, !gated);
 }
@@ -125,7 +124,7 @@ struct ProductPlan {
 ProductPlan plan_moe(void* base, int64_t n, int top_k, int E, int K, int N) {
   ProductPlan p;
   p.tile = moe_tile(n, top_k, E, blocks_of(K), N, false, TileRows::kGathered);
-  p.m = plan_arm(n, top_k, E, p.tile);
+  p.m = plan_arm(n, top_k, E);
   if (p.m.arm != kTiles) p.tile.splits = 1;
   Carver c{static_cast<uint8_t*>(base)};
   p.routed = carve_routed(c, p.m, E);
@@ -138,7 +137,7 @@ struct MlpPlan {
   MoePlan m;
   TileChoice gu, down;
   Routed routed;
-  float *h32, *part;   // h32: the few-rows kernel's h
+  float *h32, *part;   // h32: of tokens by themselves
   uint8_t* h;
   float* h_scales;
   size_t bytes;
@@ -147,7 +146,7 @@ MlpPlan plan_mlp(void* base, int64_t n, int top_k, int E, int H, int I) {
   MlpPlan p{};
   // one tile map for both products, by the gate and up projections'
   p.gu = moe_tile(n, top_k, E, blocks_of(H), I, true, TileRows::kGathered);
-  p.m = plan_arm(n, top_k, E, p.gu);
+  p.m = plan_arm(n, top_k, E);
   p.down = moe_tile(n, top_k, E, blocks_of(I), H, false, TileRows::kSlots);
   if (p.m.arm != kTiles) p.down.splits = 1;
   Carver c{static_cast<uint8_t*>(base)};
@@ -165,7 +164,7 @@ struct Operand {
   const float* scales;
 };
 
-// What the few-rows products of a chain have in common: w [E][N (gated 2 N)][K].
+// What the few-rows products have in common: w [E][N (gated 2 N)][K].
 FewRows few_rows(Operand x, Operand w, int64_t M, int top_k, int E, int K, int N, bool gated, void* y, int y_type, int* err) {
   FewRows f{};
   f.w = w.codes;
@@ -185,36 +184,23 @@ FewRows few_rows(Operand x, Operand w, int64_t M, int top_k, int E, int K, int N
   f.err = err;
   return f;
 }
-void set_tiles(FewRows& f, const Routed& r) {
-  f.tiles = r.tiles;
-  f.num_tiles = r.num_tiles;
-  f.sorted_pairs = r.sorted_pairs;
+// y[t] = sum_j topk_w[t][j] W x, in one launch: x the token's row, or its pairs' rows.
+int token_product(FewRows f, const int32_t* ids, const float* topk_w, bool gather, cudaStream_t s) {
+  f.ids = ids;
+  f.topk_w = topk_w;
+  f.segments = f.top_k;
+  f.top_k = 1;
+  f.gather = gather;
+  return launch_few_rows(f, kFewRowsFp8, s);
 }
 
 // The product of sorted pairs to partial sums by pair, its rows gathered from the
 // tokens or in slot order.
 int sorted_product(const MoePlan& m, const Routed& r, Operand x, int64_t x_rows, bool gather, Operand w, int top_k, int E,
                    int K, int N, TileChoice tile, float* part, int* err, cudaStream_t s) {
-  if (m.arm == kTiles) {
-    Fp8Gemm g{x.codes, x.scales, x_rows, w.codes, w.scales, r.sorted_pairs, r.tiles, r.num_tiles, m.cap, m.P, top_k, E,
-              K, N, gather, true, false, m.tile_m, tile.shared, tile.cols, tile.splits, part, TQ_FP32, nullptr, nullptr, err};
-    return launch_fp8_gemm(g, s);
-  }
-  FewRows f = few_rows(x, w, m.P, top_k, E, K, N, false, part, TQ_FP32, err);
-  set_tiles(f, r);
-  f.gather = gather;
-  f.scatter = 1;
-  return launch_few_rows(f, kFewRowsFp8, false, m.tile_m, m.cap, s);
-}
-
-// y[t] = sum_j topk_w[t][j] W x, in one launch: x the token's row, or its pairs' rows.
-int token_product(FewRows f, const int32_t* ids, const float* topk_w, bool gather, int64_t n, cudaStream_t s) {
-  f.ids = ids;
-  f.topk_w = topk_w;
-  f.segments = f.top_k;
-  f.top_k = 1;
-  f.gather = gather;
-  return launch_few_rows(f, kFewRowsFp8, false, 8, n, s);
+  Fp8Gemm g{x.codes, x.scales, x_rows, w.codes, w.scales, r.sorted_pairs, r.tiles, r.num_tiles, m.cap, m.P, top_k, E,
+            K, N, gather, true, false, m.tile_m, tile.shared, tile.cols, tile.splits, part, TQ_FP32, nullptr, nullptr, err};
+  return launch_fp8_gemm(g, s);
 }
 
 }  // namespace
@@ -276,8 +262,7 @@ int tq_fp8_linear(const uint8_t* x, const float* x_scales, const uint8_t* w, con
   int* err = error_word(&rc);
   if (!err) return rc;
   if (l.few)
-    return launch_few_rows(few_rows({x, x_scales}, {w, w_scales}, n, 1, 1, K, N, false, y, y_type, err), kFewRowsFp8, false,
-                           n <= 8 ? 8 : 16, 1, s);
+    return launch_few_rows(few_rows({x, x_scales}, {w, w_scales}, n, 1, 1, K, N, false, y, y_type, err), kFewRowsFp8, s);
   Fp8Gemm g{x, x_scales, n, w, w_scales, nullptr, nullptr, nullptr, (n + l.tile.tile_m - 1) / l.tile.tile_m, n, 1, 1, K, N,
             false, false, false, l.tile.tile_m, l.tile.shared, l.tile.cols, l.tile.splits, splits ? l.part : y,
             splits ? TQ_FP32 : y_type, nullptr, nullptr, err};
@@ -308,7 +293,7 @@ int tq_fp8_moe_forward(const uint8_t* x, const float* x_scales, const uint8_t* w
   if (!err) return rc;
   if (p.m.arm == kTokens)
     return token_product(few_rows({x, x_scales}, {w, w_scales}, n, top_k, E, K, N, false, y, y_type, err), topk_ids, topk_w,
-                         true, n, s);
+                         true, s);
   rc = route_pairs(p.m, p.routed, topk_ids, E, err, s);
   if (rc != TQ_OK) return rc;
   rc = sorted_product(p.m, p.routed, {x, x_scales}, n, true, {w, w_scales}, top_k, E, K, N, p.tile, p.part, err, s);
@@ -351,15 +336,12 @@ int tq_fp8_moe_mlp_forward(const uint8_t* x, const float* x_scales, const uint8_
   } else {
     FewRows f = few_rows({x, x_scales}, {w_gu, gu_scales}, m.P, top_k, E, H, I, true, p.h32, TQ_FP32, err);
     f.gather = 1;
-    if (m.arm == kTokens)
-      f.ids = topk_ids;
-    else
-      set_tiles(f, r);
-    rc = launch_few_rows(f, kFewRowsFp8, true, m.arm == kTokens ? 8 : m.tile_m, m.arm == kTokens ? m.P : m.cap, s);
+    f.ids = topk_ids;
+    rc = launch_few_rows(f, kFewRowsFp8, s);
     if (rc == TQ_OK) rc = launch_fp8_quantize_rows(p.h32, TQ_FP32, I, m.P, I, p.h, p.h_scales, s);
-    if (rc == TQ_OK && m.arm == kTokens)
-      return token_product(few_rows({p.h, p.h_scales}, {w_down, down_scales}, n, top_k, E, I, H, false, y, y_type, err),
-                           topk_ids, topk_w, false, n, s);
+    if (rc != TQ_OK) return rc;
+    return token_product(few_rows({p.h, p.h_scales}, {w_down, down_scales}, n, top_k, E, I, H, false, y, y_type, err),
+                         topk_ids, topk_w, false, s);
   }
   if (rc != TQ_OK) return rc;
   rc = sorted_product(m, r, {p.h, p.h_scales}, m.P, false, {w_down, down_scales}, top_k, E, I, H, p.down, p.part, err, s);

@@ -37,6 +37,8 @@ int launch_gemm_f16(const GemmF16& g, cudaStream_t s) {
     st = pair            ? launch<false, kPaired, 128, false, false, kGated16>(p, a, b, units, s)
          : g.cols == 128 ? launch<false, kAlone, 128, false, false, kGated16>(p, a, b, units, s)
                          : launch<false, kAlone, 64, false, false, kGated16>(p, a, b, units, s);
+  else if (!g.b_mn)
+    st = launch<false, kAlone, 64, false, false, kStore>(p, a, b, units, s);
   else if (g.a_mn)
     st = pair            ? launch<false, kPaired, 128, true, true, kStore>(p, a, b, units, s)
          : g.cols == 128 ? launch<false, kAlone, 128, true, true, kStore>(p, a, b, units, s)

@@ -24,7 +24,7 @@ enum Counter {
   // from here on only in tq_launch_counts_all
   kCntRouterScored, kCntRouterScoredBackward, kCntFp4Quantize, kCntFp4Dequantize, kCntFp4TileScales, kCntFp4Stage,
   kCntFp4Gemm, kCntFp4Combine, kCntFp4Swiglu, kCntFp4Gemv, kCntNorm, kCntNormBackward, kCntNormWeight, kCntFp8Quantize,
-  kCntFp8Dequantize, kCntFp8Gemm, kCntFewRows, kCntGatedGemm, kCntSwigluGrad, kCntNum
+  kCntFp8Dequantize, kCntFp8Gemm, kCntFewRows, kCntGatedGemm, kCntSwigluSum, kCntSwigluGrad, kCntNum
 };
 static_assert(kCntRouterScored == TQ_NUM_LAUNCH_COUNTERS, "counter layout of tq_launch_counts");
 static_assert(kCntNum == TQ_NUM_ALL_LAUNCH_COUNTERS, "counter layout of tq_launch_counts_all");
@@ -273,7 +273,8 @@ struct Fp8Gemm {
 };
 int launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s);
 
-// Product of 16-bit matrices, D[M][N] = A B^T over K (tq_tile_gemm.cuh).
+// Product of 16-bit matrices, D[M][N] = A B^T over K (tq_tile_gemm.cuh): gated; plain
+// (cols 64); or with b_mn.
 struct GemmF16 {
   int type;
   const void* a;                // [M][K], or [K][M] with a_mn
@@ -290,25 +291,26 @@ struct GemmF16 {
 };
 int launch_gemm_f16(const GemmF16& g, cudaStream_t s);
 
-// Products with few activation rows a matrix (tq_few_rows.cu); in 16 bits the gated one alone.
+// Products with few activation rows (tq_few_rows.cu): of one matrix (8 bits, or 16
+// gated), of pairs (ids; 8 bits gated), or of tokens (ids and topk_w; 8 bits).
 struct FewRows {
   const uint8_t* w;             // [E][N] rows, gated [2 N]
   const uint8_t* x;
   const float *w_scales, *x_scales;   // 8 bits
-  const int32_t *tiles, *num_tiles, *sorted_pairs;   // a unit = an m-tile
-  const int32_t* ids;           // without tiles: a unit = `segments` pairs of one row of the output
-  const float* topk_w;          // with segments: their weights
+  const int32_t* ids;           // [M][segments]
+  const float* topk_w;          // [M][segments]: y[m] = sum over segments of topk_w * W_ids x
   long long row_bytes, x_stride;   // bytes: of a row of w; between rows of x
-  int M, E, N, top_k, steps, w_blocks;   // M: slots, pairs, or (segments > 1) tokens
-  int segments;
-  int gather, scatter;          // as in Fp8Gemm; gather with segments: x holds token rows
-  void* y;
+  int M;                        // output rows
+  int E, N, top_k, steps, w_blocks;
+  int segments;                 // 1 but for tokens
+  int gather;                   // x holds a row per top_k output rows (pairs), per output row (tokens); else the segments' rows
+  void* y;                      // [M][N] of y_type
   int y_type;
-  float* gate_up;
+  float* gate_up;               // gated: fp32 [M][2 N], or nullptr
   int* err;
 };
-constexpr int kFewRowsFp8 = -1;   // `type` of the 8-bit product
-int launch_few_rows(const FewRows& p, int type, bool gated, int cols, int64_t units, cudaStream_t s);
+constexpr int kFewRowsFp8 = -1;   // `type` of the 8-bit products
+int launch_few_rows(const FewRows& p, int type, cudaStream_t s);
 
 // TQ_FORCE_ARM (auto|gemv|grouped|measured) applied to an automatic pin.
 int env_pin(int pin);

@@ -90,7 +90,8 @@ WRAPPER(tq_fp8_moe_forward, "ppppppliiiiplpip", PTR(0), PTR(1), PTR(2), PTR(3), 
         INT(8), INT(9), INT(10), PTR(11), (size_t)v[12], PTR(13), INT(14), STREAM(15))
 WRAPPER(tq_fp8_moe_mlp_forward, "ppppppppliiiiplpip", PTR(0), PTR(1), PTR(2), PTR(3), PTR(4), PTR(5), PTR(6),
         PTR(7), v[8], INT(9), INT(10), INT(11), INT(12), PTR(13), (size_t)v[14], PTR(15), INT(16), STREAM(17))
-WRAPPER(tq_swiglu_linear, "pilpliippp", PTR(0), INT(1), v[2], PTR(3), v[4], INT(5), INT(6), PTR(7), PTR(8), STREAM(9))
+WRAPPER(tq_swiglu_linear, "pilpliiplppp", PTR(0), INT(1), v[2], PTR(3), v[4], INT(5), INT(6), PTR(7), (size_t)v[8],
+        PTR(9), PTR(10), STREAM(11))
 WRAPPER(tq_swiglu_linear_backward, "pilpppliiplppp", PTR(0), INT(1), v[2], PTR(3), PTR(4), PTR(5), v[6], INT(7),
         INT(8), PTR(9), (size_t)v[10], PTR(11), PTR(12), STREAM(13))
 

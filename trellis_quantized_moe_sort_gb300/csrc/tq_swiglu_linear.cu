@@ -49,6 +49,39 @@ swiglu_grad_kernel(const float* __restrict__ gate_up, const T* __restrict__ grad
   }
 }
 
+// h (and gate and up) from the gate and up projections' partial sums, added in order: 4
+// columns a thread.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+swiglu_sum_kernel(const float* __restrict__ part, long long split_stride, int splits, long long rows, int I,
+                  T* __restrict__ h, float* __restrict__ gate_up) {
+  pdl_wait();
+  pdl_trigger();
+  const int items = I / 4;
+  const long long total = rows * items, step = static_cast<long long>(gridDim.x) * kThreads;
+  for (long long i = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x; i < total; i += step) {
+    const long long row = i / items, at = row * 2 * I + 4 * (i - row * items);
+    float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      const float4 a = __ldcs(reinterpret_cast<const float4*>(part + s * split_stride + at));
+      const float4 b = __ldcs(reinterpret_cast<const float4*>(part + s * split_stride + at + I));
+      g = make_float4(g.x + a.x, g.y + a.y, g.z + a.z, g.w + a.w);
+      u = make_float4(u.x + b.x, u.y + b.y, u.z + b.z, u.w + b.w);
+    }
+    if (gate_up) {
+      *reinterpret_cast<float4*>(gate_up + at) = g;
+      *reinterpret_cast<float4*>(gate_up + at + I) = u;
+    }
+    if (!h) continue;
+    const float gs[4] = {g.x, g.y, g.z, g.w}, us[4] = {u.x, u.y, u.z, u.w};
+    T out[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) out[j] = narrow<T>(gs[j] / (1.f + expf(-gs[j])) * us[j]);
+    *reinterpret_cast<uint2*>(h + 4 * i) = *reinterpret_cast<const uint2*>(out);
+  }
+}
+
 bool bad_sizes(int64_t n, int H, int I) {
   return n < 0 || n >= kMaxIndex || H < 8 || H % 8 != 0 || H >= kMaxIndex || I < 8 || I % 8 != 0 || 2ll * I >= kMaxIndex ||
          static_cast<double>(n) * H >= 0x1p57 || 2.0 * n * I >= 0x1p57 || 2.0 * I * H >= 0x1p57;
@@ -59,29 +92,73 @@ bool bad_x(const void* x, int64_t stride, int64_t n, int H) {
          stride >= (1ll << 38) || (n > 0 && (!x || !aligned(x, 16)));
 }
 
-constexpr int64_t kFewRowsMost = 16;
-
-int forward(const void* x, int type, int64_t x_stride, const void* w, int64_t n, int H, int I, void* h, float* gate_up,
-            int* err, cudaStream_t s) {
-  if (n <= kFewRowsMost) {
-    FewRows f{};
-    f.w = static_cast<const uint8_t*>(w);
-    f.x = static_cast<const uint8_t*>(x);
-    f.row_bytes = 2ll * H;
-    f.x_stride = 2 * x_stride;
-    f.M = static_cast<int>(n);
-    f.E = f.top_k = f.segments = 1;
-    f.N = I;
-    f.steps = (H + 63) / 64;
-    f.y = h;
-    f.y_type = type;
-    f.gate_up = gate_up;
-    f.err = err;
-    return launch_few_rows(f, type, true, n <= 8 ? 8 : 16, 1, s);
+// How gate, up and h are computed: by the few-rows kernel; in one launch of tiles; or,
+// where few rows make few tiles, in tiles with K split and a launch that adds up (128
+// rows 4096 -> 2 x 2048 took 25.7 us in one launch of 32 tiles).
+constexpr int64_t kFewRowsMost = 32;
+struct ForwardPlan {
+  bool few, split;
+  TileChoice tile;
+  size_t part;   // bytes of partial sums
+};
+ForwardPlan plan_forward(int64_t n, int H, int I) {
+  ForwardPlan f{};
+  f.few = n <= kFewRowsMost;
+  if (f.few) return f;
+  const int steps = (H + 63) / 64;
+  f.tile = choose_tile(static_cast<double>(n), 1.0, steps, I, true, TileRows::kOne, false, false);
+  const TileChoice plain = choose_tile(static_cast<double>(n), 1.0, steps, 2ll * I, false, TileRows::kOne, true, true, 64);
+  f.split = plain.cost < f.tile.cost;
+  if (f.split) {
+    f.tile = plain;
+    f.part = align256(static_cast<size_t>(plain.splits) * n * 2 * I * sizeof(float));
   }
-  const TileChoice t = choose_tile(static_cast<double>(n), 1.0, (H + 63) / 64, I, true, TileRows::kOne, false, false);
-  GemmF16 g{type, x, x_stride, w, H, n, I, H, false, false, true, t.tile_m, t.cols, 1, h, type, gate_up, err};
-  return launch_gemm_f16(g, s);
+  return f;
+}
+
+// Blocks of the kernels that walk rows * columns items.
+int walk_blocks(int64_t items) {
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((items + kThreads - 1) / kThreads, sm_count() * 16ll)));
+}
+
+int forward(const ForwardPlan& f, const void* x, int type, int64_t x_stride, const void* w, int64_t n, int H, int I,
+            void* part, void* h, float* gate_up, int* err, cudaStream_t s) {
+  if (f.few) {
+    FewRows r{};
+    r.w = static_cast<const uint8_t*>(w);
+    r.x = static_cast<const uint8_t*>(x);
+    r.row_bytes = 2ll * H;
+    r.x_stride = 2 * x_stride;
+    r.M = static_cast<int>(n);
+    r.E = r.top_k = r.segments = 1;
+    r.N = I;
+    r.steps = (H + 63) / 64;
+    r.y = h;
+    r.y_type = type;
+    r.gate_up = gate_up;
+    r.err = err;
+    return launch_few_rows(r, type, s);
+  }
+  GemmF16 g{type, x, x_stride, w, H, n, I, H, false, false, true, f.tile.tile_m, f.tile.cols, 1, h, type, gate_up, err};
+  if (!f.split) return launch_gemm_f16(g, s);
+  g.N = 2ll * I;
+  g.gated = false;
+  g.splits = f.tile.splits;
+  g.y = part;
+  g.y_type = TQ_FP32;
+  g.gate_up = nullptr;
+  int rc = launch_gemm_f16(g, s);
+  if (rc != TQ_OK) return rc;
+  const dim3 blocks(walk_blocks(n * (I / 4)));
+  const long long stride = 2ll * I * n;
+  rc = type == TQ_BF16 ? launch_pdl(swiglu_sum_kernel<__nv_bfloat16>, blocks, dim3(kThreads), 0, s,
+                                    static_cast<const float*>(part), stride, g.splits, static_cast<long long>(n), I,
+                                    static_cast<__nv_bfloat16*>(h), gate_up)
+                       : launch_pdl(swiglu_sum_kernel<__half>, blocks, dim3(kThreads), 0, s,
+                                    static_cast<const float*>(part), stride, g.splits, static_cast<long long>(n), I,
+                                    static_cast<__half*>(h), gate_up);
+  if (rc == TQ_OK) count_launch(kCntSwigluSum);
+  return rc;
 }
 
 // The two products of the gradient.
@@ -98,10 +175,12 @@ TileChoice at_least_64(TileChoice t) {   // operands across K come in boxes of 6
 
 struct GradPlan {
   TileChoice x, w;
+  ForwardPlan forward;   // of gate and up again
   size_t gate_up, d, part, bytes;   // offsets
 };
 GradPlan plan(int64_t n, int H, int I, bool has_gate_up) {
-  GradPlan p;
+  GradPlan p{};
+  if (!has_gate_up) p.forward = plan_forward(n, H, I);
   p.x = at_least_64(tile_x(n, H, I));
   p.w = at_least_64(tile_w(n, H, I));
   size_t used = 0;
@@ -114,7 +193,8 @@ GradPlan plan(int64_t n, int H, int I, bool has_gate_up) {
   p.d = take(2.0 * n * I, 2);
   const double sums_x = p.x.splits > 1 ? static_cast<double>(p.x.splits) * n * H : 0;
   const double sums_w = p.w.splits > 1 ? static_cast<double>(p.w.splits) * 2 * I * H : 0;
-  p.part = take(std::max(sums_x, sums_w), 4);   // in turn: the second product starts after the first's sums are read
+  // in turn: each product starts after the sums before it are read
+  p.part = take(std::max({sums_x, sums_w, static_cast<double>(p.forward.part / 4)}), 4);
   p.bytes = std::max<size_t>(used, 256);
   return p;
 }
@@ -138,17 +218,23 @@ using namespace tq;
 
 extern "C" {
 
-int tq_swiglu_linear(const void* x, int type, int64_t x_stride, const void* w_gu, int64_t n, int H, int I, void* h,
-                     float* gate_up, tq_stream_t stream) {
+size_t tq_swiglu_linear_workspace_size(int64_t n, int H, int I) {
+  return bad_sizes(n, H, I) ? 0 : std::max<size_t>(256, plan_forward(n, H, I).part);
+}
+
+int tq_swiglu_linear(const void* x, int type, int64_t x_stride, const void* w_gu, int64_t n, int H, int I, void* workspace,
+                     size_t workspace_bytes, void* h, float* gate_up, tq_stream_t stream) {
   if (bad_sizes(n, H, I) || bad_type16(type) || bad_x(x, x_stride, n, H)) return TQ_ERR_INVALID_ARG;
   if (n > 0 && (!w_gu || (!h && !gate_up) || !aligned(w_gu, 16) || !aligned(h, 16) || !aligned(gate_up, 16)))
     return TQ_ERR_INVALID_ARG;
+  const ForwardPlan f = plan_forward(n, H, I);
+  if (n > 0 && f.split && (!workspace || !aligned(workspace, 256) || workspace_bytes < f.part)) return TQ_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int rc = require_sm103(s);
   if (rc != TQ_OK || n == 0) return rc;
   int* err = error_word(&rc);
   if (!err) return rc;
-  return forward(x, type, x_stride, w_gu, n, H, I, h, gate_up, err, s);
+  return forward(f, x, type, x_stride, w_gu, n, H, I, workspace, h, gate_up, err, s);
 }
 
 size_t tq_swiglu_linear_backward_workspace_size(int64_t n, int H, int I, int has_gate_up) {
@@ -177,12 +263,12 @@ int tq_swiglu_linear_backward(const void* x, int type, int64_t x_stride, const v
   uint8_t* const base = static_cast<uint8_t*>(workspace);
   if (!gate_up) {
     float* const again = reinterpret_cast<float*>(base + p.gate_up);
-    rc = forward(x, type, x_stride, w_gu, n, H, I, nullptr, again, err, s);
+    rc = forward(p.forward, x, type, x_stride, w_gu, n, H, I, base + p.part, nullptr, again, err, s);
     if (rc != TQ_OK) return rc;
     gate_up = again;
   }
   void* const d = base + p.d;
-  const int blocks = static_cast<int>(std::min<int64_t>((n * (I / 8) + kThreads - 1) / kThreads, sm_count() * 16ll));
+  const int blocks = walk_blocks(n * (I / 8));
   rc = type == TQ_BF16
            ? launch_pdl(swiglu_grad_kernel<__nv_bfloat16>, dim3(blocks), dim3(kThreads), 0, s, gate_up,
                         static_cast<const __nv_bfloat16*>(grad_h), static_cast<long long>(n), I,

@@ -12,6 +12,7 @@ struct TileChoice {
   bool shared;  // two column blocks share the copies of their rows
   int cols;     // half the columns of a unit
   int splits;
+  double cost;
 };
 
 // What the rows of a product are: of one matrix; token rows of experts, gathered; or
@@ -30,7 +31,7 @@ enum class TileRows { kOne, kGathered, kSlots };
 // included), 142 by CTAs alone; 8192 tokens on 256 experts 4096 -> 2048 758 us by pairs
 // of pairs that share their rows, 695 by CTAs that do.
 inline TileChoice choose_tile(double rows, double matrices, int steps, int64_t N, bool gated, TileRows kind, bool partial,
-                              bool takes_splits) {
+                              bool takes_splits, int only_cols = 0) {
   struct Variant {
     int tile_m;
     bool shared;
@@ -44,11 +45,10 @@ inline TileChoice choose_tile(double rows, double matrices, int steps, int64_t N
                                           {128, false, 32, 500, 1650}};
   const int sms = sm_count();
   const double weights = matrices * N * (gated ? 2 : 1) * steps * 128.0 / 3400.0;
-  TileChoice best{128, false, 128, 1};
-  double best_cost = 1e300;
+  TileChoice best{128, false, 128, 1, 1e300};
   for (const Variant& v : kVariants) {
     if ((kind == TileRows::kOne) ? v.shared : v.tile_m > 128) continue;
-    if (gated && v.cols < 64) continue;
+    if ((gated && v.cols < 64) || (only_cols && (v.cols != only_cols || v.tile_m > 128))) continue;
     const int together = v.tile_m > 128 || v.shared ? 2 : 1;
     const double tiles = matrices * std::ceil(rows / v.tile_m);
     const double columns = (gated ? v.cols : 2 * v.cols) * (v.shared ? 2 : 1);
@@ -57,11 +57,8 @@ inline TileChoice choose_tile(double rows, double matrices, int steps, int64_t N
     for (int s = 1; s <= (takes_splits ? std::min(16, steps) : 1); ++s) {
       const double unit = ((steps + s - 1) / s) * step + 24.0 * v.cols + 1500.0;
       double cost = 4000.0 + std::max(std::ceil(units * s / (sms / together)) * unit, weights);
-      if (s > 1 || partial) cost += 5000.0 + 8.0 * s * rows * matrices * N / 3000.0;
-      if (cost < best_cost * 0.99) {
-        best = {v.tile_m, v.shared, v.cols, s};
-        best_cost = cost;
-      }
+      if (s > 1 || partial) cost += 9000.0 + 8.0 * s * rows * matrices * N / 3000.0;
+      if (cost < best.cost * 0.99) best = {v.tile_m, v.shared, v.cols, s, cost};
     }
   }
   return best;
