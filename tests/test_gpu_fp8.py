@@ -195,7 +195,7 @@ def _moe64(rows, values, ids, topk_w):
     return y, size
 
 
-MOE = [(1, 8, 2, 256, 128), (2, 16, 4, 128, 72), (7, 64, 6, 144, 130), (32, 64, 6, 512, 256), (64, 8, 2, 384, 257),
+MOE = [(900, 4, 2, 512, 700), (3, 256, 6, 1040, 272), (1, 8, 2, 256, 128), (2, 16, 4, 128, 72), (7, 64, 6, 144, 130), (32, 64, 6, 512, 256), (64, 8, 2, 384, 257),
        (50, 4, 1, 400, 100), (300, 8, 2, 256, 512), (1000, 4, 2, 272, 300), (700, 16, 3, 1024, 384), (129, 1, 1, 256, 256)]
 
 
@@ -285,7 +285,7 @@ def _mlp64(x64, gu, down, ids, topk_w):
     return y, slack
 
 
-MLP = [(1, 8, 2, 256, 128), (3, 16, 4, 144, 256), (40, 16, 3, 512, 384), (200, 4, 2, 272, 128), (600, 4, 2, 384, 640),
+MLP = [(1200, 4, 2, 256, 384), (2, 64, 6, 1040, 384), (1, 8, 2, 256, 128), (3, 16, 4, 144, 256), (40, 16, 3, 512, 384), (200, 4, 2, 272, 128), (600, 4, 2, 384, 640),
        (1500, 2, 1, 256, 256), (64, 1, 1, 1024, 512)]
 
 
@@ -348,6 +348,92 @@ def test_a_layer_in_a_graph_and_on_another_stream():
         for a, b in zip(want, got):
             for s, t in zip(a, b):
                 assert torch.equal(s, t)
+    check_no_device_error()
+
+
+def test_no_pair_in_range():
+    """Every id out of range: zeros, and an error that names the fault."""
+    rng = np.random.default_rng(13)
+    for n in (1, 300):
+        codes, scales = tq.tq_fp8_quantize(_x(rng, n, 256))
+        w, down = Weights(n, 4, 256, 256), Weights(n, 4, 256, 128)
+        ids = torch.full((n, 2), -1, dtype=torch.int32, device="cuda")
+        topk_w = torch.ones((n, 2), device="cuda")
+        assert (tq.tq_fp8_moe_forward(codes, scales, w.codes, w.scales, ids, topk_w) == 0).all()
+        torch.cuda.synchronize()
+        assert tq.tq_device_error()[0] == -1
+        assert (tq.tq_fp8_moe_mlp_forward(codes, scales, w.codes, w.scales, down.codes, down.scales, ids, topk_w) == 0).all()
+        torch.cuda.synchronize()
+        assert tq.tq_device_error()[0] == -1
+
+
+def test_arms():
+    """Few rows take the few-rows kernel, many the tiles; both sides of the change agree."""
+    rng = np.random.default_rng(17)
+    w = Weights(17, 1, 2048, 2048)
+    codes, scales = tq.tq_fp8_quantize(_x(rng, 300, 2048))
+    taken = {}
+    rows = {}
+    for n in (1, 8, 9, 32, 300):
+        before = tq.tq_launch_counts_all()
+        rows[n] = tq.tq_fp8_linear(codes[:n], scales[:n], w.codes[0], w.scales[0], dtype=torch.float32)
+        after = tq.tq_launch_counts_all()
+        taken[n] = tuple(after[c] - before[c] for c in ("few_rows", "fp8_gemm"))
+        assert sum(taken[n]) == 1
+    assert taken[1] == (1, 0) and taken[300] == (0, 1)
+    size = _rows64(codes, scales).abs() @ w.values[0].abs().t()
+    for n in (1, 8, 9, 32):
+        assert ((rows[n] - rows[300][:n]).abs() <= 2 * _roundings(2048) * size[:n] + 2.0 ** -23 * rows[n].abs()).all()
+    check_no_device_error()
+
+
+def test_two_streams_at_once():
+    """Calls that overlap, each with its own workspace and output, keep their results."""
+    rng = np.random.default_rng(19)
+    E, k, H, I, n = 8, 2, 512, 256, 400
+    gu, down = Weights(1, E, 2 * I, H), Weights(2, E, H, I)
+    inputs = []
+    for _ in range(2):
+        codes, scales = tq.tq_fp8_quantize(_x(rng, n, H))
+        inputs.append((codes, scales, gu.codes, gu.scales, down.codes, down.scales, *_routing(rng, n, E, k)))
+    want = [tq.tq_fp8_moe_mlp_forward(*a) for a in inputs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(tq.tq_fp8_moe_mlp_forward(*inputs[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for y in got[i]:
+            assert torch.equal(y, want[i])
+    check_no_device_error()
+
+
+def test_weights_past_four_gigabytes():
+    """The last experts of 4.9 GB of weights, by either arm, and codes past 2^32 bytes."""
+    E, N, K = 300, 4096, 4096
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of free device memory")
+    codes = torch.zeros((E, N, K), dtype=torch.uint8, device="cuda")
+    codes[E - 1] = torch.randint(0, 120, (N, K), dtype=torch.uint8, device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    scales = torch.full((E, N // 128, K // 128), 1.0 / 8192, device="cuda")
+    rng = np.random.default_rng(23)
+    for n in (1, 200):
+        x, xs = tq.tq_fp8_quantize(_x(rng, n, K))
+        ids = torch.stack((torch.full((n,), E - 1), torch.arange(n) % (E - 1)), 1).int().cuda()
+        topk_w = torch.ones((n, 2), device="cuda")
+        x64 = _rows64(x, xs)
+        values = codes[E - 1].view(torch.float8_e4m3fn).double() / 8192
+        want, size = x64 @ values.t(), x64.abs() @ values.abs().t()
+        _check(tq.tq_fp8_moe_forward(x, xs, codes, scales, ids, topk_w, dtype=torch.float32), want, size, K, "fp32", 2)
+    back = tq.tq_fp8_dequantize(codes, scales, 128, dtype=torch.bfloat16)
+    assert torch.equal(back[E - 1].double(), (codes[E - 1].view(torch.float8_e4m3fn).double() / 8192))
+    again, s = tq.tq_fp8_quantize(back, 128)
+    alone, s1 = tq.tq_fp8_quantize(back[E - 1].clone(), 128)
+    assert torch.equal(again[E - 1].view(torch.uint8), alone.view(torch.uint8)) and torch.equal(s[E - 1], s1)
+    assert (again[E - 2].view(torch.uint8) == 0).all()
     check_no_device_error()
 
 

@@ -42,10 +42,6 @@ struct Carver {
   }
 };
 
-// Rows that the few-rows kernel takes of one matrix: two passes over it (4096 -> 2048: 16
-// rows 6.0 us there and 9.7 in tiles; 17 and 32 FEW32).
-constexpr int kFewRowsMost = 32;
-
 struct LinearPlan {
   bool few;
   TileChoice tile;
@@ -54,11 +50,10 @@ struct LinearPlan {
 };
 LinearPlan plan_linear(void* base, int64_t n, int K, int N) {
   LinearPlan l{};
-  l.few = n <= kFewRowsMost;
   l.bytes = kNoWorkspace;
-  if (l.few) return l;
-  l.tile = choose_tile(static_cast<double>(n), 1.0, blocks_of(K), N, false, TileRows::kOne, false, true);
-  if (l.tile.splits > 1) {
+  l.tile = choose_tile(true, static_cast<double>(std::max<int64_t>(n, 1)), 1.0, blocks_of(K), N, false, TileRows::kOne, false, true);
+  l.few = few_rows_cost(n, static_cast<double>(N) * K, true) < l.tile.cost;
+  if (!l.few && l.tile.splits > 1) {
     Carver c{static_cast<uint8_t*>(base)};
     l.part = c.take<float>(static_cast<size_t>(l.tile.splits) * n * N);
     l.bytes = c.used;
@@ -92,7 +87,7 @@ double typical_rows(int64_t n, int top_k, int E) {
 TileChoice moe_tile(int64_t n, int top_k, int E, int steps, int N, bool gated, TileRows kind) {
   if (n == 0) return {128, false, 128, 1, 0.0};
   const double mean = tq_pairs_per_woken_expert(n, top_k, E);
-  return choose_tile(typical_rows(n, top_k, E), n * top_k / mean, steps, N, gated, kind, !gated, !gated);
+  return choose_tile(true, typical_rows(n, top_k, E), n * top_k / mean, steps, N, gated, kind, !gated, !gated);
 }
 
 struct Routed {

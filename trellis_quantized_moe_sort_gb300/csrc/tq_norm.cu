@@ -314,25 +314,25 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_kernel(const No
 }
 
 // grad_w[k] = the sum of the blocks' shares, in order: 32 columns a block, each of its
-// eight warps every eighth share.
-__global__ void __launch_bounds__(256) rms_norm_weight_kernel(const float* __restrict__ part, int shares, int K,
+// warps every 32nd share.
+__global__ void __launch_bounds__(1024) rms_norm_weight_kernel(const float* __restrict__ part, int shares, int K,
                                                               void* grad_w, int type) {
-  __shared__ float sums[8][32];
+  __shared__ float sums[32][33];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
+  int c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < K) {
 #pragma unroll 4
-    for (int b = warp; b < shares; b += 8) s += __ldcs(part + static_cast<long long>(b) * K + c);
+    for (int b = warp; b < shares; b += 32) s += __ldcs(part + static_cast<long long>(b) * K + c);
   }
   sums[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && c < K) {
-    s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s += sums[i][lane];
+  // warp w adds up column w
+  s = warp_sum(sums[lane][warp]);
+  c = blockIdx.x * 32 + warp;
+  if (lane == 0 && c < K) {
     if (type == TQ_FP32)
       static_cast<float*>(grad_w)[c] = s;
     else if (type == TQ_BF16)
@@ -411,7 +411,7 @@ int tq_rms_norm(const void* x, int x_type, int64_t x_stride, const void* residua
       !(eps <= FLT_MAX) || bad_rows(x, x_stride, n, K))
     return TQ_ERR_INVALID_ARG;
   if (residual && (bad_rows(residual, residual_stride, n, K) || (n > 0 && !residual_out))) return TQ_ERR_INVALID_ARG;
-  if (!residual && residual_out) return TQ_ERR_INVALID_ARG;
+  if ((!residual && residual_out) || (y && y == residual_out)) return TQ_ERR_INVALID_ARG;
   if (n > 0 && !y && !codes) return TQ_ERR_INVALID_ARG;
   if ((codes == nullptr) != (scales == nullptr)) return TQ_ERR_INVALID_ARG;
   const size_t size = type_size(x_type);
@@ -473,7 +473,7 @@ int tq_rms_norm_backward(const void* grad_y, int64_t grad_y_stride, const void* 
   if (rc != TQ_OK) return rc;
   count_launch(kCntNormBackward);
   if (!grad_weight) return TQ_OK;
-  rc = launch_pdl(rms_norm_weight_kernel, dim3((K + 31) / 32), dim3(256), 0, s, static_cast<const float*>(workspace),
+  rc = launch_pdl(rms_norm_weight_kernel, dim3((K + 31) / 32), dim3(1024), 0, s, static_cast<const float*>(workspace),
                   blocks, K, grad_weight, w_type);
   if (rc == TQ_OK) count_launch(kCntNormWeight);
   return rc;

@@ -95,7 +95,6 @@ bool bad_x(const void* x, int64_t stride, int64_t n, int H) {
 // How gate, up and h are computed: by the few-rows kernel; in one launch of tiles; or,
 // where few rows make few tiles, in tiles with K split and a launch that adds up (128
 // rows 4096 -> 2 x 2048 took 25.7 us in one launch of 32 tiles).
-constexpr int64_t kFewRowsMost = 32;
 struct ForwardPlan {
   bool few, split;
   TileChoice tile;
@@ -103,12 +102,11 @@ struct ForwardPlan {
 };
 ForwardPlan plan_forward(int64_t n, int H, int I) {
   ForwardPlan f{};
-  f.few = n <= kFewRowsMost;
-  if (f.few) return f;
   const int steps = (H + 63) / 64;
-  f.tile = choose_tile(static_cast<double>(n), 1.0, steps, I, true, TileRows::kOne, false, false);
-  const TileChoice plain = choose_tile(static_cast<double>(n), 1.0, steps, 2ll * I, false, TileRows::kOne, true, true, 64);
-  f.split = plain.cost < f.tile.cost;
+  f.tile = choose_tile(false, static_cast<double>(std::max<int64_t>(n, 1)), 1.0, steps, I, true, TileRows::kOne, false, false);
+  const TileChoice plain = choose_tile(false, static_cast<double>(std::max<int64_t>(n, 1)), 1.0, steps, 2ll * I, false, TileRows::kOne, true, true, 64);
+  f.few = few_rows_cost(n, 4.0 * I * H, false) < std::min(plain.cost, f.tile.cost);
+  f.split = !f.few && plain.cost < f.tile.cost;
   if (f.split) {
     f.tile = plain;
     f.part = align256(static_cast<size_t>(plain.splits) * n * 2 * I * sizeof(float));
@@ -163,10 +161,10 @@ int forward(const ForwardPlan& f, const void* x, int type, int64_t x_stride, con
 
 // The two products of the gradient.
 TileChoice tile_x(int64_t n, int H, int I) {
-  return choose_tile(static_cast<double>(n), 1.0, static_cast<int>((2ll * I + 63) / 64), H, false, TileRows::kOne, false, true);
+  return choose_tile(false, static_cast<double>(std::max<int64_t>(n, 1)), 1.0, static_cast<int>((2ll * I + 63) / 64), H, false, TileRows::kOne, false, true);
 }
 TileChoice tile_w(int64_t n, int H, int I) {
-  return choose_tile(2.0 * I, 1.0, static_cast<int>((n + 63) / 64), H, false, TileRows::kOne, false, true);
+  return choose_tile(false, 2.0 * I, 1.0, static_cast<int>((n + 63) / 64), H, false, TileRows::kOne, false, true);
 }
 TileChoice at_least_64(TileChoice t) {   // operands across K come in boxes of 64 columns
   t.cols = std::max(t.cols, 64);

@@ -30,30 +30,30 @@ enum class TileRows { kOne, kGathered, kSlots };
 // Measured: 8192 rows 4096 -> 4096 of one matrix 131 us by pairs (its quantising
 // included), 142 by CTAs alone; 8192 tokens on 256 experts 4096 -> 2048 758 us by pairs
 // of pairs that share their rows, 695 by CTAs that do.
-inline TileChoice choose_tile(double rows, double matrices, int steps, int64_t N, bool gated, TileRows kind, bool partial,
-                              bool takes_splits, int only_cols = 0) {
+inline TileChoice choose_tile(bool k8, double rows, double matrices, int steps, int64_t N, bool gated, TileRows kind,
+                              bool partial, bool takes_splits, int only_cols = 0) {
   struct Variant {
     int tile_m;
     bool shared;
     int cols;
-    double step, gathered;
+    double step, gathered, step16;
   };
-  static constexpr Variant kVariants[] = {{256, false, 128, 980, 0},
-                                          {128, true, 128, 980, 980},
-                                          {128, false, 128, 1000, 1650},
-                                          {128, false, 64, 660, 1650},
-                                          {128, false, 32, 500, 1650}};
+  static constexpr Variant kVariants[] = {{256, false, 128, 980, 0, 740},
+                                          {128, true, 128, 980, 980, 0},
+                                          {128, false, 128, 1000, 1650, 980},
+                                          {128, false, 64, 660, 1650, 660},
+                                          {128, false, 32, 500, 1650, 0}};
   const int sms = sm_count();
   const double weights = matrices * N * (gated ? 2 : 1) * steps * 128.0 / 3400.0;
   TileChoice best{128, false, 128, 1, 1e300};
   for (const Variant& v : kVariants) {
-    if ((kind == TileRows::kOne) ? v.shared : v.tile_m > 128) continue;
+    if (((kind == TileRows::kOne) ? v.shared : v.tile_m > 128) || (!k8 && v.step16 == 0)) continue;
     if ((gated && v.cols < 64) || (only_cols && (v.cols != only_cols || v.tile_m > 128))) continue;
     const int together = v.tile_m > 128 || v.shared ? 2 : 1;
     const double tiles = matrices * std::ceil(rows / v.tile_m);
     const double columns = (gated ? v.cols : 2 * v.cols) * (v.shared ? 2 : 1);
     const double units = tiles * std::ceil(static_cast<double>(N) / columns);
-    const double step = kind == TileRows::kGathered ? v.gathered : v.step;
+    const double step = !k8 ? v.step16 : kind == TileRows::kGathered ? v.gathered : v.step;
     for (int s = 1; s <= (takes_splits ? std::min(16, steps) : 1); ++s) {
       const double unit = ((steps + s - 1) / s) * step + 24.0 * v.cols + 1500.0;
       double cost = 4000.0 + std::max(std::ceil(units * s / (sms / together)) * unit, weights);
@@ -62,6 +62,17 @@ inline TileChoice choose_tile(double rows, double matrices, int steps, int64_t N
     }
   }
   return best;
+}
+
+// The same measure of the few-rows kernel, `bytes` of weights: 8 rows a pass, or 16 a
+// pass with twice the work.  Measured in 8 bits, 8, 16 and 32 rows: 4096 -> 2048 4.5, 6.2
+// and 7.9 us (tiles 9.5, 9.7, 9.4), 4096 -> 8192 11.5, 15.9 and 25.7 (13.5, 17.5, 12.8); in
+// 16 bits gated 4096 -> 2 x 2048 9.0, 10.7 and 16.4 (tiles with K split 13.4), 1024 -> 2 x
+// 512 2.8, 3.3 and 3.4 (12.8).
+inline double few_rows_cost(int64_t n, double bytes, bool k8) {
+  if (n > 256) return 1e300;
+  const double pass = n <= 8 ? (k8 ? 0.26 : 0.20) : (k8 ? 0.37 : 0.24) * static_cast<double>((n + 15) / 16);
+  return 1900.0 * (2.3 + pass * bytes * 1e-6);   // us per MB; cycles
 }
 
 }  // namespace tq
