@@ -11,7 +11,7 @@ Codes and scales: equal to those of fp32 arithmetic from the returned rstd.
 Gradient: rstd 2^-24, and per value a, x rstd, their difference, the products: below
 8 x 2^-24 of each of the terms added; the mean's sum of K values in a tree of at most
 16 + 10 additions: 26 x 2^-24 of the mean of magnitudes; then the type's rounding.
-grad_weight: rows in a chain of at most n / blocks + 8 + blocks / 8 additions of n
+grad_weight: rows in a chain of at most n / blocks + blocks / 32 + 5 additions of n
 values, at most n of them, each 2^-24 of the sum of magnitudes."""
 import numpy as np
 import pytest

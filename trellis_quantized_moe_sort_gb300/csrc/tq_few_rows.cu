@@ -15,9 +15,12 @@
 // shared memory in a fixed order.  Blocks walk their share of the units (a group of
 // rows x 16 weight rows), each warp with its next blocks of weights under way, across
 // units too.  A step costs about 200 instructions of a warp (the 8-bit MMAs are
-// expanded into conversions and 16-bit ones): 55 to 75% of the memory's rate; from
-// where experts share tokens on the tensor-memory tiles are faster (16 tokens of top-6 of
-// 256, 4096 -> 2048: 156 us here, 138 there).
+// expanded into conversions and 16-bit ones), and a unit of 32 steps gives a warp four
+// between two barriers.  Measured, six experts of one token, 8 bits: gated 4096 -> 2 x
+// 2048 25 us (100 MB, 60% of the measured copy rate, 47% of the issue slots; 1536 units on
+// 304 blocks), 2048 -> 4096 weighted and added 18 us (50 MB, 43%: a unit a block, so its
+// start and its last sums show).  From where experts share tokens on the tensor-memory
+// tiles are faster (16 tokens of top-6 of 256, 4096 -> 2048: 156 us here, 138 there).
 //
 // A single token's experts are the segments of one unit, whose sums, weighted, add up
 // in the same registers: its product is this one launch.

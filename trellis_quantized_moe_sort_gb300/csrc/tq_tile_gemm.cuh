@@ -6,7 +6,8 @@
 // of its K range.  Persistent CTAs, one per SM, walk the units.  One warp loads A
 // and one B, per step of 128 bytes along K, in 128-byte swizzled boxes; a third
 // issues four MMAs a step; eight epilogue warps drain tensor memory, lane = row,
-// two warps (kCols columns each) per 32 rows.
+// two warps (kCols columns each) per 32 rows.  Warps 0-3 load A, load B, issue MMAs and
+// load A's gathered rows; 4-11 are the epilogue.
 //
 // 8-bit products: a step is one block of 128 values, whose two scales multiply its
 // partial sums.  Each step accumulates into an accumulator of its own; the epilogue
@@ -14,11 +15,17 @@
 // rows as lanes the scale of a step is one register of each thread; with columns
 // holding the activation rows it would be a shared-memory read per column and step,
 // on the port that feeds the MMAs.  The registers of 256 columns need the uneven
-// register split of setmaxnreg.
+// register split of setmaxnreg.  Measured: 8192 rows 4096 -> 4096 116 us (2.4 PFLOP/s),
+// the tensor pipe at 55%: a step of 256 x 256 takes 980 cycles where its MMAs take 512,
+// the copies and the hand-over of accumulators alone 865, and the epilogue's reads of
+// tensor memory and additions stand out by the rest.  Sixteen epilogue warps of 64 sums
+// took 134 us where these eight of 128 take 121.
 //
 // 16-bit products accumulate their whole K range in tensor memory.  Their operands
 // may be stored with K as the slow axis (kAMn, kBMn: the gradients' transposed
-// reads), as boxes of 64 columns x 64 rows of K.
+// reads), as boxes of 64 columns x 64 rows of K.  Measured, 8192 rows 4096 -> 2 x 2048:
+// forward with gate and up kept 158 us (83% of the tensor pipe), grad_x 144 (91%) and
+// grad_w 165 (93%), at 1.75 GHz under the power limit.
 //
 // A pair shares one MMA of 256 rows and halves B: 32 KB a CTA and step for 128 x 256
 // results, in place of 48.  Experts' rows fill tiles of 128 better than of 256, and the
@@ -44,11 +51,11 @@ constexpr int kRows = 128;                    // rows of A per CTA
 constexpr int kStepBytes = 128;               // of a row and step: one swizzle row
 constexpr int kABytes = kRows * kStepBytes;
 constexpr int kMaxStages = 12, kMaxAcc = 8;
-constexpr int kThreads = 384;                 // warps 0-3: load A, load B, MMA, load A's gathered rows; 4-11: epilogue
+constexpr int kThreads = 384;
 constexpr int kWarpA = 0, kWarpB = 1, kWarpMma = 2, kWarpA2 = 3, kWarpEpi0 = 4, kEpiWarps = 8;
 constexpr int kSmemLimit = 232448;
 constexpr int kNumBars = 2 * kMaxStages + 2 * kMaxAcc + 1;
-constexpr int kPitch = 33;                    // floats per row of an epilogue warp's 32 x 32 turning block (or 32 x 128 bytes)
+constexpr int kPitch = 33;                    // floats per row of an epilogue warp's 32 x 32 turning block
 constexpr int kTurnBytes = kEpiWarps * 32 * kPitch * 4;
 constexpr int kListBytes = kRows * 4;         // rows of A that a CTA gathers
 constexpr int kTopBytes = 2 * 2 * kRows * 4;  // two buffers of both column halves' largest magnitudes
@@ -74,11 +81,10 @@ struct Params {
   const int32_t* tiles;         // {e, slot0, rows}, or nullptr: tile i = rows [i * tile_m, ...) of matrix 0
   const int32_t* num_tiles;
   const int32_t* sorted_pairs;  // with tiles: the pair of a slot
-  int gather;                   // A's row of a slot is token pair / top_k, else the slot
+  int gather;                   // (not by pairs) A's row of a slot is token pair / top_k, else the slot
   int scatter;                  // the output row of a slot is its pair, else the slot
   long long cap, split_stride;
   int M, E, N, tile_m, top_k;   // M: slots, or rows of A; N: columns (of h, when gated)
-  int tokens;                   // rows of x that are gathered from
   int col_blocks, steps, splits;
   // scales of 8-bit operands
   const float* a_scales;        // [rows of A][steps]
@@ -179,20 +185,8 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* m, int
   else
     tma_load_2d(dst, m, x, y, bar);
 }
-template <bool kPair>
-__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* m, int32_t x, int4 r, uint32_t bar) {
-  if constexpr (kPair)
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
-        : "memory");
-  else
-    tma_gather4_2d(dst, m, x, r.x, r.y, r.z, r.w, bar);
-}
-
-// The same to both CTAs of a cluster, at the same place in each; the bytes count on the
-// barrier at the same place in each.
+// A box, or four gathered rows, to both CTAs of a cluster, at the same place in each; the
+// bytes count on the barrier at the same place in each.
 __device__ __forceinline__ void load_box_to_both(uint32_t dst, const CUtensorMap* m, int32_t x, int32_t y, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
@@ -341,11 +335,9 @@ __device__ __forceinline__ int pair_of(const Params& p, int slot, int where) {
   return -1;
 }
 
-// Copies of four rows that CTA `rank` gathers of a tile's rows, and how many of `n`
-// copies a warp takes: `share` from the lead-th of every eight.
-__device__ __forceinline__ int gathered(int rows, int rank) {
-  return (max(0, min(kRows, rows - rank * kRows)) + 3) / 4;
-}
+// Copies of four rows that a tile's gathered rows take, and how many of `n` copies a warp
+// takes: `share` from the lead-th of every eight.
+__device__ __forceinline__ int gathered(int rows) { return (min(kRows, rows) + 3) / 4; }
 // Of those, the part that one of two CTAs gathers for both.
 __device__ __forceinline__ int part_of(int copies, int sharer) {
   return max(0, min(kRows / 8, copies - sharer * (kRows / 8)));
@@ -359,17 +351,17 @@ __device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
 // thread and unit took 11000 cycles with expf and a division, while the MMAs waited.
 __device__ __forceinline__ float silu_fast(float g) { return __fdividef(g, 1.f + __expf(-g)); }
 
-// kCount values of this lane's row to columns [col, col + kCount) of y, those below N;
-// `row` < 0: none.  A lane's own stores would be 32 rows' sectors an instruction (128 x
-// 256 results a CTA: 4000 cycles), so the warp turns blocks of 32 rows x 128 bytes in
-// shared memory and stores whole lines of them, 16 bytes a lane.  Rows that do not
-// start on 16-byte boundaries are turned by single values, 32 columns at a time.
-// Output rows of a warp's 32: of lane l, `row`; where they are first + l * step for l <
-// live, step is not 0.
+// Output rows of a warp's 32: of lane l, `row`, < 0: none; where they are first + l * step
+// for l < live, step is not 0.
 struct Rows {
   long long row, first;
   int step, live;
 };
+// kCount values of this lane's row to columns [col, col + kCount) of y, those below N.
+// A lane's own stores would be 32 rows' sectors an instruction (128 x 256 results a CTA:
+// 4000 cycles), so the warp turns blocks of 32 rows x 128 bytes in shared memory and
+// stores whole lines of them, 16 bytes a lane.  Rows that do not start on 16-byte
+// boundaries are turned by single values, 32 columns at a time.
 template <typename T, int kCount>
 __device__ __forceinline__ void store_columns(T* y, const float (&v)[kCount], const Rows& rows, int col, int N, bool aligned,
                                               uint8_t* turn, int lane) {
@@ -469,6 +461,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
   const int cta = kGroup != kAlone ? static_cast<int>(cluster_rank()) : 0;
   const int rank = kPair ? cta : 0, sharer = kShared ? cta : 0;
   const bool first = rank == 0;   // of a pair: the barriers that the MMA waits for are its
+  const bool gather = !kPair && p.gather;
 
   const uint32_t bar_full = base + p.off_bar;
   const uint32_t bar_empty = bar_full + 8 * kMaxStages;
@@ -480,7 +473,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
-      mbar_init(bar_full + 8 * s, p.gather ? 3 : 2);
+      mbar_init(bar_full + 8 * s, gather ? 3 : 2);
       mbar_init(bar_empty + 8 * s, kShare);   // the MMAs of every CTA that a copy writes to
     }
     for (int a = 0; a < p.accs; ++a) {
@@ -511,182 +504,180 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
   int* const err = p.err;
 
   if (warp < kWarpEpi0) {
-  if constexpr (kSplitRegisters) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-  if (warp != kWarpMma && (warp != kWarpA2 || p.gather)) {
-    // The whole warp walks the steps, so that addresses stay in uniform registers;
-    // one elected thread issues (a loop that only it walks takes about 100 cycles a
-    // copy).  Gathered rows come four to a copy, and a copy takes about 80 cycles of a
-    // warp: three warps share them, in every eight copies three, two (beside B's box)
-    // and three, none for the rows past the tile, whose results are not stored (8192
-    // tokens of top-6 of 256, 4096 -> 2048, in pairs of CTAs: 1113 us by one warp, 744 by
-    // two, 716 so).
-    const bool is_b = warp == kWarpB;
-    const int lead = is_b ? 3 : warp == kWarpA ? 0 : 5, share = is_b ? 2 : 3;
-    int* const list = reinterpret_cast<int*>(gbase + p.off_list);
-    const uint32_t full0 = kPair ? of_cta(bar_full, 0) : bar_full;
-    const bool leader = elect_one();
-    Ring ring;
-    long long issued = 0;
-    bool ok = true, ready = false;
-    for (long long u = unit0; ok && u < units; u += unit_step) {
-      const Unit t = unit_at<kShare>(p, u, num_tiles, col_units, sharer);
-      if (!t.ok) {
-        if (is_b && first && leader) record_error(err, TQ_ERR_INVALID_ARG, kWhereTileLoad);
-        continue;
-      }
-      const int row0 = t.slot0 + rank * kRows;
-      // this CTA's copies of four rows, and the bytes of this warp's copies (of a pair: in both CTAs)
-      const int copies = gathered(t.rows, rank);
-      uint32_t bytes = static_cast<uint32_t>(is_b ? kBBytes : 0) * (kPair ? 2 : 1);
-      if (p.gather) {
-#pragma unroll
-        for (int r = 0; r < (kPair ? 2 : 1); ++r) {
+    if constexpr (kSplitRegisters) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp != kWarpMma && (warp != kWarpA2 || gather)) {
+      // The whole warp walks the steps, so that addresses stay in uniform registers;
+      // one elected thread issues (a loop that only it walks takes about 100 cycles a
+      // copy).  Gathered rows come four to a copy, and a copy takes about 80 cycles of a
+      // warp: three warps share them, in every eight copies three, two (beside B's box)
+      // and three, none for the rows past the tile, whose results are not stored (8192
+      // tokens of top-6 of 256, 4096 -> 2048, in pairs of CTAs: 1113 us by one warp, 744 by
+      // two, 716 so).
+      const bool is_b = warp == kWarpB;
+      const int lead = is_b ? 3 : warp == kWarpA ? 0 : 5, share = is_b ? 2 : 3;
+      int* const list = reinterpret_cast<int*>(gbase + p.off_list);
+      const uint32_t full0 = kPair ? of_cta(bar_full, 0) : bar_full;
+      const bool leader = elect_one();
+      Ring ring;
+      long long issued = 0;
+      bool ok = true, ready = false;
+      for (long long u = unit0; ok && u < units; u += unit_step) {
+        const Unit t = unit_at<kShare>(p, u, num_tiles, col_units, sharer);
+        if (!t.ok) {
+          if (is_b && first && leader) record_error(err, TQ_ERR_INVALID_ARG, kWhereTileLoad);
+          continue;
+        }
+        const int row0 = t.slot0 + rank * kRows;
+        // a tile's copies of four gathered rows, and the bytes of this warp's copies (of a pair,
+        // whose rows lie together: in both CTAs)
+        const int copies = gathered(t.rows);
+        uint32_t bytes = static_cast<uint32_t>(is_b ? kBBytes : 0) * (kPair ? 2 : 1);
+        if (gather) {
           if (kShared)
-            bytes += 4 * kStepBytes * (shared_copies(part_of(gathered(t.rows, r), 0), lead, share) +
-                                       shared_copies(part_of(gathered(t.rows, r), 1), lead, share));
+            bytes += 4 * kStepBytes * (shared_copies(part_of(copies, 0), lead, share) +
+                                       shared_copies(part_of(copies, 1), lead, share));
           else
-            bytes += 4 * kStepBytes * shared_copies(gathered(t.rows, r), lead, share);
-        }
-        __syncwarp();
-        for (int i = lane; i < 16 * share; i += 32) {
-          const int in = 32 * (i / (4 * share)) + 4 * lead + i % (4 * share);   // row of this CTA
-          const int pair = __ldg(p.sorted_pairs + t.slot0 + min(rank * kRows + in, t.rows - 1));
-          list[in] = pair >= 0 && pair < p.M ? pair / p.top_k : 0;   // the epilogue reports and skips a bad pair
-        }
-        __syncwarp();
-      } else if (!is_b) {
-        bytes = kABytes * (kPair ? 2 : 1);
-      }
-      // column of D of this CTA's first box, and the second's distance from it
-      const int col = t.cb * (kGated ? kCols : kN);
-      const int second = kGated ? p.N : kCols;
-      const int b_row = (kBMn ? 0 : t.e * (kGated ? 2 * p.N : p.N)) + col;
-      for (int k = t.k0; k < t.k1; ++k) {
-        if (!ready && !mbar_wait_short(bar_empty + 8 * ring.at, ring.phase ^ 1u, abort_flag, err, kWhereTileLoad)) {
-          ok = false;
-          break;
-        }
-        const uint32_t full = full0 + 8 * ring.at;
-        const uint32_t dst = base + static_cast<uint32_t>(ring.at * kStageBytes);
-        const int at = k * kStepValues;
-        if (leader) {
-          if (first) mbar_arrive_expect_tx(bar_full + 8 * ring.at, bytes);
-          if (is_b) {
-#pragma unroll
-            for (int i = 0; i < kBBoxes; ++i) {
-              const int c = (kPair ? rank * kCols : 0) + i * kBoxRows;   // column of the MMA's N
-              const int row = kGated ? b_row + (c >= kCols ? second : 0) + c % kCols : b_row + c;
-              load_box<kPair>(dst + kABytes + i * kBoxRows * kStepBytes, &tm_b, kBMn ? row : at, kBMn ? at : row, full);
-            }
+            bytes += 4 * kStepBytes * shared_copies(copies, lead, share);
+          __syncwarp();
+          for (int i = lane; i < 16 * share; i += 32) {
+            const int in = 32 * (i / (4 * share)) + 4 * lead + i % (4 * share);   // row of the tile
+            const int pair = __ldg(p.sorted_pairs + t.slot0 + min(in, t.rows - 1));
+            list[in] = pair >= 0 && pair < p.M ? pair / p.top_k : 0;   // the epilogue reports and skips a bad pair
           }
-          if (p.gather) {
+          __syncwarp();
+        } else if (!is_b) {
+          bytes = kABytes * (kPair ? 2 : 1);
+        }
+        // column of D of this CTA's first box, and the second's distance from it
+        const int col = t.cb * (kGated ? kCols : kN);
+        const int second = kGated ? p.N : kCols;
+        const int b_row = (kBMn ? 0 : t.e * (kGated ? 2 * p.N : p.N)) + col;
+        for (int k = t.k0; k < t.k1; ++k) {
+          if (!ready && !mbar_wait_short(bar_empty + 8 * ring.at, ring.phase ^ 1u, abort_flag, err, kWhereTileLoad)) {
+            ok = false;
+            break;
+          }
+          const uint32_t full = full0 + 8 * ring.at;
+          const uint32_t dst = base + static_cast<uint32_t>(ring.at * kStageBytes);
+          const int at = k * kStepValues;
+          if (leader) {
+            if (first) mbar_arrive_expect_tx(bar_full + 8 * ring.at, bytes);
+            if (is_b) {
 #pragma unroll
-            for (int j = 0; j < kRows / (4 * kShare); j += 8) {
-#pragma unroll
-              for (int i = 0; i < 3; ++i) {
-                const int c = sharer * (kRows / 8) + j + lead + i;
-                if (i < share && c < copies) {
-                  const int4 rows = *reinterpret_cast<const int4*>(list + 4 * c);
-                  if constexpr (kShared)
-                    load_rows_to_both(dst + 4 * c * kStepBytes, &tm_a, at, rows, full);
-                  else
-                    load_rows<kPair>(dst + 4 * c * kStepBytes, &tm_a, at, rows, full);
-                }
+              for (int i = 0; i < kBBoxes; ++i) {
+                const int c = (kPair ? rank * kCols : 0) + i * kBoxRows;   // column of the MMA's N
+                const int row = kGated ? b_row + (c >= kCols ? second : 0) + c % kCols : b_row + c;
+                load_box<kPair>(dst + kABytes + i * kBoxRows * kStepBytes, &tm_b, kBMn ? row : at, kBMn ? at : row, full);
               }
             }
-          } else if (kShared && !is_b) {
-            load_box_to_both(dst + 8192 * sharer, &tm_a, at, row0 + 64 * sharer, full);
-          } else if (!is_b) {
+            if (gather) {
 #pragma unroll
-            for (int i = 0; i < kABoxes; ++i)
-              load_box<kPair>(dst + i * 8192, &tm_a, kAMn ? row0 + 64 * i : at, kAMn ? at : row0, full);
+              for (int j = 0; j < kRows / (4 * kShare); j += 8) {
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                  const int c = sharer * (kRows / 8) + j + lead + i;
+                  if (i < share && c < copies) {
+                    const int4 rows = *reinterpret_cast<const int4*>(list + 4 * c);
+                    if constexpr (kShared)
+                      load_rows_to_both(dst + 4 * c * kStepBytes, &tm_a, at, rows, full);
+                    else
+                      tma_gather4_2d(dst + 4 * c * kStepBytes, &tm_a, at, rows.x, rows.y, rows.z, rows.w, full);
+                  }
+                }
+              }
+            } else if (kShared && !is_b) {
+              load_box_to_both(dst + 8192 * sharer, &tm_a, at, row0 + 64 * sharer, full);
+            } else if (!is_b) {
+#pragma unroll
+              for (int i = 0; i < kABoxes; ++i)
+                load_box<kPair>(dst + i * 8192, &tm_a, kAMn ? row0 + 64 * i : at, kAMn ? at : row0, full);
+            }
+          }
+          ++issued;
+          ring.advance(stages);
+          ready = mbar_test(bar_empty + 8 * ring.at, ring.phase ^ 1u);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (leader) {
+        // Before the CTA exits, every copy issued has landed (of a pair: in both
+        // CTAs, counted on the first's barriers) and every arrival that the MMAs owe its
+        // barriers; the empty ones, whose MMAs waited for the copies, tell both.
+        const long long pending = min(issued, static_cast<long long>(stages));
+        for (long long i = 1; i <= pending; ++i) {
+          int st = ring.at - static_cast<int>(i);
+          uint32_t ph = ring.phase;
+          if (st < 0) {
+            st += stages;
+            ph ^= 1u;
+          }
+          const uint64_t t0 = globaltimer();
+          while (!mbar_try_wait(bar_empty + 8 * st, ph)) {
+            if (globaltimer() - t0 > kWaitTimeoutNs) {
+              record_error(err, TQ_ERR_DEVICE_TIMEOUT, kWhereTileTeardown);
+              break;
+            }
           }
         }
-        ++issued;
-        ring.advance(stages);
-        ready = mbar_test(bar_empty + 8 * ring.at, ring.phase ^ 1u);
       }
-      ok = __all_sync(0xffffffffu, ok);
-    }
-    if (leader) {
-      // Before the CTA exits, every copy issued has landed (of a pair: in both
-      // CTAs, counted on the first's barriers) and every arrival that the MMAs owe its
-      // barriers; the empty ones, whose MMAs waited for the copies, tell both.
-      const long long pending = min(issued, static_cast<long long>(stages));
-      for (long long i = 1; i <= pending; ++i) {
-        int st = ring.at - static_cast<int>(i);
-        uint32_t ph = ring.phase;
-        if (st < 0) {
-          st += stages;
-          ph ^= 1u;
+      __syncwarp();
+    } else if (warp == kWarpMma && first) {
+      // The whole warp walks the steps, so that addresses stay in uniform registers;
+      // one elected thread issues.
+      const uint32_t idesc = instruction<k8>(p.type, kPair ? 2 * kRows : kRows, kN, kAMn, kBMn);
+      const uint32_t desc0 = (base & 0x3FFFFu) >> 4, bar_end = bar_full + 8 * stages;
+      uint32_t desc = desc0, bar = bar_full, phase = 0;
+      bool ready = false;
+      const bool leader = elect_one();
+      Ring acc;
+      for (long long u = unit0; u < units; u += unit_step) {
+        const Unit t = unit_at<kShare>(p, u, num_tiles, col_units, sharer);
+        if (!t.ok) continue;
+        for (int k = t.k0; k < t.k1; ++k) {
+          if (k8 || k == t.k0) {
+            mbar_wait_short(bar_accempty + 8 * acc.at, acc.phase ^ 1u, abort_flag, err, kWhereTileMma);
+            tc_fence_after();
+          }
+          const uint32_t d = tmem + static_cast<uint32_t>(acc.at * kN);
+          if (!ready) mbar_wait_short(bar, phase, abort_flag, err, kWhereTileMma);
+          const uint32_t this_bar = bar, this_desc = desc;
+          desc += kStageBytes / 16;
+          bar += 8;
+          if (bar == bar_end) {
+            desc = desc0;
+            bar = bar_full;
+            phase ^= 1u;
+          }
+          ready = mbar_test(bar, phase);
+          const bool last = k8 || k == t.k1 - 1;
+          if (leader) {
+            const uint64_t a = operand<kAMn>(this_desc), b = operand<kBMn>(this_desc + kABytes / 16);
+            // K of an MMA: 32 bytes along a row, or 16 rows of 128
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma<k8, kPair>(d, a + i * (kAMn ? 128 : 2), b + i * (kBMn ? 128 : 2), idesc,
+                             (i != 0 || (!k8 && k != t.k0)) ? 1u : 0u);
+            commit<kPair, kShared>(this_bar + 8 * kMaxStages);   // the stage's empty barrier
+            if (last) commit<kPair, false>(bar_accfull + 8 * acc.at);
+          }
+          if (last) acc.advance(accs);
+          if (*abort_flag) break;
         }
+        if (*abort_flag) break;
+      }
+      __syncwarp();
+      if (elect_one()) {   // every MMA issued has completed before teardown
+        commit_own<kPair>(bar_drain);
         const uint64_t t0 = globaltimer();
-        while (!mbar_try_wait(bar_empty + 8 * st, ph)) {
+        while (!mbar_try_wait(bar_drain, 0)) {
           if (globaltimer() - t0 > kWaitTimeoutNs) {
             record_error(err, TQ_ERR_DEVICE_TIMEOUT, kWhereTileTeardown);
             break;
           }
         }
       }
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp == kWarpMma && first) {
-    // The whole warp walks the steps, so that addresses stay in uniform registers;
-    // one elected thread issues.
-    const uint32_t idesc = instruction<k8>(p.type, kPair ? 2 * kRows : kRows, kN, kAMn, kBMn);
-    const uint32_t desc0 = (base & 0x3FFFFu) >> 4, bar_end = bar_full + 8 * stages;
-    uint32_t desc = desc0, bar = bar_full, phase = 0;
-    bool ready = false;
-    const bool leader = elect_one();
-    Ring acc;
-    for (long long u = unit0; u < units; u += unit_step) {
-      const Unit t = unit_at<kShare>(p, u, num_tiles, col_units, sharer);
-      if (!t.ok) continue;
-      for (int k = t.k0; k < t.k1; ++k) {
-        if (k8 || k == t.k0) {
-          mbar_wait_short(bar_accempty + 8 * acc.at, acc.phase ^ 1u, abort_flag, err, kWhereTileMma);
-          tc_fence_after();
-        }
-        const uint32_t d = tmem + static_cast<uint32_t>(acc.at * kN);
-        if (!ready) mbar_wait_short(bar, phase, abort_flag, err, kWhereTileMma);
-        const uint32_t this_bar = bar, this_desc = desc;
-        desc += kStageBytes / 16;
-        bar += 8;
-        if (bar == bar_end) {
-          desc = desc0;
-          bar = bar_full;
-          phase ^= 1u;
-        }
-        ready = mbar_test(bar, phase);
-        const bool last = k8 || k == t.k1 - 1;
-        if (leader) {
-          const uint64_t a = operand<kAMn>(this_desc), b = operand<kBMn>(this_desc + kABytes / 16);
-          // K of an MMA: 32 bytes along a row, or 16 rows of 128
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma<k8, kPair>(d, a + i * (kAMn ? 128 : 2), b + i * (kBMn ? 128 : 2), idesc,
-                           (i != 0 || (!k8 && k != t.k0)) ? 1u : 0u);
-          commit<kPair, kShared>(this_bar + 8 * kMaxStages);   // the stage's empty barrier
-          if (last) commit<kPair, false>(bar_accfull + 8 * acc.at);
-        }
-        if (last) acc.advance(accs);
-        if (*abort_flag) break;
-      }
-      if (*abort_flag) break;
-    }
-    __syncwarp();
-    if (elect_one()) {   // every MMA issued has completed before teardown
-      commit_own<kPair>(bar_drain);
-      const uint64_t t0 = globaltimer();
-      while (!mbar_try_wait(bar_drain, 0)) {
-        if (globaltimer() - t0 > kWaitTimeoutNs) {
-          record_error(err, TQ_ERR_DEVICE_TIMEOUT, kWhereTileTeardown);
-          break;
-        }
-      }
-    }
-    __syncwarp();
-  }
   } else {
     if constexpr (kSplitRegisters) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int q = warp & 3, half = (warp - kWarpEpi0) >> 2;
@@ -706,14 +697,14 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
       const int in_tile = rank * kRows + 32 * q + lane;
       const int slot = t.slot0 + min(in_tile, t.rows - 1);
       int pair = slot;
-      if (p.gather || p.scatter) pair = pair_of(p, slot, kWhereTileEpilogue);
+      if (gather || p.scatter) pair = pair_of(p, slot, kWhereTileEpilogue);
       const bool live = in_tile < t.rows && pair >= 0;
       const int first_row = t.slot0 + rank * kRows + 32 * q;
       const Rows out_row{!live ? -1 : p.scatter ? pair : slot, first_row, p.scatter ? 0 : 1,
                          max(0, min(32, t.slot0 + t.rows - first_row))};
       bool ok = true;
       if constexpr (k8) {
-        const int a_row = p.gather ? max(pair, 0) / p.top_k : slot;
+        const int a_row = gather ? max(pair, 0) / p.top_k : slot;
         const float* sa = p.a_scales + static_cast<long long>(a_row) * p.steps + t.k0;
         // the blocks of this thread's columns; past the matrix the last one (nothing of it is stored)
         const int col = t.cb * (kGated ? kCols : kN);
