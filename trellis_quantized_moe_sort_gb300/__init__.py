@@ -695,18 +695,8 @@ def _type_code(dtype, name):
     return code
 
 
-_device_fn = None
-
-
 def _current_device():
-    """The current device, by the C-level getter where this torch build has it (half
-    the public one's time, once that has set CUDA up)."""
-    global _device_fn
-    if _device_fn is None:
-        torch = _torch()
-        torch.cuda.current_device()
-        _device_fn = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-    return _device_fn()
+    return _torch().cuda.current_device()
 
 
 def _elsewhere(t, device, name):
