@@ -196,7 +196,9 @@ def _moe64(rows, values, ids, topk_w):
 
 
 MOE = [(900, 4, 2, 512, 700), (3, 256, 6, 1040, 272), (1, 8, 2, 256, 128), (2, 16, 4, 128, 72), (7, 64, 6, 144, 130), (32, 64, 6, 512, 256), (64, 8, 2, 384, 257),
-       (50, 4, 1, 400, 100), (300, 8, 2, 256, 512), (1000, 4, 2, 272, 300), (700, 16, 3, 1024, 384), (129, 1, 1, 256, 256)]
+       (50, 4, 1, 400, 100), (300, 8, 2, 256, 512), (1000, 4, 2, 272, 300), (700, 16, 3, 1024, 384), (129, 1, 1, 256, 256),
+       (3000, 16, 2, 144, 130), (2500, 4, 1, 400, 100), (1100, 300, 3, 272, 257), (700, 64, 6, 1040, 640), (4000, 8, 1, 16, 33),
+       (64, 8, 2, 4096, 1025), (20, 4, 2, 4112, 2050), (300, 16, 2, 512, 1000)]
 
 
 @pytest.mark.parametrize("skew", [0.0, 3.0])
@@ -286,7 +288,8 @@ def _mlp64(x64, gu, down, ids, topk_w):
 
 
 MLP = [(1200, 4, 2, 256, 384), (2, 64, 6, 1040, 384), (1, 8, 2, 256, 128), (3, 16, 4, 144, 256), (40, 16, 3, 512, 384), (200, 4, 2, 272, 128), (600, 4, 2, 384, 640),
-       (1500, 2, 1, 256, 256), (64, 1, 1, 1024, 512)]
+       (1500, 2, 1, 256, 256), (64, 1, 1, 1024, 512), (2000, 16, 4, 144, 256), (2500, 4, 2, 272, 128), (40, 16, 3, 2064, 640),
+       (7, 8, 2, 1040, 384), (20, 4, 1, 144, 128)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
@@ -384,6 +387,25 @@ def test_arms():
     size = _rows64(codes, scales).abs() @ w.values[0].abs().t()
     for n in (1, 8, 9, 32):
         assert ((rows[n] - rows[300][:n]).abs() <= 2 * _roundings(2048) * size[:n] + 2.0 ** -23 * rows[n].abs()).all()
+    check_no_device_error()
+
+
+def test_arms_of_experts():
+    """Tokens go by themselves or in tiles of sorted pairs, by what either would read; the results agree."""
+    rng = np.random.default_rng(18)
+    E, k, K, N = 8, 2, 512, 768
+    w = Weights(18, E, N, K)
+    codes, scales = tq.tq_fp8_quantize(_x(rng, 600, K))
+    ids, topk_w = _routing(rng, 600, E, k)
+    rows = {}
+    for n, arm in ((4, "few_rows"), (600, "fp8_gemm")):
+        before = tq.tq_launch_counts_all()
+        rows[n] = tq.tq_fp8_moe_forward(codes[:n], scales[:n], w.codes, w.scales, ids[:n], topk_w[:n], dtype=torch.float32)
+        after = tq.tq_launch_counts_all()
+        assert {c: after[c] - before[c] for c in ("few_rows", "fp8_gemm")} == {"few_rows": 0, "fp8_gemm": 0, arm: 1}
+    _, size = _moe64(lambda t, j: _rows64(codes, scales)[t], w.values, ids, topk_w)
+    bound = 2 * _roundings(K, k) * size[:4] + 2.0 ** -23 * rows[4].abs()
+    assert ((rows[4] - rows[600][:4]).abs() <= bound).all()
     check_no_device_error()
 
 

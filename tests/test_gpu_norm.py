@@ -143,6 +143,30 @@ def test_strides_alignment_and_in_place():
         assert gx2 is dy and torch.equal(gx, gx2) and torch.equal(gw, gw2)
 
 
+def test_outputs_over_inputs():
+    """Dense rows may be written in their place by each output; rows that they would only partly cover are refused."""
+    rng = np.random.default_rng(11)
+    for n, K in ((700, 512), (300, 250)):
+        x, res, w = _rows(rng, n, K, "bf16"), _rows(rng, n, K, "bf16"), _weight(rng, K, "fp32")
+        dy, dr = _rows(rng, n, K, "bf16"), _rows(rng, n, K, "bf16")
+        y, r, rstd = tq.tq_rms_norm(x, w, residual=res)
+        for first, second in ((x, res), (res, x)):
+            a, b = first.clone(), second.clone()
+            y2, r2, rstd2 = tq.tq_rms_norm(a if first is x else b, w, residual=b if first is x else a, residual_out=a, y=b)
+            assert torch.equal(y2, y) and torch.equal(r2, r) and torch.equal(rstd2, rstd)
+        gx, gw = tq.tq_rms_norm_backward(dy, r, w, rstd, grad_residual=dr)
+        for place in range(3):
+            args = [dy.clone(), r.clone(), dr.clone()]
+            gx2, gw2 = tq.tq_rms_norm_backward(args[0], args[1], w, rstd, grad_residual=args[2], grad_x=args[place])
+            assert gx2 is args[place] and torch.equal(gx2, gx) and torch.equal(gw2, gw)
+        pad = torch.cat((x, x), 1)
+        with pytest.raises(tq.TQError):
+            tq.tq_rms_norm(pad[:, :K], w, y=pad.view(2 * n, K)[:n])
+        with pytest.raises(tq.TQError):
+            tq.tq_rms_norm(x[1:], w, y=x[:-1])
+    check_no_device_error()
+
+
 def test_rows_out_of_the_ordinary():
     K = 384
     for dtype in ("fp32", "bf16"):

@@ -28,6 +28,12 @@ bool bad_moe_shape(int64_t n, int top_k, int E) {
          n * top_k >= kMaxIndex;
 }
 bool bad_blocking(int rows_per_block) { return rows_per_block != 1 && rows_per_block != kFp8Block; }
+// Results that would be written over activations or weights still to be read.
+bool bad_place(const void* y, int64_t n, int64_t N, int y_type, const void* x, int64_t x_bytes, const void* w,
+               int64_t w_bytes) {
+  const int64_t bytes = n * N * static_cast<int64_t>(type_size(y_type));
+  return overlap(y, bytes, x, x_bytes) || overlap(y, n > 0 ? bytes : 0, w, w_bytes);
+}
 bool bad_workspace(const void* p, size_t bytes, size_t need) { return !p || bytes < need || !aligned(p, 256); }
 
 // Takes 256-byte aligned regions from a buffer, or only counts their bytes.
@@ -69,13 +75,23 @@ struct MoePlan {
   int tile_m;
   int64_t cap, P;
 };
-// Tokens by themselves where (almost) no expert has two pairs: of top-6 of 256, 4096 ->
-// 2048, 4 and 8 tokens took 57 and 83 us so and 65 and 90 in tiles, 16 156 and 138.
-MoePlan plan_arm(int64_t n, int top_k, int E) {
+// A token's pairs read their weights each, at the rate of the few-rows kernel and some
+// time for each of its units; sorted pairs read every woken expert's once, after a sort and
+// before a combine.  Fitted, in us, to 140 sizes from 256 -> 256 to 4096 -> 2048, of 1 to 256
+// tokens on 1, 8, 64 and 256 experts, of products and MLPs each: by this rule the slower
+// arm is taken for few sizes and by at most 28% (both are within 0.2% of the best on the
+// average; where only tokens whose experts nobody shares went by themselves, 21% behind,
+// and up to 2.8 times).  Of top-6 of 256, 4096 -> 2048: 4, 8 and 16 tokens 54, 87 and 150
+// us by themselves, 67, 102 and 132 in tiles; top-2 of 8, 512 -> 1024, 8, 32 and 128
+// tokens 11, 18 and 44, and 24 in tiles.
+// `bytes`: of an expert's weights; `units`: of the few-rows products.
+MoePlan plan_arm(int64_t n, int top_k, int E, bool mlp, double bytes, double units) {
   MoePlan m;
   m.P = n * top_k;
-  const double mean = n ? tq_pairs_per_woken_expert(n, top_k, E) : 0.0;
-  m.arm = n <= 2 || (mean < 1.1 && n <= 1024) ? kTokens : kTiles;
+  const double mean = n ? tq_pairs_per_woken_expert(n, top_k, E) : 1.0, P = static_cast<double>(m.P);
+  const double tokens = mlp ? 12.7 + 0.162e-6 * P * bytes + 1.75e-3 * units : 9.5 + 0.188e-6 * P * bytes + 1.13e-3 * units;
+  const double tiles = (mlp ? 28.1 : 21.1) + (mlp ? 0.221e-6 : 0.213e-6) * P / mean * bytes;   // P / mean: experts woken
+  m.arm = tokens < tiles ? kTokens : kTiles;
   m.tile_m = 128;
   m.cap = std::max<int64_t>(1, tq_tile_map_capacity(n, top_k, E, m.tile_m));
   return m;
@@ -119,7 +135,7 @@ struct ProductPlan {
 ProductPlan plan_moe(void* base, int64_t n, int top_k, int E, int K, int N) {
   ProductPlan p;
   p.tile = moe_tile(n, top_k, E, blocks_of(K), N, false, TileRows::kGathered);
-  p.m = plan_arm(n, top_k, E);
+  p.m = plan_arm(n, top_k, E, false, static_cast<double>(N) * K, static_cast<double>(n) * ((N - 1) / 16 + 1));
   if (p.m.arm != kTiles) p.tile.splits = 1;
   Carver c{static_cast<uint8_t*>(base)};
   p.routed = carve_routed(c, p.m, E);
@@ -141,7 +157,7 @@ MlpPlan plan_mlp(void* base, int64_t n, int top_k, int E, int H, int I) {
   MlpPlan p{};
   // one tile map for both products, by the gate and up projections'
   p.gu = moe_tile(n, top_k, E, blocks_of(H), I, true, TileRows::kGathered);
-  p.m = plan_arm(n, top_k, E);
+  p.m = plan_arm(n, top_k, E, true, 3.0 * H * I, static_cast<double>(n) * (top_k * (I / 8.0) + H / 16.0));
   p.down = moe_tile(n, top_k, E, blocks_of(I), H, false, TileRows::kSlots);
   if (p.m.arm != kTiles) p.down.splits = 1;
   Carver c{static_cast<uint8_t*>(base)};
@@ -216,6 +232,8 @@ int tq_fp8_quantize(const void* x, int x_type, int64_t x_stride, int E, int64_t 
   if (rows > 0 && (!x || !codes || !scales || !aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4)))
     return TQ_ERR_INVALID_ARG;
   if (rows_per_block != 1 && (n + kFp8Block - 1) / kFp8Block > 65535) return TQ_ERR_INVALID_ARG;
+  if (overlap(codes, rows * K, x, row_bytes(rows, x_stride, K, static_cast<int64_t>(type_size(x_type)))))
+    return TQ_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int rc = require_sm103(s);
   if (rc != TQ_OK || rows == 0) return rc;
@@ -229,7 +247,8 @@ int tq_fp8_dequantize(const uint8_t* codes, const float* scales, int E, int64_t 
   if (E < 0 || n < 0 || n >= kMaxIndex || E * n >= kMaxIndex || bad_k(K) || bad_type(out_type) ||
       bad_blocking(rows_per_block) || bad_output(E * n, K))
     return TQ_ERR_INVALID_ARG;
-  if (E * n > 0 && (!codes || !scales || !out || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(out, 16)))
+  if (E * n > 0 && (!codes || !scales || !out || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(out, 16) ||
+                    overlap(out, E * n * K * static_cast<int64_t>(type_size(out_type)), codes, E * n * K)))
     return TQ_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int rc = require_sm103(s);
@@ -251,6 +270,7 @@ int tq_fp8_linear(const uint8_t* x, const float* x_scales, const uint8_t* w, con
   const LinearPlan l = plan_linear(workspace, n, K, N);
   const bool splits = !l.few && l.tile.splits > 1;
   if (n > 0 && splits && bad_workspace(workspace, workspace_bytes, l.bytes)) return TQ_ERR_WORKSPACE;
+  if (bad_place(y, n, N, y_type, x, n * K, w, static_cast<int64_t>(N) * K)) return TQ_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int rc = require_sm103(s);
   if (rc != TQ_OK || n == 0) return rc;
@@ -281,6 +301,7 @@ int tq_fp8_moe_forward(const uint8_t* x, const float* x_scales, const uint8_t* w
     return TQ_ERR_INVALID_ARG;
   const ProductPlan p = plan_moe(workspace, n, top_k, E, K, N);
   if (n > 0 && p.m.arm != kTokens && bad_workspace(workspace, workspace_bytes, p.bytes)) return TQ_ERR_WORKSPACE;
+  if (bad_place(y, n, N, y_type, x, n * K, w, static_cast<int64_t>(E) * N * K)) return TQ_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int rc = require_sm103(s);
   if (rc != TQ_OK || n == 0) return rc;
@@ -315,6 +336,7 @@ int tq_fp8_moe_mlp_forward(const uint8_t* x, const float* x_scales, const uint8_
     return TQ_ERR_INVALID_ARG;
   const MlpPlan p = plan_mlp(workspace, n, top_k, E, H, I);
   if (n > 0 && bad_workspace(workspace, workspace_bytes, p.bytes)) return TQ_ERR_WORKSPACE;
+  if (bad_place(y, n, H, y_type, x, n * H, w_down, static_cast<int64_t>(E) * H * I)) return TQ_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int rc = require_sm103(s);
   if (rc != TQ_OK || n == 0) return rc;

@@ -355,6 +355,12 @@ int block_threads(int K) { return ((K + kPer - 1) / kPer + 31) / 32 * 32; }
 bool bad_rows(const void* p, int64_t stride, int64_t n, int K) {
   return stride < K || (n > 1 && static_cast<double>(n) * static_cast<double>(stride) >= 0x1p58) || (n > 0 && !p);
 }
+// An output may take the place of input rows, dense and from the same address: a row is
+// read before it is written.  It may not share memory with rows in any other way.
+bool bad_place(const void* out, const void* rows, int64_t stride, int64_t n, int K, int type) {
+  const int64_t size = static_cast<int64_t>(type_size(type));
+  return overlap(out, n * K * size, rows, row_bytes(n, stride, K, size)) && !(out == rows && (stride == K || n == 1));
+}
 bool bad_width(int K) { return K < 1 || K > TQ_NORM_MAX_WIDTH; }
 
 // Blocks of a kernel that the device holds at once (asked once per kernel, block and device).
@@ -416,7 +422,7 @@ int tq_rms_norm(const void* x, int x_type, int64_t x_stride, const void* residua
       !(eps <= FLT_MAX) || bad_rows(x, x_stride, n, K))
     return TQ_ERR_INVALID_ARG;
   if (residual && (bad_rows(residual, residual_stride, n, K) || (n > 0 && !residual_out))) return TQ_ERR_INVALID_ARG;
-  if ((!residual && residual_out) || (y && y == residual_out)) return TQ_ERR_INVALID_ARG;
+  if (!residual && residual_out) return TQ_ERR_INVALID_ARG;
   if (n > 0 && !y && !codes) return TQ_ERR_INVALID_ARG;
   if ((codes == nullptr) != (scales == nullptr)) return TQ_ERR_INVALID_ARG;
   const size_t size = type_size(x_type);
@@ -427,6 +433,16 @@ int tq_rms_norm(const void* x, int x_type, int64_t x_stride, const void* residua
                    (!residual || rows_in_vectors(residual, residual_stride, x_type)) && aligned(residual_out, 16) &&
                    aligned(y, 16) && aligned(weight, 16);
   if (codes && (!vec || !aligned(codes, 16))) return TQ_ERR_INVALID_ARG;
+  const int64_t bytes = n * K * static_cast<int64_t>(size);
+  for (const void* out : {static_cast<const void*>(y), static_cast<const void*>(residual_out)}) {
+    if (bad_place(out, x, x_stride, n, K, x_type) || bad_place(out, residual, residual_stride, n, K, x_type) ||
+        overlap(out, bytes, codes, n * K))
+      return TQ_ERR_INVALID_ARG;
+  }
+  if (overlap(y, bytes, residual_out, bytes) ||
+      overlap(codes, n * K, x, row_bytes(n, x_stride, K, static_cast<int64_t>(size))) ||
+      overlap(codes, n * K, residual, row_bytes(n, residual_stride, K, static_cast<int64_t>(size))))
+    return TQ_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int rc = require_sm103(s);
   if (rc != TQ_OK || n == 0) return rc;
@@ -459,6 +475,9 @@ int tq_rms_norm_backward(const void* grad_y, int64_t grad_y_stride, const void* 
   if (grad_weight && n > 0 &&
       (!workspace || !aligned(workspace, 256) || workspace_bytes < tq_rms_norm_backward_workspace_size(n, K)))
     return TQ_ERR_WORKSPACE;
+  if (bad_place(grad_x, x, x_stride, n, K, x_type) || bad_place(grad_x, grad_y, grad_y_stride, n, K, x_type) ||
+      bad_place(grad_x, grad_residual, grad_residual_stride, n, K, x_type))
+    return TQ_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int rc = require_sm103(s);
   if (rc != TQ_OK) return rc;

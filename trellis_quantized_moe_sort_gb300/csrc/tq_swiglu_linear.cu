@@ -167,10 +167,6 @@ TileChoice tile_x(int64_t n, int H, int I) {
 TileChoice tile_w(int64_t n, int H, int I) {
   return choose_tile(false, 2.0 * I, 1.0, static_cast<int>((n + 63) / 64), H, false, TileRows::kOne, false, true);
 }
-TileChoice at_least_64(TileChoice t) {   // operands across K come in boxes of 64 columns
-  t.cols = std::max(t.cols, 64);
-  return t;
-}
 
 struct GradPlan {
   TileChoice x, w;
@@ -180,8 +176,8 @@ struct GradPlan {
 GradPlan plan(int64_t n, int H, int I, bool has_gate_up) {
   GradPlan p{};
   if (!has_gate_up) p.forward = plan_forward(n, H, I);
-  p.x = at_least_64(tile_x(n, H, I));
-  p.w = at_least_64(tile_w(n, H, I));
+  p.x = tile_x(n, H, I);
+  p.w = tile_w(n, H, I);
   size_t used = 0;
   auto take = [&](double values, size_t size) {
     const size_t at = used;
@@ -228,6 +224,10 @@ int tq_swiglu_linear(const void* x, int type, int64_t x_stride, const void* w_gu
     return TQ_ERR_INVALID_ARG;
   const ForwardPlan f = plan_forward(n, H, I);
   if (n > 0 && f.split && (!workspace || !aligned(workspace, 256) || workspace_bytes < f.part)) return TQ_ERR_WORKSPACE;
+  const int64_t x_bytes = row_bytes(n, x_stride, H, 2), w_bytes = 4ll * I * H, h_bytes = 2 * n * I, gu_bytes = 8 * n * I;
+  if (overlap(h, h_bytes, x, x_bytes) || overlap(h, h_bytes, w_gu, w_bytes) || overlap(gate_up, gu_bytes, x, x_bytes) ||
+      overlap(gate_up, gu_bytes, w_gu, w_bytes) || overlap(h, h_bytes, gate_up, gu_bytes))
+    return TQ_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int rc = require_sm103(s);
   if (rc != TQ_OK || n == 0) return rc;
@@ -250,6 +250,12 @@ int tq_swiglu_linear_backward(const void* x, int type, int64_t x_stride, const v
     return TQ_ERR_INVALID_ARG;
   const GradPlan p = plan(n, H, I, gate_up != nullptr);
   if (n > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < p.bytes)) return TQ_ERR_WORKSPACE;
+  // (grad_h and gate_up are read before either gradient is written)
+  const int64_t x_bytes = row_bytes(n, x_stride, H, 2), gx_bytes = 2 * n * H, w_bytes = n > 0 ? 4ll * I * H : 0;
+  if (overlap(grad_x, gx_bytes, x, x_bytes) || overlap(grad_x, gx_bytes, w_gu, w_bytes) ||
+      overlap(grad_w_gu, w_bytes, x, x_bytes) || overlap(grad_w_gu, w_bytes, w_gu, w_bytes) ||
+      overlap(grad_x, gx_bytes, grad_w_gu, w_bytes))
+    return TQ_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int rc = require_sm103(s);
   if (rc != TQ_OK) return rc;
