@@ -143,6 +143,29 @@ def test_strides_alignment_and_in_place():
         assert gx2 is dy and torch.equal(gx, gx2) and torch.equal(gw, gw2)
 
 
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("n,K", [(400, 8208), (330, 16384), (160, 12304)])
+def test_gradient_of_many_wide_rows(n, K, dtype):
+    """Blocks take several rows of more than 8192 values each, with and without a residual's gradient, also in place."""
+    rng = np.random.default_rng([n, K, 1])
+    x, dy, dr = (_rows(rng, n, K, dtype) for _ in range(3))
+    w = _weight(rng, K, "fp32")
+    _, _, rstd = tq.tq_rms_norm(x, w)
+    eps = float(np.float32(1e-6))
+    for g in (None, dr):
+        gx, gw = tq.tq_rms_norm_backward(dy, x, w, rstd, grad_residual=g)
+        want_x, want_w = B.rms_norm_grad(_f64(dy), _f64(x), _f64(w), eps, None if g is None else _f64(g))
+        a, v, r = np.abs(_f64(dy) * _f64(w)), np.abs(_f64(x)), _f64(rstd)[:, None]
+        terms = r * (a + v * r ** 2 * (a * v).mean(-1, keepdims=True)) + (0 if g is None else np.abs(_f64(g)))
+        assert np.all(np.abs(_f64(gx) - want_x) <= HALF[dtype] * np.abs(want_x) + 36 * U * terms + _tiny(dtype))
+        magnitudes = (np.abs(_f64(dy)) * v * r).sum(0)
+        assert np.all(np.abs(_f64(gw) - want_w) <= (n + 4) * U * magnitudes + U * np.abs(want_w))
+        again = dy.clone()
+        gx2, gw2 = tq.tq_rms_norm_backward(again, x, w, rstd, grad_residual=g, grad_x=again)
+        assert torch.equal(gx2, gx) and torch.equal(gw2, gw)
+    check_no_device_error()
+
+
 def test_outputs_over_inputs():
     """Dense rows may be written in their place by each output; rows that they would only partly cover are refused."""
     rng = np.random.default_rng(11)

@@ -338,7 +338,7 @@ int tq_fp4_linear(const void* x, int x_type, int64_t x_stride, const uint8_t* pa
             l.tiles, n, 1, K, N, l.tile_m, l.splits, l.part, l.splits > 1 ? nullptr : y, y_type, err};
   rc = launch_fp4_gemm(g, s);
   if (rc != TQ_OK || l.splits == 1) return rc;
-  return launch_fp4_combine(l.part, n * N, l.splits, nullptr, nullptr, x_scale, w_scale, n, 1, 1, N, y, y_type, s);
+  return launch_fp4_combine(l.part, N, n * N, l.splits, nullptr, nullptr, x_scale, w_scale, n, 1, 1, N, y, y_type, s);
 }
 
 size_t tq_fp4_moe_workspace_size(int64_t n, int top_k, int E, int K, int N, int fmt) {
@@ -378,7 +378,7 @@ int tq_fp4_moe_forward(const void* x, int x_type, int64_t x_stride, const uint8_
             m.routed.tiles, m.routed.num_tiles, m.cap, m.P, E, K, N, m.tile_m, m.splits, m.part, nullptr, y_type, err};
   rc = launch_fp4_gemm(g, s);
   if (rc != TQ_OK) return rc;
-  return launch_fp4_combine(m.part, m.P * N, m.splits, topk_ids, topk_w, x_scale, w_scale, n, top_k, E, N, y, y_type,
+  return launch_fp4_combine(m.part, N, m.P * N, m.splits, topk_ids, topk_w, x_scale, w_scale, n, top_k, E, N, y, y_type,
                             s);
 }
 
@@ -425,7 +425,7 @@ int tq_fp4_moe_mlp_forward(const void* x, int x_type, int64_t x_stride, const ui
                r.num_tiles, m.cap, m.P, E, I, H, m.tile_m, m.splits_down, m.down, nullptr, y_type, err};
   rc = launch_fp4_gemm(down, s);
   if (rc != TQ_OK) return rc;
-  return launch_fp4_combine(m.down, m.P * H, m.splits_down, topk_ids, topk_w, h_scale, down_scale, n, top_k, E, H, y,
+  return launch_fp4_combine(m.down, H, m.P * H, m.splits_down, topk_ids, topk_w, h_scale, down_scale, n, top_k, E, H, y,
                             y_type, s);
 }
 

@@ -295,9 +295,10 @@ fp4_stage_swiglu_kernel(const float* __restrict__ part, long long split_stride, 
 // columns: 69 us at two and 32 registers, 84 at four, 103 at eight).
 template <typename T, int kVec>
 __global__ void __launch_bounds__(kQuantThreads, 8)
-fp4_combine_kernel(const float* __restrict__ part, long long split_stride, int splits, const int32_t* __restrict__ ids,
+fp4_combine_kernel(const float* __restrict__ part, long long part_ld, long long split_stride, int splits, const int32_t* __restrict__ ids,
                    const float* __restrict__ topk_w, const float* __restrict__ x_scale,
-                   const float* __restrict__ w_scale, int top_k, int E, int N, int blocks_per_row, T* __restrict__ y) {
+                   const float* __restrict__ w_scale, int top_k, int E, int N, int blocks_per_row, bool wide,
+                   T* __restrict__ y) {
   constexpr int kAhead = 2;
   __shared__ float coef[32];
   __shared__ bool skip[32];
@@ -317,7 +318,7 @@ fp4_combine_kernel(const float* __restrict__ part, long long split_stride, int s
   __syncthreads();
   if (c * kVec >= N) return;
   float sum[kVec] = {};
-  const float* const src = part + t * top_k * N + static_cast<long long>(c) * kVec;
+  const float* const src = part + t * top_k * part_ld + static_cast<long long>(c) * kVec;
   for (int j0 = 0; j0 < top_k; j0 += kAhead) {
     float v[kAhead][kVec] = {};
     for (int s = 0; s < splits; ++s) {
@@ -326,7 +327,7 @@ fp4_combine_kernel(const float* __restrict__ part, long long split_stride, int s
       for (int i = 0; i < kAhead; ++i) {
         const int j = j0 + i;
         if (j >= top_k || skip[j]) continue;
-        const float* const p = src + s * split_stride + static_cast<long long>(j) * N;
+        const float* const p = src + s * split_stride + static_cast<long long>(j) * part_ld;
         if constexpr (kVec == 4) {
           const float4 q = __ldcs(reinterpret_cast<const float4*>(p));
           f[i][0] = q.x;
@@ -354,7 +355,12 @@ fp4_combine_kernel(const float* __restrict__ part, long long split_stride, int s
 #pragma unroll
   for (int i = 0; i < kVec; ++i) out[i] = narrow<T>(sum[i]);
   T* const dst = y + t * N + static_cast<long long>(c) * kVec;
-  if constexpr (kVec == 4 && sizeof(T) == 4) {
+  if (kVec == 4 && !wide) {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      if (c * kVec + i < N) dst[i] = out[i];
+    }
+  } else if constexpr (kVec == 4 && sizeof(T) == 4) {
     float4 o;
     memcpy(&o, out, 16);
     *reinterpret_cast<float4*>(dst) = o;
@@ -452,11 +458,13 @@ int launch_fp4_stage_swiglu(const float* part, int64_t split_stride, int splits,
   return st;
 }
 
-int launch_fp4_combine(const float* part, int64_t split_stride, int splits, const int32_t* ids, const float* topk_w,
+int launch_fp4_combine(const float* part, int64_t part_ld, int64_t split_stride, int splits, const int32_t* ids, const float* topk_w,
                        const float* x_scale, const float* w_scale, int64_t n, int top_k, int E, int N, void* y,
                        int type, cudaStream_t s) {
-  const bool vec = N % 4 == 0 && (reinterpret_cast<uintptr_t>(y) & 15u) == 0;
-  const int cols = vec ? N / 4 : N;
+  // partial sums in whole vectors, past N too, and results in them where their rows allow it
+  const bool vec = part_ld % 4 == 0;
+  const bool wide = N % 4 == 0 && (reinterpret_cast<uintptr_t>(y) & 15u) == 0;
+  const int cols = vec ? (N - 1) / 4 + 1 : N;
   const int per_row = (cols + kQuantThreads - 1) / kQuantThreads;
   const long long blocks = n * per_row;
   if (blocks >= (1ll << 31)) return TQ_ERR_INVALID_ARG;
@@ -464,8 +472,8 @@ int launch_fp4_combine(const float* part, int64_t split_stride, int splits, cons
     using T = std::remove_pointer_t<decltype(t)>;
     auto kernel = vec ? fp4_combine_kernel<T, 4> : fp4_combine_kernel<T, 1>;
     return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kQuantThreads), 0, s, part,
-                      static_cast<long long>(split_stride), splits, ids, topk_w, x_scale, w_scale, top_k, E, N, per_row,
-                      static_cast<T*>(y));
+                      static_cast<long long>(part_ld), static_cast<long long>(split_stride), splits, ids, topk_w, x_scale,
+                      w_scale, top_k, E, N, per_row, wide, static_cast<T*>(y));
   });
   if (st == TQ_OK) count_launch(kCntFp4Combine);
   return st;

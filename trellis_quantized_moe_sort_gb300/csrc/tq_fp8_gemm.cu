@@ -14,7 +14,8 @@ int launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
   p.gather = g.gather;
   p.scatter = g.scatter;
   p.cap = g.cap;
-  p.split_stride = static_cast<long long>(g.M) * g.N;
+  p.split_stride = static_cast<long long>(g.M) * g.y_ld;
+  p.y_ld = g.y_ld;
   p.M = static_cast<int>(g.M);
   p.E = g.E;
   p.N = g.N;
@@ -30,7 +31,7 @@ int launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
   p.y = g.y;
   p.y_type = g.y_type;
   const int64_t size = g.y_type == TQ_FP32 ? 4 : 2;
-  p.aligned = g.N * size % 16 == 0 && (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0;
+  p.aligned = g.y_ld * size % 16 == 0 && (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0;
   p.codes = g.codes;
   p.scales = g.scales;
   p.err = g.err;

@@ -10,6 +10,7 @@ int launch_gemm_f16(const GemmF16& g, cudaStream_t s) {
   const bool pair = g.tile_m > kRows;
   p.cap = (g.M + g.tile_m - 1) / g.tile_m;
   p.split_stride = g.M * g.N;
+  p.y_ld = g.N;
   p.M = static_cast<int>(g.M);
   p.E = 1;
   p.N = static_cast<int>(g.N);

@@ -168,7 +168,8 @@ int launch_fp4_stage(const void* x, int type, int64_t stride, int64_t n, int K, 
 int launch_fp4_stage_swiglu(const float* part, int64_t split_stride, int splits, const float* x_scale,
                             const float* w_scale, int64_t P, int E, int I, int fmt, const float* h_scale,
                             const Fp4Slots& slots, int tile_m, uint8_t* hq, uint8_t* hs, cudaStream_t s);
-int launch_fp4_combine(const float* part, int64_t split_stride, int splits, const int32_t* ids, const float* topk_w,
+// Partial sums part[split][row], rows part_ld >= N values apart.
+int launch_fp4_combine(const float* part, int64_t part_ld, int64_t split_stride, int splits, const int32_t* ids, const float* topk_w,
                        const float* x_scale, const float* w_scale, int64_t n, int top_k, int E, int N, void* y,
                        int type, cudaStream_t s);
 struct Fp4Gemm {
@@ -277,6 +278,7 @@ struct Fp8Gemm {
   int cols;                     // half the columns of a unit: 128, 64 or 32 (128 in pairs and gated)
   int splits;                   // y is fp32 [splits][M][N]
   void* y;
+  int64_t y_ld;                 // values between rows of y, >= N
   int y_type;
   uint8_t* codes;
   float* scales;

@@ -23,7 +23,9 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
+#include "tq_device.cuh"
 #include "tq_fp8.cuh"
 #include "tq_internal.h"
 
@@ -318,6 +320,114 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_kernel(const No
   if (a.part) store16<kVec>(a.part + static_cast<long long>(blockIdx.x) * K, K, gw);
 }
 
+// The same for rows of more than 8192 values, whose blocks of up to 1024 threads have 64
+// registers a thread: the rows come through shared memory, each thread's values by its own
+// asynchronous copies, the next row's under way where two of them fit (`buffers`), and are
+// read twice from there.  (In registers, with spills, 2048 rows of 16384 in bf16 took 142
+// us and in fp32 262, 93 and 160 so.)
+template <typename T>
+__global__ void __launch_bounds__(1024) rms_norm_backward_wide_kernel(const NormGradArgs a, const int buffers) {
+  extern __shared__ uint4 rows[];   // [buffers][3][pieces][threads]
+  __shared__ float parts[2][32];
+  constexpr int kPieces = static_cast<int>(sizeof(T)), kEach = kPer / kPieces;   // 16-byte pieces of a thread, values of one
+  pdl_wait();
+  const int K = a.K, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32;
+  const int lanes = power_above(warps), at = column<true>(0);
+  const bool in = at < K;
+  const int arrays = a.grad_residual ? 3 : 2;
+  auto fetch = [&](long long row, int buffer) {
+    if (in && row < a.n) {
+      const T* const from[3] = {static_cast<const T*>(a.x) + row * a.x_stride, static_cast<const T*>(a.grad_y) + row * a.grad_y_stride,
+                                static_cast<const T*>(a.grad_residual) + row * a.grad_residual_stride};
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        if (i == arrays) break;
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+          const uint32_t to = smem_u32(rows + ((buffer * arrays + i) * kPieces + j) * blockDim.x + threadIdx.x);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from[i] + at + kEach * j) : "memory");
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  fetch(blockIdx.x, 0);
+  float w[kPer], gw[kPer] = {};
+  if (a.weight) {
+    load_weight<true>(a.weight, a.w_type, K, w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) w[i] = 1.f;
+  }
+  float next_rstd = a.rstd[blockIdx.x];
+  int parity = 0, buffer = 0;
+  for (long long row = blockIdx.x; row < a.n; row += gridDim.x, parity ^= 1) {
+    const float rstd = next_rstd;
+    if (row + gridDim.x < a.n) next_rstd = a.rstd[row + gridDim.x];
+    if (buffers == 2) {
+      fetch(row + gridDim.x, buffer ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    const uint4* const mine = rows + buffer * arrays * kPieces * blockDim.x + threadIdx.x;
+    auto piece = [&](int array, int j, float (&v)[kEach]) {
+      const uint4 raw = mine[(array * kPieces + j) * blockDim.x];
+      T t[kEach];
+      memcpy(t, &raw, 16);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) v[i] = widen(t[i]);
+    };
+    float dot = 0.f;
+    if (in) {
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        float v[kEach], d[kEach];
+        piece(0, j, v);
+        piece(1, j, d);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const float u = v[i] * rstd;
+          gw[kEach * j + i] = fmaf(d[i], u, gw[kEach * j + i]);
+          dot = fmaf(d[i] * w[kEach * j + i], u, dot);
+        }
+      }
+    }
+    dot = warp_sum(dot);
+    if (lane == 0) parts[parity][warp] = dot;   // read until the next row's barrier at the latest
+    __syncthreads();
+    dot = lane < warps ? parts[parity][lane] : 0.f;
+    dot = __shfl_sync(kAll, warp_sum(dot, lanes), 0) / static_cast<float>(K);
+    if (in) {
+      T* const out = static_cast<T*>(a.grad_x) + row * K + at;
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        float v[kEach], d[kEach], g[kEach];
+        T t[kEach];
+        piece(0, j, v);
+        piece(1, j, d);
+        if (arrays == 3) piece(2, j, g);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          float r = rstd * (d[i] * w[kEach * j + i] - v[i] * rstd * dot);
+          if (arrays == 3) r += g[i];
+          t[i] = narrow<T>(r);
+        }
+        uint4 raw;
+        memcpy(&raw, t, 16);
+        *reinterpret_cast<uint4*>(out + kEach * j) = raw;
+      }
+    }
+    if (buffers == 2)
+      buffer ^= 1;
+    else
+      fetch(row + gridDim.x, 0);   // (over values that this thread alone has read)
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  pdl_trigger();
+  if (a.part) store16<true>(a.part + static_cast<long long>(blockIdx.x) * K, K, gw);
+}
+
 // grad_w[k] = the sum of the blocks' shares, in order: 32 columns a block, each of its
 // warps every 32nd share.
 __global__ void __launch_bounds__(1024) rms_norm_weight_kernel(const float* __restrict__ part, int shares, int K,
@@ -396,7 +506,28 @@ int run_norm(const NormArgs& a, bool vec, cudaStream_t s) {
 template <typename T>
 int run_backward(const NormGradArgs& a, bool vec, int blocks, cudaStream_t s) {
   const int threads = block_threads(a.K);
-  auto kernel = vec ? (threads <= 512 ? rms_norm_backward_kernel<T, true, 512> : rms_norm_backward_kernel<T, true, 1024>)
+  if (vec && threads > 512) {
+    constexpr int kMost = 224 * 1024;
+    auto wide = rms_norm_backward_wide_kernel<T>;
+    static std::atomic<uint64_t> allowed{0};   // bit d: device d
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) {
+      cudaGetLastError();
+      return TQ_ERR_CUDA;
+    }
+    const uint64_t bit = 1ull << (device & 63);
+    if (!(allowed.load() & bit)) {
+      if (cudaFuncSetAttribute(wide, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess) {
+        cudaGetLastError();
+        return TQ_ERR_CUDA;
+      }
+      allowed.fetch_or(bit);
+    }
+    const int bytes = (a.grad_residual ? 3 : 2) * kPer * static_cast<int>(sizeof(T)) * threads;   // of a row: at most 192 KB
+    const int buffers = 2 * bytes <= kMost ? 2 : 1;
+    return launch_pdl(wide, dim3(blocks), dim3(threads), buffers * bytes, s, a, buffers);
+  }
+  auto kernel = vec ? rms_norm_backward_kernel<T, true, 512>
                     : (threads <= 512 ? rms_norm_backward_kernel<T, false, 512>
                                       : rms_norm_backward_kernel<T, false, 1024>);
   return launch_pdl(kernel, dim3(blocks), dim3(threads), 0, s, a);

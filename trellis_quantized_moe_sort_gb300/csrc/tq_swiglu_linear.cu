@@ -202,7 +202,7 @@ int product(GemmF16 g, TileChoice t, void* part, void* y, int type, cudaStream_t
   g.y_type = t.splits > 1 ? TQ_FP32 : type;
   const int rc = launch_gemm_f16(g, s);
   if (rc != TQ_OK || t.splits == 1) return rc;
-  return launch_fp4_combine(static_cast<const float*>(part), g.M * g.N, t.splits, nullptr, nullptr, nullptr, nullptr,
+  return launch_fp4_combine(static_cast<const float*>(part), g.N, g.M * g.N, t.splits, nullptr, nullptr, nullptr, nullptr,
                             g.M, 1, 1, static_cast<int>(g.N), y, type, s);
 }
 

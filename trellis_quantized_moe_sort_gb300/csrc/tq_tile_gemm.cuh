@@ -83,7 +83,7 @@ struct Params {
   const int32_t* sorted_pairs;  // with tiles: the pair of a slot
   int gather;                   // (not by pairs) A's row of a slot is token pair / top_k, else the slot
   int scatter;                  // the output row of a slot is its pair, else the slot
-  long long cap, split_stride;
+  long long cap, split_stride, y_ld;   // y_ld: values between rows of y
   int M, E, N, tile_m, top_k;   // M: slots, or rows of A; N: columns (of h, when gated)
   int col_blocks, steps, splits;
   // scales of 8-bit operands
@@ -363,8 +363,8 @@ struct Rows {
 // stores whole lines of them, 16 bytes a lane.  Rows that do not start on 16-byte
 // boundaries are turned by single values, 32 columns at a time.
 template <typename T, int kCount>
-__device__ __forceinline__ void store_columns(T* y, const float (&v)[kCount], const Rows& rows, int col, int N, bool aligned,
-                                              uint8_t* turn, int lane) {
+__device__ __forceinline__ void store_columns(T* y, const float (&v)[kCount], const Rows& rows, int col, int N, long long ld,
+                                              bool aligned, uint8_t* turn, int lane) {
   const long long row = rows.row;
   constexpr int kVec = 16 / static_cast<int>(sizeof(T)), kLine = 8 * kVec;   // values of 16 and of 128 bytes
   constexpr int kBlock = kLine < kCount ? kLine : kCount, kParts = kBlock / kVec;
@@ -390,7 +390,7 @@ __device__ __forceinline__ void store_columns(T* y, const float (&v)[kCount], co
         const int r = r0 + lane / kParts;
         const long long to = __shfl_sync(0xffffffffu, row, r);
         const uint4 o = *reinterpret_cast<const uint4*>(turn + 128 * r + 16 * (part ^ (r & 7)));
-        if (to >= 0 && at < N) *reinterpret_cast<uint4*>(y + to * N + at) = o;   // N is a multiple of kVec
+        if (to >= 0 && at < N) *reinterpret_cast<uint4*>(y + to * ld + at) = o;   // ld is a multiple of kVec
       }
     }
     return;
@@ -407,8 +407,8 @@ __device__ __forceinline__ void store_columns(T* y, const float (&v)[kCount], co
     if (rows.step) {
       // an addition a row, where the lookup of each took 12 instructions (3001 rows 2048 ->
       // 4099: 59 us with it)
-      T* to = y + rows.first * N + col + b + lane;
-      const long long next = static_cast<long long>(rows.step) * N;
+      T* to = y + rows.first * ld + col + b + lane;
+      const long long next = rows.step * ld;
 #pragma unroll 8
       for (int r = 0; r < rows.live; ++r, to += next) {
         if (in) *to = narrow<T>(floats[r * kPitch + lane]);
@@ -418,19 +418,19 @@ __device__ __forceinline__ void store_columns(T* y, const float (&v)[kCount], co
 #pragma unroll 4
     for (int r = 0; r < 32; ++r) {
       const long long to = __shfl_sync(0xffffffffu, row, r);
-      if (to >= 0 && in) y[to * N + col + b + lane] = narrow<T>(floats[r * kPitch + lane]);
+      if (to >= 0 && in) y[to * ld + col + b + lane] = narrow<T>(floats[r * kPitch + lane]);
     }
   }
 }
 template <int kCount>
 __device__ __forceinline__ void store_typed(void* y, int type, const float (&v)[kCount], const Rows& row, int col, int N,
-                                            bool aligned, uint8_t* turn, int lane) {
+                                            long long ld, bool aligned, uint8_t* turn, int lane) {
   if (type == TQ_FP32)
-    store_columns(static_cast<float*>(y), v, row, col, N, aligned, turn, lane);
+    store_columns(static_cast<float*>(y), v, row, col, N, ld, aligned, turn, lane);
   else if (type == TQ_BF16)
-    store_columns(static_cast<__nv_bfloat16*>(y), v, row, col, N, aligned, turn, lane);
+    store_columns(static_cast<__nv_bfloat16*>(y), v, row, col, N, ld, aligned, turn, lane);
   else
-    store_columns(static_cast<__half*>(y), v, row, col, N, aligned, turn, lane);
+    store_columns(static_cast<__half*>(y), v, row, col, N, ld, aligned, turn, lane);
 }
 
 template <bool k8, Group kGroup, int kCols, bool kAMn, bool kBMn, int kEpi>
@@ -798,7 +798,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
               v[2 * i] = sum[c / 2 + i].x;
               v[2 * i + 1] = sum[c / 2 + i].y;
             }
-            store_typed(y, p.y_type, v, out_row, col + half * kCols + c, p.N, p.aligned, turn, lane);
+            store_typed(y, p.y_type, v, out_row, col + half * kCols + c, p.N, p.y_ld, p.aligned, turn, lane);
           }
         }
       } else {
@@ -823,15 +823,15 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
               const Rows up_row{out_row.row < 0 ? -1 : 2 * out_row.row + 1, 2 * out_row.first + 1, 2, out_row.live};
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(g[i]);
-              store_columns(gu, v, gate_row, at, p.N, p.N % 4 == 0, turn, lane);
+              store_columns(gu, v, gate_row, at, p.N, p.N, p.N % 4 == 0, turn, lane);
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(up[i]);
-              store_columns(gu, v, up_row, at, p.N, p.N % 4 == 0, turn, lane);
+              store_columns(gu, v, up_row, at, p.N, p.N, p.N % 4 == 0, turn, lane);
             }
             if (p.y) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = silu(__uint_as_float(g[i])) * __uint_as_float(up[i]);
-              store_typed(p.y, p.y_type, v, out_row, at, p.N, p.aligned, turn, lane);
+              store_typed(p.y, p.y_type, v, out_row, at, p.N, p.y_ld, p.aligned, turn, lane);
             }
           }
         } else {
@@ -846,7 +846,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
             float f[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) f[i] = __uint_as_float(v[i / 32][i % 32]);
-            store_typed(y, p.y_type, f, out_row, col + half * kCols + 64 * c, p.N, p.aligned, turn, lane);
+            store_typed(y, p.y_type, f, out_row, col + half * kCols + 64 * c, p.N, p.y_ld, p.aligned, turn, lane);
           }
         }
         tc_fence_before();
