@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_rows_kernel(const FewRows p, 
             p.gate_up[to * 2 * p.N + f] = v[0];
             p.gate_up[(to * 2 + 1) * p.N + f] = v[1];
           }
-          out = v[0] / (1.f + expf(-v[0])) * v[1];
+          out = silu(v[0]) * v[1];
         }
         const long long at = to * p.N + f;
         if (!p.y) {

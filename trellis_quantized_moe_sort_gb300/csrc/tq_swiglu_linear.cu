@@ -40,7 +40,7 @@ swiglu_grad_kernel(const float* __restrict__ gate_up, const T* __restrict__ grad
     T dg[8], du[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float s = 1.f / (1.f + expf(-gs[j])), dh = widen(h[j]);
+      const float s = sigmoid(gs[j]), dh = widen(h[j]);
       dg[j] = narrow<T>(dh * us[j] * (s * (1.f + gs[j] * (1.f - s))));
       du[j] = narrow<T>(dh * (gs[j] * s));
     }
@@ -78,7 +78,7 @@ swiglu_sum_kernel(const float* __restrict__ part, long long split_stride, int sp
     const float gs[4] = {g.x, g.y, g.z, g.w}, us[4] = {u.x, u.y, u.z, u.w};
     T out[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) out[j] = narrow<T>(gs[j] / (1.f + expf(-gs[j])) * us[j]);
+    for (int j = 0; j < 4; ++j) out[j] = narrow<T>(silu(gs[j]) * us[j]);
     *reinterpret_cast<uint2*>(h + 4 * i) = *reinterpret_cast<const uint2*>(out);
   }
 }

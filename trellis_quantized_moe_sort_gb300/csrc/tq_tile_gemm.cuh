@@ -346,11 +346,6 @@ __device__ __forceinline__ int shared_copies(int n, int lead, int share) {
   return n / 8 * share + max(0, min(share, n % 8 - lead));
 }
 
-__device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
-// The same to about |g| 2^-23 of it, for a product that is kept in 8 bits: 64 of them a
-// thread and unit took 11000 cycles with expf and a division, while the MMAs waited.
-__device__ __forceinline__ float silu_fast(float g) { return __fdividef(g, 1.f + __expf(-g)); }
-
 // Output rows of a warp's 32: of lane l, `row`, < 0: none; where they are first + l * step
 // for l < live, step is not 0.
 struct Rows {
@@ -769,8 +764,8 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
           float h[64], top = 0.f;
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            h[2 * i] = silu_fast(sum[i].x) * sum[32 + i].x;
-            h[2 * i + 1] = silu_fast(sum[i].y) * sum[32 + i].y;
+            h[2 * i] = silu(sum[i].x) * sum[32 + i].x;
+            h[2 * i + 1] = silu(sum[i].y) * sum[32 + i].y;
           }
           top = fp8_top<64>(h);
           float* const mine = tops + (2 * parity + half) * kRows + 32 * q + lane;
