@@ -138,8 +138,10 @@ __global__ void __launch_bounds__(kThreads, 2) few_rows_kernel(const FewRows p, 
   extern __shared__ uint4 ring[];   // [kAhead][warps][4][lanes]: a lane's own bytes, read back by it alone
   __shared__ float scale_ring[kAhead][kWarps][2];
   __shared__ float sums[2][kWarps][kRows][kCols];
-  pdl_wait();
-  pdl_trigger();
+  if (!p.only_x) {
+    pdl_wait();
+    pdl_trigger();
+  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, q = lane & 3;
   const long long row_bytes = p.row_bytes;
@@ -207,6 +209,10 @@ __global__ void __launch_bounds__(kThreads, 2) few_rows_kernel(const FewRows p, 
   if (!idle) aim();
 #pragma unroll 1
   for (int i = 0; i < kAhead; ++i) load(i);
+  if (p.only_x) {
+    pdl_wait();
+    pdl_trigger();
+  }
 
   // The unit that is multiplied.  Column g (+ 8 c) is this lane's: its rows of x and of
   // the output, -1 for none.

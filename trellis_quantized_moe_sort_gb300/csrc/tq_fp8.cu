@@ -361,8 +361,9 @@ int tq_fp8_moe_mlp_forward(const uint8_t* x, const float* x_scales, const uint8_
     rc = launch_few_rows(f, kFewRowsFp8, s);
     if (rc == TQ_OK) rc = launch_fp8_quantize_rows(p.h32, TQ_FP32, I, m.P, I, p.h, p.h_scales, s);
     if (rc != TQ_OK) return rc;
-    return token_product(few_rows({p.h, p.h_scales}, {w_down, down_scales}, n, top_k, E, I, H, false, y, y_type, err),
-                         topk_ids, topk_w, false, s);
+    f = few_rows({p.h, p.h_scales}, {w_down, down_scales}, n, top_k, E, I, H, false, y, y_type, err);
+    f.only_x = 1;
+    return token_product(f, topk_ids, topk_w, false, s);
   }
   if (rc != TQ_OK) return rc;
   rc = sorted_product(m, r, {p.h, p.h_scales}, m.P, false, {w_down, down_scales}, top_k, E, I, H, p.down, p.part, err, s);

@@ -320,6 +320,9 @@ struct FewRows {
   void* y;                      // [M][N] of y_type
   int y_type;
   float* gate_up;               // gated: fp32 [M][2 N], or nullptr
+  // The launch before this one writes x and its scales and nothing else that this one
+  // reads, and lets it start only after its own wait: weights are read before waiting.
+  int only_x;
   int* err;
 };
 constexpr int kFewRowsFp8 = -1;   // `type` of the 8-bit products
