@@ -24,8 +24,9 @@
 // 16-bit products accumulate their whole K range in tensor memory.  Their operands
 // may be stored with K as the slow axis (kAMn, kBMn: the gradients' transposed
 // reads), as boxes of 64 columns x 64 rows of K.  Measured, 8192 rows 4096 -> 2 x 2048:
-// forward with gate and up kept 158 us (83% of the tensor pipe), grad_x 144 (91%) and
-// grad_w 165 (93%), at 1.75 GHz under the power limit.
+// forward with gate and up kept 155 us (79% of the tensor pipe), grad_x 143 (85%) and
+// grad_w 165 (76%: its 256 units are four rounds of 76 pairs, the last a third full), at
+// 1.74 to 1.80 GHz under the power limit.
 //
 // A pair shares one MMA of 256 rows and halves B: 32 KB a CTA and step for 128 x 256
 // results, in place of 48.  Experts' rows fill tiles of 128 better than of 256, and the
