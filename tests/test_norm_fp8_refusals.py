@@ -88,8 +88,8 @@ def test_product_refusals(tq):
                 dict(K=8), dict(N=0), dict(E=1024, N=1 << 21), dict(n=1 << 30), dict(y_type=-1), dict(w=B + 4),
                 dict(y=C + 1), dict(ws=A + 1), dict(y=A), dict(y=B + 65534), dict(x=C + 10224)):
         assert moe(**bad) == INVALID, bad
-    for bad in (dict(work=None), dict(work=A + 64), dict(size=1000)):
-        assert moe(**bad) == WORKSPACE, bad
+    for bad in (dict(work=None), dict(work=A + 64), dict(size=1000)):   # of many tokens: sorted pairs and partial sums
+        assert moe(n=4000, **bad) == WORKSPACE, bad
     assert tq.tq_fp8_moe_workspace_size(4, 9, 8, 64, 64) == 0 and tq.tq_fp8_moe_workspace_size(1 << 30, 4, 8, 64, 64) == 0
 
     def mlp(x=A, gu=B, gus=A, down=C, downs=A, ids=A, tw=A, n=40, k=2, E=8, H=64, I=128, work=A, size=1 << 40, y=D, y_type=1):
