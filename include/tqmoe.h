@@ -649,8 +649,8 @@ int tq_fp8_dequantize(const uint8_t* codes, const float* scales, int E, int64_t 
 /* ---------------------------------------------------------------------------
  * Products of 8-bit block-scaled rows x (rows_per_block 1) with 8-bit matrices
  * (rows_per_block 128).  The partial sums of each block of 128 are accumulated in
- * fp32, multiplied by both scales and added up in fp32; the result is rounded once
- * to y_type.  Sums have a fixed order, so results repeat bit for bit.
+ * fp32, multiplied by the product of both scales, which has to be in fp32's range, and
+ * added up in fp32; the result is rounded once to y_type.  Sums have a fixed order, so results repeat bit for bit.
  *
  * tq_fp8_linear:      y[t] = W x[t], w [N][K], w_scales [ceil(N/128)][ceil(K/128)].
  * tq_fp8_moe_forward: y[t] = sum_j topk_w[t][j] W_{topk_ids[t][j]} x[t], w [E][N][K]

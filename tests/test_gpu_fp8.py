@@ -459,6 +459,41 @@ def test_weights_past_four_gigabytes():
     check_no_device_error()
 
 
+def test_outputs_past_four_gigabytes():
+    """Results, pairs' partial sums and rows whose offsets pass 2^32 bytes, and 2^31 values: the last rows' are right."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB of free device memory")
+    g = torch.Generator("cuda").manual_seed(5)
+    n, K, N = 600_000, 128, 4096
+    x = torch.randn((n, K), device="cuda", generator=g).bfloat16()
+    codes, scales = tq.tq_fp8_quantize(x)
+    w = Weights(5, 2, N, K)
+    some = torch.tensor([0, 1, 255, n // 2 + 3, n - 130, n - 2, n - 1], device="cuda")
+    rows = _rows64(codes[some], scales[some])
+    want, size = rows @ w.values[0].t(), rows.abs() @ w.values[0].abs().t()
+    y = tq.tq_fp8_linear(codes, scales, w.codes[0], w.scales[0])
+    _check(y[some], want, size, K, "bf16")
+    del y
+    n = 150_000   # 2.5 GB of results, 4.9 GB of partial sums
+    ids = (torch.arange(2 * n, device="cuda") % 2).int().view(n, 2)
+    topk_w = torch.rand((n, 2), device="cuda", generator=g)
+    some = torch.tensor([0, 130, n // 2, n - 1], device="cuda")
+    want, size = _moe64(lambda t, j: _rows64(codes[some], scales[some])[t], w.values, ids[some], topk_w[some])
+    y = tq.tq_fp8_moe_forward(codes[:n], scales[:n], w.codes, w.scales, ids, topk_w, dtype=torch.float32)
+    _check(y[some], want, size, K, "fp32", 2)
+    del y, x
+    x = torch.randn((n, 16384), device="cuda", generator=g).bfloat16()
+    y, _, rstd = tq.tq_rms_norm(x)
+    gx, gw = tq.tq_rms_norm_backward(y, x, torch.ones(16384, device="cuda"), rstd)
+    back, _, again = tq.tq_rms_norm(x[some])
+    assert torch.equal(y[some], back) and torch.equal(rstd[some], again)
+    assert torch.equal(gx[some], tq.tq_rms_norm_backward(back, x[some], torch.ones(16384, device="cuda"), again)[0])
+    c8, s8, _ = tq.tq_rms_norm_fp8(x)
+    want, wants, _ = tq.tq_rms_norm_fp8(x[some])
+    assert torch.equal(c8[some].view(torch.uint8), want.view(torch.uint8)) and torch.equal(s8[some], wants)
+    check_no_device_error()
+
+
 def test_rows_behind_the_output_stay():
     """Nothing is written past the results of each operator."""
     rng = np.random.default_rng(31)

@@ -145,6 +145,31 @@ def test_large_values_and_no_rows():
     check_no_device_error()
 
 
+def test_rows_past_four_gigabytes():
+    """gate_up of 4.9 GB: the last rows of every result are those of the rows alone."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of free device memory")
+    n, H, I = 300_000, 64, 2048
+    x, w, dh = _problem(13, n, H, I, "bf16")
+    gate_up = torch.empty((n, 2 * I), device="cuda")
+    h = tq.tq_swiglu_linear(x, w, gate_up=gate_up)
+    gx, gw = tq.tq_swiglu_linear_backward(x, w, dh, gate_up=gate_up)
+    for rows in (slice(0, 256), slice(n - 288, n)):
+        want_h, want_gx, _, s, m = _reference(x[rows], w, dh[rows], "bf16")
+        _check(h[rows], want_h)
+        _check(gate_up[rows], (s, _r(H) * m + 1e-30))
+        _check(gx[rows], want_gx)
+    # the weights' gradient over all rows: added up in fp64 from slices
+    want, bound = 0, 0
+    for i in range(0, n, 30_000):
+        _, _, part, _, _ = _reference(x[i:i + 30_000], w, dh[i:i + 30_000], "bf16")
+        want, bound = want + part[0], bound + part[1]
+    bound = bound + HALF["bf16"] * want.abs()
+    # longer sums in fp32: n / 16 additions in place of 30000 / 16, of magnitudes below those that the slices' bounds hold
+    assert ((gw.double() - want).abs() <= bound * (_r(n) / _r(30_000))).all()
+    check_no_device_error()
+
+
 def test_training_step_in_a_graph():
     """Forward and backward captured together replay to the same bits, also beside an eager call."""
     x, w, dh = _problem(9, 300, 256, 128, "bf16")
