@@ -305,15 +305,21 @@ struct Unit {
 // of it (the second of them past the matrix where their number is odd: its loads read
 // what follows and its results do not exist).
 template <int kShare>
-__device__ __forceinline__ Unit unit_at(const Params& p, long long u, int num_tiles, int col_units, int sharer) {
+__device__ __forceinline__ Unit unit_at(const Params& p, unsigned u, unsigned num_tiles, unsigned col_units, int sharer) {
   Unit t;
-  t.cb = static_cast<int>(u % col_units);
-  u /= col_units;
+  const unsigned row = u / col_units;
+  t.cb = static_cast<int>(u - row * col_units);
   if (kShare == 2) t.cb = 2 * t.cb + sharer;
-  const int tile = static_cast<int>(u % num_tiles);
-  t.split = static_cast<int>(u / num_tiles);
-  t.k0 = static_cast<int>(static_cast<long long>(p.steps) * t.split / p.splits);
-  t.k1 = static_cast<int>(static_cast<long long>(p.steps) * (t.split + 1) / p.splits);
+  int tile = static_cast<int>(row);
+  t.split = 0;
+  t.k0 = 0;
+  t.k1 = p.steps;
+  if (p.splits > 1) {
+    t.split = static_cast<int>(row / num_tiles);
+    tile = static_cast<int>(row - t.split * num_tiles);
+    t.k0 = static_cast<int>(static_cast<long long>(p.steps) * t.split / p.splits);
+    t.k1 = static_cast<int>(static_cast<long long>(p.steps) * (t.split + 1) / p.splits);
+  }
   if (p.tiles) {
     const int32_t* const entry = p.tiles + 3ll * tile;
     t.e = __ldg(entry);
@@ -490,12 +496,12 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
   pdl_wait();
 
-  const int num_tiles = p.tiles ? static_cast<int>(min(static_cast<long long>(*p.num_tiles), p.cap))
+  const int num_tiles = p.tiles ? static_cast<int>(max(0ll, min(static_cast<long long>(*p.num_tiles), p.cap)))
                                 : static_cast<int>(p.cap);
-  const int col_units = (p.col_blocks + kShare - 1) / kShare;
-  const long long units = static_cast<long long>(num_tiles) * col_units * p.splits;
+  const unsigned col_units = (p.col_blocks + kShare - 1) / kShare;
+  const unsigned units = num_tiles * col_units * p.splits;   // (the host keeps them below 2^31)
   constexpr int kCtas = kGroup != kAlone ? 2 : 1;
-  const int unit0 = blockIdx.x / kCtas, unit_step = gridDim.x / kCtas;
+  const unsigned unit0 = blockIdx.x / kCtas, unit_step = gridDim.x / kCtas;
   const int stages = p.stages, accs = p.accs;
   int* const err = p.err;
 
@@ -517,7 +523,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
       Ring ring;
       long long issued = 0;
       bool ok = true, ready = false;
-      for (long long u = unit0; ok && u < units; u += unit_step) {
+      for (unsigned u = unit0; ok && u < units; u += unit_step) {
         const Unit t = unit_at<kShare>(p, u, num_tiles, col_units, sharer);
         if (!t.ok) {
           if (is_b && first && leader) record_error(err, TQ_ERR_INVALID_ARG, kWhereTileLoad);
@@ -626,7 +632,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
       bool ready = false;
       const bool leader = elect_one();
       Ring acc;
-      for (long long u = unit0; u < units; u += unit_step) {
+      for (unsigned u = unit0; u < units; u += unit_step) {
         const Unit t = unit_at<kShare>(p, u, num_tiles, col_units, sharer);
         if (!t.ok) continue;
         for (int k = t.k0; k < t.k1; ++k) {
@@ -687,7 +693,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     };
     int parity = 0;
     Ring acc;
-    for (long long u = unit0; u < units; u += unit_step) {
+    for (unsigned u = unit0; u < units; u += unit_step) {
       const Unit t = unit_at<kShare>(p, u, num_tiles, col_units, sharer);
       if (!t.ok) continue;
       const int in_tile = rank * kRows + 32 * q + lane;
@@ -915,6 +921,7 @@ int launch(Params p, const CUtensorMap& a, const CUtensorMap& b, long long units
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  if (units >= (1ll << 31)) return TQ_ERR_INVALID_ARG;
   cfg.gridDim = dim3(kCtas * static_cast<int>(std::max<long long>(1, std::min<long long>(units, sm_count() / kCtas))));
   if (cudaLaunchKernelEx(&cfg, kernel, a, b, p) != cudaSuccess) {
     cudaGetLastError();
