@@ -494,6 +494,24 @@ def test_outputs_past_four_gigabytes():
     check_no_device_error()
 
 
+def test_no_rows():
+    """Empty batches give empty results, without a launch."""
+    w, down = Weights(1, 4, 256, 128), Weights(2, 4, 128, 128)
+    x = torch.empty((0, 128), dtype=torch.bfloat16, device="cuda")
+    before = tq.tq_launch_counts_all()
+    codes, scales = tq.tq_fp8_quantize(x)
+    assert codes.shape == (0, 128) and scales.shape == (0, 1)
+    assert tq.tq_fp8_dequantize(codes, scales).shape == (0, 128)
+    assert [t.shape[0] for t in tq.tq_fp8_quantize(x, 128)] == [0, 0]
+    ids, topk_w = torch.empty((0, 2), dtype=torch.int32, device="cuda"), torch.empty((0, 2), device="cuda")
+    assert tq.tq_fp8_linear(codes, scales, w.codes[0], w.scales[0]).shape == (0, 256)
+    assert tq.tq_fp8_moe_forward(codes, scales, w.codes, w.scales, ids, topk_w).shape == (0, 256)
+    assert tq.tq_fp8_moe_mlp_forward(codes, scales, w.codes, w.scales, down.codes, down.scales, ids, topk_w).shape == (0, 128)
+    assert [t.shape[0] for t in tq.tq_rms_norm_fp8(x)] == [0, 0, 0]
+    assert tq.tq_launch_counts_all() == before
+    check_no_device_error()
+
+
 def test_rows_behind_the_output_stay():
     """Nothing is written past the results of each operator."""
     rng = np.random.default_rng(31)
