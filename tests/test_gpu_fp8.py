@@ -494,6 +494,32 @@ def test_outputs_past_four_gigabytes():
     check_no_device_error()
 
 
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+def test_results_from_any_element_on(dtype):
+    """y from an address that is a multiple of its elements' size alone: the same results, by every way that writes them."""
+    rng = np.random.default_rng(37)
+
+    def same(call, n, N):
+        room = torch.full((n * N + 9,), 7.0, dtype=DTYPES[dtype], device="cuda")
+        want = call(None)
+        for lead in (1, 2, 4):
+            room.fill_(7.0)
+            y = room[lead:lead + n * N].view(n, N)
+            assert call(y) is y and torch.equal(y, want)
+            assert (room[:lead] == 7.0).all() and (room[lead + n * N:] == 7.0).all()
+
+    for n, K, N in ((5, 256, 136), (97, 4096, 256), (97, 4096, 131), (600, 256, 512)):   # few rows, K split twice, tiles
+        codes, scales = tq.tq_fp8_quantize(_x(rng, n, K))
+        w = Weights(n, 1, N, K)
+        same(lambda y: tq.tq_fp8_linear(codes, scales, w.codes[0], w.scales[0], y=y, dtype=DTYPES[dtype]), n, N)
+    for n, N in ((3, 136), (1000, 136), (1000, 137)):   # tokens by themselves, sorted pairs
+        codes, scales = tq.tq_fp8_quantize(_x(rng, n, 256))
+        w = Weights(n, 4, N, 256)
+        ids, topk_w = _routing(rng, n, 4, 2)
+        same(lambda y: tq.tq_fp8_moe_forward(codes, scales, w.codes, w.scales, ids, topk_w, y=y, dtype=DTYPES[dtype]), n, N)
+    check_no_device_error()
+
+
 def test_no_rows():
     """Empty batches give empty results, without a launch."""
     w, down = Weights(1, 4, 256, 128), Weights(2, 4, 128, 128)
