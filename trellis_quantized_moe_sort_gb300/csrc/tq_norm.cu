@@ -449,8 +449,13 @@ __global__ void __launch_bounds__(1024) rms_norm_weight_kernel(const float* __re
   int c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < K) {
-#pragma unroll 4
-    for (int b = warp; b < shares; b += 32) s += __ldcs(part + static_cast<long long>(b) * K + c);
+    for (int b = warp; b < shares; b += 32 * 12) {   // a dozen reads under way
+      float v[12];
+#pragma unroll
+      for (int i = 0; i < 12; ++i) v[i] = b + 32 * i < shares ? __ldcs(part + static_cast<long long>(b + 32 * i) * K + c) : 0.f;
+#pragma unroll
+      for (int i = 0; i < 12; ++i) s += v[i];
+    }
   }
   sums[warp][lane] = s;
   __syncthreads();
