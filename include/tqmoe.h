@@ -650,7 +650,8 @@ int tq_fp8_dequantize(const uint8_t* codes, const float* scales, int E, int64_t 
  * Products of 8-bit block-scaled rows x (rows_per_block 1) with 8-bit matrices
  * (rows_per_block 128).  The partial sums of each block of 128 are accumulated in
  * fp32, multiplied by the product of both scales, which has to be in fp32's range, and
- * added up in fp32; the result is rounded once to y_type.  Sums have a fixed order, so results repeat bit for bit.
+ * added up in fp32; the result is rounded once to y_type.  Sums have a fixed order, so
+ * results repeat bit for bit.
  *
  * tq_fp8_linear:      y[t] = W x[t], w [N][K], w_scales [ceil(N/128)][ceil(K/128)].
  * tq_fp8_moe_forward: y[t] = sum_j topk_w[t][j] W_{topk_ids[t][j]} x[t], w [E][N][K]
@@ -662,11 +663,10 @@ int tq_fp8_dequantize(const uint8_t* codes, const float* scales, int E, int64_t 
  *   y[t] = sum_j topk_w[t][j] W_down h(t,j).  E = 1, top_k = 1: a dense MLP.
  * x, w (device) codes, 16-byte aligned; x_scales (device) fp32 [n][ceil(K/128)];
  * y (device) dense, apart from x and the weights.  K and H are multiples of 16, N is
- * any width.  E <= 1024,
- * top_k <= 32; n * top_k and E * N (E * 2I, E * H) below 2^31 - 1024, n * top_k * N
- * below 2^58.  workspace (device) of at least the matching *_workspace_size() bytes
- * (0 on invalid arguments; 256, or a NULL workspace, where none is needed),
- * 256-byte aligned; its contents are undefined after the call.
+ * any width.  E <= 1024, top_k <= 32; n * top_k and E * N (E * 2I, E * H) below 2^31 -
+ * 1024, n * top_k * N below 2^57.  workspace (device) of at least the matching
+ * *_workspace_size() bytes (0 on invalid arguments; 256, or a NULL workspace, where none
+ * is needed), 256-byte aligned; its contents are undefined after the call.
  * ------------------------------------------------------------------------- */
 size_t tq_fp8_linear_workspace_size(int64_t n, int K, int N);
 int tq_fp8_linear(const uint8_t* x, const float* x_scales, const uint8_t* w, const float* w_scales, int64_t n, int K,

@@ -241,7 +241,8 @@ __global__ void __launch_bounds__(kThreads, 2) few_rows_kernel(const FewRows p, 
       if constexpr (kKind == kFp8) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          sx[c][i] = p.x_scales + static_cast<long long>(max(__shfl_sync(0xffffffffu, row, 4 * (2 * q + i)), 0)) * p.steps + here.k;
+          sx[c][i] = p.x_scales + here.k +
+                     static_cast<long long>(max(__shfl_sync(0xffffffffu, row, 4 * (2 * q + i)), 0)) * p.steps;
       }
     }
     return e >= 0;

@@ -60,7 +60,8 @@ struct LinearPlan {
 LinearPlan plan_linear(void* base, int64_t n, int K, int N) {
   LinearPlan l{};
   l.bytes = kNoWorkspace;
-  l.tile = choose_tile(true, static_cast<double>(std::max<int64_t>(n, 1)), 1.0, blocks_of(K), N, false, TileRows::kOne, false, true);
+  l.tile = choose_tile(true, static_cast<double>(std::max<int64_t>(n, 1)), 1.0, blocks_of(K), N, false, TileRows::kOne,
+                       false, true);
   l.few = few_rows_cost(n, static_cast<double>(N) * K, true) < l.tile.cost;
   if (!l.few && l.tile.splits > 1) {
     Carver c{static_cast<uint8_t*>(base)};
@@ -287,7 +288,8 @@ int tq_fp8_linear(const uint8_t* x, const float* x_scales, const uint8_t* w, con
             splits ? part_ld(N) : N, splits ? TQ_FP32 : y_type, nullptr, nullptr, err};
   rc = launch_fp8_gemm(g, s);
   if (rc != TQ_OK || !splits) return rc;
-  return launch_fp4_combine(l.part, part_ld(N), n * part_ld(N), l.tile.splits, nullptr, nullptr, nullptr, nullptr, n, 1, 1, N, y, y_type, s);
+  return launch_fp4_combine(l.part, part_ld(N), n * part_ld(N), l.tile.splits, nullptr, nullptr, nullptr, nullptr, n, 1,
+                            1, N, y, y_type, s);
 }
 
 size_t tq_fp8_moe_workspace_size(int64_t n, int top_k, int E, int K, int N) {
@@ -318,8 +320,8 @@ int tq_fp8_moe_forward(const uint8_t* x, const float* x_scales, const uint8_t* w
   if (rc != TQ_OK) return rc;
   rc = sorted_product(p.m, p.routed, {x, x_scales}, n, true, {w, w_scales}, top_k, E, K, N, p.tile, p.part, err, s);
   if (rc != TQ_OK) return rc;
-  return launch_fp4_combine(p.part, part_ld(N), p.m.P * part_ld(N), p.tile.splits, topk_ids, topk_w, nullptr, nullptr, n, top_k, E, N, y,
-                            y_type, s);
+  return launch_fp4_combine(p.part, part_ld(N), p.m.P * part_ld(N), p.tile.splits, topk_ids, topk_w, nullptr, nullptr, n,
+                            top_k, E, N, y, y_type, s);
 }
 
 size_t tq_fp8_moe_mlp_workspace_size(int64_t n, int top_k, int E, int H, int I) {
@@ -368,8 +370,8 @@ int tq_fp8_moe_mlp_forward(const uint8_t* x, const float* x_scales, const uint8_
   if (rc != TQ_OK) return rc;
   rc = sorted_product(m, r, {p.h, p.h_scales}, m.P, false, {w_down, down_scales}, top_k, E, I, H, p.down, p.part, err, s);
   if (rc != TQ_OK) return rc;
-  return launch_fp4_combine(p.part, H, m.P * H, p.down.splits, topk_ids, topk_w, nullptr, nullptr, n, top_k, E, H, y, y_type,
-                            s);
+  return launch_fp4_combine(p.part, H, m.P * H, p.down.splits, topk_ids, topk_w, nullptr, nullptr, n, top_k, E, H, y,
+                            y_type, s);
 }
 
 }  // extern "C"

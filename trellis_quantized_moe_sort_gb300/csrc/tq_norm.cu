@@ -347,7 +347,8 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_wide_kernel(const Norm
   const int arrays = a.grad_residual ? 3 : 2;
   auto fetch = [&](long long row, int buffer) {
     if (in && row < a.n) {
-      const T* const from[3] = {static_cast<const T*>(a.x) + row * a.x_stride, static_cast<const T*>(a.grad_y) + row * a.grad_y_stride,
+      const T* const from[3] = {static_cast<const T*>(a.x) + row * a.x_stride,
+                                static_cast<const T*>(a.grad_y) + row * a.grad_y_stride,
                                 static_cast<const T*>(a.grad_residual) + row * a.grad_residual_stride};
 #pragma unroll
       for (int i = 0; i < 3; ++i) {

@@ -105,7 +105,8 @@ ForwardPlan plan_forward(int64_t n, int H, int I) {
   ForwardPlan f{};
   const int steps = (H + 63) / 64;
   f.tile = choose_tile(false, static_cast<double>(std::max<int64_t>(n, 1)), 1.0, steps, I, true, TileRows::kOne, false, false);
-  const TileChoice plain = choose_tile(false, static_cast<double>(std::max<int64_t>(n, 1)), 1.0, steps, 2ll * I, false, TileRows::kOne, true, true, 64);
+  const TileChoice plain = choose_tile(false, static_cast<double>(std::max<int64_t>(n, 1)), 1.0, steps, 2ll * I, false,
+                                       TileRows::kOne, true, true, 64);
   f.few = few_rows_cost(n, 4.0 * I * H, false) < std::min(plain.cost, f.tile.cost);
   f.split = !f.few && plain.cost < f.tile.cost;
   if (f.split) {
@@ -162,7 +163,8 @@ int forward(const ForwardPlan& f, const void* x, int type, int64_t x_stride, con
 
 // The two products of the gradient.
 TileChoice tile_x(int64_t n, int H, int I) {
-  return choose_tile(false, static_cast<double>(std::max<int64_t>(n, 1)), 1.0, static_cast<int>((2ll * I + 63) / 64), H, false, TileRows::kOne, false, true);
+  return choose_tile(false, static_cast<double>(std::max<int64_t>(n, 1)), 1.0, static_cast<int>((2ll * I + 63) / 64), H,
+                     false, TileRows::kOne, false, true);
 }
 TileChoice tile_w(int64_t n, int H, int I) {
   return choose_tile(false, 2.0 * I, 1.0, static_cast<int>((n + 63) / 64), H, false, TileRows::kOne, false, true);
