@@ -137,10 +137,9 @@ struct ProductPlan {
   size_t bytes;
 };
 ProductPlan plan_moe(void* base, int64_t n, int top_k, int E, int K, int N) {
-  ProductPlan p;
-  p.tile = moe_tile(n, top_k, E, blocks_of(K), N, false, TileRows::kGathered);
+  ProductPlan p{};
   p.m = plan_arm(n, top_k, E, false, static_cast<double>(N) * K, static_cast<double>(n) * ((N - 1) / 16 + 1));
-  if (p.m.arm != kTiles) p.tile.splits = 1;
+  if (p.m.arm == kTiles) p.tile = moe_tile(n, top_k, E, blocks_of(K), N, false, TileRows::kGathered);
   Carver c{static_cast<uint8_t*>(base)};
   p.routed = carve_routed(c, p.m, E);
   p.part = p.m.arm == kTokens ? nullptr : c.take<float>(static_cast<size_t>(p.tile.splits) * p.m.P * part_ld(N));
@@ -159,11 +158,11 @@ struct MlpPlan {
 };
 MlpPlan plan_mlp(void* base, int64_t n, int top_k, int E, int H, int I) {
   MlpPlan p{};
-  // one tile map for both products, by the gate and up projections'
-  p.gu = moe_tile(n, top_k, E, blocks_of(H), I, true, TileRows::kGathered);
   p.m = plan_arm(n, top_k, E, true, 3.0 * H * I, static_cast<double>(n) * (top_k * (I / 8.0) + H / 16.0));
-  p.down = moe_tile(n, top_k, E, blocks_of(I), H, false, TileRows::kSlots);
-  if (p.m.arm != kTiles) p.down.splits = 1;
+  if (p.m.arm == kTiles) {   // one tile map for both products
+    p.gu = moe_tile(n, top_k, E, blocks_of(H), I, true, TileRows::kGathered);
+    p.down = moe_tile(n, top_k, E, blocks_of(I), H, false, TileRows::kSlots);
+  }
   Carver c{static_cast<uint8_t*>(base)};
   p.routed = carve_routed(c, p.m, E);
   p.h32 = p.m.arm == kTiles ? nullptr : c.take<float>(static_cast<size_t>(p.m.P) * I);
