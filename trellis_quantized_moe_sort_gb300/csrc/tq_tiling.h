@@ -27,7 +27,7 @@ enum class TileRows { kOne, kGathered, kSlots };
 // 3000 bytes a clock, and the launch that adds them up.  `rows` rows for each of
 // `matrices` matrices; N columns, of h when gated (no splits: the activation needs whole
 // sums).
-// Measured: 8192 rows 4096 -> 4096 of one matrix 131 us by pairs (its quantising
+// Measured: 8192 rows 4096 -> 4096 of one matrix 130 us by pairs (its quantising
 // included), 142 by CTAs alone; 8192 tokens on 256 experts 4096 -> 2048 758 us by pairs
 // of pairs that share their rows, 695 by CTAs that do.
 inline TileChoice choose_tile(bool k8, double rows, double matrices, int steps, int64_t N, bool gated, TileRows kind,
