@@ -105,7 +105,7 @@ double typical_rows(int64_t n, int top_k, int E) {
   return mean + 2.0 * std::sqrt(mean);
 }
 TileChoice moe_tile(int64_t n, int top_k, int E, int steps, int N, bool gated, TileRows kind) {
-  if (n == 0) return {128, false, 128, 1, 0.0};
+  if (n == 0) return {128, 128, 1, 0.0};
   const double mean = tq_pairs_per_woken_expert(n, top_k, E);
   return choose_tile(true, typical_rows(n, top_k, E), n * top_k / mean, steps, N, gated, kind, !gated, !gated);
 }
@@ -213,7 +213,7 @@ int token_product(FewRows f, const int32_t* ids, const float* topk_w, bool gathe
 int sorted_product(const MoePlan& m, const Routed& r, Operand x, int64_t x_rows, bool gather, Operand w, int top_k, int E,
                    int K, int N, TileChoice tile, float* part, int* err, cudaStream_t s) {
   Fp8Gemm g{x.codes, x.scales, x_rows, w.codes, w.scales, r.sorted_pairs, r.tiles, r.num_tiles, m.cap, m.P, top_k, E,
-            K, N, gather, true, false, m.tile_m, tile.shared, tile.cols, tile.splits, part, part_ld(N),
+            K, N, gather, true, false, m.tile_m, tile.cols, tile.splits, part, part_ld(N),
             TQ_FP32, nullptr, nullptr, err};
   return launch_fp8_gemm(g, s);
 }
@@ -283,7 +283,7 @@ int tq_fp8_linear(const uint8_t* x, const float* x_scales, const uint8_t* w, con
   if (l.few)
     return launch_few_rows(few_rows({x, x_scales}, {w, w_scales}, n, 1, 1, K, N, false, y, y_type, err), kFewRowsFp8, s);
   Fp8Gemm g{x, x_scales, n, w, w_scales, nullptr, nullptr, nullptr, (n + l.tile.tile_m - 1) / l.tile.tile_m, n, 1, 1, K, N,
-            false, false, false, l.tile.tile_m, l.tile.shared, l.tile.cols, l.tile.splits, splits ? l.part : y,
+            false, false, false, l.tile.tile_m, l.tile.cols, l.tile.splits, splits ? l.part : y,
             splits ? part_ld(N) : N, splits ? TQ_FP32 : y_type, nullptr, nullptr, err};
   rc = launch_fp8_gemm(g, s);
   if (rc != TQ_OK || !splits) return rc;
@@ -353,7 +353,7 @@ int tq_fp8_moe_mlp_forward(const uint8_t* x, const float* x_scales, const uint8_
   if (rc != TQ_OK) return rc;
   if (m.arm == kTiles) {
     Fp8Gemm g{x, x_scales, n, w_gu, gu_scales, r.sorted_pairs, r.tiles, r.num_tiles, m.cap, m.P, top_k, E, H, I, true,
-              false, true, m.tile_m, p.gu.shared, 128, 1, nullptr, I, TQ_FP32, p.h, p.h_scales, err};
+              false, true, m.tile_m, 128, 1, nullptr, I, TQ_FP32, p.h, p.h_scales, err};
     rc = launch_fp8_gemm(g, s);
   } else {
     FewRows f = few_rows({x, x_scales}, {w_gu, gu_scales}, m.P, top_k, E, H, I, true, p.h32, TQ_FP32, err);

@@ -7,7 +7,7 @@ namespace tq {
 int launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
   using namespace tile;
   Params p{};
-  const bool pair = g.tile_m > kRows, shared = !pair && g.shared;
+  const bool pair = g.tile_m > kRows;
   p.tiles = g.tiles;
   p.num_tiles = g.num_tiles;
   p.sorted_pairs = g.sorted_pairs;
@@ -37,20 +37,18 @@ int launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
   p.err = g.err;
   CUtensorMap a, b;
   const int64_t w_rows = static_cast<int64_t>(g.E) * (g.gated ? 2 : 1) * g.N;
-  if (!encode(&a, g.x, 1, g.K, g.x_rows, g.K, g.gather ? 1 : shared ? kRows / 2 : kRows) ||
+  if (!encode(&a, g.x, 1, g.K, g.x_rows, g.K, g.gather ? 1 : kRows) ||
       !encode(&b, g.w, 1, g.K, w_rows, g.K, g.cols))
     return TQ_ERR_INVALID_ARG;
-  const long long units = g.cap * (shared ? (p.col_blocks + 1) / 2 : p.col_blocks) * g.splits;
+  const long long units = g.cap * p.col_blocks * g.splits;
   int st;
   if (g.gated)
-    st = shared ? launch<true, kSharing, 128, false, false, kGated8>(p, a, b, units, s)
-                : launch<true, kAlone, 128, false, false, kGated8>(p, a, b, units, s);
+    st = launch<true, false, 128, false, false, kGated8>(p, a, b, units, s);
   else
-    st = pair            ? launch<true, kPaired, 128, false, false, kStore>(p, a, b, units, s)
-         : shared        ? launch<true, kSharing, 128, false, false, kStore>(p, a, b, units, s)
-         : g.cols == 128 ? launch<true, kAlone, 128, false, false, kStore>(p, a, b, units, s)
-         : g.cols == 64  ? launch<true, kAlone, 64, false, false, kStore>(p, a, b, units, s)
-                         : launch<true, kAlone, 32, false, false, kStore>(p, a, b, units, s);
+    st = pair            ? launch<true, true, 128, false, false, kStore>(p, a, b, units, s)
+         : g.cols == 128 ? launch<true, false, 128, false, false, kStore>(p, a, b, units, s)
+         : g.cols == 64  ? launch<true, false, 64, false, false, kStore>(p, a, b, units, s)
+                         : launch<true, false, 32, false, false, kStore>(p, a, b, units, s);
   if (st == TQ_OK) count_launch(kCntFp8Gemm);
   return st;
 }

@@ -35,19 +35,19 @@ int launch_gemm_f16(const GemmF16& g, cudaStream_t s) {
   const long long units = p.cap * p.col_blocks * g.splits;
   int st;
   if (g.gated)
-    st = pair            ? launch<false, kPaired, 128, false, false, kGated16>(p, a, b, units, s)
-         : g.cols == 128 ? launch<false, kAlone, 128, false, false, kGated16>(p, a, b, units, s)
-                         : launch<false, kAlone, 64, false, false, kGated16>(p, a, b, units, s);
+    st = pair            ? launch<false, true, 128, false, false, kGated16>(p, a, b, units, s)
+         : g.cols == 128 ? launch<false, false, 128, false, false, kGated16>(p, a, b, units, s)
+                         : launch<false, false, 64, false, false, kGated16>(p, a, b, units, s);
   else if (!g.b_mn)
-    st = launch<false, kAlone, 64, false, false, kStore>(p, a, b, units, s);
+    st = launch<false, false, 64, false, false, kStore>(p, a, b, units, s);
   else if (g.a_mn)
-    st = pair            ? launch<false, kPaired, 128, true, true, kStore>(p, a, b, units, s)
-         : g.cols == 128 ? launch<false, kAlone, 128, true, true, kStore>(p, a, b, units, s)
-                         : launch<false, kAlone, 64, true, true, kStore>(p, a, b, units, s);
+    st = pair            ? launch<false, true, 128, true, true, kStore>(p, a, b, units, s)
+         : g.cols == 128 ? launch<false, false, 128, true, true, kStore>(p, a, b, units, s)
+                         : launch<false, false, 64, true, true, kStore>(p, a, b, units, s);
   else
-    st = pair            ? launch<false, kPaired, 128, false, true, kStore>(p, a, b, units, s)
-         : g.cols == 128 ? launch<false, kAlone, 128, false, true, kStore>(p, a, b, units, s)
-                         : launch<false, kAlone, 64, false, true, kStore>(p, a, b, units, s);
+    st = pair            ? launch<false, true, 128, false, true, kStore>(p, a, b, units, s)
+         : g.cols == 128 ? launch<false, false, 128, false, true, kStore>(p, a, b, units, s)
+                         : launch<false, false, 64, false, true, kStore>(p, a, b, units, s);
   if (st == TQ_OK) count_launch(kCntGatedGemm);
   return st;
 }

@@ -274,7 +274,6 @@ struct Fp8Gemm {
   bool scatter;                 // output rows are pairs, else slots
   bool gated;                   // h in codes and scales, else y
   int tile_m;                   // 128, or 256: pairs of CTAs (one matrix alone)
-  bool shared;                  // tiles of 128: two column blocks share the copies of their rows (cols 128)
   int cols;                     // half the columns of a unit: 128, 64 or 32 (128 in pairs and gated)
   int splits;                   // y is fp32 [splits][M][N]
   void* y;

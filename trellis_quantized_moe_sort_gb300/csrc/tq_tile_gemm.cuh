@@ -29,9 +29,9 @@
 // 1.74 to 1.80 GHz under the power limit.
 //
 // A pair shares one MMA of 256 rows and halves B: 32 KB a CTA and step for 128 x 256
-// results, in place of 48.  Experts' rows fill tiles of 128 better than of 256, and the
-// copies of their gathered rows, four at a time, cost 50 cycles each: there two CTAs
-// take neighbouring columns of 128 rows and copy half of them each, to both.
+// results, in place of 48.  Experts' rows fill tiles of 128 better than of 256 and go by
+// CTAs alone.  Every copy fills its own CTA's shared memory: tensor maps hold the caller's
+// addresses, and a copy to several CTAs at once may only read this GPU's own memory.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -65,11 +65,6 @@ constexpr int kTopBytes = 2 * 2 * kRows * 4;  // two buffers of both column halv
 // up registers to 256, 128 x 40 + 256 x 232 = 384 x 168, which the launch has to have.
 constexpr bool splits_registers(bool k8, int cols) { return k8 && cols == 128; }
 constexpr int kLaunchRegisters = 168;
-
-// How CTAs work together: each by itself; as a pair on one MMA of 256 rows; or two by
-// two on neighbouring column blocks of the same 128 rows, of which each copies half to
-// both.
-enum Group { kAlone = 0, kPaired = 1, kSharing = 2 };
 
 enum Epilogue {
   kStore = 0,     // y[row][column], or partial sums, one fp32 matrix per split
@@ -186,36 +181,13 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* m, int
   else
     tma_load_2d(dst, m, x, y, bar);
 }
-// A box, or four gathered rows, to both CTAs of a cluster, at the same place in each; the
-// bytes count on the barrier at the same place in each.
-__device__ __forceinline__ void load_box_to_both(uint32_t dst, const CUtensorMap* m, int32_t x, int32_t y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
-      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar), "h"(static_cast<uint16_t>(3))
-      : "memory");
-}
-__device__ __forceinline__ void load_rows_to_both(uint32_t dst, const CUtensorMap* m, int32_t x, int4 r, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.multicast::cluster"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar),
-      "h"(static_cast<uint16_t>(3))
-      : "memory");
-}
-
-// Arrives on the barrier (of both CTAs of a pair, or of two that share their rows of A)
-// once every MMA issued so far has completed.
-template <bool kPair, bool kShared>
+// Arrives on the barrier (of both CTAs of a pair) once every MMA issued so far has
+// completed.
+template <bool kPair>
 __device__ __forceinline__ void commit(uint32_t bar) {
   if constexpr (kPair)
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(static_cast<uint16_t>(3))
-        : "memory");
-  else if constexpr (kShared)
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
         "h"(static_cast<uint16_t>(3))
         : "memory");
   else
@@ -301,15 +273,10 @@ struct Unit {
   bool ok;
 };
 
-// Unit u of a cluster; two CTAs that share the rows of A take neighbouring column blocks
-// of it (the second of them past the matrix where their number is odd: its loads read
-// what follows and its results do not exist).
-template <int kShare>
-__device__ __forceinline__ Unit unit_at(const Params& p, unsigned u, unsigned num_tiles, unsigned col_units, int sharer) {
+__device__ __forceinline__ Unit unit_at(const Params& p, unsigned u, unsigned num_tiles) {
   Unit t;
-  const unsigned row = u / col_units;
-  t.cb = static_cast<int>(u - row * col_units);
-  if (kShare == 2) t.cb = 2 * t.cb + sharer;
+  const unsigned row = u / static_cast<unsigned>(p.col_blocks);
+  t.cb = static_cast<int>(u - row * p.col_blocks);
   int tile = static_cast<int>(row);
   t.split = 0;
   t.k0 = 0;
@@ -345,10 +312,6 @@ __device__ __forceinline__ int pair_of(const Params& p, int slot, int where) {
 // Copies of four rows that a tile's gathered rows take, and how many of `n` copies a warp
 // takes: `share` from the lead-th of every eight.
 __device__ __forceinline__ int gathered(int rows) { return (min(kRows, rows) + 3) / 4; }
-// Of those, the part that one of two CTAs gathers for both.
-__device__ __forceinline__ int part_of(int copies, int sharer) {
-  return max(0, min(kRows / 8, copies - sharer * (kRows / 8)));
-}
 __device__ __forceinline__ int shared_copies(int n, int lead, int share) {
   return n / 8 * share + max(0, min(share, n % 8 - lead));
 }
@@ -435,7 +398,7 @@ __device__ __forceinline__ void store_typed(void* y, int type, const float (&v)[
     store_columns(static_cast<__half*>(y), v, row, col, N, ld, aligned, turn, lane);
 }
 
-template <bool k8, Group kGroup, int kCols, bool kAMn, bool kBMn, int kEpi>
+template <bool k8, bool kPair, int kCols, bool kAMn, bool kBMn, int kEpi>
 __global__ void __launch_bounds__(kThreads, 1)
 tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Params p) {
   static_assert(kCols == 128 || kCols == 64 || kCols == 32, "");
@@ -444,9 +407,6 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
   static_assert(kEpi == kStore || kCols >= 64, "");
   static_assert(k8 || kCols >= 64, "16-bit sums are read 64 columns at a time");
   static_assert(!kBMn || kCols >= 64, "");
-  static_assert(kGroup != kSharing || k8, "");
-  constexpr bool kPair = kGroup == kPaired, kShared = kGroup == kSharing;
-  constexpr int kShare = kShared ? 2 : 1;
   constexpr bool kGated = kEpi != kStore, kSplitRegisters = splits_registers(k8, kCols);
   constexpr int kN = 2 * kCols;                                   // the MMA's N
   constexpr int kBBytes = (kPair ? kCols : kN) * kStepBytes;      // of B per CTA and step
@@ -460,8 +420,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const gbase = smem_raw + (base - raw);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  const int cta = kGroup != kAlone ? static_cast<int>(cluster_rank()) : 0;
-  const int rank = kPair ? cta : 0, sharer = kShared ? cta : 0;
+  const int rank = kPair ? static_cast<int>(cluster_rank()) : 0;
   const bool first = rank == 0;   // of a pair: the barriers that the MMA waits for are its
   const bool gather = !kPair && p.gather;
 
@@ -476,7 +435,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(bar_full + 8 * s, gather ? 3 : 2);
-      mbar_init(bar_empty + 8 * s, kShare);   // the MMAs of every CTA that a copy writes to
+      mbar_init(bar_empty + 8 * s, 1);
     }
     for (int a = 0; a < p.accs; ++a) {
       mbar_init(bar_accfull + 8 * a, 1);
@@ -491,16 +450,15 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
   if (warp == kWarpA) alloc_columns<kPair>(smem_u32(tmem_holder), static_cast<uint32_t>(p.tmem_cols));
   tc_fence_before();
   __syncthreads();
-  if (kGroup != kAlone) cluster_sync();   // every CTA's barriers are ready
+  if (kPair) cluster_sync();   // both CTAs' barriers are ready
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
   pdl_wait();
 
   const int num_tiles = p.tiles ? static_cast<int>(max(0ll, min(static_cast<long long>(*p.num_tiles), p.cap)))
                                 : static_cast<int>(p.cap);
-  const unsigned col_units = (p.col_blocks + kShare - 1) / kShare;
-  const unsigned units = num_tiles * col_units * p.splits;   // (the host keeps them below 2^31)
-  constexpr int kCtas = kGroup != kAlone ? 2 : 1;
+  const unsigned units = num_tiles * p.col_blocks * p.splits;   // (the host keeps them below 2^31)
+  constexpr int kCtas = kPair ? 2 : 1;
   const unsigned unit0 = blockIdx.x / kCtas, unit_step = gridDim.x / kCtas;
   const int stages = p.stages, accs = p.accs;
   int* const err = p.err;
@@ -524,7 +482,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
       long long issued = 0;
       bool ok = true, ready = false;
       for (unsigned u = unit0; ok && u < units; u += unit_step) {
-        const Unit t = unit_at<kShare>(p, u, num_tiles, col_units, sharer);
+        const Unit t = unit_at(p, u, num_tiles);
         if (!t.ok) {
           if (is_b && first && leader) record_error(err, TQ_ERR_INVALID_ARG, kWhereTileLoad);
           continue;
@@ -535,11 +493,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
         const int copies = gathered(t.rows);
         uint32_t bytes = static_cast<uint32_t>(is_b ? kBBytes : 0) * (kPair ? 2 : 1);
         if (gather) {
-          if (kShared)
-            bytes += 4 * kStepBytes * (shared_copies(part_of(copies, 0), lead, share) +
-                                       shared_copies(part_of(copies, 1), lead, share));
-          else
-            bytes += 4 * kStepBytes * shared_copies(copies, lead, share);
+          bytes += 4 * kStepBytes * shared_copies(copies, lead, share);
           __syncwarp();
           for (int i = lane; i < 16 * share; i += 32) {
             const int in = 32 * (i / (4 * share)) + 4 * lead + i % (4 * share);   // row of the tile
@@ -574,21 +528,16 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
             }
             if (gather) {
 #pragma unroll
-              for (int j = 0; j < kRows / (4 * kShare); j += 8) {
+              for (int j = 0; j < kRows / 4; j += 8) {
 #pragma unroll
                 for (int i = 0; i < 3; ++i) {
-                  const int c = sharer * (kRows / 8) + j + lead + i;
+                  const int c = j + lead + i;
                   if (i < share && c < copies) {
                     const int4 rows = *reinterpret_cast<const int4*>(list + 4 * c);
-                    if constexpr (kShared)
-                      load_rows_to_both(dst + 4 * c * kStepBytes, &tm_a, at, rows, full);
-                    else
-                      tma_gather4_2d(dst + 4 * c * kStepBytes, &tm_a, at, rows.x, rows.y, rows.z, rows.w, full);
+                    tma_gather4_2d(dst + 4 * c * kStepBytes, &tm_a, at, rows.x, rows.y, rows.z, rows.w, full);
                   }
                 }
               }
-            } else if (kShared && !is_b) {
-              load_box_to_both(dst + 8192 * sharer, &tm_a, at, row0 + 64 * sharer, full);
             } else if (!is_b) {
 #pragma unroll
               for (int i = 0; i < kABoxes; ++i)
@@ -633,7 +582,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
       const bool leader = elect_one();
       Ring acc;
       for (unsigned u = unit0; u < units; u += unit_step) {
-        const Unit t = unit_at<kShare>(p, u, num_tiles, col_units, sharer);
+        const Unit t = unit_at(p, u, num_tiles);
         if (!t.ok) continue;
         for (int k = t.k0; k < t.k1; ++k) {
           if (k8 || k == t.k0) {
@@ -659,8 +608,8 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
             for (int i = 0; i < 4; ++i)
               mma<k8, kPair>(d, a + i * (kAMn ? 128 : 2), b + i * (kBMn ? 128 : 2), idesc,
                              (i != 0 || (!k8 && k != t.k0)) ? 1u : 0u);
-            commit<kPair, kShared>(this_bar + 8 * kMaxStages);   // the stage's empty barrier
-            if (last) commit<kPair, false>(bar_accfull + 8 * acc.at);
+            commit<kPair>(this_bar + 8 * kMaxStages);   // the stage's empty barrier
+            if (last) commit<kPair>(bar_accfull + 8 * acc.at);
           }
           if (last) acc.advance(accs);
           if (*abort_flag) break;
@@ -694,7 +643,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     int parity = 0;
     Ring acc;
     for (unsigned u = unit0; u < units; u += unit_step) {
-      const Unit t = unit_at<kShare>(p, u, num_tiles, col_units, sharer);
+      const Unit t = unit_at(p, u, num_tiles);
       if (!t.ok) continue;
       const int in_tile = rank * kRows + 32 * q + lane;
       const int slot = t.slot0 + min(in_tile, t.rows - 1);
@@ -867,7 +816,7 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
   pdl_trigger();
   tc_fence_before();
   __syncthreads();
-  if (kGroup != kAlone) cluster_sync();   // no CTA's memory is needed by another any more
+  if (kPair) cluster_sync();   // neither CTA's memory is needed by the other any more
   if (warp == kWarpA) {
     tc_fence_after();
     free_columns<kPair>(tmem, static_cast<uint32_t>(p.tmem_cols));
@@ -876,11 +825,10 @@ tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
 
 // Launches one variant; `units` bounds the units of a launch whose tile map is on the
 // device.  Stages, accumulators and shared memory are filled in here.
-template <bool k8, Group kGroup, int kCols, bool kAMn, bool kBMn, int kEpi>
+template <bool k8, bool kPair, int kCols, bool kAMn, bool kBMn, int kEpi>
 int launch(Params p, const CUtensorMap& a, const CUtensorMap& b, long long units, cudaStream_t s) {
-  constexpr bool kPair = kGroup == kPaired;
-  constexpr int kCtas = kGroup != kAlone ? 2 : 1;
-  auto kernel = tile_gemm_kernel<k8, kGroup, kCols, kAMn, kBMn, kEpi>;
+  constexpr int kCtas = kPair ? 2 : 1;
+  auto kernel = tile_gemm_kernel<k8, kPair, kCols, kAMn, kBMn, kEpi>;
   static std::atomic<uint64_t> allowed{0};   // bit d: device d
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) {

@@ -9,7 +9,6 @@ namespace tq {
 
 struct TileChoice {
   int tile_m;   // 128, or 256: a pair of CTAs
-  bool shared;  // two column blocks share the copies of their rows
   int cols;     // half the columns of a unit
   int splits;
   double cost;
@@ -21,44 +20,47 @@ enum class TileRows { kOne, kGathered, kSlots };
 
 // By the time that the parts take (cycles of an SM; of two where they work together): a
 // step, by its bytes at 50 a clock, its MMAs and the way of an accumulator to the
-// epilogue and back, or the copies of its gathered rows; a unit's first copies, last
+// epilogue and back; with the copies of gathered rows, `gathered` for a full tile and 24
+// less for each copy of four rows that it lacks; a unit's first copies, last
 // drain and stores; the matrices from memory at 3400 bytes a clock over the chip; the
 // partial sums of splits (and of experts' pairs, `partial`) written and read again at
 // 3000 bytes a clock, and the launch that adds them up.  `rows` rows for each of
 // `matrices` matrices; N columns, of h when gated (no splits: the activation needs whole
 // sums).
 // Measured: 8192 rows 4096 -> 4096 of one matrix 130 us by pairs (its quantising
-// included), 142 by CTAs alone; 8192 tokens on 256 experts 4096 -> 2048 758 us by pairs
-// of pairs that share their rows, 695 by CTAs that do.
+// included), 142 by CTAs alone.  Experts 4096 -> 2048, of 128, 64 and 32 columns a half:
+// 256 rows for each of 76 213, 340 and 639 us, 96 for each of 152 260, 292 and 535; 512
+// tokens of top-6 of 256 351, 357 and 588.
 inline TileChoice choose_tile(bool k8, double rows, double matrices, int steps, int64_t N, bool gated, TileRows kind,
                               bool partial, bool takes_splits, int only_cols = 0) {
   struct Variant {
     int tile_m;
-    bool shared;
     int cols;
     double step, gathered, step16;
   };
-  static constexpr Variant kVariants[] = {{256, false, 128, 980, 0, 740},
-                                          {128, true, 128, 980, 980, 0},
-                                          {128, false, 128, 1000, 1650, 980},
-                                          {128, false, 64, 660, 1650, 660},
-                                          {128, false, 32, 500, 1650, 0}};
+  static constexpr Variant kVariants[] = {{256, 128, 980, 0, 740},
+                                          {128, 128, 1000, 1440, 980},
+                                          {128, 64, 660, 1180, 660},
+                                          {128, 32, 500, 1120, 0}};
   const int sms = sm_count();
   const double weights = matrices * N * (gated ? 2 : 1) * steps * 128.0 / 3400.0;
-  TileChoice best{128, false, 128, 1, 1e300};
+  TileChoice best{128, 128, 1, 1e300};
   for (const Variant& v : kVariants) {
-    if (((kind == TileRows::kOne) ? v.shared : v.tile_m > 128) || (!k8 && v.step16 == 0)) continue;
+    if ((kind != TileRows::kOne && v.tile_m > 128) || (!k8 && v.step16 == 0)) continue;
     if ((gated && v.cols < 64) || (only_cols && (v.cols != only_cols || v.tile_m > 128))) continue;
-    const int together = v.tile_m > 128 || v.shared ? 2 : 1;
+    const int together = v.tile_m > 128 ? 2 : 1;
     const double tiles = matrices * std::ceil(rows / v.tile_m);
-    const double columns = (gated ? v.cols : 2 * v.cols) * (v.shared ? 2 : 1);
+    const double columns = gated ? v.cols : 2 * v.cols;
     const double units = tiles * std::ceil(static_cast<double>(N) / columns);
-    const double step = !k8 ? v.step16 : kind == TileRows::kGathered ? v.gathered : v.step;
+    const double copies = std::ceil(rows / std::ceil(rows / v.tile_m) / 4.0);   // of a tile
+    const double step = !k8                          ? v.step16
+                        : kind == TileRows::kGathered ? std::max(v.step, v.gathered - 24.0 * (32.0 - copies))
+                                                      : v.step;
     for (int s = 1; s <= (takes_splits ? std::min(16, steps) : 1); ++s) {
       const double unit = ((steps + s - 1) / s) * step + 24.0 * v.cols + 1500.0;
       double cost = 4000.0 + std::max(std::ceil(units * s / (sms / together)) * unit, weights);
       if (s > 1 || partial) cost += 9000.0 + 8.0 * s * rows * matrices * N / 3000.0;
-      if (cost < best.cost * 0.99) best = {v.tile_m, v.shared, v.cols, s, cost};
+      if (cost < best.cost * 0.99) best = {v.tile_m, v.cols, s, cost};
     }
   }
   return best;
