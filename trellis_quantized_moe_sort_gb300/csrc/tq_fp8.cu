@@ -353,7 +353,7 @@ int tq_fp8_moe_mlp_forward(const uint8_t* x, const float* x_scales, const uint8_
   if (rc != TQ_OK) return rc;
   if (m.arm == kTiles) {
     Fp8Gemm g{x, x_scales, n, w_gu, gu_scales, r.sorted_pairs, r.tiles, r.num_tiles, m.cap, m.P, top_k, E, H, I, true,
-              false, true, m.tile_m, 128, 1, nullptr, I, TQ_FP32, p.h, p.h_scales, err};
+              false, true, m.tile_m, p.gu.cols, 1, nullptr, I, TQ_FP32, p.h, p.h_scales, err};
     rc = launch_fp8_gemm(g, s);
   } else {
     FewRows f = few_rows({x, x_scales}, {w_gu, gu_scales}, m.P, top_k, E, H, I, true, p.h32, TQ_FP32, err);

@@ -6,6 +6,7 @@
 namespace tq {
 int launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
   using namespace tile;
+  if ((g.gated || g.tile_m > kRows) && g.cols != 128) return TQ_ERR_INVALID_ARG;
   Params p{};
   const bool pair = g.tile_m > kRows;
   p.tiles = g.tiles;

@@ -47,7 +47,8 @@ inline TileChoice choose_tile(bool k8, double rows, double matrices, int steps, 
   TileChoice best{128, 128, 1, 1e300};
   for (const Variant& v : kVariants) {
     if ((kind != TileRows::kOne && v.tile_m > 128) || (!k8 && v.step16 == 0)) continue;
-    if ((gated && v.cols < 64) || (only_cols && (v.cols != only_cols || v.tile_m > 128))) continue;
+    if (gated && v.cols < (k8 ? 128 : 64)) continue;   // (in 8 bits a block of h is one unit's columns)
+    if (only_cols && (v.cols != only_cols || v.tile_m > 128)) continue;
     const int together = v.tile_m > 128 ? 2 : 1;
     const double tiles = matrices * std::ceil(rows / v.tile_m);
     const double columns = gated ? v.cols : 2 * v.cols;
