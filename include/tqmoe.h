@@ -629,8 +629,8 @@ int tq_rms_norm_backward(const void* grad_y, int64_t grad_y_stride, const void* 
  * rows_per_block is 1 (activations) or 128 (weights).  Both quotients are rounded
  * to fp32 and the conversion to nearest even, saturating.  NaN is kept as NaN and
  * does not count for the maximum, an infinity counts as the largest finite number
- * and is kept as 448 (so code * s is that number).  In a block with s = 0 all but
- * NaN is kept as 0.
+ * and is kept as 448 (so code * s is that number).  Zeros keep their sign.  In a block
+ * with s = 0 all but NaN is kept as 0 (code 0).
  *
  * tq_fp8_quantize: x (device) E matrices of n rows of K x_type values, x_stride
  *   elements apart (matrix e starts at row e * n), base and rows 16-byte aligned ->

@@ -6,8 +6,9 @@
 // to nearest even: 16-bit values often lie on a border of the E4M3 grid, where a
 // product with a reciprocal falls to the other side.  NaN is kept as NaN and does
 // not count for the maximum; an infinity counts as the largest finite number and is
-// kept as 448.  In a block whose scale is 0 (no value but zeros, NaN or ones whose
-// quotient by 448 underflows) all but NaN is kept as 0.
+// kept as 448.  Zeros, and values that round to 0, keep their sign.  In a block whose scale
+// is 0 (no value but zeros, NaN or ones whose quotient by 448 underflows) all but NaN is
+// kept as 0.
 #pragma once
 #include <cfloat>
 
@@ -24,6 +25,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a
 __device__ __forceinline__ float2 sub2(float2 a, float2 b) { return __ffma2_rn(b, make_float2(-1.f, -1.f), a); }
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 fma2_down(float2 a, float2 b, float2 c) { return __ffma2_rd(a, b, c); }
 
 // Largest magnitude; NaN is passed over.
 template <int kCount>
@@ -41,10 +43,11 @@ __device__ __forceinline__ float fp8_top(const float (&v)[kCount]) {
 // That holds while nothing under- or overflows on the way: b within 2^-80 .. 2^100,
 // and quotients, here at most 449, that matter for E4M3 (2^-11 and more) then have
 // remainders of at least 2^-137, above fp32's smallest 2^-149.  Infinities come with
-// b = FLT_MAX / 448 and take the division.
+// b = FLT_MAX / 448 and take the division.  A remainder of 0 is -0 by its rounding down,
+// which leaves a quotient of -0 its sign.
 __device__ __forceinline__ float fp8_divide(float a, float b, float r) {
   const float q = __fmul_rn(a, r);
-  return __fmaf_rn(__fmaf_rn(-q, b, a), r, q);
+  return __fmaf_rn(__fmaf_rd(-q, b, a), r, q);
 }
 struct Fp8Scale {
   float s, r;
@@ -92,7 +95,7 @@ __device__ __forceinline__ uint4 fp8_codes16(const float* v, const Fp8Scale& s) 
     for (int i = 0; i < 8; ++i) {   // fp8_divide, two at a time
       const float2 a = make_float2(v[2 * i], v[2 * i + 1]);
       q[i] = mul2(a, r);
-      q[i] = fma2(fma2(q[i], minus, a), r, q[i]);
+      q[i] = fma2(fma2_down(q[i], minus, a), r, q[i]);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = e4m3x4(q[2 * i].x, q[2 * i].y, q[2 * i + 1].x, q[2 * i + 1].y);
