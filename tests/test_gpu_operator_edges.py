@@ -69,3 +69,75 @@ def test_norm_codes_keep_the_sign_of_zero():
     assert torch.equal(codes.view(torch.uint8), want) and torch.equal(plain[0].view(torch.uint8), want)
     assert (want == 0x80).any() and (want == 0).any()
     check_no_device_error()
+
+
+# ------------------------------------------------------------------ gates
+
+# Tolerance of h = g e u / (1 + e), e = exp(-|g|) for these gates: e is off by two of its own
+# steps (2^-149 where it is subnormal), the other operations by 6 x 2^-24 together, and h is
+# rounded once.
+def _gated(gates, up):
+    g = gates.double()
+    e = torch.exp(g)
+    h = g * e / (1 + e) * up
+    return h, (2 * 2.0 ** -149 * g.abs() * up + 12 * 2.0 ** -24 * h.abs()), e
+
+
+@pytest.mark.parametrize("n,H,I,kernels", [(4, 64, 64, ("few_rows",)), (128, 4096, 2048, ("gemm_f16", "swiglu_sum")),
+                                           (1500, 64, 64, ("gemm_f16",))])
+def test_gates_of_large_magnitude(n, H, I, kernels):
+    """silu of gates around -88, whose exponential passes 2^126, is still a number: -5e-37, and
+    with a large up projection an ordinary one."""
+    up = 2.0 ** 40
+    values = torch.arange(-94.0, -80.0, 0.5)   # each has 8 bits
+    gates = values.repeat(I // len(values) + 1)[:I].cuda()
+    x = torch.zeros((n, H), dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 1.0
+    w = torch.zeros((2 * I, H), dtype=torch.bfloat16, device="cuda")
+    w[:I, 0], w[I:, 0] = gates.to(torch.bfloat16), up
+    want, bound, e = _gated(gates, up)
+    gate_up = torch.empty((n, 2 * I), device="cuda")
+    h = _ran(lambda: tq.tq_swiglu_linear(x, w, gate_up=gate_up), *kernels)
+    assert torch.equal(gate_up[:, :I], gates.expand(n, I)) and (gate_up[:, I:] == up).all()
+    assert ((h.double() - want).abs() <= bound + BF16 * want.abs()).all()
+    # d = [dgate dup] by grad_w of a single row (the others' dh is 0): x is 1 in its first column
+    dh = torch.zeros((n, I), dtype=torch.bfloat16, device="cuda")
+    dh[0] = 1.0
+    _, grad_w = _ran(lambda: tq.tq_swiglu_linear_backward(x, w, dh, gate_up=gate_up), "swiglu_grad")
+    g, s = gates.double(), e / (1 + e)
+    d = torch.cat((up * s * (1 + g * (1 - s)), g * s))
+    wide = torch.cat((2 * 2.0 ** -149 * up * (1 + g.abs()), 2 * 2.0 ** -149 * g.abs())) + 16 * 2.0 ** -24 * d.abs()
+    # the product reads d rounded to the type, and is rounded itself (to bf16's smallest step at least)
+    assert ((grad_w[:, 0].double() - d).abs() <= wide + 2.01 * BF16 * d.abs() + 2.0 ** -133).all()
+    assert (grad_w[:, 1:] == 0).all()
+    check_no_device_error()
+
+
+@pytest.mark.parametrize("n,kernel", [(1, "few_rows"), (2048, "fp8_gemm")])
+def test_expert_gates_of_large_magnitude(n, kernel):
+    """The same in 8 bits: gates of -88 and around it, one to each block of 128."""
+    H, I, up = 256, 512, 448.0 * 2.0 ** 30
+    x = torch.zeros((n, H), dtype=torch.float8_e4m3fn, device="cuda").view(torch.uint8)
+    x[:, 0] = 0x38   # 1
+    x_scales = torch.ones((n, 2), device="cuda")
+    w_gu = torch.zeros((1, 2 * I, H), dtype=torch.uint8, device="cuda")
+    w_gu[0, :I, 0] = torch.tensor(-88.0).to(torch.float8_e4m3fn).view(torch.uint8).item()
+    w_gu[0, I:, 0] = 0x7e   # 448
+    gu_scales = torch.ones((1, 8, 2), device="cuda")
+    gu_scales[0, :4, 0] = torch.tensor([0.995, 1.0, 1.003, 1.006], device="cuda")
+    gu_scales[0, 4:] = 2.0 ** 30
+    # y[j] = h of column 128 j, for j < 4
+    w_down = torch.zeros((1, H, I), dtype=torch.uint8, device="cuda")
+    for j in range(4):
+        w_down[0, j, 128 * j] = 0x38
+    down_scales = torch.ones((1, 2, 4), device="cuda")
+    ids = torch.zeros((n, 1), dtype=torch.int32, device="cuda")
+    y = _ran(lambda: tq.tq_fp8_moe_mlp_forward(x, x_scales, w_gu, gu_scales, w_down, down_scales, ids,
+                                               torch.ones((n, 1), device="cuda"), dtype=torch.float32), kernel)
+    # h is the largest of its block: code 448, scale h / 448 rounded, and their product rounded
+    gates = (-88.0 * gu_scales[0, :4, 0].double()).float()
+    want, bound, _ = _gated(gates, up)
+    # (the gate is rounded to 2^-24 of itself, by which h moves 88 times as much)
+    assert ((y[:, :4].double() - want).abs() <= bound + (4 + 90) * 2.0 ** -24 * want.abs()).all()
+    assert (y[:, 4:] == 0).all()
+    check_no_device_error()

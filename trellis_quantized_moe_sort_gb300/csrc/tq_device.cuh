@@ -289,11 +289,16 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(uint32_t M, uint32_t N) {
          | ((M >> 4) << 24);    // M / 16
 }
 
-// 1 / (1 + exp(-g)) and g times that, to about |g| 2^-23 of themselves: for gates that are
-// sums of products, off by more, and for results that are kept in 16 or 8 bits.  With expf
-// and a division the 64 of them that a thread of the tile products has to do a unit took
-// 11000 cycles while the MMAs waited (4735 rows 664 -> 2 x 1240: 38 us, 22 so).
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + __expf(-g)); }
+// 1 / (1 + exp(-g)) and g times that.  With e = exp(-|g|) the denominator 1 + e is between 1
+// and 2 for every g, where __fdividef is within 2 ulp: a few ulp in all, down to the
+// subnormal e of g < -87 (1 + exp(-g) would pass 2^126 there, where __fdividef gives 0).
+__device__ __forceinline__ float sigmoid(float g) {
+  const float e = expf(-fabsf(g));
+  return __fdividef(g < 0.f ? e : 1.f, 1.f + e);
+}
+__device__ __forceinline__ float silu(float g) {
+  const float e = expf(-fabsf(g));
+  return __fdividef(g < 0.f ? g * e : g, 1.f + e);
+}
 
 }  // namespace tq
