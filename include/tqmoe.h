@@ -649,8 +649,10 @@ int tq_fp8_dequantize(const uint8_t* codes, const float* scales, int E, int64_t 
 /* ---------------------------------------------------------------------------
  * Products of 8-bit block-scaled rows x (rows_per_block 1) with 8-bit matrices
  * (rows_per_block 128).  The partial sums of each block of 128 are accumulated in
- * fp32, multiplied by the product of both scales, which has to be in fp32's range, and
- * added up in fp32; the result is rounded once to y_type.  Sums have a fixed order, so
+ * fp32, multiplied by the product of both scales, which has to be in fp32's range (the
+ * scale of a block with an infinity is 2^119: its weights' scales have to be at most 448,
+ * or results are infinite or NaN), and added up in fp32, pair by pair before topk_w
+ * multiplies them; the result is rounded once to y_type.  Sums have a fixed order, so
  * results repeat bit for bit.
  *
  * tq_fp8_linear:      y[t] = W x[t], w [N][K], w_scales [ceil(N/128)][ceil(K/128)].

@@ -141,3 +141,31 @@ def test_expert_gates_of_large_magnitude(n, kernel):
     assert ((y[:, :4].double() - want).abs() <= bound + (4 + 90) * 2.0 ** -24 * want.abs()).all()
     assert (y[:, 4:] == 0).all()
     check_no_device_error()
+
+
+# ------------------------------------------------------------------ router weights
+
+@pytest.mark.parametrize("x_exp,w_exp,weight_exp", [(-50, -60, -30), (40, 60, -110), (-100, 120, 10), (100, -120, -10),
+                                                    (0, 0, 0)])
+@pytest.mark.parametrize("n,E,kernel", [(2, 64, "few_rows"), (2048, 4, "fp8_gemm")])
+def test_scales_and_router_weights_far_from_one(n, E, kernel, x_exp, w_exp, weight_exp):
+    """The scales' product is in fp32's range, and so are W x of each expert and the result: a
+    router weight that takes one of the scales out of that range changes nothing."""
+    K, N, top_k = 400, 48, 2
+    g = torch.Generator(device="cuda").manual_seed(8)
+    codes = lambda *s: (100.0 * torch.randn(s, device="cuda", generator=g)).clamp(-448, 448).to(torch.float8_e4m3fn)
+    x, w = codes(n, K), codes(E, N, K)
+    x_scales = torch.full((n, 4), 2.0 ** x_exp, device="cuda")
+    w_scales = torch.full((E, 1, 4), 2.0 ** w_exp, device="cuda")
+    ids = (torch.arange(n * top_k, device="cuda", dtype=torch.int32) % E).view(n, top_k)
+    topk_w = (1 + torch.rand((n, top_k), device="cuda", generator=g)) * 2.0 ** weight_exp
+    y = _ran(lambda: tq.tq_fp8_moe_forward(x, x_scales, w, w_scales, ids, topk_w, dtype=torch.float32), kernel)
+    scale = 2.0 ** (x_exp + w_exp)
+    picked = w.double()[ids.long()]   # [n, top_k, N, K]
+    want = torch.einsum("nk,nj,njrk->nr", x.double(), topk_w.double(), picked) * scale
+    size = torch.einsum("nk,nj,njrk->nr", x.double().abs(), topk_w.double(), picked.abs()) * scale
+    # a block of 128 in any order, four blocks, two pairs and their weights; results near the smallest normal number
+    bound = (160 + 4 + 6) * 2.0 ** -23 * size + 8 * 2.0 ** -149
+    assert want.abs().max() > 2.0 ** -126
+    assert ((y.double() - want).abs() <= bound).all()
+    check_no_device_error()

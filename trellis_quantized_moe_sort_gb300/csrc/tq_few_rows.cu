@@ -22,8 +22,10 @@
 // start and its last sums show).  From where experts share tokens on the tensor-memory
 // tiles are faster (16 tokens of top-6 of 256, 4096 -> 2048: 156 us here, 138 there).
 //
-// A single token's experts are the segments of one unit, whose sums, weighted, add up
-// in the same registers: its product is this one launch.
+// A single token's experts are the segments of one unit: the sums of each are added,
+// weighted, to the token's, and its product is this one launch.  (The weight does not
+// multiply a scale: the two scales' product is in fp32's range, one scale's with the
+// router's weight need not be.)
 //
 // 8-bit products: 128 bytes are a scale block, whose partial sums are scaled into
 // fp32 registers.
@@ -284,6 +286,16 @@ __global__ void __launch_bounds__(kThreads, 2) few_rows_kernel(const FewRows p, 
   }
 
   float sum[kTiles][4] = {};
+  float total[kTiles][4] = {};   // of the segments before the present one, weighted
+  auto end_segment = [&] {
+#pragma unroll
+    for (int c = 0; c < kTiles; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (live) total[c][j] = fmaf(sum[c][j], weight, total[c][j]);
+        sum[c][j] = 0.f;
+      }
+  };
   int buffer = 0, slot = 0;
   const int per_unit = (p.steps - warp + kWarps - 1) / kWarps;   // steps of this warp, without segments
   // One step, its x in `now`; false after the last.
@@ -304,7 +316,6 @@ __global__ void __launch_bounds__(kThreads, 2) few_rows_kernel(const FewRows p, 
             for (int j = 0; j < 4; ++j) part[c][j] = 0.f;
         }
         auto& to = either<kKind == kFp8>(part, sum);
-        const float f0 = w0 * weight, f1 = w1 * weight;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const uint4 lo = read16(src + 512 * j), hi = read16(src + 512 * (2 + j));
@@ -318,10 +329,10 @@ __global__ void __launch_bounds__(kThreads, 2) few_rows_kernel(const FewRows p, 
         if constexpr (kKind == kFp8) {
 #pragma unroll
           for (int c = 0; c < kTiles; ++c) {
-            sum[c][0] = fmaf(part[c][0], now.s0[c] * f0, sum[c][0]);
-            sum[c][1] = fmaf(part[c][1], now.s1[c] * f0, sum[c][1]);
-            sum[c][2] = fmaf(part[c][2], now.s0[c] * f1, sum[c][2]);
-            sum[c][3] = fmaf(part[c][3], now.s1[c] * f1, sum[c][3]);
+            sum[c][0] = fmaf(part[c][0], now.s0[c] * w0, sum[c][0]);
+            sum[c][1] = fmaf(part[c][1], now.s1[c] * w0, sum[c][1]);
+            sum[c][2] = fmaf(part[c][2], now.s0[c] * w1, sum[c][2]);
+            sum[c][3] = fmaf(part[c][3], now.s1[c] * w1, sum[c][3]);
           }
         }
       }
@@ -330,6 +341,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_rows_kernel(const FewRows p, 
       if (++slot == kAhead) slot = 0;
       here.k += kWarps;
       const bool moved = here.settle(p);
+      if (kSegments && moved) end_segment();
       if (!here.past_unit(p)) {
         if (moved) {
           live = enter_segment();
@@ -344,8 +356,8 @@ __global__ void __launch_bounds__(kThreads, 2) few_rows_kernel(const FewRows p, 
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         *reinterpret_cast<float2*>(&sums[buffer][warp][g + 8 * h][8 * c + 2 * q]) =
-            make_float2(sum[c][2 * h], sum[c][2 * h + 1]);
-        sum[c][2 * h] = sum[c][2 * h + 1] = 0.f;
+            kSegments ? make_float2(total[c][2 * h], total[c][2 * h + 1]) : make_float2(sum[c][2 * h], sum[c][2 * h + 1]);
+        sum[c][2 * h] = sum[c][2 * h + 1] = total[c][2 * h] = total[c][2 * h + 1] = 0.f;
       }
     }
     __syncthreads();   // (a buffer is written again after the next unit's barrier)
