@@ -599,7 +599,7 @@ int tq_fp4_moe_mlp_forward(const void* x, int x_type, int64_t x_stride,
  * rstd (device) fp32 [n] or NULL: what the gradient takes.
  * codes (device) uint8 [n][K], 16-byte aligned, and scales (device) fp32
  *   [n][ceil(K / 128)], or both NULL.
- * Outputs that share memory with the rows in another way, or with each other, are
+ * Outputs that share memory with an input in another way, or with each other, are
  * refused.  Limits: 1 <= K <= TQ_NORM_MAX_WIDTH, eps >= 0 and finite.
  *
  * tq_rms_norm_backward: with x the normed rows (residual_out of the forward call,
@@ -608,7 +608,9 @@ int tq_fp4_moe_mlp_forward(const void* x, int x_type, int64_t x_stride,
  *   dense [n][K]: the gradient of x and of the residual alike;
  *   grad_weight[k] = sum over rows of grad_y * x * rstd, in w_type, or NULL.
  *   grad_residual (what arrives through residual_out) may be NULL.  Sums are fp32
- *   in a fixed order.  grad_x may be x, grad_y or grad_residual where that is dense.
+ *   in a fixed order.  grad_x may be x, grad_y or grad_residual where that is dense;
+ *   results and workspace that share other memory with an input or each other are
+ *   refused.
  *   workspace (device, 256-byte aligned) of tq_rms_norm_backward_workspace_size()
  *   bytes (0 on invalid arguments); not used without grad_weight.
  * ------------------------------------------------------------------------- */
@@ -638,8 +640,8 @@ int tq_rms_norm_backward(const void* grad_y, int64_t grad_y_stride, const void* 
  *   [E][ceil(n / rows_per_block)][ceil(K / 128)].
  * tq_fp8_dequantize: code * s rounded once to out_type; out (device) [E][n][K],
  *   16-byte aligned.
- * Limits: E * n below 2^31 - 1024; with rows_per_block 128 also E <= 65535.  The
- * output may not share memory with the input.
+ * Limits: E * n below 2^31 - 1024; with rows_per_block 128 also E <= 65535.  No
+ * output may share memory with an input or the other output.
  * ------------------------------------------------------------------------- */
 int tq_fp8_quantize(const void* x, int x_type, int64_t x_stride, int E, int64_t n, int K, int rows_per_block,
                     uint8_t* codes, float* scales, tq_stream_t stream);
@@ -664,7 +666,8 @@ int tq_fp8_dequantize(const uint8_t* codes, const float* scales, int E, int64_t 
  *   h = silu(gate) * up per pair in fp32, kept in 8 bits (blocks of 128 of a row),
  *   y[t] = sum_j topk_w[t][j] W_down h(t,j).  E = 1, top_k = 1: a dense MLP.
  * x, w (device) codes, 16-byte aligned; x_scales (device) fp32 [n][ceil(K/128)];
- * y (device) dense, apart from x and the weights.  K and H are multiples of 16, N is
+ * y (device) dense; y and a workspace that is used may not share memory with an input
+ * or each other.  K and H are multiples of 16, N is
  * any width.  E <= 1024, top_k <= 32; n * top_k and E * N (E * 2I, E * H) below 2^31 -
  * 1024, n * top_k * N below 2^57.  workspace (device) of at least the matching
  * *_workspace_size() bytes (0 on invalid arguments; 256, or a NULL workspace, where none
@@ -705,8 +708,8 @@ int tq_fp8_moe_mlp_forward(const uint8_t* x, const float* x_scales, const uint8_
  *   the forward call's, or NULL: computed again from x and w_gu.  Sums have a fixed
  *   order.  workspace (device, 256-byte aligned) of
  *   tq_swiglu_linear_backward_workspace_size() bytes (0 on invalid arguments).
- * Outputs may not share memory with x, w_gu or each other (grad_x may lie over grad_h
- * or gate_up).  Limits: n, 2I and H below 2^31 - 1024, products of two of them below
+ * Outputs and workspace may not share memory with x, w_gu or each other, the workspace
+ * not with grad_h or gate_up either (grad_x may lie over those).  Limits: n, 2I and H below 2^31 - 1024, products of two of them below
  * 2^57.
  * ------------------------------------------------------------------------- */
 size_t tq_swiglu_linear_workspace_size(int64_t n, int H, int I);

@@ -169,3 +169,31 @@ def test_scales_and_router_weights_far_from_one(n, E, kernel, x_exp, w_exp, weig
     assert want.abs().max() > 2.0 ** -126
     assert ((y.double() - want).abs() <= bound).all()
     check_no_device_error()
+
+
+# ------------------------------------------------------------------ workspaces
+
+def test_results_in_a_used_workspace_are_refused():
+    """Where K is split the partial sums are read while results are written."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    n, K, N = 300, 4096, 256
+    x, x_scales = tq.tq_fp8_quantize(torch.randn((n, K), device="cuda", generator=g))
+    w, w_scales = tq.tq_fp8_quantize(torch.randn((N, K), device="cuda", generator=g), 128)
+    size = tq.tq_fp8_linear_workspace_size(n, K, N)
+    assert size > 256
+    work = torch.empty(size, dtype=torch.uint8, device="cuda")
+    y = tq.tq_fp8_linear(x, x_scales, w, w_scales, workspace=work)
+    inside = work[:2 * n * N].view(torch.bfloat16).view(n, N)
+    with pytest.raises(tq.TQError):
+        tq.tq_fp8_linear(x, x_scales, w, w_scales, workspace=work, y=inside)
+    assert torch.equal(y, tq.tq_fp8_linear(x, x_scales, w, w_scales))
+    n, H, I = 128, 4096, 2048
+    x = torch.randn((n, H), device="cuda", generator=g).bfloat16()
+    w = (torch.randn((2 * I, H), device="cuda", generator=g) / H ** 0.5).bfloat16()
+    size = tq.tq_swiglu_linear_workspace_size(n, H, I)
+    assert size > 256
+    work = torch.empty(size, dtype=torch.uint8, device="cuda")
+    with pytest.raises(tq.TQError):
+        tq.tq_swiglu_linear(x, w, h=work[:2 * n * I].view(torch.bfloat16).view(n, I), workspace=work)
+    assert torch.equal(tq.tq_swiglu_linear(x, w, workspace=work), tq.tq_swiglu_linear(x, w))
+    check_no_device_error()

@@ -31,12 +31,9 @@ bool bad_moe_shape(int64_t n, int top_k, int E) {
          n * top_k >= kMaxIndex;
 }
 bool bad_blocking(int rows_per_block) { return rows_per_block != 1 && rows_per_block != kFp8Block; }
-// Results that would be written over activations or weights still to be read.
-bool bad_place(const void* y, int64_t n, int64_t N, int y_type, const void* x, int64_t x_bytes, const void* w,
-               int64_t w_bytes) {
-  const int64_t bytes = n * N * static_cast<int64_t>(type_size(y_type));
-  return overlap(y, bytes, x, x_bytes) || overlap(y, n > 0 ? bytes : 0, w, w_bytes);
-}
+// What codes and scales of E matrices of n rows of K take, in blocks of `rows` x 128.
+int64_t scale_bytes(int64_t E, int64_t n, int K, int rows) { return 4 * E * ((n + rows - 1) / rows) * blocks_of(K); }
+int64_t y_bytes(int64_t n, int64_t N, int y_type) { return n * N * static_cast<int64_t>(type_size(y_type)); }
 bool bad_workspace(const void* p, size_t bytes, size_t need) { return !p || bytes < need || !aligned(p, 256); }
 
 // Takes 256-byte aligned regions from a buffer, or only counts their bytes.
@@ -236,7 +233,8 @@ int tq_fp8_quantize(const void* x, int x_type, int64_t x_stride, int E, int64_t 
   if (rows > 0 && (!x || !codes || !scales || !aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4)))
     return TQ_ERR_INVALID_ARG;
   if (rows_per_block != 1 && (n + kFp8Block - 1) / kFp8Block > 65535) return TQ_ERR_INVALID_ARG;
-  if (overlap(codes, rows * K, x, row_bytes(rows, x_stride, K, static_cast<int64_t>(type_size(x_type)))))
+  if (outputs_overlap({{codes, rows * K}, {scales, scale_bytes(E, n, K, rows_per_block)}},
+                      {{x, row_bytes(rows, x_stride, K, static_cast<int64_t>(type_size(x_type)))}}))
     return TQ_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int rc = require_sm103(s);
@@ -252,7 +250,8 @@ int tq_fp8_dequantize(const uint8_t* codes, const float* scales, int E, int64_t 
       bad_blocking(rows_per_block) || bad_output(E * n, K))
     return TQ_ERR_INVALID_ARG;
   if (E * n > 0 && (!codes || !scales || !out || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(out, 16) ||
-                    overlap(out, E * n * K * static_cast<int64_t>(type_size(out_type)), codes, E * n * K)))
+                    outputs_overlap({{out, y_bytes(E * n, K, out_type)}},
+                                    {{codes, E * n * K}, {scales, scale_bytes(E, n, K, rows_per_block)}})))
     return TQ_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int rc = require_sm103(s);
@@ -274,7 +273,10 @@ int tq_fp8_linear(const uint8_t* x, const float* x_scales, const uint8_t* w, con
   const LinearPlan l = plan_linear(workspace, n, K, N);
   const bool splits = !l.few && l.tile.splits > 1;
   if (n > 0 && splits && bad_workspace(workspace, workspace_bytes, l.bytes)) return TQ_ERR_WORKSPACE;
-  if (bad_place(y, n, N, y_type, x, n * K, w, static_cast<int64_t>(N) * K)) return TQ_ERR_INVALID_ARG;
+  if (n > 0 && outputs_overlap({{y, y_bytes(n, N, y_type)}, {splits ? workspace : nullptr, static_cast<int64_t>(l.bytes)}},
+                               {{x, n * K}, {x_scales, scale_bytes(1, n, K, 1)}, {w, static_cast<int64_t>(N) * K},
+                                {w_scales, scale_bytes(1, N, K, kFp8Block)}}))
+    return TQ_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int rc = require_sm103(s);
   if (rc != TQ_OK || n == 0) return rc;
@@ -306,7 +308,11 @@ int tq_fp8_moe_forward(const uint8_t* x, const float* x_scales, const uint8_t* w
     return TQ_ERR_INVALID_ARG;
   const ProductPlan p = plan_moe(workspace, n, top_k, E, K, N);
   if (n > 0 && p.m.arm != kTokens && bad_workspace(workspace, workspace_bytes, p.bytes)) return TQ_ERR_WORKSPACE;
-  if (bad_place(y, n, N, y_type, x, n * K, w, static_cast<int64_t>(E) * N * K)) return TQ_ERR_INVALID_ARG;
+  if (n > 0 &&
+      outputs_overlap({{y, y_bytes(n, N, y_type)}, {p.m.arm != kTokens ? workspace : nullptr, static_cast<int64_t>(p.bytes)}},
+                      {{x, n * K}, {x_scales, scale_bytes(1, n, K, 1)}, {w, static_cast<int64_t>(E) * N * K},
+                       {w_scales, scale_bytes(E, N, K, kFp8Block)}, {topk_ids, 4 * n * top_k}, {topk_w, 4 * n * top_k}}))
+    return TQ_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int rc = require_sm103(s);
   if (rc != TQ_OK || n == 0) return rc;
@@ -341,7 +347,13 @@ int tq_fp8_moe_mlp_forward(const uint8_t* x, const float* x_scales, const uint8_
     return TQ_ERR_INVALID_ARG;
   const MlpPlan p = plan_mlp(workspace, n, top_k, E, H, I);
   if (n > 0 && bad_workspace(workspace, workspace_bytes, p.bytes)) return TQ_ERR_WORKSPACE;
-  if (bad_place(y, n, H, y_type, x, n * H, w_down, static_cast<int64_t>(E) * H * I)) return TQ_ERR_INVALID_ARG;
+  if (n > 0 &&
+      outputs_overlap({{y, y_bytes(n, H, y_type)}, {workspace, static_cast<int64_t>(p.bytes)}},
+                      {{x, n * H}, {x_scales, scale_bytes(1, n, H, 1)}, {w_gu, 2ll * E * I * H},
+                       {gu_scales, scale_bytes(E, 2ll * I, H, kFp8Block)}, {w_down, static_cast<int64_t>(E) * H * I},
+                       {down_scales, scale_bytes(E, H, I, kFp8Block)}, {topk_ids, 4 * n * top_k},
+                       {topk_w, 4 * n * top_k}}))
+    return TQ_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int rc = require_sm103(s);
   if (rc != TQ_OK || n == 0) return rc;

@@ -1,6 +1,7 @@
 // Host-side internals shared by the library's translation units.
 #pragma once
 #include <cstdint>
+#include <initializer_list>
 #include <cuda_runtime.h>
 
 #include "tqmoe.h"
@@ -217,19 +218,33 @@ int launch_fp4_gemv(const Fp4Gemv& g, cudaStream_t s);
 // a step for 128 x 224 results in place of 51 (experts, 8192 tokens: 460 -> 424
 // us).  At 64 rows the pairs are no faster, and their second CTA idles where
 // there are few weight rows.
+inline bool fp4_takes_pairs(int tile_m) { return tile_m >= 128; }
+int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s);
+
 // Whether two buffers share bytes (a null or an empty one shares none).
 inline bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
   const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
   return a && b && a_bytes > 0 && b_bytes > 0 && p < q + static_cast<uintptr_t>(b_bytes) &&
          q < p + static_cast<uintptr_t>(a_bytes);
 }
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+// Whether an output shares bytes with another or with an input.
+inline bool outputs_overlap(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+  for (const Span* o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const Span* other = o + 1; other != outputs.end(); ++other)
+      if (overlap(o->p, o->bytes, other->p, other->bytes)) return true;
+    for (const Span& in : inputs)
+      if (overlap(o->p, o->bytes, in.p, in.bytes)) return true;
+  }
+  return false;
+}
 // Bytes from the first to the last value of `n` rows, `stride` values apart.
 inline int64_t row_bytes(int64_t n, int64_t stride, int64_t width, int64_t size) {
   return n > 0 ? ((n - 1) * stride + width) * size : 0;
 }
-
-inline bool fp4_takes_pairs(int tile_m) { return tile_m >= 128; }
-int launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t s);
 
 // The norm and its gradient (tq_norm.cu).  Rows of the outputs are dense.
 struct NormArgs {

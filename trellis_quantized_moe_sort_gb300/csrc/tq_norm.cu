@@ -580,15 +580,16 @@ int tq_rms_norm(const void* x, int x_type, int64_t x_stride, const void* residua
                    (!residual || rows_in_vectors(residual, residual_stride, x_type)) && aligned(residual_out, 16) &&
                    aligned(y, 16) && aligned(weight, 16);
   if (codes && (!vec || !aligned(codes, 16))) return TQ_ERR_INVALID_ARG;
-  const int64_t bytes = n * K * static_cast<int64_t>(size);
+  const int64_t each = static_cast<int64_t>(size), w_size = static_cast<int64_t>(type_size(w_type));
+  const Span y_rows{y, n * K * each}, r_rows{residual_out, n * K * each}, rstds{rstd, 4 * n}, code_rows{codes, n * K},
+      scale_rows{scales, 4 * n * ((K + kFp8Block - 1) / kFp8Block)}, weights{weight, K * w_size};
   for (const void* out : {static_cast<const void*>(y), static_cast<const void*>(residual_out)}) {
-    if (bad_place(out, x, x_stride, n, K, x_type) || bad_place(out, residual, residual_stride, n, K, x_type) ||
-        overlap(out, bytes, codes, n * K))
+    if (bad_place(out, x, x_stride, n, K, x_type) || bad_place(out, residual, residual_stride, n, K, x_type))
       return TQ_ERR_INVALID_ARG;
   }
-  if (overlap(y, bytes, residual_out, bytes) ||
-      overlap(codes, n * K, x, row_bytes(n, x_stride, K, static_cast<int64_t>(size))) ||
-      overlap(codes, n * K, residual, row_bytes(n, residual_stride, K, static_cast<int64_t>(size))))
+  if (n > 0 && (outputs_overlap({y_rows, r_rows, rstds, code_rows, scale_rows}, {weights}) ||
+                outputs_overlap({rstds, code_rows, scale_rows}, {{x, row_bytes(n, x_stride, K, each)},
+                                                                 {residual, row_bytes(n, residual_stride, K, each)}})))
     return TQ_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int rc = require_sm103(s);
@@ -624,6 +625,14 @@ int tq_rms_norm_backward(const void* grad_y, int64_t grad_y_stride, const void* 
     return TQ_ERR_WORKSPACE;
   if (bad_place(grad_x, x, x_stride, n, K, x_type) || bad_place(grad_x, grad_y, grad_y_stride, n, K, x_type) ||
       bad_place(grad_x, grad_residual, grad_residual_stride, n, K, x_type))
+    return TQ_ERR_INVALID_ARG;
+  const int64_t each = static_cast<int64_t>(size), w_bytes = K * static_cast<int64_t>(type_size(w_type));
+  const Span gw{grad_weight, w_bytes}, weights{weight, w_bytes}, rstds{rstd, 4 * n};
+  const Span work{grad_weight ? workspace : nullptr, static_cast<int64_t>(tq_rms_norm_backward_workspace_size(n, K))};
+  if (n > 0 && (outputs_overlap({{grad_x, n * K * each}, gw, work}, {weights, rstds}) ||
+                outputs_overlap({gw, work}, {{x, row_bytes(n, x_stride, K, each)},
+                                             {grad_y, row_bytes(n, grad_y_stride, K, each)},
+                                             {grad_residual, row_bytes(n, grad_residual_stride, K, each)}})))
     return TQ_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int rc = require_sm103(s);

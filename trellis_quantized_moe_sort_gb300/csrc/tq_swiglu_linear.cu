@@ -227,8 +227,8 @@ int tq_swiglu_linear(const void* x, int type, int64_t x_stride, const void* w_gu
   const ForwardPlan f = plan_forward(n, H, I);
   if (n > 0 && f.split && (!workspace || !aligned(workspace, 256) || workspace_bytes < f.part)) return TQ_ERR_WORKSPACE;
   const int64_t x_bytes = row_bytes(n, x_stride, H, 2), w_bytes = 4ll * I * H, h_bytes = 2 * n * I, gu_bytes = 8 * n * I;
-  if (overlap(h, h_bytes, x, x_bytes) || overlap(h, h_bytes, w_gu, w_bytes) || overlap(gate_up, gu_bytes, x, x_bytes) ||
-      overlap(gate_up, gu_bytes, w_gu, w_bytes) || overlap(h, h_bytes, gate_up, gu_bytes))
+  if (n > 0 && outputs_overlap({{h, h_bytes}, {gate_up, gu_bytes}, {f.split ? workspace : nullptr, static_cast<int64_t>(f.part)}},
+                               {{x, x_bytes}, {w_gu, w_bytes}}))
     return TQ_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int rc = require_sm103(s);
@@ -254,9 +254,9 @@ int tq_swiglu_linear_backward(const void* x, int type, int64_t x_stride, const v
   if (n > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < p.bytes)) return TQ_ERR_WORKSPACE;
   // (grad_h and gate_up are read before either gradient is written)
   const int64_t x_bytes = row_bytes(n, x_stride, H, 2), gx_bytes = 2 * n * H, w_bytes = n > 0 ? 4ll * I * H : 0;
-  if (overlap(grad_x, gx_bytes, x, x_bytes) || overlap(grad_x, gx_bytes, w_gu, w_bytes) ||
-      overlap(grad_w_gu, w_bytes, x, x_bytes) || overlap(grad_w_gu, w_bytes, w_gu, w_bytes) ||
-      overlap(grad_x, gx_bytes, grad_w_gu, w_bytes))
+  const Span work{workspace, static_cast<int64_t>(p.bytes)};
+  if (n > 0 && (outputs_overlap({{grad_x, gx_bytes}, {grad_w_gu, w_bytes}, work}, {{x, x_bytes}, {w_gu, w_bytes}}) ||
+                outputs_overlap({work}, {{grad_h, 2 * n * I}, {gate_up, 8 * n * I}})))
     return TQ_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int rc = require_sm103(s);
