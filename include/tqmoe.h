@@ -559,7 +559,9 @@ int tq_fp4_tile_scales(const uint8_t* scales, int E, int N, int K, int fmt, uint
  * E, K and N) take one launch that needs no workspace.  workspace (device) of
  * at least the matching *_workspace_size() bytes (0 on invalid arguments; 256,
  * or a NULL workspace, where none is needed), 256-byte aligned; its contents
- * are undefined after the call.
+ * are undefined after the call.  The size does not grow with n throughout (K is
+ * split where few rows leave the device idle): ask for each n that a workspace
+ * is to serve, and take the largest.
  * ------------------------------------------------------------------------- */
 size_t tq_fp4_linear_workspace_size(int64_t n, int K, int N, int fmt);
 int tq_fp4_linear(const void* x, int x_type, int64_t x_stride, const uint8_t* packed,
@@ -667,11 +669,12 @@ int tq_fp8_dequantize(const uint8_t* codes, const float* scales, int E, int64_t 
  *   y[t] = sum_j topk_w[t][j] W_down h(t,j).  E = 1, top_k = 1: a dense MLP.
  * x, w (device) codes, 16-byte aligned; x_scales (device) fp32 [n][ceil(K/128)];
  * y (device) dense; y and a workspace that is used may not share memory with an input
- * or each other.  K and H are multiples of 16, N is
- * any width.  E <= 1024, top_k <= 32; n * top_k and E * N (E * 2I, E * H) below 2^31 -
- * 1024, n * top_k * N below 2^57.  workspace (device) of at least the matching
- * *_workspace_size() bytes (0 on invalid arguments; 256, or a NULL workspace, where none
- * is needed), 256-byte aligned; its contents are undefined after the call.
+ * or each other.  K and H are multiples of 16, N is any width.  E <= 1024, top_k <= 32;
+ * n * top_k and E * N (E * 2I, E * H) below 2^31 - 1024, n * top_k * N below 2^57.
+ * workspace (device) of at least the matching *_workspace_size() bytes (0 on invalid
+ * arguments; 256, or a NULL workspace, where none is needed), 256-byte aligned; its
+ * contents are undefined after the call.  The size does not grow with n throughout: ask
+ * for each n that a workspace is to serve, and take the largest.
  * ------------------------------------------------------------------------- */
 size_t tq_fp8_linear_workspace_size(int64_t n, int K, int N);
 int tq_fp8_linear(const uint8_t* x, const float* x_scales, const uint8_t* w, const float* w_scales, int64_t n, int K,
@@ -698,7 +701,9 @@ int tq_fp8_moe_mlp_forward(const uint8_t* x, const float* x_scales, const uint8_
  *   gradient takes them (fp32: their roundings to 16 bits would be as large as the
  *   one of d below).
  * workspace (device, 256-byte aligned) of tq_swiglu_linear_workspace_size() bytes (0
- *   on invalid arguments; 256, or a NULL workspace, where none is needed).
+ *   on invalid arguments; 256, or a NULL workspace, where none is needed).  The size,
+ *   and that of the gradient's, does not grow with n throughout: ask for each n that a
+ *   workspace is to serve, and take the largest.
  *
  * tq_swiglu_linear_backward: from grad_h (device, [n][I] dense, 16-byte aligned)
  *   dgate = grad_h * up * s * (1 + gate * (1 - s)), dup = grad_h * gate * s,
@@ -709,8 +714,8 @@ int tq_fp8_moe_mlp_forward(const uint8_t* x, const float* x_scales, const uint8_
  *   order.  workspace (device, 256-byte aligned) of
  *   tq_swiglu_linear_backward_workspace_size() bytes (0 on invalid arguments).
  * Outputs and workspace may not share memory with x, w_gu or each other, the workspace
- * not with grad_h or gate_up either (grad_x may lie over those).  Limits: n, 2I and H below 2^31 - 1024, products of two of them below
- * 2^57.
+ * not with grad_h or gate_up either (grad_x may lie over those).  Limits: n, 2I and H
+ * below 2^31 - 1024, products of two of them below 2^57.
  * ------------------------------------------------------------------------- */
 size_t tq_swiglu_linear_workspace_size(int64_t n, int H, int I);
 int tq_swiglu_linear(const void* x, int type, int64_t x_stride, const void* w_gu, int64_t n, int H, int I,

@@ -197,3 +197,30 @@ def test_results_in_a_used_workspace_are_refused():
         tq.tq_swiglu_linear(x, w, h=work[:2 * n * I].view(torch.bfloat16).view(n, I), workspace=work)
     assert torch.equal(tq.tq_swiglu_linear(x, w, workspace=work), tq.tq_swiglu_linear(x, w))
     check_no_device_error()
+
+
+def test_one_workspace_for_batches_of_many_sizes():
+    """Sizes asked for each batch: a smaller batch can need more (K split), and the largest
+    serves them all."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    K, N, batches = 4096, 256, (1, 40, 300, 1000, 8000)
+    w, w_scales = tq.tq_fp8_quantize(torch.randn((N, K), device="cuda", generator=g), 128)
+    sizes = [tq.tq_fp8_linear_workspace_size(n, K, N) for n in batches]
+    assert max(sizes) > sizes[-1]
+    work = torch.empty(max(sizes), dtype=torch.uint8, device="cuda")
+    for n, size in zip(batches, sizes):
+        x, x_scales = tq.tq_fp8_quantize(torch.randn((n, K), device="cuda", generator=g))
+        want = tq.tq_fp8_linear(x, x_scales, w, w_scales)
+        assert torch.equal(tq.tq_fp8_linear(x, x_scales, w, w_scales, workspace=work), want)
+        if size > 256:
+            with pytest.raises(tq.TQError):
+                tq.tq_fp8_linear(x, x_scales, w, w_scales, workspace=work[:size - 256])
+    H, I, batches = 4096, 2048, (1, 128, 2000)
+    w = (torch.randn((2 * I, H), device="cuda", generator=g) / H ** 0.5).bfloat16()
+    sizes = [tq.tq_swiglu_linear_workspace_size(n, H, I) for n in batches]
+    assert max(sizes) > sizes[-1]
+    work = torch.empty(max(sizes), dtype=torch.uint8, device="cuda")
+    for n in batches:
+        x = torch.randn((n, H), device="cuda", generator=g).bfloat16()
+        assert torch.equal(tq.tq_swiglu_linear(x, w, workspace=work), tq.tq_swiglu_linear(x, w))
+    check_no_device_error()
