@@ -224,3 +224,51 @@ def test_one_workspace_for_batches_of_many_sizes():
         x = torch.randn((n, H), device="cuda", generator=g).bfloat16()
         assert torch.equal(tq.tq_swiglu_linear(x, w, workspace=work), tq.tq_swiglu_linear(x, w))
     check_no_device_error()
+
+
+# ------------------------------------------------------------------ one gradient alone
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+@pytest.mark.parametrize("n,H,I", [(20, 64, 16), (300, 512, 256), (1000, 136, 1000)])
+@pytest.mark.parametrize("keep", (True, False))
+def test_one_gradient_of_the_gated_projection(n, H, I, keep):
+    """A C caller leaves out either gradient: the other has the same bits."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    x = torch.randn((n, H), device="cuda", generator=g).bfloat16()
+    w = (torch.randn((2 * I, H), device="cuda", generator=g) / H ** 0.5).bfloat16()
+    dh = torch.randn((n, I), device="cuda", generator=g).bfloat16()
+    gate_up = None
+    if keep:
+        gate_up = torch.empty((n, 2 * I), device="cuda")
+        tq.tq_swiglu_linear(x, w, gate_up=gate_up)
+    want = tq.tq_swiglu_linear_backward(x, w, dh, gate_up=gate_up)
+    size = tq.tq_swiglu_linear_backward_workspace_size(n, H, I, keep)
+    for which in (0, 1):
+        out = torch.full_like(want[which], float("nan"))
+        work = torch.empty(size, dtype=torch.uint8, device="cuda")
+        grads = (out, None) if which == 0 else (None, out)
+        rc = tq.lib().tq_swiglu_linear_backward(_ptr(x), 1, H, _ptr(w), _ptr(gate_up), _ptr(dh), n, H, I, _ptr(work), size,
+                                                _ptr(grads[0]), _ptr(grads[1]), torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        assert torch.equal(out, want[which])
+    check_no_device_error()
+
+
+@pytest.mark.parametrize("n,K", [(5, 144), (300, 2048), (200, 1023), (160, 12304)])
+def test_norm_gradient_without_the_weights(n, K):
+    """Without grad_weight, and without a workspace, grad_x has the same bits."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.randn((n, K), device="cuda", generator=g).bfloat16()
+    dy = torch.randn((n, K), device="cuda", generator=g).bfloat16()
+    weight = torch.randn(K, device="cuda", generator=g)
+    _, _, rstd = tq.tq_rms_norm(x, weight)
+    want, _ = tq.tq_rms_norm_backward(dy, x, weight, rstd)
+    out = torch.full_like(want, float("nan"))
+    rc = tq.lib().tq_rms_norm_backward(_ptr(dy), K, _ptr(x), 1, K, _ptr(weight), 0, _ptr(rstd), None, 0, n, K, None, 0,
+                                       _ptr(out), None, torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    assert torch.equal(out, want)
+    check_no_device_error()
