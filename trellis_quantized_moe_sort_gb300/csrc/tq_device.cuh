@@ -292,6 +292,8 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(uint32_t M, uint32_t N) {
 // 1 / (1 + exp(-g)) and g times that.  With e = exp(-|g|) the denominator 1 + e is between 1
 // and 2 for every g, where __fdividef is within 2 ulp: a few ulp in all, down to the
 // subnormal e of g < -87 (1 + exp(-g) would pass 2^126 there, where __fdividef gives 0).
+// The 64 of them that a thread of the tile products does in a unit, while the MMAs wait, do
+// not show (4735 rows 664 -> 2 x 1240: 23 us; with a division's 11000 cycles 38).
 __device__ __forceinline__ float sigmoid(float g) {
   const float e = expf(-fabsf(g));
   return __fdividef(g < 0.f ? e : 1.f, 1.f + e);

@@ -17,10 +17,10 @@
 // units too.  A step costs about 200 instructions of a warp (the 8-bit MMAs are
 // expanded into conversions and 16-bit ones), and a unit of 32 steps gives a warp four
 // between two barriers.  Measured, six experts of one token, 8 bits: gated 4096 -> 2 x
-// 2048 25 us (100 MB, 60% of the measured copy rate, 47% of the issue slots; 1536 units on
-// 304 blocks), 2048 -> 4096 weighted and added 18 us (50 MB, 43%: a unit a block, so its
+// 2048 24 us (100 MB, 62% of the measured copy rate, 45% of the issue slots; 1536 units on
+// 304 blocks), 2048 -> 4096 weighted and added 20 us (50 MB, 38%: a unit a block, so its
 // start and its last sums show).  From where experts share tokens on the tensor-memory
-// tiles are faster (16 tokens of top-6 of 256, 4096 -> 2048: 156 us here, 138 there).
+// tiles are faster (16 tokens of top-6 of 256, 4096 -> 2048: 150 us here, 132 there).
 //
 // A single token's experts are the segments of one unit: the sums of each are added,
 // weighted, to the token's, and its product is this one launch.  (The weight does not

@@ -80,11 +80,11 @@ struct MoePlan {
 // time for each of its units; sorted pairs read every woken expert's once, after a sort and
 // before a combine.  Fitted, in us, to 140 sizes from 256 -> 256 to 4096 -> 2048, of 1 to 256
 // tokens on 1, 8, 64 and 256 experts, of products and MLPs each: by this rule the slower
-// arm is taken for few sizes and by at most 28% (both are within 0.2% of the best on the
-// average; where only tokens whose experts nobody shares went by themselves, 21% behind,
-// and up to 2.8 times).  Of top-6 of 256, 4096 -> 2048: 4, 8 and 16 tokens 54, 87 and 150
-// us by themselves, 67, 102 and 132 in tiles; top-2 of 8, 512 -> 1024, 8, 32 and 128
-// tokens 11, 18 and 44, and 24 in tiles.
+// arm is taken for few sizes and by at most 35% (6 us; 0.5% behind the best on the average;
+// where only tokens whose experts nobody shares went by themselves, 21% behind, and up to
+// 2.8 times).  Of top-6 of 256, 4096 -> 2048: 4, 8, 16 and 32 tokens 54, 89, 150 and 276 us
+// by themselves, 67, 100, 132 and 216 in tiles; top-2 of 8, 512 -> 1024, 8, 32 and 128
+// tokens 11, 18 and 44, and 20 in tiles.
 // `bytes`: of an expert's weights; `units`: of the few-rows products.
 MoePlan plan_arm(int64_t n, int top_k, int E, bool mlp, double bytes, double units) {
   MoePlan m;

@@ -3,8 +3,9 @@
 //
 // All of these move bytes: a thread takes 16 consecutive values, a block of 128 of a
 // row is eight neighbouring lanes, which share their maximum by three shuffles.
-// Measured: rows of 8192 x 4096 bf16 18 us (102 MB, 85% of the measured copy rate); 71% of
-// the issue slots (a correctly rounded quotient a value).
+// Measured: rows of 8192 x 4096 bf16 18 us (102 MB, 85% of the measured copy rate; 71% of
+// the issue slots: a correctly rounded quotient a value); 8 matrices of 4096 x 4096 bf16
+// quantised 78 us (403 MB, 77%), dequantised 77 us (78%).
 #include <cuda_runtime.h>
 
 #include <algorithm>

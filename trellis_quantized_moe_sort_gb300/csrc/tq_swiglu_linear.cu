@@ -18,7 +18,12 @@ size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // d = [dgate dup] of 8 columns a thread; reads gate, up and grad_h once: bound by memory
-// (8192 rows of 2048: 29 us for 235 MB, most of its writes left in L2).
+// (8192 rows of 2048: 30 us for 235 MB, most of its writes left in L2).
+//
+// d is rounded to the type: it is an operand of both products, and the tensor cores take
+// operands of 16 bits.  The gradients are off by 2.3e-3 of themselves for it (rms, bf16, 8192
+// rows 4096 -> 2 x 2048), where their own rounding is 1.7e-3; with d in two parts, each
+// product run twice, they would take 300 us more of 545.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 swiglu_grad_kernel(const float* __restrict__ gate_up, const T* __restrict__ grad_h, long long rows, int I,
